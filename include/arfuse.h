@@ -89,6 +89,7 @@ typedef enum ar_status {
 /* Bits of the device error word (ar_workspace_device_error). */
 #define AR_DEVERR_PERM_RANGE 0x1   /* some perm value was outside [0, rows_e); clamped */
 #define AR_DEVERR_TIMEOUT 0x2      /* a pipeline wait gave up after its time limit     */
+#define AR_DEVERR_EXPERT_RANGE 0x4 /* some expert id was neither -1 nor an expert; skipped (ar_moe_device_error) */
 
 /* Kernel regimes (ar_workspace_set_regime / ar_workspace_last_regime). */
 #define AR_REGIME_AUTO 0     /* pick by (T, R, K, H) and the SM count                    */
@@ -489,6 +490,142 @@ ARFUSE_API ar_status ar_finalize_rmsnorm_noalloc(const void* const* expert_out, 
                                                  float weight_bias, float eps, int64_t T, int R,
                                                  int K, int H, void* out, void* residual_out,
                                                  int residual_out_is_fp32, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The mixture-of-experts layer of a few tokens (decode): the router, the
+ * experts' products, and products with a 4-bit weight matrix.  (No
+ * counterpart on the pages, which start at the experts' outputs: an addition
+ * of this library.)  ar_moe_experts' result is one rank's partial [T, H] as
+ * ar_rmsnorm and ar_finalize_rmsnorm (shared_out) take it.
+ *
+ * 4-bit weights: a matrix [rows, cols] is a byte array q [rows, cols / 2] and
+ * bf16 scales s [rows, cols / group]; byte j of a row holds the codes of
+ * columns 2j (low four bits) and 2j + 1 (high); the value of a code c is
+ * s[row, col / group] * (c - 8).  group is 32, 64 or 128 and divides cols.
+ */
+#define AR_MAX_MOE_TOKENS 64    /* T of the calls below                       */
+#define AR_MAX_MOE_EXPERTS 512  /* experts + shared                           */
+#define AR_MAX_MOE_GROUPS 32    /* n_group                                    */
+#define AR_MAX_MATVEC_COLS 65536
+#define AR_MAX_MATVEC_ROWS 1048576
+
+#define AR_MOE_SOFTMAX 0
+#define AR_MOE_SIGMOID 1
+
+typedef struct ar_moe ar_moe; /* opaque, library-owned */
+
+/*
+ * Create the handle of a model's MoE layers (shared by the layers, as a
+ * workspace is).  Allocates its scratch on `device`: the activations between
+ * the two products (T * slots * inter * 4 bytes), the router's logits and the
+ * error word.  Calls on one handle must be ordered on the GPU (one stream, or
+ * event ordering; graphs captured on it must not run at the same time);
+ * concurrent callers need a handle each.  Call it outside any stream capture.
+ *   experts     routed experts E, 1 ..
+ *   shared      shared experts S, 0 ..: every token's slots end with experts
+ *               E .. E + S - 1 at weight 1; E + S <= AR_MAX_MOE_EXPERTS
+ *   top_k       routed experts per token, 1 .. E; a token has top_k + S slots,
+ *               at most AR_MAX_TOP_K
+ *   hidden      H, 8 .. AR_MAX_HIDDEN, a multiple of 8
+ *   inter       I, columns of an expert's intermediate vector on this rank,
+ *               8 .. AR_MAX_HIDDEN, a multiple of 8; 0: only ar_moe_route
+ *   max_tokens  1 .. AR_MAX_MOE_TOKENS
+ *   flags       0, or any of AR_WS_DRY_RUN, AR_WS_PDL (as for a workspace)
+ *   out         receives the handle (NULL on error)
+ * Errors: AR_ERR_INVALID_ARG (out NULL, max_tokens < 1, a negative count,
+ * top_k > experts, unknown flags), AR_ERR_ALIGNMENT (hidden or inter not a
+ * multiple of 8), AR_ERR_UNSUPPORTED (limits above, or a device older than
+ * sm_100), AR_ERR_CUDA.
+ */
+ARFUSE_API ar_status ar_moe_create(int device, int experts, int shared, int top_k, int hidden,
+                                   int inter, int64_t max_tokens, unsigned flags, ar_moe** out);
+
+/* Free the handle.  NULL is accepted.  No call using it may still be running. */
+ARFUSE_API ar_status ar_moe_destroy(ar_moe* moe);
+
+/* Read and clear the handle's error word, as ar_workspace_device_error. */
+ARFUSE_API ar_status ar_moe_device_error(ar_moe* moe, int* code);
+
+/*
+ * The router: logits l = x gate^T, scores s = softmax(l) or sigmoid(l) over
+ * the E routed experts, the top_k experts of the largest choice value c (the
+ * lowest index first among equals), in descending order of c.
+ *   c = s + bias with a bias, s with expert groups and no bias, else l.
+ *   Expert groups (n_group > 1): E / n_group consecutive experts form a group;
+ *   only the topk_group groups with the largest sum of their two largest c
+ *   take part.
+ *   x        device bf16 [T, H]
+ *   gate     device bf16 [E, H]
+ *   bias     device fp32 [E], or NULL (minus infinity bars an expert as long
+ *            as top_k others remain)
+ *   scoring  AR_MOE_SOFTMAX or AR_MOE_SIGMOID
+ *   renorm   1: divide the chosen scores by their sum (0 if that is 0)
+ *   scale    factor of the routed weights
+ *   n_group, topk_group  1, 1 for no groups; n_group divides E with at least
+ *            two experts each, n_group <= AR_MAX_MOE_GROUPS, and topk_group *
+ *            E / n_group >= top_k
+ *   ids      device int32 [T, top_k + S]: chosen experts, then the shared ones
+ *   weights  device fp32 [T, top_k + S]: weights (1 for the shared experts)
+ * The choice is that of 64-bit scores: logits carry about 45 bits, so neither
+ * T nor the GPU's summation order moves it.  NaN choices rank last; ids are
+ * always distinct experts.  T == 0 returns AR_OK.
+ * Errors: AR_ERR_INVALID_ARG (NULL, ranges above, an output overlapping an
+ * input or the other), AR_ERR_ALIGNMENT (x, gate 16 bytes, the others 4),
+ * AR_ERR_CAPACITY (T > max_tokens), AR_ERR_CUDA.  The handle's device must be
+ * the current one (else AR_ERR_INVALID_ARG).
+ */
+ARFUSE_API ar_status ar_moe_route(ar_moe* moe, const void* x, const void* gate, const float* bias,
+                                  int scoring, int renorm, float scale, int n_group, int topk_group,
+                                  int64_t T, int32_t* ids, float* weights, void* stream);
+
+/*
+ * The experts: out[t] = sum_k weights[t,k] * W2_e (silu(G_e x[t]) * (U_e x[t])),
+ * e = ids[t,k], W13_e = [G_e; U_e].
+ *   x        device bf16 [T, H]
+ *   ids      device int32 [T, top_k + S], each -1 (no expert: the slot adds
+ *            nothing) or 0 .. E + S - 1; another value is skipped and sets
+ *            AR_DEVERR_EXPERT_RANGE.  A token may name an expert twice (its
+ *            weights add up).
+ *   weights  device fp32 [T, top_k + S]
+ *   w13      device bf16 [E + S, 2 I, H]: gate rows, then up rows
+ *   w2       device bf16 [E + S, H, I]
+ *   out      device bf16 [T, H]; a token without experts gets zeros
+ * Sums are fp32 and `out` is the only rounding (the activations between the
+ * products keep 16 bits).  Deterministic for given sizes, ids and GPU.
+ * T == 0 returns AR_OK.  Errors as for ar_moe_route, and AR_ERR_UNSUPPORTED
+ * for a handle with inter = 0; every matrix, x and out 16-byte aligned.
+ */
+ARFUSE_API ar_status ar_moe_experts(ar_moe* moe, const void* x, const int32_t* ids,
+                                    const float* weights, const void* w13, const void* w2,
+                                    int64_t T, void* out, void* stream);
+
+/*
+ * ar_moe_experts with 4-bit weights: q13 [E + S, 2 I, H / 2] with s13
+ * [E + S, 2 I, H / group], q2 [E + S, H, I / 2] with s2 [E + S, H, I / group].
+ * A group other than 32, 64 or 128, or one that does not divide H and I, is
+ * AR_ERR_UNSUPPORTED.
+ */
+ARFUSE_API ar_status ar_moe_experts_w4(ar_moe* moe, const void* x, const int32_t* ids,
+                                       const float* weights, const void* q13, const void* s13,
+                                       const void* q2, const void* s2, int group, int64_t T,
+                                       void* out, void* stream);
+
+/*
+ * out[t] = W x[t] with a 4-bit matrix W [N, K]; needs no handle and allocates
+ * nothing (the first call on a device sets kernel attributes: make it outside
+ * any stream capture).  Runs on the current device.
+ *   x      device bf16 [T, K]
+ *   q, s   device: codes [N, K / 2] and bf16 scales [N, K / group]
+ *   T      0 .. AR_MAX_MOE_TOKENS (0 returns AR_OK)
+ *   N, K   1 .. AR_MAX_MATVEC_ROWS, group .. AR_MAX_MATVEC_COLS
+ *   out    device [T, N], bf16 or (out_is_fp32 = 1) fp32
+ * Errors: AR_ERR_INVALID_ARG (NULL, negative sizes, overlap of out with an
+ * input, out_is_fp32 not 0 or 1), AR_ERR_ALIGNMENT (x, q, s, out 16 bytes),
+ * AR_ERR_UNSUPPORTED (group, sizes), AR_ERR_CAPACITY (T), AR_ERR_CUDA.
+ */
+ARFUSE_API ar_status ar_matvec_w4(const void* x, const void* q, const void* s, int group, int64_t T,
+                                  int64_t N, int64_t K, void* out, int out_is_fp32, void* stream);
 
 /* Static description of a status code; never NULL.  Every status other than
  * AR_OK / AR_VALIDATED is a clean decline: nothing was launched and the

@@ -32,6 +32,7 @@ AR_WS_NORM_BF16_H = 0x2
 AR_WS_PDL = 0x4
 AR_DEVERR_PERM_RANGE = 0x1
 AR_DEVERR_TIMEOUT = 0x2
+AR_DEVERR_EXPERT_RANGE = 0x4
 AR_REGIME_AUTO = 0
 AR_REGIME_CLUSTER = 1
 AR_REGIME_STREAM = 2
@@ -41,6 +42,13 @@ AR_REGIME_SPLIT = 4
 AR_MAX_RANKS = 16
 AR_MAX_TOP_K = 16
 AR_MAX_HIDDEN = 16384
+AR_MAX_MOE_TOKENS = 64
+AR_MAX_MOE_EXPERTS = 512
+AR_MAX_MOE_GROUPS = 32
+AR_MAX_MATVEC_COLS = 65536
+AR_MAX_MATVEC_ROWS = 1048576
+AR_MOE_SOFTMAX = 0
+AR_MOE_SIGMOID = 1
 
 _lock = threading.Lock()
 _lib = None
@@ -107,6 +115,20 @@ def load_library(path: str | None = None):
         lib.ar_workspace_last_grid.argtypes = [P]
         lib.ar_workspace_last_plan.restype = I
         lib.ar_workspace_last_plan.argtypes = [P, P]
+        lib.ar_moe_create.restype = I
+        lib.ar_moe_create.argtypes = [I, I, I, I, I, I, I64, U, ctypes.POINTER(P)]
+        lib.ar_moe_destroy.restype = I
+        lib.ar_moe_destroy.argtypes = [P]
+        lib.ar_moe_device_error.restype = I
+        lib.ar_moe_device_error.argtypes = [P, ctypes.POINTER(I)]
+        lib.ar_moe_route.restype = I
+        lib.ar_moe_route.argtypes = [P, P, P, P, I, I, F, I, I, I64, P, P, P]
+        lib.ar_moe_experts.restype = I
+        lib.ar_moe_experts.argtypes = [P, P, P, P, P, P, I64, P, P]
+        lib.ar_moe_experts_w4.restype = I
+        lib.ar_moe_experts_w4.argtypes = [P, P, P, P, P, P, P, P, I, I64, P, P]
+        lib.ar_matvec_w4.restype = I
+        lib.ar_matvec_w4.argtypes = [P, P, P, I, I64, I64, I64, P, I, P]
         lib.ar_status_string.restype = ctypes.c_char_p
         lib.ar_status_string.argtypes = [I]
         _lib = lib
@@ -462,4 +484,185 @@ def ar_mhc_post(ws: Workspace, partials, streams, post, comb, out=None, stream=N
                                     _ptr(streams), _ptr(post), _ptr(comb), int(T), int(H), int(hc),
                                     _ptr(out), _stream_handle(stream, dev) if not ws.dry_run else None)
     _check(st, "ar_mhc_post", ok=(AR_OK, AR_VALIDATED) if ws.dry_run else (AR_OK,))
+    return out
+
+
+# ------------------------------------------------------ few-token MoE layer
+class Moe:
+    """Owner of one ``ar_moe*`` (fixed experts, shared, top_k, hidden, inter, max_tokens)."""
+
+    def __init__(self, handle: int, experts: int, shared: int, top_k: int, hidden: int, inter: int,
+                 max_tokens: int, device: int, dry_run: bool):
+        self.handle = handle
+        self.experts, self.shared, self.top_k, self.H, self.I = experts, shared, top_k, hidden, inter
+        self.slots = top_k + shared
+        self.max_tokens, self.device, self.dry_run = max_tokens, device, dry_run
+        self._fin = weakref.finalize(self, _destroy_moe_handle, handle)
+
+    def destroy(self):
+        self.handle = None
+        self._fin()
+
+    @property
+    def alive(self) -> bool:
+        return self._fin.alive
+
+
+def _destroy_moe_handle(handle):
+    if handle:
+        load_library().ar_moe_destroy(ctypes.c_void_p(handle))
+
+
+def ar_moe_create(experts: int, top_k: int, hidden: int, inter: int, max_tokens: int, shared: int = 0,
+                  device: int | None = None, flags: int = 0) -> Moe:
+    """Handle of a model's MoE layers for up to ``max_tokens`` (<= 64) tokens:
+    ``experts`` routed and ``shared`` shared experts, ``top_k`` routed experts
+    per token, ``inter`` columns of an expert's intermediate vector on this
+    rank (0: routing only).  `device` and `flags` as for ar_workspace_create
+    (AR_WS_DRY_RUN, AR_WS_PDL)."""
+    lib = load_library()
+    dry = bool(flags & AR_WS_DRY_RUN)
+    if device is None:
+        device = torch.cuda.current_device() if not dry else 0
+    h = ctypes.c_void_p()
+    _check(lib.ar_moe_create(int(device), int(experts), int(shared), int(top_k), int(hidden), int(inter),
+                             int(max_tokens), int(flags), ctypes.byref(h)), "ar_moe_create")
+    return Moe(h.value, int(experts), int(shared), int(top_k), int(hidden), int(inter), int(max_tokens),
+               int(device), dry)
+
+
+def ar_moe_destroy(moe: Moe) -> None:
+    """Free the handle (no call on it may still be running)."""
+    moe.destroy()
+
+
+def ar_moe_device_error(moe: Moe) -> int:
+    """Synchronise, read and clear the handle's error word (AR_DEVERR_EXPERT_RANGE)."""
+    code = ctypes.c_int(0)
+    _check(load_library().ar_moe_device_error(moe.handle, ctypes.byref(code)), "ar_moe_device_error",
+           ok=(AR_OK, AR_ERR_DEVICE_CHECK))
+    return int(code.value)
+
+
+def _need_on(device, t, dtype, shape, name):
+    """A contiguous tensor of this type and shape on CUDA device ``device``
+    (None: anywhere -- a dry run only looks at addresses)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and (device is None or t.get_device() == device):
+        return
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
+
+
+def _moe_device(moe):
+    return None if moe.dry_run else moe.device
+
+
+def _moe_stream(moe, stream):
+    return None if moe.dry_run else _stream_handle(stream, moe.device)
+
+
+def ar_moe_route(moe: Moe, x, gate, bias=None, scoring: int = AR_MOE_SIGMOID, renorm: bool = True,
+                 scale: float = 1.0, n_group: int = 1, topk_group: int = 1, ids=None, weights=None, stream=None):
+    """The router: softmax or sigmoid scores of ``x @ gate.T``, the top_k
+    experts by score + bias (by logit without a bias or groups; the lowest
+    index first among equals) and their weights, the shared experts appended.
+
+    x: bf16 [T, H]; gate: bf16 [E, H]; bias: fp32 [E] or None.  n_group > 1
+    keeps only the topk_group groups of E / n_group experts with the largest
+    sum of their two best.  Returns (ids int32, weights fp32), both
+    [T, top_k + shared], allocated when not given."""
+    T, dev = x.shape[0], _moe_device(moe)
+    _need_on(dev, x, torch.bfloat16, (T, moe.H), "x")
+    _need_on(dev, gate, torch.bfloat16, (moe.experts, moe.H), "gate")
+    if bias is not None:
+        _need_on(dev, bias, torch.float32, (moe.experts,), "bias")
+    shape = (T, moe.slots)
+    if ids is None:
+        ids = torch.empty(shape, dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty(shape, dtype=torch.float32, device=x.device)
+    _need_on(dev, ids, torch.int32, shape, "ids")
+    _need_on(dev, weights, torch.float32, shape, "weights")
+    st = load_library().ar_moe_route(
+        moe.handle, x.data_ptr(), gate.data_ptr(), None if bias is None else bias.data_ptr(), int(scoring),
+        1 if renorm else 0, float(scale), int(n_group), int(topk_group), T, ids.data_ptr(), weights.data_ptr(),
+        _moe_stream(moe, stream))
+    if st != AR_OK:
+        _check(st, "ar_moe_route", ok=(AR_VALIDATED,) if moe.dry_run else ())
+    return ids, weights
+
+
+def _moe_io(moe, x, ids, weights, out):
+    T, dev = x.shape[0], _moe_device(moe)
+    _need_on(dev, x, torch.bfloat16, (T, moe.H), "x")
+    _need_on(dev, ids, torch.int32, (T, moe.slots), "ids")
+    _need_on(dev, weights, torch.float32, (T, moe.slots), "weights")
+    if out is None:
+        out = torch.empty((T, moe.H), dtype=torch.bfloat16, device=x.device)
+    _need_on(dev, out, torch.bfloat16, (T, moe.H), "out")
+    return T, dev, out
+
+
+def ar_moe_experts(moe: Moe, x, ids, weights, w13, w2, out=None, stream=None):
+    """The experts' products: out[t] = sum_k weights[t,k] * W2_e (silu(G_e x[t]) * (U_e x[t])),
+    e = ids[t,k] (-1: none).  x: bf16 [T, H]; ids int32, weights fp32
+    [T, top_k + shared]; w13: bf16 [E + shared, 2 I, H], gate rows then up
+    rows; w2: bf16 [E + shared, H, I].  Returns out (bf16 [T, H], one rank's
+    partial), allocated when not given."""
+    T, dev, out = _moe_io(moe, x, ids, weights, out)
+    E = moe.experts + moe.shared
+    _need_on(dev, w13, torch.bfloat16, (E, 2 * moe.I, moe.H), "w13")
+    _need_on(dev, w2, torch.bfloat16, (E, moe.H, moe.I), "w2")
+    st = load_library().ar_moe_experts(moe.handle, x.data_ptr(), ids.data_ptr(), weights.data_ptr(), w13.data_ptr(),
+                                       w2.data_ptr(), T, out.data_ptr(), _moe_stream(moe, stream))
+    if st != AR_OK:
+        _check(st, "ar_moe_experts", ok=(AR_VALIDATED,) if moe.dry_run else ())
+    return out
+
+
+def ar_moe_experts_w4(moe: Moe, x, ids, weights, q13, s13, q2, s2, group: int, out=None, stream=None):
+    """ar_moe_experts with 4-bit weights: codes q13 uint8 [E + shared, 2 I, H / 2], q2 uint8
+    [E + shared, H, I / 2] (two a byte, the lower column in the low four bits) and bf16 scales s13
+    [E + shared, 2 I, H / group], s2 [E + shared, H, I / group]; a weight is scale * (code - 8).
+    ``group`` is 32, 64 or 128 and divides H and I."""
+    T, dev, out = _moe_io(moe, x, ids, weights, out)
+    E, H, I = moe.experts + moe.shared, moe.H, moe.I
+    _need_group(group, H, "hidden")
+    _need_group(group, I, "inter")
+    _need_on(dev, q13, torch.uint8, (E, 2 * I, H // 2), "q13")
+    _need_on(dev, s13, torch.bfloat16, (E, 2 * I, H // group), "s13")
+    _need_on(dev, q2, torch.uint8, (E, H, I // 2), "q2")
+    _need_on(dev, s2, torch.bfloat16, (E, H, I // group), "s2")
+    st = load_library().ar_moe_experts_w4(moe.handle, x.data_ptr(), ids.data_ptr(), weights.data_ptr(), q13.data_ptr(),
+                                          s13.data_ptr(), q2.data_ptr(), s2.data_ptr(), int(group), T, out.data_ptr(),
+                                          _moe_stream(moe, stream))
+    if st != AR_OK:
+        _check(st, "ar_moe_experts_w4", ok=(AR_VALIDATED,) if moe.dry_run else ())
+    return out
+
+
+def _need_group(group, cols, name):
+    if group not in (32, 64, 128) or cols % group:
+        raise ArfuseError(AR_ERR_UNSUPPORTED, f"group {group} with {name} = {cols} (groups of 32, 64 or 128 that divide it)")
+
+
+def ar_matvec_w4(x, q, s, group: int, out=None, out_fp32: bool = False, stream=None):
+    """x @ W.T with a 4-bit matrix W: x bf16 [T, K], T <= 64; q uint8 [N, K / 2] (two codes a byte, the lower
+    column in the low four bits); s bf16 [N, K / group]; a weight is scale * (code - 8).  Returns out
+    ([T, N], bf16 or, with ``out_fp32``, fp32), allocated when not given.  Runs on x's device, which must be
+    the current one."""
+    T, K = x.shape
+    N = q.shape[0]
+    dev = torch.cuda.current_device()
+    _need_group(group, K, "columns")
+    _need_on(dev, x, torch.bfloat16, (T, K), "x")
+    _need_on(dev, q, torch.uint8, (N, K // 2), "q")
+    _need_on(dev, s, torch.bfloat16, (N, K // group), "s")
+    dtype = torch.float32 if out_fp32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype, device=x.device)
+    _need_on(dev, out, dtype, (T, N), "out")
+    st = load_library().ar_matvec_w4(x.data_ptr(), q.data_ptr(), s.data_ptr(), int(group), T, N, K, out.data_ptr(),
+                                     1 if out_fp32 else 0, _stream_handle(stream, dev))
+    _check(st, "ar_matvec_w4")
     return out

@@ -14,6 +14,7 @@
 #include <mutex>
 #include <new>
 
+#include "arf_check.h"
 #include "arf_host.h"
 #include "arfuse.h"
 
@@ -52,7 +53,10 @@ constexpr int64_t kMaxTokensLimit = int64_t(1) << 26;
 constexpr int kDryRunSms = 152;          // GB300
 constexpr int kDryRunSmemOptin = 232448;  // 227 KB
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using arf::aligned;
+using arf::overlap;
+using arf::Range;
+using arf::range_of;
 
 // Split-row workspace: num_sms counters (rounded up to 256 bytes), then
 // num_sms fp32 rows of H.
@@ -60,17 +64,6 @@ size_t part_counter_words(int num_sms) { return ((size_t)num_sms * 4 + 255) / 25
 size_t part_bytes(int num_sms, int H) {
     return part_counter_words(num_sms) * 4 + (size_t)num_sms * H * 4;
 }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, int64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + static_cast<uintptr_t>(bytes)};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
 
 // Regime tables measured on GB300 (tp_reduce_moe_gb300.tune: every regime,
 // cluster size and ring variant, L2-cold, at 28 token counts from 1 to 256; a
