@@ -2,150 +2,97 @@
 //
 //   y[t, n] = sum_g s[n, g] * sum_{k in group g} (q[n, k] - 8) * x[t, k]
 //
-// Weight rows are dealt evenly over the SMs; a CTA takes its rows in blocks of
-// up to 16 * MT, its sixteen warps split the columns of a block and add their
-// parts through shared memory.  The codes are exact in bf16, so the inner sum
-// is one of exact products in fp32, scaled once per group.
+// Weight rows are dealt evenly over the SMs; a CTA's sixteen warps split the
+// columns of its rows (and the rows where that leaves less idle) and add their
+// parts through shared memory.  More tokens than the columns hold read the
+// CTA's rows again, from L2.
 #include "moe_common.cuh"
 
 namespace arf {
 namespace {
 
-template <int GS, int MT, int NT>
-constexpr int smem_bytes() {
-    return kMvWarps * Fmt<GS>::kRingBytes + 2 * kMvWarps * MT * NT * 512;
-}
-
-template <int GS, int MT, int NT>
-__global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_constant__ MatvecArgs a) {
-    using F = Fmt<GS>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    float* red = reinterpret_cast<float*>(smem + kMvWarps * F::kRingBytes);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int r0 = (int)((int64_t)a.N * blockIdx.x / gridDim.x), r1 = (int)((int64_t)a.N * (blockIdx.x + 1) / gridDim.x);
-    if (r0 >= r1) return;
-    Rows m;
-    m.q = a.q;
-    m.s = a.s;
-    m.row_bytes = F::row_bytes(a.K);
-    m.row_scales = a.K / (128 / GS);
-    m.s_end = a.s + (int64_t)a.N * m.row_scales;
-    const int steps = F::steps(a.K);
-    const int s0 = steps * warp / kMvWarps, s1 = steps * (warp + 1) / kMvWarps;
-    const uint32_t ring = smem_addr(smem) + warp * F::kRingBytes;
-
-    // Blocks in the order (rows, tokens): more tokens than columns read the same
-    // rows again at once, from L2.
-    int crow = r0, ctok = 0, cstep = s0, ctile = 0, cslot = 0;
-    bool more = s0 < s1;
-    auto copy_next = [&]() {
-        if (more) {
-            const int n = min(16 * MT, r1 - crow) - 16 * ctile;
-            const int64_t lo = crow + 16 * ctile;
-            copy_stage<GS>(ring + cslot * F::kStageBytes, m, lo, n, lo + 8, n - 8, cstep, lane);
-            cslot = cslot + 1 == F::kStages ? 0 : cslot + 1;
-            if (n <= 16 || ++ctile == MT) {
-                ctile = 0;
-                if (++cstep == s1) {
-                    cstep = s0;
-                    ctok += 8 * NT;
-                    if (ctok >= a.T) {
-                        ctok = 0;
-                        crow += 16 * MT;
-                        more = crow < r1;
-                    }
-                }
-            }
-        }
-        cp_async_commit();
+// Two halves of a range of rows make pairs; blocks in the order (rows, tokens).
+template <int GS>
+struct Matvec {
+    const MatvecArgs& a;
+    int r0, r1;
+    int block, chunk;  // rows and tokens per job
+    struct Job {
+        int pairs, tokens;
+        int row, rows, token;
     };
-    for (int s = 0; s < F::kStages - 1; ++s) copy_next();
-
-    int slot = 0, buf = 0;
-    for (int row = r0; row < r1; row += 16 * MT)
-        for (int tok = 0; tok < a.T; tok += 8 * NT) {
-            const int rows = min(16 * MT, r1 - row), tiles = (rows + 15) >> 4;
-            float acc[MT][NT][4] = {};
-            uint4 col[NT][F::kBlocks], next[NT][F::kBlocks];
-            auto columns = [&](uint4 (&c)[NT][F::kBlocks], int step) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int token = tok + 8 * n + g;
-                    const bool ok = token < a.T && step < s1;
-                    load_columns<GS, false>(c[n], a.x + (ok ? (int64_t)token * a.K + (int64_t)step * F::kStepK : 0),
-                                            a.K - step * F::kStepK, ok, t);
-                }
-            };
-            columns(next, s0);
-            for (int step = s0; step < s1; ++step) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < F::kBlocks; ++i) col[n][i] = next[n][i];
-                columns(next, step + 1);
-#pragma unroll
-                for (int tile = 0; tile < MT; ++tile)
-                    if (tile < tiles) {
-                        cp_async_wait<F::kStages - 2>();
-                        __syncwarp();  // other lanes' copies; and all reads of the slot that is filled next
-                        copy_next();
-                        const int64_t lo = row + 16 * tile + g;
-                        multiply_stage<GS, NT>(acc[tile], ring + slot * F::kStageBytes, col, scale_shift<GS>(m, lo, step),
-                                               scale_shift<GS>(m, lo + 8, step), m.row_scales - step * GS, lane);
-                        slot = slot + 1 == F::kStages ? 0 : slot + 1;
-                    }
-            }
-            // add the warps' parts in warp order
-            float* r = red + buf * kMvWarps * MT * NT * 128;
-#pragma unroll
-            for (int tile = 0; tile < MT; ++tile)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    *reinterpret_cast<float4*>(r + ((warp * MT + tile) * NT + n) * 128 + lane * 4) =
-                        make_float4(acc[tile][n][0], acc[tile][n][1], acc[tile][n][2], acc[tile][n][3]);
-            __syncthreads();  // and the other buffer's readers are done before it is written again
-            for (int i = threadIdx.x; i < MT * NT * 128; i += kMvThreads) {
-                float y = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kMvWarps; ++w) y += r[w * MT * NT * 128 + i];
-                const int l = (i >> 2) & 31, n = (i >> 7) % NT, tile = (i >> 7) / NT;
-                const int rr = 16 * tile + (l >> 2) + 8 * ((i >> 1) & 1), token = tok + 8 * n + 2 * (l & 3) + (i & 1);
-                if (rr < rows && token < a.T) {
-                    const int64_t o = (int64_t)token * a.N + row + rr;
-                    if (a.out_f32)
-                        reinterpret_cast<float*>(a.out)[o] = y;
-                    else
-                        reinterpret_cast<uint16_t*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-                }
-            }
-            buf ^= 1;
+    __device__ void at(Job& j, int row, int token) const {
+        j.row = row;
+        j.rows = min(block, r1 - row);
+        j.pairs = (j.rows + 1) / 2;
+        j.token = token;
+        j.tokens = min(chunk, a.T - token);
+    }
+    __device__ bool first(Job& j) const {
+        if (r0 >= r1) return false;
+        at(j, r0, 0);
+        return true;
+    }
+    __device__ bool next(Job& j) const {
+        if (j.token + j.tokens < a.T) {
+            at(j, j.row, j.token + j.tokens);
+            return true;
         }
-    cp_async_wait<0>();
+        if (j.row + j.rows >= r1) return false;
+        at(j, j.row + j.rows, 0);
+        return true;
+    }
+    __device__ const uint8_t* weights() const { return a.q; }
+    __device__ const uint16_t* scales() const { return a.s; }
+    __device__ int64_t rows(const Job& j) const { return j.row; }
+    __device__ int row_step(const Job& j) const { return j.rows / 2; }
+    __device__ void lost() const {}
+    __device__ const uint16_t* x(const Job& j, int token) const { return a.x + (int64_t)(j.token + token) * a.K; }
+    __device__ int key(const Job& j) const { return j.token; }
+    __device__ void store(const Job& j, int pair, int token, float first, float second) const {
+        const int64_t o = (int64_t)(j.token + token) * a.N + j.row + pair;
+        const bool both = pair > 0 || j.rows % 2 == 0;  // the middle row of an odd number is a first row
+        if (a.out_f32) {
+            float* out = reinterpret_cast<float*>(a.out) + o;
+            out[0] = first;
+            if (both) out[j.rows / 2] = second;
+        } else {
+            uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + o;
+            out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(first));
+            if (both) out[j.rows / 2] = __bfloat16_as_ushort(__float2bfloat16_rn(second));
+        }
+    }
+};
+
+template <int GS, int NT>
+__global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__ ProductPlan plan) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    Matvec<GS> jobs{a, (int)((int64_t)a.N * blockIdx.x / gridDim.x), (int)((int64_t)a.N * (blockIdx.x + 1) / gridDim.x), 0, 8 * NT};
+    const int ways = pick_ways(plan.panel, (jobs.r1 - jobs.r0 + 15) / 16);
+    jobs.block = 16 * (kMvWarps / ways);
+    run_product<GS, NT>(jobs, smem, plan, a.K, ways);
 }
 
-template <typename Kernel>
-cudaError_t launch_kernel(Kernel kernel, const MatvecArgs& a, int grid, int smem, cudaStream_t stream) {
+template <int GS, int NT>
+cudaError_t launch_kernel(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
+    const ProductPlan plan = plan_product<GS, NT>(a.K, a.T, 0);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)(a.N < num_sms ? a.N : num_sms));
     cfg.blockDim = dim3(kMvThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.dynamicSmemBytes = (size_t)plan.smem;
     cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, matvec_w4_kernel<GS, NT>, a, plan);
 }
 
 template <int GS>
 cudaError_t launch(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
-    const int grid = a.N < num_sms ? a.N : num_sms;
-    if (a.T <= 8) return launch_kernel(matvec_w4_kernel<GS, 4, 1>, a, grid, smem_bytes<GS, 4, 1>(), stream);
-    return launch_kernel(matvec_w4_kernel<GS, 2, 2>, a, grid, smem_bytes<GS, 2, 2>(), stream);
+    return a.T <= 8 ? launch_kernel<GS, 1>(a, num_sms, stream) : launch_kernel<GS, 2>(a, num_sms, stream);
 }
 
 template <int GS>
 cudaError_t set_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(matvec_w4_kernel<GS, 4, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<GS, 4, 1>());
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(matvec_w4_kernel<GS, 2, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<GS, 2, 2>());
+    cudaError_t e = cudaFuncSetAttribute(matvec_w4_kernel<GS, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(matvec_w4_kernel<GS, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     return e;
 }
 

@@ -5,16 +5,17 @@
 // Products of a few tokens with a large weight matrix read every weight once
 // and use it a handful of times, so the time is the weights' bytes over the
 // memory bandwidth.  One CTA per SM holds sixteen warps; each warp streams its
-// own share of the weights through a private ring in shared memory (16-byte
-// cp.async, six or seven stages of 16 rows x 64 bytes in flight per warp, about
-// 100 KB per SM) and multiplies them with mma.sync m16n8k16, weight rows as
-// the 16-row operand and up to eight tokens as the 8-column one.  The
-// instruction does eight columns whatever the token count, which the tensor
-// pipe has room for: 16 rows x 64 bytes are two bf16 or eight 4-bit
-// instructions per warp, against the 44 cycles that the memory takes to
-// deliver them to an SM.  A tcgen05 tile of 128 rows would need all its
-// operands in shared memory (the 4-bit codes expanded there first) and pay in
-// granularity: at one token an SM owns about 27 rows of the first product.
+// own share of the weights through a private ring in shared memory, filled by
+// bulk copies of 256-byte row segments (7.0 TB/s with three 16-row stages, a
+// copy every 10 cycles; 128-byte ones 4.2 TB/s; cp.async from the same warps
+// 5.9 TB/s, and plain loads issued behind those return behind them), and
+// multiplies them with mma.sync, weight rows as the 16-row operand and tokens as
+// the 8-column one.  A kilobyte of weights takes the memory 44 cycles to deliver
+// to an SM; the matrix instructions for it take 4 (bf16) to 16 (4-bit), so that
+// what counts is the instructions around them.  A tcgen05 tile of 128 rows would
+// need all its operands in shared memory, the 4-bit codes expanded there first,
+// and pay in granularity: at one token an SM owns about 27 rows of the first
+// product.
 #pragma once
 
 #include "arf_common.cuh"
@@ -73,66 +74,41 @@ cudaError_t launch_matvec_w4(const MatvecArgs& a, int group, int num_sms, cudaSt
 cudaError_t matvec_w4_set_attributes();
 
 // ------------------------------------------------------------ weight formats
-// A step is 64 bytes of every row of a tile: 32 bf16 values or 128 4-bit
-// codes.  GS: scale groups per step (0: bf16 weights).
+// A step is 64 bytes of a row: 32 bf16 values or 128 4-bit codes; a segment is
+// four steps.  GS: scale groups per step (0: bf16 weights).
+constexpr int kSegment = 256;
 template <int GS>
 struct Fmt {
     static constexpr bool kW4 = GS > 0;
     static constexpr int kStepK = kW4 ? 128 : 32;
-    static constexpr int kBlocks = kW4 ? 4 : 1;   // 16-byte activation loads per step and column
-    static constexpr int kScaleRow = 16;          // bytes of one row's scale window in a stage
-    static constexpr int kStageBytes = 1024 + (kW4 ? 16 * kScaleRow : 0);
-    static constexpr int kStages = kW4 ? 7 : 8;  // ring slots per warp; one less in flight
-    static constexpr int kRingBytes = kStages * kStageBytes;
-    __host__ __device__ static int64_t row_bytes(int64_t k) { return kW4 ? k / 2 : k * 2; }
-    __host__ __device__ static int steps(int k) { return (k + kStepK - 1) / kStepK; }
+    static constexpr int kSegK = 4 * kStepK;
+    __host__ __device__ static int row_bytes(int k) { return kW4 ? k / 2 : k * 2; }
+    __host__ __device__ static int segments(int k) { return (row_bytes(k) + kSegment - 1) / kSegment; }
+    __host__ __device__ static int scales(int k) { return kW4 ? k / (128 / (GS ? GS : 1)) : 0; }
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // c += A (16 x 16, row-major fragments) * B (16 x 8): bf16 operands, fp32 sums.
-__device__ __forceinline__ void mma_16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
+__device__ __forceinline__ void mma_bf16(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// Two codes of a word (nibbles 0 and 4 of w) as a pair of bf16 values code - 8.
-// 0x4300 is 128 in bf16, whose last place is 1, so or-ing a code into the
-// mantissa adds it exactly, and so does taking 136 off.
-__device__ __forceinline__ uint32_t dequant2(uint32_t w) {
-    const uint32_t v = (w & 0x000f000fu) | 0x43004300u;
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));
-    return r;
+// d = c + A * B
+__device__ __forceinline__ void mma_bf16_from(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ float lds_bf16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-    return __uint_as_float((uint32_t)v << 16);
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
+template <int WORDS>
+__device__ __forceinline__ void lds(uint32_t (&v)[WORDS], uint32_t a) {
+    if constexpr (WORDS == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a) : "memory");
+    if constexpr (WORDS == 2) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
+    if constexpr (WORDS == 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
 }
 // 16 bytes that this grid's predecessor wrote (not the read-only path).
 __device__ __forceinline__ uint4 ld_coherent16(const void* p) {
@@ -140,130 +116,621 @@ __device__ __forceinline__ uint4 ld_coherent16(const void* p) {
     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t ld_u16(const uint16_t* p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
-// One matrix of weights as the copies see it.
-struct Rows {
-    const uint8_t* q;       // packed rows
-    const uint16_t* s;      // group scales (4-bit)
-    const uint16_t* s_end;  // one past the last scale
-    int64_t row_bytes;
-    int row_scales;         // scales per row
+// A value that is the same in all lanes, in a form that the compiler knows to
+// be (branches and addresses made of it are the warp's, not the lanes').
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int warp_index() { return uniform((int)(threadIdx.x >> 5)); }
+
+// --------------------------------------------------------------------- ring
+// Rows go through the kernels in pairs: a tile is eight pairs, the first rows
+// of the pairs as rows 0-7 of the matrix instruction and the second ones as
+// rows 8-15 (a gate row and its up row; or the two halves of a range of rows,
+// which share the middle row if their number is odd).
+//
+// A ring slot holds a segment of the eight first or second rows of a tile, each
+// row 16 bytes further than it is long, so that reads of eight rows meet a bank
+// at most twice.  Rows of 128 bytes and less come several in one copy (the
+// pad then behind each copy).  Every slot has its mbarrier; the warp that fills
+// it is the one that reads it.
+constexpr int kSlotBytes = 8 * (kSegment + 16);
+constexpr int kMaxSlots = 8;
+
+struct RowShape {
+    int row_bytes, rows_per_copy, copy_stride;
+    __device__ __forceinline__ RowShape(int bytes) : row_bytes(bytes) {
+        rows_per_copy = bytes >= kSegment ? 1 : kSegment / bytes;
+        copy_stride = (bytes >= kSegment ? kSegment : rows_per_copy * bytes) + 16;
+    }
+    // Offset of row g in a slot.
+    __device__ __forceinline__ int offset(int g) const { return g / rows_per_copy * copy_stride + g % rows_per_copy * row_bytes; }
+    __device__ __forceinline__ int bytes(int segment) const { return min(kSegment, row_bytes - segment * kSegment); }
 };
 
-// Copies step `step` of the 16-row tile (rows lo .. lo+7 and hi .. hi+7, of
-// which n_lo and n_hi exist) into a ring stage.  Lane (g, t) = (lane / 4,
-// lane % 4) brings the 16 bytes t of rows g and g + 8; bytes behind the row's
-// end and rows that do not exist become zero.
-//
-// bf16: each lane reads back what it copied itself.  4-bit: the chunks of the
-// eight rows are stored side by side, so that lane (g, t) reads word t of
-// chunk b of row g without bank conflicts: one word then holds eight
-// consecutive codes, and a pair of mma covers the 32 values of chunk b, all of
-// one scale group.
-template <int GS>
-__device__ __forceinline__ void copy_stage(uint32_t stage, const Rows& m, int64_t lo, int n_lo, int64_t hi, int n_hi,
-                                           int step, int lane) {
-    using F = Fmt<GS>;
-    const int g = lane >> 2, t = lane & 3;
-    const int64_t at = (int64_t)step * 64 + t * 16;
-    const bool in_row = at < m.row_bytes;
-    const bool vl = in_row && g < n_lo, vh = in_row && g < n_hi;
-    const uint32_t dst = stage + (F::kW4 ? (t * 8 + g) * 16 : lane * 16);
-    cp_async16(dst, vl ? m.q + (lo + g) * m.row_bytes + at : m.q, vl);
-    cp_async16(dst + 512, vh ? m.q + (hi + g) * m.row_bytes + at : m.q, vh);
-    if (F::kW4) {
-        // The row's scales of this step, as the aligned 4-byte words that hold
-        // them (scales are 2-byte aligned; a step has at most four, so at most
-        // three words), 16 bytes a row.  The last word is cut at the end of the
-        // array.
-        const int r = lane & 15;
-        const bool ok = r < 8 ? r < n_lo : r - 8 < n_hi;
-        const int64_t row = r < 8 ? lo + r : hi + r - 8;
-        const int first = step * GS;
-        const uint16_t* b = m.s + (ok ? row * m.row_scales + first : 0);
-        const uint16_t* e = b + (ok ? min(GS, m.row_scales - first) : 0);
-        const uintptr_t base = reinterpret_cast<uintptr_t>(b) & ~uintptr_t(3);
-        const uint32_t sdst = stage + 1024 + r * F::kScaleRow;
+struct SlotRing {
+    uint32_t slots, bars;  // shared addresses
+    int n, fill, read;     // slots; the next to fill and to read
+    uint32_t phase;        // of the next to read
+    bool alive;            // no wait has run out
+
+    __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int lane)
+        : slots(slots), bars(bars), n(n), fill(0), read(0), phase(0), alive(true) {
+        if (lane < n) mbar_init(bars + lane * 8, 1);
+        fence_mbar_init();
+        __syncwarp();
+    }
+    // Copies `rows` rows' segment at `at` (of the first row).
+    __device__ __forceinline__ void copy(const RowShape& shape, const uint8_t* at, int rows, int bytes, int lane) {
+        const uint32_t bar = bars + fill * 8, dst = slots + fill * kSlotBytes;
+        if (lane == 0) mbar_arrive_expect_tx(bar, rows * bytes);
+        __syncwarp();
+        const int first = lane * shape.rows_per_copy;
+        if (first < rows)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             dst + lane * shape.copy_stride),
+                         "l"(at + (int64_t)first * shape.row_bytes), "r"(min(shape.rows_per_copy, rows - first) * bytes), "r"(bar)
+                         : "memory");
+        fill = fill + 1 == n ? 0 : fill + 1;
+    }
+    // Waits for the next slot and returns its address.  A wait that runs out
+    // (nothing but a lost copy makes it) ends the waiting for good.
+    __device__ __forceinline__ uint32_t wait() {
+        const uint32_t at = slots + read * kSlotBytes;
+        if (alive) alive = mbar_wait_bounded(bars + read * 8, phase, nullptr);
+        if (++read == n) {
+            read = 0;
+            phase ^= 1;
+        }
+        return at;
+    }
+};
+
+// ------------------------------------------------------------ products, bf16
+// The activations that meet a segment, one segment ahead in registers: lane (g,
+// t) = (lane / 4, lane % 4) holds values 8t .. 8t+7 of every 32 of column g.  A
+// column that does not exist may repeat one that does.
+template <bool COHERENT>
+__device__ __forceinline__ uint4 load_column(const uint16_t* p, int left, int t) {
+    if (8 * t >= left) return make_uint4(0, 0, 0, 0);
+    return COHERENT ? ld_coherent16(p + 8 * t) : ld_early16(p + 8 * t);
+}
+
+// acc += (tile) * (columns), one segment; lo, hi: the lane's rows in the slots.
+// load(q) replaces step q of the columns by a later segment's.  bytes: of the
+// segment; what lies behind them in the slots may be anything.
+template <class Load>
+__device__ __forceinline__ void multiply_bf16(float (&acc)[4], uint32_t lo, uint32_t hi, uint4 (&b)[4], int bytes, int t, Load load) {
+    if (bytes == kSegment) {
+        float odd[4] = {};
 #pragma unroll
-        for (int w0 = 0; w0 < (GS == 4 ? 3 : 2); w0 += 2) {
-            const int w = w0 + (lane >> 4);
-            const uintptr_t p = base + 4 * w;
-            if (p < reinterpret_cast<uintptr_t>(e)) {
-                const int64_t left = (int64_t)(reinterpret_cast<uintptr_t>(m.s_end) - p);
-                cp_async4(sdst + 4 * w, reinterpret_cast<const void*>(p), left >= 4 ? 4 : 2);
+        for (int q = 0; q < 4; ++q) {
+            uint32_t l[4], h[4];
+            lds(l, lo + q * 64 + t * 16);
+            lds(h, hi + q * 64 + t * 16);
+            mma_bf16(acc, l[0], h[0], l[1], h[1], b[q].x, b[q].y);
+            mma_bf16(odd, l[2], h[2], l[3], h[3], b[q].z, b[q].w);
+            load(q);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[u] += odd[u];
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q * 64 < bytes) {
+                uint32_t l[4] = {}, h[4] = {};
+                if (q * 64 + t * 16 < bytes) {
+                    lds(l, lo + q * 64 + t * 16);
+                    lds(h, hi + q * 64 + t * 16);
+                }
+                mma_bf16(acc, l[0], h[0], l[1], h[1], b[q].x, b[q].y);
+                mma_bf16(acc, l[2], h[2], l[3], h[3], b[q].z, b[q].w);
+            }
+            load(q);
+        }
+    }
+}
+
+// ----------------------------------------------------------- products, 4-bit
+// 4-bit codes need no conversion.  A code in the low four bits of a bf16 is the
+// subnormal number code * 2^-133, and one in bits 4-7 is code * 2^-129, since
+// the smallest normal binade keeps the subnormals' spacing; the matrix
+// instruction takes both exactly (measured: errors of 2^-23 of the sum of
+// magnitudes, as for normal operands).  So one AND takes two codes out of a
+// word, with one shift for half of them.  The activations are multiplied by a
+// power of two that puts the largest of the step's 128 values of a token into
+// [2^90, 2^91) (by 2^-4 of that where they meet codes in bits 4-7), so that all
+// products are normal numbers; a factor per column brings a step's sum back.
+// The columns' own sums times -8 are where the groups' sums start from.
+// (Or-ing the codes into the mantissa of 128 and taking 136 off takes twice the
+// instructions per code; e4m3 operands, which would take half the ANDs, are
+// converted to half precision by the compiler first: 14 more per instruction.)
+//
+// A lane reads the codes that stand for 32 / GS consecutive values of every
+// scale group of a step, in one word per eight, so that each matrix instruction
+// stays within a group.
+//
+// In shared memory the values lie as the instructions take them: of every column
+// the steps one after the other, 256 bytes each, in four parts (one per word of
+// codes that a lane reads) of 16 bytes a lane: values (0, 4) (1, 5) (2, 6) (3,
+// 7) of eight.  Columns are 64 bytes further apart than that, so that reads of
+// two of them meet no bank twice.
+template <int GS, int NT>
+struct StagedView {
+    static constexpr int kSums = GS * 8 * NT * 4;  // bytes per step
+    uint32_t values, sums, factors;                // shared addresses
+    int stride;                                    // between columns
+    // `segments` of `columns` tokens: bytes in all
+    __host__ __device__ static int bytes(int segments, int columns) {
+        return columns * (segments * 1024 + 64) + segments * (4 * kSums + 8 * NT * 4);
+    }
+    __device__ __forceinline__ StagedView(uint32_t at, int segments, int columns) {
+        values = at;
+        stride = segments * 1024 + 64;
+        sums = at + columns * stride;
+        factors = sums + segments * 4 * kSums;
+    }
+};
+
+__device__ __forceinline__ void sts_f32(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ float2 lds_f32x2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// One warp: a segment (512 bf16 values) of a token into column `col`; of step q
+// the lane holds values 4 * lane .. + 3 in w[q] (zero behind the end of the row).
+template <int GS, int NT>
+__device__ __forceinline__ void stage_segment(const StagedView<GS, NT>& v, int segment, int col, const uint2 (&w)[4], int lane) {
+    float big = 0.0f;
+    bool undefined = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float v0 = fabsf(__uint_as_float(w[q].x << 16)), v1 = fabsf(__uint_as_float(w[q].x & 0xffff0000u));
+        const float v2 = fabsf(__uint_as_float(w[q].y << 16)), v3 = fabsf(__uint_as_float(w[q].y & 0xffff0000u));
+        big = fmaxf(big, fmaxf(fmaxf(v0, v1), fmaxf(v2, v3)));
+        undefined = undefined || v0 != v0 || v1 != v1 || v2 != v2 || v3 != v3;
+    }
+    const unsigned top = __reduce_max_sync(0xffffffffu, undefined || !(big < INFINITY) ? 0x7f800000u : __float_as_uint(big)) >> 23;
+    const bool bad = top == 255;  // an infinite or undefined activation: so is every sum it is in
+    // 2^(up - 127) * 2^(top - 127) = 2^90, as far as bf16 goes
+    const unsigned up = bad ? 127u : min(344u - top, 254u);
+    const uint32_t one = up << 7 | up << 23, sixteenth = (up - 4) << 7 | (up - 4) << 23;
+    const int odd = lane & 1;  // an even lane holds values 0-3 of eight, an odd one 4-7
+    const int u = lane >> 1;   // word of eight values: word i of lane t
+    constexpr int kPer = 4 / GS;
+    const int t = u / kPer % 4, i = u / (4 * kPer) * kPer + u % kPer;
+    const uint32_t at = v.values + col * v.stride + segment * 1024 + i * 64 + t * 16 + odd * 8;
+    const float minus8 = __uint_as_float(up << 23) * (-8.0f * 0x1p-126f) * 0x1p-7f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w[q].x : w[q].y, 1);
+        const uint32_t a = odd ? other : w[q].x, b = odd ? w[q].y : other;
+        const uint32_t c0 = mul_bf16x2(__byte_perm(a, b, 0x5410), one), c1 = mul_bf16x2(__byte_perm(a, b, 0x7632), sixteenth);
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + q * 256), "r"(c0), "r"(c1) : "memory");
+        // -8 * 2^-133 times the scaled values' sum, in each group
+        float sum = (__uint_as_float(w[q].x << 16) + __uint_as_float(w[q].x & 0xffff0000u)) +
+                    (__uint_as_float(w[q].y << 16) + __uint_as_float(w[q].y & 0xffff0000u));
+#pragma unroll
+        for (int o = 1; o < 32 / GS; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane % (32 / GS) == 0)
+            sts_f32(v.sums + (segment * 4 + q) * v.kSums + lane / (32 / GS) * 32 * NT + col * 4, sum * minus8);
+    }
+    if (lane == 0)
+        sts_f32(v.factors + (segment * 8 * NT + col) * 4,
+                bad ? __uint_as_float(0x7fc00000u) : 0x1p127f / __uint_as_float(up << 23) * 0x1p6f);
+}
+
+// Where the products take their columns from: words(n, q, s, c, eight) gives the
+// lane's values of scale group s of step q and what the group's sums start from,
+// factor(n) what the sums are multiplied by.
+//
+// Staged in shared memory: a segment.
+template <int GS, int NT>
+struct StagedColumns {
+    uint32_t values[NT], sums, factors;
+    __device__ __forceinline__ StagedColumns(const StagedView<GS, NT>& v, int columns, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) values[n] = v.values + (8 * n + g < columns ? 8 * n + g : 0) * v.stride + t * 16;
+        sums = v.sums + t * 8;
+        factors = v.factors + t * 8;
+    }
+    __device__ __forceinline__ StagedColumns at(int segment) const {
+        StagedColumns c = *this;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c.values[n] += segment * 1024;
+        c.sums += segment * 4 * StagedView<GS, NT>::kSums;
+        c.factors += segment * 32 * NT;
+        return c;
+    }
+    __device__ __forceinline__ void words(int n, int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
+#pragma unroll
+        for (int j = 0; j < 4 / GS; ++j) lds(c[j], values[n] + q * 256 + (s * (4 / GS) + j) * 64);
+        eight = lds_f32x2(sums + q * StagedView<GS, NT>::kSums + (s * NT + n) * 32);
+    }
+    __device__ __forceinline__ float2 factor(int n) const { return lds_f32x2(factors + n * 32); }
+};
+
+// Straight from global memory, one step ahead in registers: v[i] holds the eight
+// values of lane (g, t) that meet its word i.  The power of two is 2^64 whatever
+// the values (sums keep 24 bits while these are between 2^-56 and 2^63), and -8
+// times the sums comes from the matrix instruction with a constant operand.
+template <int GS>
+struct DirectColumns {
+    uint4 v[4];
+    __device__ __forceinline__ void load(const uint16_t* p, int left, int t) {
+        constexpr int kPer = 4 / GS;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = 32 * kPer * (i / kPer) + 8 * kPer * t + 8 * (i % kPer);
+            if (left >= Fmt<GS>::kStepK) {
+                v[i] = ld_coherent16(p + at);
+            } else {
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (at < left) v[i] = ld_coherent16(p + at);
             }
         }
     }
-}
-
-// Activations of one step for one 8-column tile: lane (g, t) holds values
-// 8t .. 8t+7 of every 32 of column g (p: the column's first value of the step;
-// left: values from there to the end of the row; zeros beyond, and for a
-// column that does not exist).
-template <int GS, bool COHERENT>
-__device__ __forceinline__ void load_columns(uint4 b[Fmt<GS>::kBlocks], const uint16_t* p, int left, bool ok, int t) {
+    __device__ __forceinline__ void words(int, int, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
+        constexpr uint32_t kUp64 = 0x5f805f80u, kUp60 = 0x5d805d80u;  // 2^64 and 2^60, twice
+        constexpr uint32_t kMinus8 = 0x80088008u, kMinus8x16 = 0x80808080u;
+        float sum[4];
 #pragma unroll
-    for (int i = 0; i < Fmt<GS>::kBlocks; ++i) {
-        const int at = 32 * i + 8 * t;
-        b[i] = make_uint4(0, 0, 0, 0);
-        if (ok && at < left) b[i] = COHERENT ? ld_coherent16(p + at) : ld_early16(p + at);
-    }
-}
-
-// The products of a stage: acc[nt] += tile (16 rows x one step) * columns.
-// shift_lo, shift_hi: bytes from the scale window's start to the step's first
-// scale, for the rows of each half.  groups: scale groups from the step's start
-// to the end of the row; what lies behind them in a stage is not looked at (it
-// may be the next row's, and zero columns times an infinite scale are not zero).
-template <int GS, int NT>
-__device__ __forceinline__ void multiply_stage(float (&acc)[NT][4], uint32_t stage, const uint4 (&b)[NT][Fmt<GS>::kBlocks],
-                                               int shift_lo, int shift_hi, int groups, int lane) {
-    using F = Fmt<GS>;
-    if constexpr (!F::kW4) {
-        const uint4 lo = lds128(stage + lane * 16), hi = lds128(stage + 512 + lane * 16);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            mma_16816(acc[n], lo.x, hi.x, lo.y, hi.y, b[n][0].x, b[n][0].y);
-            mma_16816(acc[n], lo.z, hi.z, lo.w, hi.w, b[n][0].z, b[n][0].w);
+        for (int j = 0; j < 4 / GS; ++j) {
+            const uint4 w = v[s * (4 / GS) + j];
+            c[j][0] = mul_bf16x2(__byte_perm(w.x, w.z, 0x5410), kUp64);
+            c[j][1] = mul_bf16x2(__byte_perm(w.x, w.z, 0x7632), kUp60);
+            c[j][2] = mul_bf16x2(__byte_perm(w.y, w.w, 0x5410), kUp64);
+            c[j][3] = mul_bf16x2(__byte_perm(w.y, w.w, 0x7632), kUp60);
+            if (j == 0)
+                mma_bf16_from(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][0], c[j][1], 0.f, 0.f, 0.f, 0.f);
+            else
+                mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][0], c[j][1]);
+            mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][2], c[j][3]);
         }
-    } else {
-        const int g = lane >> 2, t = lane & 3;
-        const uint32_t at = stage + g * 16 + t * 4, sc = stage + 1024 + g * F::kScaleRow;
-        constexpr int kPer = 4 / GS;  // 32-value blocks per scale group (within the step)
+        eight = make_float2(sum[0], sum[1]);
+    }
+    __device__ __forceinline__ float2 factor(int) const { return make_float2(0x1p69f, 0x1p69f); }
+};
+
+// ------------------------------------------------------------------- scales
+// bf16 group scales of a segment's rows, one segment ahead in registers: lane
+// (g, t) holds those of step t for the first and second row of pair g.
+template <int GS>
+struct Scales {
+    static constexpr int kWords = GS == 4 ? 2 : 1;
+    uint32_t raw[2][kWords];
+    // p0, p1: the lane's first scale in its two rows; groups: from there to the end of the row (zeros behind it); wide:
+    // they are aligned to their size
+    __device__ __forceinline__ void load(const uint16_t* p0, const uint16_t* p1, int groups, bool wide) {
 #pragma unroll
-        for (int s = 0; s < GS; ++s) {
-            if (s >= groups) break;
-            float part[NT][4] = {};
+        for (int h = 0; h < 2; ++h) {
+            const uint16_t* p = h ? p1 : p0;
+            uint32_t* r = raw[h];
+            if (GS == 1) {
+                r[0] = groups > 0 ? ld_u16(p) : 0;
+            } else if (wide) {  // then a step has all its groups or none
+                if constexpr (GS == 2) r[0] = groups > 0 ? ld_early4(p) : 0;
+                if constexpr (GS == 4) {
+                    const uint2 v = groups > 0 ? ld_early8(p) : make_uint2(0, 0);
+                    r[0] = v.x;
+                    r[kWords - 1] = v.y;
+                }
+            } else {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int i = s * kPer + j;
-                const uint32_t lo = lds32(at + i * 128), hi = lds32(at + 512 + i * 128);
-                const uint32_t l0 = dequant2(lo), l1 = dequant2(lo >> 4), l2 = dequant2(lo >> 8), l3 = dequant2(lo >> 12);
-                const uint32_t h0 = dequant2(hi), h1 = dequant2(hi >> 4), h2 = dequant2(hi >> 8), h3 = dequant2(hi >> 12);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 v = b[n][i];  // values (0,1) (2,3) (4,5) (6,7); a code pair is (i, i + 4)
-                    mma_16816(part[n], l0, h0, l1, h1, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
-                    mma_16816(part[n], l2, h2, l3, h3, __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+                for (int w = 0; w < kWords; ++w) {
+                    r[w] = 2 * w < groups ? ld_u16(p + 2 * w) : 0;
+                    if (2 * w + 1 < groups) r[w] |= ld_u16(p + 2 * w + 1) << 16;
                 }
             }
-            const float sl = lds_bf16(sc + shift_lo + 2 * s), sh = lds_bf16(sc + 8 * F::kScaleRow + shift_hi + 2 * s);
+        }
+    }
+    // Scale of group s of step q for the lane's row.
+    __device__ __forceinline__ float get(int h, int q, int s, int lane) const {
+        const uint32_t w = __shfl_sync(0xffffffffu, raw[h][s / 2], (lane & ~3) | q);
+        return __uint_as_float(s & 1 ? w & 0xffff0000u : w << 16);
+    }
+};
+
+// sum[n] += (tile) * (column tile n), step q of a segment; lo, hi: the lane's
+// rows in the slots.  Without the columns' factors.
+template <int GS, int NT, class Columns>
+__device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t lo, uint32_t hi, const Columns& columns,
+                                            const Scales<GS>& sc, int q, int lane) {
+    const int t = lane & 3;
+    constexpr int kPer = 4 / GS;  // words of a lane per scale group
+    constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+#pragma unroll
+    for (int s = 0; s < GS; ++s) {
+        const int at = q * 64 + s * 16 * kPer + t * 4 * kPer;
+        uint32_t c[NT][kPer][4], l[kPer], h[kPer];
+        float2 eight[NT];
+        lds(l, lo + at);
+        lds(h, hi + at);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) columns.words(n, q, s, c[n], eight[n]);
+        // two chains of matrix instructions
+        float part[NT][4], more[NT][4];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t l8 = l[j] >> 8, h8 = h[j] >> 8;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(sl, part[n][0], acc[n][0]);
-                acc[n][1] = fmaf(sl, part[n][1], acc[n][1]);
-                acc[n][2] = fmaf(sh, part[n][2], acc[n][2]);
-                acc[n][3] = fmaf(sh, part[n][3], acc[n][3]);
+                if (j == 0) {
+                    mma_bf16_from(part[n], l[j] & kLow, h[j] & kLow, l[j] & kHigh, h[j] & kHigh, c[n][j][0], c[n][j][1], eight[n].x,
+                                  eight[n].y, eight[n].x, eight[n].y);
+                    mma_bf16_from(more[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3], 0.f, 0.f, 0.f, 0.f);
+                } else {
+                    mma_bf16(part[n], l[j] & kLow, h[j] & kLow, l[j] & kHigh, h[j] & kHigh, c[n][j][0], c[n][j][1]);
+                    mma_bf16(more[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3]);
+                }
             }
         }
+        const float sl = sc.get(0, q, s, lane), sh = sc.get(1, q, s, lane);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sum[n][u] = fmaf(u < 2 ? sl : sh, part[n][u] + more[n][u], sum[n][u]);
+    }
+}
+template <int NT, class Columns>
+__device__ __forceinline__ void add_scaled(float (&acc)[NT][4], const float (&sum)[NT][4], const Columns& columns) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float2 f = columns.factor(n);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[n][u] = fmaf(u & 1 ? f.y : f.x, sum[n][u], acc[n][u]);
     }
 }
 
-// Bytes from a row's aligned scale window to its first scale of the step.
-template <int GS>
-__device__ __forceinline__ int scale_shift(const Rows& m, int64_t row, int step) {
-    if constexpr (GS == 0) return 0;
-    return (int)(((unsigned)row * (unsigned)m.row_scales + (unsigned)(step * GS)) & 1u) * 2;
+// ----------------------------------------------------------------- products
+// How the sixteen warps of a CTA share tiles: `ways` of them split a tile's
+// segments, 16 / ways tiles go side by side.  The least work for the busiest
+// warp; among equals the fewest rounds (each costs a reduction, and 4-bit weights
+// of many tokens their activations again), then the most ways.
+__host__ __device__ inline int pick_ways(int segments, int tiles) {
+    int best = 16, cost = 0x7fffffff;
+    for (int w = 16; w >= 1; w >>= 1) {
+        const int rounds = (tiles * w + 15) / 16, c = (segments + w - 1) / w * rounds * 64 + (rounds < 63 ? rounds : 63);
+        if (c < cost) {
+            cost = c;
+            best = w;
+        }
+    }
+    return best;
+}
+
+// Shared memory of a product: barriers, two buffers of partial tiles, staged
+// activations, `extra` bytes, the rings.
+constexpr int kSmemLimit = 227 * 1024;
+struct ProductPlan {
+    int panel;    // segments whose activations are staged at a time
+    int columns;  // staged columns
+    int staged;   // bytes
+    int extra;    // bytes, at extra_at
+    int slots;    // per warp
+    int extra_at, ring_at, smem;
+};
+template <int GS, int NT>
+inline ProductPlan plan_product(int K, int tokens, int extra) {
+    ProductPlan p;
+    const int segments = Fmt<GS>::segments(K), fixed = kMvWarps * kMaxSlots * 8 + 2 * kMvWarps * NT * 512 + extra;
+    p.extra = extra;
+    p.columns = tokens < 8 * NT ? tokens : 8 * NT;
+    p.panel = segments;
+    p.staged = 0;
+    if (GS > 0) {
+        // at least four slots per warp
+        using View = StagedView<GS ? GS : 1, NT>;
+        const int none = View::bytes(0, p.columns), each = View::bytes(1, p.columns) - none;
+        const int most = (kSmemLimit - fixed - 4 * kMvWarps * kSlotBytes - none) / each;
+        const int panels = (segments + most - 1) / most;
+        p.panel = (segments + panels - 1) / panels;
+        p.staged = (View::bytes(p.panel, p.columns) + 15) / 16 * 16;
+    }
+    p.extra_at = fixed - extra + p.staged;
+    p.ring_at = (p.extra_at + extra + 127) / 128 * 128;
+    const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlotBytes);
+    p.slots = slots < kMaxSlots ? slots : kMaxSlots;
+    p.smem = p.ring_at + p.slots * kMvWarps * kSlotBytes;
+    return p;
+}
+
+// The products of blocks of row pairs with up to 8 * NT tokens each, one block
+// ("job") after the other, the copies running ahead across their borders.  Jobs
+// is a class with
+//   struct Job { int pairs, tokens; .. }: at most 8 * 16 / ways pairs, at least one token
+//   bool first(Job&), next(Job&)          the CTA's jobs in order
+//   rows(job), row_step                   first row of the first pair, rows between a pair's rows
+//   weights(), scales()                   row 0 of all
+//   x(job, token), key(job)               a token's activations; equal keys: the same tokens
+//   store(job, pair, token, first, second)  results of a pair's two rows
+//   lost()                                a wait ran out
+// Deterministic: a tile's sums are added in the order of the ways.
+template <int GS, int NT, class Jobs>
+__device__ __forceinline__ void run_product(const Jobs& jobs, uint8_t* smem, const ProductPlan& plan, int K, int ways) {
+    using F = Fmt<GS>;
+    using Job = typename Jobs::Job;
+    static_assert(F::kW4 || NT == 1, "bf16 weights: one column tile");
+    constexpr int kGS = GS ? GS : 1;
+    constexpr int kRed = kMvWarps * NT * 128;  // floats, one buffer
+    constexpr int kRedAt = kMvWarps * kMaxSlots * 8, kStagedAt = kRedAt + 2 * kRed * 4;
+    float* red = reinterpret_cast<float*>(smem + kRedAt);
+    const StagedView<kGS, NT> staged(smem_addr(smem) + kStagedAt, plan.panel, plan.columns);
+    const StagedColumns<kGS, NT> staged_columns(staged, plan.columns, threadIdx.x & 31);
+    const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
+    const RowShape shape(F::row_bytes(K));
+    const int row_scales = F::scales(K), segments = F::segments(K), panel = plan.panel;
+    const bool wide = row_scales % kGS == 0;
+    const int split = 31 - __clz(ways);  // ways is a power of two
+    const int mine = warp >> split, way = warp & (ways - 1);  // tile; segments way, way + ways, .. of a panel
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
+    const int row_at = shape.offset(g);
+
+    auto to = [&](int p) { return min(p + panel, segments); };
+    // The warp's first segment of the panels from p on; `segments` or more: none.
+    auto first_from = [&](int p) {
+        while (p < segments && p + way >= to(p)) p += panel;
+        return p + way;
+    };
+    auto pairs_of = [&](const Job& j) { return min(8, j.pairs - 8 * mine); };  // of the warp's tile; none if not positive
+
+    // Copies: the next half (job, panel, segment, first or second rows).
+    Job cj;
+    bool more = jobs.first(cj);
+    if (!more) return;
+    int cpanel = 0, cseg = way, cpairs = 0, chalf = 0;
+    const uint8_t* cbase = nullptr;
+    int64_t cstep = 0;  // bytes between a pair's rows
+    auto enter = [&]() {
+        cpairs = pairs_of(cj);
+        cbase = jobs.weights() + (jobs.rows(cj) + 8 * mine) * shape.row_bytes;
+        cstep = (int64_t)jobs.row_step(cj) * shape.row_bytes;
+    };
+    auto settle = [&]() {  // to the first segment from here on
+        while (more && (cpairs <= 0 || cseg >= to(cpanel))) {
+            cpanel += panel;
+            if (cpairs <= 0 || cpanel >= segments) {
+                cpanel = 0;
+                more = jobs.next(cj);
+                if (more) enter();
+            }
+            cseg = cpanel + way;
+        }
+    };
+    auto copy_half = [&]() {
+        if (!more) return;
+        ring.copy(shape, cbase + cseg * kSegment + (chalf ? cstep : 0), cpairs, shape.bytes(cseg), lane);
+        chalf ^= 1;
+        if (chalf == 0) {
+            cseg += ways;
+            if (cseg >= to(cpanel)) settle();
+        }
+    };
+    enter();
+    settle();
+    for (int s = 0; s < plan.slots; ++s) copy_half();
+
+    // Operands of the next segment, asked for one segment ahead, across panels and jobs.
+    uint4 col[4];
+    Scales<kGS> next;
+    const uint16_t* x = nullptr;
+    const uint16_t *scale0 = nullptr, *scale1 = nullptr;
+    auto load_step = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK + q * F::kStepK, K - segment * F::kSegK - q * F::kStepK, t); };
+    auto load_scales = [&](int segment) {
+        const int at = (segment * 4 + t) * kGS;
+        next.load(scale0 + at, scale1 + at, row_scales - at, wide);
+    };
+    auto begin_job = [&](const Job& j) {
+        const int first = first_from(0);
+        if constexpr (F::kW4) {
+            scale0 = jobs.scales() + (jobs.rows(j) + max(0, min(8 * mine + g, j.pairs - 1))) * row_scales;
+            scale1 = scale0 + (int64_t)jobs.row_step(j) * row_scales;
+            load_scales(first);
+        } else {
+            x = jobs.x(j, g < j.tokens ? g : 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) load_step(first, q);
+        }
+    };
+    auto stage = [&](const Job& j, int p) {
+        const int units = (to(p) - p) * j.tokens;  // (segment, token)
+        __syncthreads();                           // the panel before it is done with
+        for (int i = warp; i < units; i += kMvWarps) {
+            const int s = i / j.tokens, token = i - s * j.tokens;
+            const uint16_t* from = jobs.x(j, token);
+            uint2 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = (p + s) * F::kSegK + q * F::kStepK + lane * 4;
+                w[q] = make_uint2(0, 0);
+                if (k < K) w[q] = ld_early8(from + k);
+            }
+            stage_segment<kGS, NT>(staged, s, token, w, lane);
+        }
+        __syncthreads();
+    };
+    Job job;
+    jobs.first(job);
+    begin_job(job);
+    int key = -1;
+    for (int buf = 0;; buf ^= 1) {
+        float acc[NT][4] = {};
+        const int pairs = pairs_of(job);
+        for (int p = 0; p < segments; p += panel) {
+            if (F::kW4 && (panel < segments || jobs.key(job) != key)) {
+                key = jobs.key(job);
+                stage(job, p);
+            }
+            if (pairs <= 0) continue;
+            const int end = to(p), behind = first_from(p + panel);
+            for (int seg = p + way; seg < end; seg += ways) {
+                const int after = seg + ways < end ? seg + ways : behind, bytes = shape.bytes(seg);
+                const uint32_t lo = ring.wait() + row_at, hi = ring.wait() + row_at;
+                if constexpr (F::kW4) {
+                    const Scales<kGS> now = next;
+                    load_scales(after);
+                    const StagedColumns<kGS, NT> columns = staged_columns.at(seg - p);
+                    float sum[NT][4] = {};
+                    if (bytes == kSegment) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) multiply_w4<kGS, NT>(sum, lo, hi, columns, now, q, lane);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (q * 64 < bytes) multiply_w4<kGS, NT>(sum, lo, hi, columns, now, q, lane);
+                    }
+                    add_scaled(acc, sum, columns);
+                } else {
+                    float(&one)[4] = acc[0];
+                    multiply_bf16(one, lo, hi, col, bytes, t, [&](int q) { load_step(after, q); });
+                }
+                __syncwarp();  // all lanes have read both slots
+                copy_half();
+                copy_half();
+            }
+        }
+        const Job done = job;
+        const bool end = !jobs.next(job);
+        if (!end) begin_job(job);
+        if (!ring.alive) {
+            jobs.lost();
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = __uint_as_float(0x7fc00000u);
+        }
+        // add the ways' parts in order
+        float* r = red + buf * kRed;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<float4*>(r + (warp * NT + n) * 128 + lane * 4) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+        __syncthreads();  // and the other buffer's readers are done before it is written again
+        constexpr int kPairs = 64 * NT;  // (pair, token) per tile
+        for (int i = threadIdx.x; i < (done.pairs + 7) / 8 * kPairs; i += kMvThreads) {
+            const int tile = i / kPairs, n = i % kPairs / 64, l = i % 64;  // l: two columns of a lane's first row
+            const int pair = 8 * tile + (l >> 3), token = 8 * n + (l & 7);
+            if (pair >= done.pairs || token >= done.tokens) continue;
+            const float* q = r + ((tile << split) * NT + n) * 128 + (l >> 1) * 4 + (l & 1);
+            float first = 0.0f, second = 0.0f;
+            for (int w = 0; w < ways; ++w) {
+                first += q[w * NT * 128];
+                second += q[w * NT * 128 + 2];
+            }
+            jobs.store(done, pair, token, first, second);
+        }
+        if (end) break;
+    }
+    if (!ring.alive) grace_period(10000000ull);  // copies that may still land
 }
 
 }  // namespace arf

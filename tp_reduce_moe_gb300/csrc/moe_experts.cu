@@ -11,49 +11,61 @@
 //
 // The activations travel as a bf16 high part and a bf16 low part (16 bits of
 // mantissa together), columns 0-3 and 4-7 of the matrix instruction's eight:
-// rounding them to one bf16 would double the result's error against 32-bit
-// arithmetic, and up to four tokens per expert the second part costs nothing.
+// rounding them to one bf16 would make the result's error 1.4 times that of its
+// own rounding, and up to four tokens per expert the second part costs nothing.
 #include "moe_common.cuh"
 
 namespace arf {
 namespace {
 
-constexpr int kPairTiles = 2;      // 16-row tiles (8 gate rows, 8 up rows) per block of the first kernel
-constexpr int kChunk1 = 8;         // tokens per item of the first kernel
-constexpr int kChunk2 = 4;         // and of the second (high and low part)
+constexpr int kChunk1 = 8;  // tokens per item of the first kernel
+constexpr int kChunk2 = 4;  // and of the second
 
 // The chosen experts, in order, each with the tokens that chose it, in order,
-// cut into items of up to `chunk` tokens.
+// cut into items of up to `chunk` tokens.  In shared memory, for `slots` = T * K
+// entries.
 struct Items {
-    uint16_t expert[kMoeMaxSlots];
-    uint16_t off[kMoeMaxSlots];     // first entry
-    uint8_t n[kMoeMaxSlots];
-    uint16_t slot[kMoeMaxSlots];    // entries: token * K + k
-    float w[kMoeMaxSlots];          // entries: routing weight
-    uint16_t at[kMoeMaxExperts];    // an expert's first entry
-    uint32_t mask[kMoeMaxExperts][2];  // tokens that chose it
-    int warp_items[kMvWarps], warp_entries[kMvWarps];
-    int count;
+    float* w;          // entries: routing weight
+    uint16_t* slot;    // entries: token * K + k
+    uint16_t* expert;  // items
+    uint16_t* off;     // items: first entry
+    uint16_t* at;      // experts: first entry
+    int* part;         // sums over the warps, then the number of items
+    uint8_t* token;    // entries
+    uint8_t* n;        // items: entries
+    __host__ __device__ static int bytes(int slots, int experts) { return (slots * 12 + experts * 2 + (2 * kMvWarps + 1) * 4 + 15) / 16 * 16; }
+    __device__ Items(uint8_t* p, int slots, int experts) {
+        w = reinterpret_cast<float*>(p);
+        part = reinterpret_cast<int*>(w + slots);
+        slot = reinterpret_cast<uint16_t*>(part + 2 * kMvWarps + 1);
+        expert = slot + slots;
+        off = expert + slots;
+        at = off + slots;
+        token = reinterpret_cast<uint8_t*>(at + experts);
+        n = token + slots;
+    }
+    __device__ int count() const { return uniform(part[2 * kMvWarps]); }
 };
 
 // Called by all threads of a CTA.  A token that names an expert twice gets one
 // entry with the sum of its weights.  -1 names no expert; other values outside
-// [0, E) are skipped too and flagged.
-__device__ void build_items(Items& it, const ExpertsArgs& a, int chunk) {
+// [0, E) are skipped too and flagged.  mask: scratch, two words per expert (the
+// tokens that chose it), free again afterwards.
+__device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsArgs& a, int chunk) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slots = a.T * a.K;
-    for (int e = tid; e < a.E; e += kMvThreads) it.mask[e][0] = it.mask[e][1] = 0;
+    for (int e = tid; e < a.E; e += kMvThreads) mask[e][0] = mask[e][1] = 0;
     __syncthreads();
     for (int s = tid; s < slots; s += kMvThreads) {
         const int e = a.ids[s], t = s / a.K;
         if ((unsigned)e < (unsigned)a.E)
-            atomicOr(&it.mask[e][t >> 5], 1u << (t & 31));
+            atomicOr(&mask[e][t >> 5], 1u << (t & 31));
         else if (e != -1)
             atomicOr(a.err, kErrExpertRange);
     }
     __syncthreads();
     static_assert(kMoeMaxExperts <= kMvThreads, "one expert per thread");
-    const int n = tid < a.E ? __popc(it.mask[tid][0]) + __popc(it.mask[tid][1]) : 0;
+    const int n = tid < a.E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
     const int m = (n + chunk - 1) / chunk;
     int ni = m, ne = n;  // inclusive sums over the warp
 #pragma unroll
@@ -65,15 +77,15 @@ __device__ void build_items(Items& it, const ExpertsArgs& a, int chunk) {
         }
     }
     if (lane == 31) {
-        it.warp_items[warp] = ni;
-        it.warp_entries[warp] = ne;
+        it.part[warp] = ni;
+        it.part[kMvWarps + warp] = ne;
     }
     __syncthreads();
     for (int w = 0; w < warp; ++w) {
-        ni += it.warp_items[w];
-        ne += it.warp_entries[w];
+        ni += it.part[w];
+        ne += it.part[kMvWarps + w];
     }
-    if (tid == kMvThreads - 1) it.count = ni;
+    if (tid == kMvThreads - 1) it.part[2 * kMvWarps] = ni;
     if (n > 0) {
         it.at[tid] = ne - n;
         for (int j = 0; j < m; ++j) {
@@ -92,310 +104,295 @@ __device__ void build_items(Items& it, const ExpertsArgs& a, int chunk) {
         float w = a.weights[s];
         for (int j = k + 1; j < a.K; ++j)
             if (a.ids[t * a.K + j] == e) w += a.weights[t * a.K + j];
-        const uint32_t low = it.mask[e][0], high = it.mask[e][1];
+        const uint32_t low = mask[e][0], high = mask[e][1];
         const int before = t < 32 ? __popc(low & ((1u << t) - 1)) : __popc(low) + __popc(high & ((1u << (t - 32)) - 1));
         it.slot[it.at[e] + before] = s;
+        it.token[it.at[e] + before] = t;
         it.w[it.at[e] + before] = w;
     }
     __syncthreads();
 }
 
-template <int GS>
-constexpr int smem1() {
-    return kMvWarps * Fmt<GS>::kRingBytes + 2 * kMvWarps * kPairTiles * 512 + (int)sizeof(Items);
-}
-// MT tiles of 16 rows at a time and up to 64 / MT tokens
-template <int GS>
-constexpr int smem2() {
-    return kMvWarps * Fmt<GS>::kRingBytes + kMvWarps * 64 * 64 + (int)sizeof(Items);
-}
-
 // ------------------------------------------------------------- first product
-// The CTA's row pairs (gate row i, up row I + i of an item's expert) in blocks
-// of up to 16; the sixteen warps split a block's columns and add their parts
-// through shared memory.
+// The CTA's share of the (item, row pair) list, a pair being gate row i and up
+// row I + i of the item's expert.
 template <int GS>
-__global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid_constant__ ExpertsArgs a) {
-    using F = Fmt<GS>;
+struct GateUp {
+    const ExpertsArgs& a;
+    const Items& it;
+    int64_t q0, q1;   // pairs
+    int block;        // pairs per job
+    struct Job {
+        int pairs, tokens;
+        int64_t q;
+        int item, i0, expert;
+    };
+    __device__ void at(Job& j, int64_t q) const {
+        j.q = q;
+        j.item = (int)(q / a.I);
+        j.i0 = (int)(q - (int64_t)j.item * a.I);
+        j.pairs = (int)min((int64_t)min(block, a.I - j.i0), q1 - q);
+        j.tokens = uniform(it.n[j.item]);
+        j.expert = uniform(it.expert[j.item]);
+    }
+    __device__ bool first(Job& j) const {
+        if (q0 >= q1) return false;
+        at(j, q0);
+        return true;
+    }
+    __device__ bool next(Job& j) const {
+        if (j.q + j.pairs >= q1) return false;
+        at(j, j.q + j.pairs);
+        return true;
+    }
+    __device__ const uint8_t* weights() const { return a.w13; }
+    __device__ const uint16_t* scales() const { return a.s13; }
+    __device__ int64_t rows(const Job& j) const { return (int64_t)j.expert * 2 * a.I + j.i0; }
+    __device__ int row_step(const Job&) const { return a.I; }
+    __device__ void lost() const { atomicOr(a.err, kErrTimeout); }
+    __device__ int entry(const Job& j, int token) const { return it.off[j.item] + token; }
+    __device__ const uint16_t* x(const Job& j, int token) const { return a.x + (int64_t)it.token[entry(j, token)] * a.H; }
+    __device__ int key(const Job& j) const { return a.T == 1 ? 0 : j.item; }
+    __device__ void store(const Job& j, int pair, int token, float gate, float up) const {
+        const float v = gate / (1.0f + expf(-gate)) * up;
+        const __nv_bfloat16 high = __float2bfloat16_rn(v);
+        const float rest = v - __bfloat162float(high);  // an infinite value has no rest
+        uint16_t* o = a.act + (int64_t)it.slot[entry(j, token)] * 2 * a.I + j.i0 + pair;
+        o[0] = __bfloat16_as_ushort(high);
+        o[a.I] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.0f));
+    }
+};
+
+template <int GS>
+__global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ ProductPlan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
-    float* red = reinterpret_cast<float*>(smem + kMvWarps * F::kRingBytes);
-    Items& it = *reinterpret_cast<Items*>(smem + kMvWarps * F::kRingBytes + 2 * kMvWarps * kPairTiles * 512);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const Items it(smem + plan.extra_at, a.T * a.K, a.E);
     pdl_wait();     // no global memory access before this point
     pdl_trigger();  // after it: what the second kernel reads before its own wait is complete
-    build_items(it, a, kChunk1);
-
-    const int64_t pairs = (int64_t)it.count * a.I;
-    const int64_t q0 = pairs * blockIdx.x / gridDim.x, q1 = pairs * (blockIdx.x + 1) / gridDim.x;
-    if (q0 >= q1) return;
-    Rows m;
-    m.q = a.w13;
-    m.s = a.s13;
-    m.row_bytes = F::row_bytes(a.H);
-    m.row_scales = F::kW4 ? a.H / (128 / (GS ? GS : 1)) : 0;
-    m.s_end = a.s13 + (int64_t)a.E * 2 * a.I * m.row_scales;
-    const int steps = F::steps(a.H);
-    const int s0 = steps * warp / kMvWarps, s1 = steps * (warp + 1) / kMvWarps;
-    const uint32_t ring = smem_addr(smem) + warp * F::kRingBytes;
-
-    // A block of pairs, for the copies and (seven stages later) the products.
-    struct Block {
-        int64_t q;
-        int item, i0, n;
-    };
-    auto block_at = [&](int64_t q) {
-        Block b;
-        b.q = q;
-        b.item = (int)(q / a.I);
-        b.i0 = (int)(q - (int64_t)b.item * a.I);
-        b.n = (int)min((int64_t)min(8 * kPairTiles, a.I - b.i0), q1 - q);
-        return b;
-    };
-    Block cb = block_at(q0);
-    int cstep = s0, ctile = 0, cslot = 0;
-    bool more = s0 < s1;
-    auto copy_next = [&]() {
-        if (more) {
-            const int64_t lo = (int64_t)it.expert[cb.item] * 2 * a.I + cb.i0 + 8 * ctile;
-            const int n = cb.n - 8 * ctile;
-            copy_stage<GS>(ring + cslot * F::kStageBytes, m, lo, n, lo + a.I, n, cstep, lane);
-            cslot = cslot + 1 == F::kStages ? 0 : cslot + 1;
-            if (++ctile * 8 >= cb.n) {
-                ctile = 0;
-                if (++cstep == s1) {
-                    cstep = s0;
-                    if (cb.q + cb.n < q1)
-                        cb = block_at(cb.q + cb.n);
-                    else
-                        more = false;
-                }
-            }
-        }
-        cp_async_commit();
-    };
-    for (int s = 0; s < F::kStages - 1; ++s) copy_next();
-
-    int slot = 0, buf = 0;
-    for (int64_t q = q0; q < q1;) {
-        const Block b = block_at(q);
-        const int tiles = (b.n + 7) >> 3, tokens = it.n[b.item];
-        const uint16_t* x = a.x + (g < tokens ? (int64_t)(it.slot[it.off[b.item] + g] / a.K) * a.H : 0);
-        float acc[kPairTiles][1][4] = {};
-        uint4 col[1][F::kBlocks], next[1][F::kBlocks];
-        auto columns = [&](uint4 (&c)[1][F::kBlocks], int step) {
-            load_columns<GS, false>(c[0], x + (int64_t)step * F::kStepK, a.H - step * F::kStepK, g < tokens && step < s1, t);
-        };
-        columns(next, s0);
-        for (int step = s0; step < s1; ++step) {
-#pragma unroll
-            for (int i = 0; i < F::kBlocks; ++i) col[0][i] = next[0][i];
-            columns(next, step + 1);
-#pragma unroll
-            for (int tile = 0; tile < kPairTiles; ++tile)
-                if (tile < tiles) {
-                    cp_async_wait<F::kStages - 2>();
-                    if (F::kW4) __syncwarp();  // other lanes' copies; and all reads of the slot that is filled next
-                    copy_next();
-                    const int64_t lo = (int64_t)it.expert[b.item] * 2 * a.I + b.i0 + 8 * tile + g;
-                    multiply_stage<GS, 1>(acc[tile], ring + slot * F::kStageBytes, col, scale_shift<GS>(m, lo, step),
-                                          scale_shift<GS>(m, lo + a.I, step), m.row_scales - step * GS, lane);
-                    slot = slot + 1 == F::kStages ? 0 : slot + 1;
-                }
-        }
-        // add the warps' parts in warp order
-        float* r = red + buf * kMvWarps * kPairTiles * 128;
-#pragma unroll
-        for (int tile = 0; tile < kPairTiles; ++tile)
-            *reinterpret_cast<float4*>(r + (warp * kPairTiles + tile) * 128 + lane * 4) =
-                make_float4(acc[tile][0][0], acc[tile][0][1], acc[tile][0][2], acc[tile][0][3]);
-        __syncthreads();  // and the other buffer's readers are done before it is written again
-        if (threadIdx.x < kPairTiles * 64) {
-            const int tile = threadIdx.x >> 6, l = (threadIdx.x & 63) >> 1, c = threadIdx.x & 1;
-            float gate = 0.0f, up = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kMvWarps; ++w) {
-                gate += r[(w * kPairTiles + tile) * 128 + l * 4 + c];
-                up += r[(w * kPairTiles + tile) * 128 + l * 4 + c + 2];
-            }
-            const int pair = 8 * tile + (l >> 2), column = 2 * (l & 3) + c;
-            if (pair < b.n && column < tokens) {
-                const float v = gate / (1.0f + expf(-gate)) * up;
-                const __nv_bfloat16 high = __float2bfloat16_rn(v);
-                const float rest = v - __bfloat162float(high);  // an infinite value has no rest
-                const __nv_bfloat16 low = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
-                uint16_t* p = a.act + (int64_t)it.slot[it.off[b.item] + column] * 2 * a.I + b.i0 + pair;
-                p[0] = __bfloat16_as_ushort(high);
-                p[a.I] = __bfloat16_as_ushort(low);
-            }
-        }
-        buf ^= 1;
-        q += b.n;
-    }
-    cp_async_wait<0>();
+    build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk1);
+    const int64_t pairs = (int64_t)it.count() * a.I;
+    GateUp<GS> jobs{a, it, pairs * blockIdx.x / gridDim.x, pairs * (blockIdx.x + 1) / gridDim.x, 0};
+    const int ways = pick_ways(plan.panel, (int)min((int64_t)1 << 16, (jobs.q1 - jobs.q0 + 7) / 8));
+    jobs.block = 8 * (kMvWarps / ways);
+    run_product<GS, 1>(jobs, smem, plan, a.H, ways);
 }
 
 // ------------------------------------------------------------ second product
-// The CTA's output rows in blocks of up to 16 * MT; a block's work is the
-// concatenation of all items' columns (item, step), cut into sixteen equal
-// ranges.  Each warp adds its items' results, weighted, to its own sums [T][16
-// * MT] in shared memory; the sixteen sums are added in warp order.
-template <int GS, int MT>
-__global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_constant__ ExpertsArgs a) {
+// The CTA's output rows in tiles of 16; a tile's work is the concatenation of
+// all items' columns (item, segment), cut into sixteen equal ranges.  Each warp
+// adds its items' results, weighted, to its own sums [T][16] in shared memory;
+// the sixteen sums are added in warp order.
+struct DownPlan {
+    int buffers, items_at, ring_at, slots, smem;
+};
+DownPlan plan_down(int T, int K, int E) {
+    DownPlan p;
+    // two buffers of sums, so that a tile's may be added while the next tile's are made, where that leaves room for four slots
+    p.buffers = T <= 24 ? 2 : 1;
+    p.items_at = kMvWarps * kMaxSlots * 8 + p.buffers * kMvWarps * T * 64;
+    p.ring_at = (p.items_at + Items::bytes(T * K, E) + 127) / 128 * 128;
+    const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlotBytes);
+    p.slots = slots < kMaxSlots ? slots : kMaxSlots;
+    p.smem = p.ring_at + p.slots * kMvWarps * kSlotBytes;
+    return p;
+}
+
+template <int GS>
+__global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ DownPlan plan) {
     using F = Fmt<GS>;
+    constexpr int kGS = GS ? GS : 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* sums = reinterpret_cast<float*>(smem + kMvWarps * F::kRingBytes);  // [warp][T][16 * MT]
-    Items& it = *reinterpret_cast<Items*>(smem + kMvWarps * F::kRingBytes + kMvWarps * 64 * 64);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    float* sums = reinterpret_cast<float*>(smem + kMvWarps * kMaxSlots * 8);  // [buffer][warp][T][16]
+    const Items it(smem + plan.items_at, a.T * a.K, a.E);
+    const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     pdl_trigger();
     // Before the wait: ids, weights and expert weights.  The first kernel starts
     // nothing before its own wait, so everything ahead of it has completed; it
     // writes the activations alone.
-    build_items(it, a, kChunk2);
+    build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk2);
 
     const int r0 = (int)((int64_t)a.H * blockIdx.x / gridDim.x), r1 = (int)((int64_t)a.H * (blockIdx.x + 1) / gridDim.x);
-    Rows m;
-    m.q = a.w2;
-    m.s = a.s2;
-    m.row_bytes = F::row_bytes(a.I);
-    m.row_scales = F::kW4 ? a.I / (128 / (GS ? GS : 1)) : 0;
-    m.s_end = a.s2 + (int64_t)a.E * a.H * m.row_scales;
-    const int steps = F::steps(a.I);
-    const int total = it.count * steps;
-    const int f0 = (int)((int64_t)total * warp / kMvWarps), f1 = (int)((int64_t)total * (warp + 1) / kMvWarps);
-    const uint32_t ring = smem_addr(smem) + warp * F::kRingBytes;
+    const RowShape shape(F::row_bytes(a.I));
+    const int row_scales = F::scales(a.I), segments = F::segments(a.I);
+    const bool wide = row_scales % kGS == 0;
+    const int total = it.count() * segments;
+    const int f0 = total * warp / kMvWarps, f1 = total * (warp + 1) / kMvWarps;  // total <= 2^18
+    const int item0 = f0 / segments, seg0 = f0 - item0 * segments;
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
+    const int row_at = shape.offset(g);
 
-    int crow = r0, cf = f0, ctile = 0, cslot = 0;
-    int citem = f0 / steps, cstep = f0 - citem * steps;
+    // Copies: the next half (tile, item, segment, first or second rows).
+    int crow = r0, cf = f0, citem = item0, cseg = seg0, chalf = 0, crows = 0;
     bool more = f0 < f1 && r0 < r1;
-    auto copy_next = [&]() {
-        if (more) {
-            const int n = min(16 * MT, r1 - crow) - 16 * ctile;
-            const int64_t lo = (int64_t)it.expert[citem] * a.H + crow + 16 * ctile;
-            copy_stage<GS>(ring + cslot * F::kStageBytes, m, lo, n, lo + 8, n - 8, cstep, lane);
-            cslot = cslot + 1 == F::kStages ? 0 : cslot + 1;
-            if (n <= 16 || ++ctile == MT) {
-                ctile = 0;
-                if (++cstep == steps) {
-                    cstep = 0;
-                    ++citem;
-                }
-                if (++cf == f1) {
-                    cf = f0;
-                    citem = f0 / steps;
-                    cstep = f0 - citem * steps;
-                    crow += 16 * MT;
-                    more = crow < r1;
-                }
-            }
-        }
-        cp_async_commit();
+    const uint8_t* cbase = nullptr;
+    auto aim = [&]() {
+        crows = min(16, r1 - crow);
+        cbase = a.w2 + ((int64_t)uniform(it.expert[citem]) * a.H + crow) * shape.row_bytes;
     };
-    for (int s = 0; s < F::kStages - 1; ++s) copy_next();
+    auto copy_half = [&]() {
+        if (!more) return;
+        ring.copy(shape, cbase + cseg * kSegment + (chalf ? (int64_t)(crows / 2) * shape.row_bytes : 0), (crows + 1) / 2, shape.bytes(cseg), lane);
+        chalf ^= 1;
+        if (chalf) return;
+        if (++cf == f1) {
+            cf = f0;
+            citem = item0;
+            cseg = seg0;
+            crow += 16;
+            more = crow < r1;
+            if (more) aim();
+        } else if (++cseg == segments) {
+            cseg = 0;
+            ++citem;
+            aim();
+        }
+    };
+    if (more) aim();
+    for (int s = 0; s < plan.slots; ++s) copy_half();
     pdl_wait();  // the activations
 
-    float* mine = sums + warp * a.T * 16 * MT;
-    int slot = 0;
-    for (int row = r0; row < r1; row += 16 * MT) {
-        const int rows = min(16 * MT, r1 - row), tiles = (rows + 15) >> 4;
-        for (int i = threadIdx.x; i < kMvWarps * a.T * 16 * MT; i += kMvThreads) sums[i] = 0.0f;
-        __syncthreads();
-        int item = f0 / steps, step = f0 - item * steps;
-        uint4 col[1][F::kBlocks], next[1][F::kBlocks];
-        auto columns = [&](uint4 (&c)[1][F::kBlocks], int item, int step, bool ok) {
-            const int e = g & 3;
-            ok = ok && e < it.n[item];
-            const uint16_t* p = a.act;
-            if (ok) p += ((int64_t)it.slot[it.off[item] + e] * 2 + (g >> 2)) * a.I + (int64_t)step * F::kStepK;
-            load_columns<GS, true>(c[0], p, a.I - step * F::kStepK, ok, t);
+    for (int row = r0, buf = 0; row < r1; row += 16, buf ^= plan.buffers - 1) {
+        const int rows = min(16, r1 - row), pairs = (rows + 1) / 2;
+        if (plan.buffers == 1 && row > r0) __syncthreads();  // the sums are added
+        float* all = sums + buf * kMvWarps * a.T * 16;
+        float* mine = all + warp * a.T * 16;
+        for (int i = lane; i < a.T * 16; i += 32) mine[i] = 0.0f;
+        __syncwarp();
+        // the next segment's operands
+        uint4 col[4];
+        DirectColumns<kGS> direct;
+        Scales<kGS> next;
+        const uint16_t* act = nullptr;
+        const uint16_t *scale0 = nullptr, *scale1 = nullptr;
+        auto enter = [&](int item) {
+            const int e = (g & 3) < it.n[item] ? g & 3 : 0;
+            act = a.act + ((int64_t)it.slot[it.off[item] + e] * 2 + (g >> 2)) * a.I;
+            if constexpr (F::kW4) {
+                scale0 = a.s2 + ((int64_t)uniform(it.expert[item]) * a.H + row + min(g, pairs - 1)) * row_scales;
+                scale1 = scale0 + rows / 2 * row_scales;
+            }
         };
-        if (f0 < f1) columns(next, item, step, true);
-        float acc[MT][1][4] = {};
+        auto load_step = [&](int segment, int q) {
+            const int at = segment * F::kSegK + q * F::kStepK;
+            if constexpr (F::kW4)
+                direct.load(act + at, a.I - at, t);
+            else
+                col[q] = load_column<true>(act + at, a.I - at, t);
+        };
+        auto load_scales = [&](int segment) {
+            const int at = (segment * 4 + t) * kGS;
+            next.load(scale0 + at, scale1 + at, row_scales - at, wide);
+        };
+        int item = item0, seg = seg0;
+        if (f0 < f1) {
+            enter(item);
+            if constexpr (F::kW4) {
+                load_scales(seg);
+                load_step(seg, 0);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) load_step(seg, q);
+            }
+        }
+        float acc[1][4] = {};
         for (int f = f0; f < f1; ++f) {
+            const bool last = seg + 1 == segments, final = f + 1 == f1;
+            const int after = last ? 0 : seg + 1, bytes = shape.bytes(seg);
+            const uint32_t lo = ring.wait() + row_at, hi = ring.wait() + row_at;
+            if constexpr (F::kW4) {
+                const Scales<kGS> now = next;
 #pragma unroll
-            for (int i = 0; i < F::kBlocks; ++i) col[0][i] = next[0][i];
-            const bool last = step + 1 == steps;
-            if (f + 1 < f1) columns(next, last ? item + 1 : item, last ? 0 : step + 1, true);
-#pragma unroll
-            for (int tile = 0; tile < MT; ++tile)
-                if (tile < tiles) {
-                    cp_async_wait<F::kStages - 2>();
-                    if (F::kW4) __syncwarp();
-                    copy_next();
-                    const int64_t lo = (int64_t)it.expert[item] * a.H + row + 16 * tile + g;
-                    multiply_stage<GS, 1>(acc[tile], ring + slot * F::kStageBytes, col, scale_shift<GS>(m, lo, step),
-                                          scale_shift<GS>(m, lo + 8, step), m.row_scales - step * GS, lane);
-                    slot = slot + 1 == F::kStages ? 0 : slot + 1;
-                }
-            if (last || f + 1 == f1) {
-                // high part + low part, times the routing weight, to the token's sums
-                const int n = it.n[item], off = it.off[item];
-#pragma unroll
-                for (int tile = 0; tile < MT; ++tile)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float v = acc[tile][0][j] + __shfl_xor_sync(0xffffffffu, acc[tile][0][j], 2);
-                        const int column = 2 * t + (j & 1);
-                        if (t < 2 && column < n) {
-                            float* y = mine + (it.slot[off + column] / a.K) * 16 * MT + 16 * tile + g + 8 * (j >> 1);
-                            *y = fmaf(it.w[off + column], v, *y);
+                for (int q = 0; q < 4; ++q)
+                    if (q * 64 < bytes) {
+                        const DirectColumns<kGS> columns = direct;
+                        if (q * 64 + 64 < bytes) {
+                            load_step(seg, q + 1);
+                        } else if (!final) {
+                            if (last) enter(item + 1);
+                            load_scales(after);
+                            load_step(after, 0);
                         }
-                        acc[tile][0][j] = 0.0f;
+                        multiply_w4<kGS, 1>(acc, lo, hi, columns, now, q, lane);
                     }
+            } else {
+                if (last && !final) enter(item + 1);
+                multiply_bf16(acc[0], lo, hi, col, bytes, t, [&](int q) {
+                    if (!final) load_step(after, q);
+                });
+            }
+            __syncwarp();  // all lanes have read both slots
+            copy_half();
+            copy_half();
+            if (last || final) {
+                // high part + low part, times the routing weight, to the token's sums
+                const int n = it.n[item], at = it.off[item];
+                if (F::kW4)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[0][u] *= direct.factor(0).x;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[0][u] += __shfl_xor_sync(0xffffffffu, acc[0][u], 2);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int column = 2 * t + c;
+                    if (t < 2 && column < n) {
+                        const float w = it.w[at + column];
+                        float* y = mine + it.token[at + column] * 16 + g;
+                        y[0] = fmaf(w, acc[0][c], y[0]);
+                        y[8] = fmaf(w, acc[0][c + 2], y[8]);
+                    }
+                }
+                acc[0][0] = acc[0][1] = acc[0][2] = acc[0][3] = 0.0f;
                 __syncwarp();  // the next item's columns may be other lanes' tokens
             }
-            if (last) {
-                step = 0;
-                ++item;
-            } else {
-                ++step;
-            }
+            seg = after;
+            item += last;
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < a.T * 16 * MT; i += kMvThreads) {
-            const int r = i % (16 * MT), token = i / (16 * MT);
-            if (r < rows) {
+        if (!ring.alive) {
+            atomicOr(a.err, kErrTimeout);
+            for (int i = lane; i < a.T * 16; i += 32) mine[i] = __uint_as_float(0x7fc00000u);
+        }
+        __syncthreads();  // and the other buffer's readers are done before it is written again
+        for (int i = threadIdx.x; i < a.T * 16; i += kMvThreads) {
+            const int token = i >> 4, pair = i & 7, second = i >> 3 & 1;
+            if (pair < pairs) {
                 float y = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kMvWarps; ++w) y += sums[w * a.T * 16 * MT + i];
-                a.out[(int64_t)token * a.H + row + r] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                for (int w = 0; w < kMvWarps; ++w) y += all[w * a.T * 16 + i];
+                if (second == 0 || pair > 0 || rows % 2 == 0)  // the middle row of an odd number is a first row
+                    a.out[(int64_t)token * a.H + row + pair + second * (rows / 2)] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
             }
         }
-        __syncthreads();
     }
-    cp_async_wait<0>();
+    if (!ring.alive) grace_period(10000000ull);  // copies that may still land
 }
 
-template <typename Kernel>
-cudaError_t launch(Kernel kernel, const ExpertsArgs& a, int grid, int smem, cudaStream_t stream, bool pdl) {
+template <typename Kernel, typename Plan>
+cudaError_t launch(Kernel kernel, const ExpertsArgs& a, const Plan& plan, int grid, cudaStream_t stream, bool pdl) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kMvThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.dynamicSmemBytes = (size_t)plan.smem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a, plan);
 }
 
 template <int GS>
 cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
-    cudaError_t e = launch(moe_gate_up_kernel<GS>, a, num_sms, smem1<GS>(), stream, pdl);
+    const int tokens = a.T < kChunk1 ? a.T : kChunk1;
+    cudaError_t e = launch(moe_gate_up_kernel<GS>, a, plan_product<GS, 1>(a.H, tokens, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
     if (e != cudaSuccess) return e;
-    // the more tokens, the fewer rows' sums fit
-    if (a.T <= 16) return launch(moe_down_kernel<GS, 4>, a, num_sms, smem2<GS>(), stream, true);
-    if (a.T <= 32) return launch(moe_down_kernel<GS, 2>, a, num_sms, smem2<GS>(), stream, true);
-    return launch(moe_down_kernel<GS, 1>, a, num_sms, smem2<GS>(), stream, true);
+    return launch(moe_down_kernel<GS>, a, plan_down(a.T, a.K, a.E), num_sms, stream, true);
 }
 
 template <int GS>
 cudaError_t set_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(moe_gate_up_kernel<GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1<GS>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<GS, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2<GS>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<GS, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2<GS>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<GS, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2<GS>());
+    cudaError_t e = cudaFuncSetAttribute(moe_gate_up_kernel<GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     return e;
 }
 
