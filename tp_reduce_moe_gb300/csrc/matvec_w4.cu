@@ -42,7 +42,6 @@ struct Matvec {
         at(j, j.row + j.rows, 0);
         return true;
     }
-    __device__ const uint8_t* weights() const { return a.q; }
     __device__ const uint16_t* scales() const { return a.s; }
     __device__ int64_t rows(const Job& j) const { return j.row; }
     __device__ int row_step(const Job& j) const { return j.rows / 2; }
@@ -65,23 +64,27 @@ struct Matvec {
 };
 
 template <int GS, int NT>
-__global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__ ProductPlan plan) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    Matvec<GS> jobs{a, (int)((int64_t)a.N * blockIdx.x / gridDim.x), (int)((int64_t)a.N * (blockIdx.x + 1) / gridDim.x), 0, 8 * NT};
-    const int ways = pick_ways(plan.panel, (jobs.r1 - jobs.r0 + 15) / 16);
-    jobs.block = 16 * (kMvWarps / ways);
-    run_product<GS, NT>(jobs, smem, plan, a.K, ways);
+__global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__ Weights weights, const __grid_constant__ ProductPlan plan) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const Share rows(a.N);
+    Matvec<GS> jobs{a, rows.first, rows.last, 0, 8 * NT};
+    const int split = plan.ways.pick((rows.last - rows.first + 15) >> 4);
+    jobs.block = 16 * (kMvWarps >> split);
+    run_product<GS, NT>(jobs, weights, smem, plan, a.K, split);
 }
 
 template <int GS, int NT>
 cudaError_t launch_kernel(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
     const ProductPlan plan = plan_product<GS, NT>(a.K, a.T, 0);
+    Weights weights;
+    const cudaError_t e = describe_weights(&weights, a.q, a.N, Fmt<GS>::row_bytes(a.K));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.N < num_sms ? a.N : num_sms));
     cfg.blockDim = dim3(kMvThreads);
     cfg.dynamicSmemBytes = (size_t)plan.smem;
     cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, matvec_w4_kernel<GS, NT>, a, plan);
+    return cudaLaunchKernelEx(&cfg, matvec_w4_kernel<GS, NT>, a, weights, plan);
 }
 
 template <int GS>

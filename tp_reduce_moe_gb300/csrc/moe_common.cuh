@@ -6,17 +6,19 @@
 // and use it a handful of times, so the time is the weights' bytes over the
 // memory bandwidth.  One CTA per SM holds sixteen warps; each warp streams its
 // own share of the weights through a private ring in shared memory, filled by
-// bulk copies of 256-byte row segments (7.0 TB/s with three 16-row stages, a
-// copy every 10 cycles; 128-byte ones 4.2 TB/s; cp.async from the same warps
-// 5.9 TB/s, and plain loads issued behind those return behind them), and
-// multiplies them with mma.sync, weight rows as the 16-row operand and tokens as
-// the 8-column one.  A kilobyte of weights takes the memory 44 cycles to deliver
-// to an SM; the matrix instructions for it take 4 (bf16) to 16 (4-bit), so that
-// what counts is the instructions around them.  A tcgen05 tile of 128 rows would
-// need all its operands in shared memory, the 4-bit codes expanded there first,
-// and pay in granularity: at one token an SM owns about 27 rows of the first
-// product.
+// tensor copies (TMA) of eight rows by 128 bytes, and multiplies them with
+// mma.sync, weight rows as the 16-row operand and tokens as the 8-column one.
+// (Tried before: cp.async from the same warps, 5.9 TB/s and ten instructions per
+// KB, and plain loads issued behind it return behind it; bulk copies of single
+// 256-byte row segments, 7 TB/s but issued lane by lane, 14 instructions each.)
+// A kilobyte of weights takes the memory 44 cycles to deliver to an SM; the
+// matrix instructions for it take 4 (bf16) to 16 (4-bit), so that what counts is
+// the instructions around them.  A tcgen05 tile of 128 rows would need all its
+// operands in shared memory, the 4-bit codes expanded there first, and pay in
+// granularity: at one token an SM owns about 27 rows of the first product.
 #pragma once
+
+#include <cuda.h>
 
 #include "arf_common.cuh"
 
@@ -83,7 +85,6 @@ struct Fmt {
     static constexpr int kStepK = kW4 ? 128 : 32;
     static constexpr int kSegK = 4 * kStepK;
     __host__ __device__ static int row_bytes(int k) { return kW4 ? k / 2 : k * 2; }
-    __host__ __device__ static int segments(int k) { return (row_bytes(k) + kSegment - 1) / kSegment; }
     __host__ __device__ static int scales(int k) { return kW4 ? k / (128 / (GS ? GS : 1)) : 0; }
 };
 
@@ -138,106 +139,158 @@ __device__ __forceinline__ int warp_index() { return uniform((int)(threadIdx.x >
 // rows 8-15 (a gate row and its up row; or the two halves of a range of rows,
 // which share the middle row if their number is odd).
 //
-// A ring slot holds a segment of the eight first or second rows of a tile, each
-// row 16 bytes further than it is long, so that reads of eight rows meet a bank
-// at most twice.  Rows of 128 bytes and less come several in one copy (the
-// pad then behind each copy).  Every slot has its mbarrier; the warp that fills
-// it is the one that reads it.
-constexpr int kSlotBytes = 8 * (kSegment + 16);
-constexpr int kMaxSlots = 8;
+// A ring slot holds a segment of a tile: four boxes of eight rows by 128 bytes
+// (first rows, then second rows, two boxes each), swizzled by the copy: the
+// 16-byte chunk c of row g lies at place c ^ g of the row's eight.  What lies
+// behind the end of the rows is zero in a box that begins before it; boxes that
+// begin behind it are not copied.  Every slot has its mbarrier; the warp that
+// fills it is the one that reads it, and refills it at once.
+constexpr int kBox = 128;
+constexpr int kBoxBytes = 8 * kBox;
+constexpr int kHalfBytes = 2 * kBoxBytes;
+constexpr int kSlotBytes = 2 * kHalfBytes;
+constexpr int kMaxSlots = 4;
+
+// A weight matrix for the copies, in boxes of eight rows and of one.
+struct Weights {
+    CUtensorMap eight, one;
+};
+cudaError_t describe_weights(Weights* w, const void* q, int64_t rows, int row_bytes);
 
 struct RowShape {
-    int row_bytes, rows_per_copy, copy_stride;
-    __device__ __forceinline__ RowShape(int bytes) : row_bytes(bytes) {
-        rows_per_copy = bytes >= kSegment ? 1 : kSegment / bytes;
-        copy_stride = (bytes >= kSegment ? kSegment : rows_per_copy * bytes) + 16;
-    }
-    // Offset of row g in a slot.
-    __device__ __forceinline__ int offset(int g) const { return g / rows_per_copy * copy_stride + g % rows_per_copy * row_bytes; }
+    int row_bytes, segments;
+    __host__ static RowShape of(int bytes) { return RowShape{bytes, (bytes + kSegment - 1) / kSegment}; }
     __device__ __forceinline__ int bytes(int segment) const { return min(kSegment, row_bytes - segment * kSegment); }
 };
 
+// A range of `total` things dealt evenly over the grid, whole ones to each CTA.
+struct Share {
+    int first, last;
+    __device__ __forceinline__ Share(unsigned total) {
+        const unsigned each = total / gridDim.x, rest = total - each * gridDim.x, b = blockIdx.x;
+        first = b * each + min(b, rest);
+        last = first + each + (b < rest);
+    }
+};
+
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap& map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(to),
+                 "l"(&map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+// A wait that sleeps in the instruction (the hint, in nanoseconds, is a limit)
+// instead of polling: sixteen warps that poll take issue slots from those that
+// have data.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(10000)
+        : "memory");
+    return ok != 0;
+}
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase) {
+    const unsigned long long t0 = global_timer_ns();
+    for (unsigned it = 0; it < kWaitMaxIters; ++it) {
+        if (mbar_sleep(bar, phase)) return true;
+        if ((it & 31u) == 31u && global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
+    return false;
+}
+
 struct SlotRing {
     uint32_t slots, bars;  // shared addresses
-    int n, fill, read;     // slots; the next to fill and to read
-    uint32_t phase;        // of the next to read
-    bool alive;            // no wait has run out
+    uint32_t slot, bar;    // the next
+    int n;
+    uint32_t phase;
+    bool alive;  // no wait has run out
 
     __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int lane)
-        : slots(slots), bars(bars), n(n), fill(0), read(0), phase(0), alive(true) {
+        : slots(slots), bars(bars), slot(slots), bar(bars), n(n), phase(0), alive(true) {
         if (lane < n) mbar_init(bars + lane * 8, 1);
         fence_mbar_init();
         __syncwarp();
     }
-    // Copies `rows` rows' segment at `at` (of the first row).
-    __device__ __forceinline__ void copy(const RowShape& shape, const uint8_t* at, int rows, int bytes, int lane) {
-        const uint32_t bar = bars + fill * 8, dst = slots + fill * kSlotBytes;
-        if (lane == 0) mbar_arrive_expect_tx(bar, rows * bytes);
-        __syncwarp();
-        const int first = lane * shape.rows_per_copy;
-        if (first < rows)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             dst + lane * shape.copy_stride),
-                         "l"(at + (int64_t)first * shape.row_bytes), "r"(min(shape.rows_per_copy, rows - first) * bytes), "r"(bar)
-                         : "memory");
-        fill = fill + 1 == n ? 0 : fill + 1;
+    // Copies `bytes` bytes of each row of a tile (rows first .., second .., `pairs` of them), from column x on, into the slot
+    // that was read last (or, at the start, one after the other).
+    __device__ __forceinline__ void fill(const Weights& w, int first, int second, int pairs, int x, int bytes, int lane) {
+        if (lane != 0) return;
+        const bool wide = bytes > kBox;
+        if (pairs == 8) {
+            mbar_arrive_expect_tx(bar, wide ? 4 * kBoxBytes : 2 * kBoxBytes);
+            copy_box(slot, w.eight, x, first, bar);
+            copy_box(slot + kHalfBytes, w.eight, x, second, bar);
+            if (wide) {
+                copy_box(slot + kBoxBytes, w.eight, x + kBox, first, bar);
+                copy_box(slot + kHalfBytes + kBoxBytes, w.eight, x + kBox, second, bar);
+            }
+        } else {
+            mbar_arrive_expect_tx(bar, (wide ? 4 : 2) * pairs * kBox);
+            for (int r = 0; r < pairs; ++r) {
+                copy_box(slot + r * kBox, w.one, x, first + r, bar);
+                copy_box(slot + kHalfBytes + r * kBox, w.one, x, second + r, bar);
+                if (wide) {
+                    copy_box(slot + kBoxBytes + r * kBox, w.one, x + kBox, first + r, bar);
+                    copy_box(slot + kHalfBytes + kBoxBytes + r * kBox, w.one, x + kBox, second + r, bar);
+                }
+            }
+        }
     }
-    // Waits for the next slot and returns its address.  A wait that runs out
-    // (nothing but a lost copy makes it) ends the waiting for good.
-    __device__ __forceinline__ uint32_t wait() {
-        const uint32_t at = slots + read * kSlotBytes;
-        if (alive) alive = mbar_wait_bounded(bars + read * 8, phase, nullptr);
-        if (++read == n) {
-            read = 0;
+    // Waits for the next slot.  A wait that runs out (nothing but a lost copy
+    // makes it) ends the waiting for good.
+    __device__ __forceinline__ void wait() {
+        if (!mbar_sleep(bar, phase) && alive) alive = wait_long(bar, phase);
+    }
+    __device__ __forceinline__ void next() {
+        slot += kSlotBytes;
+        bar += 8;
+        if (slot == slots + n * kSlotBytes) {
+            slot = slots;
+            bar = bars;
             phase ^= 1;
         }
-        return at;
     }
 };
 
 // ------------------------------------------------------------ products, bf16
-// The activations that meet a segment, one segment ahead in registers: lane (g,
-// t) = (lane / 4, lane % 4) holds values 8t .. 8t+7 of every 32 of column g.  A
-// column that does not exist may repeat one that does.
+// Of every box lane (g, t) = (lane / 4, lane % 4) takes the chunks 2t and 2t + 1
+// of rows g (reads of eight lanes then meet every bank once), and so the values
+// 16t .. 16t+15 of every 64 of column g, which come one segment ahead in
+// registers.  A column that does not exist may repeat one that does.
+//
+// Part q of a segment: chunk 2t + q % 2 of box q / 2.
 template <bool COHERENT>
-__device__ __forceinline__ uint4 load_column(const uint16_t* p, int left, int t) {
-    if (8 * t >= left) return make_uint4(0, 0, 0, 0);
-    return COHERENT ? ld_coherent16(p + 8 * t) : ld_early16(p + 8 * t);
+__device__ __forceinline__ uint4 load_column(const uint16_t* p, int left, int q, int t) {
+    const int at = 64 * (q >> 1) + 16 * t + 8 * (q & 1);
+    if (at >= left) return make_uint4(0, 0, 0, 0);
+    return COHERENT ? ld_coherent16(p + at) : ld_early16(p + at);
 }
 
-// acc += (tile) * (columns), one segment; lo, hi: the lane's rows in the slots.
-// load(q) replaces step q of the columns by a later segment's.  bytes: of the
-// segment; what lies behind them in the slots may be anything.
+// acc += (tile) * (columns), one segment of `bytes` bytes at `slot`.  load(q)
+// replaces part q of the columns by a later segment's.
 template <class Load>
-__device__ __forceinline__ void multiply_bf16(float (&acc)[4], uint32_t lo, uint32_t hi, uint4 (&b)[4], int bytes, int t, Load load) {
-    if (bytes == kSegment) {
-        float odd[4] = {};
+__device__ __forceinline__ void multiply_bf16(float (&acc)[4], uint32_t slot, uint4 (&b)[4], int bytes, int lane, Load load) {
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t even = slot + g * kBox + ((2 * t) ^ g) * 16, odd = even ^ 16;
+    float more[4] = {};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 4; ++q) {
+        if (q < 2 || bytes > kBox) {
             uint32_t l[4], h[4];
-            lds(l, lo + q * 64 + t * 16);
-            lds(h, hi + q * 64 + t * 16);
+            const uint32_t at = (q & 1 ? odd : even) + (q >> 1) * kBoxBytes;
+            lds(l, at);
+            lds(h, at + kHalfBytes);
             mma_bf16(acc, l[0], h[0], l[1], h[1], b[q].x, b[q].y);
-            mma_bf16(odd, l[2], h[2], l[3], h[3], b[q].z, b[q].w);
-            load(q);
+            mma_bf16(more, l[2], h[2], l[3], h[3], b[q].z, b[q].w);
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) acc[u] += odd[u];
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (q * 64 < bytes) {
-                uint32_t l[4] = {}, h[4] = {};
-                if (q * 64 + t * 16 < bytes) {
-                    lds(l, lo + q * 64 + t * 16);
-                    lds(h, hi + q * 64 + t * 16);
-                }
-                mma_bf16(acc, l[0], h[0], l[1], h[1], b[q].x, b[q].y);
-                mma_bf16(acc, l[2], h[2], l[3], h[3], b[q].z, b[q].w);
-            }
-            load(q);
-        }
+        load(q);
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc[u] += more[u];
 }
 
 // ----------------------------------------------------------- products, 4-bit
@@ -411,19 +464,19 @@ template <int GS>
 struct Scales {
     static constexpr int kWords = GS == 4 ? 2 : 1;
     uint32_t raw[2][kWords];
-    // p0, p1: the lane's first scale in its two rows; groups: from there to the end of the row (zeros behind it); wide:
-    // they are aligned to their size
-    __device__ __forceinline__ void load(const uint16_t* p0, const uint16_t* p1, int groups, bool wide) {
+    // base: the segment's first scale in the tile's first row; off0, off1: from there to the lane's first in its two rows;
+    // groups: from the lane's first to the end of the row (zeros behind it), all of them: no lane's step is cut; wide: aligned
+    // to their size
+    __device__ __forceinline__ void load(const uint16_t* base, uint32_t off0, uint32_t off1, int groups, bool all, bool wide) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint16_t* p = h ? p1 : p0;
+            const uint16_t* p = base + (h ? off1 : off0);
             uint32_t* r = raw[h];
-            if (GS == 1) {
-                r[0] = groups > 0 ? ld_u16(p) : 0;
-            } else if (wide) {  // then a step has all its groups or none
-                if constexpr (GS == 2) r[0] = groups > 0 ? ld_early4(p) : 0;
+            if (all && (GS == 1 || wide)) {
+                if constexpr (GS == 1) r[0] = ld_u16(p);
+                if constexpr (GS == 2) r[0] = ld_early4(p);
                 if constexpr (GS == 4) {
-                    const uint2 v = groups > 0 ? ld_early8(p) : make_uint2(0, 0);
+                    const uint2 v = ld_early8(p);
                     r[0] = v.x;
                     r[kWords - 1] = v.y;
                 }
@@ -431,7 +484,7 @@ struct Scales {
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
                     r[w] = 2 * w < groups ? ld_u16(p + 2 * w) : 0;
-                    if (2 * w + 1 < groups) r[w] |= ld_u16(p + 2 * w + 1) << 16;
+                    if (GS > 1 && 2 * w + 1 < groups) r[w] |= ld_u16(p + 2 * w + 1) << 16;
                 }
             }
         }
@@ -443,24 +496,29 @@ struct Scales {
     }
 };
 
-// sum[n] += (tile) * (column tile n), step q of a segment; lo, hi: the lane's
-// rows in the slots.  Without the columns' factors.
+// sum[n] += (tile) * (column tile n), step q of the segment at `slot`.  Without
+// the columns' factors.  (Reads of one word a row meet every bank once, wider
+// ones twice.)
 template <int GS, int NT, class Columns>
-__device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t lo, uint32_t hi, const Columns& columns,
+__device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, const Columns& columns,
                                             const Scales<GS>& sc, int q, int lane) {
-    const int t = lane & 3;
+    const int g = lane >> 2, t = lane & 3;
     constexpr int kPer = 4 / GS;  // words of a lane per scale group
+    // the lane's first chunk of the step's first group, and its bytes of it; other groups and the box's second step lie at an
+    // exclusive or from there
+    const uint32_t base = slot + g * kBox + ((GS == 1 ? t : GS == 2 ? t >> 1 : 0) ^ g) * 16 + (GS == 1 ? 0 : GS == 2 ? (t & 1) * 8 : t * 4);
     constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 #pragma unroll
     for (int s = 0; s < GS; ++s) {
-        const int at = q * 64 + s * 16 * kPer + t * 4 * kPer;
+        const uint32_t at = (base ^ (s * (GS == 2 ? 32 : 16) + (q & 1) * 64)) + (q >> 1) * kBoxBytes;
         uint32_t c[NT][kPer][4], l[kPer], h[kPer];
         float2 eight[NT];
-        lds(l, lo + at);
-        lds(h, hi + at);
+        lds(l, at);
+        lds(h, at + kHalfBytes);
 #pragma unroll
         for (int n = 0; n < NT; ++n) columns.words(n, q, s, c[n], eight[n]);
-        // two chains of matrix instructions
+        // two chains of matrix instructions where a group has eight
+        constexpr bool kTwo = kPer == 4;
         float part[NT][4], more[NT][4];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -470,10 +528,13 @@ __device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t lo, ui
                 if (j == 0) {
                     mma_bf16_from(part[n], l[j] & kLow, h[j] & kLow, l[j] & kHigh, h[j] & kHigh, c[n][j][0], c[n][j][1], eight[n].x,
                                   eight[n].y, eight[n].x, eight[n].y);
-                    mma_bf16_from(more[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3], 0.f, 0.f, 0.f, 0.f);
+                    if (kTwo)
+                        mma_bf16_from(more[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3], 0.f, 0.f, 0.f, 0.f);
+                    else
+                        mma_bf16(part[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3]);
                 } else {
                     mma_bf16(part[n], l[j] & kLow, h[j] & kLow, l[j] & kHigh, h[j] & kHigh, c[n][j][0], c[n][j][1]);
-                    mma_bf16(more[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3]);
+                    mma_bf16(kTwo ? more[n] : part[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3]);
                 }
             }
         }
@@ -481,7 +542,7 @@ __device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t lo, ui
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) sum[n][u] = fmaf(u < 2 ? sl : sh, part[n][u] + more[n][u], sum[n][u]);
+            for (int u = 0; u < 4; ++u) sum[n][u] = fmaf(u < 2 ? sl : sh, kTwo ? part[n][u] + more[n][u] : part[n][u], sum[n][u]);
     }
 }
 template <int NT, class Columns>
@@ -495,26 +556,37 @@ __device__ __forceinline__ void add_scaled(float (&acc)[NT][4], const float (&su
 }
 
 // ----------------------------------------------------------------- products
-// How the sixteen warps of a CTA share tiles: `ways` of them split a tile's
-// segments, 16 / ways tiles go side by side.  The least work for the busiest
+// How the sixteen warps of a CTA share tiles: 2^ways of them split a tile's
+// segments, 16 / 2^ways tiles go side by side.  The least work for the busiest
 // warp; among equals the fewest rounds (each costs a reduction, and 4-bit weights
 // of many tokens their activations again), then the most ways.
-__host__ __device__ inline int pick_ways(int segments, int tiles) {
-    int best = 16, cost = 0x7fffffff;
-    for (int w = 16; w >= 1; w >>= 1) {
-        const int rounds = (tiles * w + 15) / 16, c = (segments + w - 1) / w * rounds * 64 + (rounds < 63 ? rounds : 63);
-        if (c < cost) {
-            cost = c;
-            best = w;
-        }
+struct Ways {
+    int each[5];  // segments of the busiest way, for 2^i ways
+    __host__ static Ways of(int segments) {
+        Ways w;
+        for (int i = 0; i < 5; ++i) w.each[i] = (segments + (1 << i) - 1) >> i;
+        return w;
     }
-    return best;
-}
+    __device__ __forceinline__ int pick(int tiles) const {
+        int best = 4, cost = 0x7fffffff;
+#pragma unroll
+        for (int i = 4; i >= 0; --i) {
+            const int rounds = (min(tiles, 1 << 14) + (16 >> i) - 1) >> (4 - i), c = each[i] * rounds * 64 + min(rounds, 63);
+            if (c < cost) {
+                cost = c;
+                best = i;
+            }
+        }
+        return best;
+    }
+};
 
 // Shared memory of a product: barriers, two buffers of partial tiles, staged
 // activations, `extra` bytes, the rings.
 constexpr int kSmemLimit = 227 * 1024;
 struct ProductPlan {
+    RowShape shape;
+    Ways ways;
     int panel;    // segments whose activations are staged at a time
     int columns;  // staged columns
     int staged;   // bytes
@@ -525,22 +597,24 @@ struct ProductPlan {
 template <int GS, int NT>
 inline ProductPlan plan_product(int K, int tokens, int extra) {
     ProductPlan p;
-    const int segments = Fmt<GS>::segments(K), fixed = kMvWarps * kMaxSlots * 8 + 2 * kMvWarps * NT * 512 + extra;
+    p.shape = RowShape::of(Fmt<GS>::row_bytes(K));
+    const int segments = p.shape.segments, fixed = kMvWarps * kMaxSlots * 8 + 2 * kMvWarps * NT * 512 + extra;
     p.extra = extra;
     p.columns = tokens < 8 * NT ? tokens : 8 * NT;
     p.panel = segments;
     p.staged = 0;
     if (GS > 0) {
-        // at least four slots per warp
+        // at least two slots per warp
         using View = StagedView<GS ? GS : 1, NT>;
         const int none = View::bytes(0, p.columns), each = View::bytes(1, p.columns) - none;
-        const int most = (kSmemLimit - fixed - 4 * kMvWarps * kSlotBytes - none) / each;
+        const int most = (kSmemLimit - fixed - 2 * kMvWarps * kSlotBytes - none) / each;
         const int panels = (segments + most - 1) / most;
         p.panel = (segments + panels - 1) / panels;
         p.staged = (View::bytes(p.panel, p.columns) + 15) / 16 * 16;
     }
+    p.ways = Ways::of(p.panel);
     p.extra_at = fixed - extra + p.staged;
-    p.ring_at = (p.extra_at + extra + 127) / 128 * 128;
+    p.ring_at = (p.extra_at + extra + 1023) / 1024 * 1024;
     const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlotBytes);
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
     p.smem = p.ring_at + p.slots * kMvWarps * kSlotBytes;
@@ -550,16 +624,16 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
 // The products of blocks of row pairs with up to 8 * NT tokens each, one block
 // ("job") after the other, the copies running ahead across their borders.  Jobs
 // is a class with
-//   struct Job { int pairs, tokens; .. }: at most 8 * 16 / ways pairs, at least one token
+//   struct Job { int pairs, tokens; .. }: at most 8 * 16 / 2^split pairs, at least one token
 //   bool first(Job&), next(Job&)          the CTA's jobs in order
 //   rows(job), row_step                   first row of the first pair, rows between a pair's rows
-//   weights(), scales()                   row 0 of all
+//   scales()                              row 0's
 //   x(job, token), key(job)               a token's activations; equal keys: the same tokens
 //   store(job, pair, token, first, second)  results of a pair's two rows
 //   lost()                                a wait ran out
 // Deterministic: a tile's sums are added in the order of the ways.
 template <int GS, int NT, class Jobs>
-__device__ __forceinline__ void run_product(const Jobs& jobs, uint8_t* smem, const ProductPlan& plan, int K, int ways) {
+__device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& weights, uint8_t* smem, const ProductPlan& plan, int K, int split) {
     using F = Fmt<GS>;
     using Job = typename Jobs::Job;
     static_assert(F::kW4 || NT == 1, "bf16 weights: one column tile");
@@ -570,13 +644,12 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, uint8_t* smem, con
     const StagedView<kGS, NT> staged(smem_addr(smem) + kStagedAt, plan.panel, plan.columns);
     const StagedColumns<kGS, NT> staged_columns(staged, plan.columns, threadIdx.x & 31);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
-    const RowShape shape(F::row_bytes(K));
-    const int row_scales = F::scales(K), segments = F::segments(K), panel = plan.panel;
+    const RowShape& shape = plan.shape;
+    const int row_scales = F::scales(K), segments = shape.segments, panel = plan.panel;
     const bool wide = row_scales % kGS == 0;
-    const int split = 31 - __clz(ways);  // ways is a power of two
+    const int ways = 1 << split;
     const int mine = warp >> split, way = warp & (ways - 1);  // tile; segments way, way + ways, .. of a panel
     SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
-    const int row_at = shape.offset(g);
 
     auto to = [&](int p) { return min(p + panel, segments); };
     // The warp's first segment of the panels from p on; `segments` or more: none.
@@ -586,17 +659,15 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, uint8_t* smem, con
     };
     auto pairs_of = [&](const Job& j) { return min(8, j.pairs - 8 * mine); };  // of the warp's tile; none if not positive
 
-    // Copies: the next half (job, panel, segment, first or second rows).
+    // Copies: the next (job, panel, segment).
     Job cj;
     bool more = jobs.first(cj);
     if (!more) return;
-    int cpanel = 0, cseg = way, cpairs = 0, chalf = 0;
-    const uint8_t* cbase = nullptr;
-    int64_t cstep = 0;  // bytes between a pair's rows
+    int cpanel = 0, cseg = way, cpairs = 0, cfirst = 0, csecond = 0;
     auto enter = [&]() {
         cpairs = pairs_of(cj);
-        cbase = jobs.weights() + (jobs.rows(cj) + 8 * mine) * shape.row_bytes;
-        cstep = (int64_t)jobs.row_step(cj) * shape.row_bytes;
+        cfirst = (int)jobs.rows(cj) + 8 * mine;
+        csecond = cfirst + jobs.row_step(cj);
     };
     auto settle = [&]() {  // to the first segment from here on
         while (more && (cpairs <= 0 || cseg >= to(cpanel))) {
@@ -609,39 +680,42 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, uint8_t* smem, con
             cseg = cpanel + way;
         }
     };
-    auto copy_half = [&]() {
+    auto fill = [&]() {
         if (!more) return;
-        ring.copy(shape, cbase + cseg * kSegment + (chalf ? cstep : 0), cpairs, shape.bytes(cseg), lane);
-        chalf ^= 1;
-        if (chalf == 0) {
-            cseg += ways;
-            if (cseg >= to(cpanel)) settle();
-        }
+        ring.fill(weights, cfirst, csecond, cpairs, cseg * kSegment, shape.bytes(cseg), lane);
+        cseg += ways;
+        if (cseg >= to(cpanel)) settle();
     };
     enter();
     settle();
-    for (int s = 0; s < plan.slots; ++s) copy_half();
+    for (int s = 0; s < plan.slots; ++s) {
+        fill();
+        ring.next();
+    }
+    ring.phase = 0;
 
     // Operands of the next segment, asked for one segment ahead, across panels and jobs.
     uint4 col[4];
     Scales<kGS> next;
     const uint16_t* x = nullptr;
-    const uint16_t *scale0 = nullptr, *scale1 = nullptr;
-    auto load_step = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK + q * F::kStepK, K - segment * F::kSegK - q * F::kStepK, t); };
+    const uint16_t* scale = nullptr;
+    uint32_t off0 = 0, off1 = 0;
+    auto load_part = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK, K - segment * F::kSegK, q, t); };
     auto load_scales = [&](int segment) {
-        const int at = (segment * 4 + t) * kGS;
-        next.load(scale0 + at, scale1 + at, row_scales - at, wide);
+        const int at = segment * 4 * kGS;
+        next.load(scale + at, off0, off1, row_scales - at - t * kGS, at + 4 * kGS <= row_scales, wide);
     };
     auto begin_job = [&](const Job& j) {
         const int first = first_from(0);
         if constexpr (F::kW4) {
-            scale0 = jobs.scales() + (jobs.rows(j) + max(0, min(8 * mine + g, j.pairs - 1))) * row_scales;
-            scale1 = scale0 + (int64_t)jobs.row_step(j) * row_scales;
+            scale = jobs.scales() + jobs.rows(j) * row_scales;
+            off0 = (unsigned)max(0, min(8 * mine + g, j.pairs - 1)) * row_scales + t * kGS;
+            off1 = off0 + (unsigned)jobs.row_step(j) * row_scales;
             load_scales(first);
         } else {
             x = jobs.x(j, g < j.tokens ? g : 0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) load_step(first, q);
+            for (int q = 0; q < 4; ++q) load_part(first, q);
         }
     };
     auto stage = [&](const Job& j, int p) {
@@ -677,7 +751,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, uint8_t* smem, con
             const int end = to(p), behind = first_from(p + panel);
             for (int seg = p + way; seg < end; seg += ways) {
                 const int after = seg + ways < end ? seg + ways : behind, bytes = shape.bytes(seg);
-                const uint32_t lo = ring.wait() + row_at, hi = ring.wait() + row_at;
+                ring.wait();
                 if constexpr (F::kW4) {
                     const Scales<kGS> now = next;
                     load_scales(after);
@@ -685,20 +759,20 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, uint8_t* smem, con
                     float sum[NT][4] = {};
                     if (bytes == kSegment) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) multiply_w4<kGS, NT>(sum, lo, hi, columns, now, q, lane);
+                        for (int q = 0; q < 4; ++q) multiply_w4<kGS, NT>(sum, ring.slot, columns, now, q, lane);
                     } else {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            if (q * 64 < bytes) multiply_w4<kGS, NT>(sum, lo, hi, columns, now, q, lane);
+                            if (q * 64 < bytes) multiply_w4<kGS, NT>(sum, ring.slot, columns, now, q, lane);
                     }
                     add_scaled(acc, sum, columns);
                 } else {
                     float(&one)[4] = acc[0];
-                    multiply_bf16(one, lo, hi, col, bytes, t, [&](int q) { load_step(after, q); });
+                    multiply_bf16(one, ring.slot, col, bytes, lane, [&](int q) { load_part(after, q); });
                 }
-                __syncwarp();  // all lanes have read both slots
-                copy_half();
-                copy_half();
+                __syncwarp();  // all lanes have read the slot
+                fill();
+                ring.next();
             }
         }
         const Job done = job;

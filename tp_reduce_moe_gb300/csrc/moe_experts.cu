@@ -13,6 +13,8 @@
 // mantissa together), columns 0-3 and 4-7 of the matrix instruction's eight:
 // rounding them to one bf16 would make the result's error 1.4 times that of its
 // own rounding, and up to four tokens per expert the second part costs nothing.
+#include <atomic>
+
 #include "moe_common.cuh"
 
 namespace arf {
@@ -48,11 +50,33 @@ struct Items {
 };
 
 // Called by all threads of a CTA.  A token that names an expert twice gets one
-// entry with the sum of its weights.  -1 names no expert; other values outside
+// entry with the sum of its weights (a single token: an item each).  -1 names no expert; other values outside
 // [0, E) are skipped too and flagged.  mask: scratch, two words per expert (the
 // tokens that chose it), free again afterwards.
 __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsArgs& a, int chunk) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (a.T == 1) {  // every slot an item: one warp does it
+        if (warp == 0) {
+            const int e = lane < a.K ? a.ids[lane] : -1;
+            const float w = lane < a.K ? a.weights[lane] : 0.0f;
+            const bool ok = (unsigned)e < (unsigned)a.E;
+            const unsigned all = __ballot_sync(0xffffffffu, ok);
+            const int i = __popc(all & ((1u << lane) - 1));
+            if (ok) {
+                it.expert[i] = e;
+                it.off[i] = i;
+                it.slot[i] = lane;
+                it.n[i] = 1;
+                it.token[i] = 0;
+                it.w[i] = w;
+            } else if (e != -1) {
+                atomicOr(a.err, kErrExpertRange);
+            }
+            if (lane == 0) it.part[2 * kMvWarps] = __popc(all);
+        }
+        __syncthreads();
+        return;
+    }
     const int slots = a.T * a.K;
     for (int e = tid; e < a.E; e += kMvThreads) mask[e][0] = mask[e][1] = 0;
     __syncthreads();
@@ -120,18 +144,17 @@ template <int GS>
 struct GateUp {
     const ExpertsArgs& a;
     const Items& it;
-    int64_t q0, q1;   // pairs
+    int q0, q1;       // pairs
     int block;        // pairs per job
     struct Job {
         int pairs, tokens;
-        int64_t q;
-        int item, i0, expert;
+        int q, item, i0, expert;
     };
-    __device__ void at(Job& j, int64_t q) const {
+    __device__ void at(Job& j, int q) const {
         j.q = q;
-        j.item = (int)(q / a.I);
-        j.i0 = (int)(q - (int64_t)j.item * a.I);
-        j.pairs = (int)min((int64_t)min(block, a.I - j.i0), q1 - q);
+        j.item = q / a.I;
+        j.i0 = q - j.item * a.I;
+        j.pairs = min(min(block, a.I - j.i0), q1 - q);
         j.tokens = uniform(it.n[j.item]);
         j.expert = uniform(it.expert[j.item]);
     }
@@ -145,7 +168,6 @@ struct GateUp {
         at(j, j.q + j.pairs);
         return true;
     }
-    __device__ const uint8_t* weights() const { return a.w13; }
     __device__ const uint16_t* scales() const { return a.s13; }
     __device__ int64_t rows(const Job& j) const { return (int64_t)j.expert * 2 * a.I + j.i0; }
     __device__ int row_step(const Job&) const { return a.I; }
@@ -164,17 +186,18 @@ struct GateUp {
 };
 
 template <int GS>
-__global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ ProductPlan plan) {
-    extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ Weights weights,
+                                                                       const __grid_constant__ ProductPlan plan) {
+    extern __shared__ __align__(1024) uint8_t smem[];
     const Items it(smem + plan.extra_at, a.T * a.K, a.E);
     pdl_wait();     // no global memory access before this point
     pdl_trigger();  // after it: what the second kernel reads before its own wait is complete
     build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk1);
-    const int64_t pairs = (int64_t)it.count() * a.I;
-    GateUp<GS> jobs{a, it, pairs * blockIdx.x / gridDim.x, pairs * (blockIdx.x + 1) / gridDim.x, 0};
-    const int ways = pick_ways(plan.panel, (int)min((int64_t)1 << 16, (jobs.q1 - jobs.q0 + 7) / 8));
-    jobs.block = 8 * (kMvWarps / ways);
-    run_product<GS, 1>(jobs, smem, plan, a.H, ways);
+    const Share pairs(it.count() * a.I);  // at most 2^24
+    GateUp<GS> jobs{a, it, pairs.first, pairs.last, 0};
+    const int split = plan.ways.pick((pairs.last - pairs.first + 7) >> 3);
+    jobs.block = 8 * (kMvWarps >> split);
+    run_product<GS, 1>(jobs, weights, smem, plan, a.H, split);
 }
 
 // ------------------------------------------------------------ second product
@@ -183,14 +206,16 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
 // adds its items' results, weighted, to its own sums [T][16] in shared memory;
 // the sixteen sums are added in warp order.
 struct DownPlan {
+    RowShape shape;
     int buffers, items_at, ring_at, slots, smem;
 };
-DownPlan plan_down(int T, int K, int E) {
+DownPlan plan_down(int T, int K, int E, int row_bytes) {
     DownPlan p;
-    // two buffers of sums, so that a tile's may be added while the next tile's are made, where that leaves room for four slots
+    p.shape = RowShape::of(row_bytes);
+    // two buffers of sums, so that a tile's may be added while the next tile's are made, where that leaves room for two slots
     p.buffers = T <= 24 ? 2 : 1;
     p.items_at = kMvWarps * kMaxSlots * 8 + p.buffers * kMvWarps * T * 64;
-    p.ring_at = (p.items_at + Items::bytes(T * K, E) + 127) / 128 * 128;
+    p.ring_at = (p.items_at + Items::bytes(T * K, E) + 1023) / 1024 * 1024;
     const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlotBytes);
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
     p.smem = p.ring_at + p.slots * kMvWarps * kSlotBytes;
@@ -198,10 +223,11 @@ DownPlan plan_down(int T, int K, int E) {
 }
 
 template <int GS>
-__global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ DownPlan plan) {
+__global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ Weights weights,
+                                                                    const __grid_constant__ DownPlan plan) {
     using F = Fmt<GS>;
     constexpr int kGS = GS ? GS : 1;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     float* sums = reinterpret_cast<float*>(smem + kMvWarps * kMaxSlots * 8);  // [buffer][warp][T][16]
     const Items it(smem + plan.items_at, a.T * a.K, a.E);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
@@ -211,29 +237,25 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     // writes the activations alone.
     build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk2);
 
-    const int r0 = (int)((int64_t)a.H * blockIdx.x / gridDim.x), r1 = (int)((int64_t)a.H * (blockIdx.x + 1) / gridDim.x);
-    const RowShape shape(F::row_bytes(a.I));
-    const int row_scales = F::scales(a.I), segments = F::segments(a.I);
+    const Share share(a.H);
+    const int r0 = share.first, r1 = share.last;
+    const RowShape& shape = plan.shape;
+    const int row_scales = F::scales(a.I), segments = shape.segments;
     const bool wide = row_scales % kGS == 0;
     const int total = it.count() * segments;
     const int f0 = total * warp / kMvWarps, f1 = total * (warp + 1) / kMvWarps;  // total <= 2^18
     const int item0 = f0 / segments, seg0 = f0 - item0 * segments;
     SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
-    const int row_at = shape.offset(g);
 
-    // Copies: the next half (tile, item, segment, first or second rows).
-    int crow = r0, cf = f0, citem = item0, cseg = seg0, chalf = 0, crows = 0;
+    // Copies: the next (tile, item, segment).
+    int crow = r0, cf = f0, citem = item0, cseg = seg0;
     bool more = f0 < f1 && r0 < r1;
-    const uint8_t* cbase = nullptr;
-    auto aim = [&]() {
-        crows = min(16, r1 - crow);
-        cbase = a.w2 + ((int64_t)uniform(it.expert[citem]) * a.H + crow) * shape.row_bytes;
-    };
-    auto copy_half = [&]() {
+    int cfirst = 0;
+    auto aim = [&]() { cfirst = uniform(it.expert[citem]) * a.H + crow; };  // at most 2^23
+    auto fill = [&]() {
         if (!more) return;
-        ring.copy(shape, cbase + cseg * kSegment + (chalf ? (int64_t)(crows / 2) * shape.row_bytes : 0), (crows + 1) / 2, shape.bytes(cseg), lane);
-        chalf ^= 1;
-        if (chalf) return;
+        const int rows = min(16, r1 - crow);
+        ring.fill(weights, cfirst, cfirst + rows / 2, (rows + 1) / 2, cseg * kSegment, shape.bytes(cseg), lane);
         if (++cf == f1) {
             cf = f0;
             citem = item0;
@@ -248,7 +270,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         }
     };
     if (more) aim();
-    for (int s = 0; s < plan.slots; ++s) copy_half();
+    for (int s = 0; s < plan.slots; ++s) {
+        fill();
+        ring.next();
+    }
+    ring.phase = 0;
     pdl_wait();  // the activations
 
     for (int row = r0, buf = 0; row < r1; row += 16, buf ^= plan.buffers - 1) {
@@ -263,42 +289,42 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         DirectColumns<kGS> direct;
         Scales<kGS> next;
         const uint16_t* act = nullptr;
-        const uint16_t *scale0 = nullptr, *scale1 = nullptr;
+        const uint16_t* scale = nullptr;
+        const uint32_t off0 = (unsigned)min(g, pairs - 1) * row_scales + t * kGS, off1 = off0 + rows / 2 * row_scales;
         auto enter = [&](int item) {
             const int e = (g & 3) < it.n[item] ? g & 3 : 0;
             act = a.act + ((int64_t)it.slot[it.off[item] + e] * 2 + (g >> 2)) * a.I;
             if constexpr (F::kW4) {
-                scale0 = a.s2 + ((int64_t)uniform(it.expert[item]) * a.H + row + min(g, pairs - 1)) * row_scales;
-                scale1 = scale0 + rows / 2 * row_scales;
+                scale = a.s2 + ((int64_t)uniform(it.expert[item]) * a.H + row) * row_scales;
             }
         };
-        auto load_step = [&](int segment, int q) {
-            const int at = segment * F::kSegK + q * F::kStepK;
+        auto load_part = [&](int segment, int q) {  // a step (4-bit) or a quarter of the lane's values
+            const int at = segment * F::kSegK;
             if constexpr (F::kW4)
-                direct.load(act + at, a.I - at, t);
+                direct.load(act + at + q * F::kStepK, a.I - at - q * F::kStepK, t);
             else
-                col[q] = load_column<true>(act + at, a.I - at, t);
+                col[q] = load_column<true>(act + at, a.I - at, q, t);
         };
         auto load_scales = [&](int segment) {
-            const int at = (segment * 4 + t) * kGS;
-            next.load(scale0 + at, scale1 + at, row_scales - at, wide);
+            const int at = segment * 4 * kGS;
+            next.load(scale + at, off0, off1, row_scales - at - t * kGS, at + 4 * kGS <= row_scales, wide);
         };
         int item = item0, seg = seg0;
         if (f0 < f1) {
             enter(item);
             if constexpr (F::kW4) {
                 load_scales(seg);
-                load_step(seg, 0);
+                load_part(seg, 0);
             } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) load_step(seg, q);
+                for (int q = 0; q < 4; ++q) load_part(seg, q);
             }
         }
         float acc[1][4] = {};
         for (int f = f0; f < f1; ++f) {
             const bool last = seg + 1 == segments, final = f + 1 == f1;
             const int after = last ? 0 : seg + 1, bytes = shape.bytes(seg);
-            const uint32_t lo = ring.wait() + row_at, hi = ring.wait() + row_at;
+            ring.wait();
             if constexpr (F::kW4) {
                 const Scales<kGS> now = next;
 #pragma unroll
@@ -306,23 +332,23 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                     if (q * 64 < bytes) {
                         const DirectColumns<kGS> columns = direct;
                         if (q * 64 + 64 < bytes) {
-                            load_step(seg, q + 1);
+                            load_part(seg, q + 1);
                         } else if (!final) {
                             if (last) enter(item + 1);
                             load_scales(after);
-                            load_step(after, 0);
+                            load_part(after, 0);
                         }
-                        multiply_w4<kGS, 1>(acc, lo, hi, columns, now, q, lane);
+                        multiply_w4<kGS, 1>(acc, ring.slot, columns, now, q, lane);
                     }
             } else {
                 if (last && !final) enter(item + 1);
-                multiply_bf16(acc[0], lo, hi, col, bytes, t, [&](int q) {
-                    if (!final) load_step(after, q);
+                multiply_bf16(acc[0], ring.slot, col, bytes, lane, [&](int q) {
+                    if (!final) load_part(after, q);
                 });
             }
-            __syncwarp();  // all lanes have read both slots
-            copy_half();
-            copy_half();
+            __syncwarp();  // all lanes have read the slot
+            fill();
+            ring.next();
             if (last || final) {
                 // high part + low part, times the routing weight, to the token's sums
                 const int n = it.n[item], at = it.off[item];
@@ -367,7 +393,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
 }
 
 template <typename Kernel, typename Plan>
-cudaError_t launch(Kernel kernel, const ExpertsArgs& a, const Plan& plan, int grid, cudaStream_t stream, bool pdl) {
+cudaError_t launch(Kernel kernel, const ExpertsArgs& a, const Weights& weights, const Plan& plan, int grid, cudaStream_t stream, bool pdl) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)grid);
@@ -378,15 +404,19 @@ cudaError_t launch(Kernel kernel, const ExpertsArgs& a, const Plan& plan, int gr
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a, plan);
+    return cudaLaunchKernelEx(&cfg, kernel, a, weights, plan);
 }
 
 template <int GS>
 cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
     const int tokens = a.T < kChunk1 ? a.T : kChunk1;
-    cudaError_t e = launch(moe_gate_up_kernel<GS>, a, plan_product<GS, 1>(a.H, tokens, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
+    Weights w13, w2;
+    cudaError_t e = describe_weights(&w13, a.w13, (int64_t)a.E * 2 * a.I, Fmt<GS>::row_bytes(a.H));
+    if (e == cudaSuccess) e = describe_weights(&w2, a.w2, (int64_t)a.E * a.H, Fmt<GS>::row_bytes(a.I));
     if (e != cudaSuccess) return e;
-    return launch(moe_down_kernel<GS>, a, plan_down(a.T, a.K, a.E), num_sms, stream, true);
+    e = launch(moe_gate_up_kernel<GS>, a, w13, plan_product<GS, 1>(a.H, tokens, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
+    if (e != cudaSuccess) return e;
+    return launch(moe_down_kernel<GS>, a, w2, plan_down(a.T, a.K, a.E, Fmt<GS>::row_bytes(a.I)), num_sms, stream, true);
 }
 
 template <int GS>
@@ -397,6 +427,33 @@ cudaError_t set_attributes() {
 }
 
 }  // namespace
+
+cudaError_t describe_weights(Weights* w, const void* q, int64_t rows, int row_bytes) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<Encode> cached{nullptr};  // the same in every thread
+    Encode encode = cached.load(std::memory_order_acquire);
+    if (!encode) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+        encode = reinterpret_cast<Encode>(f);
+        cached.store(encode, std::memory_order_release);
+    }
+    const cuuint64_t dim[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t unit[2] = {1, 1};
+    for (int i = 0; i < 2; ++i) {
+        const cuuint32_t box[2] = {kBox, i == 0 ? 8u : 1u};
+        if (encode(i == 0 ? &w->eight : &w->one, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dim, pitch, box, unit,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    return cudaSuccess;
+}
 
 cudaError_t launch_moe_experts(const ExpertsArgs& a, int group, int num_sms, cudaStream_t stream, bool pdl) {
     switch (group) {
