@@ -16,17 +16,32 @@ template <int GS>
 struct Matvec {
     const MatvecArgs& a;
     int r0, r1;
-    int block, chunk;  // rows and tokens per job
+    int block, chunk;  // rows and tokens per job, at most
     struct Job {
-        int pairs, tokens;
-        int row, rows, token;
+        int count;
+        int row, rows, token, tokens;
+    };
+    struct Tile {
+        int pairs, tokens, first, second;
+        int odd, token;  // whether the first pair's rows are one and the same rows' middle
     };
     __device__ void at(Job& j, int row, int token) const {
         j.row = row;
         j.rows = min(block, r1 - row);
-        j.pairs = (j.rows + 1) / 2;
+        j.count = (j.rows + 15) >> 4;
         j.token = token;
         j.tokens = min(chunk, a.T - token);
+    }
+    __device__ Tile tile(const Job& j, int i) const {
+        Tile t;
+        const int pairs = (j.rows + 1) / 2 - 8 * i;
+        t.pairs = max(0, min(8, pairs));
+        t.tokens = j.tokens;
+        t.first = j.row + 8 * i;
+        t.second = t.first + j.rows / 2;
+        t.odd = i == 0 && j.rows % 2;
+        t.token = j.token;
+        return t;
     }
     __device__ bool first(Job& j) const {
         if (r0 >= r1) return false;
@@ -43,22 +58,23 @@ struct Matvec {
         return true;
     }
     __device__ const uint16_t* scales() const { return a.s; }
-    __device__ int64_t rows(const Job& j) const { return j.row; }
-    __device__ int row_step(const Job& j) const { return j.rows / 2; }
     __device__ void lost() const {}
-    __device__ const uint16_t* x(const Job& j, int token) const { return a.x + (int64_t)(j.token + token) * a.K; }
-    __device__ int key(const Job& j) const { return j.token; }
-    __device__ void store(const Job& j, int pair, int token, float first, float second) const {
-        const int64_t o = (int64_t)(j.token + token) * a.N + j.row + pair;
-        const bool both = pair > 0 || j.rows % 2 == 0;  // the middle row of an odd number is a first row
+    __device__ const uint16_t* x(const Tile& t, int i) const { return a.x + (int64_t)(t.token + i) * a.K; }
+    __device__ int staged_key(const Job& j) const { return j.token; }
+    __device__ int staged(const Job& j) const { return j.tokens; }
+    __device__ const uint16_t* staged_x(const Job& j, int i) const { return a.x + (int64_t)(j.token + i) * a.K; }
+    __device__ int column(const Tile&, int i) const { return i; }
+    __device__ void store(const Tile& t, int pair, int token, float first, float second) const {
+        const int64_t o = (int64_t)(t.token + token) * a.N;
+        const bool both = pair > 0 || !t.odd;  // the middle row of an odd number is a first row
         if (a.out_f32) {
-            float* out = reinterpret_cast<float*>(a.out) + o;
-            out[0] = first;
-            if (both) out[j.rows / 2] = second;
+            float* out = reinterpret_cast<float*>(a.out) + o + pair;
+            out[t.first] = first;
+            if (both) out[t.second] = second;
         } else {
-            uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + o;
-            out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(first));
-            if (both) out[j.rows / 2] = __bfloat16_as_ushort(__float2bfloat16_rn(second));
+            uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + o + pair;
+            out[t.first] = __bfloat16_as_ushort(__float2bfloat16_rn(first));
+            if (both) out[t.second] = __bfloat16_as_ushort(__float2bfloat16_rn(second));
         }
     }
 };
@@ -68,7 +84,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_c
     extern __shared__ __align__(1024) uint8_t smem[];
     const Share rows(a.N);
     Matvec<GS> jobs{a, rows.first, rows.last, 0, 8 * NT};
-    const int split = plan.ways.pick((rows.last - rows.first + 15) >> 4);
+    const int split = plan.ways.pick((rows.last - rows.first + 15) >> 4, false);
     jobs.block = 16 * (kMvWarps >> split);
     run_product<GS, NT>(jobs, weights, smem, plan, a.K, split);
 }

@@ -335,9 +335,9 @@ struct StagedView {
 };
 
 __device__ __forceinline__ void sts_f32(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-__device__ __forceinline__ float2 lds_f32x2(uint32_t a) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
 
@@ -391,34 +391,50 @@ __device__ __forceinline__ void stage_segment(const StagedView<GS, NT>& v, int s
 // Staged in shared memory: a segment.
 template <int GS, int NT>
 struct StagedColumns {
-    uint32_t values[NT], sums, factors;
-    __device__ __forceinline__ StagedColumns(const StagedView<GS, NT>& v, int columns, int lane) {
+    uint32_t values[NT], sums[NT][2], factors[NT][2];
+    // column(i): the staged column of column i of the instructions
+    template <class Column>
+    __device__ __forceinline__ void set(const StagedView<GS, NT>& v, int lane, Column column) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) values[n] = v.values + (8 * n + g < columns ? 8 * n + g : 0) * v.stride + t * 16;
-        sums = v.sums + t * 8;
-        factors = v.factors + t * 8;
+        for (int n = 0; n < NT; ++n) {
+            values[n] = v.values + column(8 * n + g) * v.stride + t * 16;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                sums[n][u] = v.sums + column(8 * n + 2 * t + u) * 4;
+                factors[n][u] = v.factors + column(8 * n + 2 * t + u) * 4;
+            }
+        }
     }
     __device__ __forceinline__ StagedColumns at(int segment) const {
         StagedColumns c = *this;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) c.values[n] += segment * 1024;
-        c.sums += segment * 4 * StagedView<GS, NT>::kSums;
-        c.factors += segment * 32 * NT;
+        for (int n = 0; n < NT; ++n) {
+            c.values[n] += segment * 1024;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                c.sums[n][u] += segment * 4 * StagedView<GS, NT>::kSums;
+                c.factors[n][u] += segment * 32 * NT;
+            }
+        }
         return c;
     }
     __device__ __forceinline__ void words(int n, int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
 #pragma unroll
         for (int j = 0; j < 4 / GS; ++j) lds(c[j], values[n] + q * 256 + (s * (4 / GS) + j) * 64);
-        eight = lds_f32x2(sums + q * StagedView<GS, NT>::kSums + (s * NT + n) * 32);
+        const int at = q * StagedView<GS, NT>::kSums + s * NT * 32;
+        eight = make_float2(lds_f32(sums[n][0] + at), lds_f32(sums[n][1] + at));
     }
-    __device__ __forceinline__ float2 factor(int n) const { return lds_f32x2(factors + n * 32); }
+    __device__ __forceinline__ float2 factor(int n) const { return make_float2(lds_f32(factors[n][0]), lds_f32(factors[n][1])); }
 };
 
-// Straight from global memory, one step ahead in registers: v[i] holds the eight
-// values of lane (g, t) that meet its word i.  The power of two is 2^64 whatever
-// the values (sums keep 24 bits while these are between 2^-56 and 2^63), and -8
-// times the sums comes from the matrix instruction with a constant operand.
+// Straight from global memory, where they lie ready for the instruction
+// (ready_at, ready_scale), ahead in registers: v[i] meets the lane's word i.  The
+// power of two is 2^64 whatever the values (sums keep 24 bits while these are
+// between 2^-56 and 2^63), and -8 times the sums comes from the matrix
+// instruction with a constant operand.
+__host__ __device__ inline int ready_at(int i) { return (i & ~7) + (i & 3) * 2 + (i >> 2 & 1); }
+__device__ __forceinline__ float ready_scale(int i) { return i & 1 ? 0x1p60f : 0x1p64f; }
 template <int GS>
 struct DirectColumns {
     uint4 v[4];
@@ -436,21 +452,20 @@ struct DirectColumns {
         }
     }
     __device__ __forceinline__ void words(int, int, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
-        constexpr uint32_t kUp64 = 0x5f805f80u, kUp60 = 0x5d805d80u;  // 2^64 and 2^60, twice
         constexpr uint32_t kMinus8 = 0x80088008u, kMinus8x16 = 0x80808080u;
         float sum[4];
 #pragma unroll
         for (int j = 0; j < 4 / GS; ++j) {
             const uint4 w = v[s * (4 / GS) + j];
-            c[j][0] = mul_bf16x2(__byte_perm(w.x, w.z, 0x5410), kUp64);
-            c[j][1] = mul_bf16x2(__byte_perm(w.x, w.z, 0x7632), kUp60);
-            c[j][2] = mul_bf16x2(__byte_perm(w.y, w.w, 0x5410), kUp64);
-            c[j][3] = mul_bf16x2(__byte_perm(w.y, w.w, 0x7632), kUp60);
+            c[j][0] = w.x;
+            c[j][1] = w.y;
+            c[j][2] = w.z;
+            c[j][3] = w.w;
             if (j == 0)
-                mma_bf16_from(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][0], c[j][1], 0.f, 0.f, 0.f, 0.f);
+                mma_bf16_from(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, w.x, w.y, 0.f, 0.f, 0.f, 0.f);
             else
-                mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][0], c[j][1]);
-            mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][2], c[j][3]);
+                mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, w.x, w.y);
+            mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, w.z, w.w);
         }
         eight = make_float2(sum[0], sum[1]);
     }
@@ -488,6 +503,10 @@ struct Scales {
                 }
             }
         }
+    }
+    // Brings a later segment's into L2.
+    __device__ static __forceinline__ void prefetch(const uint16_t* base, uint32_t off0, uint32_t off1, int t) {
+        if (t < 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(base + (t ? off1 : off0)));
     }
     // Scale of group s of step q for the lane's row.
     __device__ __forceinline__ float get(int h, int q, int s, int lane) const {
@@ -557,9 +576,10 @@ __device__ __forceinline__ void add_scaled(float (&acc)[NT][4], const float (&su
 
 // ----------------------------------------------------------------- products
 // How the sixteen warps of a CTA share tiles: 2^ways of them split a tile's
-// segments, 16 / 2^ways tiles go side by side.  The least work for the busiest
-// warp; among equals the fewest rounds (each costs a reduction, and 4-bit weights
-// of many tokens their activations again), then the most ways.
+// segments, 16 / 2^ways tiles go side by side (the ways take turns at what is
+// left over from one round of tiles to the next).  The least work for the
+// busiest warp; among equals the fewest rounds (each costs a reduction), then the
+// most ways.  cut: rounds may end early once (at an expert's end).
 struct Ways {
     int each[5];  // segments of the busiest way, for 2^i ways
     __host__ static Ways of(int segments) {
@@ -567,11 +587,12 @@ struct Ways {
         for (int i = 0; i < 5; ++i) w.each[i] = (segments + (1 << i) - 1) >> i;
         return w;
     }
-    __device__ __forceinline__ int pick(int tiles) const {
+    __device__ __forceinline__ int pick(int tiles, bool cut) const {
         int best = 4, cost = 0x7fffffff;
 #pragma unroll
         for (int i = 4; i >= 0; --i) {
-            const int rounds = (min(tiles, 1 << 14) + (16 >> i) - 1) >> (4 - i), c = each[i] * rounds * 64 + min(rounds, 63);
+            const int side = 16 >> i, rounds = (min(tiles, 1 << 14) + (cut ? side - 1 : 0) + side - 1) >> (4 - i);
+            const int c = each[i] * rounds * 64 + min(rounds, 63);
             if (c < cost) {
                 cost = c;
                 best = i;
@@ -621,72 +642,80 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
     return p;
 }
 
-// The products of blocks of row pairs with up to 8 * NT tokens each, one block
-// ("job") after the other, the copies running ahead across their borders.  Jobs
-// is a class with
-//   struct Job { int pairs, tokens; .. }: at most 8 * 16 / 2^split pairs, at least one token
+// The products of tiles of row pairs with up to 8 * NT tokens each, up to 16 >>
+// split tiles at a time ("job"), the copies running ahead across the jobs'
+// borders.  Jobs is a class with
+//   struct Job { int count; .. }          tiles of the job
+//   struct Tile { int pairs, tokens, first, second; .. }  0 pairs: no such tile; rows first, first + 1, .. and second, ..
 //   bool first(Job&), next(Job&)          the CTA's jobs in order
-//   rows(job), row_step                   first row of the first pair, rows between a pair's rows
+//   Tile tile(job, i)
 //   scales()                              row 0's
-//   x(job, token), key(job)               a token's activations; equal keys: the same tokens
-//   store(job, pair, token, first, second)  results of a pair's two rows
+//   x(tile, i)                            activations of the tile's token i
+//   staged_key(job), staged(job), staged_x(job, i), column(tile, i): with 4-bit weights the job's tokens that are staged
+//       (equal keys: the same ones), and which of them is the tile's token i
+//   store(tile, pair, token, first, second)  results of a pair's two rows
 //   lost()                                a wait ran out
 // Deterministic: a tile's sums are added in the order of the ways.
 template <int GS, int NT, class Jobs>
 __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& weights, uint8_t* smem, const ProductPlan& plan, int K, int split) {
     using F = Fmt<GS>;
     using Job = typename Jobs::Job;
+    using Tile = typename Jobs::Tile;
     static_assert(F::kW4 || NT == 1, "bf16 weights: one column tile");
     constexpr int kGS = GS ? GS : 1;
     constexpr int kRed = kMvWarps * NT * 128;  // floats, one buffer
     constexpr int kRedAt = kMvWarps * kMaxSlots * 8, kStagedAt = kRedAt + 2 * kRed * 4;
     float* red = reinterpret_cast<float*>(smem + kRedAt);
     const StagedView<kGS, NT> staged(smem_addr(smem) + kStagedAt, plan.panel, plan.columns);
-    const StagedColumns<kGS, NT> staged_columns(staged, plan.columns, threadIdx.x & 31);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     const RowShape& shape = plan.shape;
     const int row_scales = F::scales(K), segments = shape.segments, panel = plan.panel;
     const bool wide = row_scales % kGS == 0;
     const int ways = 1 << split;
-    const int mine = warp >> split, way = warp & (ways - 1);  // tile; segments way, way + ways, .. of a panel
+    const int mine = warp >> split;  // tile of a job
     SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
 
     auto to = [&](int p) { return min(p + panel, segments); };
-    // The warp's first segment of the panels from p on; `segments` or more: none.
-    auto first_from = [&](int p) {
-        while (p < segments && p + way >= to(p)) p += panel;
-        return p + way;
-    };
-    auto pairs_of = [&](const Job& j) { return min(8, j.pairs - 8 * mine); };  // of the warp's tile; none if not positive
+    // The warp's segments of a panel: p + way, p + way + ways, .., with way turning by the panel's length from panel to panel.
+    auto turn = [&](int way, int p) { return (way - (to(p) - p)) & (ways - 1); };
 
     // Copies: the next (job, panel, segment).
     Job cj;
     bool more = jobs.first(cj);
     if (!more) return;
-    int cpanel = 0, cseg = way, cpairs = 0, cfirst = 0, csecond = 0;
-    auto enter = [&]() {
-        cpairs = pairs_of(cj);
-        cfirst = (int)jobs.rows(cj) + 8 * mine;
-        csecond = cfirst + jobs.row_step(cj);
+    auto tile_of = [&](const Job& j) {
+        Tile t = jobs.tile(j, mine);
+        t.pairs = uniform(t.pairs);
+        t.tokens = uniform(t.tokens);
+        t.first = uniform(t.first);
+        t.second = uniform(t.second);
+        return t;
     };
+    Tile ct = tile_of(cj);
+    int cpanel = 0, cway = warp & (ways - 1), cseg = cway;
     auto settle = [&]() {  // to the first segment from here on
-        while (more && (cpairs <= 0 || cseg >= to(cpanel))) {
+        while (more && (ct.pairs == 0 || cseg >= to(cpanel))) {
+            cway = turn(cway, cpanel);
             cpanel += panel;
-            if (cpairs <= 0 || cpanel >= segments) {
+            if (cpanel >= segments) {
                 cpanel = 0;
                 more = jobs.next(cj);
-                if (more) enter();
+                if (more) ct = tile_of(cj);
             }
-            cseg = cpanel + way;
+            cseg = cpanel + cway;
         }
     };
     auto fill = [&]() {
         if (!more) return;
-        ring.fill(weights, cfirst, csecond, cpairs, cseg * kSegment, shape.bytes(cseg), lane);
+        ring.fill(weights, ct.first, ct.second, ct.pairs, cseg * kSegment, shape.bytes(cseg), lane);
+        if constexpr (F::kW4) {
+            const uint32_t off = min(g, ct.pairs - 1) * row_scales;
+            Scales<kGS>::prefetch(jobs.scales() + (int64_t)ct.first * row_scales + cseg * 4 * kGS, off,
+                                  off + (unsigned)(ct.second - ct.first) * row_scales, t);
+        }
         cseg += ways;
         if (cseg >= to(cpanel)) settle();
     };
-    enter();
     settle();
     for (int s = 0; s < plan.slots; ++s) {
         fill();
@@ -697,33 +726,45 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     // Operands of the next segment, asked for one segment ahead, across panels and jobs.
     uint4 col[4];
     Scales<kGS> next;
+    StagedColumns<kGS, NT> columns;
     const uint16_t* x = nullptr;
     const uint16_t* scale = nullptr;
     uint32_t off0 = 0, off1 = 0;
+    int way = warp & (ways - 1);  // in the panel at hand
+    // The warp's first segment of the panels from p on, with way w in the first; `segments` or more: none.
+    auto first_from = [&](int p, int w) {
+        while (p < segments && p + w >= to(p)) {
+            w = turn(w, p);
+            p += panel;
+        }
+        return p < segments ? p + w : segments;
+    };
     auto load_part = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK, K - segment * F::kSegK, q, t); };
     auto load_scales = [&](int segment) {
         const int at = segment * 4 * kGS;
         next.load(scale + at, off0, off1, row_scales - at - t * kGS, at + 4 * kGS <= row_scales, wide);
     };
-    auto begin_job = [&](const Job& j) {
-        const int first = first_from(0);
+    auto begin = [&](const Tile& tile) {
+        if (tile.pairs == 0) return;
+        const int first = first_from(0, way);
         if constexpr (F::kW4) {
-            scale = jobs.scales() + jobs.rows(j) * row_scales;
-            off0 = (unsigned)max(0, min(8 * mine + g, j.pairs - 1)) * row_scales + t * kGS;
-            off1 = off0 + (unsigned)jobs.row_step(j) * row_scales;
+            scale = jobs.scales() + (int64_t)tile.first * row_scales;
+            off0 = (unsigned)min(g, tile.pairs - 1) * row_scales + t * kGS;
+            off1 = off0 + (unsigned)(tile.second - tile.first) * row_scales;
             load_scales(first);
+            columns.set(staged, lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : 0); });
         } else {
-            x = jobs.x(j, g < j.tokens ? g : 0);
+            x = jobs.x(tile, g < tile.tokens ? g : 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) load_part(first, q);
         }
     };
     auto stage = [&](const Job& j, int p) {
-        const int units = (to(p) - p) * j.tokens;  // (segment, token)
-        __syncthreads();                           // the panel before it is done with
+        const int tokens = jobs.staged(j), units = (to(p) - p) * tokens;  // (segment, token)
+        __syncthreads();                                                 // the panel before it is done with
         for (int i = warp; i < units; i += kMvWarps) {
-            const int s = i / j.tokens, token = i - s * j.tokens;
-            const uint16_t* from = jobs.x(j, token);
+            const int s = i / tokens, token = i - s * tokens;
+            const uint16_t* from = jobs.staged_x(j, token);
             uint2 w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -737,70 +778,79 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     };
     Job job;
     jobs.first(job);
-    begin_job(job);
+    Tile tile = tile_of(job);
+    begin(tile);
     int key = -1;
     for (int buf = 0;; buf ^= 1) {
         float acc[NT][4] = {};
-        const int pairs = pairs_of(job);
+        const int order = way;  // of this warp's parts among the job's
         for (int p = 0; p < segments; p += panel) {
-            if (F::kW4 && (panel < segments || jobs.key(job) != key)) {
-                key = jobs.key(job);
+            if (F::kW4 && (panel < segments || jobs.staged_key(job) != key)) {
+                key = jobs.staged_key(job);
                 stage(job, p);
             }
-            if (pairs <= 0) continue;
-            const int end = to(p), behind = first_from(p + panel);
-            for (int seg = p + way; seg < end; seg += ways) {
-                const int after = seg + ways < end ? seg + ways : behind, bytes = shape.bytes(seg);
-                ring.wait();
-                if constexpr (F::kW4) {
-                    const Scales<kGS> now = next;
-                    load_scales(after);
-                    const StagedColumns<kGS, NT> columns = staged_columns.at(seg - p);
-                    float sum[NT][4] = {};
-                    if (bytes == kSegment) {
+            const int end = to(p), then = turn(way, p);
+            if (tile.pairs > 0) {
+                const int behind = first_from(p + panel, then);
+                for (int seg = p + way; seg < end; seg += ways) {
+                    const int after = seg + ways < end ? seg + ways : behind, bytes = shape.bytes(seg);
+                    ring.wait();
+                    if constexpr (F::kW4) {
+                        const Scales<kGS> now = next;
+                        load_scales(after);
+                        const StagedColumns<kGS, NT> here = columns.at(seg - p);
+                        float sum[NT][4] = {};
+                        if (bytes == kSegment) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) multiply_w4<kGS, NT>(sum, ring.slot, columns, now, q, lane);
+                            for (int q = 0; q < 4; ++q) multiply_w4<kGS, NT>(sum, ring.slot, here, now, q, lane);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (q * 64 < bytes) multiply_w4<kGS, NT>(sum, ring.slot, here, now, q, lane);
+                        }
+                        add_scaled(acc, sum, here);
                     } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (q * 64 < bytes) multiply_w4<kGS, NT>(sum, ring.slot, columns, now, q, lane);
+                        float(&one)[4] = acc[0];
+                        multiply_bf16(one, ring.slot, col, bytes, lane, [&](int q) { load_part(after, q); });
                     }
-                    add_scaled(acc, sum, columns);
-                } else {
-                    float(&one)[4] = acc[0];
-                    multiply_bf16(one, ring.slot, col, bytes, lane, [&](int q) { load_part(after, q); });
+                    __syncwarp();  // all lanes have read the slot
+                    fill();
+                    ring.next();
                 }
-                __syncwarp();  // all lanes have read the slot
-                fill();
-                ring.next();
             }
+            way = then;
         }
         const Job done = job;
         const bool end = !jobs.next(job);
-        if (!end) begin_job(job);
+        if (!end) {
+            tile = tile_of(job);
+            begin(tile);
+        }
         if (!ring.alive) {
             jobs.lost();
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = __uint_as_float(0x7fc00000u);
         }
-        // add the ways' parts in order
+        // add the parts in the order of their first segments
         float* r = red + buf * kRed;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            *reinterpret_cast<float4*>(r + (warp * NT + n) * 128 + lane * 4) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            *reinterpret_cast<float4*>(r + (((mine << split) + order) * NT + n) * 128 + lane * 4) =
+                make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
         __syncthreads();  // and the other buffer's readers are done before it is written again
         constexpr int kPairs = 64 * NT;  // (pair, token) per tile
-        for (int i = threadIdx.x; i < (done.pairs + 7) / 8 * kPairs; i += kMvThreads) {
-            const int tile = i / kPairs, n = i % kPairs / 64, l = i % 64;  // l: two columns of a lane's first row
-            const int pair = 8 * tile + (l >> 3), token = 8 * n + (l & 7);
-            if (pair >= done.pairs || token >= done.tokens) continue;
-            const float* q = r + ((tile << split) * NT + n) * 128 + (l >> 1) * 4 + (l & 1);
+        for (int i = threadIdx.x; i < done.count * kPairs; i += kMvThreads) {
+            const int at = i / kPairs, n = i % kPairs / 64, l = i % 64;  // l: two columns of a lane's first row
+            const int pair = l >> 3, token = 8 * n + (l & 7);
+            const Tile of = jobs.tile(done, at);
+            if (pair >= of.pairs || token >= of.tokens) continue;
+            const float* q = r + ((at << split) * NT + n) * 128 + (l >> 1) * 4 + (l & 1);
             float first = 0.0f, second = 0.0f;
             for (int w = 0; w < ways; ++w) {
                 first += q[w * NT * 128];
                 second += q[w * NT * 128 + 2];
             }
-            jobs.store(done, pair, token, first, second);
+            jobs.store(of, pair, token, first, second);
         }
         if (end) break;
     }

@@ -139,47 +139,79 @@ __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsA
 
 // ------------------------------------------------------------- first product
 // The CTA's share of the (item, row pair) list, a pair being gate row i and up
-// row I + i of the item's expert.
+// row I + i of the item's expert.  Tiles are the list's eights (I is a multiple
+// of 8, so that each is one item's), the share's first and last cut where it is.
+//
+// Staged activations (4-bit): all tokens if there are no more than eight, else a
+// job's tiles are one item's and its tokens are staged.
 template <int GS>
 struct GateUp {
     const ExpertsArgs& a;
     const Items& it;
-    int q0, q1;       // pairs
-    int block;        // pairs per job
+    int q0, q1;     // pairs
+    int eights;     // per item
+    int side;       // tiles per job, at most
+    bool together;  // tiles of several items in a job
     struct Job {
-        int pairs, tokens;
-        int q, item, i0, expert;
+        int count;
+        int eight;  // first
+        int item, tokens;
     };
-    __device__ void at(Job& j, int q) const {
-        j.q = q;
-        j.item = q / a.I;
-        j.i0 = q - j.item * a.I;
-        j.pairs = min(min(block, a.I - j.i0), q1 - q);
-        j.tokens = uniform(it.n[j.item]);
-        j.expert = uniform(it.expert[j.item]);
+    struct Tile {
+        int pairs, tokens, first, second;
+        int item, entry, i0;
+    };
+    __device__ void at(Job& j, int eight) const {
+        j.eight = eight;
+        j.count = min(side, ((q1 + 7) >> 3) - eight);
+        j.item = 0;
+        j.tokens = a.T;
+        if (!together) {
+            j.item = eight / eights;
+            j.count = min(j.count, (j.item + 1) * eights - eight);
+            j.tokens = it.n[j.item];
+        }
+    }
+    __device__ Tile tile(const Job& j, int i) const {
+        Tile t;
+        t.pairs = t.tokens = t.first = t.second = t.item = t.entry = t.i0 = 0;
+        if (i >= j.count) return t;
+        const int eight = j.eight + i, begin = max(q0, eight * 8), end = min(q1, eight * 8 + 8);
+        t.pairs = end - begin;
+        t.item = eight / eights;
+        t.tokens = it.n[t.item];
+        t.entry = it.off[t.item];
+        t.i0 = begin - t.item * a.I;
+        t.first = it.expert[t.item] * 2 * a.I + t.i0;  // at most 2^24
+        t.second = t.first + a.I;
+        return t;
     }
     __device__ bool first(Job& j) const {
         if (q0 >= q1) return false;
-        at(j, q0);
+        at(j, q0 >> 3);
         return true;
     }
     __device__ bool next(Job& j) const {
-        if (j.q + j.pairs >= q1) return false;
-        at(j, j.q + j.pairs);
+        const int eight = j.eight + j.count;
+        if (eight * 8 >= q1) return false;
+        at(j, eight);
         return true;
     }
     __device__ const uint16_t* scales() const { return a.s13; }
-    __device__ int64_t rows(const Job& j) const { return (int64_t)j.expert * 2 * a.I + j.i0; }
-    __device__ int row_step(const Job&) const { return a.I; }
     __device__ void lost() const { atomicOr(a.err, kErrTimeout); }
-    __device__ int entry(const Job& j, int token) const { return it.off[j.item] + token; }
-    __device__ const uint16_t* x(const Job& j, int token) const { return a.x + (int64_t)it.token[entry(j, token)] * a.H; }
-    __device__ int key(const Job& j) const { return a.T == 1 ? 0 : j.item; }
-    __device__ void store(const Job& j, int pair, int token, float gate, float up) const {
-        const float v = gate / (1.0f + expf(-gate)) * up;
+    __device__ const uint16_t* x(const Tile& t, int i) const { return a.x + (int64_t)it.token[t.entry + i] * a.H; }
+    __device__ int staged_key(const Job& j) const { return j.item; }
+    __device__ int staged(const Job& j) const { return j.tokens; }
+    __device__ const uint16_t* staged_x(const Job& j, int i) const {
+        return a.x + (int64_t)(together ? i : it.token[it.off[j.item] + i]) * a.H;
+    }
+    __device__ int column(const Tile& t, int i) const { return together ? it.token[t.entry + i] : i; }
+    __device__ void store(const Tile& t, int pair, int token, float gate, float up) const {
+        const int i = t.i0 + pair;
+        const float v = gate / (1.0f + expf(-gate)) * up * (GS ? ready_scale(i) : 1.0f);
         const __nv_bfloat16 high = __float2bfloat16_rn(v);
         const float rest = v - __bfloat162float(high);  // an infinite value has no rest
-        uint16_t* o = a.act + (int64_t)it.slot[entry(j, token)] * 2 * a.I + j.i0 + pair;
+        uint16_t* o = a.act + (int64_t)it.slot[t.entry + token] * 2 * a.I + (GS ? ready_at(i) : i);
         o[0] = __bfloat16_as_ushort(high);
         o[a.I] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.0f));
     }
@@ -193,10 +225,13 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
     pdl_wait();     // no global memory access before this point
     pdl_trigger();  // after it: what the second kernel reads before its own wait is complete
     build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk1);
-    const Share pairs(it.count() * a.I);  // at most 2^24
-    GateUp<GS> jobs{a, it, pairs.first, pairs.last, 0};
-    const int split = plan.ways.pick((pairs.last - pairs.first + 7) >> 3);
-    jobs.block = 8 * (kMvWarps >> split);
+    // Shares of whole tiles where a CTA has at least eight (then at most one in nine is idle at the end), else of pairs.
+    const int pairs = it.count() * a.I;  // at most 2^24
+    const bool tiles = pairs >= 64 * (int)gridDim.x;
+    const Share share(tiles ? pairs >> 3 : pairs);
+    GateUp<GS> jobs{a, it, share.first << (tiles ? 3 : 0), share.last << (tiles ? 3 : 0), a.I >> 3, 0, GS == 0 || a.T <= kChunk1};
+    const int split = plan.ways.pick(((jobs.q1 + 7) >> 3) - (jobs.q0 >> 3), !jobs.together);
+    jobs.side = kMvWarps >> split;
     run_product<GS, 1>(jobs, weights, smem, plan, a.H, split);
 }
 
@@ -256,6 +291,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         if (!more) return;
         const int rows = min(16, r1 - crow);
         ring.fill(weights, cfirst, cfirst + rows / 2, (rows + 1) / 2, cseg * kSegment, shape.bytes(cseg), lane);
+        if constexpr (F::kW4) {
+            const uint32_t off = min(g, (rows + 1) / 2 - 1) * row_scales;
+            Scales<kGS>::prefetch(a.s2 + (int64_t)cfirst * row_scales + cseg * 4 * kGS, off, off + rows / 2 * row_scales, t);
+        }
         if (++cf == f1) {
             cf = f0;
             citem = item0;
@@ -286,7 +325,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         __syncwarp();
         // the next segment's operands
         uint4 col[4];
-        DirectColumns<kGS> direct;
+        DirectColumns<kGS> direct[2];  // a box's two steps
         Scales<kGS> next;
         const uint16_t* act = nullptr;
         const uint16_t* scale = nullptr;
@@ -301,7 +340,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         auto load_part = [&](int segment, int q) {  // a step (4-bit) or a quarter of the lane's values
             const int at = segment * F::kSegK;
             if constexpr (F::kW4)
-                direct.load(act + at + q * F::kStepK, a.I - at - q * F::kStepK, t);
+                direct[q & 1].load(act + at + q * F::kStepK, a.I - at - q * F::kStepK, t);
             else
                 col[q] = load_column<true>(act + at, a.I - at, q, t);
         };
@@ -315,6 +354,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             if constexpr (F::kW4) {
                 load_scales(seg);
                 load_part(seg, 0);
+                load_part(seg, 1);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) load_part(seg, q);
@@ -327,18 +367,23 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             ring.wait();
             if constexpr (F::kW4) {
                 const Scales<kGS> now = next;
+                // boxes of two steps; of what is behind the end of the rows codes and activations are zero
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (q * 64 < bytes) {
-                        const DirectColumns<kGS> columns = direct;
-                        if (q * 64 + 64 < bytes) {
-                            load_part(seg, q + 1);
-                        } else if (!final) {
+                for (int box = 0; box < 2; ++box)
+                    if (box * kBox < bytes) {
+                        const bool end = box == 1 || bytes <= kBox;
+                        if (end && !final) {
                             if (last) enter(item + 1);
                             load_scales(after);
-                            load_part(after, 0);
                         }
-                        multiply_w4<kGS, 1>(acc, ring.slot, columns, now, q, lane);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            multiply_w4<kGS, 1>(acc, ring.slot, direct[q], now, 2 * box + q, lane);
+                            if (!end)
+                                load_part(seg, 2 + q);
+                            else if (!final)
+                                load_part(after, q);
+                        }
                     }
             } else {
                 if (last && !final) enter(item + 1);
@@ -354,7 +399,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                 const int n = it.n[item], at = it.off[item];
                 if (F::kW4)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[0][u] *= direct.factor(0).x;
+                    for (int u = 0; u < 4; ++u) acc[0][u] *= direct[0].factor(0).x;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) acc[0][u] += __shfl_xor_sync(0xffffffffu, acc[0][u], 2);
 #pragma unroll
