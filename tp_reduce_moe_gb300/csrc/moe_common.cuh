@@ -133,6 +133,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ int warp_index() { return uniform((int)(threadIdx.x >> 5)); }
 
+// The pair of a tile that lane row g (of the eight) stands for: an order in which
+// reads of a quarter (16 bytes a lane), half (8) or whole warp (4) meet every
+// bank of the swizzled rows once.
+template <int GS>
+__host__ __device__ constexpr int pair_of_row(int g) {
+    return GS == 1 ? (g >> 1 | (g & 1) << 2) : GS == 2 ? ((g & 3) << 1 | g >> 2) : g;
+}
+
 // --------------------------------------------------------------------- ring
 // Rows go through the kernels in pairs: a tile is eight pairs, the first rows
 // of the pairs as rows 0-7 of the matrix instruction and the second ones as
@@ -149,7 +157,7 @@ constexpr int kBox = 128;
 constexpr int kBoxBytes = 8 * kBox;
 constexpr int kHalfBytes = 2 * kBoxBytes;
 constexpr int kSlotBytes = 2 * kHalfBytes;
-constexpr int kMaxSlots = 4;
+constexpr int kMaxSlots = 2;
 
 // A weight matrix for the copies, in boxes of eight rows and of one.
 struct Weights {
@@ -317,20 +325,20 @@ __device__ __forceinline__ void multiply_bf16(float (&acc)[4], uint32_t slot, ui
 // codes that a lane reads) of 16 bytes a lane: values (0, 4) (1, 5) (2, 6) (3,
 // 7) of eight.  Columns are 64 bytes further apart than that, so that reads of
 // two of them meet no bank twice.
-template <int GS, int NT>
+// Behind the columns, for every column: of each segment the sums of its 4 * GS
+// groups, then the factor (padded to 16 bytes).
+template <int GS>
 struct StagedView {
-    static constexpr int kSums = GS * 8 * NT * 4;  // bytes per step
-    uint32_t values, sums, factors;                // shared addresses
-    int stride;                                    // between columns
+    static constexpr int kExtra = (4 * GS + 4) * 4;  // bytes per segment and column
+    uint32_t values, extras;                         // shared addresses
+    int stride, extra_stride;                        // between columns
     // `segments` of `columns` tokens: bytes in all
-    __host__ __device__ static int bytes(int segments, int columns) {
-        return columns * (segments * 1024 + 64) + segments * (4 * kSums + 8 * NT * 4);
-    }
+    __host__ __device__ static int bytes(int segments, int columns) { return columns * (segments * (1024 + kExtra) + 64); }
     __device__ __forceinline__ StagedView(uint32_t at, int segments, int columns) {
         values = at;
         stride = segments * 1024 + 64;
-        sums = at + columns * stride;
-        factors = sums + segments * 4 * kSums;
+        extras = at + columns * stride;
+        extra_stride = segments * kExtra;
     }
 };
 
@@ -343,8 +351,8 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
 
 // One warp: a segment (512 bf16 values) of a token into column `col`; of step q
 // the lane holds values 4 * lane .. + 3 in w[q] (zero behind the end of the row).
-template <int GS, int NT>
-__device__ __forceinline__ void stage_segment(const StagedView<GS, NT>& v, int segment, int col, const uint2 (&w)[4], int lane) {
+template <int GS>
+__device__ __forceinline__ void stage_segment(const StagedView<GS>& v, int segment, int col, const uint2 (&w)[4], int lane) {
     float big = 0.0f;
     bool undefined = false;
 #pragma unroll
@@ -364,6 +372,7 @@ __device__ __forceinline__ void stage_segment(const StagedView<GS, NT>& v, int s
     constexpr int kPer = 4 / GS;
     const int t = u / kPer % 4, i = u / (4 * kPer) * kPer + u % kPer;
     const uint32_t at = v.values + col * v.stride + segment * 1024 + i * 64 + t * 16 + odd * 8;
+    const uint32_t extra = v.extras + col * v.extra_stride + segment * v.kExtra;
     const float minus8 = __uint_as_float(up << 23) * (-8.0f * 0x1p-126f) * 0x1p-7f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -376,11 +385,10 @@ __device__ __forceinline__ void stage_segment(const StagedView<GS, NT>& v, int s
                     (__uint_as_float(w[q].y << 16) + __uint_as_float(w[q].y & 0xffff0000u));
 #pragma unroll
         for (int o = 1; o < 32 / GS; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane % (32 / GS) == 0)
-            sts_f32(v.sums + (segment * 4 + q) * v.kSums + lane / (32 / GS) * 32 * NT + col * 4, sum * minus8);
+        if (lane % (32 / GS) == 0) sts_f32(extra + (q * GS + lane / (32 / GS)) * 4, sum * minus8);
     }
     if (lane == 0)
-        sts_f32(v.factors + (segment * 8 * NT + col) * 4,
+        sts_f32(extra + 16 * GS,
                 bad ? __uint_as_float(0x7fc00000u) : 0x1p127f / __uint_as_float(up << 23) * 0x1p6f);
 }
 
@@ -391,41 +399,41 @@ __device__ __forceinline__ void stage_segment(const StagedView<GS, NT>& v, int s
 // Staged in shared memory: a segment.
 template <int GS, int NT>
 struct StagedColumns {
-    uint32_t values[NT], sums[NT][2], factors[NT][2];
+    uint32_t values[NT], extras[NT][2];
+    uint32_t sums[NT][2][4];  // four of columns 2t and 2t + 1
     // column(i): the staged column of column i of the instructions
     template <class Column>
-    __device__ __forceinline__ void set(const StagedView<GS, NT>& v, int lane, Column column) {
+    __device__ __forceinline__ void set(const StagedView<GS>& v, int lane, Column column) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             values[n] = v.values + column(8 * n + g) * v.stride + t * 16;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                sums[n][u] = v.sums + column(8 * n + 2 * t + u) * 4;
-                factors[n][u] = v.factors + column(8 * n + 2 * t + u) * 4;
-            }
+            for (int u = 0; u < 2; ++u) extras[n][u] = v.extras + column(8 * n + 2 * t + u) * v.extra_stride;
         }
     }
     __device__ __forceinline__ StagedColumns at(int segment) const {
-        StagedColumns c = *this;
+        StagedColumns c;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            c.values[n] += segment * 1024;
+            c.values[n] = values[n] + segment * 1024;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                c.sums[n][u] += segment * 4 * StagedView<GS, NT>::kSums;
-                c.factors[n][u] += segment * 32 * NT;
-            }
+            for (int u = 0; u < 2; ++u) c.extras[n][u] = extras[n][u] + segment * StagedView<GS>::kExtra;
         }
         return c;
     }
-    __device__ __forceinline__ void words(int n, int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
+    // In order: q, s.
+    __device__ __forceinline__ void words(int n, int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) {
 #pragma unroll
         for (int j = 0; j < 4 / GS; ++j) lds(c[j], values[n] + q * 256 + (s * (4 / GS) + j) * 64);
-        const int at = q * StagedView<GS, NT>::kSums + s * NT * 32;
-        eight = make_float2(lds_f32(sums[n][0] + at), lds_f32(sums[n][1] + at));
+        const int i = q * GS + s;
+        if (i % 4 == 0) {
+            lds(sums[n][0], extras[n][0] + i * 4);
+            lds(sums[n][1], extras[n][1] + i * 4);
+        }
+        eight = make_float2(__uint_as_float(sums[n][0][i % 4]), __uint_as_float(sums[n][1][i % 4]));
     }
-    __device__ __forceinline__ float2 factor(int n) const { return make_float2(lds_f32(factors[n][0]), lds_f32(factors[n][1])); }
+    __device__ __forceinline__ float2 factor(int n) const { return make_float2(lds_f32(extras[n][0] + 16 * GS), lds_f32(extras[n][1] + 16 * GS)); }
 };
 
 // Straight from global memory, where they lie ready for the instruction
@@ -473,33 +481,34 @@ struct DirectColumns {
 };
 
 // ------------------------------------------------------------------- scales
-// bf16 group scales of a segment's rows, one segment ahead in registers: lane
-// (g, t) holds those of step t for the first and second row of pair g.
+// bf16 group scales of a segment's rows, one segment ahead in registers: a lane
+// holds those of its two rows, all (up to two groups a step) or those of step t
+// (four groups; the others come from its neighbours).
 template <int GS>
 struct Scales {
-    static constexpr int kWords = GS == 4 ? 2 : 1;
+    static constexpr bool kAll = GS < 4;
+    static constexpr int kGroups = kAll ? 4 * GS : GS;  // scales of a row in a lane
+    static constexpr int kWords = kGroups / 2;
     uint32_t raw[2][kWords];
-    // base: the segment's first scale in the tile's first row; off0, off1: from there to the lane's first in its two rows;
-    // groups: from the lane's first to the end of the row (zeros behind it), all of them: no lane's step is cut; wide: aligned
-    // to their size
-    __device__ __forceinline__ void load(const uint16_t* base, uint32_t off0, uint32_t off1, int groups, bool all, bool wide) {
+    // base: the segment's first scale in the tile's first row; off0, off1: from there to the lane's rows; groups: from there to
+    // the end of the row; wide: rows begin at multiples of eight bytes
+    __device__ __forceinline__ void load(const uint16_t* base, uint32_t off0, uint32_t off1, int groups, bool wide, int t) {
+        const int mine = kAll ? 0 : t * GS;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint16_t* p = base + (h ? off1 : off0);
-            uint32_t* r = raw[h];
-            if (all && (GS == 1 || wide)) {
-                if constexpr (GS == 1) r[0] = ld_u16(p);
-                if constexpr (GS == 2) r[0] = ld_early4(p);
-                if constexpr (GS == 4) {
-                    const uint2 v = ld_early8(p);
-                    r[0] = v.x;
-                    r[kWords - 1] = v.y;
+            const uint16_t* p = base + (h ? off1 : off0) + mine;
+            if (wide && groups >= 4 * GS) {
+#pragma unroll
+                for (int w = 0; w < kWords; w += 2) {
+                    const uint2 v = ld_early8(p + 2 * w);
+                    raw[h][w] = v.x;
+                    raw[h][w + 1] = v.y;
                 }
             } else {
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
-                    r[w] = 2 * w < groups ? ld_u16(p + 2 * w) : 0;
-                    if (GS > 1 && 2 * w + 1 < groups) r[w] |= ld_u16(p + 2 * w + 1) << 16;
+                    raw[h][w] = mine + 2 * w < groups ? ld_u16(p + 2 * w) : 0;
+                    if (mine + 2 * w + 1 < groups) raw[h][w] |= ld_u16(p + 2 * w + 1) << 16;
                 }
             }
         }
@@ -510,22 +519,23 @@ struct Scales {
     }
     // Scale of group s of step q for the lane's row.
     __device__ __forceinline__ float get(int h, int q, int s, int lane) const {
-        const uint32_t w = __shfl_sync(0xffffffffu, raw[h][s / 2], (lane & ~3) | q);
-        return __uint_as_float(s & 1 ? w & 0xffff0000u : w << 16);
+        const int i = kAll ? q * GS + s : s;
+        const uint32_t w = kAll ? raw[h][i / 2] : __shfl_sync(0xffffffffu, raw[h][i / 2], (lane & ~3) | q);
+        return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
     }
 };
 
 // sum[n] += (tile) * (column tile n), step q of the segment at `slot`.  Without
-// the columns' factors.  (Reads of one word a row meet every bank once, wider
-// ones twice.)
+// the columns' factors.
 template <int GS, int NT, class Columns>
-__device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, const Columns& columns,
+__device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, Columns& columns,
                                             const Scales<GS>& sc, int q, int lane) {
     const int g = lane >> 2, t = lane & 3;
     constexpr int kPer = 4 / GS;  // words of a lane per scale group
     // the lane's first chunk of the step's first group, and its bytes of it; other groups and the box's second step lie at an
     // exclusive or from there
-    const uint32_t base = slot + g * kBox + ((GS == 1 ? t : GS == 2 ? t >> 1 : 0) ^ g) * 16 + (GS == 1 ? 0 : GS == 2 ? (t & 1) * 8 : t * 4);
+    const int row = pair_of_row<GS>(g);
+    const uint32_t base = slot + row * kBox + ((GS == 1 ? t : GS == 2 ? t >> 1 : 0) ^ row) * 16 + (GS == 1 ? 0 : GS == 2 ? (t & 1) * 8 : t * 4);
     constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 #pragma unroll
     for (int s = 0; s < GS; ++s) {
@@ -626,7 +636,7 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
     p.staged = 0;
     if (GS > 0) {
         // at least two slots per warp
-        using View = StagedView<GS ? GS : 1, NT>;
+        using View = StagedView<GS ? GS : 1>;
         const int none = View::bytes(0, p.columns), each = View::bytes(1, p.columns) - none;
         const int most = (kSmemLimit - fixed - 2 * kMvWarps * kSlotBytes - none) / each;
         const int panels = (segments + most - 1) / most;
@@ -666,11 +676,11 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     constexpr int kRed = kMvWarps * NT * 128;  // floats, one buffer
     constexpr int kRedAt = kMvWarps * kMaxSlots * 8, kStagedAt = kRedAt + 2 * kRed * 4;
     float* red = reinterpret_cast<float*>(smem + kRedAt);
-    const StagedView<kGS, NT> staged(smem_addr(smem) + kStagedAt, plan.panel, plan.columns);
+    const StagedView<kGS> staged(smem_addr(smem) + kStagedAt, plan.panel, plan.columns);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     const RowShape& shape = plan.shape;
     const int row_scales = F::scales(K), segments = shape.segments, panel = plan.panel;
-    const bool wide = row_scales % kGS == 0;
+    const bool wide = row_scales % 4 == 0;
     const int ways = 1 << split;
     const int mine = warp >> split;  // tile of a job
     SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
@@ -709,7 +719,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         if (!more) return;
         ring.fill(weights, ct.first, ct.second, ct.pairs, cseg * kSegment, shape.bytes(cseg), lane);
         if constexpr (F::kW4) {
-            const uint32_t off = min(g, ct.pairs - 1) * row_scales;
+            const uint32_t off = min(pair_of_row<GS>(g), ct.pairs - 1) * row_scales;
             Scales<kGS>::prefetch(jobs.scales() + (int64_t)ct.first * row_scales + cseg * 4 * kGS, off,
                                   off + (unsigned)(ct.second - ct.first) * row_scales, t);
         }
@@ -742,14 +752,14 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     auto load_part = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK, K - segment * F::kSegK, q, t); };
     auto load_scales = [&](int segment) {
         const int at = segment * 4 * kGS;
-        next.load(scale + at, off0, off1, row_scales - at - t * kGS, at + 4 * kGS <= row_scales, wide);
+        next.load(scale + at, off0, off1, row_scales - at, wide, t);
     };
     auto begin = [&](const Tile& tile) {
         if (tile.pairs == 0) return;
         const int first = first_from(0, way);
         if constexpr (F::kW4) {
             scale = jobs.scales() + (int64_t)tile.first * row_scales;
-            off0 = (unsigned)min(g, tile.pairs - 1) * row_scales + t * kGS;
+            off0 = (unsigned)min(pair_of_row<GS>(g), tile.pairs - 1) * row_scales;
             off1 = off0 + (unsigned)(tile.second - tile.first) * row_scales;
             load_scales(first);
             columns.set(staged, lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : 0); });
@@ -772,7 +782,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                 w[q] = make_uint2(0, 0);
                 if (k < K) w[q] = ld_early8(from + k);
             }
-            stage_segment<kGS, NT>(staged, s, token, w, lane);
+            stage_segment<kGS>(staged, s, token, w, lane);
         }
         __syncthreads();
     };
@@ -798,7 +808,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                     if constexpr (F::kW4) {
                         const Scales<kGS> now = next;
                         load_scales(after);
-                        const StagedColumns<kGS, NT> here = columns.at(seg - p);
+                        StagedColumns<kGS, NT> here = columns.at(seg - p);
                         float sum[NT][4] = {};
                         if (bytes == kSegment) {
 #pragma unroll
@@ -841,7 +851,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         constexpr int kPairs = 64 * NT;  // (pair, token) per tile
         for (int i = threadIdx.x; i < done.count * kPairs; i += kMvThreads) {
             const int at = i / kPairs, n = i % kPairs / 64, l = i % 64;  // l: two columns of a lane's first row
-            const int pair = l >> 3, token = 8 * n + (l & 7);
+            const int pair = pair_of_row<GS>(l >> 3), token = 8 * n + (l & 7);
             const Tile of = jobs.tile(done, at);
             if (pair >= of.pairs || token >= of.tokens) continue;
             const float* q = r + ((at << split) * NT + n) * 128 + (l >> 1) * 4 + (l & 1);

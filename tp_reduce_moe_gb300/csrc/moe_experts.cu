@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     const int r0 = share.first, r1 = share.last;
     const RowShape& shape = plan.shape;
     const int row_scales = F::scales(a.I), segments = shape.segments;
-    const bool wide = row_scales % kGS == 0;
+    const bool wide = row_scales % 4 == 0;
     const int total = it.count() * segments;
     const int f0 = total * warp / kMvWarps, f1 = total * (warp + 1) / kMvWarps;  // total <= 2^18
     const int item0 = f0 / segments, seg0 = f0 - item0 * segments;
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         const int rows = min(16, r1 - crow);
         ring.fill(weights, cfirst, cfirst + rows / 2, (rows + 1) / 2, cseg * kSegment, shape.bytes(cseg), lane);
         if constexpr (F::kW4) {
-            const uint32_t off = min(g, (rows + 1) / 2 - 1) * row_scales;
+            const uint32_t off = min(pair_of_row<GS>(g), (rows + 1) / 2 - 1) * row_scales;
             Scales<kGS>::prefetch(a.s2 + (int64_t)cfirst * row_scales + cseg * 4 * kGS, off, off + rows / 2 * row_scales, t);
         }
         if (++cf == f1) {
@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         Scales<kGS> next;
         const uint16_t* act = nullptr;
         const uint16_t* scale = nullptr;
-        const uint32_t off0 = (unsigned)min(g, pairs - 1) * row_scales + t * kGS, off1 = off0 + rows / 2 * row_scales;
+        const int pair = pair_of_row<GS>(g);
+        const uint32_t off0 = (unsigned)min(pair, pairs - 1) * row_scales, off1 = off0 + rows / 2 * row_scales;
         auto enter = [&](int item) {
             const int e = (g & 3) < it.n[item] ? g & 3 : 0;
             act = a.act + ((int64_t)it.slot[it.off[item] + e] * 2 + (g >> 2)) * a.I;
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         };
         auto load_scales = [&](int segment) {
             const int at = segment * 4 * kGS;
-            next.load(scale + at, off0, off1, row_scales - at - t * kGS, at + 4 * kGS <= row_scales, wide);
+            next.load(scale + at, off0, off1, row_scales - at, wide, t);
         };
         int item = item0, seg = seg0;
         if (f0 < f1) {
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                     const int column = 2 * t + c;
                     if (t < 2 && column < n) {
                         const float w = it.w[at + column];
-                        float* y = mine + it.token[at + column] * 16 + g;
+                        float* y = mine + it.token[at + column] * 16 + pair;
                         y[0] = fmaf(w, acc[0][c], y[0]);
                         y[8] = fmaf(w, acc[0][c + 2], y[8]);
                     }
