@@ -10,8 +10,10 @@
 // of a token group to arrive chooses, one warp per token.  The choice must not
 // depend on how a sum was split, so the sums carry a second word: bf16
 // products are exact in fp32, and each addition's error is kept (two-sum), which
-// leaves a relative error of about 2^-45 of the sum of magnitudes; scores are
-// then formed and compared in 64 bits.
+// leaves a relative error of about 2^-45 of the sum of magnitudes.  Scores are
+// formed and compared in 32 bits where the gaps between the chosen are wider than
+// what 32 bits can get wrong, else (one token in some thousands) in 64 bits,
+// whose rate on this GPU is 1/64 of that; the weights of the chosen always are.
 #include "moe_common.cuh"
 
 namespace arf {
@@ -33,6 +35,45 @@ __device__ __forceinline__ Sum2 add2(Sum2 s, float hi, float lo) {
     const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(r, b)), __fsub_rn(hi, b));
     return Sum2{r, __fadd_rn(s.lo, __fadd_rn(e, lo))};
 }
+
+// Two such sums side by side, in packed instructions (twice the rate).
+struct Pair {
+    unsigned long long v;
+};
+__device__ __forceinline__ Pair pack(float a, float b) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ float2 unpack(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+    return f;
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair sub(Pair a, Pair b) {  // exact product by -1, one rounding
+    Pair r;
+    const Pair m = pack(-1.0f, -1.0f);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(b.v), "l"(m.v), "l"(a.v));
+    return r;
+}
+struct Sum2x2 {
+    Pair hi, lo;
+    __device__ __forceinline__ void add_product(Pair x, Pair w) {
+        const Pair p = mul(x, w), r = add(hi, p), b = sub(r, hi);
+        lo = add(lo, add(sub(hi, sub(r, b)), sub(p, b)));
+        hi = r;
+    }
+};
 
 // A double as an integer of the same order; NaN below everything.
 __device__ __forceinline__ long long ordered(double v) {
@@ -62,8 +103,172 @@ __device__ __forceinline__ double warp_sum_d(double v) {
     return v;
 }
 
-// One warp: the choice for one token.  Lane l holds experts l, l + 32, ...
-__device__ void choose(const RouteArgs& a, int token, int lane, double* scores /* shared, [E] */,
+// A float as an unsigned integer of the same order, above 0 (NaN aside).
+__device__ __forceinline__ unsigned ordered32(float v) {
+    const unsigned b = __float_as_uint(v + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered32(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+
+// A sigmoid, or a softmax's exponential.
+__device__ __noinline__ double score64(const RouteArgs& a, double z, double top) {
+    const double x = exp(a.sigmoid ? -z : z - top);
+    return a.sigmoid ? 1.0 / (1.0 + x) : x;
+}
+
+// One warp: the weights of the chosen ids (lane k holds the k-th), in 64 bits.
+__device__ __noinline__ void store_choice(const RouteArgs& a, int token, int lane, int id, double score, double sum) {
+    const int slots = a.K + a.shared;
+    if (lane < a.K) {
+        double w = score;
+        if (a.renorm) w = sum > 0.0 || sum != sum ? w / sum : 0.0;
+        a.ids[(int64_t)token * slots + lane] = id;
+        a.weights[(int64_t)token * slots + lane] = (float)(w * (double)a.scale);
+    } else if (lane < slots) {
+        a.ids[(int64_t)token * slots + lane] = a.E + lane - a.K;
+        a.weights[(int64_t)token * slots + lane] = 1.0f;
+    }
+}
+
+// One warp: the choice for one token in 32 bits.  Lane l holds experts l, l +
+// 32, ...  False if some gap that decides is too narrow, or something is not a
+// number: nothing is written then.
+//
+// What the difference of two choice values c = s + b may be off by, relative to
+// |c| + 2 max|b| (no less than either score): a sigmoid's logit is rounded to 32
+// bits, 2^-24 |l| of s; expf and the division are good to 2^-21.4 of it, the sum
+// with b to 2^-24: for |l| <= 8 and two values 2^-19.  A softmax's exponent
+// carries three such roundings and the difference's own, and the sum of the
+// exponentials 2^-19.6: 2^-17.2.  Twice that is taken, and more for larger |l|.
+//
+// Loops, not unrolled code: one SM runs this once, and an instruction that has to
+// be fetched costs it more than the instruction (unrolled over sixteen registers
+// it took 20 us for one token).
+__device__ bool choose32(const RouteArgs& a, int token, int lane, unsigned* keys /* shared, [E] */) {
+    const float2* l = a.logits + (int64_t)token * a.E;
+    const bool by_logit = a.bias == nullptr && a.n_group == 1;
+    float top = -INFINITY, big = 0.0f, bias = 0.0f, total = 0.0f;
+    bool fine = true;
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32) {
+        const float v = __ldcg(l + e).x;
+        fine = fine && fabsf(v) < INFINITY;
+        top = fmaxf(top, v);
+        big = fmaxf(big, fabsf(v));
+        keys[e] = by_logit ? ordered32(v) : __float_as_uint(v);
+    }
+    top = from_ordered32(__reduce_max_sync(0xffffffffu, ordered32(top)));
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    if (!by_logit) {
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) {
+            const float v = __uint_as_float(keys[e]), x = expf(a.sigmoid ? -v : v - top), s = a.sigmoid ? 1.0f / (1.0f + x) : x;
+            total += s;
+            keys[e] = __float_as_uint(s);
+        }
+        const float scale = a.sigmoid ? 1.0f : 1.0f / warp_sum(total);
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) {
+            const float b = a.bias ? __ldg(a.bias + e) : 0.0f;
+            fine = fine && b == b && b < INFINITY;
+            if (fabsf(b) < INFINITY) bias = fmaxf(bias, fabsf(b));
+            keys[e] = ordered32(__uint_as_float(keys[e]) * scale + b);
+        }
+        bias = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bias)));
+    }
+    if (!__all_sync(0xffffffffu, fine)) return false;
+    const float wide = by_logit ? 0x1p-22f : (a.sigmoid ? 0x1p-18f : 0x1p-16f) * fmaxf(1.0f, big * 0.125f);
+    if (a.n_group > 1) {
+        __syncwarp();
+        // a group's two best, group by group
+        const int size = a.E / a.n_group;
+        unsigned mine = 0u, kept = 0u, last = 0u;
+        float reach = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < a.n_group; ++j) {
+            unsigned b0 = 0u, b1 = 0u;
+#pragma unroll 1
+            for (int e = lane; e < size; e += 32) {
+                const unsigned k = keys[j * size + e];
+                b1 = max(b1, min(b0, k));
+                b0 = max(b0, k);
+            }
+            const unsigned first = __reduce_max_sync(0xffffffffu, b0);
+            const int holder = __ffs(__ballot_sync(0xffffffffu, b0 == first)) - 1;
+            const unsigned second = __reduce_max_sync(0xffffffffu, lane == holder ? b1 : b0);
+            const float c0 = from_ordered32(first), c1 = from_ordered32(second);
+            if (lane == j) mine = ordered32(c0 + c1);
+            reach = fmaxf(reach, fabsf(c0) < INFINITY && fabsf(c1) < INFINITY ? fabsf(c0) + fabsf(c1) : 0.0f);
+        }
+#pragma unroll 1
+        for (int r = 0; r <= a.topk_group && r < a.n_group; ++r) {
+            const unsigned best = __reduce_max_sync(0xffffffffu, mine);
+            const int holder = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
+            if (r == a.topk_group) {
+                if (!(from_ordered32(last) - from_ordered32(best) > 2.0f * wide * (reach + 4.0f * bias))) return false;
+                break;
+            }
+            kept |= 1u << holder;
+            last = best;
+            if (lane == holder) mine = 0u;
+        }
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32)
+            if (!(kept >> (e / size) & 1u)) keys[e] = 0u;
+        __syncwarp();
+    }
+    // the top_k largest, and the one behind them
+    unsigned mine = 0u, last = 0u;
+    int at = 0, my_id = 0;
+    bool again = true;  // the lane's best is to be looked for
+#pragma unroll 1
+    for (int k = 0; k <= a.K; ++k) {
+        if (again) {
+            mine = 0u;
+#pragma unroll 1
+            for (int e = lane; e < a.E; e += 32)
+                if (keys[e] > mine) {
+                    mine = keys[e];
+                    at = e;
+                }
+        }
+        __syncwarp();
+        const unsigned best = __reduce_max_sync(0xffffffffu, mine);
+        const int holder = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
+        if (k > 0 && best != 0u) {  // (equal ones are for 64 bits too, lowest index first)
+            const float c0 = from_ordered32(last), c1 = from_ordered32(best);
+            if (!(c0 - c1 > wide * (fabsf(c0) + (by_logit ? 0.0f : 2.0f * bias)))) return false;
+        }
+        if (k == a.K) break;
+        if (best == 0u) return false;
+        const int id = __shfl_sync(0xffffffffu, at, holder);
+        if (lane == k) my_id = id;
+        last = best;
+        again = lane == holder;
+        if (again) keys[at] = 0u;
+    }
+    // weights in 64 bits
+    const float2 v = __ldcg(l + my_id);
+    double score = score64(a, (double)v.x + (double)v.y, (double)top), sum = 0.0;
+    if (lane >= a.K) score = 0.0;
+#pragma unroll 1
+    for (int k = 0; k < a.K; ++k) sum += __shfl_sync(0xffffffffu, score, k);
+    if (!a.sigmoid && !a.renorm) {
+        double all = 0.0;
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) {
+            const float2 u = __ldcg(l + e);
+            all += score64(a, (double)u.x + (double)u.y, (double)top);
+        }
+        score /= warp_sum_d(all);
+    }
+    store_choice(a, token, lane, my_id, score, sum);
+    return true;
+}
+
+// One warp: the choice for one token in 64 bits, for every input.  Lane l holds
+// experts l, l + 32, ...
+__device__ __noinline__ void choose(const RouteArgs& a, int token, int lane, double* scores /* shared, [E] */,
                        long long* keys /* shared, [E] */) {
     constexpr long long kNone = (long long)0x8000000000000000ull;
     const float2* l = a.logits + (int64_t)token * a.E;
@@ -81,7 +286,7 @@ __device__ void choose(const RouteArgs& a, int token, int lane, double* scores /
     for (int e = lane; e < a.E; e += 32) {
         const double z = scores[e];
         if (by_logit) keys[e] = ordered(z);
-        scores[e] = a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - top);
+        scores[e] = score64(a, z, top);
         total += scores[e];
     }
     if (!a.sigmoid) {
@@ -127,7 +332,7 @@ __device__ void choose(const RouteArgs& a, int token, int lane, double* scores /
     int my_id = 0;
     for (int k = 0; k < a.K; ++k) {
         Best b{kNone, 0x7fffffff};
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kPerLane; ++i) {
             const int e = lane + 32 * i;
             if (e < a.E && !(taken >> i & 1)) b = better(b, Best{keys[e], e});
@@ -141,92 +346,114 @@ __device__ void choose(const RouteArgs& a, int token, int lane, double* scores /
             my_score = s;
         }
     }
-    const int slots = a.K + a.shared;
-    if (lane < a.K) {
-        double w = my_score;
-        if (a.renorm) w = sum > 0.0 || sum != sum ? w / sum : 0.0;
-        a.ids[(int64_t)token * slots + lane] = my_id;
-        a.weights[(int64_t)token * slots + lane] = (float)(w * (double)a.scale);
-    } else if (lane < slots) {
-        a.ids[(int64_t)token * slots + lane] = a.E + lane - a.K;
-        a.weights[(int64_t)token * slots + lane] = 1.0f;
-    }
+    store_choice(a, token, lane, my_id, my_score, sum);
 }
 
+// TOKENS per CTA.  One token: four of a thread's chunks of the expert's row at a
+// time, all asked for before the first is used; more: a chunk of all tokens.
+template <int TOKENS>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];  // the choice: [warp][E] scores and keys
-    __shared__ Sum2 part[kRouteWarps][kRouteTokens];
+    __shared__ Sum2 part[kRouteWarps][TOKENS];
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int expert = blockIdx.x, t0 = blockIdx.y * kRouteTokens, nt = min(kRouteTokens, a.T - t0);
+    const int expert = blockIdx.x, t0 = blockIdx.y * TOKENS, nt = min(TOKENS, a.T - t0);
     pdl_trigger();
     pdl_wait();  // no global memory access before this point
 
-    Sum2 acc[kRouteTokens] = {};
+    Sum2x2 sums[TOKENS];
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) sums[j].hi = sums[j].lo = pack(0.0f, 0.0f);
     const uint16_t* w = a.gate + (int64_t)expert * a.H;
-    for (int c = threadIdx.x; c < a.H / 8; c += kRouteThreads) {
-        float f[8];
-        bf16x8_to_f32(ld_early16(w + c * 8), f);
+    const int chunks = a.H / 8;
+    constexpr int kAhead = TOKENS == 1 ? 4 : 1;
+    for (int c0 = threadIdx.x; c0 < chunks; c0 += kAhead * kRouteThreads) {
+        uint4 wv[kAhead], xv[kAhead][TOKENS];
 #pragma unroll
-        for (int j = 0; j < kRouteTokens; ++j)
-            if (j < nt) {
-                float v[8];
-                bf16x8_to_f32(ld_early16(a.x + (int64_t)(t0 + j) * a.H + c * 8), v);
+        for (int u = 0; u < kAhead; ++u) {
+            const int c = c0 + u * kRouteThreads;
+            wv[u] = make_uint4(0, 0, 0, 0);
+            if (c < chunks) wv[u] = ld_early16_stream(w + c * 8);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[j] = add2(acc[j], __fmul_rn(f[i], v[i]), 0.0f);
+            for (int j = 0; j < TOKENS; ++j) {
+                xv[u][j] = make_uint4(0, 0, 0, 0);
+                if (c < chunks && j < nt) xv[u][j] = ld_early16(a.x + (int64_t)(t0 + j) * a.H + c * 8);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            float f[8];
+            bf16x8_to_f32(wv[u], f);
+#pragma unroll
+            for (int j = 0; j < TOKENS; ++j)
+                if (j < nt) {
+                    float v[8];
+                    bf16x8_to_f32(xv[u][j], v);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) sums[j].add_product(pack(v[i], v[i + 1]), pack(f[i], f[i + 1]));
+                }
+        }
     }
 #pragma unroll
-    for (int j = 0; j < kRouteTokens; ++j) {
+    for (int j = 0; j < TOKENS; ++j) {
         if (j >= nt) break;
+        const float2 h = unpack(sums[j].hi), l = unpack(sums[j].lo);
+        Sum2 acc = add2(Sum2{h.x, l.x}, h.y, l.y);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const float hi = __shfl_xor_sync(0xffffffffu, acc[j].hi, o), lo = __shfl_xor_sync(0xffffffffu, acc[j].lo, o);
-            acc[j] = add2(acc[j], hi, lo);
+            const float hi = __shfl_xor_sync(0xffffffffu, acc.hi, o), lo = __shfl_xor_sync(0xffffffffu, acc.lo, o);
+            acc = add2(acc, hi, lo);
         }
-        if (lane == 0) part[warp][j] = acc[j];
+        if (lane == 0) part[warp][j] = acc;
     }
     __syncthreads();
-    if (threadIdx.x < nt) {
-        Sum2 s = part[0][threadIdx.x];
-        for (int u = 1; u < kRouteWarps; ++u) s = add2(s, part[u][threadIdx.x].hi, part[u][threadIdx.x].lo);
-        // an infinite or undefined sum has no meaningful error word
-        if (!isfinite(s.hi)) s.lo = 0.0f;
-        a.logits[(int64_t)(t0 + threadIdx.x) * a.E + expert] = make_float2(s.hi, s.lo);
-        __threadfence();
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        last = atomicAdd(a.count + blockIdx.y, 1u) == (unsigned)a.E - 1;
+    if (threadIdx.x < 32) {  // one warp writes, then arrives for all
+        if (lane < nt) {
+            Sum2 s = part[0][lane];
+#pragma unroll
+            for (int u = 1; u < kRouteWarps; ++u) s = add2(s, part[u][lane].hi, part[u][lane].lo);
+            // the sum rounded, and the rest; an infinite or undefined sum has none
+            const float hi = s.hi + s.lo;
+            a.logits[(int64_t)(t0 + lane) * a.E + expert] =
+                isfinite(hi) ? make_float2(hi, __fsub_rn(s.lo, __fsub_rn(hi, s.hi))) : make_float2(isfinite(s.hi) ? hi : s.hi, 0.0f);
+            __threadfence();
+        }
+        __syncwarp();
+        if (lane == 0) last = atomicAdd(a.count + blockIdx.y, 1u) == (unsigned)a.E - 1;
     }
     __syncthreads();
     if (!last) return;
     __threadfence();
     if (threadIdx.x == 0) a.count[blockIdx.y] = 0;  // for the next call
+    if (warp >= nt) return;
     double* scores = reinterpret_cast<double*>(smem) + warp * 2 * a.E;
-    if (warp < nt) choose(a, t0 + warp, lane, scores, reinterpret_cast<long long*>(scores + a.E));
+    if (!choose32(a, t0 + warp, lane, reinterpret_cast<unsigned*>(scores)))
+        choose(a, t0 + warp, lane, scores, reinterpret_cast<long long*>(scores + a.E));
 }
 
-}  // namespace
-
-cudaError_t moe_route_set_attributes() {
-    return cudaFuncSetAttribute(moe_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteWarps * kMoeMaxExperts * 16);
-}
-
-cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t stream, bool pdl) {
-    const int smem = kRouteWarps * a.E * 16;  // at most 64 KB
+template <int TOKENS>
+cudaError_t launch(const RouteArgs& a, cudaStream_t stream, bool pdl) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)a.E, (unsigned)((a.T + kRouteTokens - 1) / kRouteTokens));
+    cfg.gridDim = dim3((unsigned)a.E, (unsigned)((a.T + TOKENS - 1) / TOKENS));
     cfg.blockDim = dim3(kRouteThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.dynamicSmemBytes = (size_t)TOKENS * a.E * 16;  // at most 64 KB
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, moe_route_kernel, a);
+    return cudaLaunchKernelEx(&cfg, moe_route_kernel<TOKENS>, a);
+}
+
+}  // namespace
+
+cudaError_t moe_route_set_attributes() {
+    return cudaFuncSetAttribute(moe_route_kernel<kRouteTokens>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteTokens * kMoeMaxExperts * 16);
+}
+
+cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t stream, bool pdl) {
+    return a.T <= 2 ? launch<1>(a, stream, pdl) : launch<kRouteTokens>(a, stream, pdl);
 }
 
 }  // namespace arf
