@@ -105,6 +105,9 @@ cudaError_t launch_kernel(const MatvecArgs& a, int num_sms, cudaStream_t stream)
 
 template <int GS>
 cudaError_t launch(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
+#ifdef MV1
+    return launch_kernel<GS, 1>(a, num_sms, stream);
+#endif
     return a.T <= 8 ? launch_kernel<GS, 1>(a, num_sms, stream) : launch_kernel<GS, 2>(a, num_sms, stream);
 }
 

@@ -353,19 +353,14 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
 // the lane holds values 4 * lane .. + 3 in w[q] (zero behind the end of the row).
 template <int GS>
 __device__ __forceinline__ void stage_segment(const StagedView<GS>& v, int segment, int col, const uint2 (&w)[4], int lane) {
-    float big = 0.0f;
-    bool undefined = false;
+    // magnitudes as integers, two to a word: NaN is above everything
+    unsigned big = 0u;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float v0 = fabsf(__uint_as_float(w[q].x << 16)), v1 = fabsf(__uint_as_float(w[q].x & 0xffff0000u));
-        const float v2 = fabsf(__uint_as_float(w[q].y << 16)), v3 = fabsf(__uint_as_float(w[q].y & 0xffff0000u));
-        big = fmaxf(big, fmaxf(fmaxf(v0, v1), fmaxf(v2, v3)));
-        undefined = undefined || v0 != v0 || v1 != v1 || v2 != v2 || v3 != v3;
-    }
-    const unsigned top = __reduce_max_sync(0xffffffffu, undefined || !(big < INFINITY) ? 0x7f800000u : __float_as_uint(big)) >> 23;
-    const bool bad = top == 255;  // an infinite or undefined activation: so is every sum it is in
-    // 2^(up - 127) * 2^(top - 127) = 2^90, as far as bf16 goes
-    const unsigned up = bad ? 127u : min(344u - top, 254u);
+    for (int q = 0; q < 4; ++q) big = __vmaxu2(big, __vmaxu2(w[q].x & 0x7fff7fffu, w[q].y & 0x7fff7fffu));
+    const unsigned top = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16)) >> 7;
+    const bool bad = top > 227;  // infinite, undefined, or 2^101 and more: so is every sum it is in
+    // 2^(up - 127) * 2^(top - 127) = 2^90, as far as bf16 goes and the factor does
+    const unsigned up = bad ? 133u : max(min(344u - top, 254u), 133u);
     const uint32_t one = up << 7 | up << 23, sixteenth = (up - 4) << 7 | (up - 4) << 23;
     const int odd = lane & 1;  // an even lane holds values 0-3 of eight, an odd one 4-7
     const int u = lane >> 1;   // word of eight values: word i of lane t
@@ -373,7 +368,7 @@ __device__ __forceinline__ void stage_segment(const StagedView<GS>& v, int segme
     const int t = u / kPer % 4, i = u / (4 * kPer) * kPer + u % kPer;
     const uint32_t at = v.values + col * v.stride + segment * 1024 + i * 64 + t * 16 + odd * 8;
     const uint32_t extra = v.extras + col * v.extra_stride + segment * v.kExtra;
-    const float minus8 = __uint_as_float(up << 23) * (-8.0f * 0x1p-126f) * 0x1p-7f;
+    const float minus8 = __uint_as_float((up - 130) << 23 | 0x80000000u);  // -8 * 2^(up - 127) * 2^-133
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w[q].x : w[q].y, 1);
@@ -389,7 +384,7 @@ __device__ __forceinline__ void stage_segment(const StagedView<GS>& v, int segme
     }
     if (lane == 0)
         sts_f32(extra + 16 * GS,
-                bad ? __uint_as_float(0x7fc00000u) : 0x1p127f / __uint_as_float(up << 23) * 0x1p6f);
+                __uint_as_float(bad ? 0x7fc00000u : (387 - up) << 23));  // 2^(127 - up) * 2^133
 }
 
 // Where the products take their columns from: words(n, q, s, c, eight) gives the
@@ -587,9 +582,9 @@ __device__ __forceinline__ void add_scaled(float (&acc)[NT][4], const float (&su
 // ----------------------------------------------------------------- products
 // How the sixteen warps of a CTA share tiles: 2^ways of them split a tile's
 // segments, 16 / 2^ways tiles go side by side (the ways take turns at what is
-// left over from one round of tiles to the next).  The least work for the
-// busiest warp; among equals the fewest rounds (each costs a reduction), then the
-// most ways.  cut: rounds may end early once (at an expert's end).
+// left over from one round of tiles to the next).  The least time for the
+// busiest warp, a round's end taking that of half a segment to a whole one.
+//  cut: rounds may end early once (at an expert's end).
 struct Ways {
     int each[5];  // segments of the busiest way, for 2^i ways
     __host__ static Ways of(int segments) {
@@ -598,11 +593,14 @@ struct Ways {
         return w;
     }
     __device__ __forceinline__ int pick(int tiles, bool cut) const {
+#ifdef FS
+        return FS;
+#endif
         int best = 4, cost = 0x7fffffff;
 #pragma unroll
         for (int i = 4; i >= 0; --i) {
             const int side = 16 >> i, rounds = (min(tiles, 1 << 14) + (cut ? side - 1 : 0) + side - 1) >> (4 - i);
-            const int c = each[i] * rounds * 64 + min(rounds, 63);
+            const int c = rounds * (2 * each[i] + 1);
             if (c < cost) {
                 cost = c;
                 best = i;
@@ -618,9 +616,8 @@ constexpr int kSmemLimit = 227 * 1024;
 struct ProductPlan {
     RowShape shape;
     Ways ways;
-    int panel;    // segments whose activations are staged at a time
-    int columns;  // staged columns
-    int staged;   // bytes
+    uint8_t panel[17];  // segments whose activations are staged at a time, by the number of staged tokens
+    int staged;         // bytes
     int extra;    // bytes, at extra_at
     int slots;    // per warp
     int extra_at, ring_at, smem;
@@ -631,19 +628,20 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
     p.shape = RowShape::of(Fmt<GS>::row_bytes(K));
     const int segments = p.shape.segments, fixed = kMvWarps * kMaxSlots * 8 + 2 * kMvWarps * NT * 512 + extra;
     p.extra = extra;
-    p.columns = tokens < 8 * NT ? tokens : 8 * NT;
-    p.panel = segments;
     p.staged = 0;
-    if (GS > 0) {
+    for (int n = 0; n <= 16; ++n) {
+        p.panel[n] = (uint8_t)segments;  // at most 128
+        if (GS == 0 || n == 0 || n > tokens || n > 8 * NT) continue;
         // at least two slots per warp
         using View = StagedView<GS ? GS : 1>;
-        const int none = View::bytes(0, p.columns), each = View::bytes(1, p.columns) - none;
-        const int most = (kSmemLimit - fixed - 2 * kMvWarps * kSlotBytes - none) / each;
+        const int none = View::bytes(0, n), each = View::bytes(1, n) - none;
+        const int most = (kSmemLimit - fixed - kMaxSlots * kMvWarps * kSlotBytes - 1024 - none) / each;
         const int panels = (segments + most - 1) / most;
-        p.panel = (segments + panels - 1) / panels;
-        p.staged = (View::bytes(p.panel, p.columns) + 15) / 16 * 16;
+        p.panel[n] = (uint8_t)((segments + panels - 1) / panels);
+        const int bytes = (View::bytes(p.panel[n], n) + 15) / 16 * 16;
+        p.staged = bytes > p.staged ? bytes : p.staged;
     }
-    p.ways = Ways::of(p.panel);
+    p.ways = Ways::of(segments);
     p.extra_at = fixed - extra + p.staged;
     p.ring_at = (p.extra_at + extra + 1023) / 1024 * 1024;
     const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlotBytes);
@@ -676,18 +674,18 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     constexpr int kRed = kMvWarps * NT * 128;  // floats, one buffer
     constexpr int kRedAt = kMvWarps * kMaxSlots * 8, kStagedAt = kRedAt + 2 * kRed * 4;
     float* red = reinterpret_cast<float*>(smem + kRedAt);
-    const StagedView<kGS> staged(smem_addr(smem) + kStagedAt, plan.panel, plan.columns);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     const RowShape& shape = plan.shape;
-    const int row_scales = F::scales(K), segments = shape.segments, panel = plan.panel;
+    const int row_scales = F::scales(K), segments = shape.segments;
     const bool wide = row_scales % 4 == 0;
     const int ways = 1 << split;
     const int mine = warp >> split;  // tile of a job
     SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
 
-    auto to = [&](int p) { return min(p + panel, segments); };
+    auto panel_of = [&](const Job& j) { return uniform(F::kW4 ? (int)plan.panel[jobs.staged(j)] : segments); };
+    auto to = [&](int p, int panel) { return min(p + panel, segments); };
     // The warp's segments of a panel: p + way, p + way + ways, .., with way turning by the panel's length from panel to panel.
-    auto turn = [&](int way, int p) { return (way - (to(p) - p)) & (ways - 1); };
+    auto turn = [&](int way, int p, int panel) { return (way - (to(p, panel) - p)) & (ways - 1); };
 
     // Copies: the next (job, panel, segment).
     Job cj;
@@ -702,17 +700,20 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         return t;
     };
     Tile ct = tile_of(cj);
-    int cpanel = 0, cway = warp & (ways - 1), cseg = cway;
+    int cp = 0, cpanel = panel_of(cj), cway = warp & (ways - 1), cseg = cway;
     auto settle = [&]() {  // to the first segment from here on
-        while (more && (ct.pairs == 0 || cseg >= to(cpanel))) {
-            cway = turn(cway, cpanel);
-            cpanel += panel;
-            if (cpanel >= segments) {
-                cpanel = 0;
+        while (more && (ct.pairs == 0 || cseg >= to(cp, cpanel))) {
+            cway = turn(cway, cp, cpanel);
+            cp += cpanel;
+            if (cp >= segments) {
+                cp = 0;
                 more = jobs.next(cj);
-                if (more) ct = tile_of(cj);
+                if (more) {
+                    ct = tile_of(cj);
+                    cpanel = panel_of(cj);
+                }
             }
-            cseg = cpanel + cway;
+            cseg = cp + cway;
         }
     };
     auto fill = [&]() {
@@ -724,7 +725,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                                   off + (unsigned)(ct.second - ct.first) * row_scales, t);
         }
         cseg += ways;
-        if (cseg >= to(cpanel)) settle();
+        if (cseg >= to(cp, cpanel)) settle();
     };
     settle();
     for (int s = 0; s < plan.slots; ++s) {
@@ -742,9 +743,9 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     uint32_t off0 = 0, off1 = 0;
     int way = warp & (ways - 1);  // in the panel at hand
     // The warp's first segment of the panels from p on, with way w in the first; `segments` or more: none.
-    auto first_from = [&](int p, int w) {
-        while (p < segments && p + w >= to(p)) {
-            w = turn(w, p);
+    auto first_from = [&](int p, int w, int panel) {
+        while (p < segments && p + w >= to(p, panel)) {
+            w = turn(w, p, panel);
             p += panel;
         }
         return p < segments ? p + w : segments;
@@ -754,42 +755,56 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         const int at = segment * 4 * kGS;
         next.load(scale + at, off0, off1, row_scales - at, wide, t);
     };
-    auto begin = [&](const Tile& tile) {
+    auto view = [&](const Job& j, int panel) { return StagedView<kGS>(smem_addr(smem) + kStagedAt, panel, jobs.staged(j)); };
+    auto begin = [&](const Job& j, const Tile& tile, int panel) {
         if (tile.pairs == 0) return;
-        const int first = first_from(0, way);
+        const int first = first_from(0, way, panel);
         if constexpr (F::kW4) {
             scale = jobs.scales() + (int64_t)tile.first * row_scales;
             off0 = (unsigned)min(pair_of_row<GS>(g), tile.pairs - 1) * row_scales;
             off1 = off0 + (unsigned)(tile.second - tile.first) * row_scales;
             load_scales(first);
-            columns.set(staged, lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : 0); });
+            columns.set(view(j, panel), lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : 0); });
         } else {
             x = jobs.x(tile, g < tile.tokens ? g : 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) load_part(first, q);
         }
     };
-    auto stage = [&](const Job& j, int p) {
-        const int tokens = jobs.staged(j), units = (to(p) - p) * tokens;  // (segment, token)
-        __syncthreads();                                                 // the panel before it is done with
-        for (int i = warp; i < units; i += kMvWarps) {
-            const int s = i / tokens, token = i - s * tokens;
-            const uint16_t* from = jobs.staged_x(j, token);
-            uint2 w[4];
+    auto stage = [&](const Job& j, int p, int panel) {
+        const int tokens = jobs.staged(j), units = (to(p, panel) - p) * tokens;  // (segment, token)
+        const StagedView<kGS> staged = view(j, panel);
+        __syncthreads();  // the panel before it is done with
+        // four at a time, asked for together: beside the weights' copies an answer takes more than a microsecond
+        constexpr int kAhead = 4;
+#pragma unroll 1
+        for (int i0 = warp; i0 < units; i0 += kAhead * kMvWarps) {
+            uint2 w[kAhead][4];
+            int s[kAhead], token[kAhead];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int k = (p + s) * F::kSegK + q * F::kStepK + lane * 4;
-                w[q] = make_uint2(0, 0);
-                if (k < K) w[q] = ld_early8(from + k);
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = min(i0 + u * kMvWarps, units - 1);
+                s[u] = i / tokens;
+                token[u] = i - s[u] * tokens;
+                const uint16_t* from = jobs.staged_x(j, token[u]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int k = (p + s[u]) * F::kSegK + q * F::kStepK + lane * 4;
+                    w[u][q] = make_uint2(0, 0);
+                    if (k < K && i0 + u * kMvWarps < units) w[u][q] = ld_early8(from + k);
+                }
             }
-            stage_segment<kGS>(staged, s, token, w, lane);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (i0 + u * kMvWarps < units) stage_segment<kGS>(staged, s[u], token[u], w[u], lane);
         }
         __syncthreads();
     };
     Job job;
     jobs.first(job);
     Tile tile = tile_of(job);
-    begin(tile);
+    int panel = panel_of(job);
+    begin(job, tile, panel);
     int key = -1;
     for (int buf = 0;; buf ^= 1) {
         float acc[NT][4] = {};
@@ -797,11 +812,11 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         for (int p = 0; p < segments; p += panel) {
             if (F::kW4 && (panel < segments || jobs.staged_key(job) != key)) {
                 key = jobs.staged_key(job);
-                stage(job, p);
+                stage(job, p, panel);
             }
-            const int end = to(p), then = turn(way, p);
+            const int end = to(p, panel), then = turn(way, p, panel);
             if (tile.pairs > 0) {
-                const int behind = first_from(p + panel, then);
+                const int behind = first_from(p + panel, then, panel);
                 for (int seg = p + way; seg < end; seg += ways) {
                     const int after = seg + ways < end ? seg + ways : behind, bytes = shape.bytes(seg);
                     ring.wait();
@@ -834,7 +849,8 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         const bool end = !jobs.next(job);
         if (!end) {
             tile = tile_of(job);
-            begin(tile);
+            panel = panel_of(job);
+            begin(job, tile, panel);
         }
         if (!ring.alive) {
             jobs.lost();
