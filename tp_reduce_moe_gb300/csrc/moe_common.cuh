@@ -217,9 +217,10 @@ struct SlotRing {
     uint32_t phase;
     bool alive;  // no wait has run out
 
-    __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int lane)
+    // arrivals: of a slot's barrier, for each filling
+    __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int arrivals, int lane)
         : slots(slots), bars(bars), slot(slots), bar(bars), n(n), phase(0), alive(true) {
-        if (lane < n) mbar_init(bars + lane * 8, 1);
+        if (lane < n) mbar_init(bars + lane * 8, arrivals);
         fence_mbar_init();
         __syncwarp();
     }
@@ -228,7 +229,7 @@ struct SlotRing {
     __device__ __forceinline__ void fill(const Weights& w, int first, int second, int pairs, int x, int bytes, int lane) {
         if (lane != 0) return;
         const bool wide = bytes > kBox;
-        if (pairs == 8) {
+        if (pairs > 4) {  // (a copy takes as long to issue for one row as for eight; rows that are not the tile's are not used)
             mbar_arrive_expect_tx(bar, wide ? 4 * kBoxBytes : 2 * kBoxBytes);
             copy_box(slot, w.eight, x, first, bar);
             copy_box(slot + kHalfBytes, w.eight, x, second, bar);
@@ -476,56 +477,69 @@ struct DirectColumns {
 };
 
 // ------------------------------------------------------------------- scales
-// bf16 group scales of a segment's rows, one segment ahead in registers: a lane
-// holds those of its two rows, all (up to two groups a step) or those of step t
-// (four groups; the others come from its neighbours).
+// bf16 group scales of a segment's sixteen rows lie beside the slot, 8 * GS
+// bytes each, first rows then second rows, and come with it: a load that is
+// waited for comes back behind all the copies in flight, which takes two to three
+// microseconds, more than a segment's products.  Each lane copies half a row's
+// in pieces of `piece` bytes, asynchronously, and arrives at the slot's barrier;
+// rows of an odd number of scales are copied by loads and stores.
 template <int GS>
 struct Scales {
-    static constexpr bool kAll = GS < 4;
-    static constexpr int kGroups = kAll ? 4 * GS : GS;  // scales of a row in a lane
-    static constexpr int kWords = kGroups / 2;
+    static constexpr int kSlot = 128 * GS;  // bytes beside a slot
+    static constexpr int kHalf = 4 * GS;    // a lane's
+    static constexpr int kWords = GS == 1 ? 2 : GS == 2 ? 4 : 2;
     uint32_t raw[2][kWords];
-    // base: the segment's first scale in the tile's first row; off0, off1: from there to the lane's rows; groups: from there to
-    // the end of the row; wide: rows begin at multiples of eight bytes
-    __device__ __forceinline__ void load(const uint16_t* base, uint32_t off0, uint32_t off1, int groups, bool wide, int t) {
-        const int mine = kAll ? 0 : t * GS;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint16_t* p = base + (h ? off1 : off0) + mine;
-            if (wide && groups >= 4 * GS) {
-#pragma unroll
-                for (int w = 0; w < kWords; w += 2) {
-                    const uint2 v = ld_early8(p + 2 * w);
-                    raw[h][w] = v.x;
-                    raw[h][w + 1] = v.y;
-                }
-            } else {
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) {
-                    raw[h][w] = mine + 2 * w < groups ? ld_u16(p + 2 * w) : 0;
-                    if (mine + 2 * w + 1 < groups) raw[h][w] |= ld_u16(p + 2 * w + 1) << 16;
-                }
+    __host__ static int piece(int row_scales) { return row_scales * 2 % kHalf == 0 ? kHalf : row_scales % 2 == 0 ? 4 : 2; }
+    // base: the tile's first row's scales; second: rows from there to the first of the second ones; column: the segment's first
+    __device__ static __forceinline__ void fill(uint32_t to, uint32_t bar, const uint16_t* base, int second, int pairs, int column,
+                                                int row_scales, int piece, int lane) {
+        const int row = lane & 15, mine = column + (lane >> 4) * (kHalf / 2);
+        const int left = (row_scales - mine) * 2;  // bytes; none or less: zeros
+        const uint16_t* from = base + (uint32_t)((row >= 8 ? second : 0) + min(row & 7, pairs - 1)) * row_scales;
+        const uint32_t at = to + row * (2 * kHalf) + (lane >> 4) * kHalf;
+        if (piece == kHalf) {
+            if constexpr (GS == 4)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(left > 0 ? from + mine : from), "r"(left > 0 ? 16 : 0) : "memory");
+            else if constexpr (GS == 2)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at), "l"(left > 0 ? from + mine : from), "r"(left > 0 ? 8 : 0) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(left > 0 ? from + mine : from), "r"(left > 0 ? 4 : 0) : "memory");
+        } else if (piece == 4) {
+#pragma unroll 1
+            for (int o = 0; o < kHalf; o += 4)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + o), "l"(left > o ? from + mine + o / 2 : from), "r"(left > o ? 4 : 0) : "memory");
+        } else {
+#pragma unroll 1
+            for (int o = 0; o < kHalf; o += 2) {
+                const uint32_t v = left > o ? ld_u16(from + mine + o / 2) : 0;
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + o), "h"((uint16_t)v) : "memory");
             }
+            mbar_arrive(bar);
+            return;
         }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
     }
-    // Brings a later segment's into L2.
-    __device__ static __forceinline__ void prefetch(const uint16_t* base, uint32_t off0, uint32_t off1, int t) {
-        if (t < 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(base + (t ? off1 : off0)));
+    // The lane's two rows, at `at`: of step q.
+    __device__ __forceinline__ void read(uint32_t at, int q) {
+        if (GS < 4 && q > 0) return;  // all at once
+#pragma unroll
+        for (int h = 0; h < 2; ++h) lds(raw[h], at + h * 8 * (2 * kHalf) + (GS == 4 ? q * 8 : 0));
     }
     // Scale of group s of step q for the lane's row.
-    __device__ __forceinline__ float get(int h, int q, int s, int lane) const {
-        const int i = kAll ? q * GS + s : s;
-        const uint32_t w = kAll ? raw[h][i / 2] : __shfl_sync(0xffffffffu, raw[h][i / 2], (lane & ~3) | q);
+    __device__ __forceinline__ float get(int h, int q, int s) const {
+        const int i = GS < 4 ? q * GS + s : s;
+        const uint32_t w = raw[h][i / 2];
         return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
     }
 };
 
-// sum[n] += (tile) * (column tile n), step q of the segment at `slot`.  Without
-// the columns' factors.
+// sum[n] += (tile) * (column tile n), step q of the segment at `slot`, its scales
+// at `scales`.  Without the columns' factors.  In order: q.
 template <int GS, int NT, class Columns>
-__device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, Columns& columns,
-                                            const Scales<GS>& sc, int q, int lane) {
+__device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, uint32_t scales, Columns& columns, Scales<GS>& sc, int q,
+                                            int lane) {
     const int g = lane >> 2, t = lane & 3;
+    sc.read(scales + pair_of_row<GS>(g) * (2 * sc.kHalf), q);
     constexpr int kPer = 4 / GS;  // words of a lane per scale group
     // the lane's first chunk of the step's first group, and its bytes of it; other groups and the box's second step lie at an
     // exclusive or from there
@@ -562,7 +576,7 @@ __device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, 
                 }
             }
         }
-        const float sl = sc.get(0, q, s, lane), sh = sc.get(1, q, s, lane);
+        const float sl = sc.get(0, q, s), sh = sc.get(1, q, s);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -620,13 +634,16 @@ struct ProductPlan {
     int staged;         // bytes
     int extra;    // bytes, at extra_at
     int slots;    // per warp
-    int extra_at, ring_at, smem;
+    int extra_at, ring_at, scales_at, smem;
+    int piece;  // of the scales' copies
 };
 template <int GS, int NT>
 inline ProductPlan plan_product(int K, int tokens, int extra) {
     ProductPlan p;
     p.shape = RowShape::of(Fmt<GS>::row_bytes(K));
     const int segments = p.shape.segments, fixed = kMvWarps * kMaxSlots * 8 + 2 * kMvWarps * NT * 512 + extra;
+    constexpr int kScales = GS ? Scales<GS ? GS : 1>::kSlot : 0, kSlot = kSlotBytes + kScales;
+    p.piece = GS ? Scales<GS ? GS : 1>::piece(Fmt<GS>::scales(K)) : 0;
     p.extra = extra;
     p.staged = 0;
     for (int n = 0; n <= 16; ++n) {
@@ -635,7 +652,7 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
         // at least two slots per warp
         using View = StagedView<GS ? GS : 1>;
         const int none = View::bytes(0, n), each = View::bytes(1, n) - none;
-        const int most = (kSmemLimit - fixed - kMaxSlots * kMvWarps * kSlotBytes - 1024 - none) / each;
+        const int most = (kSmemLimit - fixed - kMaxSlots * kMvWarps * kSlot - 1024 - none) / each;
         const int panels = (segments + most - 1) / most;
         p.panel[n] = (uint8_t)((segments + panels - 1) / panels);
         const int bytes = (View::bytes(p.panel[n], n) + 15) / 16 * 16;
@@ -644,9 +661,10 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
     p.ways = Ways::of(segments);
     p.extra_at = fixed - extra + p.staged;
     p.ring_at = (p.extra_at + extra + 1023) / 1024 * 1024;
-    const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlotBytes);
+    const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlot);
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
-    p.smem = p.ring_at + p.slots * kMvWarps * kSlotBytes;
+    p.scales_at = p.ring_at + p.slots * kMvWarps * kSlotBytes;
+    p.smem = p.scales_at + p.slots * kMvWarps * kScales;
     return p;
 }
 
@@ -677,10 +695,11 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     const RowShape& shape = plan.shape;
     const int row_scales = F::scales(K), segments = shape.segments;
-    const bool wide = row_scales % 4 == 0;
     const int ways = 1 << split;
     const int mine = warp >> split;  // tile of a job
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, F::kW4 ? 33 : 1, lane);
+    const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
+    auto scales_slot = [&]() { return ring_scales + (ring.slot - ring.slots) / (kSlotBytes / Scales<kGS>::kSlot); };
 
     auto panel_of = [&](const Job& j) { return uniform(F::kW4 ? (int)plan.panel[jobs.staged(j)] : segments); };
     auto to = [&](int p, int panel) { return min(p + panel, segments); };
@@ -719,28 +738,25 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     auto fill = [&]() {
         if (!more) return;
         ring.fill(weights, ct.first, ct.second, ct.pairs, cseg * kSegment, shape.bytes(cseg), lane);
-        if constexpr (F::kW4) {
-            const uint32_t off = min(pair_of_row<GS>(g), ct.pairs - 1) * row_scales;
-            Scales<kGS>::prefetch(jobs.scales() + (int64_t)ct.first * row_scales + cseg * 4 * kGS, off,
-                                  off + (unsigned)(ct.second - ct.first) * row_scales, t);
-        }
+        if constexpr (F::kW4)
+            Scales<kGS>::fill(scales_slot(), ring.bar, jobs.scales() + (int64_t)ct.first * row_scales, ct.second - ct.first, ct.pairs,
+                              cseg * 4 * kGS, row_scales, plan.piece, lane);
         cseg += ways;
         if (cseg >= to(cp, cpanel)) settle();
     };
     settle();
-    for (int s = 0; s < plan.slots; ++s) {
-        fill();
-        ring.next();
-    }
-    ring.phase = 0;
+    auto fill_all = [&]() {
+        for (int s = 0; s < plan.slots; ++s) {
+            fill();
+            ring.next();
+        }
+        ring.phase = 0;
+    };
 
-    // Operands of the next segment, asked for one segment ahead, across panels and jobs.
+    // The columns, with bf16 weights asked for one segment ahead, across panels and jobs.
     uint4 col[4];
-    Scales<kGS> next;
     StagedColumns<kGS, NT> columns;
     const uint16_t* x = nullptr;
-    const uint16_t* scale = nullptr;
-    uint32_t off0 = 0, off1 = 0;
     int way = warp & (ways - 1);  // in the panel at hand
     // The warp's first segment of the panels from p on, with way w in the first; `segments` or more: none.
     auto first_from = [&](int p, int w, int panel) {
@@ -751,34 +767,26 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         return p < segments ? p + w : segments;
     };
     auto load_part = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK, K - segment * F::kSegK, q, t); };
-    auto load_scales = [&](int segment) {
-        const int at = segment * 4 * kGS;
-        next.load(scale + at, off0, off1, row_scales - at, wide, t);
-    };
     auto view = [&](const Job& j, int panel) { return StagedView<kGS>(smem_addr(smem) + kStagedAt, panel, jobs.staged(j)); };
     auto begin = [&](const Job& j, const Tile& tile, int panel) {
         if (tile.pairs == 0) return;
-        const int first = first_from(0, way, panel);
         if constexpr (F::kW4) {
-            scale = jobs.scales() + (int64_t)tile.first * row_scales;
-            off0 = (unsigned)min(pair_of_row<GS>(g), tile.pairs - 1) * row_scales;
-            off1 = off0 + (unsigned)(tile.second - tile.first) * row_scales;
-            load_scales(first);
             columns.set(view(j, panel), lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : 0); });
         } else {
+            const int first = first_from(0, way, panel);
             x = jobs.x(tile, g < tile.tokens ? g : 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) load_part(first, q);
         }
     };
-    auto stage = [&](const Job& j, int p, int panel) {
+    auto stage = [&](const Job& j, int p, int panel, bool start) {
         const int tokens = jobs.staged(j), units = (to(p, panel) - p) * tokens;  // (segment, token)
         const StagedView<kGS> staged = view(j, panel);
-        __syncthreads();  // the panel before it is done with
-        // four at a time, asked for together: beside the weights' copies an answer takes more than a microsecond
+        if (!start) __syncthreads();  // the panel before it is done with
+        // four at a time, asked for together (and, at the start, before the first copies: an answer comes back behind them)
         constexpr int kAhead = 4;
 #pragma unroll 1
-        for (int i0 = warp; i0 < units; i0 += kAhead * kMvWarps) {
+        for (int i0 = warp; i0 < units || (start && i0 == warp); i0 += kAhead * kMvWarps) {
             uint2 w[kAhead][4];
             int s[kAhead], token[kAhead];
 #pragma unroll
@@ -794,6 +802,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                     if (k < K && i0 + u * kMvWarps < units) w[u][q] = ld_early8(from + k);
                 }
             }
+            if (start && i0 == warp) fill_all();
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
                 if (i0 + u * kMvWarps < units) stage_segment<kGS>(staged, s[u], token[u], w[u], lane);
@@ -805,15 +814,21 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     Tile tile = tile_of(job);
     int panel = panel_of(job);
     begin(job, tile, panel);
-    int key = -1;
+    if constexpr (F::kW4)
+        stage(job, 0, panel, true);
+    else
+        fill_all();
+    int key = F::kW4 ? jobs.staged_key(job) : 0;
+    bool staged = true;  // what comes next
     for (int buf = 0;; buf ^= 1) {
         float acc[NT][4] = {};
         const int order = way;  // of this warp's parts among the job's
         for (int p = 0; p < segments; p += panel) {
-            if (F::kW4 && (panel < segments || jobs.staged_key(job) != key)) {
+            if (F::kW4 && !staged && (panel < segments || jobs.staged_key(job) != key)) {
                 key = jobs.staged_key(job);
-                stage(job, p, panel);
+                stage(job, p, panel, false);
             }
+            staged = false;
             const int end = to(p, panel), then = turn(way, p, panel);
             if (tile.pairs > 0) {
                 const int behind = first_from(p + panel, then, panel);
@@ -821,17 +836,17 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                     const int after = seg + ways < end ? seg + ways : behind, bytes = shape.bytes(seg);
                     ring.wait();
                     if constexpr (F::kW4) {
-                        const Scales<kGS> now = next;
-                        load_scales(after);
+                        Scales<kGS> now;
+                        const uint32_t scales = scales_slot();
                         StagedColumns<kGS, NT> here = columns.at(seg - p);
                         float sum[NT][4] = {};
                         if (bytes == kSegment) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) multiply_w4<kGS, NT>(sum, ring.slot, here, now, q, lane);
+                            for (int q = 0; q < 4; ++q) multiply_w4<kGS, NT>(sum, ring.slot, scales, here, now, q, lane);
                         } else {
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                if (q * 64 < bytes) multiply_w4<kGS, NT>(sum, ring.slot, here, now, q, lane);
+                                if (q * 64 < bytes) multiply_w4<kGS, NT>(sum, ring.slot, scales, here, now, q, lane);
                         }
                         add_scaled(acc, sum, here);
                     } else {

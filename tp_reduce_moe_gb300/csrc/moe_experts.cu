@@ -225,9 +225,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
     pdl_wait();     // no global memory access before this point
     pdl_trigger();  // after it: what the second kernel reads before its own wait is complete
     build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk1);
-    // Shares of whole tiles where a CTA has at least eight (then at most one in nine is idle at the end), else of pairs.
+    // Shares of whole tiles where there is one for every CTA, else of pairs: cutting tiles to deal 13.5 pairs to each CTA instead
+    // of one or two tiles took 23.7 us instead of 18.5 for one token and 8 experts of 2 x 256 x 7168.
     const int pairs = it.count() * a.I;  // at most 2^24
-    const bool tiles = pairs >= 64 * (int)gridDim.x;
+    const bool tiles = pairs >= 8 * (int)gridDim.x;
     const Share share(tiles ? pairs >> 3 : pairs);
     GateUp<GS> jobs{a, it, share.first << (tiles ? 3 : 0), share.last << (tiles ? 3 : 0), a.I >> 3, 0, GS == 0 || a.T <= kChunk1};
     const int split = plan.ways.pick(((jobs.q1 + 7) >> 3) - (jobs.q0 >> 3), !jobs.together);
@@ -242,18 +243,22 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
 // the sixteen sums are added in warp order.
 struct DownPlan {
     RowShape shape;
-    int buffers, items_at, ring_at, slots, smem;
+    int buffers, items_at, ring_at, scales_at, slots, smem, piece;
 };
-DownPlan plan_down(int T, int K, int E, int row_bytes) {
+template <int GS>
+DownPlan plan_down(int T, int K, int E, int I) {
     DownPlan p;
-    p.shape = RowShape::of(row_bytes);
+    constexpr int kScales = GS ? Scales<GS ? GS : 1>::kSlot : 0;
+    p.shape = RowShape::of(Fmt<GS>::row_bytes(I));
+    p.piece = GS ? Scales<GS ? GS : 1>::piece(Fmt<GS>::scales(I)) : 0;
     // two buffers of sums, so that a tile's may be added while the next tile's are made, where that leaves room for two slots
     p.buffers = T <= 24 ? 2 : 1;
     p.items_at = kMvWarps * kMaxSlots * 8 + p.buffers * kMvWarps * T * 64;
     p.ring_at = (p.items_at + Items::bytes(T * K, E) + 1023) / 1024 * 1024;
-    const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlotBytes);
+    const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * (kSlotBytes + kScales));
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
-    p.smem = p.ring_at + p.slots * kMvWarps * kSlotBytes;
+    p.scales_at = p.ring_at + p.slots * kMvWarps * kSlotBytes;
+    p.smem = p.scales_at + p.slots * kMvWarps * kScales;
     return p;
 }
 
@@ -276,11 +281,12 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     const int r0 = share.first, r1 = share.last;
     const RowShape& shape = plan.shape;
     const int row_scales = F::scales(a.I), segments = shape.segments;
-    const bool wide = row_scales % 4 == 0;
     const int total = it.count() * segments;
     const int f0 = total * warp / kMvWarps, f1 = total * (warp + 1) / kMvWarps;  // total <= 2^18
     const int item0 = f0 / segments, seg0 = f0 - item0 * segments;
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, lane);
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, F::kW4 ? 33 : 1, lane);
+    const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
+    auto scales_slot = [&]() { return ring_scales + (ring.slot - ring.slots) / (kSlotBytes / Scales<kGS>::kSlot); };
 
     // Copies: the next (tile, item, segment).
     int crow = r0, cf = f0, citem = item0, cseg = seg0;
@@ -291,10 +297,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         if (!more) return;
         const int rows = min(16, r1 - crow);
         ring.fill(weights, cfirst, cfirst + rows / 2, (rows + 1) / 2, cseg * kSegment, shape.bytes(cseg), lane);
-        if constexpr (F::kW4) {
-            const uint32_t off = min(pair_of_row<GS>(g), (rows + 1) / 2 - 1) * row_scales;
-            Scales<kGS>::prefetch(a.s2 + (int64_t)cfirst * row_scales + cseg * 4 * kGS, off, off + rows / 2 * row_scales, t);
-        }
+        if constexpr (F::kW4)
+            Scales<kGS>::fill(scales_slot(), ring.bar, a.s2 + (int64_t)cfirst * row_scales, rows / 2, (rows + 1) / 2, cseg * 4 * kGS, row_scales,
+                              plan.piece, lane);
         if (++cf == f1) {
             cf = f0;
             citem = item0;
@@ -326,17 +331,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         // the next segment's operands
         uint4 col[4];
         DirectColumns<kGS> direct[2];  // a box's two steps
-        Scales<kGS> next;
         const uint16_t* act = nullptr;
-        const uint16_t* scale = nullptr;
         const int pair = pair_of_row<GS>(g);
-        const uint32_t off0 = (unsigned)min(pair, pairs - 1) * row_scales, off1 = off0 + rows / 2 * row_scales;
         auto enter = [&](int item) {
             const int e = (g & 3) < it.n[item] ? g & 3 : 0;
             act = a.act + ((int64_t)it.slot[it.off[item] + e] * 2 + (g >> 2)) * a.I;
-            if constexpr (F::kW4) {
-                scale = a.s2 + ((int64_t)uniform(it.expert[item]) * a.H + row) * row_scales;
-            }
         };
         auto load_part = [&](int segment, int q) {  // a step (4-bit) or a quarter of the lane's values
             const int at = segment * F::kSegK;
@@ -345,15 +344,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             else
                 col[q] = load_column<true>(act + at, a.I - at, q, t);
         };
-        auto load_scales = [&](int segment) {
-            const int at = segment * 4 * kGS;
-            next.load(scale + at, off0, off1, row_scales - at, wide, t);
-        };
         int item = item0, seg = seg0;
         if (f0 < f1) {
             enter(item);
             if constexpr (F::kW4) {
-                load_scales(seg);
                 load_part(seg, 0);
                 load_part(seg, 1);
             } else {
@@ -367,19 +361,17 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             const int after = last ? 0 : seg + 1, bytes = shape.bytes(seg);
             ring.wait();
             if constexpr (F::kW4) {
-                const Scales<kGS> now = next;
+                Scales<kGS> now;
+                const uint32_t scales = scales_slot();
                 // boxes of two steps; of what is behind the end of the rows codes and activations are zero
 #pragma unroll
                 for (int box = 0; box < 2; ++box)
                     if (box * kBox < bytes) {
                         const bool end = box == 1 || bytes <= kBox;
-                        if (end && !final) {
-                            if (last) enter(item + 1);
-                            load_scales(after);
-                        }
+                        if (end && !final && last) enter(item + 1);
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            multiply_w4<kGS, 1>(acc, ring.slot, direct[q], now, 2 * box + q, lane);
+                            multiply_w4<kGS, 1>(acc, ring.slot, scales, direct[q], now, 2 * box + q, lane);
                             if (!end)
                                 load_part(seg, 2 + q);
                             else if (!final)
@@ -462,7 +454,7 @@ cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, 
     if (e != cudaSuccess) return e;
     e = launch(moe_gate_up_kernel<GS>, a, w13, plan_product<GS, 1>(a.H, tokens, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
     if (e != cudaSuccess) return e;
-    return launch(moe_down_kernel<GS>, a, w2, plan_down(a.T, a.K, a.E, Fmt<GS>::row_bytes(a.I)), num_sms, stream, true);
+    return launch(moe_down_kernel<GS>, a, w2, plan_down<GS>(a.T, a.K, a.E, a.I), num_sms, stream, true);
 }
 
 template <int GS>
