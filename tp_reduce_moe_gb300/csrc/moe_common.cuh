@@ -148,15 +148,16 @@ __host__ __device__ constexpr int pair_of_row(int g) {
 // which share the middle row if their number is odd).
 //
 // A ring slot holds a segment of a tile: four boxes of eight rows by 128 bytes
-// (first rows, then second rows, two boxes each), swizzled by the copy: the
+// (first rows, second rows; then the same of the next 128 bytes), swizzled by the copy: the
 // 16-byte chunk c of row g lies at place c ^ g of the row's eight.  What lies
 // behind the end of the rows is zero in a box that begins before it; boxes that
 // begin behind it are not copied.  Every slot has its mbarrier; the warp that
 // fills it is the one that reads it, and refills it at once.
 constexpr int kBox = 128;
 constexpr int kBoxBytes = 8 * kBox;
-constexpr int kHalfBytes = 2 * kBoxBytes;
-constexpr int kSlotBytes = 2 * kHalfBytes;
+constexpr int kHalfAt = kBoxBytes;       // the second rows
+constexpr int kNextAt = 2 * kBoxBytes;   // the next 128 bytes
+constexpr int kSlotBytes = 4 * kBoxBytes;
 constexpr int kMaxSlots = 2;
 
 // A weight matrix for the copies, in boxes of eight rows and of one.
@@ -187,6 +188,13 @@ __device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap& map, in
                  : "memory");
 }
 
+// Multiples of 16 bytes at such addresses.
+__device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
+}
+
 // A wait that sleeps in the instruction (the hint, in nanoseconds, is a limit)
 // instead of polling: sixteen warps that poll take issue slots from those that
 // have data.
@@ -213,13 +221,13 @@ static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase) {
 struct SlotRing {
     uint32_t slots, bars;  // shared addresses
     uint32_t slot, bar;    // the next
-    int n;
+    int n, step;           // slots, bytes between them
     uint32_t phase;
     bool alive;  // no wait has run out
 
     // arrivals: of a slot's barrier, for each filling
-    __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int arrivals, int lane)
-        : slots(slots), bars(bars), slot(slots), bar(bars), n(n), phase(0), alive(true) {
+    __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int step, int arrivals, int lane)
+        : slots(slots), bars(bars), slot(slots), bar(bars), n(n), step(step), phase(0), alive(true) {
         if (lane < n) mbar_init(bars + lane * 8, arrivals);
         fence_mbar_init();
         __syncwarp();
@@ -232,19 +240,19 @@ struct SlotRing {
         if (pairs > 4) {  // (a copy takes as long to issue for one row as for eight; rows that are not the tile's are not used)
             mbar_arrive_expect_tx(bar, wide ? 4 * kBoxBytes : 2 * kBoxBytes);
             copy_box(slot, w.eight, x, first, bar);
-            copy_box(slot + kHalfBytes, w.eight, x, second, bar);
+            copy_box(slot + kHalfAt, w.eight, x, second, bar);
             if (wide) {
-                copy_box(slot + kBoxBytes, w.eight, x + kBox, first, bar);
-                copy_box(slot + kHalfBytes + kBoxBytes, w.eight, x + kBox, second, bar);
+                copy_box(slot + kNextAt, w.eight, x + kBox, first, bar);
+                copy_box(slot + kNextAt + kHalfAt, w.eight, x + kBox, second, bar);
             }
         } else {
             mbar_arrive_expect_tx(bar, (wide ? 4 : 2) * pairs * kBox);
             for (int r = 0; r < pairs; ++r) {
                 copy_box(slot + r * kBox, w.one, x, first + r, bar);
-                copy_box(slot + kHalfBytes + r * kBox, w.one, x, second + r, bar);
+                copy_box(slot + kHalfAt + r * kBox, w.one, x, second + r, bar);
                 if (wide) {
-                    copy_box(slot + kBoxBytes + r * kBox, w.one, x + kBox, first + r, bar);
-                    copy_box(slot + kHalfBytes + kBoxBytes + r * kBox, w.one, x + kBox, second + r, bar);
+                    copy_box(slot + kNextAt + r * kBox, w.one, x + kBox, first + r, bar);
+                    copy_box(slot + kNextAt + kHalfAt + r * kBox, w.one, x + kBox, second + r, bar);
                 }
             }
         }
@@ -254,10 +262,12 @@ struct SlotRing {
     __device__ __forceinline__ void wait() {
         if (!mbar_sleep(bar, phase) && alive) alive = wait_long(bar, phase);
     }
+    // Where what comes with the slot lies, `bytes` bytes a slot.
+    __device__ __forceinline__ uint32_t beside(uint32_t first, int bytes) const { return first + (bar - bars) / 8 * bytes; }
     __device__ __forceinline__ void next() {
-        slot += kSlotBytes;
+        slot += step;
         bar += 8;
-        if (slot == slots + n * kSlotBytes) {
+        if (bar == bars + n * 8) {
             slot = slots;
             bar = bars;
             phase ^= 1;
@@ -290,9 +300,9 @@ __device__ __forceinline__ void multiply_bf16(float (&acc)[4], uint32_t slot, ui
     for (int q = 0; q < 4; ++q) {
         if (q < 2 || bytes > kBox) {
             uint32_t l[4], h[4];
-            const uint32_t at = (q & 1 ? odd : even) + (q >> 1) * kBoxBytes;
+            const uint32_t at = (q & 1 ? odd : even) + (q >> 1) * kNextAt;
             lds(l, at);
-            lds(h, at + kHalfBytes);
+            lds(h, at + kHalfAt);
             mma_bf16(acc, l[0], h[0], l[1], h[1], b[q].x, b[q].y);
             mma_bf16(more, l[2], h[2], l[3], h[3], b[q].z, b[q].w);
         }
@@ -432,21 +442,50 @@ struct StagedColumns {
     __device__ __forceinline__ float2 factor(int n) const { return make_float2(lds_f32(extras[n][0] + 16 * GS), lds_f32(extras[n][1] + 16 * GS)); }
 };
 
-// Straight from global memory, where they lie ready for the instruction
-// (ready_at, ready_scale), ahead in registers: v[i] meets the lane's word i.  The
-// power of two is 2^64 whatever the values (sums keep 24 bits while these are
-// between 2^-56 and 2^63), and -8 times the sums comes from the matrix
-// instruction with a constant operand.
-__host__ __device__ inline int ready_at(int i) { return (i & ~7) + (i & 3) * 2 + (i >> 2 & 1); }
+// Ready for the instruction in global memory, in the order of the staged values
+// (ready_at), the power of two 2^64 whatever they are (ready_scale; sums keep 24
+// bits while they are between 2^-56 and 2^63).  -8 times the sums comes from the
+// matrix instruction with a constant operand.
+template <int GS>
+__device__ __forceinline__ int ready_at(int i) {
+    constexpr int kPer = 4 / GS;
+    const int u = i >> 3 & 15;
+    return (i & ~127) + (u / (4 * kPer) * kPer + u % kPer) * 32 + u / kPer % 4 * 8 + (i & 3) * 2 + (i >> 2 & 1);
+}
 __device__ __forceinline__ float ready_scale(int i) { return i & 1 ? 0x1p60f : 0x1p64f; }
+constexpr float kReadyFactor = 0x1p69f;
+template <int GS>
+__device__ __forceinline__ float2 minus8(const uint32_t (&c)[4 / GS][4]) {
+    constexpr uint32_t kMinus8 = 0x80088008u, kMinus8x16 = 0x80808080u;
+    float sum[4];
+#pragma unroll
+    for (int j = 0; j < 4 / GS; ++j) {
+        if (j == 0)
+            mma_bf16_from(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][0], c[j][1], 0.f, 0.f, 0.f, 0.f);
+        else
+            mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][0], c[j][1]);
+        mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, c[j][2], c[j][3]);
+    }
+    return make_float2(sum[0], sum[1]);
+}
+// .. in shared memory, a segment of the lane's column (its part of the first step).
+template <int GS>
+struct ReadyColumns {
+    uint32_t values;
+    __device__ __forceinline__ void words(int, int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
+#pragma unroll
+        for (int j = 0; j < 4 / GS; ++j) lds(c[j], values + q * 256 + (s * (4 / GS) + j) * 64);
+        eight = minus8<GS>(c);
+    }
+};
+// .. in registers, a step, ahead.
 template <int GS>
 struct DirectColumns {
     uint4 v[4];
     __device__ __forceinline__ void load(const uint16_t* p, int left, int t) {
-        constexpr int kPer = 4 / GS;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int at = 32 * kPer * (i / kPer) + 8 * kPer * t + 8 * (i % kPer);
+            const int at = 32 * i + 8 * t;
             if (left >= Fmt<GS>::kStepK) {
                 v[i] = ld_coherent16(p + at);
             } else {
@@ -456,8 +495,6 @@ struct DirectColumns {
         }
     }
     __device__ __forceinline__ void words(int, int, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
-        constexpr uint32_t kMinus8 = 0x80088008u, kMinus8x16 = 0x80808080u;
-        float sum[4];
 #pragma unroll
         for (int j = 0; j < 4 / GS; ++j) {
             const uint4 w = v[s * (4 / GS) + j];
@@ -465,15 +502,9 @@ struct DirectColumns {
             c[j][1] = w.y;
             c[j][2] = w.z;
             c[j][3] = w.w;
-            if (j == 0)
-                mma_bf16_from(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, w.x, w.y, 0.f, 0.f, 0.f, 0.f);
-            else
-                mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, w.x, w.y);
-            mma_bf16(sum, kMinus8, kMinus8, kMinus8x16, kMinus8x16, w.z, w.w);
         }
-        eight = make_float2(sum[0], sum[1]);
+        eight = minus8<GS>(c);
     }
-    __device__ __forceinline__ float2 factor(int) const { return make_float2(0x1p69f, 0x1p69f); }
 };
 
 // ------------------------------------------------------------------- scales
@@ -548,11 +579,11 @@ __device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, 
     constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 #pragma unroll
     for (int s = 0; s < GS; ++s) {
-        const uint32_t at = (base ^ (s * (GS == 2 ? 32 : 16) + (q & 1) * 64)) + (q >> 1) * kBoxBytes;
+        const uint32_t at = (base ^ (s * (GS == 2 ? 32 : 16) + (q & 1) * 64)) + (q >> 1) * kNextAt;
         uint32_t c[NT][kPer][4], l[kPer], h[kPer];
         float2 eight[NT];
         lds(l, at);
-        lds(h, at + kHalfBytes);
+        lds(h, at + kHalfAt);
 #pragma unroll
         for (int n = 0; n < NT; ++n) columns.words(n, q, s, c[n], eight[n]);
         // two chains of matrix instructions where a group has eight
@@ -697,9 +728,9 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     const int row_scales = F::scales(K), segments = shape.segments;
     const int ways = 1 << split;
     const int mine = warp >> split;  // tile of a job
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, F::kW4 ? 33 : 1, lane);
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, kSlotBytes, F::kW4 ? 33 : 1, lane);
     const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
-    auto scales_slot = [&]() { return ring_scales + (ring.slot - ring.slots) / (kSlotBytes / Scales<kGS>::kSlot); };
+    auto scales_slot = [&]() { return ring.beside(ring_scales, Scales<kGS>::kSlot); };
 
     auto panel_of = [&](const Job& j) { return uniform(F::kW4 ? (int)plan.panel[jobs.staged(j)] : segments); };
     auto to = [&](int p, int panel) { return min(p + panel, segments); };

@@ -211,7 +211,7 @@ struct GateUp {
         const float v = gate / (1.0f + expf(-gate)) * up * (GS ? ready_scale(i) : 1.0f);
         const __nv_bfloat16 high = __float2bfloat16_rn(v);
         const float rest = v - __bfloat162float(high);  // an infinite value has no rest
-        uint16_t* o = a.act + (int64_t)it.slot[t.entry + token] * 2 * a.I + (GS ? ready_at(i) : i);
+        uint16_t* o = a.act + (int64_t)it.slot[t.entry + token] * 2 * a.I + (GS ? ready_at<GS ? GS : 1>(i) : i);
         o[0] = __bfloat16_as_ushort(high);
         o[a.I] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.0f));
     }
@@ -241,9 +241,15 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
 // all items' columns (item, segment), cut into sixteen equal ranges.  Each warp
 // adds its items' results, weighted, to its own sums [T][16] in shared memory;
 // the sixteen sums are added in warp order.
+//
+// 4-bit weights: the activations are copied to shared memory once, every warp's
+// by itself, if there is room for all.  Loads of them come back behind the
+// copies in flight, which took 2.6 us per segment (one token, 8 experts of 7168 x
+// 2048) where the products take 1.
 struct DownPlan {
     RowShape shape;
-    int buffers, items_at, ring_at, scales_at, slots, smem, piece;
+    int buffers, items_at, ring_at, scales_at, slots, step, smem, piece;
+    int act_at, act_entry, act_part;  // staged activations: at, bytes of an entry and of its high parts (0: not staged)
 };
 template <int GS>
 DownPlan plan_down(int T, int K, int E, int I) {
@@ -251,27 +257,44 @@ DownPlan plan_down(int T, int K, int E, int I) {
     constexpr int kScales = GS ? Scales<GS ? GS : 1>::kSlot : 0;
     p.shape = RowShape::of(Fmt<GS>::row_bytes(I));
     p.piece = GS ? Scales<GS ? GS : 1>::piece(Fmt<GS>::scales(I)) : 0;
-    // two buffers of sums, so that a tile's may be added while the next tile's are made, where that leaves room for two slots
-    p.buffers = T <= 24 ? 2 : 1;
-    p.items_at = kMvWarps * kMaxSlots * 8 + p.buffers * kMvWarps * T * 64;
-    p.ring_at = (p.items_at + Items::bytes(T * K, E) + 1023) / 1024 * 1024;
-    const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * (kSlotBytes + kScales));
-    p.slots = slots < kMaxSlots ? slots : kMaxSlots;
-    p.scales_at = p.ring_at + p.slots * kMvWarps * kSlotBytes;
-    p.smem = p.scales_at + p.slots * kMvWarps * kScales;
-    return p;
+    p.step = p.shape.row_bytes <= kBox ? kSlotBytes / 2 : kSlotBytes;
+    p.act_part = (2 * I + 255) / 256 * 256;
+    for (int option = GS ? 0 : 3;; ++option) {
+        // two buffers of sums, so that a tile's may be added while the next tile's are made, where that leaves room
+        p.buffers = option % 3 == 0 && T <= 24 ? 2 : 1;
+        // staged: entries 64 bytes off a multiple of 128 (no bank conflicts), or not
+        p.act_entry = option >= 3 ? 0 : 2 * p.act_part + (option < 2 ? 64 : 0);
+        p.items_at = (kMaxSlots + 1) * kMvWarps * 8 + p.buffers * kMvWarps * T * 64;
+        p.ring_at = (p.items_at + Items::bytes(T * K, E) + 1023) / 1024 * 1024;
+        const int slots = (kSmemLimit - p.ring_at - T * K * p.act_entry) / (kMvWarps * (p.step + kScales));
+        p.slots = slots < kMaxSlots ? slots : kMaxSlots;
+        p.scales_at = p.ring_at + p.slots * kMvWarps * p.step;
+        p.act_at = p.scales_at + p.slots * kMvWarps * kScales;
+        p.smem = p.act_at + T * K * p.act_entry;
+        if (p.act_entry == 0 || p.slots == kMaxSlots) return p;
+    }
 }
 
-template <int GS>
+template <int GS, bool STAGED>
 __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ Weights weights,
                                                                     const __grid_constant__ DownPlan plan) {
     using F = Fmt<GS>;
     constexpr int kGS = GS ? GS : 1;
     extern __shared__ __align__(1024) uint8_t smem[];
-    float* sums = reinterpret_cast<float*>(smem + kMvWarps * kMaxSlots * 8);  // [buffer][warp][T][16]
+    float* sums = reinterpret_cast<float*>(smem + kMvWarps * (kMaxSlots + 1) * 8);  // [buffer][warp][T][16]
     const Items it(smem + plan.items_at, a.T * a.K, a.E);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     pdl_trigger();
+    const uint32_t act_bar = smem_addr(smem) + (kMvWarps * kMaxSlots + warp) * 8;
+    if constexpr (STAGED) {
+        if (lane == 0) mbar_init(act_bar, 1);
+        // zeros between the values and the next 256 bytes
+        const int pad = (plan.act_part - 2 * a.I) >> 4;
+        for (int i = threadIdx.x; i < a.T * a.K * 2 * pad; i += kMvThreads) {
+            const int row = i / pad, at = plan.act_at + (row >> 1) * plan.act_entry + (row & 1) * plan.act_part + 2 * a.I + (i - row * pad) * 16;
+            *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
+        }
+    }
     // Before the wait: ids, weights and expert weights.  The first kernel starts
     // nothing before its own wait, so everything ahead of it has completed; it
     // writes the activations alone.
@@ -284,9 +307,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     const int total = it.count() * segments;
     const int f0 = total * warp / kMvWarps, f1 = total * (warp + 1) / kMvWarps;  // total <= 2^18
     const int item0 = f0 / segments, seg0 = f0 - item0 * segments;
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, F::kW4 ? 33 : 1, lane);
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * plan.step, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, plan.step, F::kW4 ? 33 : 1, lane);
     const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
-    auto scales_slot = [&]() { return ring_scales + (ring.slot - ring.slots) / (kSlotBytes / Scales<kGS>::kSlot); };
+    auto scales_slot = [&]() { return ring.beside(ring_scales, Scales<kGS>::kSlot); };
 
     // Copies: the next (tile, item, segment).
     int crow = r0, cf = f0, citem = item0, cseg = seg0;
@@ -320,6 +343,21 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     }
     ring.phase = 0;
     pdl_wait();  // the activations
+    if constexpr (STAGED) {
+        // the warp's: of every item a range of its columns, lane = (entry, part)
+        uint32_t bytes = 0;
+        for (int f = f0, item = item0, seg = seg0; f < f1; ++item, seg = 0) {
+            const int n = it.n[item], to = min(segments, seg + f1 - f), size = min(to * F::kSegK, a.I) * 2 - seg * F::kSegK * 2;
+            const int entry = it.off[item] + (lane >> 1), part = lane & 1;
+            if (lane < 2 * n)
+                bulk_copy(smem_addr(smem) + plan.act_at + entry * plan.act_entry + part * plan.act_part + seg * F::kSegK * 2,
+                          a.act + ((int64_t)it.slot[entry] * 2 + part) * a.I + seg * F::kSegK, size, act_bar);
+            bytes += 2 * n * size;
+            f += to - seg;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(act_bar, bytes);
+        if (!mbar_sleep(act_bar, 0)) ring.alive = wait_long(act_bar, 0);
+    }
 
     for (int row = r0, buf = 0; row < r1; row += 16, buf ^= plan.buffers - 1) {
         const int rows = min(16, r1 - row), pairs = (rows + 1) / 2;
@@ -332,10 +370,14 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         uint4 col[4];
         DirectColumns<kGS> direct[2];  // a box's two steps
         const uint16_t* act = nullptr;
+        uint32_t staged = 0;
         const int pair = pair_of_row<GS>(g);
         auto enter = [&](int item) {
             const int e = (g & 3) < it.n[item] ? g & 3 : 0;
-            act = a.act + ((int64_t)it.slot[it.off[item] + e] * 2 + (g >> 2)) * a.I;
+            if constexpr (STAGED)
+                staged = smem_addr(smem) + plan.act_at + (it.off[item] + e) * plan.act_entry + (g >> 2) * plan.act_part + t * 16;
+            else
+                act = a.act + ((int64_t)it.slot[it.off[item] + e] * 2 + (g >> 2)) * a.I;
         };
         auto load_part = [&](int segment, int q) {  // a step (4-bit) or a quarter of the lane's values
             const int at = segment * F::kSegK;
@@ -347,10 +389,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         int item = item0, seg = seg0;
         if (f0 < f1) {
             enter(item);
-            if constexpr (F::kW4) {
+            if constexpr (F::kW4 && !STAGED) {
                 load_part(seg, 0);
                 load_part(seg, 1);
-            } else {
+            } else if constexpr (!STAGED) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) load_part(seg, q);
             }
@@ -360,7 +402,15 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             const bool last = seg + 1 == segments, final = f + 1 == f1;
             const int after = last ? 0 : seg + 1, bytes = shape.bytes(seg);
             ring.wait();
-            if constexpr (F::kW4) {
+            if constexpr (STAGED) {
+                Scales<kGS> now;
+                const uint32_t scales = scales_slot();
+                ReadyColumns<kGS> columns{staged + seg * (F::kSegK * 2)};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q * 64 < bytes) multiply_w4<kGS, 1>(acc, ring.slot, scales, columns, now, q, lane);
+                if (last && !final) enter(item + 1);
+            } else if constexpr (F::kW4) {
                 Scales<kGS> now;
                 const uint32_t scales = scales_slot();
                 // boxes of two steps; of what is behind the end of the rows codes and activations are zero
@@ -392,7 +442,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                 const int n = it.n[item], at = it.off[item];
                 if (F::kW4)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[0][u] *= direct[0].factor(0).x;
+                    for (int u = 0; u < 4; ++u) acc[0][u] *= kReadyFactor;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) acc[0][u] += __shfl_xor_sync(0xffffffffu, acc[0][u], 2);
 #pragma unroll
@@ -454,13 +504,16 @@ cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, 
     if (e != cudaSuccess) return e;
     e = launch(moe_gate_up_kernel<GS>, a, w13, plan_product<GS, 1>(a.H, tokens, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
     if (e != cudaSuccess) return e;
-    return launch(moe_down_kernel<GS>, a, w2, plan_down<GS>(a.T, a.K, a.E, a.I), num_sms, stream, true);
+    const DownPlan plan = plan_down<GS>(a.T, a.K, a.E, a.I);
+    if (GS > 0 && plan.act_entry > 0) return launch(moe_down_kernel<GS, (GS > 0)>, a, w2, plan, num_sms, stream, true);
+    return launch(moe_down_kernel<GS, false>, a, w2, plan, num_sms, stream, true);
 }
 
 template <int GS>
 cudaError_t set_attributes() {
     cudaError_t e = cudaFuncSetAttribute(moe_gate_up_kernel<GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<GS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<GS, (GS > 0)>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     return e;
 }
 
