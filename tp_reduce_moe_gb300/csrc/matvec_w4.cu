@@ -11,9 +11,10 @@
 namespace arf {
 namespace {
 
-// Two halves of a range of rows make pairs; blocks in the order (rows, tokens).
+// Blocks of rows and tokens in the order (rows, tokens).
 template <int GS>
 struct Matvec {
+    static constexpr bool kPairs = false;
     const MatvecArgs& a;
     int r0, r1;
     int block, chunk;  // rows and tokens per job, at most
@@ -22,8 +23,8 @@ struct Matvec {
         int row, rows, token, tokens;
     };
     struct Tile {
-        int pairs, tokens, first, second;
-        int odd, token;  // whether the first pair's rows are one and the same rows' middle
+        int n, tokens, row, expert;
+        int token;
     };
     __device__ void at(Job& j, int row, int token) const {
         j.row = row;
@@ -34,12 +35,10 @@ struct Matvec {
     }
     __device__ Tile tile(const Job& j, int i) const {
         Tile t;
-        const int pairs = (j.rows + 1) / 2 - 8 * i;
-        t.pairs = max(0, min(8, pairs));
+        t.n = max(0, min(16, j.rows - 16 * i));
         t.tokens = j.tokens;
-        t.first = j.row + 8 * i;
-        t.second = t.first + j.rows / 2;
-        t.odd = i == 0 && j.rows % 2;
+        t.row = j.row + 16 * i;
+        t.expert = 0;
         t.token = j.token;
         return t;
     }
@@ -57,7 +56,8 @@ struct Matvec {
         at(j, j.row + j.rows, 0);
         return true;
     }
-    __device__ const uint16_t* scales() const { return a.s; }
+    __device__ const uint16_t* scales(const Tile& t) const { return a.s + (int64_t)t.row * (a.K / (128 / GS)); }
+    __device__ int second() const { return 8; }
     __device__ void lost() const {}
     __device__ const uint16_t* x(const Tile& t, int i) const { return a.x + (int64_t)(t.token + i) * a.K; }
     __device__ int staged_key(const Job& j) const { return j.token; }
@@ -65,16 +65,15 @@ struct Matvec {
     __device__ const uint16_t* staged_x(const Job& j, int i) const { return a.x + (int64_t)(j.token + i) * a.K; }
     __device__ int column(const Tile&, int i) const { return i; }
     __device__ void store(const Tile& t, int pair, int token, float first, float second) const {
-        const int64_t o = (int64_t)(t.token + token) * a.N;
-        const bool both = pair > 0 || !t.odd;  // the middle row of an odd number is a first row
+        const int64_t o = (int64_t)(t.token + token) * a.N + t.row + pair;
         if (a.out_f32) {
-            float* out = reinterpret_cast<float*>(a.out) + o + pair;
-            out[t.first] = first;
-            if (both) out[t.second] = second;
+            float* out = reinterpret_cast<float*>(a.out) + o;
+            out[0] = first;
+            if (pair + 8 < t.n) out[8] = second;
         } else {
-            uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + o + pair;
-            out[t.first] = __bfloat16_as_ushort(__float2bfloat16_rn(first));
-            if (both) out[t.second] = __bfloat16_as_ushort(__float2bfloat16_rn(second));
+            uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + o;
+            out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(first));
+            if (pair + 8 < t.n) out[8] = __bfloat16_as_ushort(__float2bfloat16_rn(second));
         }
     }
 };
@@ -82,6 +81,7 @@ struct Matvec {
 template <int GS, int NT>
 __global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__ Weights weights, const __grid_constant__ ProductPlan plan) {
     extern __shared__ __align__(1024) uint8_t smem[];
+    if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, plan.piece == 0);
     const Share rows(a.N);
     Matvec<GS> jobs{a, rows.first, rows.last, 0, 8 * NT};
     const int split = plan.ways.pick((rows.last - rows.first + 15) >> 4, false);
@@ -92,11 +92,12 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_c
 template <int GS, int NT>
 cudaError_t launch_kernel(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
     const ProductPlan plan = plan_product<GS, NT>(a.K, a.T, 0);
-    Weights weights;
-    const cudaError_t e = describe_weights(&weights, a.q, a.N, Fmt<GS>::row_bytes(a.K));
+    Weights weights{};
+    const int grid = a.N < num_sms ? a.N : num_sms;
+    const cudaError_t e = describe_weights(&weights, {a.q, a.s, a.N, Fmt<GS>::row_bytes(a.K), Fmt<GS>::scales(a.K), GS, 0, a.N / grid});
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.N < num_sms ? a.N : num_sms));
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kMvThreads);
     cfg.dynamicSmemBytes = (size_t)plan.smem;
     cfg.stream = stream;
@@ -105,9 +106,6 @@ cudaError_t launch_kernel(const MatvecArgs& a, int num_sms, cudaStream_t stream)
 
 template <int GS>
 cudaError_t launch(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
-#ifdef MV1
-    return launch_kernel<GS, 1>(a, num_sms, stream);
-#endif
     return a.T <= 8 ? launch_kernel<GS, 1>(a, num_sms, stream) : launch_kernel<GS, 2>(a, num_sms, stream);
 }
 

@@ -142,17 +142,19 @@ __host__ __device__ constexpr int pair_of_row(int g) {
 }
 
 // --------------------------------------------------------------------- ring
-// Rows go through the kernels in pairs: a tile is eight pairs, the first rows
-// of the pairs as rows 0-7 of the matrix instruction and the second ones as
-// rows 8-15 (a gate row and its up row; or the two halves of a range of rows,
-// which share the middle row if their number is odd).
+// A tile is sixteen rows, two by two in a lane of the matrix instruction: rows i
+// and i + 8 of a range of rows ("rows"), or a gate row and its up row, eight of
+// each ("pairs").
 //
-// A ring slot holds a segment of a tile: four boxes of eight rows by 128 bytes
-// (first rows, second rows; then the same of the next 128 bytes), swizzled by the copy: the
-// 16-byte chunk c of row g lies at place c ^ g of the row's eight.  What lies
-// behind the end of the rows is zero in a box that begins before it; boxes that
-// begin behind it are not copied.  Every slot has its mbarrier; the warp that
-// fills it is the one that reads it, and refills it at once.
+// A ring slot holds a segment of a tile: of its first 128 bytes the eight first
+// rows, then the eight second ones; then the same of the next 128 bytes; swizzled
+// by the copy: the 16-byte chunk c of row g lies at place c ^ g of the row's
+// eight.  All of it is one tensor copy (four copies of eight rows by 128 bytes
+// took 0.4 us of a warp's 1.4 us per segment to issue).  What lies behind the end
+// of the rows is zero in 128 bytes that begin before it; 128 bytes that begin
+// behind it are not copied.  Rows that are not the tile's may be copied and are
+// not used.  Every slot has its mbarrier; the warp that fills it is the one that
+// reads it, and refills it at once.
 constexpr int kBox = 128;
 constexpr int kBoxBytes = 8 * kBox;
 constexpr int kHalfAt = kBoxBytes;       // the second rows
@@ -160,11 +162,24 @@ constexpr int kNextAt = 2 * kBoxBytes;   // the next 128 bytes
 constexpr int kSlotBytes = 4 * kBoxBytes;
 constexpr int kMaxSlots = 2;
 
-// A weight matrix for the copies, in boxes of eight rows and of one.
+// A weight matrix for the copies.  A segment of 256 bytes of a whole tile takes
+// `full`: rows of 128 bytes, one dimension the 128 bytes' index in the row.  The
+// rest takes 128 bytes at a time: of 16, 8 or 4 rows ("rows"), or of a whole tile
+// ("pairs", the first).  scales: of a segment of a tile, where rows have a multiple
+// of eight.
 struct Weights {
-    CUtensorMap eight, one;
+    CUtensorMap full, part[3], scales;
 };
-cudaError_t describe_weights(Weights* w, const void* q, int64_t rows, int row_bytes);
+// What there is to describe.
+struct WeightRows {
+    const void* q;
+    const void* s;  // 4-bit: group scales, row_scales per row
+    int64_t rows;   // in all
+    int row_bytes, row_scales, group_steps;
+    int inter;      // pairs: rows come as [experts][2][inter]; 0: rows
+    int each;       // rows: fewest rows of a CTA (the others have one more)
+};
+cudaError_t describe_weights(Weights* w, const WeightRows& rows);
 
 struct RowShape {
     int row_bytes, segments;
@@ -182,10 +197,30 @@ struct Share {
     }
 };
 
-__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap& map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void copy_tensor(uint32_t to, const CUtensorMap& map, uint32_t bar, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(to),
                  "l"(&map), "r"(x), "r"(y), "r"(bar)
                  : "memory");
+}
+__device__ __forceinline__ void copy_tensor(uint32_t to, const CUtensorMap& map, uint32_t bar, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+                 "l"(&map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_tensor(uint32_t to, const CUtensorMap& map, uint32_t bar, int x, int y, int z, int u) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+                 "l"(&map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_tensor(uint32_t to, const CUtensorMap& map, uint32_t bar, int x, int y, int z, int u, int v) {
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(to),
+                 "l"(&map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
+                 : "memory");
+}
+// By one thread, ahead of the first copy: the maps come from memory otherwise.
+__device__ __forceinline__ void prefetch_maps(const Weights& w, bool full, bool scales) {
+    if (full) asm volatile("prefetch.tensormap [%0];" ::"l"(&w.full) : "memory");
+    if (scales) asm volatile("prefetch.tensormap [%0];" ::"l"(&w.scales) : "memory");
 }
 
 // Multiples of 16 bytes at such addresses.
@@ -232,29 +267,33 @@ struct SlotRing {
         fence_mbar_init();
         __syncwarp();
     }
-    // Copies `bytes` bytes of each row of a tile (rows first .., second .., `pairs` of them), from column x on, into the slot
-    // that was read last (or, at the start, one after the other).
-    __device__ __forceinline__ void fill(const Weights& w, int first, int second, int pairs, int x, int bytes, int lane) {
-        if (lane != 0) return;
-        const bool wide = bytes > kBox;
-        if (pairs > 4) {  // (a copy takes as long to issue for one row as for eight; rows that are not the tile's are not used)
-            mbar_arrive_expect_tx(bar, wide ? 4 * kBoxBytes : 2 * kBoxBytes);
-            copy_box(slot, w.eight, x, first, bar);
-            copy_box(slot + kHalfAt, w.eight, x, second, bar);
-            if (wide) {
-                copy_box(slot + kNextAt, w.eight, x + kBox, first, bar);
-                copy_box(slot + kNextAt + kHalfAt, w.eight, x + kBox, second, bar);
+    // Copies `bytes` bytes of each row of a tile, from byte 256 * seg on, into the slot that was read last (or, at the start, one
+    // after the other).  Rows: `n` of them from `row` on; pairs: from `row` of the expert's gate and up rows on.  more: bytes that
+    // come with it.
+    template <bool PAIRS>
+    __device__ __forceinline__ void fill(const Weights& w, int row, int n, int expert, int seg, int bytes, int more) {
+        const int x = seg * kSegment;
+        if (PAIRS || n > 8) {
+            const bool wide = bytes > kBox;
+            mbar_arrive_expect_tx(bar, (wide ? 4 * kBoxBytes : 2 * kBoxBytes) + more);
+            if (bytes == kSegment) {
+                if constexpr (PAIRS)
+                    copy_tensor(slot, w.full, bar, 0, row, 0, 2 * seg, expert);
+                else
+                    copy_tensor(slot, w.full, bar, 0, row, 2 * seg);
+            } else if constexpr (PAIRS) {
+                copy_tensor(slot, w.part[0], bar, x, row, 0, expert);
+                if (wide) copy_tensor(slot + kNextAt, w.part[0], bar, x + kBox, row, 0, expert);
+            } else {
+                copy_tensor(slot, w.part[0], bar, x, row);
+                if (wide) copy_tensor(slot + kNextAt, w.part[0], bar, x + kBox, row);
             }
         } else {
-            mbar_arrive_expect_tx(bar, (wide ? 4 : 2) * pairs * kBox);
-            for (int r = 0; r < pairs; ++r) {
-                copy_box(slot + r * kBox, w.one, x, first + r, bar);
-                copy_box(slot + kHalfAt + r * kBox, w.one, x, second + r, bar);
-                if (wide) {
-                    copy_box(slot + kNextAt + r * kBox, w.one, x + kBox, first + r, bar);
-                    copy_box(slot + kNextAt + kHalfAt + r * kBox, w.one, x + kBox, second + r, bar);
-                }
-            }
+            const bool wide = bytes > kBox, eight = n > 4;
+            const CUtensorMap& map = w.part[eight ? 1 : 2];
+            mbar_arrive_expect_tx(bar, (eight ? 8 : 4) * kBox * (wide ? 2 : 1) + more);
+            copy_tensor(slot, map, bar, x, row);
+            if (wide) copy_tensor(slot + kNextAt, map, bar, x + kBox, row);
         }
     }
     // Waits for the next slot.  A wait that runs out (nothing but a lost copy
@@ -508,37 +547,58 @@ struct DirectColumns {
 };
 
 // ------------------------------------------------------------------- scales
-// bf16 group scales of a segment's sixteen rows lie beside the slot, 8 * GS
-// bytes each, first rows then second rows, and come with it: a load that is
-// waited for comes back behind all the copies in flight, which takes two to three
-// microseconds, more than a segment's products.  Each lane copies half a row's
-// in pieces of `piece` bytes, asynchronously, and arrives at the slot's barrier;
-// rows of an odd number of scales are copied by loads and stores.
+// bf16 group scales of a segment's sixteen rows lie beside the slot, first rows
+// then second rows, and come with it: a load that is waited for comes back behind
+// all the copies in flight, which takes two to three microseconds, more than a
+// segment's products.  Where rows have a multiple of eight they are a tensor copy
+// (of at least 16 bytes of a row: two segments' with one group a step), else each
+// lane copies half a row's in pieces of `piece` bytes, asynchronously, and
+// arrives at the slot's barrier; rows of an odd number are copied by loads and
+// stores.
 template <int GS>
 struct Scales {
-    static constexpr int kSlot = 128 * GS;  // bytes beside a slot
-    static constexpr int kHalf = 4 * GS;    // a lane's
-    static constexpr int kWords = GS == 1 ? 2 : GS == 2 ? 4 : 2;
+    static constexpr int kHalf = 4 * GS;                     // bytes of a lane's half row
+    static constexpr int kPitch = GS == 1 ? 16 : 2 * kHalf;  // between rows
+    static constexpr int kSlot = 16 * kPitch;                // bytes beside a slot
+    static constexpr int kWords = GS == 2 ? 4 : 2;
     uint32_t raw[2][kWords];
-    __host__ static int piece(int row_scales) { return row_scales * 2 % kHalf == 0 ? kHalf : row_scales % 2 == 0 ? 4 : 2; }
-    // base: the tile's first row's scales; second: rows from there to the first of the second ones; column: the segment's first
-    __device__ static __forceinline__ void fill(uint32_t to, uint32_t bar, const uint16_t* base, int second, int pairs, int column,
+    // 0: a tensor copy
+    __host__ static int piece(int row_scales) { return row_scales % 8 == 0 ? 0 : row_scales * 2 % kHalf == 0 ? kHalf : row_scales % 2 == 0 ? 4 : 2; }
+    __host__ __device__ static int arrivals(int piece) { return piece == 0 ? 1 : 33; }
+    // where a segment's begin in a row of the slot
+    __device__ static __forceinline__ int skip(int seg) { return GS == 1 ? (seg & 1) * 8 : 0; }
+    template <bool PAIRS>
+    __device__ static __forceinline__ void copy(uint32_t to, uint32_t bar, const Weights& w, int row, int expert, int seg) {
+        const int x = GS == 1 ? seg * 4 & ~7 : seg * 4 * GS;
+        if constexpr (PAIRS)
+            copy_tensor(to, w.scales, bar, x, row, 0, expert);
+        else
+            copy_tensor(to, w.scales, bar, x, row);
+    }
+    // base: the tile's first row's scales; n: its rows or pairs; second: rows from a pair's first to its second; column: the
+    // segment's first
+    template <bool PAIRS>
+    __device__ static __forceinline__ void fill(uint32_t to, uint32_t bar, const uint16_t* base, int n, int second, int column,
                                                 int row_scales, int piece, int lane) {
         const int row = lane & 15, mine = column + (lane >> 4) * (kHalf / 2);
         const int left = (row_scales - mine) * 2;  // bytes; none or less: zeros
-        const uint16_t* from = base + (uint32_t)((row >= 8 ? second : 0) + min(row & 7, pairs - 1)) * row_scales;
-        const uint32_t at = to + row * (2 * kHalf) + (lane >> 4) * kHalf;
+        const uint16_t* from = base + (uint32_t)(PAIRS ? (row >= 8 ? second : 0) + min(row & 7, n - 1) : min(row, n - 1)) * row_scales;
+        const uint32_t at = to + row * kPitch + (lane >> 4) * kHalf + skip(column / (4 * GS));
         if (piece == kHalf) {
+            const uint16_t* p = left > 0 ? from + mine : from;
+            const int size = left > 0 ? kHalf : 0;
             if constexpr (GS == 4)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(left > 0 ? from + mine : from), "r"(left > 0 ? 16 : 0) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(p), "r"(size) : "memory");
             else if constexpr (GS == 2)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at), "l"(left > 0 ? from + mine : from), "r"(left > 0 ? 8 : 0) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at), "l"(p), "r"(size) : "memory");
             else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(left > 0 ? from + mine : from), "r"(left > 0 ? 4 : 0) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(p), "r"(size) : "memory");
         } else if (piece == 4) {
 #pragma unroll 1
             for (int o = 0; o < kHalf; o += 4)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + o), "l"(left > o ? from + mine + o / 2 : from), "r"(left > o ? 4 : 0) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + o), "l"(left > o ? from + mine + o / 2 : from),
+                             "r"(left > o ? 4 : 0)
+                             : "memory");
         } else {
 #pragma unroll 1
             for (int o = 0; o < kHalf; o += 2) {
@@ -554,7 +614,7 @@ struct Scales {
     __device__ __forceinline__ void read(uint32_t at, int q) {
         if (GS < 4 && q > 0) return;  // all at once
 #pragma unroll
-        for (int h = 0; h < 2; ++h) lds(raw[h], at + h * 8 * (2 * kHalf) + (GS == 4 ? q * 8 : 0));
+        for (int h = 0; h < 2; ++h) lds(raw[h], at + h * 8 * kPitch + (GS == 4 ? q * 8 : 0));
     }
     // Scale of group s of step q for the lane's row.
     __device__ __forceinline__ float get(int h, int q, int s) const {
@@ -570,7 +630,7 @@ template <int GS, int NT, class Columns>
 __device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, uint32_t scales, Columns& columns, Scales<GS>& sc, int q,
                                             int lane) {
     const int g = lane >> 2, t = lane & 3;
-    sc.read(scales + pair_of_row<GS>(g) * (2 * sc.kHalf), q);
+    sc.read(scales + pair_of_row<GS>(g) * sc.kPitch, q);
     constexpr int kPer = 4 / GS;  // words of a lane per scale group
     // the lane's first chunk of the step's first group, and its bytes of it; other groups and the box's second step lie at an
     // exclusive or from there
@@ -703,10 +763,11 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
 // split tiles at a time ("job"), the copies running ahead across the jobs'
 // borders.  Jobs is a class with
 //   struct Job { int count; .. }          tiles of the job
-//   struct Tile { int pairs, tokens, first, second; .. }  0 pairs: no such tile; rows first, first + 1, .. and second, ..
+//   kPairs
+//   struct Tile { int n, tokens, row, expert; .. }  n: rows or pairs, 0: no such tile; row: the first, with pairs of the expert's
 //   bool first(Job&), next(Job&)          the CTA's jobs in order
 //   Tile tile(job, i)
-//   scales()                              row 0's
+//   scales(tile), second()                its first row's; rows from a pair's first to its second
 //   x(tile, i)                            activations of the tile's token i
 //   staged_key(job), staged(job), staged_x(job, i), column(tile, i): with 4-bit weights the job's tokens that are staged
 //       (equal keys: the same ones), and which of them is the tile's token i
@@ -728,7 +789,8 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     const int row_scales = F::scales(K), segments = shape.segments;
     const int ways = 1 << split;
     const int mine = warp >> split;  // tile of a job
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, kSlotBytes, F::kW4 ? 33 : 1, lane);
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, kSlotBytes,
+                  F::kW4 ? Scales<kGS>::arrivals(plan.piece) : 1, lane);
     const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
     auto scales_slot = [&]() { return ring.beside(ring_scales, Scales<kGS>::kSlot); };
 
@@ -743,16 +805,16 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     if (!more) return;
     auto tile_of = [&](const Job& j) {
         Tile t = jobs.tile(j, mine);
-        t.pairs = uniform(t.pairs);
+        t.n = uniform(t.n);
         t.tokens = uniform(t.tokens);
-        t.first = uniform(t.first);
-        t.second = uniform(t.second);
+        t.row = uniform(t.row);
+        t.expert = uniform(t.expert);
         return t;
     };
     Tile ct = tile_of(cj);
     int cp = 0, cpanel = panel_of(cj), cway = warp & (ways - 1), cseg = cway;
     auto settle = [&]() {  // to the first segment from here on
-        while (more && (ct.pairs == 0 || cseg >= to(cp, cpanel))) {
+        while (more && (ct.n == 0 || cseg >= to(cp, cpanel))) {
             cway = turn(cway, cp, cpanel);
             cp += cpanel;
             if (cp >= segments) {
@@ -768,10 +830,16 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     };
     auto fill = [&]() {
         if (!more) return;
-        ring.fill(weights, ct.first, ct.second, ct.pairs, cseg * kSegment, shape.bytes(cseg), lane);
+        const bool scales = F::kW4 && plan.piece == 0;
+        if (lane == 0) {
+            ring.template fill<Jobs::kPairs>(weights, ct.row, ct.n, ct.expert, cseg, shape.bytes(cseg), scales ? Scales<kGS>::kSlot : 0);
+            if constexpr (F::kW4)
+                if (scales) Scales<kGS>::template copy<Jobs::kPairs>(scales_slot(), ring.bar, weights, ct.row, ct.expert, cseg);
+        }
         if constexpr (F::kW4)
-            Scales<kGS>::fill(scales_slot(), ring.bar, jobs.scales() + (int64_t)ct.first * row_scales, ct.second - ct.first, ct.pairs,
-                              cseg * 4 * kGS, row_scales, plan.piece, lane);
+            if (!scales)
+                Scales<kGS>::template fill<Jobs::kPairs>(scales_slot(), ring.bar, jobs.scales(ct), ct.n, jobs.second(), cseg * 4 * kGS, row_scales,
+                                                         plan.piece, lane);
         cseg += ways;
         if (cseg >= to(cp, cpanel)) settle();
     };
@@ -800,7 +868,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     auto load_part = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK, K - segment * F::kSegK, q, t); };
     auto view = [&](const Job& j, int panel) { return StagedView<kGS>(smem_addr(smem) + kStagedAt, panel, jobs.staged(j)); };
     auto begin = [&](const Job& j, const Tile& tile, int panel) {
-        if (tile.pairs == 0) return;
+        if (tile.n == 0) return;
         if constexpr (F::kW4) {
             columns.set(view(j, panel), lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : 0); });
         } else {
@@ -861,14 +929,14 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
             }
             staged = false;
             const int end = to(p, panel), then = turn(way, p, panel);
-            if (tile.pairs > 0) {
+            if (tile.n > 0) {
                 const int behind = first_from(p + panel, then, panel);
                 for (int seg = p + way; seg < end; seg += ways) {
                     const int after = seg + ways < end ? seg + ways : behind, bytes = shape.bytes(seg);
                     ring.wait();
                     if constexpr (F::kW4) {
                         Scales<kGS> now;
-                        const uint32_t scales = scales_slot();
+                        const uint32_t scales = scales_slot() + Scales<kGS>::skip(seg);
                         StagedColumns<kGS, NT> here = columns.at(seg - p);
                         float sum[NT][4] = {};
                         if (bytes == kSegment) {
@@ -915,7 +983,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
             const int at = i / kPairs, n = i % kPairs / 64, l = i % 64;  // l: two columns of a lane's first row
             const int pair = pair_of_row<GS>(l >> 3), token = 8 * n + (l & 7);
             const Tile of = jobs.tile(done, at);
-            if (pair >= of.pairs || token >= of.tokens) continue;
+            if (pair >= of.n || token >= of.tokens) continue;
             const float* q = r + ((at << split) * NT + n) * 128 + (l >> 1) * 4 + (l & 1);
             float first = 0.0f, second = 0.0f;
             for (int w = 0; w < ways; ++w) {

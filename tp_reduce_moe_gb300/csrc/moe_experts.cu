@@ -139,75 +139,107 @@ __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsA
 
 // ------------------------------------------------------------- first product
 // The CTA's share of the (item, row pair) list, a pair being gate row i and up
-// row I + i of the item's expert.  Tiles are the list's eights (I is a multiple
-// of 8, so that each is one item's), the share's first and last cut where it is.
+// row I + i of the item's expert: whole eights of the list (I is a multiple of 8,
+// so that each is one item's and a tile), or, where there is less than one for
+// every CTA, up to eight pairs, cut where the item ends.
 //
-// Staged activations (4-bit): all tokens if there are no more than eight, else a
-// job's tiles are one item's and its tokens are staged.
+// Staged activations (4-bit): all tokens if there are no more than eight, else
+// those of as many items as fit, and a job's tiles are of these.
 template <int GS>
 struct GateUp {
+    static constexpr bool kPairs = true;
     const ExpertsArgs& a;
     const Items& it;
-    int q0, q1;     // pairs
-    int eights;     // per item
-    int side;       // tiles per job, at most
-    bool together;  // tiles of several items in a job
+    const ProductPlan& plan;
+    int q0, q1;      // pairs
+    int eights;      // per item; 0: up to eight pairs
+    int t0, t1;      // tiles
+    bool together;   // all tokens are staged
+    int side;        // tiles per job, at most
     struct Job {
         int count;
-        int eight;  // first
-        int item, tokens;
+        int tile;                // first
+        int last, base, tokens;  // last item of those staged, first entry, entries
     };
     struct Tile {
-        int pairs, tokens, first, second;
-        int item, entry, i0;
+        int n, tokens, row, expert;
+        int entry, column;
     };
-    __device__ void at(Job& j, int eight) const {
-        j.eight = eight;
-        j.count = min(side, ((q1 + 7) >> 3) - eight);
-        j.item = 0;
-        j.tokens = a.T;
-        if (!together) {
-            j.item = eight / eights;
-            j.count = min(j.count, (j.item + 1) * eights - eight);
-            j.tokens = it.n[j.item];
+    __device__ GateUp(const ExpertsArgs& a, const Items& it, const ProductPlan& plan) : a(a), it(it), plan(plan) {
+        const int pairs = it.count() * a.I;  // at most 2^24
+        const bool whole = pairs >= 8 * (int)gridDim.x;
+        const Share share(whole ? pairs >> 3 : pairs);
+        eights = whole ? a.I >> 3 : 0;
+        q0 = share.first;
+        q1 = share.last;
+        t0 = whole ? q0 : 0;
+        t1 = whole ? q1 : (q0 < q1) + (q0 / a.I < (q1 - 1) / a.I);
+        together = GS == 0 || a.T <= kChunk1;
+        side = 1;
+    }
+    __device__ int item_of(int tile) const { return eights ? tile / eights : q0 / a.I + tile; }
+    __device__ void at(Job& j, int tile, bool fresh) const {
+        j.tile = tile;
+        j.count = min(side, t1 - tile);
+        if (together) {
+            j.last = 0;
+            j.base = 0;
+            j.tokens = a.T;
+            return;
         }
+        if (fresh || item_of(tile) > j.last) {
+            const int item = item_of(tile), end = item_of(t1 - 1);
+            j.base = it.off[item];
+            j.tokens = it.n[item];
+            for (j.last = item; j.last < end; ++j.last) {
+                const int n = j.tokens + it.n[j.last + 1];
+                if (n > kChunk1 || plan.panel[n] < plan.shape.segments) break;
+                j.tokens = n;
+            }
+        }
+        j.count = min(j.count, (eights ? (j.last + 1) * eights : j.last + 1 - q0 / a.I) - tile);
     }
     __device__ Tile tile(const Job& j, int i) const {
         Tile t;
-        t.pairs = t.tokens = t.first = t.second = t.item = t.entry = t.i0 = 0;
+        t.n = t.tokens = t.row = t.expert = t.entry = t.column = 0;
         if (i >= j.count) return t;
-        const int eight = j.eight + i, begin = max(q0, eight * 8), end = min(q1, eight * 8 + 8);
-        t.pairs = end - begin;
-        t.item = eight / eights;
-        t.tokens = it.n[t.item];
-        t.entry = it.off[t.item];
-        t.i0 = begin - t.item * a.I;
-        t.first = it.expert[t.item] * 2 * a.I + t.i0;  // at most 2^24
-        t.second = t.first + a.I;
+        const int item = item_of(j.tile + i);
+        if (eights) {
+            t.n = 8;
+            t.row = (j.tile + i - item * eights) * 8;
+        } else {
+            const int begin = max(q0, item * a.I);
+            t.n = min(q1, (item + 1) * a.I) - begin;
+            t.row = begin - item * a.I;
+        }
+        t.expert = it.expert[item];
+        t.tokens = it.n[item];
+        t.entry = it.off[item];
+        t.column = t.entry - j.base;
         return t;
     }
     __device__ bool first(Job& j) const {
-        if (q0 >= q1) return false;
-        at(j, q0 >> 3);
+        if (t0 >= t1) return false;
+        at(j, t0, true);
         return true;
     }
     __device__ bool next(Job& j) const {
-        const int eight = j.eight + j.count;
-        if (eight * 8 >= q1) return false;
-        at(j, eight);
+        if (j.tile + j.count >= t1) return false;
+        at(j, j.tile + j.count, false);
         return true;
     }
-    __device__ const uint16_t* scales() const { return a.s13; }
+    __device__ const uint16_t* scales(const Tile& t) const { return a.s13 + ((int64_t)t.expert * 2 * a.I + t.row) * Fmt<GS>::scales(a.H); }
+    __device__ int second() const { return a.I; }
     __device__ void lost() const { atomicOr(a.err, kErrTimeout); }
     __device__ const uint16_t* x(const Tile& t, int i) const { return a.x + (int64_t)it.token[t.entry + i] * a.H; }
-    __device__ int staged_key(const Job& j) const { return j.item; }
+    __device__ int staged_key(const Job& j) const { return j.base; }
     __device__ int staged(const Job& j) const { return j.tokens; }
     __device__ const uint16_t* staged_x(const Job& j, int i) const {
-        return a.x + (int64_t)(together ? i : it.token[it.off[j.item] + i]) * a.H;
+        return a.x + (int64_t)(together ? i : it.token[j.base + i]) * a.H;
     }
-    __device__ int column(const Tile& t, int i) const { return together ? it.token[t.entry + i] : i; }
+    __device__ int column(const Tile& t, int i) const { return together ? it.token[t.entry + i] : t.column + i; }
     __device__ void store(const Tile& t, int pair, int token, float gate, float up) const {
-        const int i = t.i0 + pair;
+        const int i = t.row + pair;
         const float v = gate / (1.0f + expf(-gate)) * up * (GS ? ready_scale(i) : 1.0f);
         const __nv_bfloat16 high = __float2bfloat16_rn(v);
         const float rest = v - __bfloat162float(high);  // an infinite value has no rest
@@ -221,17 +253,15 @@ template <int GS>
 __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ Weights weights,
                                                                        const __grid_constant__ ProductPlan plan) {
     extern __shared__ __align__(1024) uint8_t smem[];
+    if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     const Items it(smem + plan.extra_at, a.T * a.K, a.E);
     pdl_wait();     // no global memory access before this point
     pdl_trigger();  // after it: what the second kernel reads before its own wait is complete
     build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk1);
-    // Shares of whole tiles where there is one for every CTA, else of pairs: cutting tiles to deal 13.5 pairs to each CTA instead
-    // of one or two tiles took 23.7 us instead of 18.5 for one token and 8 experts of 2 x 256 x 7168.
-    const int pairs = it.count() * a.I;  // at most 2^24
-    const bool tiles = pairs >= 8 * (int)gridDim.x;
-    const Share share(tiles ? pairs >> 3 : pairs);
-    GateUp<GS> jobs{a, it, share.first << (tiles ? 3 : 0), share.last << (tiles ? 3 : 0), a.I >> 3, 0, GS == 0 || a.T <= kChunk1};
-    const int split = plan.ways.pick(((jobs.q1 + 7) >> 3) - (jobs.q0 >> 3), !jobs.together);
+    // (Cutting tiles to deal 13.5 pairs to each CTA instead of one or two tiles took 23.7 us instead of 18.5 for one token and 8
+    // experts of 2 x 256 x 7168.)
+    GateUp<GS> jobs(a, it, plan);
+    const int split = plan.ways.pick(jobs.t1 - jobs.t0, !jobs.together);
     jobs.side = kMvWarps >> split;
     run_product<GS, 1>(jobs, weights, smem, plan, a.H, split);
 }
@@ -285,6 +315,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     const Items it(smem + plan.items_at, a.T * a.K, a.E);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     pdl_trigger();
+    if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     const uint32_t act_bar = smem_addr(smem) + (kMvWarps * kMaxSlots + warp) * 8;
     if constexpr (STAGED) {
         if (lane == 0) mbar_init(act_bar, 1);
@@ -307,7 +338,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     const int total = it.count() * segments;
     const int f0 = total * warp / kMvWarps, f1 = total * (warp + 1) / kMvWarps;  // total <= 2^18
     const int item0 = f0 / segments, seg0 = f0 - item0 * segments;
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * plan.step, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, plan.step, F::kW4 ? 33 : 1, lane);
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * plan.step, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, plan.step,
+                  F::kW4 ? Scales<kGS>::arrivals(plan.piece) : 1, lane);
     const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
     auto scales_slot = [&]() { return ring.beside(ring_scales, Scales<kGS>::kSlot); };
 
@@ -319,10 +351,16 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     auto fill = [&]() {
         if (!more) return;
         const int rows = min(16, r1 - crow);
-        ring.fill(weights, cfirst, cfirst + rows / 2, (rows + 1) / 2, cseg * kSegment, shape.bytes(cseg), lane);
+        const bool scales = F::kW4 && plan.piece == 0;
+        if (lane == 0) {
+            ring.fill<false>(weights, cfirst, rows, 0, cseg, shape.bytes(cseg), scales ? Scales<kGS>::kSlot : 0);
+            if constexpr (F::kW4)
+                if (scales) Scales<kGS>::template copy<false>(scales_slot(), ring.bar, weights, cfirst, 0, cseg);
+        }
         if constexpr (F::kW4)
-            Scales<kGS>::fill(scales_slot(), ring.bar, a.s2 + (int64_t)cfirst * row_scales, rows / 2, (rows + 1) / 2, cseg * 4 * kGS, row_scales,
-                              plan.piece, lane);
+            if (!scales)
+                Scales<kGS>::template fill<false>(scales_slot(), ring.bar, a.s2 + (int64_t)cfirst * row_scales, rows, 8, cseg * 4 * kGS, row_scales,
+                                                  plan.piece, lane);
         if (++cf == f1) {
             cf = f0;
             citem = item0;
@@ -360,7 +398,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     }
 
     for (int row = r0, buf = 0; row < r1; row += 16, buf ^= plan.buffers - 1) {
-        const int rows = min(16, r1 - row), pairs = (rows + 1) / 2;
+        const int rows = min(16, r1 - row);
         if (plan.buffers == 1 && row > r0) __syncthreads();  // the sums are added
         float* all = sums + buf * kMvWarps * a.T * 16;
         float* mine = all + warp * a.T * 16;
@@ -404,7 +442,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             ring.wait();
             if constexpr (STAGED) {
                 Scales<kGS> now;
-                const uint32_t scales = scales_slot();
+                const uint32_t scales = scales_slot() + Scales<kGS>::skip(seg);
                 ReadyColumns<kGS> columns{staged + seg * (F::kSegK * 2)};
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -412,7 +450,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                 if (last && !final) enter(item + 1);
             } else if constexpr (F::kW4) {
                 Scales<kGS> now;
-                const uint32_t scales = scales_slot();
+                const uint32_t scales = scales_slot() + Scales<kGS>::skip(seg);
                 // boxes of two steps; of what is behind the end of the rows codes and activations are zero
 #pragma unroll
                 for (int box = 0; box < 2; ++box)
@@ -467,14 +505,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         }
         __syncthreads();  // and the other buffer's readers are done before it is written again
         for (int i = threadIdx.x; i < a.T * 16; i += kMvThreads) {
-            const int token = i >> 4, pair = i & 7, second = i >> 3 & 1;
-            if (pair < pairs) {
-                float y = 0.0f;
+            if ((i & 15) >= rows) continue;
+            float y = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kMvWarps; ++w) y += all[w * a.T * 16 + i];
-                if (second == 0 || pair > 0 || rows % 2 == 0)  // the middle row of an odd number is a first row
-                    a.out[(int64_t)token * a.H + row + pair + second * (rows / 2)] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-            }
+            for (int w = 0; w < kMvWarps; ++w) y += all[w * a.T * 16 + i];
+            a.out[(int64_t)(i >> 4) * a.H + row + (i & 15)] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
         }
     }
     if (!ring.alive) grace_period(10000000ull);  // copies that may still land
@@ -498,9 +533,10 @@ cudaError_t launch(Kernel kernel, const ExpertsArgs& a, const Weights& weights, 
 template <int GS>
 cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
     const int tokens = a.T < kChunk1 ? a.T : kChunk1;
-    Weights w13, w2;
-    cudaError_t e = describe_weights(&w13, a.w13, (int64_t)a.E * 2 * a.I, Fmt<GS>::row_bytes(a.H));
-    if (e == cudaSuccess) e = describe_weights(&w2, a.w2, (int64_t)a.E * a.H, Fmt<GS>::row_bytes(a.I));
+    Weights w13{}, w2{};
+    cudaError_t e = describe_weights(&w13, {a.w13, a.s13, (int64_t)a.E * 2 * a.I, Fmt<GS>::row_bytes(a.H), Fmt<GS>::scales(a.H), GS, a.I, 0});
+    if (e == cudaSuccess)
+        e = describe_weights(&w2, {a.w2, a.s2, (int64_t)a.E * a.H, Fmt<GS>::row_bytes(a.I), Fmt<GS>::scales(a.I), GS, 0, a.H / num_sms});
     if (e != cudaSuccess) return e;
     e = launch(moe_gate_up_kernel<GS>, a, w13, plan_product<GS, 1>(a.H, tokens, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
     if (e != cudaSuccess) return e;
@@ -519,7 +555,7 @@ cudaError_t set_attributes() {
 
 }  // namespace
 
-cudaError_t describe_weights(Weights* w, const void* q, int64_t rows, int row_bytes) {
+cudaError_t describe_weights(Weights* w, const WeightRows& m) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -534,16 +570,59 @@ cudaError_t describe_weights(Weights* w, const void* q, int64_t rows, int row_by
         encode = reinterpret_cast<Encode>(f);
         cached.store(encode, std::memory_order_release);
     }
-    const cuuint64_t dim[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)row_bytes};
-    const cuuint32_t unit[2] = {1, 1};
-    for (int i = 0; i < 2; ++i) {
-        const cuuint32_t box[2] = {kBox, i == 0 ? 8u : 1u};
-        if (encode(i == 0 ? &w->eight : &w->one, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dim, pitch, box, unit,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
+    bool ok = true;
+    auto map = [&](CUtensorMap* to, bool codes, int rank, const cuuint64_t* dim, const cuuint64_t* pitch, const cuuint32_t* box) {
+        const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+        ok = ok && encode(to, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, (cuuint32_t)rank,
+                          const_cast<void*>(codes ? m.q : m.s), dim, pitch, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          codes ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t bytes = (cuuint64_t)m.row_bytes, rows = (cuuint64_t)m.rows, whole = bytes / kBox;
+    const bool ragged = bytes % kSegment != 0;
+    const cuuint32_t scales = m.group_steps == 1 ? 8 : 4 * m.group_steps;
+    const cuuint64_t scale_bytes = (cuuint64_t)m.row_scales * 2;
+    const bool tensor_scales = m.group_steps > 0 && m.row_scales % 8 == 0;
+    if (m.inter > 0) {
+        const cuuint64_t inter = (cuuint64_t)m.inter, experts = rows / (2 * inter);
+        if (bytes >= kSegment) {
+            const cuuint64_t dim[5] = {kBox, inter, 2, whole, experts}, pitch[4] = {bytes, inter * bytes, kBox, 2 * inter * bytes};
+            const cuuint32_t box[5] = {kBox, 8, 2, 2, 1};
+            map(&w->full, true, 5, dim, pitch, box);
+        }
+        if (ragged) {
+            const cuuint64_t dim[4] = {bytes, inter, 2, experts}, pitch[3] = {bytes, inter * bytes, 2 * inter * bytes};
+            const cuuint32_t box[4] = {kBox, 8, 2, 1};
+            map(&w->part[0], true, 4, dim, pitch, box);
+        }
+        if (tensor_scales) {
+            const cuuint64_t dim[4] = {(cuuint64_t)m.row_scales, inter, 2, experts},
+                             pitch[3] = {scale_bytes, inter * scale_bytes, 2 * inter * scale_bytes};
+            const cuuint32_t box[4] = {scales, 8, 2, 1};
+            map(&w->scales, false, 4, dim, pitch, box);
+        }
+    } else {
+        // heights of the CTAs' last tiles
+        const int last = m.each % 16, one_more = (m.each + 1) % 16;
+        auto ends = [&](int from, int to) { return (last >= from && last <= to) || (one_more >= from && one_more <= to); };
+        if (bytes >= kSegment) {
+            const cuuint64_t dim[3] = {kBox, rows, whole}, pitch[2] = {bytes, kBox};
+            const cuuint32_t box[3] = {kBox, 16, 2};
+            map(&w->full, true, 3, dim, pitch, box);
+        }
+        const cuuint64_t dim[2] = {bytes, rows}, pitch[1] = {bytes};
+        for (int i = 0; i < 3; ++i)
+            if (i == 0 ? ragged : i == 1 ? ends(5, 8) : ends(1, 4)) {
+                const cuuint32_t box[2] = {kBox, 16u >> i};
+                map(&w->part[i], true, 2, dim, pitch, box);
+            }
+        if (tensor_scales) {
+            const cuuint64_t dims[2] = {(cuuint64_t)m.row_scales, rows}, pitches[1] = {scale_bytes};
+            const cuuint32_t box[2] = {scales, 16};
+            map(&w->scales, false, 2, dims, pitches, box);
+        }
     }
-    return cudaSuccess;
+    return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 cudaError_t launch_moe_experts(const ExpertsArgs& a, int group, int num_sms, cudaStream_t stream, bool pdl) {
