@@ -78,22 +78,22 @@ struct Matvec {
     }
 };
 
-template <int GS, int NT>
+template <int GS>
 __global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__ Weights weights, const __grid_constant__ ProductPlan plan) {
     extern __shared__ __align__(1024) uint8_t smem[];
+    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, plan.slots, Scales<GS>::arrivals(plan.piece), threadIdx.x & 31);
     if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, plan.piece == 0);
     const Share rows(a.N);
-    Matvec<GS> jobs{a, rows.first, rows.last, 0, 8 * NT};
-    const int split = plan.ways.pick((rows.last - rows.first + 15) >> 4, false);
-    jobs.block = 16 * (kMvWarps >> split);
-    run_product<GS, NT>(jobs, weights, smem, plan, a.K, split);
+    Matvec<GS> jobs{a, rows.first, rows.last, 0, 8};
+    jobs.block = 16 * kJobTiles<GS>;
+    run_product<GS>(jobs, weights, smem, plan, a.K);
 }
 
-template <int GS, int NT>
-cudaError_t launch_kernel(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
-    const ProductPlan plan = plan_product<GS, NT>(a.K, a.T, 0);
+template <int GS>
+cudaError_t launch(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
     Weights weights{};
     const int grid = a.N < num_sms ? a.N : num_sms;
+    const ProductPlan plan = plan_product<GS>(a.K, a.T, ((a.N + grid - 1) / grid + 15) / 16, 0);
     const cudaError_t e = describe_weights(&weights, {a.q, a.s, a.N, Fmt<GS>::row_bytes(a.K), Fmt<GS>::scales(a.K), GS, 0, a.N / grid});
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -101,19 +101,7 @@ cudaError_t launch_kernel(const MatvecArgs& a, int num_sms, cudaStream_t stream)
     cfg.blockDim = dim3(kMvThreads);
     cfg.dynamicSmemBytes = (size_t)plan.smem;
     cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, matvec_w4_kernel<GS, NT>, a, weights, plan);
-}
-
-template <int GS>
-cudaError_t launch(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
-    return a.T <= 8 ? launch_kernel<GS, 1>(a, num_sms, stream) : launch_kernel<GS, 2>(a, num_sms, stream);
-}
-
-template <int GS>
-cudaError_t set_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(matvec_w4_kernel<GS, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(matvec_w4_kernel<GS, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-    return e;
+    return cudaLaunchKernelEx(&cfg, matvec_w4_kernel<GS>, a, weights, plan);
 }
 
 }  // namespace
@@ -128,9 +116,9 @@ cudaError_t launch_matvec_w4(const MatvecArgs& a, int group, int num_sms, cudaSt
 }
 
 cudaError_t matvec_w4_set_attributes() {
-    cudaError_t e = set_attributes<1>();
-    if (e == cudaSuccess) e = set_attributes<2>();
-    if (e == cudaSuccess) e = set_attributes<4>();
+    cudaError_t e = cudaFuncSetAttribute(matvec_w4_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(matvec_w4_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(matvec_w4_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     return e;
 }
 

@@ -133,6 +133,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ int warp_index() { return uniform((int)(threadIdx.x >> 5)); }
 
+// a / b for 0 <= a <= 2^23, 0 < b, a / b < 2^20: in floating point off by one at most.
+__device__ __forceinline__ int quotient(int a, int b) {
+    int q = (int)__fdividef((float)a, (float)b);
+    q -= q * b > a;
+    q += a - q * b >= b;
+    return q;
+}
+
 // The pair of a tile that lane row g (of the eight) stands for: an order in which
 // reads of a quarter (16 bytes a lane), half (8) or whole warp (4) meet every
 // bank of the swizzled rows once.
@@ -260,9 +268,10 @@ struct SlotRing {
     uint32_t phase;
     bool alive;  // no wait has run out
 
-    // arrivals: of a slot's barrier, for each filling
-    __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int step, int arrivals, int lane)
-        : slots(slots), bars(bars), slot(slots), bar(bars), n(n), step(step), phase(0), alive(true) {
+    __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int step)
+        : slots(slots), bars(bars), slot(slots), bar(bars), n(n), step(step), phase(0), alive(true) {}
+    // The warp's barriers, before anything else; arrivals: of each, for each filling.
+    __device__ static __forceinline__ void init(uint32_t bars, int n, int arrivals, int lane) {
         if (lane < n) mbar_init(bars + lane * 8, arrivals);
         fence_mbar_init();
         __syncwarp();
@@ -399,86 +408,84 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
     return v;
 }
 
-// One warp: a segment (512 bf16 values) of a token into column `col`; of step q
-// the lane holds values 4 * lane .. + 3 in w[q] (zero behind the end of the row).
+// One warp: a segment (512 bf16 values) of a token into column `col`; w[h]: of
+// step 2 * h + lane / 16 the values 8 * (lane % 16) .. + 7 (zero behind the end of
+// the row).
 template <int GS>
-__device__ __forceinline__ void stage_segment(const StagedView<GS>& v, int segment, int col, const uint2 (&w)[4], int lane) {
+__device__ __forceinline__ void stage_segment(const StagedView<GS>& v, int segment, int col, const uint4 (&w)[2], int lane) {
     // magnitudes as integers, two to a word: NaN is above everything
+    constexpr unsigned kMagnitude = 0x7fff7fffu;
     unsigned big = 0u;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) big = __vmaxu2(big, __vmaxu2(w[q].x & 0x7fff7fffu, w[q].y & 0x7fff7fffu));
+    for (int h = 0; h < 2; ++h)
+        big = __vmaxu2(__vmaxu2(__vmaxu2(w[h].x & kMagnitude, w[h].y & kMagnitude), __vmaxu2(w[h].z & kMagnitude, w[h].w & kMagnitude)), big);
     const unsigned top = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16)) >> 7;
     const bool bad = top > 227;  // infinite, undefined, or 2^101 and more: so is every sum it is in
     // 2^(up - 127) * 2^(top - 127) = 2^90, as far as bf16 goes and the factor does
     const unsigned up = bad ? 133u : max(min(344u - top, 254u), 133u);
     const uint32_t one = up << 7 | up << 23, sixteenth = (up - 4) << 7 | (up - 4) << 23;
-    const int odd = lane & 1;  // an even lane holds values 0-3 of eight, an odd one 4-7
-    const int u = lane >> 1;   // word of eight values: word i of lane t
-    constexpr int kPer = 4 / GS;
+    const int u = lane & 15;  // word of eight values: word i of lane t
+    constexpr int kPer = 4 / GS, kLanes = 16 / GS;
     const int t = u / kPer % 4, i = u / (4 * kPer) * kPer + u % kPer;
-    const uint32_t at = v.values + col * v.stride + segment * 1024 + i * 64 + t * 16 + odd * 8;
+    const uint32_t at = v.values + col * v.stride + segment * 1024 + (lane >> 4) * 256 + i * 64 + t * 16;
     const uint32_t extra = v.extras + col * v.extra_stride + segment * v.kExtra;
     const float minus8 = __uint_as_float((up - 130) << 23 | 0x80000000u);  // -8 * 2^(up - 127) * 2^-133
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w[q].x : w[q].y, 1);
-        const uint32_t a = odd ? other : w[q].x, b = odd ? w[q].y : other;
-        const uint32_t c0 = mul_bf16x2(__byte_perm(a, b, 0x5410), one), c1 = mul_bf16x2(__byte_perm(a, b, 0x7632), sixteenth);
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + q * 256), "r"(c0), "r"(c1) : "memory");
+    for (int h = 0; h < 2; ++h) {
+        const uint4 x = w[h];
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + h * 512), "r"(mul_bf16x2(__byte_perm(x.x, x.z, 0x5410), one)),
+                     "r"(mul_bf16x2(__byte_perm(x.x, x.z, 0x7632), sixteenth)), "r"(mul_bf16x2(__byte_perm(x.y, x.w, 0x5410), one)),
+                     "r"(mul_bf16x2(__byte_perm(x.y, x.w, 0x7632), sixteenth))
+                     : "memory");
         // -8 * 2^-133 times the scaled values' sum, in each group
-        float sum = (__uint_as_float(w[q].x << 16) + __uint_as_float(w[q].x & 0xffff0000u)) +
-                    (__uint_as_float(w[q].y << 16) + __uint_as_float(w[q].y & 0xffff0000u));
+        float f[8];
+        bf16x8_to_f32(x, f);
+        float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
 #pragma unroll
-        for (int o = 1; o < 32 / GS; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane % (32 / GS) == 0) sts_f32(extra + (q * GS + lane / (32 / GS)) * 4, sum * minus8);
+        for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (u % kLanes == 0) sts_f32(extra + ((2 * h + (lane >> 4)) * GS + u / kLanes) * 4, sum * minus8);
     }
     if (lane == 0)
         sts_f32(extra + 16 * GS,
                 __uint_as_float(bad ? 0x7fc00000u : (387 - up) << 23));  // 2^(127 - up) * 2^133
 }
 
-// Where the products take their columns from: words(n, q, s, c, eight) gives the
+// Where the products take their columns from: words(q, s, c, eight) gives the
 // lane's values of scale group s of step q and what the group's sums start from,
-// factor(n) what the sums are multiplied by.
+// factor() what the sums are multiplied by.
 //
 // Staged in shared memory: a segment.
-template <int GS, int NT>
+template <int GS>
 struct StagedColumns {
-    uint32_t values[NT], extras[NT][2];
-    uint32_t sums[NT][2][4];  // four of columns 2t and 2t + 1
+    uint32_t values, extras[2];
+    uint32_t sums[2][4];  // four of columns 2t and 2t + 1
     // column(i): the staged column of column i of the instructions
     template <class Column>
     __device__ __forceinline__ void set(const StagedView<GS>& v, int lane, Column column) {
         const int g = lane >> 2, t = lane & 3;
+        values = v.values + column(g) * v.stride + t * 16;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            values[n] = v.values + column(8 * n + g) * v.stride + t * 16;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) extras[n][u] = v.extras + column(8 * n + 2 * t + u) * v.extra_stride;
-        }
+        for (int u = 0; u < 2; ++u) extras[u] = v.extras + column(2 * t + u) * v.extra_stride;
     }
     __device__ __forceinline__ StagedColumns at(int segment) const {
         StagedColumns c;
+        c.values = values + segment * 1024;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            c.values[n] = values[n] + segment * 1024;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) c.extras[n][u] = extras[n][u] + segment * StagedView<GS>::kExtra;
-        }
+        for (int u = 0; u < 2; ++u) c.extras[u] = extras[u] + segment * StagedView<GS>::kExtra;
         return c;
     }
     // In order: q, s.
-    __device__ __forceinline__ void words(int n, int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) {
+    __device__ __forceinline__ void words(int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) {
 #pragma unroll
-        for (int j = 0; j < 4 / GS; ++j) lds(c[j], values[n] + q * 256 + (s * (4 / GS) + j) * 64);
+        for (int j = 0; j < 4 / GS; ++j) lds(c[j], values + q * 256 + (s * (4 / GS) + j) * 64);
         const int i = q * GS + s;
         if (i % 4 == 0) {
-            lds(sums[n][0], extras[n][0] + i * 4);
-            lds(sums[n][1], extras[n][1] + i * 4);
+            lds(sums[0], extras[0] + i * 4);
+            lds(sums[1], extras[1] + i * 4);
         }
-        eight = make_float2(__uint_as_float(sums[n][0][i % 4]), __uint_as_float(sums[n][1][i % 4]));
+        eight = make_float2(__uint_as_float(sums[0][i % 4]), __uint_as_float(sums[1][i % 4]));
     }
-    __device__ __forceinline__ float2 factor(int n) const { return make_float2(lds_f32(extras[n][0] + 16 * GS), lds_f32(extras[n][1] + 16 * GS)); }
+    __device__ __forceinline__ float2 factor() const { return make_float2(lds_f32(extras[0] + 16 * GS), lds_f32(extras[1] + 16 * GS)); }
 };
 
 // Ready for the instruction in global memory, in the order of the staged values
@@ -511,7 +518,7 @@ __device__ __forceinline__ float2 minus8(const uint32_t (&c)[4 / GS][4]) {
 template <int GS>
 struct ReadyColumns {
     uint32_t values;
-    __device__ __forceinline__ void words(int, int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
+    __device__ __forceinline__ void words(int q, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
 #pragma unroll
         for (int j = 0; j < 4 / GS; ++j) lds(c[j], values + q * 256 + (s * (4 / GS) + j) * 64);
         eight = minus8<GS>(c);
@@ -533,7 +540,7 @@ struct DirectColumns {
             }
         }
     }
-    __device__ __forceinline__ void words(int, int, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
+    __device__ __forceinline__ void words(int, int s, uint32_t (&c)[4 / GS][4], float2& eight) const {
 #pragma unroll
         for (int j = 0; j < 4 / GS; ++j) {
             const uint4 w = v[s * (4 / GS) + j];
@@ -624,11 +631,10 @@ struct Scales {
     }
 };
 
-// sum[n] += (tile) * (column tile n), step q of the segment at `slot`, its scales
-// at `scales`.  Without the columns' factors.  In order: q.
-template <int GS, int NT, class Columns>
-__device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, uint32_t scales, Columns& columns, Scales<GS>& sc, int q,
-                                            int lane) {
+// sum += (tile) * (columns), step q of the segment at `slot`, its scales at
+// `scales`.  Without the columns' factors.  In order: q.
+template <int GS, class Columns>
+__device__ __forceinline__ void multiply_w4(float (&sum)[4], uint32_t slot, uint32_t scales, Columns& columns, Scales<GS>& sc, int q, int lane) {
     const int g = lane >> 2, t = lane & 3;
     sc.read(scales + pair_of_row<GS>(g) * sc.kPitch, q);
     constexpr int kPer = 4 / GS;  // words of a lane per scale group
@@ -640,117 +646,97 @@ __device__ __forceinline__ void multiply_w4(float (&sum)[NT][4], uint32_t slot, 
 #pragma unroll
     for (int s = 0; s < GS; ++s) {
         const uint32_t at = (base ^ (s * (GS == 2 ? 32 : 16) + (q & 1) * 64)) + (q >> 1) * kNextAt;
-        uint32_t c[NT][kPer][4], l[kPer], h[kPer];
-        float2 eight[NT];
+        uint32_t c[kPer][4], l[kPer], h[kPer];
+        float2 eight;
         lds(l, at);
         lds(h, at + kHalfAt);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) columns.words(n, q, s, c[n], eight[n]);
+        columns.words(q, s, c, eight);
         // two chains of matrix instructions where a group has eight
         constexpr bool kTwo = kPer == 4;
-        float part[NT][4], more[NT][4];
+        float part[4], more[4];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const uint32_t l8 = l[j] >> 8, h8 = h[j] >> 8;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (j == 0) {
-                    mma_bf16_from(part[n], l[j] & kLow, h[j] & kLow, l[j] & kHigh, h[j] & kHigh, c[n][j][0], c[n][j][1], eight[n].x,
-                                  eight[n].y, eight[n].x, eight[n].y);
-                    if (kTwo)
-                        mma_bf16_from(more[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3], 0.f, 0.f, 0.f, 0.f);
-                    else
-                        mma_bf16(part[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3]);
-                } else {
-                    mma_bf16(part[n], l[j] & kLow, h[j] & kLow, l[j] & kHigh, h[j] & kHigh, c[n][j][0], c[n][j][1]);
-                    mma_bf16(kTwo ? more[n] : part[n], l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[n][j][2], c[n][j][3]);
-                }
+            if (j == 0) {
+                mma_bf16_from(part, l[j] & kLow, h[j] & kLow, l[j] & kHigh, h[j] & kHigh, c[j][0], c[j][1], eight.x, eight.y, eight.x, eight.y);
+                if (kTwo)
+                    mma_bf16_from(more, l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[j][2], c[j][3], 0.f, 0.f, 0.f, 0.f);
+                else
+                    mma_bf16(part, l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[j][2], c[j][3]);
+            } else {
+                mma_bf16(part, l[j] & kLow, h[j] & kLow, l[j] & kHigh, h[j] & kHigh, c[j][0], c[j][1]);
+                mma_bf16(kTwo ? more : part, l8 & kLow, h8 & kLow, l8 & kHigh, h8 & kHigh, c[j][2], c[j][3]);
             }
         }
         const float sl = sc.get(0, q, s), sh = sc.get(1, q, s);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) sum[n][u] = fmaf(u < 2 ? sl : sh, kTwo ? part[n][u] + more[n][u] : part[n][u], sum[n][u]);
+        for (int u = 0; u < 4; ++u) sum[u] = fmaf(u < 2 ? sl : sh, kTwo ? part[u] + more[u] : part[u], sum[u]);
     }
 }
-template <int NT, class Columns>
-__device__ __forceinline__ void add_scaled(float (&acc)[NT][4], const float (&sum)[NT][4], const Columns& columns) {
+template <class Columns>
+__device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&sum)[4], const Columns& columns) {
+    const float2 f = columns.factor();
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const float2 f = columns.factor(n);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) acc[n][u] = fmaf(u & 1 ? f.y : f.x, sum[n][u], acc[n][u]);
-    }
+    for (int u = 0; u < 4; ++u) acc[u] = fmaf(u & 1 ? f.y : f.x, sum[u], acc[u]);
 }
 
 // ----------------------------------------------------------------- products
-// How the sixteen warps of a CTA share tiles: 2^ways of them split a tile's
-// segments, 16 / 2^ways tiles go side by side (the ways take turns at what is
-// left over from one round of tiles to the next).  The least time for the
-// busiest warp, a round's end taking that of half a segment to a whole one.
-//  cut: rounds may end early once (at an expert's end).
-struct Ways {
-    int each[5];  // segments of the busiest way, for 2^i ways
-    __host__ static Ways of(int segments) {
-        Ways w;
-        for (int i = 0; i < 5; ++i) w.each[i] = (segments + (1 << i) - 1) >> i;
-        return w;
-    }
-    __device__ __forceinline__ int pick(int tiles, bool cut) const {
-#ifdef FS
-        return FS;
+// How the sixteen warps of a CTA share tiles: a job's tiles, one after the other,
+// are a list of segments, which is cut into sixteen ranges of equal length.  A
+// warp adds up the segments that it has of a tile; the parts of a tile are added
+// in the order of the warps, once a job.  (Tiles side by side and their segments
+// dealt to powers of two of warps left a seventh of the warps idle, or took a
+// round with two barriers for every few tiles, 1.8 us each.)
+#ifndef JT
+#define JT 32
 #endif
-        int best = 4, cost = 0x7fffffff;
-#pragma unroll
-        for (int i = 4; i >= 0; --i) {
-            const int side = 16 >> i, rounds = (min(tiles, 1 << 14) + (cut ? side - 1 : 0) + side - 1) >> (4 - i);
-            const int c = rounds * (2 * each[i] + 1);
-            if (c < cost) {
-                cost = c;
-                best = i;
-            }
-        }
-        return best;
-    }
-};
+template <int GS>
+constexpr int kJobTiles = GS ? 32 : JT;
 
-// Shared memory of a product: barriers, two buffers of partial tiles, staged
-// activations, `extra` bytes, the rings.
+// Shared memory of a product: barriers, parts of tiles (warp w's of tile i at i + w:
+// ranges are in order), with several panels the sums over those done, staged activations, `extra` bytes, the
+// rings, their scales.
 constexpr int kSmemLimit = 227 * 1024;
 struct ProductPlan {
     RowShape shape;
-    Ways ways;
-    uint8_t panel[17];  // segments whose activations are staged at a time, by the number of staged tokens
+    uint8_t panel[9];   // segments whose activations are staged at a time, by the number of staged tokens
     int staged;         // bytes
+    int sums_at, staged_at;
     int extra;    // bytes, at extra_at
     int slots;    // per warp
     int extra_at, ring_at, scales_at, smem;
     int piece;  // of the scales' copies
 };
-template <int GS, int NT>
-inline ProductPlan plan_product(int K, int tokens, int extra) {
+template <int GS>
+inline ProductPlan plan_product(int K, int tokens, int tiles, int extra) {  // tiles: of a CTA, at most
     ProductPlan p;
     p.shape = RowShape::of(Fmt<GS>::row_bytes(K));
-    const int segments = p.shape.segments, fixed = kMvWarps * kMaxSlots * 8 + 2 * kMvWarps * NT * 512 + extra;
+    const int segments = p.shape.segments;
     constexpr int kScales = GS ? Scales<GS ? GS : 1>::kSlot : 0, kSlot = kSlotBytes + kScales;
     p.piece = GS ? Scales<GS ? GS : 1>::piece(Fmt<GS>::scales(K)) : 0;
     p.extra = extra;
+    tiles = tiles < kJobTiles<GS> ? tiles : kJobTiles<GS>;
+    p.sums_at = kMvWarps * kMaxSlots * 8 + (tiles + kMvWarps) * 512;
+    p.staged_at = p.sums_at;
+    int fixed = p.staged_at + extra;
+    using View = StagedView<GS ? GS : 1>;
+    // at least two slots per warp
+    auto room = [&](int n) { return (kSmemLimit - fixed - kMaxSlots * kMvWarps * kSlot - 1024 - View::bytes(0, n)) / (View::bytes(1, n) - View::bytes(0, n)); };
+    const int columns = tokens < 8 ? tokens : 8;
+    if (GS > 0 && room(columns) < segments) {
+        p.staged_at += tiles * 512;
+        fixed += tiles * 512;
+    }
     p.staged = 0;
-    for (int n = 0; n <= 16; ++n) {
+    for (int n = 0; n <= 8; ++n) {
         p.panel[n] = (uint8_t)segments;  // at most 128
-        if (GS == 0 || n == 0 || n > tokens || n > 8 * NT) continue;
-        // at least two slots per warp
-        using View = StagedView<GS ? GS : 1>;
-        const int none = View::bytes(0, n), each = View::bytes(1, n) - none;
-        const int most = (kSmemLimit - fixed - kMaxSlots * kMvWarps * kSlot - 1024 - none) / each;
-        const int panels = (segments + most - 1) / most;
+        if (GS == 0 || n == 0 || n > columns) continue;
+        const int most = room(n), panels = (segments + most - 1) / most;
         p.panel[n] = (uint8_t)((segments + panels - 1) / panels);
         const int bytes = (View::bytes(p.panel[n], n) + 15) / 16 * 16;
         p.staged = bytes > p.staged ? bytes : p.staged;
     }
-    p.ways = Ways::of(segments);
-    p.extra_at = fixed - extra + p.staged;
+    p.extra_at = p.staged_at + p.staged;
     p.ring_at = (p.extra_at + extra + 1023) / 1024 * 1024;
     const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlot);
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
@@ -759,12 +745,12 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
     return p;
 }
 
-// The products of tiles of row pairs with up to 8 * NT tokens each, up to 16 >>
-// split tiles at a time ("job"), the copies running ahead across the jobs'
-// borders.  Jobs is a class with
-//   struct Job { int count; .. }          tiles of the job
+// The products of tiles with up to 8 tokens each, up to kJobTiles tiles at a
+// time ("job"), the copies running ahead across the jobs' borders.  Jobs is a
+// class with
 //   kPairs
-//   struct Tile { int n, tokens, row, expert; .. }  n: rows or pairs, 0: no such tile; row: the first, with pairs of the expert's
+//   struct Job { int count; .. }          tiles of the job
+//   struct Tile { int n, tokens, row, expert; .. }  n: rows or pairs; row: the first, with pairs of the expert's
 //   bool first(Job&), next(Job&)          the CTA's jobs in order
 //   Tile tile(job, i)
 //   scales(tile), second()                its first row's; rows from a pair's first to its second
@@ -773,75 +759,85 @@ inline ProductPlan plan_product(int K, int tokens, int extra) {
 //       (equal keys: the same ones), and which of them is the tile's token i
 //   store(tile, pair, token, first, second)  results of a pair's two rows
 //   lost()                                a wait ran out
-// Deterministic: a tile's sums are added in the order of the ways.
-template <int GS, int NT, class Jobs>
-__device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& weights, uint8_t* smem, const ProductPlan& plan, int K, int split) {
+// Deterministic: a tile's sums are added in the order of the warps.
+template <int GS, class Jobs>
+__device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& weights, uint8_t* smem, const ProductPlan& plan, int K) {
     using F = Fmt<GS>;
     using Job = typename Jobs::Job;
     using Tile = typename Jobs::Tile;
-    static_assert(F::kW4 || NT == 1, "bf16 weights: one column tile");
     constexpr int kGS = GS ? GS : 1;
-    constexpr int kRed = kMvWarps * NT * 128;  // floats, one buffer
-    constexpr int kRedAt = kMvWarps * kMaxSlots * 8, kStagedAt = kRedAt + 2 * kRed * 4;
-    float* red = reinterpret_cast<float*>(smem + kRedAt);
+    constexpr int kPart = 128;  // floats
+    float* parts = reinterpret_cast<float*>(smem + kMvWarps * kMaxSlots * 8);
+    float* sums = reinterpret_cast<float*>(smem + plan.sums_at);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     const RowShape& shape = plan.shape;
     const int row_scales = F::scales(K), segments = shape.segments;
-    const int ways = 1 << split;
-    const int mine = warp >> split;  // tile of a job
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, kSlotBytes,
-                  F::kW4 ? Scales<kGS>::arrivals(plan.piece) : 1, lane);
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, kSlotBytes);
     const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
     auto scales_slot = [&]() { return ring.beside(ring_scales, Scales<kGS>::kSlot); };
 
     auto panel_of = [&](const Job& j) { return uniform(F::kW4 ? (int)plan.panel[jobs.staged(j)] : segments); };
-    auto to = [&](int p, int panel) { return min(p + panel, segments); };
-    // The warp's segments of a panel: p + way, p + way + ways, .., with way turning by the panel's length from panel to panel.
-    auto turn = [&](int way, int p, int panel) { return (way - (to(p, panel) - p)) & (ways - 1); };
-
-    // Copies: the next (job, panel, segment).
-    Job cj;
-    bool more = jobs.first(cj);
-    if (!more) return;
-    auto tile_of = [&](const Job& j) {
-        Tile t = jobs.tile(j, mine);
+    auto tile_of = [&](const Job& j, int i) {
+        Tile t = jobs.tile(j, i);
         t.n = uniform(t.n);
         t.tokens = uniform(t.tokens);
         t.row = uniform(t.row);
         t.expert = uniform(t.expert);
         return t;
     };
-    Tile ct = tile_of(cj);
-    int cp = 0, cpanel = panel_of(cj), cway = warp & (ways - 1), cseg = cway;
-    auto settle = [&]() {  // to the first segment from here on
-        while (more && (ct.n == 0 || cseg >= to(cp, cpanel))) {
-            cway = turn(cway, cp, cpanel);
-            cp += cpanel;
+    // The warp's range of a job's panel of `len` segments: from segment `seg` of tile `tile` on, `left` of them.
+    struct Range {
+        int tile, seg, left;
+        __device__ __forceinline__ Range(int count, int len, int warp) {
+            const unsigned total = count * len;
+            const int f0 = (int)(total * warp / kMvWarps);
+            left = (int)(total * (warp + 1) / kMvWarps) - f0;
+            tile = quotient(f0, len);
+            seg = f0 - tile * len;
+        }
+    };
+
+    // Copies: the next (job, panel, range).
+    Job cj;
+    bool more = jobs.first(cj);
+    if (!more) return;
+    int cp = 0, cpanel = panel_of(cj), clen = min(cpanel, segments);
+    Range c(cj.count, clen, warp);
+    Tile ct;
+    auto settle = [&]() {  // to the next panel, while nothing is left
+        while (more && c.left == 0) {
+            cp += clen;
             if (cp >= segments) {
                 cp = 0;
                 more = jobs.next(cj);
-                if (more) {
-                    ct = tile_of(cj);
-                    cpanel = panel_of(cj);
-                }
+                if (more) cpanel = panel_of(cj);
             }
-            cseg = cp + cway;
+            if (more) {
+                clen = min(cpanel, segments - cp);
+                c = Range(cj.count, clen, warp);
+            }
         }
+        if (more) ct = tile_of(cj, c.tile);
     };
     auto fill = [&]() {
         if (!more) return;
         const bool scales = F::kW4 && plan.piece == 0;
+        const int seg = cp + c.seg;
         if (lane == 0) {
-            ring.template fill<Jobs::kPairs>(weights, ct.row, ct.n, ct.expert, cseg, shape.bytes(cseg), scales ? Scales<kGS>::kSlot : 0);
+            ring.template fill<Jobs::kPairs>(weights, ct.row, ct.n, ct.expert, seg, shape.bytes(seg), scales ? Scales<kGS>::kSlot : 0);
             if constexpr (F::kW4)
-                if (scales) Scales<kGS>::template copy<Jobs::kPairs>(scales_slot(), ring.bar, weights, ct.row, ct.expert, cseg);
+                if (scales) Scales<kGS>::template copy<Jobs::kPairs>(scales_slot(), ring.bar, weights, ct.row, ct.expert, seg);
         }
         if constexpr (F::kW4)
             if (!scales)
-                Scales<kGS>::template fill<Jobs::kPairs>(scales_slot(), ring.bar, jobs.scales(ct), ct.n, jobs.second(), cseg * 4 * kGS, row_scales,
+                Scales<kGS>::template fill<Jobs::kPairs>(scales_slot(), ring.bar, jobs.scales(ct), ct.n, jobs.second(), seg * 4 * kGS, row_scales,
                                                          plan.piece, lane);
-        cseg += ways;
-        if (cseg >= to(cp, cpanel)) settle();
+        if (--c.left == 0) {
+            settle();
+        } else if (++c.seg == clen) {
+            c.seg = 0;
+            ct = tile_of(cj, ++c.tile);
+        }
     };
     settle();
     auto fill_all = [&]() {
@@ -852,147 +848,161 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         ring.phase = 0;
     };
 
-    // The columns, with bf16 weights asked for one segment ahead, across panels and jobs.
+    // The columns, with bf16 weights asked for one segment ahead.
     uint4 col[4];
-    StagedColumns<kGS, NT> columns;
+    StagedColumns<kGS> columns;
     const uint16_t* x = nullptr;
-    int way = warp & (ways - 1);  // in the panel at hand
-    // The warp's first segment of the panels from p on, with way w in the first; `segments` or more: none.
-    auto first_from = [&](int p, int w, int panel) {
-        while (p < segments && p + w >= to(p, panel)) {
-            w = turn(w, p, panel);
-            p += panel;
-        }
-        return p < segments ? p + w : segments;
-    };
     auto load_part = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK, K - segment * F::kSegK, q, t); };
-    auto view = [&](const Job& j, int panel) { return StagedView<kGS>(smem_addr(smem) + kStagedAt, panel, jobs.staged(j)); };
-    auto begin = [&](const Job& j, const Tile& tile, int panel) {
-        if (tile.n == 0) return;
-        if constexpr (F::kW4) {
+    auto view = [&](const Job& j, int panel) { return StagedView<kGS>(smem_addr(smem) + plan.staged_at, panel, jobs.staged(j)); };
+    auto enter = [&](const Job& j, int i, int panel) {
+        const Tile tile = tile_of(j, i);
+        if constexpr (F::kW4)
             columns.set(view(j, panel), lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : 0); });
-        } else {
-            const int first = first_from(0, way, panel);
+        else
             x = jobs.x(tile, g < tile.tokens ? g : 0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) load_part(first, q);
-        }
     };
     auto stage = [&](const Job& j, int p, int panel, bool start) {
-        const int tokens = jobs.staged(j), units = (to(p, panel) - p) * tokens;  // (segment, token)
+        const int tokens = jobs.staged(j), units = min(panel, segments - p) * tokens;  // (segment, token)
         const StagedView<kGS> staged = view(j, panel);
         if (!start) __syncthreads();  // the panel before it is done with
         // four at a time, asked for together (and, at the start, before the first copies: an answer comes back behind them)
         constexpr int kAhead = 4;
 #pragma unroll 1
         for (int i0 = warp; i0 < units || (start && i0 == warp); i0 += kAhead * kMvWarps) {
-            uint2 w[kAhead][4];
+            uint4 w[kAhead][2];
             int s[kAhead], token[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int i = min(i0 + u * kMvWarps, units - 1);
-                s[u] = i / tokens;
+                const int i = i0 + u * kMvWarps;
+                if (i >= units) break;
+                s[u] = quotient(i, tokens);
                 token[u] = i - s[u] * tokens;
                 const uint16_t* from = jobs.staged_x(j, token[u]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int k = (p + s[u]) * F::kSegK + q * F::kStepK + lane * 4;
-                    w[u][q] = make_uint2(0, 0);
-                    if (k < K && i0 + u * kMvWarps < units) w[u][q] = ld_early8(from + k);
+                for (int h = 0; h < 2; ++h) {
+                    const int k = (p + s[u]) * F::kSegK + h * 256 + lane * 8;
+                    w[u][h] = make_uint4(0, 0, 0, 0);
+                    if (k < K) w[u][h] = ld_early16(from + k);
                 }
             }
             if (start && i0 == warp) fill_all();
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (i0 + u * kMvWarps < units) stage_segment<kGS>(staged, s[u], token[u], w[u], lane);
+            for (int u = 0; u < kAhead; ++u) {
+                if (i0 + u * kMvWarps >= units) break;
+                stage_segment<kGS>(staged, s[u], token[u], w[u], lane);
+            }
         }
         __syncthreads();
     };
     Job job;
     jobs.first(job);
-    Tile tile = tile_of(job);
     int panel = panel_of(job);
-    begin(job, tile, panel);
-    if constexpr (F::kW4)
+    Range range(job.count, min(panel, segments), warp);
+    auto begin = [&]() {  // bf16: the first columns of a range
+        if (range.left == 0) return;
+        enter(job, range.tile, panel);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_part(range.seg, q);
+    };
+    if constexpr (F::kW4) {
         stage(job, 0, panel, true);
-    else
+    } else {
+        begin();
         fill_all();
+    }
     int key = F::kW4 ? jobs.staged_key(job) : 0;
-    bool staged = true;  // what comes next
-    for (int buf = 0;; buf ^= 1) {
-        float acc[NT][4] = {};
-        const int order = way;  // of this warp's parts among the job's
-        for (int p = 0; p < segments; p += panel) {
-            if (F::kW4 && !staged && (panel < segments || jobs.staged_key(job) != key)) {
-                key = jobs.staged_key(job);
-                stage(job, p, panel, false);
+    for (int p = 0;;) {
+        const int len = min(panel, segments - p);
+        float* part = parts + warp * kPart + lane * 4;
+        if (F::kW4 && range.left > 0) enter(job, range.tile, panel);
+        float acc[4] = {};
+        while (range.left > 0) {
+            const bool last = range.seg + 1 == len, final = range.left == 1;
+            const int bytes = shape.bytes(p + range.seg), after = last ? 0 : range.seg + 1;
+            if (!F::kW4 && last && !final) enter(job, range.tile + 1, panel);
+            ring.wait();
+            if constexpr (F::kW4) {
+                Scales<kGS> now;
+                const uint32_t scales = scales_slot() + Scales<kGS>::skip(p + range.seg);
+                StagedColumns<kGS> here = columns.at(range.seg);
+                float sum[4] = {};
+                // of what is behind the end of the rows activations and scales are zero, codes whatever they are
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < 2 || bytes > kBox) multiply_w4<kGS>(sum, ring.slot, scales, here, now, q, lane);
+                add_scaled(acc, sum, here);
+            } else {
+                multiply_bf16(acc, ring.slot, col, bytes, lane, [&](int q) {
+                    if (!final) load_part(after, q);
+                });
             }
-            staged = false;
-            const int end = to(p, panel), then = turn(way, p, panel);
-            if (tile.n > 0) {
-                const int behind = first_from(p + panel, then, panel);
-                for (int seg = p + way; seg < end; seg += ways) {
-                    const int after = seg + ways < end ? seg + ways : behind, bytes = shape.bytes(seg);
-                    ring.wait();
-                    if constexpr (F::kW4) {
-                        Scales<kGS> now;
-                        const uint32_t scales = scales_slot() + Scales<kGS>::skip(seg);
-                        StagedColumns<kGS, NT> here = columns.at(seg - p);
-                        float sum[NT][4] = {};
-                        if (bytes == kSegment) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) multiply_w4<kGS, NT>(sum, ring.slot, scales, here, now, q, lane);
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (q * 64 < bytes) multiply_w4<kGS, NT>(sum, ring.slot, scales, here, now, q, lane);
-                        }
-                        add_scaled(acc, sum, here);
-                    } else {
-                        float(&one)[4] = acc[0];
-                        multiply_bf16(one, ring.slot, col, bytes, lane, [&](int q) { load_part(after, q); });
-                    }
-                    __syncwarp();  // all lanes have read the slot
-                    fill();
-                    ring.next();
+            __syncwarp();  // all lanes have read the slot
+            fill();
+            ring.next();
+            if (last || final) {
+                if (!ring.alive) {
+                    jobs.lost();
+                    acc[0] = acc[1] = acc[2] = acc[3] = __uint_as_float(0x7fc00000u);
                 }
+                *reinterpret_cast<float4*>(part + range.tile * kPart) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+                range.tile += last;
+                if (F::kW4 && !final) enter(job, range.tile, panel);
             }
-            way = then;
+            range.seg = after;
+            --range.left;
         }
         const Job done = job;
-        const bool end = !jobs.next(job);
+        const unsigned total = job.count * len;
+        const int p0 = p;
+        const bool whole = p + len >= segments;  // the sums are complete
+        bool end = false;
+        p += len;
+        if (whole) {
+            p = 0;
+            end = !jobs.next(job);
+        }
         if (!end) {
-            tile = tile_of(job);
             panel = panel_of(job);
-            begin(job, tile, panel);
+            range = Range(job.count, min(panel, segments - p), warp);
+            if constexpr (!F::kW4) begin();
         }
-        if (!ring.alive) {
-            jobs.lost();
-#pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = __uint_as_float(0x7fc00000u);
-        }
-        // add the parts in the order of their first segments
-        float* r = red + buf * kRed;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            *reinterpret_cast<float4*>(r + (((mine << split) + order) * NT + n) * 128 + lane * 4) =
-                make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-        __syncthreads();  // and the other buffer's readers are done before it is written again
-        constexpr int kPairs = 64 * NT;  // (pair, token) per tile
-        for (int i = threadIdx.x; i < done.count * kPairs; i += kMvThreads) {
-            const int at = i / kPairs, n = i % kPairs / 64, l = i % 64;  // l: two columns of a lane's first row
-            const int pair = pair_of_row<GS>(l >> 3), token = 8 * n + (l & 7);
-            const Tile of = jobs.tile(done, at);
-            if (pair >= of.n || token >= of.tokens) continue;
-            const float* q = r + ((at << split) * NT + n) * 128 + (l >> 1) * 4 + (l & 1);
-            float first = 0.0f, second = 0.0f;
-            for (int w = 0; w < ways; ++w) {
-                first += q[w * NT * 128];
-                second += q[w * NT * 128 + 2];
+        __syncthreads();
+        // add the parts in the order of the warps, a tile per warp
+#pragma unroll 1
+        for (int at = warp; at < done.count; at += kMvWarps) {
+            const unsigned lo = at * len, hi = lo + len;
+            float4* sum = reinterpret_cast<float4*>(sums + at * kPart + lane * 4);
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (p0 > 0) s = *sum;
+#pragma unroll 1
+            for (int w = quotient(at * kMvWarps, done.count); w < kMvWarps; ++w) {
+                const unsigned f0 = total * w / kMvWarps, f1 = total * (w + 1) / kMvWarps;
+                if (f0 >= hi) break;
+                if (f1 <= lo || f1 == f0) continue;
+                const float4 v = *reinterpret_cast<const float4*>(parts + (w + at) * kPart + lane * 4);
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
             }
-            jobs.store(of, pair, token, first, second);
+            if (whole) {
+                const Tile of = jobs.tile(done, at);
+                const int pair = pair_of_row<GS>(g), token = 2 * t;
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u)
+                    if (pair < of.n && token + u < of.tokens) jobs.store(of, pair, token + u, u ? s.y : s.x, u ? s.w : s.z);
+            } else {
+                *sum = s;
+            }
         }
         if (end) break;
+        if (F::kW4 && (panel < segments || jobs.staged_key(job) != key)) {
+            key = jobs.staged_key(job);
+            stage(job, p, panel, false);  // with a barrier before
+        } else {
+            __syncthreads();
+        }
     }
     if (!ring.alive) grace_period(10000000ull);  // copies that may still land
 }

@@ -155,7 +155,6 @@ struct GateUp {
     int eights;      // per item; 0: up to eight pairs
     int t0, t1;      // tiles
     bool together;   // all tokens are staged
-    int side;        // tiles per job, at most
     struct Job {
         int count;
         int tile;                // first
@@ -175,12 +174,11 @@ struct GateUp {
         t0 = whole ? q0 : 0;
         t1 = whole ? q1 : (q0 < q1) + (q0 / a.I < (q1 - 1) / a.I);
         together = GS == 0 || a.T <= kChunk1;
-        side = 1;
     }
-    __device__ int item_of(int tile) const { return eights ? tile / eights : q0 / a.I + tile; }
+    __device__ int item_of(int tile) const { return eights ? quotient(tile, eights) : q0 / a.I + tile; }
     __device__ void at(Job& j, int tile, bool fresh) const {
         j.tile = tile;
-        j.count = min(side, t1 - tile);
+        j.count = min(kJobTiles<GS>, t1 - tile);
         if (together) {
             j.last = 0;
             j.base = 0;
@@ -201,8 +199,6 @@ struct GateUp {
     }
     __device__ Tile tile(const Job& j, int i) const {
         Tile t;
-        t.n = t.tokens = t.row = t.expert = t.entry = t.column = 0;
-        if (i >= j.count) return t;
         const int item = item_of(j.tile + i);
         if (eights) {
             t.n = 8;
@@ -253,17 +249,17 @@ template <int GS>
 __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ Weights weights,
                                                                        const __grid_constant__ ProductPlan plan) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     const Items it(smem + plan.extra_at, a.T * a.K, a.E);
+    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, plan.slots, GS > 0 ? Scales<GS ? GS : 1>::arrivals(plan.piece) : 1,
+                   threadIdx.x & 31);
+    if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     pdl_wait();     // no global memory access before this point
     pdl_trigger();  // after it: what the second kernel reads before its own wait is complete
     build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk1);
     // (Cutting tiles to deal 13.5 pairs to each CTA instead of one or two tiles took 23.7 us instead of 18.5 for one token and 8
     // experts of 2 x 256 x 7168.)
     GateUp<GS> jobs(a, it, plan);
-    const int split = plan.ways.pick(jobs.t1 - jobs.t0, !jobs.together);
-    jobs.side = kMvWarps >> split;
-    run_product<GS, 1>(jobs, weights, smem, plan, a.H, split);
+    run_product<GS>(jobs, weights, smem, plan, a.H);
 }
 
 // ------------------------------------------------------------ second product
@@ -288,7 +284,7 @@ DownPlan plan_down(int T, int K, int E, int I) {
     p.shape = RowShape::of(Fmt<GS>::row_bytes(I));
     p.piece = GS ? Scales<GS ? GS : 1>::piece(Fmt<GS>::scales(I)) : 0;
     p.step = p.shape.row_bytes <= kBox ? kSlotBytes / 2 : kSlotBytes;
-    p.act_part = (2 * I + 255) / 256 * 256;
+    p.act_part = (2 * I + 511) / 512 * 512;
     for (int option = GS ? 0 : 3;; ++option) {
         // two buffers of sums, so that a tile's may be added while the next tile's are made, where that leaves room
         p.buffers = option % 3 == 0 && T <= 24 ? 2 : 1;
@@ -315,17 +311,18 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     const Items it(smem + plan.items_at, a.T * a.K, a.E);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     pdl_trigger();
-    if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     const uint32_t act_bar = smem_addr(smem) + (kMvWarps * kMaxSlots + warp) * 8;
     if constexpr (STAGED) {
         if (lane == 0) mbar_init(act_bar, 1);
-        // zeros between the values and the next 256 bytes
+        // zeros behind the values, to the end of two steps
         const int pad = (plan.act_part - 2 * a.I) >> 4;
         for (int i = threadIdx.x; i < a.T * a.K * 2 * pad; i += kMvThreads) {
             const int row = i / pad, at = plan.act_at + (row >> 1) * plan.act_entry + (row & 1) * plan.act_part + 2 * a.I + (i - row * pad) * 16;
             *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
         }
     }
+    SlotRing::init(smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, F::kW4 ? Scales<kGS>::arrivals(plan.piece) : 1, lane);
+    if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     // Before the wait: ids, weights and expert weights.  The first kernel starts
     // nothing before its own wait, so everything ahead of it has completed; it
     // writes the activations alone.
@@ -337,9 +334,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     const int row_scales = F::scales(a.I), segments = shape.segments;
     const int total = it.count() * segments;
     const int f0 = total * warp / kMvWarps, f1 = total * (warp + 1) / kMvWarps;  // total <= 2^18
-    const int item0 = f0 / segments, seg0 = f0 - item0 * segments;
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * plan.step, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, plan.step,
-                  F::kW4 ? Scales<kGS>::arrivals(plan.piece) : 1, lane);
+    const int item0 = quotient(f0, segments), seg0 = f0 - item0 * segments;
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * plan.step, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, plan.step);
     const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
     auto scales_slot = [&]() { return ring.beside(ring_scales, Scales<kGS>::kSlot); };
 
@@ -446,7 +442,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                 ReadyColumns<kGS> columns{staged + seg * (F::kSegK * 2)};
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (q * 64 < bytes) multiply_w4<kGS, 1>(acc, ring.slot, scales, columns, now, q, lane);
+                    if (q < 2 || bytes > kBox) multiply_w4<kGS>(acc[0], ring.slot, scales, columns, now, q, lane);
                 if (last && !final) enter(item + 1);
             } else if constexpr (F::kW4) {
                 Scales<kGS> now;
@@ -459,7 +455,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                         if (end && !final && last) enter(item + 1);
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            multiply_w4<kGS, 1>(acc, ring.slot, scales, direct[q], now, 2 * box + q, lane);
+                            multiply_w4<kGS>(acc[0], ring.slot, scales, direct[q], now, 2 * box + q, lane);
                             if (!end)
                                 load_part(seg, 2 + q);
                             else if (!final)
@@ -533,12 +529,14 @@ cudaError_t launch(Kernel kernel, const ExpertsArgs& a, const Weights& weights, 
 template <int GS>
 cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
     const int tokens = a.T < kChunk1 ? a.T : kChunk1;
+    const int64_t pairs = (int64_t)a.T * a.K * a.I;
+    const int most = (int)((pairs / 8 + num_sms - 1) / num_sms), tiles = most > 2 ? most : 2;
     Weights w13{}, w2{};
     cudaError_t e = describe_weights(&w13, {a.w13, a.s13, (int64_t)a.E * 2 * a.I, Fmt<GS>::row_bytes(a.H), Fmt<GS>::scales(a.H), GS, a.I, 0});
     if (e == cudaSuccess)
         e = describe_weights(&w2, {a.w2, a.s2, (int64_t)a.E * a.H, Fmt<GS>::row_bytes(a.I), Fmt<GS>::scales(a.I), GS, 0, a.H / num_sms});
     if (e != cudaSuccess) return e;
-    e = launch(moe_gate_up_kernel<GS>, a, w13, plan_product<GS, 1>(a.H, tokens, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
+    e = launch(moe_gate_up_kernel<GS>, a, w13, plan_product<GS>(a.H, tokens, tiles, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
     if (e != cudaSuccess) return e;
     const DownPlan plan = plan_down<GS>(a.T, a.K, a.E, a.I);
     if (GS > 0 && plan.act_entry > 0) return launch(moe_down_kernel<GS, (GS > 0)>, a, w2, plan, num_sms, stream, true);
