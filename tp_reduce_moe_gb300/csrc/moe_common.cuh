@@ -133,7 +133,7 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ int warp_index() { return uniform((int)(threadIdx.x >> 5)); }
 
-// a / b for 0 <= a <= 2^23, 0 < b, a / b < 2^20: in floating point off by one at most.
+// a / b for 0 <= a <= 2^24, 0 < b, a / b < 2^20: in floating point off by one at most.
 __device__ __forceinline__ int quotient(int a, int b) {
     int q = (int)__fdividef((float)a, (float)b);
     q -= q * b > a;
@@ -195,11 +195,11 @@ struct RowShape {
     __device__ __forceinline__ int bytes(int segment) const { return min(kSegment, row_bytes - segment * kSegment); }
 };
 
-// A range of `total` things dealt evenly over the grid, whole ones to each CTA.
+// A range of `total` things (up to 2^24, 2^20 a CTA) dealt evenly over the grid, whole ones to each CTA.
 struct Share {
     int first, last;
     __device__ __forceinline__ Share(unsigned total) {
-        const unsigned each = total / gridDim.x, rest = total - each * gridDim.x, b = blockIdx.x;
+        const unsigned each = quotient(total, gridDim.x), rest = total - each * gridDim.x, b = blockIdx.x;
         first = b * each + min(b, rest);
         last = first + each + (b < rest);
     }
@@ -706,6 +706,7 @@ struct ProductPlan {
     int slots;    // per warp
     int extra_at, ring_at, scales_at, smem;
     int piece;  // of the scales' copies
+    int chunk;  // tokens per item, at most
 };
 template <int GS>
 inline ProductPlan plan_product(int K, int tokens, int tiles, int extra) {  // tiles: of a CTA, at most
@@ -976,15 +977,18 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (p0 > 0) s = *sum;
 #pragma unroll 1
-            for (int w = quotient(at * kMvWarps, done.count); w < kMvWarps; ++w) {
-                const unsigned f0 = total * w / kMvWarps, f1 = total * (w + 1) / kMvWarps;
-                if (f0 >= hi) break;
-                if (f1 <= lo || f1 == f0) continue;
-                const float4 v = *reinterpret_cast<const float4*>(parts + (w + at) * kPart + lane * 4);
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
+            for (int w0 = quotient(at * kMvWarps, done.count); w0 < kMvWarps && total * w0 / kMvWarps < hi; w0 += 4) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const unsigned w = w0 + u, f0 = total * w / kMvWarps, f1 = total * (w + 1) / kMvWarps;
+                    if (f0 < hi && f1 > lo && f1 > f0 && w < kMvWarps) {
+                        const float4 v = *reinterpret_cast<const float4*>(parts + (w + at) * kPart + lane * 4);
+                        s.x += v.x;
+                        s.y += v.y;
+                        s.z += v.z;
+                        s.w += v.w;
+                    }
+                }
             }
             if (whole) {
                 const Tile of = jobs.tile(done, at);

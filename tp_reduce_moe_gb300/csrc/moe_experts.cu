@@ -20,8 +20,12 @@
 namespace arf {
 namespace {
 
-constexpr int kChunk1 = 8;  // tokens per item of the first kernel
-constexpr int kChunk2 = 4;  // and of the second
+// Tokens per item of the first kernel (a power of two), and of the second.  Items
+// of up to four leave the activations of whole rows in shared memory; more tokens
+// of an expert take its rows out of L2 again, which is the less the fewer experts
+// have so many.
+int chunk_first(int T, int K, int E) { return T <= 8 || T * K > 4 * E ? 8 : 4; }
+constexpr int kChunk2 = 4;
 
 // The chosen experts, in order, each with the tokens that chose it, in order,
 // cut into items of up to `chunk` tokens.  In shared memory, for `slots` = T * K
@@ -77,20 +81,35 @@ __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsA
         __syncthreads();
         return;
     }
+    // a thread's slots, and their weights, asked for together
+    constexpr int kMine = kMoeMaxTokens * kMaxTopK / kMvThreads;
     const int slots = a.T * a.K;
+    int mine[kMine];
+    float weight[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int s = tid + i * kMvThreads;
+        mine[i] = s < slots ? a.ids[s] : -1;
+        weight[i] = s < slots ? a.weights[s] : 0.0f;
+    }
+    int* twice = it.part + 2 * kMvWarps;  // some token names an expert twice; later the number of items
+    if (tid == 0) *twice = 0;
     for (int e = tid; e < a.E; e += kMvThreads) mask[e][0] = mask[e][1] = 0;
     __syncthreads();
-    for (int s = tid; s < slots; s += kMvThreads) {
-        const int e = a.ids[s], t = s / a.K;
-        if ((unsigned)e < (unsigned)a.E)
-            atomicOr(&mask[e][t >> 5], 1u << (t & 31));
-        else if (e != -1)
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int e = mine[i], t = quotient(tid + i * kMvThreads, a.K);
+        if ((unsigned)e < (unsigned)a.E) {
+            if (atomicOr(&mask[e][t >> 5], 1u << (t & 31)) >> (t & 31) & 1) *twice = 1;
+        } else if (e != -1) {
             atomicOr(a.err, kErrExpertRange);
+        }
     }
     __syncthreads();
+    const bool dedupe = *twice != 0;
     static_assert(kMoeMaxExperts <= kMvThreads, "one expert per thread");
     const int n = tid < a.E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
-    const int m = (n + chunk - 1) / chunk;
+    const int m = (n + chunk - 1) >> (chunk == 8 ? 3 : 2);
     int ni = m, ne = n;  // inclusive sums over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -119,15 +138,20 @@ __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsA
         }
     }
     __syncthreads();
-    for (int s = tid; s < slots; s += kMvThreads) {
-        const int e = a.ids[s], t = s / a.K, k = s % a.K;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int s = tid + i * kMvThreads, e = mine[i];
         if ((unsigned)e >= (unsigned)a.E) continue;
-        bool first = true;
-        for (int j = 0; j < k; ++j) first = first && a.ids[t * a.K + j] != e;
-        if (!first) continue;
-        float w = a.weights[s];
-        for (int j = k + 1; j < a.K; ++j)
-            if (a.ids[t * a.K + j] == e) w += a.weights[t * a.K + j];
+        const int t = quotient(s, a.K);
+        float w = weight[i];
+        if (dedupe) {
+            const int k = s - t * a.K;
+            bool first = true;
+            for (int j = 0; j < k; ++j) first = first && a.ids[t * a.K + j] != e;
+            if (!first) continue;
+            for (int j = k + 1; j < a.K; ++j)
+                if (a.ids[t * a.K + j] == e) w += a.weights[t * a.K + j];
+        }
         const uint32_t low = mask[e][0], high = mask[e][1];
         const int before = t < 32 ? __popc(low & ((1u << t) - 1)) : __popc(low) + __popc(high & ((1u << (t - 32)) - 1));
         it.slot[it.at[e] + before] = s;
@@ -152,7 +176,8 @@ struct GateUp {
     const Items& it;
     const ProductPlan& plan;
     int q0, q1;      // pairs
-    int eights;      // per item; 0: up to eight pairs
+    int eights;      // per item; 0: up to eight pairs, from this item on:
+    int item0;
     int t0, t1;      // tiles
     bool together;   // all tokens are staged
     struct Job {
@@ -172,10 +197,11 @@ struct GateUp {
         q0 = share.first;
         q1 = share.last;
         t0 = whole ? q0 : 0;
-        t1 = whole ? q1 : (q0 < q1) + (q0 / a.I < (q1 - 1) / a.I);
-        together = GS == 0 || a.T <= kChunk1;
+        item0 = whole ? 0 : quotient(q0, a.I);
+        t1 = whole ? q1 : (q0 < q1) + (q1 > (item0 + 1) * a.I);
+        together = GS == 0 || a.T <= 8;
     }
-    __device__ int item_of(int tile) const { return eights ? quotient(tile, eights) : q0 / a.I + tile; }
+    __device__ int item_of(int tile) const { return eights ? quotient(tile, eights) : item0 + tile; }
     __device__ void at(Job& j, int tile, bool fresh) const {
         j.tile = tile;
         j.count = min(kJobTiles<GS>, t1 - tile);
@@ -191,11 +217,11 @@ struct GateUp {
             j.tokens = it.n[item];
             for (j.last = item; j.last < end; ++j.last) {
                 const int n = j.tokens + it.n[j.last + 1];
-                if (n > kChunk1 || plan.panel[n] < plan.shape.segments) break;
+                if (n > plan.chunk || plan.panel[n] < plan.shape.segments) break;
                 j.tokens = n;
             }
         }
-        j.count = min(j.count, (eights ? (j.last + 1) * eights : j.last + 1 - q0 / a.I) - tile);
+        j.count = min(j.count, (eights ? (j.last + 1) * eights : j.last + 1 - item0) - tile);
     }
     __device__ Tile tile(const Job& j, int i) const {
         Tile t;
@@ -255,7 +281,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
     if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     pdl_wait();     // no global memory access before this point
     pdl_trigger();  // after it: what the second kernel reads before its own wait is complete
-    build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk1);
+    build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, plan.chunk);
     // (Cutting tiles to deal 13.5 pairs to each CTA instead of one or two tiles took 23.7 us instead of 18.5 for one token and 8
     // experts of 2 x 256 x 7168.)
     GateUp<GS> jobs(a, it, plan);
@@ -274,11 +300,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
 // 2048) where the products take 1.
 struct DownPlan {
     RowShape shape;
-    int buffers, items_at, ring_at, scales_at, slots, step, smem, piece;
+    int round, items_at, ring_at, scales_at, slots, step, smem, piece;
     int act_at, act_entry, act_part;  // staged activations: at, bytes of an entry and of its high parts (0: not staged)
 };
 template <int GS>
-DownPlan plan_down(int T, int K, int E, int I) {
+DownPlan plan_down(int T, int K, int E, int I, int tiles) {  // tiles: of a CTA, at most
     DownPlan p;
     constexpr int kScales = GS ? Scales<GS ? GS : 1>::kSlot : 0;
     p.shape = RowShape::of(Fmt<GS>::row_bytes(I));
@@ -286,11 +312,12 @@ DownPlan plan_down(int T, int K, int E, int I) {
     p.step = p.shape.row_bytes <= kBox ? kSlotBytes / 2 : kSlotBytes;
     p.act_part = (2 * I + 511) / 512 * 512;
     for (int option = GS ? 0 : 3;; ++option) {
-        // two buffers of sums, so that a tile's may be added while the next tile's are made, where that leaves room
-        p.buffers = option % 3 == 0 && T <= 24 ? 2 : 1;
+        // sums of a round of tiles: all of them (one barrier in all) where that takes up to 48 KB, else as many as fit there
+        const int most = 48 * 1024 / (kMvWarps * T * 64);
+        p.round = option % 3 == 2 || most < 1 ? 1 : tiles < most ? tiles : most;
         // staged: entries 64 bytes off a multiple of 128 (no bank conflicts), or not
         p.act_entry = option >= 3 ? 0 : 2 * p.act_part + (option < 2 ? 64 : 0);
-        p.items_at = (kMaxSlots + 1) * kMvWarps * 8 + p.buffers * kMvWarps * T * 64;
+        p.items_at = (kMaxSlots + 1) * kMvWarps * 8 + p.round * kMvWarps * T * 64;
         p.ring_at = (p.items_at + Items::bytes(T * K, E) + 1023) / 1024 * 1024;
         const int slots = (kSmemLimit - p.ring_at - T * K * p.act_entry) / (kMvWarps * (p.step + kScales));
         p.slots = slots < kMaxSlots ? slots : kMaxSlots;
@@ -307,7 +334,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     using F = Fmt<GS>;
     constexpr int kGS = GS ? GS : 1;
     extern __shared__ __align__(1024) uint8_t smem[];
-    float* sums = reinterpret_cast<float*>(smem + kMvWarps * (kMaxSlots + 1) * 8);  // [buffer][warp][T][16]
+    float* sums = reinterpret_cast<float*>(smem + kMvWarps * (kMaxSlots + 1) * 8);  // [tile of the round][warp][T][16]
     const Items it(smem + plan.items_at, a.T * a.K, a.E);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     pdl_trigger();
@@ -393,11 +420,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         if (!mbar_sleep(act_bar, 0)) ring.alive = wait_long(act_bar, 0);
     }
 
-    for (int row = r0, buf = 0; row < r1; row += 16, buf ^= plan.buffers - 1) {
+    for (int row = r0, in_round = 0; row < r1; row += 16) {
         const int rows = min(16, r1 - row);
-        if (plan.buffers == 1 && row > r0) __syncthreads();  // the sums are added
-        float* all = sums + buf * kMvWarps * a.T * 16;
-        float* mine = all + warp * a.T * 16;
+        const int round_sums = kMvWarps * a.T * 16;
+        float* mine = sums + in_round * round_sums + warp * a.T * 16;
         for (int i = lane; i < a.T * 16; i += 32) mine[i] = 0.0f;
         __syncwarp();
         // the next segment's operands
@@ -499,14 +525,20 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             atomicOr(a.err, kErrTimeout);
             for (int i = lane; i < a.T * 16; i += 32) mine[i] = __uint_as_float(0x7fc00000u);
         }
-        __syncthreads();  // and the other buffer's readers are done before it is written again
-        for (int i = threadIdx.x; i < a.T * 16; i += kMvThreads) {
-            if ((i & 15) >= rows) continue;
+        if (++in_round < plan.round && row + 16 < r1) continue;
+        __syncthreads();
+        const int from = row - 16 * (in_round - 1);  // the round's rows, in the order (tile, token, row)
+        for (int i = threadIdx.x; i < in_round * a.T * 16; i += kMvThreads) {
+            const int tile = quotient(i >> 4, a.T), token = (i >> 4) - tile * a.T, at = from + 16 * tile + (i & 15);
+            if (at >= r1) continue;
+            const float* all = sums + tile * round_sums + token * 16 + (i & 15);
             float y = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kMvWarps; ++w) y += all[w * a.T * 16 + i];
-            a.out[(int64_t)(i >> 4) * a.H + row + (i & 15)] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+            for (int w = 0; w < kMvWarps; ++w) y += all[w * a.T * 16];
+            a.out[(int64_t)token * a.H + at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
         }
+        in_round = 0;
+        if (row + 16 < r1) __syncthreads();  // the sums are added
     }
     if (!ring.alive) grace_period(10000000ull);  // copies that may still land
 }
@@ -528,7 +560,7 @@ cudaError_t launch(Kernel kernel, const ExpertsArgs& a, const Weights& weights, 
 
 template <int GS>
 cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
-    const int tokens = a.T < kChunk1 ? a.T : kChunk1;
+    const int chunk = chunk_first(a.T, a.K, a.E), tokens = a.T < chunk ? a.T : chunk;
     const int64_t pairs = (int64_t)a.T * a.K * a.I;
     const int most = (int)((pairs / 8 + num_sms - 1) / num_sms), tiles = most > 2 ? most : 2;
     Weights w13{}, w2{};
@@ -536,9 +568,11 @@ cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, 
     if (e == cudaSuccess)
         e = describe_weights(&w2, {a.w2, a.s2, (int64_t)a.E * a.H, Fmt<GS>::row_bytes(a.I), Fmt<GS>::scales(a.I), GS, 0, a.H / num_sms});
     if (e != cudaSuccess) return e;
-    e = launch(moe_gate_up_kernel<GS>, a, w13, plan_product<GS>(a.H, tokens, tiles, Items::bytes(a.T * a.K, a.E)), num_sms, stream, pdl);
+    ProductPlan first = plan_product<GS>(a.H, tokens, tiles, Items::bytes(a.T * a.K, a.E));
+    first.chunk = chunk;
+    e = launch(moe_gate_up_kernel<GS>, a, w13, first, num_sms, stream, pdl);
     if (e != cudaSuccess) return e;
-    const DownPlan plan = plan_down<GS>(a.T, a.K, a.E, a.I);
+    const DownPlan plan = plan_down<GS>(a.T, a.K, a.E, a.I, ((a.H + num_sms - 1) / num_sms + 15) / 16);
     if (GS > 0 && plan.act_entry > 0) return launch(moe_down_kernel<GS, (GS > 0)>, a, w2, plan, num_sms, stream, true);
     return launch(moe_down_kernel<GS, false>, a, w2, plan, num_sms, stream, true);
 }
