@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_c
     extern __shared__ __align__(1024) uint8_t smem[];
     SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, plan.slots, Scales<GS>::arrivals(plan.piece), threadIdx.x & 31);
     if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, plan.piece == 0);
+    pdl_wait();  // no global memory access before this point
+    pdl_trigger();
     const Share rows(a.N);
     Matvec<GS> jobs{a, rows.first, rows.last, 0, 8};
     jobs.block = 16 * kJobTiles<GS>;
@@ -101,6 +103,12 @@ cudaError_t launch(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
     cfg.blockDim = dim3(kMvThreads);
     cfg.dynamicSmemBytes = (size_t)plan.smem;
     cfg.stream = stream;
+    // always: it only moves the launch and the barriers' initialisation under the end of the kernel before
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, matvec_w4_kernel<GS>, a, weights, plan);
 }
 
