@@ -95,7 +95,7 @@ template <int GS>
 cudaError_t launch(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
     Weights weights{};
     const int grid = a.N < num_sms ? a.N : num_sms;
-    const ProductPlan plan = plan_product<GS>(a.K, a.T, ((a.N + grid - 1) / grid + 15) / 16, 0);
+    const ProductPlan plan = plan_product<GS>(a.K, a.T < 8 ? a.T : 8, 8, ((a.N + grid - 1) / grid + 15) / 16, 0);
     const cudaError_t e = describe_weights(&weights, {a.q, a.s, a.N, Fmt<GS>::row_bytes(a.K), Fmt<GS>::scales(a.K), GS, 0, a.N / grid});
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -699,17 +699,19 @@ constexpr int kJobTiles = GS ? 32 : JT;
 constexpr int kSmemLimit = 227 * 1024;
 struct ProductPlan {
     RowShape shape;
-    uint8_t panel[9];   // segments whose activations are staged at a time, by the number of staged tokens
+    uint8_t panel[9];  // segments whose activations are staged at a time, by the number of staged tokens
     int staged;         // bytes
     int sums_at, staged_at;
+    int pairs;          // of columns that a tile has at most
     int extra;    // bytes, at extra_at
     int slots;    // per warp
     int extra_at, ring_at, scales_at, smem;
     int piece;  // of the scales' copies
     int chunk;  // tokens per item, at most
 };
+// tokens: staged for a tile, at most; columns: staged at a time where whole rows of so many fit; tiles: of a CTA, at most
 template <int GS>
-inline ProductPlan plan_product(int K, int tokens, int tiles, int extra) {  // tiles: of a CTA, at most
+inline ProductPlan plan_product(int K, int tokens, int columns, int tiles, int extra) {
     ProductPlan p;
     p.shape = RowShape::of(Fmt<GS>::row_bytes(K));
     const int segments = p.shape.segments;
@@ -717,22 +719,27 @@ inline ProductPlan plan_product(int K, int tokens, int tiles, int extra) {  // t
     p.piece = GS ? Scales<GS ? GS : 1>::piece(Fmt<GS>::scales(K)) : 0;
     p.extra = extra;
     tiles = tiles < kJobTiles<GS> ? tiles : kJobTiles<GS>;
-    p.sums_at = kMvWarps * kMaxSlots * 8 + (tiles + kMvWarps) * 512;
+    p.pairs = ((tokens < 8 ? tokens : 8) + 1) / 2;
+    p.sums_at = kMvWarps * kMaxSlots * 8 + (tiles + kMvWarps) * p.pairs * 128;
     p.staged_at = p.sums_at;
     int fixed = p.staged_at + extra;
     using View = StagedView<GS ? GS : 1>;
     // at least two slots per warp
     auto room = [&](int n) { return (kSmemLimit - fixed - kMaxSlots * kMvWarps * kSlot - 1024 - View::bytes(0, n)) / (View::bytes(1, n) - View::bytes(0, n)); };
-    const int columns = tokens < 8 ? tokens : 8;
-    if (GS > 0 && room(columns) < segments) {
-        p.staged_at += tiles * 512;
-        fixed += tiles * 512;
+    if (GS > 0 && room(tokens) < segments) {
+        p.staged_at += tiles * p.pairs * 128;
+        fixed += tiles * p.pairs * 128;
     }
     p.staged = 0;
     for (int n = 0; n <= 8; ++n) {
         p.panel[n] = (uint8_t)segments;  // at most 128
-        if (GS == 0 || n == 0 || n > columns) continue;
-        const int most = room(n), panels = (segments + most - 1) / most;
+        if (GS == 0 || n == 0) continue;
+        const int most = room(n);
+        if (n > tokens && (n > columns || most < segments)) {
+            p.panel[n] = 0;
+            continue;
+        }
+        const int panels = (segments + most - 1) / most;
         p.panel[n] = (uint8_t)((segments + panels - 1) / panels);
         const int bytes = (View::bytes(p.panel[n], n) + 15) / 16 * 16;
         p.staged = bytes > p.staged ? bytes : p.staged;
@@ -767,12 +774,13 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     using Job = typename Jobs::Job;
     using Tile = typename Jobs::Tile;
     constexpr int kGS = GS ? GS : 1;
-    constexpr int kPart = 128;  // floats
     float* parts = reinterpret_cast<float*>(smem + kMvWarps * kMaxSlots * 8);
     float* sums = reinterpret_cast<float*>(smem + plan.sums_at);
     const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, t = lane & 3;
     const RowShape& shape = plan.shape;
     const int row_scales = F::scales(K), segments = shape.segments;
+    const int part_size = plan.pairs * 32, in_part = (g * plan.pairs + t) * 4;  // floats
+    const bool in_use = t < plan.pairs;
     SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, kSlotBytes);
     const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
     auto scales_slot = [&]() { return ring.beside(ring_scales, Scales<kGS>::kSlot); };
@@ -914,7 +922,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     int key = F::kW4 ? jobs.staged_key(job) : 0;
     for (int p = 0;;) {
         const int len = min(panel, segments - p);
-        float* part = parts + warp * kPart + lane * 4;
+        float* part = parts + warp * part_size + in_part;
         if (F::kW4 && range.left > 0) enter(job, range.tile, panel);
         float acc[4] = {};
         while (range.left > 0) {
@@ -945,7 +953,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                     jobs.lost();
                     acc[0] = acc[1] = acc[2] = acc[3] = __uint_as_float(0x7fc00000u);
                 }
-                *reinterpret_cast<float4*>(part + range.tile * kPart) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                if (in_use) *reinterpret_cast<float4*>(part + range.tile * part_size) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                 acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
                 range.tile += last;
                 if (F::kW4 && !final) enter(job, range.tile, panel);
@@ -973,8 +981,9 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
 #pragma unroll 1
         for (int at = warp; at < done.count; at += kMvWarps) {
             const unsigned lo = at * len, hi = lo + len;
-            float4* sum = reinterpret_cast<float4*>(sums + at * kPart + lane * 4);
+            float4* sum = reinterpret_cast<float4*>(sums + at * part_size + in_part);
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (!in_use) continue;
             if (p0 > 0) s = *sum;
 #pragma unroll 1
             for (int w0 = quotient(at * kMvWarps, done.count); w0 < kMvWarps && total * w0 / kMvWarps < hi; w0 += 4) {
@@ -982,7 +991,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                 for (int u = 0; u < 4; ++u) {
                     const unsigned w = w0 + u, f0 = total * w / kMvWarps, f1 = total * (w + 1) / kMvWarps;
                     if (f0 < hi && f1 > lo && f1 > f0 && w < kMvWarps) {
-                        const float4 v = *reinterpret_cast<const float4*>(parts + (w + at) * kPart + lane * 4);
+                        const float4 v = *reinterpret_cast<const float4*>(parts + (w + at) * part_size + in_part);
                         s.x += v.x;
                         s.y += v.y;
                         s.z += v.z;

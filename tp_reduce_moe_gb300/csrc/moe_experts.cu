@@ -20,11 +20,13 @@
 namespace arf {
 namespace {
 
-// Tokens per item of the first kernel (a power of two), and of the second.  Items
-// of up to four leave the activations of whole rows in shared memory; more tokens
-// of an expert take its rows out of L2 again, which is the less the fewer experts
-// have so many.
-int chunk_first(int T, int K, int E) { return T <= 8 || T * K > 4 * E ? 8 : 4; }
+// Tokens per item of the first kernel (a power of two), and of the second.  The
+// activations of the items that a CTA meets stay in shared memory if they are few
+// (four of 7168 values); an expert's tokens beyond an item's take its rows out of
+// L2 again.  So: small items where experts have few tokens on average.  (16 tokens
+// with 8 of 256 experts: the first kernel's last CTA ended after 59 us with items
+// of eight, CHUNK4 with four, CHUNK2 with two.)
+int chunk_first(int T, int K, int E) { return T <= 8 || T * K > 4 * E ? 8 : T * K > E ? 4 : 2; }
 constexpr int kChunk2 = 4;
 
 // The chosen experts, in order, each with the tokens that chose it, in order,
@@ -109,7 +111,7 @@ __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsA
     const bool dedupe = *twice != 0;
     static_assert(kMoeMaxExperts <= kMvThreads, "one expert per thread");
     const int n = tid < a.E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
-    const int m = (n + chunk - 1) >> (chunk == 8 ? 3 : 2);
+    const int m = (n + chunk - 1) >> (chunk == 8 ? 3 : chunk == 4 ? 2 : 1);
     int ni = m, ne = n;  // inclusive sums over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -217,7 +219,7 @@ struct GateUp {
             j.tokens = it.n[item];
             for (j.last = item; j.last < end; ++j.last) {
                 const int n = j.tokens + it.n[j.last + 1];
-                if (n > plan.chunk || plan.panel[n] < plan.shape.segments) break;
+                if (n > 8 || plan.panel[n] < plan.shape.segments) break;
                 j.tokens = n;
             }
         }
@@ -568,7 +570,7 @@ cudaError_t launch_both(const ExpertsArgs& a, int num_sms, cudaStream_t stream, 
     if (e == cudaSuccess)
         e = describe_weights(&w2, {a.w2, a.s2, (int64_t)a.E * a.H, Fmt<GS>::row_bytes(a.I), Fmt<GS>::scales(a.I), GS, 0, a.H / num_sms});
     if (e != cudaSuccess) return e;
-    ProductPlan first = plan_product<GS>(a.H, tokens, tiles, Items::bytes(a.T * a.K, a.E));
+    ProductPlan first = plan_product<GS>(a.H, tokens, a.T < 8 ? a.T : 8, tiles, Items::bytes(a.T * a.K, a.E));
     first.chunk = chunk;
     e = launch(moe_gate_up_kernel<GS>, a, w13, first, num_sms, stream, pdl);
     if (e != cudaSuccess) return e;
