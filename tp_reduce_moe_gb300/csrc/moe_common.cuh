@@ -567,7 +567,7 @@ struct Scales {
     static constexpr int kHalf = 4 * GS;                     // bytes of a lane's half row
     static constexpr int kPitch = GS == 1 ? 16 : 2 * kHalf;  // between rows
     static constexpr int kSlot = 16 * kPitch;                // bytes beside a slot
-    static constexpr int kWords = GS == 2 ? 4 : 2;
+    static constexpr int kWords = GS == 2 ? 1 : 2;           // of a row: all (one group a step), or a step's
     uint32_t raw[2][kWords];
     // 0: a tensor copy
     __host__ static int piece(int row_scales) { return row_scales % 8 == 0 ? 0 : row_scales * 2 % kHalf == 0 ? kHalf : row_scales % 2 == 0 ? 4 : 2; }
@@ -619,13 +619,13 @@ struct Scales {
     }
     // The lane's two rows, at `at`: of step q.
     __device__ __forceinline__ void read(uint32_t at, int q) {
-        if (GS < 4 && q > 0) return;  // all at once
+        if (GS == 1 && q > 0) return;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) lds(raw[h], at + h * 8 * kPitch + (GS == 4 ? q * 8 : 0));
+        for (int h = 0; h < 2; ++h) lds(raw[h], at + h * 8 * kPitch + (GS == 1 ? 0 : q * 2 * GS));
     }
     // Scale of group s of step q for the lane's row.
     __device__ __forceinline__ float get(int h, int q, int s) const {
-        const int i = GS < 4 ? q * GS + s : s;
+        const int i = GS == 1 ? q : s;
         const uint32_t w = raw[h][i / 2];
         return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
     }
@@ -687,11 +687,10 @@ __device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&sum)[4
 // in the order of the warps, once a job.  (Tiles side by side and their segments
 // dealt to powers of two of warps left a seventh of the warps idle, or took a
 // round with two barriers for every few tiles, 1.8 us each.)
-#ifndef JT
-#define JT 32
-#endif
 template <int GS>
-constexpr int kJobTiles = GS ? 32 : JT;
+constexpr int kJobTiles = GS ? 32 : 8;
+template <int GS>
+constexpr int kPartBuffers = GS ? 1 : 2;
 
 // Shared memory of a product: barriers, parts of tiles (warp w's of tile i at i + w:
 // ranges are in order), with several panels the sums over those done, staged activations, `extra` bytes, the
@@ -703,6 +702,7 @@ struct ProductPlan {
     int staged;         // bytes
     int sums_at, staged_at;
     int pairs;          // of columns that a tile has at most
+    int tiles;          // of a job, at most
     int extra;    // bytes, at extra_at
     int slots;    // per warp
     int extra_at, ring_at, scales_at, smem;
@@ -720,7 +720,8 @@ inline ProductPlan plan_product(int K, int tokens, int columns, int tiles, int e
     p.extra = extra;
     tiles = tiles < kJobTiles<GS> ? tiles : kJobTiles<GS>;
     p.pairs = ((tokens < 8 ? tokens : 8) + 1) / 2;
-    p.sums_at = kMvWarps * kMaxSlots * 8 + (tiles + kMvWarps) * p.pairs * 128;
+    p.sums_at = kMvWarps * kMaxSlots * 8 + kPartBuffers<GS> * (tiles + kMvWarps) * p.pairs * 128;
+    p.tiles = tiles;
     p.staged_at = p.sums_at;
     int fixed = p.staged_at + extra;
     using View = StagedView<GS ? GS : 1>;
@@ -920,9 +921,9 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         fill_all();
     }
     int key = F::kW4 ? jobs.staged_key(job) : 0;
-    for (int p = 0;;) {
+    for (int p = 0, buffer = 0;;) {
         const int len = min(panel, segments - p);
-        float* part = parts + warp * part_size + in_part;
+        float* part = parts + (buffer + warp) * part_size + in_part;
         if (F::kW4 && range.left > 0) enter(job, range.tile, panel);
         float acc[4] = {};
         while (range.left > 0) {
@@ -991,7 +992,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                 for (int u = 0; u < 4; ++u) {
                     const unsigned w = w0 + u, f0 = total * w / kMvWarps, f1 = total * (w + 1) / kMvWarps;
                     if (f0 < hi && f1 > lo && f1 > f0 && w < kMvWarps) {
-                        const float4 v = *reinterpret_cast<const float4*>(parts + (w + at) * part_size + in_part);
+                        const float4 v = *reinterpret_cast<const float4*>(parts + (buffer + w + at) * part_size + in_part);
                         s.x += v.x;
                         s.y += v.y;
                         s.z += v.z;
@@ -1013,9 +1014,10 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         if (F::kW4 && (panel < segments || jobs.staged_key(job) != key)) {
             key = jobs.staged_key(job);
             stage(job, p, panel, false);  // with a barrier before
-        } else {
+        } else if (F::kW4) {
             __syncthreads();
         }
+        if (!F::kW4) buffer = buffer ? 0 : plan.tiles + kMvWarps;  // (the other one has been read before the barrier above)
     }
     if (!ring.alive) grace_period(10000000ull);  // copies that may still land
 }
