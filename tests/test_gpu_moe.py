@@ -357,6 +357,68 @@ def test_matvec_w4_infinite_scale_stays_in_its_row():
     assert not bool(torch.isfinite(after[:, 31]).any())
 
 
+# Shapes that take every way through the products: jobs of several rounds, activations that do not fit in one piece,
+# groups of items, rows whose scales are copied in pieces of 16, 8, 4 and 2 bytes, last tiles of every height.
+MORE_EXPERTS = [  # T, H, E, K, I
+    (64, 256, 64, 4, 1024), (3, 64, 160, 10, 520),
+]
+MORE_W4 = [  # T, H, E, K, I, group
+    (8, 16384, 4, 2, 64, 32), (16, 7168, 2, 2, 64, 64), (20, 7168, 16, 2, 64, 32), (12, 4096, 64, 4, 64, 32),
+    (64, 256, 64, 4, 1024, 32), (40, 256, 16, 8, 1024, 64), (10, 192, 24, 4, 192, 32), (7, 768, 6, 3, 256, 64),
+    (50, 1280, 60, 6, 256, 128), (1, 8192, 4, 4, 32, 32),
+]
+MORE_MATVECS = [  # T, N, K, group
+    (3, 80000, 64, 32), (9, 80001, 64, 32), (1, 2888, 96, 32), (2, 3496, 4096, 64), (1, 4256, 224, 32), (4, 100, 256, 64),
+    (2, 2900, 768, 64), (2, 33, 320, 64), (6, 3500, 1024, 128), (8, 300, 24576, 32), (12, 170, 7168, 64),
+]
+
+
+@pytest.mark.parametrize("T,H,E,K,I", MORE_EXPERTS)
+def test_experts_more(T, H, E, K, I):
+    test_experts(T, H, E, K, I)
+
+
+@pytest.mark.parametrize("T,H,E,K,I,group", MORE_W4)
+def test_experts_w4_more(T, H, E, K, I, group):
+    test_experts_w4(T, H, E, K, I, group)
+
+
+@pytest.mark.parametrize("T,N,K,group", MORE_MATVECS)
+def test_matvec_w4_more(T, N, K, group):
+    g = gen(T + N + K)
+    x = normal((T, K), g)
+    q, s = _moe.make_w4((N,), K, group, g, DEV)
+    W = _moe.w4_values(q, s)
+    y, m = x.double() @ W.t(), x.double().abs() @ W.abs().t()
+    f, ok = guarded((T, N), torch.float32)
+    arf.ar_matvec_w4(x, q, s, group, out=f, out_fp32=True)
+    torch.cuda.synchronize()
+    assert bool(((f.double() - y).abs() <= _moe.gamma(K) * m + 2.0 ** -24 * y.abs()).all())
+    assert ok()
+    assert torch.equal(arf.ar_matvec_w4(x, q, s, group), f.bfloat16())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_matvec_w4_range_of_activations(group):
+    """Activations are scaled by powers of two inside, exactly, up to 2^101; beyond that a token's results are undefined."""
+    g = gen(group)
+    T, N, K = 5, 90, 1152
+    x = normal((T, K), g)
+    q, s = _moe.make_w4((N,), K, group, g, DEV)
+    y = arf.ar_matvec_w4(x, q, s, group, out_fp32=True)
+    for power in (-80, -30, 60, 95):
+        z = arf.ar_matvec_w4((x.float() * 2.0 ** power).bfloat16(), q, s, group, out_fp32=True)
+        assert torch.equal(z.double(), y.double() * 2.0 ** power), power
+    assert bool((arf.ar_matvec_w4(torch.zeros_like(x), q, s, group) == 0).all())
+    for value in (float("nan"), float("inf"), -float("inf"), 2.0 ** 101):
+        bad = x.clone()
+        bad[3, K - 1] = value
+        z = arf.ar_matvec_w4(bad, q, s, group, out_fp32=True)
+        assert bool(torch.isnan(z[3]).all())
+        keep = [0, 1, 2, 4]
+        assert torch.equal(z[keep], y[keep])
+
+
 # ------------------------------------------------------------------ together
 def layer_step(m, ws, layer, x, gate, bias, residual, gamma, bufs, stream=None):
     ids, w, y, out, res = bufs
@@ -431,6 +493,43 @@ def test_layer_eager_and_captured(T, group, flags):
     assert arf.ar_moe_device_error(m) == 0
     m.destroy()
     ws.destroy()
+
+
+def test_products_captured_with_forks_and_copies():
+    """4-bit products captured behind a kernel, a copy, a fork and a join, replayed on new inputs."""
+    T, N, K, group = 3, 700, 512, 64
+    g = gen(41)
+    q, s = _moe.make_w4((N,), K, group, g, DEV)
+    W = _moe.w4_values(q, s)
+    x, y = normal((T, K), g), torch.empty(T, K, dtype=torch.bfloat16, device=DEV)
+    outs = [torch.empty(T, N, device=DEV) for _ in range(5)]
+
+    def chain(main, side):
+        y.copy_(x)                                                        # a copy before
+        arf.ar_matvec_w4(y, q, s, group, out=outs[0], out_fp32=True)
+        y.neg_()                                                          # a kernel before
+        arf.ar_matvec_w4(y, q, s, group, out=outs[1], out_fp32=True)
+        side.wait_stream(main)                                            # first on a forked stream
+        arf.ar_matvec_w4(y, q, s, group, out=outs[2], out_fp32=True, stream=side)
+        arf.ar_matvec_w4(x, q, s, group, out=outs[3], out_fp32=True)      # beside it
+        main.wait_stream(side)                                            # behind both
+        arf.ar_matvec_w4(x, q, s, group, out=outs[4], out_fp32=True)
+
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        chain(main, side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        chain(main, side)
+    for _ in range(4):
+        x.copy_(normal((T, K), g))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, m = x.double() @ W.t(), x.double().abs() @ W.abs().t()
+        for i, sign in enumerate((1, -1, -1, 1, 1)):
+            assert bool(((outs[i].double() - sign * ref).abs() <= _moe.gamma(K) * m + 2.0 ** -24 * ref.abs()).all()), i
 
 
 def test_two_handles_on_two_streams():

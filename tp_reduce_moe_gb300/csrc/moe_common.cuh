@@ -111,7 +111,8 @@ __device__ __forceinline__ void lds(uint32_t (&v)[WORDS], uint32_t a) {
     if constexpr (WORDS == 4)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
 }
-// 16 bytes that this grid's predecessor wrote (not the read-only path).
+// 16 bytes that an earlier grid wrote, perhaps one that still ran when this one
+// began: not the read-only path, which need not see that.
 __device__ __forceinline__ uint4 ld_coherent16(const void* p) {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
@@ -119,7 +120,7 @@ __device__ __forceinline__ uint4 ld_coherent16(const void* p) {
 }
 __device__ __forceinline__ uint32_t ld_u16(const uint16_t* p) {
     uint16_t v;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -330,11 +331,10 @@ struct SlotRing {
 // registers.  A column that does not exist may repeat one that does.
 //
 // Part q of a segment: chunk 2t + q % 2 of box q / 2.
-template <bool COHERENT>
 __device__ __forceinline__ uint4 load_column(const uint16_t* p, int left, int q, int t) {
     const int at = 64 * (q >> 1) + 16 * t + 8 * (q & 1);
     if (at >= left) return make_uint4(0, 0, 0, 0);
-    return COHERENT ? ld_coherent16(p + at) : ld_early16(p + at);
+    return ld_coherent16(p + at);
 }
 
 // acc += (tile) * (columns), one segment of `bytes` bytes at `slot`.  load(q)
@@ -862,7 +862,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     uint4 col[4];
     StagedColumns<kGS> columns;
     const uint16_t* x = nullptr;
-    auto load_part = [&](int segment, int q) { col[q] = load_column<false>(x + segment * F::kSegK, K - segment * F::kSegK, q, t); };
+    auto load_part = [&](int segment, int q) { col[q] = load_column(x + segment * F::kSegK, K - segment * F::kSegK, q, t); };
     auto view = [&](const Job& j, int panel) { return StagedView<kGS>(smem_addr(smem) + plan.staged_at, panel, jobs.staged(j)); };
     auto enter = [&](const Job& j, int i, int panel) {
         const Tile tile = tile_of(j, i);
@@ -892,7 +892,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                 for (int h = 0; h < 2; ++h) {
                     const int k = (p + s[u]) * F::kSegK + h * 256 + lane * 8;
                     w[u][h] = make_uint4(0, 0, 0, 0);
-                    if (k < K) w[u][h] = ld_early16(from + k);
+                    if (k < K) w[u][h] = ld_coherent16(from + k);
                 }
             }
             if (start && i0 == warp) fill_all();

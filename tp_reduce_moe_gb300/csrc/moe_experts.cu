@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             if constexpr (F::kW4)
                 direct[q & 1].load(act + at + q * F::kStepK, a.I - at - q * F::kStepK, t);
             else
-                col[q] = load_column<true>(act + at, a.I - at, q, t);
+                col[q] = load_column(act + at, a.I - at, q, t);
         };
         int item = item0, seg = seg0;
         if (f0 < f1) {

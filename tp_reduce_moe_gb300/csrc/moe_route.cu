@@ -161,7 +161,7 @@ __device__ bool choose32(const RouteArgs& a, int token, int lane, unsigned* keys
 #pragma unroll 8
     for (int e = lane; e < a.E; e += 32) {
         const float v = __ldcg(l + e).x;
-        biases[e] = a.bias ? __ldg(a.bias + e) : 0.0f;
+        biases[e] = a.bias ? a.bias[e] : 0.0f;
         fine = fine && fabsf(v) < INFINITY;
         top = fmaxf(top, v);
         big = fmaxf(big, fabsf(v));
@@ -384,11 +384,11 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
         for (int u = 0; u < kAhead; ++u) {
             const int c = c0 + u * kRouteThreads;
             wv[u] = make_uint4(0, 0, 0, 0);
-            if (c < chunks) wv[u] = ld_early16_stream(row + c * 8);
+            if (c < chunks) wv[u] = ld_coherent16(row + c * 8);
 #pragma unroll
             for (int j = 0; j < TOKENS; ++j) {
                 xv[u][j] = make_uint4(0, 0, 0, 0);
-                if (c < chunks && j < nt) xv[u][j] = ld_early16(a.x + (int64_t)(t0 + j) * a.H + c * 8);
+                if (c < chunks && j < nt) xv[u][j] = ld_coherent16(a.x + (int64_t)(t0 + j) * a.H + c * 8);
             }
         }
 #pragma unroll
