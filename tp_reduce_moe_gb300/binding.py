@@ -351,8 +351,11 @@ def _ptr_array(ts):
 
 def _stream_handle(stream, device) -> int:
     if stream is None:
+        index = device if isinstance(device, int) else getattr(device, "index", None)
+        if index is None:
+            return torch.cuda.current_stream(device).cuda_stream
         # the handle alone: a Stream object costs a microsecond, a tenth of a small call
-        return torch._C._cuda_getCurrentRawStream(device)
+        return torch._C._cuda_getCurrentRawStream(index)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
