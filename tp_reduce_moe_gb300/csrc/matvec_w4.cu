@@ -81,7 +81,7 @@ struct Matvec {
 template <int GS>
 __global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__ Weights weights, const __grid_constant__ ProductPlan plan) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, plan.slots, Scales<GS>::arrivals(plan.piece), threadIdx.x & 31);
+    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, kMaxSlots, Scales<GS>::arrivals(plan.piece), threadIdx.x & 31);
     if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, plan.piece == 0);
     pdl_wait();  // no global memory access before this point
     pdl_trigger();

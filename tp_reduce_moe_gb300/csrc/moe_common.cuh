@@ -264,13 +264,14 @@ static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase) {
 
 struct SlotRing {
     uint32_t slots, bars;  // shared addresses
-    uint32_t slot, bar;    // the next
-    int n, step;           // slots, bytes between them
-    uint32_t phase;
-    bool alive;  // no wait has run out
+    int two, step;         // whether there are two slots (else one), bytes between them
+    uint32_t at;           // the next: counts fillings, later readings
+    bool alive;            // no wait has run out
 
     __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int step)
-        : slots(slots), bars(bars), slot(slots), bar(bars), n(n), step(step), phase(0), alive(true) {}
+        : slots(slots), bars(bars), two(n == 2), step(step), at(0), alive(true) {}
+    __device__ __forceinline__ uint32_t slot() const { return slots + (at & two) * step; }
+    __device__ __forceinline__ uint32_t bar() const { return bars + (at & two) * 8; }
     // The warp's barriers, before anything else; arrivals: of each, for each filling.
     __device__ static __forceinline__ void init(uint32_t bars, int n, int arrivals, int lane) {
         if (lane < n) mbar_init(bars + lane * 8, arrivals);
@@ -283,6 +284,7 @@ struct SlotRing {
     template <bool PAIRS>
     __device__ __forceinline__ void fill(const Weights& w, int row, int n, int expert, int seg, int bytes, int more) {
         const int x = seg * kSegment;
+        const uint32_t slot = this->slot(), bar = this->bar();
         if (PAIRS || n > 8) {
             const bool wide = bytes > kBox;
             mbar_arrive_expect_tx(bar, (wide ? 4 * kBoxBytes : 2 * kBoxBytes) + more);
@@ -309,19 +311,12 @@ struct SlotRing {
     // Waits for the next slot.  A wait that runs out (nothing but a lost copy
     // makes it) ends the waiting for good.
     __device__ __forceinline__ void wait() {
-        if (!mbar_sleep(bar, phase) && alive) alive = wait_long(bar, phase);
+        const uint32_t phase = at >> two & 1;
+        if (!mbar_sleep(bar(), phase) && alive) alive = wait_long(bar(), phase);
     }
     // Where what comes with the slot lies, `bytes` bytes a slot.
-    __device__ __forceinline__ uint32_t beside(uint32_t first, int bytes) const { return first + (bar - bars) / 8 * bytes; }
-    __device__ __forceinline__ void next() {
-        slot += step;
-        bar += 8;
-        if (bar == bars + n * 8) {
-            slot = slots;
-            bar = bars;
-            phase ^= 1;
-        }
-    }
+    __device__ __forceinline__ uint32_t beside(uint32_t first, int bytes) const { return first + (at & two) * bytes; }
+    __device__ __forceinline__ void next() { ++at; }
 };
 
 // ------------------------------------------------------------ products, bf16
@@ -704,7 +699,6 @@ struct ProductPlan {
     int pairs;          // of columns that a tile has at most
     int tiles;          // of a job, at most
     int extra;    // bytes, at extra_at
-    int slots;    // per warp
     int extra_at, ring_at, scales_at, smem;
     int piece;  // of the scales' copies
     int chunk;  // tokens per item, at most
@@ -725,7 +719,6 @@ inline ProductPlan plan_product(int K, int tokens, int columns, int tiles, int e
     p.staged_at = p.sums_at;
     int fixed = p.staged_at + extra;
     using View = StagedView<GS ? GS : 1>;
-    // at least two slots per warp
     auto room = [&](int n) { return (kSmemLimit - fixed - kMaxSlots * kMvWarps * kSlot - 1024 - View::bytes(0, n)) / (View::bytes(1, n) - View::bytes(0, n)); };
     if (GS > 0 && room(tokens) < segments) {
         p.staged_at += tiles * p.pairs * 128;
@@ -747,10 +740,8 @@ inline ProductPlan plan_product(int K, int tokens, int columns, int tiles, int e
     }
     p.extra_at = p.staged_at + p.staged;
     p.ring_at = (p.extra_at + extra + 1023) / 1024 * 1024;
-    const int slots = (kSmemLimit - p.ring_at) / (kMvWarps * kSlot);
-    p.slots = slots < kMaxSlots ? slots : kMaxSlots;
-    p.scales_at = p.ring_at + p.slots * kMvWarps * kSlotBytes;
-    p.smem = p.scales_at + p.slots * kMvWarps * kScales;
+    p.scales_at = p.ring_at + kMaxSlots * kMvWarps * kSlotBytes;
+    p.smem = p.scales_at + kMaxSlots * kMvWarps * kScales;
     return p;
 }
 
@@ -782,8 +773,8 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     const int row_scales = F::scales(K), segments = shape.segments;
     const int part_size = plan.pairs * 32, in_part = (g * plan.pairs + t) * 4;  // floats
     const bool in_use = t < plan.pairs;
-    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * plan.slots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, kSlotBytes);
-    const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * plan.slots * Scales<kGS>::kSlot;
+    SlotRing ring(smem_addr(smem) + plan.ring_at + warp * kMaxSlots * kSlotBytes, smem_addr(smem) + warp * kMaxSlots * 8, kMaxSlots, kSlotBytes);
+    const uint32_t ring_scales = smem_addr(smem) + plan.scales_at + warp * kMaxSlots * Scales<kGS>::kSlot;
     auto scales_slot = [&]() { return ring.beside(ring_scales, Scales<kGS>::kSlot); };
 
     auto panel_of = [&](const Job& j) { return uniform(F::kW4 ? (int)plan.panel[jobs.staged(j)] : segments); };
@@ -836,11 +827,11 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         if (lane == 0) {
             ring.template fill<Jobs::kPairs>(weights, ct.row, ct.n, ct.expert, seg, shape.bytes(seg), scales ? Scales<kGS>::kSlot : 0);
             if constexpr (F::kW4)
-                if (scales) Scales<kGS>::template copy<Jobs::kPairs>(scales_slot(), ring.bar, weights, ct.row, ct.expert, seg);
+                if (scales) Scales<kGS>::template copy<Jobs::kPairs>(scales_slot(), ring.bar(), weights, ct.row, ct.expert, seg);
         }
         if constexpr (F::kW4)
             if (!scales)
-                Scales<kGS>::template fill<Jobs::kPairs>(scales_slot(), ring.bar, jobs.scales(ct), ct.n, jobs.second(), seg * 4 * kGS, row_scales,
+                Scales<kGS>::template fill<Jobs::kPairs>(scales_slot(), ring.bar(), jobs.scales(ct), ct.n, jobs.second(), seg * 4 * kGS, row_scales,
                                                          plan.piece, lane);
         if (--c.left == 0) {
             settle();
@@ -851,11 +842,11 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     };
     settle();
     auto fill_all = [&]() {
-        for (int s = 0; s < plan.slots; ++s) {
+        for (int s = 0; s < kMaxSlots; ++s) {
             fill();
             ring.next();
         }
-        ring.phase = 0;
+        ring.at = 0;
     };
 
     // The columns, with bf16 weights asked for one segment ahead.
@@ -939,10 +930,10 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
                 // of what is behind the end of the rows activations and scales are zero, codes whatever they are
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (q < 2 || bytes > kBox) multiply_w4<kGS>(sum, ring.slot, scales, here, now, q, lane);
+                    if (q < 2 || bytes > kBox) multiply_w4<kGS>(sum, ring.slot(), scales, here, now, q, lane);
                 add_scaled(acc, sum, here);
             } else {
-                multiply_bf16(acc, ring.slot, col, bytes, lane, [&](int q) {
+                multiply_bf16(acc, ring.slot(), col, bytes, lane, [&](int q) {
                     if (!final) load_part(after, q);
                 });
             }

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
                                                                        const __grid_constant__ ProductPlan plan) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const Items it(smem + plan.extra_at, a.T * a.K, a.E);
-    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, plan.slots, GS > 0 ? Scales<GS ? GS : 1>::arrivals(plan.piece) : 1,
+    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, kMaxSlots, GS > 0 ? Scales<GS ? GS : 1>::arrivals(plan.piece) : 1,
                    threadIdx.x & 31);
     if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     pdl_wait();     // no global memory access before this point
@@ -380,11 +380,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         if (lane == 0) {
             ring.fill<false>(weights, cfirst, rows, 0, cseg, shape.bytes(cseg), scales ? Scales<kGS>::kSlot : 0);
             if constexpr (F::kW4)
-                if (scales) Scales<kGS>::template copy<false>(scales_slot(), ring.bar, weights, cfirst, 0, cseg);
+                if (scales) Scales<kGS>::template copy<false>(scales_slot(), ring.bar(), weights, cfirst, 0, cseg);
         }
         if constexpr (F::kW4)
             if (!scales)
-                Scales<kGS>::template fill<false>(scales_slot(), ring.bar, a.s2 + (int64_t)cfirst * row_scales, rows, 8, cseg * 4 * kGS, row_scales,
+                Scales<kGS>::template fill<false>(scales_slot(), ring.bar(), a.s2 + (int64_t)cfirst * row_scales, rows, 8, cseg * 4 * kGS, row_scales,
                                                   plan.piece, lane);
         if (++cf == f1) {
             cf = f0;
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         fill();
         ring.next();
     }
-    ring.phase = 0;
+    ring.at = 0;
     pdl_wait();  // the activations
     if constexpr (STAGED) {
         // the warp's: of every item a range of its columns, lane = (entry, part)
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                 ReadyColumns<kGS> columns{staged + seg * (F::kSegK * 2)};
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (q < 2 || bytes > kBox) multiply_w4<kGS>(acc[0], ring.slot, scales, columns, now, q, lane);
+                    if (q < 2 || bytes > kBox) multiply_w4<kGS>(acc[0], ring.slot(), scales, columns, now, q, lane);
                 if (last && !final) enter(item + 1);
             } else if constexpr (F::kW4) {
                 Scales<kGS> now;
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                         if (end && !final && last) enter(item + 1);
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            multiply_w4<kGS>(acc[0], ring.slot, scales, direct[q], now, 2 * box + q, lane);
+                            multiply_w4<kGS>(acc[0], ring.slot(), scales, direct[q], now, 2 * box + q, lane);
                             if (!end)
                                 load_part(seg, 2 + q);
                             else if (!final)
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
                     }
             } else {
                 if (last && !final) enter(item + 1);
-                multiply_bf16(acc[0], ring.slot, col, bytes, lane, [&](int q) {
+                multiply_bf16(acc[0], ring.slot(), col, bytes, lane, [&](int q) {
                     if (!final) load_part(after, q);
                 });
             }
