@@ -544,7 +544,9 @@ ARFUSE_API ar_status ar_moe_create(int device, int experts, int shared, int top_
 /* Free the handle.  NULL is accepted.  No call using it may still be running. */
 ARFUSE_API ar_status ar_moe_destroy(ar_moe* moe);
 
-/* Read and clear the handle's error word, as ar_workspace_device_error. */
+/* Read and clear the handle's error word, as ar_workspace_device_error
+ * (AR_DEVERR_EXPERT_RANGE; AR_DEVERR_TIMEOUT: a bounded wait for a copy ran out,
+ * that call's results are NaN). */
 ARFUSE_API ar_status ar_moe_device_error(ar_moe* moe, int* code);
 
 /*
@@ -592,7 +594,9 @@ ARFUSE_API ar_status ar_moe_route(ar_moe* moe, const void* x, const void* gate, 
  *   w2       device bf16 [E + S, H, I]
  *   out      device bf16 [T, H]; a token without experts gets zeros
  * Sums are fp32 and `out` is the only rounding (the activations between the
- * products keep 16 bits).  Deterministic for given sizes, ids and GPU.
+ * products keep 16 bits).  Deterministic for given sizes, ids and GPU; the
+ * order of a sum may depend on the batch.  Two launches; weights are described
+ * to the copy engine anew by every call, nothing of a call is kept.
  * T == 0 returns AR_OK.  Errors as for ar_moe_route, and AR_ERR_UNSUPPORTED
  * for a handle with inter = 0; every matrix, x and out 16-byte aligned.
  */
@@ -604,7 +608,10 @@ ARFUSE_API ar_status ar_moe_experts(ar_moe* moe, const void* x, const int32_t* i
  * ar_moe_experts with 4-bit weights: q13 [E + S, 2 I, H / 2] with s13
  * [E + S, 2 I, H / group], q2 [E + S, H, I / 2] with s2 [E + S, H, I / group].
  * A group other than 32, 64 or 128, or one that does not divide H and I, is
- * AR_ERR_UNSUPPORTED.
+ * AR_ERR_UNSUPPORTED.  Products are formed at a common power of two: a token
+ * with an |x| of 2^101 or more, an infinity or a NaN gets NaN; the activations
+ * between the products keep their 16 bits from 2^-56 to 2^63 (below that
+ * fewer, above that they are infinite).
  */
 ARFUSE_API ar_status ar_moe_experts_w4(ar_moe* moe, const void* x, const int32_t* ids,
                                        const float* weights, const void* q13, const void* s13,
@@ -614,12 +621,16 @@ ARFUSE_API ar_status ar_moe_experts_w4(ar_moe* moe, const void* x, const int32_t
 /*
  * out[t] = W x[t] with a 4-bit matrix W [N, K]; needs no handle and allocates
  * nothing (the first call on a device sets kernel attributes: make it outside
- * any stream capture).  Runs on the current device.
+ * any stream capture).  Runs on the current device.  The launch may begin under
+ * the end of the kernel before it on the stream (programmatic dependent launch);
+ * it reads and writes nothing before that kernel has completed.
  *   x      device bf16 [T, K]
  *   q, s   device: codes [N, K / 2] and bf16 scales [N, K / group]
  *   T      0 .. AR_MAX_MOE_TOKENS (0 returns AR_OK)
  *   N, K   1 .. AR_MAX_MATVEC_ROWS, group .. AR_MAX_MATVEC_COLS
  *   out    device [T, N], bf16 or (out_is_fp32 = 1) fp32
+ * A token with an |x| of 2^101 or more, an infinity or a NaN gets NaN.  Sums are
+ * fp32; deterministic, but their order may depend on T.
  * Errors: AR_ERR_INVALID_ARG (NULL, negative sizes, overlap of out with an
  * input, out_is_fp32 not 0 or 1), AR_ERR_ALIGNMENT (x, q, s, out 16 bytes),
  * AR_ERR_UNSUPPORTED (group, sizes), AR_ERR_CAPACITY (T), AR_ERR_CUDA.

@@ -6,16 +6,20 @@
 // and use it a handful of times, so the time is the weights' bytes over the
 // memory bandwidth.  One CTA per SM holds sixteen warps; each warp streams its
 // own share of the weights through a private ring in shared memory, filled by
-// tensor copies (TMA) of eight rows by 128 bytes, and multiplies them with
+// tensor copies (TMA) of sixteen rows by 256 bytes, and multiplies them with
 // mma.sync, weight rows as the 16-row operand and tokens as the 8-column one.
 // (Tried before: cp.async from the same warps, 5.9 TB/s and ten instructions per
 // KB, and plain loads issued behind it return behind it; bulk copies of single
-// 256-byte row segments, 7 TB/s but issued lane by lane, 14 instructions each.)
+// 256-byte row segments, 7 TB/s but issued lane by lane, 14 instructions each;
+// tensor copies of eight rows by 128 bytes, four times as many to issue.)
 // A kilobyte of weights takes the memory 44 cycles to deliver to an SM; the
-// matrix instructions for it take 4 (bf16) to 16 (4-bit), so that what counts is
-// the instructions around them.  A tcgen05 tile of 128 rows would need all its
-// operands in shared memory, the 4-bit codes expanded there first, and pay in
-// granularity: at one token an SM owns about 27 rows of the first product.
+// matrix instructions for it take 4 (bf16) to 16 (4-bit) on each of its four
+// schedulers, and taking the codes out as long again, so that what counts is the
+// instructions: bf16 weights come at the memory's rate, 4-bit ones at 55 to 80 %
+// of it (half the issue slots busy, half the integer pipe).  A tcgen05 tile of
+// 128 rows would need all its operands in shared memory, the 4-bit codes expanded
+// there first, and pay in granularity: at one token an SM owns about 27 rows of
+// the first product.
 #pragma once
 
 #include <cuda.h>
@@ -158,8 +162,8 @@ __host__ __device__ constexpr int pair_of_row(int g) {
 // A ring slot holds a segment of a tile: of its first 128 bytes the eight first
 // rows, then the eight second ones; then the same of the next 128 bytes; swizzled
 // by the copy: the 16-byte chunk c of row g lies at place c ^ g of the row's
-// eight.  All of it is one tensor copy (four copies of eight rows by 128 bytes
-// took 0.4 us of a warp's 1.4 us per segment to issue).  What lies behind the end
+// eight.  All of it is one tensor copy (with four copies of eight rows by 128
+// bytes 36864 rows of 7168 4-bit weights took 29.9 instead of 25.6 us).  What lies behind the end
 // of the rows is zero in 128 bytes that begin before it; 128 bytes that begin
 // behind it are not copied.  Rows that are not the tile's may be copied and are
 // not used.  Every slot has its mbarrier; the warp that fills it is the one that

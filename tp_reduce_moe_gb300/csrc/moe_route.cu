@@ -14,6 +14,11 @@
 // formed and compared in 32 bits where the gaps between the chosen are wider than
 // what 32 bits can get wrong, else (one token in some thousands) in 64 bits,
 // whose rate on this GPU is 1/64 of that; the weights of the chosen always are.
+//
+// Bound by latency: the gate is read in a microsecond or two, and the choice is
+// one warp's chain of top_k + groups reductions.  One token of 256 experts in
+// groups takes 11.7 us, 16 tokens 16.8, 64 tokens (bound by the two-sums, eight
+// operations a product) 23.3.
 #include "moe_common.cuh"
 
 namespace arf {
