@@ -200,13 +200,13 @@ struct RowShape {
     __device__ __forceinline__ int bytes(int segment) const { return min(kSegment, row_bytes - segment * kSegment); }
 };
 
-// A range of `total` things (up to 2^24, 2^20 a CTA) dealt evenly over the grid, whole ones to each CTA.
+// The `index`-th of `parts` ranges of `total` things (up to 2^24, 2^20 a part), dealt evenly, whole ones to each.
 struct Share {
     int first, last;
-    __device__ __forceinline__ Share(unsigned total) {
-        const unsigned each = quotient(total, gridDim.x), rest = total - each * gridDim.x, b = blockIdx.x;
-        first = b * each + min(b, rest);
-        last = first + each + (b < rest);
+    __device__ __forceinline__ Share(unsigned total, unsigned parts, unsigned index) {
+        const unsigned each = quotient(total, parts), rest = total - each * parts;
+        first = index * each + min(index, rest);
+        last = first + each + (index < rest);
     }
 };
 
@@ -862,7 +862,8 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
     auto enter = [&](const Job& j, int i, int panel) {
         const Tile tile = tile_of(j, i);
         if constexpr (F::kW4)
-            columns.set(view(j, panel), lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : 0); });
+            // a column that does not exist repeats one of its parity: neighbours meet other banks
+            columns.set(view(j, panel), lane, [&](int i) { return jobs.column(tile, i < tile.tokens ? i : min(i & 1, tile.tokens - 1)); });
         else
             x = jobs.x(tile, g < tile.tokens ? g : 0);
     };

@@ -197,7 +197,7 @@ struct GateUp {
     __device__ GateUp(const ExpertsArgs& a, const Items& it, const ProductPlan& plan) : a(a), it(it), plan(plan) {
         const int pairs = it.count() * a.I;  // at most 2^24
         const bool whole = pairs >= 8 * (int)gridDim.x;
-        const Share share(whole ? pairs >> 3 : pairs);
+        const Share share(whole ? pairs >> 3 : pairs, gridDim.x, blockIdx.x);
         eights = whole ? a.I >> 3 : 0;
         q0 = share.first;
         q1 = share.last;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
     // writes the activations alone.
     build_items(it, reinterpret_cast<uint32_t(*)[2]>(smem + plan.ring_at), a, kChunk2);
 
-    const Share share(a.H);
+    const Share share(a.H, gridDim.x, blockIdx.x);
     const int r0 = share.first, r1 = share.last;
     const RowShape& shape = plan.shape;
     const int row_scales = F::scales(a.I), segments = shape.segments;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         uint32_t staged = 0;
         const int pair = pair_of_row<GS>(g);
         auto enter = [&](int item) {
-            const int e = (g & 3) < it.n[item] ? g & 3 : 0;
+            const int e = (g & 3) < it.n[item] ? g & 3 : min(g & 1, it.n[item] - 1);
             if constexpr (STAGED)
                 staged = smem_addr(smem) + plan.act_at + (it.off[item] + e) * plan.act_entry + (g >> 2) * plan.act_part + t * 16;
             else
