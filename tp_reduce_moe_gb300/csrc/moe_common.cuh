@@ -705,7 +705,8 @@ struct ProductPlan {
     int extra;    // bytes, at extra_at
     int extra_at, ring_at, scales_at, smem;
     int piece;  // of the scales' copies
-    int chunk;  // tokens per item, at most
+    int chunk = 8;          // tokens per item, at most
+    bool together = false;  // all tokens are staged
 };
 // tokens: staged for a tile, at most; columns: staged at a time where whole rows of so many fit; tiles: of a CTA, at most
 template <int GS>
