@@ -30,6 +30,7 @@ namespace arf {
 
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;  // routed + shared
+constexpr int kMoeMaxGroups = 32;
 constexpr int kMoeMaxSlots = kMoeMaxTokens * kMaxTopK;
 constexpr unsigned kErrExpertRange = 0x4u;
 

@@ -143,9 +143,10 @@ __device__ __noinline__ void store_choice(const RouteArgs& a, int token, int lan
     }
 }
 
-// One warp: the choice for one token in 32 bits.  Lane l holds experts l, l +
-// 32, ...  False if some gap that decides is too narrow, or something is not a
-// number: nothing is written then.
+// The choice in 32 bits, for every token of the CTA at once: 1 << kShift tokens, the
+// CTA's warps dealt to them evenly, warp `part` of a token's first.  What the
+// tokens' warps tell each other goes through Part; False in `good` if some gap
+// that decides is too narrow, or something is not a number: nothing is chosen then.
 //
 // What the difference of two choice values c = s + b may be off by, relative to
 // |c| + 2 max|b| (no less than either score): a sigmoid's logit is rounded to 32
@@ -156,51 +157,83 @@ __device__ __noinline__ void store_choice(const RouteArgs& a, int token, int lan
 //
 // Loops, not unrolled code: one SM runs this once, and an instruction that has to
 // be fetched costs it more than the instruction (unrolled over sixteen registers
-// it took 20 us for one token).
-__device__ bool choose32(const RouteArgs& a, int token, int lane, unsigned* keys /* shared, [E] */, float* biases /* the same */,
-                         Chosen& chosen) {
+// it took 20 us for one token).  One warp per token took 6.5 us for 256 experts,
+// all warps of the CTA take CHOICE.
+struct Part {
+    unsigned top, big, bias;  // largest logit, magnitudes (ordered; bits)
+    float total;
+    int fine;
+};
+struct Group {
+    unsigned key;
+    float reach;
+};
+template <int TOKENS>
+__device__ void choose32(const RouteArgs& a, int token, bool live, int part, int lane, unsigned* keys /* shared, [E] */,
+                         float* biases /* the same */, Part* parts /* shared, one per warp of the token */, Group* groups /* shared */,
+                         unsigned* kept_groups /* shared */, Chosen& chosen, int* good /* shared */) {
+    constexpr int kParts = kRouteWarps / TOKENS, kStep = kParts * 32;
     const float2* l = a.logits + (int64_t)token * a.E;
     const bool by_logit = a.bias == nullptr && a.n_group == 1;
-    float top = -INFINITY, big = 0.0f, bias = 0.0f, total = 0.0f;
-    bool fine = true;
-#pragma unroll 8
-    for (int e = lane; e < a.E; e += 32) {
+    const int e0 = part * 32 + lane, E = live ? a.E : 0;
+    Part mine{0u, 0u, 0u, 0.0f, 1};
+#pragma unroll 4
+    for (int e = e0; e < E; e += kStep) {
         const float v = __ldcg(l + e).x;
         biases[e] = a.bias ? a.bias[e] : 0.0f;
-        fine = fine && fabsf(v) < INFINITY;
-        top = fmaxf(top, v);
-        big = fmaxf(big, fabsf(v));
+        mine.fine = mine.fine && fabsf(v) < INFINITY;
+        mine.top = max(mine.top, ordered32(v));
+        mine.big = max(mine.big, __float_as_uint(fabsf(v)));
         keys[e] = by_logit ? ordered32(v) : __float_as_uint(v);
     }
-    top = from_ordered32(__reduce_max_sync(0xffffffffu, ordered32(top)));
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    mine.top = __reduce_max_sync(0xffffffffu, mine.top);
+    mine.big = __reduce_max_sync(0xffffffffu, mine.big);
+    float top = 0.0f;
+    if (!a.sigmoid && !by_logit) {  // exponentials are of differences from the largest logit
+        if (lane == 0) parts[part] = mine;
+        __syncthreads();
+        unsigned all = 0u;
+        for (int w = 0; w < kParts; ++w) all = max(all, parts[w].top);
+        top = from_ordered32(all);
+        __syncthreads();
+    }
     if (!by_logit) {
 #pragma unroll 1
-        for (int e = lane; e < a.E; e += 32) {
-            const float v = __uint_as_float(keys[e]), x = expf(a.sigmoid ? -v : v - top), s = a.sigmoid ? 1.0f / (1.0f + x) : x;
-            total += s;
-            keys[e] = __float_as_uint(s);
+        for (int e = e0; e < E; e += kStep) {
+            const float v = __uint_as_float(keys[e]), x = expf(a.sigmoid ? -v : v - top), s = a.sigmoid ? 1.0f / (1.0f + x) : x, b = biases[e];
+            mine.total += s;
+            mine.fine = mine.fine && b == b && b < INFINITY;
+            if (fabsf(b) < INFINITY) mine.bias = max(mine.bias, __float_as_uint(fabsf(b)));
+            keys[e] = a.sigmoid ? ordered32(s + b) : __float_as_uint(s);
         }
-        const float scale = a.sigmoid ? 1.0f : 1.0f / warp_sum(total);
-#pragma unroll 1
-        for (int e = lane; e < a.E; e += 32) {
-            const float b = biases[e];
-            fine = fine && b == b && b < INFINITY;
-            if (fabsf(b) < INFINITY) bias = fmaxf(bias, fabsf(b));
-            keys[e] = ordered32(__uint_as_float(keys[e]) * scale + b);
-        }
-        bias = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bias)));
+        mine.bias = __reduce_max_sync(0xffffffffu, mine.bias);
+        mine.total = warp_sum(mine.total);
     }
-    if (!__all_sync(0xffffffffu, fine)) return false;
-    const float wide = by_logit ? 0x1p-22f : (a.sigmoid ? 0x1p-18f : 0x1p-16f) * fmaxf(1.0f, big * 0.125f);
-    if (a.n_group > 1) {
-        __syncwarp();
-        // a group's two best, group by group
-        const int size = a.E / a.n_group;
-        unsigned mine = 0u, kept = 0u, last = 0u;
-        float reach = 0.0f;
+    mine.fine = __all_sync(0xffffffffu, mine.fine);
+    if (lane == 0) parts[part] = mine;
+    __syncthreads();
+    Part all = parts[0];
+    for (int w = 1; w < kParts; ++w) {
+        const Part p = parts[w];
+        all.top = max(all.top, p.top);
+        all.big = max(all.big, p.big);
+        all.bias = max(all.bias, p.bias);
+        all.total += p.total;
+        all.fine = all.fine && p.fine;
+    }
+    const float bias = __uint_as_float(all.bias);
+    const float wide = by_logit ? 0x1p-22f : (a.sigmoid ? 0x1p-18f : 0x1p-16f) * fmaxf(1.0f, __uint_as_float(all.big) * 0.125f);
+    if (!a.sigmoid && !by_logit) {
+        const float scale = 1.0f / all.total;
 #pragma unroll 1
-        for (int j = 0; j < a.n_group; ++j) {
+        for (int e = e0; e < E; e += kStep) keys[e] = ordered32(__uint_as_float(keys[e]) * scale + biases[e]);
+        __syncthreads();
+    }
+    if (a.n_group > 1) {
+        // a group's two best, a group per warp
+        const int size = quotient(a.E, a.n_group);
+#pragma unroll 1
+        for (int j = part; live && j < a.n_group; j += kParts) {
             unsigned b0 = 0u, b1 = 0u;
 #pragma unroll 1
             for (int e = lane; e < size; e += 32) {
@@ -212,73 +245,89 @@ __device__ bool choose32(const RouteArgs& a, int token, int lane, unsigned* keys
             const int holder = __ffs(__ballot_sync(0xffffffffu, b0 == first)) - 1;
             const unsigned second = __reduce_max_sync(0xffffffffu, lane == holder ? b1 : b0);
             const float c0 = from_ordered32(first), c1 = from_ordered32(second);
-            if (lane == j) mine = ordered32(c0 + c1);
-            reach = fmaxf(reach, fabsf(c0) < INFINITY && fabsf(c1) < INFINITY ? fabsf(c0) + fabsf(c1) : 0.0f);
+            if (lane == 0) groups[j] = Group{ordered32(c0 + c1), fabsf(c0) < INFINITY && fabsf(c1) < INFINITY ? fabsf(c0) + fabsf(c1) : 0.0f};
         }
-#pragma unroll 1
-        for (int r = 0; r <= a.topk_group && r < a.n_group; ++r) {
-            const unsigned best = __reduce_max_sync(0xffffffffu, mine);
-            const int holder = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
-            if (r == a.topk_group) {
-                if (!(from_ordered32(last) - from_ordered32(best) > 2.0f * wide * (reach + 4.0f * bias))) return false;
-                break;
+        __syncthreads();
+        if (part == 0) {
+            unsigned mine = 0u, kept = 0u, last = 0u;
+            float reach = 0.0f;
+            if (live && lane < a.n_group) {
+                mine = groups[lane].key;
+                reach = groups[lane].reach;
             }
-            kept |= 1u << holder;
-            last = best;
-            if (lane == holder) mine = 0u;
-        }
+            reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
 #pragma unroll 1
-        for (int e = lane; e < a.E; e += 32)
-            if (!(kept >> (e / size) & 1u)) keys[e] = 0u;
-        __syncwarp();
+            for (int r = 0; r <= a.topk_group && r < a.n_group; ++r) {
+                const unsigned best = __reduce_max_sync(0xffffffffu, mine);
+                const int holder = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
+                if (r == a.topk_group) {
+                    if (!(from_ordered32(last) - from_ordered32(best) > 2.0f * wide * (reach + 4.0f * bias))) kept = 0u;
+                    break;
+                }
+                kept |= 1u << holder;
+                last = best;
+                if (lane == holder) mine = 0u;
+            }
+            if (lane == 0) *kept_groups = kept;  // 0: too close
+        }
+        __syncthreads();
+        const unsigned kept = *kept_groups;
+        all.fine = all.fine && kept != 0u;
+#pragma unroll 1
+        for (int e = e0; e < E; e += kStep)
+            if (!(kept >> quotient(e, size) & 1u)) keys[e] = 0u;
+        __syncthreads();
     }
+    if (part > 0 || !live) return;
+    bool ok = all.fine;
     // the top_k largest, and the one behind them
-    unsigned mine = 0u, last = 0u;
+    unsigned best_of_lane = 0u, last = 0u;
     int at = 0, my_id = 0;
     bool again = true;  // the lane's best is to be looked for
 #pragma unroll 1
-    for (int k = 0; k <= a.K; ++k) {
+    for (int k = 0; ok && k <= a.K; ++k) {
         if (again) {
-            mine = 0u;
+            best_of_lane = 0u;
 #pragma unroll 4
             for (int e = lane; e < a.E; e += 32)
-                if (keys[e] > mine) {
-                    mine = keys[e];
+                if (keys[e] > best_of_lane) {
+                    best_of_lane = keys[e];
                     at = e;
                 }
         }
         __syncwarp();
-        const unsigned best = __reduce_max_sync(0xffffffffu, mine);
-        const int holder = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
+        const unsigned best = __reduce_max_sync(0xffffffffu, best_of_lane);
+        const int holder = __ffs(__ballot_sync(0xffffffffu, best_of_lane == best)) - 1;
         if (k > 0 && best != 0u) {  // (equal ones are for 64 bits too, lowest index first)
             const float c0 = from_ordered32(last), c1 = from_ordered32(best);
-            if (!(c0 - c1 > wide * (fabsf(c0) + (by_logit ? 0.0f : 2.0f * bias)))) return false;
+            if (!(c0 - c1 > wide * (fabsf(c0) + (by_logit ? 0.0f : 2.0f * bias)))) ok = false;
         }
         if (k == a.K) break;
-        if (best == 0u) return false;
+        if (best == 0u) ok = false;
         const int id = __shfl_sync(0xffffffffu, at, holder);
         if (lane == k) my_id = id;
         last = best;
         again = lane == holder;
         if (again) keys[at] = 0u;
     }
+    if (lane == 0) *good = ok;
+    if (!ok) return;
     if (lane < a.K) {
         const float2 v = __ldcg(l + my_id);
         chosen.id[lane] = my_id;
         chosen.z[lane] = (double)v.x + (double)v.y;
     }
-    if (lane == 0) chosen.top = top;
+    if (lane == 0) chosen.top = from_ordered32(all.top);
     if (!a.sigmoid && !a.renorm) {
-        double all = 0.0;
+        double sum = 0.0;
 #pragma unroll 1
         for (int e = lane; e < a.E; e += 32) {
             const float2 u = __ldcg(l + e);
-            all += score64(a, (double)u.x + (double)u.y, (double)top);
+            sum += score64(a, (double)u.x + (double)u.y, (double)from_ordered32(all.top));
         }
-        all = warp_sum_d(all);
-        if (lane == 0) chosen.total = all;
+        sum = warp_sum_d(sum);
+        if (lane == 0) chosen.total = sum;
     }
-    return true;
 }
 
 // One warp: the choice for one token in 64 bits, for every input.  Lane l holds
@@ -371,6 +420,10 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
     extern __shared__ __align__(16) uint8_t smem[];  // the choice: [warp][E] scores and keys
     __shared__ Sum2 part[kRouteWarps][TOKENS];
     __shared__ Chosen chosen[TOKENS];
+    __shared__ Part parts[kRouteWarps];
+    __shared__ Group groups[TOKENS][kMoeMaxGroups];
+    __shared__ unsigned kept[TOKENS];
+    __shared__ int good[TOKENS];
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int expert = blockIdx.x, t0 = blockIdx.y * TOKENS, nt = min(TOKENS, a.T - t0);
@@ -440,23 +493,30 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
     if (!last) return;
     __threadfence();
     if (threadIdx.x == 0) a.count[blockIdx.y] = 0;  // for the next call
-    if (warp < nt) {
-        double* scores = reinterpret_cast<double*>(smem) + warp * 2 * a.E;
-        const bool done = !choose32(a, t0 + warp, lane, reinterpret_cast<unsigned*>(scores), reinterpret_cast<float*>(scores + a.E), chosen[warp]);
-        if (done) choose(a, t0 + warp, lane, scores, reinterpret_cast<long long*>(scores + a.E));
-        if (lane == 0) chosen[warp].done = done;
+    {
+        constexpr int kParts = kRouteWarps / TOKENS;
+        const int j = warp / kParts, part = warp % kParts;
+        double* scores = reinterpret_cast<double*>(smem) + j * 2 * a.E;
+        choose32<TOKENS>(a, t0 + j, j < nt, part, lane, reinterpret_cast<unsigned*>(scores), reinterpret_cast<float*>(scores + a.E),
+                         parts + j * kParts, groups[j], kept + j, chosen[j], good + j);
+        __syncwarp();
+        if (part == 0 && j < nt) {
+            const bool done = !good[j];
+            if (done) choose(a, t0 + j, lane, scores, reinterpret_cast<long long*>(scores + a.E));
+            if (lane == 0) chosen[j].done = done;
+        }
     }
     __syncthreads();
     // the weights in 64 bits, all tokens' chosen side by side: a warp's instruction takes that unit as long for one as for 32
     const int slots = a.K + a.shared;
     for (int i = threadIdx.x; i < nt * slots; i += kRouteThreads) {
-        const int token = i / slots, k = i - token * slots;
+        const int token = quotient(i, slots), k = i - token * slots;
         Chosen& c = chosen[token];
         if (!c.done && k < a.K) c.z[k] = score64(a, c.z[k], (double)c.top);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < nt * slots; i += kRouteThreads) {
-        const int token = i / slots, k = i - token * slots;
+        const int token = quotient(i, slots), k = i - token * slots;
         const Chosen& c = chosen[token];
         if (c.done) continue;
         double w = 1.0;
