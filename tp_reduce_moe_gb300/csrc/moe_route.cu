@@ -7,7 +7,7 @@
 //   weights[t] = s[ids], optionally over their sum, times scale
 //
 // One CTA per (expert, four tokens) computes four dot products; the last CTA of
-// a token group to arrive chooses, one warp per token.  The choice must not
+// a token group to arrive chooses.  The choice must not
 // depend on how a sum was split, so the sums carry a second word: bf16
 // products are exact in fp32, and each addition's error is kept (two-sum), which
 // leaves a relative error of about 2^-45 of the sum of magnitudes.  Scores are
@@ -15,10 +15,10 @@
 // what 32 bits can get wrong, else (one token in some thousands) in 64 bits,
 // whose rate on this GPU is 1/64 of that; the weights of the chosen always are.
 //
-// Bound by latency: the gate is read in a microsecond or two, and the choice is
-// one warp's chain of top_k + groups reductions.  One token of 256 experts in
-// groups takes 11.7 us, 16 tokens 16.8, 64 tokens (bound by the two-sums, eight
-// operations a product) 23.3.
+// Bound by latency: the gate is read in 1.5 us, the arrivals take 1.2, the choice
+// 3.9 (a chain of top_k + 1 reductions at its end) and the weights 2.  One token of
+// 256 experts in groups takes 9.4 us, 16 tokens 15.7, 64 tokens (bound by the
+// two-sums, eight operations a product) 22.5.
 #include "moe_common.cuh"
 
 namespace arf {
@@ -157,8 +157,8 @@ __device__ __noinline__ void store_choice(const RouteArgs& a, int token, int lan
 //
 // Loops, not unrolled code: one SM runs this once, and an instruction that has to
 // be fetched costs it more than the instruction (unrolled over sixteen registers
-// it took 20 us for one token).  One warp per token took 6.5 us for 256 experts,
-// all warps of the CTA take CHOICE.
+// it took 20 us for one token).  One warp per token took 6.5 us for 256 experts in
+// groups, all warps of the CTA take 3.9.
 struct Part {
     unsigned top, big, bias;  // largest logit, magnitudes (ordered; bits)
     float total;
@@ -281,34 +281,46 @@ __device__ void choose32(const RouteArgs& a, int token, bool live, int part, int
     if (part > 0 || !live) return;
     bool ok = all.fine;
     // the top_k largest, and the one behind them
-    unsigned best_of_lane = 0u, last = 0u;
-    int at = 0, my_id = 0;
-    bool again = true;  // the lane's best is to be looked for
+    unsigned first = 0u, second = 0u, last = 0u;  // the lane's best two
+    int first_at = 0, second_at = 0, my_id = 0;
+    int known = 0;  // of those two
 #pragma unroll 1
     for (int k = 0; ok && k <= a.K; ++k) {
-        if (again) {
-            best_of_lane = 0u;
+        if (known == 0) {
+            first = second = 0u;
 #pragma unroll 4
-            for (int e = lane; e < a.E; e += 32)
-                if (keys[e] > best_of_lane) {
-                    best_of_lane = keys[e];
-                    at = e;
+            for (int e = lane; e < a.E; e += 32) {
+                const unsigned v = keys[e];
+                if (v > first) {
+                    second = first;
+                    second_at = first_at;
+                    first = v;
+                    first_at = e;
+                } else if (v > second) {
+                    second = v;
+                    second_at = e;
                 }
+            }
+            known = 2;
         }
         __syncwarp();
-        const unsigned best = __reduce_max_sync(0xffffffffu, best_of_lane);
-        const int holder = __ffs(__ballot_sync(0xffffffffu, best_of_lane == best)) - 1;
+        const unsigned best = __reduce_max_sync(0xffffffffu, first);
+        const int holder = __ffs(__ballot_sync(0xffffffffu, first == best)) - 1;
+        const int id = __shfl_sync(0xffffffffu, first_at, holder);
         if (k > 0 && best != 0u) {  // (equal ones are for 64 bits too, lowest index first)
             const float c0 = from_ordered32(last), c1 = from_ordered32(best);
             if (!(c0 - c1 > wide * (fabsf(c0) + (by_logit ? 0.0f : 2.0f * bias)))) ok = false;
         }
         if (k == a.K) break;
         if (best == 0u) ok = false;
-        const int id = __shfl_sync(0xffffffffu, at, holder);
         if (lane == k) my_id = id;
         last = best;
-        again = lane == holder;
-        if (again) keys[at] = 0u;
+        if (lane == holder) {
+            keys[first_at] = 0u;
+            first = second;
+            first_at = second_at;
+            --known;
+        }
     }
     if (lane == 0) *good = ok;
     if (!ok) return;
