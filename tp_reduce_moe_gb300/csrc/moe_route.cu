@@ -18,7 +18,7 @@
 // Bound by latency: the gate is read in 1.5 us, the arrivals take 1.2, the choice
 // 3.9 (a chain of top_k + 1 reductions at its end) and the weights 2.  One token of
 // 256 experts in groups takes 9.4 us, 16 tokens 15.7, 64 tokens (bound by the
-// two-sums, eight operations a product) 22.5.
+// two-sums, seven operations a product) 22.5.
 #include "moe_common.cuh"
 
 namespace arf {
@@ -60,22 +60,23 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
-__device__ __forceinline__ Pair mul(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
 __device__ __forceinline__ Pair sub(Pair a, Pair b) {  // exact product by -1, one rounding
     Pair r;
     const Pair m = pack(-1.0f, -1.0f);
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(b.v), "l"(m.v), "l"(a.v));
     return r;
 }
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
 struct Sum2x2 {
     Pair hi, lo;
+    // A two-sum of hi and the product, which is exact and needs no instruction of its own.
     __device__ __forceinline__ void add_product(Pair x, Pair w) {
-        const Pair p = mul(x, w), r = add(hi, p), b = sub(r, hi);
-        lo = add(lo, add(sub(hi, sub(r, b)), sub(p, b)));
+        const Pair r = fma(x, w, hi), minus = sub(hi, r);  // -(r - hi)
+        lo = add(lo, add(sub(hi, add(r, minus)), fma(x, w, minus)));
         hi = r;
     }
 };
@@ -474,18 +475,30 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
                 }
         }
     }
+    // over the lanes, halving the tokens that a lane is left with
+    Sum2 acc[TOKENS];
 #pragma unroll
     for (int j = 0; j < TOKENS; ++j) {
-        if (j >= nt) break;
         const float2 h = unpack(sums[j].hi), l = unpack(sums[j].lo);
-        Sum2 acc = add2(Sum2{h.x, l.x}, h.y, l.y);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float hi = __shfl_xor_sync(0xffffffffu, acc.hi, o), lo = __shfl_xor_sync(0xffffffffu, acc.lo, o);
-            acc = add2(acc, hi, lo);
-        }
-        if (lane == 0) part[warp][j] = acc;
+        acc[j] = add2(Sum2{h.x, l.x}, h.y, l.y);
     }
+    int o = 16;
+#pragma unroll
+    for (int n = TOKENS / 2; n > 0; n >>= 1, o >>= 1) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            const Sum2 keep = upper ? acc[j + n] : acc[j], give = upper ? acc[j] : acc[j + n];
+            const float hi = __shfl_xor_sync(0xffffffffu, give.hi, o), lo = __shfl_xor_sync(0xffffffffu, give.lo, o);
+            acc[j] = add2(keep, hi, lo);
+        }
+    }
+#pragma unroll
+    for (; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(0xffffffffu, acc[0].hi, o), lo = __shfl_xor_sync(0xffffffffu, acc[0].lo, o);
+        acc[0] = add2(acc[0], hi, lo);
+    }
+    if (lane % (32 / TOKENS) == 0) part[warp][lane / (32 / TOKENS)] = acc[0];
     __syncthreads();
     if (threadIdx.x < 32) {  // one warp writes, then arrives for all
         if (lane < nt) {
