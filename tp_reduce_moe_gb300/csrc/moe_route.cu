@@ -17,8 +17,8 @@
 //
 // Bound by latency: the gate is read in 1.5 us, the arrivals take 1.2, the choice
 // 3.9 (a chain of top_k + 1 reductions at its end) and the weights 2.  One token of
-// 256 experts in groups takes 9.4 us, 16 tokens 15.7, 64 tokens (bound by the
-// two-sums, seven operations a product) 22.5.
+// 256 experts in groups takes 9.3 us, 16 tokens 14.9, 64 tokens (bound by the
+// two-sums, seven operations a product) 20.3.
 #include "moe_common.cuh"
 
 namespace arf {
@@ -429,7 +429,7 @@ __device__ __noinline__ void choose(const RouteArgs& a, int token, int lane, dou
 // TOKENS per CTA.  One token: four of a thread's chunks of the expert's row at a
 // time, all asked for before the first is used; more: a chunk of all tokens.
 template <int TOKENS>
-__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, 4) moe_route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];  // the choice: [warp][E] scores and keys
     __shared__ Sum2 part[kRouteWarps][TOKENS];
     __shared__ Chosen chosen[TOKENS];
@@ -583,8 +583,9 @@ cudaError_t moe_route_set_attributes() {
     return cudaFuncSetAttribute(moe_route_kernel<kRouteTokens>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteTokens * kMoeMaxExperts * 16);
 }
 
-// 16 tokens of 256 experts took 16.9 us with four tokens per CTA and 19.5 with
-// eight, 64 tokens 23.4 and 26.3; two experts per CTA gain nothing.
+// 16 tokens took 16.9 us with four tokens per CTA and 19.5 with eight, 64 tokens
+// 23.4 and 26.3; two experts per CTA gain nothing.  (Four CTAs to an SM, 64
+// registers: 20.3 us for 64 tokens, 21.7 with 70.)
 cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t stream, bool pdl) {
     return a.T <= 2 ? launch<1>(a, stream, pdl) : launch<kRouteTokens>(a, stream, pdl);
 }
