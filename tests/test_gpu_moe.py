@@ -370,6 +370,7 @@ MORE_W4 = [  # T, H, E, K, I, group
 MORE_MATVECS = [  # T, N, K, group
     (3, 80000, 64, 32), (9, 80001, 64, 32), (1, 2888, 96, 32), (2, 3496, 4096, 64), (1, 4256, 224, 32), (4, 100, 256, 64),
     (2, 2900, 768, 64), (2, 33, 320, 64), (6, 3500, 1024, 128), (8, 300, 24576, 32), (12, 170, 7168, 64),
+    (9, 1048576, 32, 32), (64, 300000, 128, 128),
 ]
 
 
