@@ -10,7 +10,8 @@
 #include "arfuse.h"
 #include "moe_common.cuh"
 
-static_assert(arf::kMoeMaxTokens == AR_MAX_MOE_TOKENS && arf::kMoeMaxGroups == AR_MAX_MOE_GROUPS && arf::kMoeMaxExperts == AR_MAX_MOE_EXPERTS &&
+static_assert(arf::kMoeMaxTokens == AR_MAX_MOE_TOKENS && arf::kMoeMaxGroups == AR_MAX_MOE_GROUPS &&
+                  arf::kMaxTopK == AR_MAX_TOP_K && arf::kMoeMaxExperts == AR_MAX_MOE_EXPERTS &&
                   arf::kErrExpertRange == AR_DEVERR_EXPERT_RANGE,
               "the kernels' limits are the header's");
 

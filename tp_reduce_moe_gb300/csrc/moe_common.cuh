@@ -687,25 +687,27 @@ __device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&sum)[4
 // in the order of the warps, once a job.  (Tiles side by side and their segments
 // dealt to powers of two of warps left a seventh of the warps idle, or took a
 // round with two barriers for every few tiles, 1.8 us each.)
+//
+// 4-bit weights: as many tiles a job as a CTA has as a rule, since a job's end costs
+// instructions.  bf16 weights: eight, and parts in two buffers, so that the memory
+// does not wait at a job's end: 5 tokens with 10 of 32 experts of 3 x 1400 x 8192
+// take 271 us, with 32 tiles and one buffer 284.
 template <int GS>
 constexpr int kJobTiles = GS ? 32 : 8;
 template <int GS>
 constexpr int kPartBuffers = GS ? 1 : 2;
 
 // Shared memory of a product: barriers, parts of tiles (warp w's of tile i at i + w:
-// ranges are in order), with several panels the sums over those done, staged activations, `extra` bytes, the
-// rings, their scales.
+// ranges are in order), with several panels the sums over those done, staged
+// activations, `extra` bytes, the rings, their scales.
 constexpr int kSmemLimit = 227 * 1024;
 struct ProductPlan {
     RowShape shape;
     uint8_t panel[9];  // segments whose activations are staged at a time, by the number of staged tokens
-    int staged;         // bytes
-    int sums_at, staged_at;
-    int pairs;          // of columns that a tile has at most
-    int tiles;          // of a job, at most
-    int extra;    // bytes, at extra_at
-    int extra_at, ring_at, scales_at, smem;
-    int piece;  // of the scales' copies
+    int pairs;         // of columns that a tile has at most
+    int tiles;         // of a job, at most
+    int sums_at, staged_at, extra_at, ring_at, scales_at, smem;
+    int piece;              // of the scales' copies
     int chunk = 8;          // tokens per item, at most
     bool together = false;  // all tokens are staged
 };
@@ -717,7 +719,6 @@ inline ProductPlan plan_product(int K, int tokens, int columns, int tiles, int e
     const int segments = p.shape.segments;
     constexpr int kScales = GS ? Scales<GS ? GS : 1>::kSlot : 0, kSlot = kSlotBytes + kScales;
     p.piece = GS ? Scales<GS ? GS : 1>::piece(Fmt<GS>::scales(K)) : 0;
-    p.extra = extra;
     tiles = tiles < kJobTiles<GS> ? tiles : kJobTiles<GS>;
     p.pairs = ((tokens < 8 ? tokens : 8) + 1) / 2;
     p.sums_at = kMvWarps * kMaxSlots * 8 + kPartBuffers<GS> * (tiles + kMvWarps) * p.pairs * 128;
@@ -730,7 +731,7 @@ inline ProductPlan plan_product(int K, int tokens, int columns, int tiles, int e
         p.staged_at += tiles * p.pairs * 128;
         fixed += tiles * p.pairs * 128;
     }
-    p.staged = 0;
+    int staged = 0;
     for (int n = 0; n <= 8; ++n) {
         p.panel[n] = (uint8_t)segments;  // at most 128
         if (GS == 0 || n == 0) continue;
@@ -742,9 +743,9 @@ inline ProductPlan plan_product(int K, int tokens, int columns, int tiles, int e
         const int panels = (segments + most - 1) / most;
         p.panel[n] = (uint8_t)((segments + panels - 1) / panels);
         const int bytes = (View::bytes(p.panel[n], n) + 15) / 16 * 16;
-        p.staged = bytes > p.staged ? bytes : p.staged;
+        staged = bytes > staged ? bytes : staged;
     }
-    p.extra_at = p.staged_at + p.staged;
+    p.extra_at = p.staged_at + staged;
     p.ring_at = (p.extra_at + extra + 1023) / 1024 * 1024;
     p.scales_at = p.ring_at + kMaxSlots * kMvWarps * kSlotBytes;
     p.smem = p.scales_at + kMaxSlots * kMvWarps * kScales;

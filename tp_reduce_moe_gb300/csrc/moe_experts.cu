@@ -87,7 +87,7 @@ __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsA
         return;
     }
     // a thread's slots, and their weights, asked for together
-    constexpr int kMine = kMoeMaxTokens * kMaxTopK / kMvThreads;
+    constexpr int kMine = (kMoeMaxSlots + kMvThreads - 1) / kMvThreads;
     const int slots = a.T * a.K;
     int mine[kMine];
     float weight[kMine];
