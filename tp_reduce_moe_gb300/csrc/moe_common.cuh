@@ -237,6 +237,11 @@ __device__ __forceinline__ void prefetch_maps(const Weights& w, bool full, bool 
     if (scales) asm volatile("prefetch.tensormap [%0];" ::"l"(&w.scales) : "memory");
 }
 
+// The thread's ordinary accesses to shared memory before it come before what
+// asynchronous copies do to it that a barrier orders behind it: the barrier alone
+// does not order the two kinds.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // Multiples of 16 bytes at such addresses.
 __device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from), "r"(bytes),

@@ -61,7 +61,8 @@ struct Items {
 // Called by all threads of a CTA.  A token that names an expert twice gets one
 // entry with the sum of its weights (a single token: an item each).  -1 names no expert; other values outside
 // [0, E) are skipped too and flagged.  mask: scratch, two words per expert (the
-// tokens that chose it), free again afterwards.
+// tokens that chose it), free again afterwards: it may be the ring's memory, since
+// each thread's accesses to it are ordered before copies that follow the barrier.
 __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsArgs& a, int chunk) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (a.T == 1) {  // every slot an item: one warp does it
@@ -163,6 +164,7 @@ __device__ void build_items(const Items& it, uint32_t (*mask)[2], const ExpertsA
         it.token[it.at[e] + before] = t;
         it.w[it.at[e] + before] = w;
     }
+    fence_proxy_async();  // ordinary accesses to the masks, then copies over them
     __syncthreads();
 }
 
