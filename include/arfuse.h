@@ -544,10 +544,25 @@ ARFUSE_API ar_status ar_moe_create(int device, int experts, int shared, int top_
 /* Free the handle.  NULL is accepted.  No call using it may still be running. */
 ARFUSE_API ar_status ar_moe_destroy(ar_moe* moe);
 
-/* Read and clear the handle's error word, as ar_workspace_device_error
- * (AR_DEVERR_EXPERT_RANGE; AR_DEVERR_TIMEOUT: a bounded wait for a copy ran out,
- * that call's results are NaN). */
+/* Read and clear the handle's error word, as ar_workspace_device_error:
+ * AR_DEVERR_EXPERT_RANGE; AR_DEVERR_TIMEOUT: a bounded wait for a copy ran out.
+ * What that call computed from the lost copy, and from what would have followed
+ * it, is NaN: of the first product, all of `out` of the tokens whose experts' rows
+ * were lost; of the second, columns of `out` for all tokens.  The rest of `out`
+ * may be right or NaN: discard the call's results. */
 ARFUSE_API ar_status ar_moe_device_error(ar_moe* moe, int* code);
+
+/*
+ * Failure injection for tests of that path, as ar_workspace_inject_wait_timeout:
+ * with limit_ns > 0 every warp of the first (product 1) or second (product 2)
+ * product of later ar_moe_experts and ar_moe_experts_w4 calls on this handle
+ * leaves a copy out, and waits for it instead of its first wait, up to limit_ns
+ * nanoseconds.  The call then sets AR_DEVERR_TIMEOUT, its results are NaN (first
+ * product: of all tokens with experts; second: all), and it returns.  0 turns it
+ * off.  The two products are set separately.
+ * Errors: AR_ERR_INVALID_ARG (NULL, another product, limits outside [0, 1e9]).
+ */
+ARFUSE_API ar_status ar_moe_inject_wait_timeout(ar_moe* moe, int product, int64_t limit_ns);
 
 /*
  * The router: logits l = x gate^T, scores s = softmax(l) or sigmoid(l) over
@@ -630,7 +645,9 @@ ARFUSE_API ar_status ar_moe_experts_w4(ar_moe* moe, const void* x, const int32_t
  *   N, K   1 .. AR_MAX_MATVEC_ROWS, group .. AR_MAX_MATVEC_COLS
  *   out    device [T, N], bf16 or (out_is_fp32 = 1) fp32
  * A token with an |x| of 2^101 or more, an infinity or a NaN gets NaN.  Sums are
- * fp32; deterministic, but their order may depend on T.
+ * fp32; deterministic, but their order may depend on T.  Should the bounded wait
+ * for a copy run out (nothing known makes it), what needed the copy is NaN; with no
+ * handle, nothing else tells.
  * Errors: AR_ERR_INVALID_ARG (NULL, negative sizes, overlap of out with an
  * input, out_is_fp32 not 0 or 1), AR_ERR_ALIGNMENT (x, q, s, out 16 bytes),
  * AR_ERR_UNSUPPORTED (group, sizes), AR_ERR_CAPACITY (T), AR_ERR_CUDA.

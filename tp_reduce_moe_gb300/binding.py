@@ -121,6 +121,8 @@ def load_library(path: str | None = None):
         lib.ar_moe_destroy.argtypes = [P]
         lib.ar_moe_device_error.restype = I
         lib.ar_moe_device_error.argtypes = [P, ctypes.POINTER(I)]
+        lib.ar_moe_inject_wait_timeout.restype = I
+        lib.ar_moe_inject_wait_timeout.argtypes = [P, I, I64]
         lib.ar_moe_route.restype = I
         lib.ar_moe_route.argtypes = [P, P, P, P, I, I, F, I, I, I64, P, P, P]
         lib.ar_moe_experts.restype = I
@@ -541,11 +543,19 @@ def ar_moe_destroy(moe: Moe) -> None:
 
 
 def ar_moe_device_error(moe: Moe) -> int:
-    """Synchronise, read and clear the handle's error word (AR_DEVERR_EXPERT_RANGE)."""
+    """Synchronise, read and clear the handle's error word (AR_DEVERR_EXPERT_RANGE, AR_DEVERR_TIMEOUT)."""
     code = ctypes.c_int(0)
     _check(load_library().ar_moe_device_error(moe.handle, ctypes.byref(code)), "ar_moe_device_error",
            ok=(AR_OK, AR_ERR_DEVICE_CHECK))
     return int(code.value)
+
+
+def ar_moe_inject_wait_timeout(moe: Moe, product: int, limit_ns: int) -> None:
+    """Failure injection for tests (0 = off): later expert calls wait in their
+    first (1) or second (2) product for a copy that is never made, for limit_ns,
+    so that they take the device-side timeout path (AR_DEVERR_TIMEOUT, results
+    NaN)."""
+    _check(load_library().ar_moe_inject_wait_timeout(moe.handle, int(product), int(limit_ns)), "ar_moe_inject_wait_timeout")
 
 
 def _need_on(device, t, dtype, shape, name):

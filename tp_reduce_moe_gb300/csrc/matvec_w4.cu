@@ -50,7 +50,8 @@ struct Matvec {
     }
     __device__ const uint16_t* scales(const Tile& t) const { return a.s + (int64_t)t.row * (a.K / (128 / GS)); }
     __device__ int second() const { return 8; }
-    __device__ void lost() const {}
+    __device__ void lost() const {}  // (there is no handle whose error word could say so)
+    __device__ static constexpr unsigned long long stall() { return 0; }
     __device__ const uint16_t* x(const Tile&, int i) const { return a.x + (int64_t)(token + i) * a.K; }
     __device__ int staged_key(const Job&) const { return 0; }
     __device__ int staged(const Job&) const { return tokens; }
@@ -74,7 +75,7 @@ template <int GS>
 __global__ void __launch_bounds__(kMvThreads, 1) matvec_w4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__ Weights weights,
                                                                      const __grid_constant__ ProductPlan plan, int groups) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, kMaxSlots, Scales<GS>::arrivals(plan.piece), threadIdx.x & 31);
+    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, Scales<GS>::arrivals(plan.piece), threadIdx.x & 31);
     if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, plan.piece == 0);
     pdl_wait();  // no global memory access before this point
     pdl_trigger();

@@ -21,6 +21,7 @@ struct ar_moe {
     int64_t max_tokens;
     unsigned flags;
     int num_sms;
+    unsigned long long stall_ns[2];  // failure injection, first and second product
     uint8_t* d_mem;  // everything below
     unsigned* d_err;
     unsigned* d_count;  // [token groups], zero between calls
@@ -91,6 +92,8 @@ ar_status experts(ar_moe* m, const void* x, const int32_t* ids, const float* wei
     a.act = m->d_act;
     a.out = static_cast<uint16_t*>(out);
     a.err = m->d_err;
+    a.stall_ns[0] = m->stall_ns[0];
+    a.stall_ns[1] = m->stall_ns[1];
     a.T = (int)T;
     a.K = slots(m);
     a.E = (int)E;
@@ -199,6 +202,13 @@ ar_status ar_moe_device_error(ar_moe* m, int* code) {
     if (st != AR_OK) return st;
     *code = (int)v;
     return v ? AR_ERR_DEVICE_CHECK : AR_OK;
+}
+
+ar_status ar_moe_inject_wait_timeout(ar_moe* m, int product, int64_t limit_ns) {
+    if (!m || product < 1 || product > 2) return AR_ERR_INVALID_ARG;
+    if (limit_ns < 0 || limit_ns > (int64_t)arf::kWaitLimitNs) return AR_ERR_INVALID_ARG;
+    m->stall_ns[product - 1] = (unsigned long long)limit_ns;
+    return AR_OK;
 }
 
 ar_status ar_moe_route(ar_moe* m, const void* x, const void* gate, const float* bias, int scoring, int renorm, float scale,

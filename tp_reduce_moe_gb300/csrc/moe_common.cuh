@@ -61,6 +61,9 @@ struct ExpertsArgs {
     uint16_t* act;        // scratch bf16 [T * K, 2, I]: high and low part of the activations
     uint16_t* out;        // bf16 [T, H]
     unsigned* err;
+    // Failure injection (0 = off): how long the warps of the first and of the second
+    // product wait for a copy that is never made before they give up.
+    unsigned long long stall_ns[2];
     int T, K, E, H, I;
 };
 
@@ -263,11 +266,11 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase) {
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase, unsigned long long limit_ns) {
     const unsigned long long t0 = global_timer_ns();
     for (unsigned it = 0; it < kWaitMaxIters; ++it) {
         if (mbar_sleep(bar, phase)) return true;
-        if ((it & 31u) == 31u && global_timer_ns() - t0 > kWaitLimitNs) return false;
+        if (global_timer_ns() - t0 > limit_ns) return false;
     }
     return false;
 }
@@ -276,15 +279,15 @@ struct SlotRing {
     uint32_t slots, bars;  // shared addresses
     int two, step;         // whether there are two slots (else one), bytes between them
     uint32_t at;           // the next: counts fillings, later readings
-    bool alive;            // no wait has run out
+    bool alive;            // the lane's waits have all ended in time
 
     __device__ __forceinline__ SlotRing(uint32_t slots, uint32_t bars, int n, int step)
         : slots(slots), bars(bars), two(n == 2), step(step), at(0), alive(true) {}
     __device__ __forceinline__ uint32_t slot() const { return slots + (at & two) * step; }
     __device__ __forceinline__ uint32_t bar() const { return bars + (at & two) * 8; }
     // The warp's barriers, before anything else; arrivals: of each, for each filling.
-    __device__ static __forceinline__ void init(uint32_t bars, int n, int arrivals, int lane) {
-        if (lane < n) mbar_init(bars + lane * 8, arrivals);
+    __device__ static __forceinline__ void init(uint32_t bars, int arrivals, int lane) {
+        if (lane < kMaxSlots) mbar_init(bars + lane * 8, arrivals);
         fence_mbar_init();
         __syncwarp();
     }
@@ -318,11 +321,27 @@ struct SlotRing {
             if (wide) copy_tensor(slot + kNextAt, map, bar, x + kBox, row);
         }
     }
-    // Waits for the next slot.  A wait that runs out (nothing but a lost copy
-    // makes it) ends the waiting for good.
+    // Waits for the next slot.  A lane whose wait runs out (nothing but a lost copy
+    // makes it) waits no more, and neither copies nor arrives any more: a barrier
+    // whose phase has not ended takes no further arrivals, and the lost copy may
+    // still land.  The warp learns of it at the end of a tile (ended).
     __device__ __forceinline__ void wait() {
         const uint32_t phase = at >> two & 1;
-        if (!mbar_sleep(bar(), phase) && alive) alive = wait_long(bar(), phase);
+        if (!mbar_sleep(bar(), phase) && alive) alive = wait_long(bar(), phase, kWaitLimitNs);
+    }
+    // Whether any lane's wait has run out, for every lane the same: then all stop,
+    // and what the warp has made of the slots is not a number.  (Asked at every wait
+    // with a branch around the products it cost 2 to 5 %, behind them up to 4 %.)
+    __device__ __forceinline__ bool ended(bool& more) {
+        if (__all_sync(0xffffffffu, alive)) return false;
+        alive = more = false;
+        return true;
+    }
+    // Failure injection: instead of the first wait, one on the second slot's
+    // barrier, before anything is copied there.
+    __device__ __forceinline__ void lose(unsigned long long limit_ns, bool& more) {
+        alive = wait_long(bars + 8, 0, limit_ns);
+        ended(more);
     }
     // Where what comes with the slot lies, `bytes` bytes a slot.
     __device__ __forceinline__ uint32_t beside(uint32_t first, int bytes) const { return first + (at & two) * bytes; }
@@ -770,7 +789,8 @@ inline ProductPlan plan_product(int K, int tokens, int columns, int tiles, int e
 //   staged_key(job), staged(job), staged_x(job, i), column(tile, i): with 4-bit weights the job's tokens that are staged
 //       (equal keys: the same ones), and which of them is the tile's token i
 //   store(tile, pair, token, first, second)  results of a pair's two rows
-//   lost()                                a wait ran out
+//   lost()                                a wait ran out: what needed the warp's copies from there on is NaN
+//   stall()                               failure injection: SlotRing::lose's limit, 0: off
 // Deterministic: a tile's sums are added in the order of the warps.
 template <int GS, class Jobs>
 __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& weights, uint8_t* smem, const ProductPlan& plan, int K) {
@@ -836,13 +856,13 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         if (!more) return;
         const bool scales = F::kW4 && plan.piece == 0;
         const int seg = cp + c.seg;
-        if (lane == 0) {
+        if (lane == 0 && ring.alive) {
             ring.template fill<Jobs::kPairs>(weights, ct.row, ct.n, ct.expert, seg, shape.bytes(seg), scales ? Scales<kGS>::kSlot : 0);
             if constexpr (F::kW4)
                 if (scales) Scales<kGS>::template copy<Jobs::kPairs>(scales_slot(), ring.bar(), weights, ct.row, ct.expert, seg);
         }
         if constexpr (F::kW4)
-            if (!scales)
+            if (!scales && ring.alive)
                 Scales<kGS>::template fill<Jobs::kPairs>(scales_slot(), ring.bar(), jobs.scales(ct), ct.n, jobs.second(), seg * 4 * kGS, row_scales,
                                                          plan.piece, lane);
         if (--c.left == 0) {
@@ -853,8 +873,9 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         }
     };
     settle();
+    const unsigned long long stall = jobs.stall();
     auto fill_all = [&]() {
-        for (int s = 0; s < kMaxSlots; ++s) {
+        for (int s = 0; s < (stall ? 1 : kMaxSlots); ++s) {
             fill();
             ring.next();
         }
@@ -924,6 +945,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         begin();
         fill_all();
     }
+    if (stall) ring.lose(stall, more);
     int key = F::kW4 ? jobs.staged_key(job) : 0;
     for (int p = 0, buffer = 0;;) {
         const int len = min(panel, segments - p);
@@ -954,10 +976,7 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
             fill();
             ring.next();
             if (last || final) {
-                if (!ring.alive) {
-                    jobs.lost();
-                    acc[0] = acc[1] = acc[2] = acc[3] = __uint_as_float(0x7fc00000u);
-                }
+                if (ring.ended(more)) acc[0] = acc[1] = acc[2] = acc[3] = __uint_as_float(0x7fc00000u);
                 if (in_use) *reinterpret_cast<float4*>(part + range.tile * part_size) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                 acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
                 range.tile += last;
@@ -1023,7 +1042,10 @@ __device__ __forceinline__ void run_product(const Jobs& jobs, const Weights& wei
         }
         if (!F::kW4) buffer = buffer ? 0 : plan.tiles + kMvWarps;  // (the other one has been read before the barrier above)
     }
-    if (!ring.alive) grace_period(10000000ull);  // copies that may still land
+    if (ring.ended(more)) {
+        jobs.lost();
+        grace_period(10000000ull);  // copies that may still land
+    }
 }
 
 }  // namespace arf

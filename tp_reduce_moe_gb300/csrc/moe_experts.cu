@@ -262,6 +262,7 @@ struct GateUp {
     __device__ const uint16_t* scales(const Tile& t) const { return a.s13 + ((int64_t)t.expert * 2 * a.I + t.row) * Fmt<GS>::scales(a.H); }
     __device__ int second() const { return a.I; }
     __device__ void lost() const { atomicOr(a.err, kErrTimeout); }
+    __device__ unsigned long long stall() const { return a.stall_ns[0]; }
     __device__ const uint16_t* x(const Tile& t, int i) const { return a.x + (int64_t)it.token[t.entry + i] * a.H; }
     __device__ int staged_key(const Job& j) const { return j.base; }
     __device__ int staged(const Job& j) const { return j.tokens; }
@@ -285,8 +286,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
                                                                        const __grid_constant__ ProductPlan plan) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const Items it(smem + plan.extra_at, a.T * a.K, a.E);
-    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, kMaxSlots, GS > 0 ? Scales<GS ? GS : 1>::arrivals(plan.piece) : 1,
-                   threadIdx.x & 31);
+    SlotRing::init(smem_addr(smem) + warp_index() * kMaxSlots * 8, GS > 0 ? Scales<GS ? GS : 1>::arrivals(plan.piece) : 1, threadIdx.x & 31);
     if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     pdl_wait();     // no global memory access before this point
     pdl_trigger();  // after it: what the second kernel reads before its own wait is complete
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
         }
     }
-    SlotRing::init(smem_addr(smem) + warp * kMaxSlots * 8, plan.slots, F::kW4 ? Scales<kGS>::arrivals(plan.piece) : 1, lane);
+    SlotRing::init(smem_addr(smem) + warp * kMaxSlots * 8, F::kW4 ? Scales<kGS>::arrivals(plan.piece) : 1, lane);
     if (threadIdx.x == 0) prefetch_maps(weights, plan.shape.row_bytes >= kSegment, GS > 0 && plan.piece == 0);
     // Before the wait: ids, weights and expert weights.  The first kernel starts
     // nothing before its own wait, so everything ahead of it has completed; it
@@ -386,13 +386,13 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         if (!more) return;
         const int rows = min(16, r1 - crow);
         const bool scales = F::kW4 && plan.piece == 0;
-        if (lane == 0) {
+        if (lane == 0 && ring.alive) {
             ring.fill<false>(weights, cfirst, rows, 0, cseg, shape.bytes(cseg), scales ? Scales<kGS>::kSlot : 0);
             if constexpr (F::kW4)
                 if (scales) Scales<kGS>::template copy<false>(scales_slot(), ring.bar(), weights, cfirst, 0, cseg);
         }
         if constexpr (F::kW4)
-            if (!scales)
+            if (!scales && ring.alive)
                 Scales<kGS>::template fill<false>(scales_slot(), ring.bar(), a.s2 + (int64_t)cfirst * row_scales, rows, 8, cseg * 4 * kGS, row_scales,
                                                   plan.piece, lane);
         if (++cf == f1) {
@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
         }
     };
     if (more) aim();
-    for (int s = 0; s < plan.slots; ++s) {
+    const unsigned long long stall = a.stall_ns[1];
+    for (int s = 0; s < (stall ? 1 : plan.slots); ++s) {
         fill();
         ring.next();
     }
@@ -428,8 +429,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             f += to - seg;
         }
         if (lane == 0) mbar_arrive_expect_tx(act_bar, bytes);
-        if (!mbar_sleep(act_bar, 0)) ring.alive = wait_long(act_bar, 0);
+        if (!mbar_sleep(act_bar, 0)) ring.alive = wait_long(act_bar, 0, kWaitLimitNs);
     }
+    if (stall) ring.lose(stall, more);
 
     for (int row = r0, in_round = 0; row < r1; row += 16) {
         const int rows = min(16, r1 - row);
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_down_kernel(const __grid_co
             seg = after;
             item += last;
         }
-        if (!ring.alive) {
+        if (ring.ended(more)) {
             atomicOr(a.err, kErrTimeout);
             for (int i = lane; i < a.T * 16; i += 32) mine[i] = __uint_as_float(0x7fc00000u);
         }
