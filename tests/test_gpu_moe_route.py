@@ -139,3 +139,34 @@ def test_groups_with_equal_and_undefined_choices(sigmoid, biased, renorm):
     up[14] = NAN
     check(y, up, bias, K, sigmoid, G, keep, renorm)
     check(y, up, None if bias is None else torch.full((E,), -INF), K, sigmoid, G, keep, renorm)
+
+
+def logits_as(values, H=64):
+    """(x, gate) with these logits: two bf16 terms each."""
+    v = torch.tensor(values, dtype=torch.float64)
+    gate = torch.zeros(len(values), H, dtype=torch.bfloat16)
+    gate[:, 3] = v.bfloat16()
+    gate[:, 44] = (v - gate[:, 3].double()).bfloat16()
+    x = torch.zeros(1, H, dtype=torch.bfloat16)
+    x[:, [3, 44]] = 1.0
+    return x, gate
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_scores_at_the_end_of_the_range(T):
+    """Scores whose 32-bit form is zero, subnormal or coarse: the order is still that of 64-bit scores."""
+    # two groups; by 32-bit sigmoids the other one's sum is larger: e^-88.875 is zero in them
+    x, gate = logits_as([-88.0, -88.875, -88.5, -88.5625])
+    assert check(x.repeat(T, 1), gate, None, 2, True, 2, 1)[0].tolist() == [0, 1]
+    x, gate = logits_as([-88.5, -88.5625, -88.0, -88.875])
+    assert check(x.repeat(T, 1), gate, None, 2, True, 2, 1)[0].tolist() == [2, 3]
+    g = gen(60 + T)
+    for sigmoid in (False, True):
+        for low, high in ((-92.0, -86.0), (-106.0, -84.0), (-800.0, -700.0), (-120.0, 3.0), (60.0, 90.0)):
+            x, gate = logits_as((torch.rand(48, generator=g, dtype=torch.float64) * (high - low) + low).tolist())
+            if not sigmoid and low > -800:
+                gate[5, 3], gate[5, 44] = 0.0, 0.0  # the largest: the others' exponentials are tiny
+            x = x.repeat(T, 1)
+            for bias in (None, torch.zeros(48), torch.full((48,), 1e-40)):
+                for groups, keep in ((1, 1), (8, 3), (24, 4)):
+                    check(x, gate, bias, 6, sigmoid, groups, keep)

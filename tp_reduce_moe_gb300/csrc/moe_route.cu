@@ -155,6 +155,8 @@ __device__ __noinline__ void store_choice(const RouteArgs& a, int token, int lan
 // with b to 2^-24: for |l| <= 8 and two values 2^-19.  A softmax's exponent
 // carries three such roundings and the difference's own, and the sum of the
 // exponentials 2^-19.6: 2^-17.2.  Twice that is taken, and more for larger |l|.
+// All of it holds for normal numbers: a score below e^-80 (over 512 experts, in a
+// softmax, still above 2^-126) is for 64 bits, since in 32 it is coarse or zero.
 //
 // Loops, not unrolled code: one SM runs this once, and an instruction that has to
 // be fetched costs it more than the instruction (unrolled over sixteen registers
@@ -203,7 +205,7 @@ __device__ void choose32(const RouteArgs& a, int token, bool live, int part, int
         for (int e = e0; e < E; e += kStep) {
             const float v = __uint_as_float(keys[e]), x = expf(a.sigmoid ? -v : v - top), s = a.sigmoid ? 1.0f / (1.0f + x) : x, b = biases[e];
             mine.total += s;
-            mine.fine = mine.fine && b == b && b < INFINITY;
+            mine.fine = mine.fine && b == b && b < INFINITY && (a.sigmoid ? v : v - top) > -80.0f;
             if (fabsf(b) < INFINITY) mine.bias = max(mine.bias, __float_as_uint(fabsf(b)));
             keys[e] = a.sigmoid ? ordered32(s + b) : __float_as_uint(s);
         }
