@@ -7,7 +7,7 @@ import torch
 
 import tp_reduce_moe_gb300 as arf
 from tests import _moe
-from tests.test_gpu_moe import DEV, Layer, choice, gen, normal
+from tests.test_gpu_moe import DEV, Layer, check, choice, gen, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -73,4 +73,14 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_clean(T, H, E, K,
             arf.ar_moe_inject_wait_timeout(m, i + 1, 0)
         assert torch.equal(layer.run(m, x, ids, w), right)
         assert arf.ar_moe_device_error(m) == 0
+    m.destroy()
+
+
+@pytest.mark.parametrize("T,H,E,K,I,group", [(16, 7168, 32, 8, 256, 64), (16, 7168, 32, 8, 256, 128), (14, 7168, 32, 8, 256, 32), (6, 4096, 16, 5, 1024, 128)])
+def test_second_product_with_one_tile_a_round(T, H, E, K, I, group):
+    """Staged activations that leave the sums of one tile room, not those of all."""
+    g = gen(T + H + I + group)
+    layer = Layer(E, H, I, group, g)
+    m = arf.ar_moe_create(E, K, H, I, T, device=0)
+    check(m, layer, normal((T, H), g), *choice(T, E, K, g), "one tile a round")
     m.destroy()

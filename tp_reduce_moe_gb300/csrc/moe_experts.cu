@@ -322,12 +322,13 @@ DownPlan plan_down(int T, int K, int E, int I, int tiles) {  // tiles: of a CTA,
     p.piece = GS ? Scales<GS ? GS : 1>::piece(Fmt<GS>::scales(I)) : 0;
     p.step = p.shape.row_bytes <= kBox ? kSlotBytes / 2 : kSlotBytes;
     p.act_part = (2 * I + 511) / 512 * 512;
+    // The first that fits of: activations staged, entries 64 bytes off a multiple of 128 (no bank conflicts); the same with one
+    // tile a round; one tile a round, entries side by side; activations not staged.
     for (int option = GS ? 0 : 3;; ++option) {
         // sums of a round of tiles: all of them (one barrier in all) where that takes up to 48 KB, else as many as fit there
         const int most = 48 * 1024 / (kMvWarps * T * 64);
-        p.round = option % 3 == 2 || most < 1 ? 1 : tiles < most ? tiles : most;
-        // staged: entries 64 bytes off a multiple of 128 (no bank conflicts), or not
-        p.act_entry = option >= 3 ? 0 : 2 * p.act_part + (option < 2 ? 64 : 0);
+        p.round = option == 1 || option == 2 || most < 1 ? 1 : tiles < most ? tiles : most;
+        p.act_entry = option == 3 ? 0 : 2 * p.act_part + (option < 2 ? 64 : 0);
         p.items_at = (kMaxSlots + 1) * kMvWarps * 8 + p.round * kMvWarps * T * 64;
         p.ring_at = (p.items_at + Items::bytes(T * K, E) + 1023) / 1024 * 1024;
         const int slots = (kSmemLimit - p.ring_at - T * K * p.act_entry) / (kMvWarps * (p.step + kScales));
