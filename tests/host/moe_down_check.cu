@@ -1,4 +1,4 @@
-// Host check of which plan the experts' second product takes: the first that fits, of padded entries with a round's tiles,
+// Host check of the pieces that group scales are copied in, and of which plan the experts' second product takes: the first that fits, of padded entries with a round's tiles,
 // padded entries with one tile, entries without padding with one tile, and activations that are not staged.
 #include <cstdio>
 
@@ -31,7 +31,24 @@ static void check(int T, int K, int E, int I, int tiles) {
     }
 }
 
+// Rows of a multiple of eight scales take a tensor copy (0); so no piece is larger than 8 bytes, and 8 are a lane's half row
+// with two groups a step alone.
+template <int GS>
+static void pieces() {
+    bool met[9] = {};
+    for (int n = 1; n <= 4096; ++n) {
+        const int p = Scales<GS>::piece(n);
+        const bool right = p == 0 ? n % 8 == 0 : n % 8 != 0 && n * 2 % p == 0 && (p == 8 ? GS == 2 : p == 4 ? GS != 2 || n % 4 != 0 : p == 2 && n % 2 == 1);
+        if (!right && bad++ < 10) printf("GS %d, %d scales a row: pieces of %d\n", GS, n, p);
+        if (p >= 0 && p <= 8) met[p] = true;
+    }
+    if (!(met[0] && met[2] && met[4]) || met[8] != (GS == 2)) ++bad;
+}
+
 int main() {
+    pieces<1>();
+    pieces<2>();
+    pieces<4>();
     for (int T = 1; T <= 64; ++T)
         for (int K = 1; K <= 16; ++K)
             for (int I = 128; I <= 16384; I += I < 2048 ? 128 : 1024)

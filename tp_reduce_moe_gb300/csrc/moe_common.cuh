@@ -583,7 +583,7 @@ struct DirectColumns {
 // all the copies in flight, which takes two to three microseconds, more than a
 // segment's products.  Where rows have a multiple of eight they are a tensor copy
 // (of at least 16 bytes of a row: two segments' with one group a step), else each
-// lane copies half a row's in pieces of `piece` bytes, asynchronously, and
+// lane copies half a row's in pieces of `piece` bytes (8 or 4), asynchronously, and
 // arrives at the slot's barrier; rows of an odd number are copied by loads and
 // stores.
 template <int GS>
@@ -594,7 +594,7 @@ struct Scales {
     static constexpr int kWords = GS == 2 ? 1 : 2;           // of a row: all (one group a step), or a step's
     uint32_t raw[2][kWords];
     // 0: a tensor copy
-    __host__ static int piece(int row_scales) { return row_scales % 8 == 0 ? 0 : row_scales * 2 % kHalf == 0 ? kHalf : row_scales % 2 == 0 ? 4 : 2; }
+    __host__ static int piece(int row_scales) { return row_scales % 8 == 0 ? 0 : GS == 2 && row_scales % 4 == 0 ? 8 : row_scales % 2 == 0 ? 4 : 2; }
     __host__ __device__ static int arrivals(int piece) { return piece == 0 ? 1 : 33; }
     // where a segment's begin in a row of the slot
     __device__ static __forceinline__ int skip(int seg) { return GS == 1 ? (seg & 1) * 8 : 0; }
@@ -615,15 +615,8 @@ struct Scales {
         const int left = (row_scales - mine) * 2;  // bytes; none or less: zeros
         const uint16_t* from = base + (uint32_t)(PAIRS ? (row >= 8 ? second : 0) + min(row & 7, n - 1) : min(row, n - 1)) * row_scales;
         const uint32_t at = to + row * kPitch + (lane >> 4) * kHalf + skip(column / (4 * GS));
-        if (piece == kHalf) {
-            const uint16_t* p = left > 0 ? from + mine : from;
-            const int size = left > 0 ? kHalf : 0;
-            if constexpr (GS == 4)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(p), "r"(size) : "memory");
-            else if constexpr (GS == 2)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at), "l"(p), "r"(size) : "memory");
-            else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(p), "r"(size) : "memory");
+        if (GS == 2 && piece == 8) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at), "l"(left > 0 ? from + mine : from), "r"(left > 0 ? 8 : 0) : "memory");
         } else if (piece == 4) {
 #pragma unroll 1
             for (int o = 0; o < kHalf; o += 4)
