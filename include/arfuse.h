@@ -512,6 +512,7 @@ ARFUSE_API ar_status ar_finalize_rmsnorm_noalloc(const void* const* expert_out, 
 
 #define AR_MOE_SOFTMAX 0
 #define AR_MOE_SIGMOID 1
+#define AR_MOE_GROUP_MAX 0x10  /* added to either: a group counts with its largest c */
 
 typedef struct ar_moe ar_moe; /* opaque, library-owned */
 
@@ -571,12 +572,13 @@ ARFUSE_API ar_status ar_moe_inject_wait_timeout(ar_moe* moe, int product, int64_
  *   c = s + bias with a bias, s with expert groups and no bias, else l.
  *   Expert groups (n_group > 1): E / n_group consecutive experts form a group;
  *   only the topk_group groups with the largest sum of their two largest c
- *   take part.
+ *   take part, or, with AR_MOE_GROUP_MAX, with the largest c.  (Models whose
+ *   router has a bias use the sums as a rule, those without one the largest.)
  *   x        device bf16 [T, H]
  *   gate     device bf16 [E, H]
  *   bias     device fp32 [E], or NULL (minus infinity bars an expert as long
  *            as top_k others remain)
- *   scoring  AR_MOE_SOFTMAX or AR_MOE_SIGMOID
+ *   scoring  AR_MOE_SOFTMAX or AR_MOE_SIGMOID, with or without AR_MOE_GROUP_MAX
  *   renorm   1: divide the chosen scores by their sum (0 if that is 0)
  *   scale    factor of the routed weights
  *   n_group, topk_group  1, 1 for no groups; n_group divides E with at least

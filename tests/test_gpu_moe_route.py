@@ -29,25 +29,26 @@ def scores(l, sigmoid):
     return torch.sigmoid(l) if sigmoid else torch.softmax(l, dim=-1)
 
 
-def chosen(l, bias, K, sigmoid, n_group, topk_group):
+def chosen(l, bias, K, sigmoid, n_group, topk_group, group_max=False):
     """The ids of one token's logits `l` (64 bits), undefined choice values last, the lowest index first among equals."""
     s = scores(l, sigmoid)
     c = (l if bias is None and n_group == 1 else s if bias is None else s + bias.double()).tolist()
     c = [-INF if v != v else v for v in c]
     nan = [v != v for v in (l if bias is None and n_group == 1 else s if bias is None else s + bias.double()).tolist()]
     size = len(c) // n_group
-    best = [sum(sorted(c[j * size:(j + 1) * size])[-2:]) if size > 1 else c[j] for j in range(n_group)]
+    best = [sum(sorted(c[j * size:(j + 1) * size])[-1 if group_max else -2:]) for j in range(n_group)]
     kept = set(sorted(range(n_group), key=lambda j: (-best[j], j))[:topk_group])
     return sorted((e for e in range(len(c)) if e // size in kept), key=lambda e: (nan[e], -c[e], e))[:K]
 
 
-def check(x, gate, bias, K, sigmoid, n_group=1, topk_group=1, renorm=True):
+def check(x, gate, bias, K, sigmoid, n_group=1, topk_group=1, renorm=True, group_max=False):
     T, E = x.shape[0], gate.shape[0]
     l = x.double() @ gate.double().t()
-    want = torch.tensor([chosen(l[t], bias, K, sigmoid, n_group, topk_group) for t in range(T)], dtype=torch.int32)
+    want = torch.tensor([chosen(l[t], bias, K, sigmoid, n_group, topk_group, group_max) for t in range(T)], dtype=torch.int32)
     m = arf.ar_moe_create(E, K, x.shape[1], 0, T, device=0)
     ids, w = arf.ar_moe_route(m, x.to(DEV), gate.to(DEV), None if bias is None else bias.to(DEV),
-                              arf.AR_MOE_SIGMOID if sigmoid else arf.AR_MOE_SOFTMAX, renorm, 1.0, n_group, topk_group)
+                              (arf.AR_MOE_SIGMOID if sigmoid else arf.AR_MOE_SOFTMAX) | (arf.AR_MOE_GROUP_MAX if group_max else 0),
+                              renorm, 1.0, n_group, topk_group)
     ids, w = ids.cpu(), w.cpu().double()
     m.destroy()
     assert torch.equal(ids, want), [(t, ids[t].tolist(), want[t].tolist()) for t in range(T) if not torch.equal(ids[t], want[t])][:3]
@@ -107,7 +108,8 @@ def test_near_ties_with_terms_that_cancel(T):
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
-def test_groups_with_equal_and_undefined_choices(sigmoid, biased, renorm):
+@pytest.mark.parametrize("group_max", [False, True])
+def test_groups_with_equal_and_undefined_choices(sigmoid, biased, renorm, group_max):
     """Four groups of six, two of them kept: what 64-bit scores decide, group by group."""
     H, E, K, G, keep = 256, 24, 5, 4, 2
     g = gen(50 + sigmoid + 2 * biased)
@@ -125,20 +127,20 @@ def test_groups_with_equal_and_undefined_choices(sigmoid, biased, renorm):
         bias[18:24] = bias[12:18]
         bias[13] = bias[12]
         bias[[0, 1, 2, 6]] = -INF  # half a group barred, and one of another
-    check(x, gate, bias, K, sigmoid, G, keep, renorm)
+    check(x, gate, bias, K, sigmoid, G, keep, renorm, group_max)
     for t in range(7):  # alone, by the other split of the CTA's warps
-        check(x[t:t + 1], gate, bias, K, sigmoid, G, keep, renorm)
+        check(x[t:t + 1], gate, bias, K, sigmoid, G, keep, renorm, group_max)
     # the twin groups are the best two, then just one of them
     up = gate.clone()
     up[12:24] = (up[12:24].float() * 3).bfloat16()
     y = x.clone()
     y[0], y[4] = up[12] * 8, up[14] * 8
-    check(y, up, bias, K, sigmoid, G, keep, renorm)
-    check(y, up, bias, K, sigmoid, G, 1, renorm)
+    check(y, up, bias, K, sigmoid, G, keep, renorm, group_max)
+    check(y, up, bias, K, sigmoid, G, 1, renorm, group_max)
     # an expert whose logits are undefined
     up[14] = NAN
-    check(y, up, bias, K, sigmoid, G, keep, renorm)
-    check(y, up, None if bias is None else torch.full((E,), -INF), K, sigmoid, G, keep, renorm)
+    check(y, up, bias, K, sigmoid, G, keep, renorm, group_max)
+    check(y, up, None if bias is None else torch.full((E,), -INF), K, sigmoid, G, keep, renorm, group_max)
 
 
 def logits_as(values, H=64):
@@ -170,3 +172,20 @@ def test_scores_at_the_end_of_the_range(T):
             for bias in (None, torch.zeros(48), torch.full((48,), 1e-40)):
                 for groups, keep in ((1, 1), (8, 3), (24, 4)):
                     check(x, gate, bias, 6, sigmoid, groups, keep)
+
+
+@pytest.mark.parametrize("T,E,K,groups,keep", [(1, 160, 6, 8, 3), (3, 64, 4, 16, 2), (16, 256, 8, 8, 4), (33, 96, 6, 32, 5), (64, 160, 6, 8, 1)])
+def test_groups_by_their_largest(T, E, K, groups, keep):
+    """A group counts with its best expert: other groups than by the sums of two, for some tokens."""
+    g = gen(70 + T)
+    x = torch.randn(T, 1024, generator=g).bfloat16()
+    gate = (torch.randn(E, 1024, generator=g) / 32).bfloat16()
+    bias = torch.randn(E, generator=g) * 0.1
+    other = 0
+    for sigmoid in (False, True):
+        for b in (None, bias):
+            for renorm in (False, True):
+                by_max = check(x, gate, b, K, sigmoid, groups, keep, renorm, True)
+                other += int((by_max != check(x, gate, b, K, sigmoid, groups, keep, renorm, False)).any(1).sum())
+            check(x, gate, b, K, sigmoid, 1, 1, True, True)  # without groups it says nothing
+    assert T == 1 or other > 0

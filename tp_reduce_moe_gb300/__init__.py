@@ -20,5 +20,5 @@ from .binding import (  # noqa: F401
     AR_MAX_HC_STREAMS, ar_mhc_post, AR_MAX_SPLIT_PARTS, ar_workspace_set_split_rows,
     ar_workspace_set_split_column_groups, ar_workspace_inject_wait_timeout,
     AR_DEVERR_EXPERT_RANGE, AR_MAX_MATVEC_COLS, AR_MAX_MATVEC_ROWS, AR_MAX_MOE_EXPERTS, AR_MAX_MOE_GROUPS,
-    AR_MAX_MOE_TOKENS, AR_MOE_SIGMOID, AR_MOE_SOFTMAX, Moe, ar_matvec_w4, ar_moe_create, ar_moe_destroy,
+    AR_MAX_MOE_TOKENS, AR_MOE_GROUP_MAX, AR_MOE_SIGMOID, AR_MOE_SOFTMAX, Moe, ar_matvec_w4, ar_moe_create, ar_moe_destroy,
     ar_moe_device_error, ar_moe_inject_wait_timeout, ar_moe_experts, ar_moe_experts_w4, ar_moe_route)

@@ -49,6 +49,7 @@ AR_MAX_MATVEC_COLS = 65536
 AR_MAX_MATVEC_ROWS = 1048576
 AR_MOE_SOFTMAX = 0
 AR_MOE_SIGMOID = 1
+AR_MOE_GROUP_MAX = 0x10
 
 _lock = threading.Lock()
 _lib = None
@@ -583,7 +584,7 @@ def ar_moe_route(moe: Moe, x, gate, bias=None, scoring: int = AR_MOE_SIGMOID, re
 
     x: bf16 [T, H]; gate: bf16 [E, H]; bias: fp32 [E] or None.  n_group > 1
     keeps only the topk_group groups of E / n_group experts with the largest
-    sum of their two best.  Returns (ids int32, weights fp32), both
+    sum of their two best, or (scoring | AR_MOE_GROUP_MAX) the largest best.  Returns (ids int32, weights fp32), both
     [T, top_k + shared], allocated when not given."""
     T, dev = x.shape[0], _moe_device(moe)
     _need_on(dev, x, torch.bfloat16, (T, moe.H), "x")

@@ -215,7 +215,8 @@ ar_status ar_moe_route(ar_moe* m, const void* x, const void* gate, const float* 
                        int n_group, int topk_group, int64_t T, int32_t* ids, float* weights, void* stream) {
     ar_status st = check_call(m, T);
     if (st != AR_OK) return st;
-    if ((scoring != AR_MOE_SOFTMAX && scoring != AR_MOE_SIGMOID) || (renorm != 0 && renorm != 1)) return AR_ERR_INVALID_ARG;
+    const int function = scoring & ~AR_MOE_GROUP_MAX;
+    if ((function != AR_MOE_SOFTMAX && function != AR_MOE_SIGMOID) || (renorm != 0 && renorm != 1)) return AR_ERR_INVALID_ARG;
     if (n_group < 1 || n_group > AR_MAX_MOE_GROUPS || m->E % n_group != 0 || topk_group < 1 || topk_group > n_group ||
         (n_group > 1 && m->E / n_group < 2) || topk_group * (m->E / n_group) < m->K)
         return AR_ERR_INVALID_ARG;
@@ -246,7 +247,8 @@ ar_status ar_moe_route(ar_moe* m, const void* x, const void* gate, const float* 
     a.E = m->E;
     a.K = m->K;
     a.shared = m->S;
-    a.sigmoid = scoring == AR_MOE_SIGMOID;
+    a.sigmoid = function == AR_MOE_SIGMOID;
+    a.group_max = (scoring & AR_MOE_GROUP_MAX) != 0;
     a.renorm = renorm;
     a.n_group = n_group;
     a.topk_group = topk_group;

@@ -46,7 +46,7 @@ struct RouteArgs {
     float2* logits;        // scratch [T, E], high and low part
     unsigned* count;       // scratch, one arrival counter per token group (zero between calls)
     int T, H, E, K, shared;
-    int sigmoid, renorm, n_group, topk_group;
+    int sigmoid, renorm, n_group, topk_group, group_max;
     float scale;
 };
 

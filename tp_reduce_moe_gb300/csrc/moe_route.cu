@@ -3,7 +3,7 @@
 //   l[t,e] = x[t] . gate[e];  s = softmax_e(l) or sigmoid(l)
 //   c = l, or s + bias (with a bias or expert groups)
 //   expert groups: only the topk_group groups with the largest sum of their two
-//   best c stay; ids[t] = the top_k largest c, lowest index first among equals
+//   best c (or the largest best c) stay; ids[t] = the top_k largest c, lowest index first among equals
 //   weights[t] = s[ids], optionally over their sum, times scale
 //
 // One CTA per (expert, four tokens) computes four dot products; the last CTA of
@@ -144,7 +144,7 @@ __device__ __noinline__ void store_choice(const RouteArgs& a, int token, int lan
     }
 }
 
-// The choice in 32 bits, for every token of the CTA at once: 1 << kShift tokens, the
+// The choice in 32 bits, for every token of the CTA at once, the
 // CTA's warps dealt to them evenly, warp `part` of a token's first.  What the
 // tokens' warps tell each other goes through Part; False in `good` if some gap
 // that decides is too narrow, or something is not a number: nothing is chosen then.
@@ -233,7 +233,7 @@ __device__ void choose32(const RouteArgs& a, int token, bool live, int part, int
         __syncthreads();
     }
     if (a.n_group > 1) {
-        // a group's two best, a group per warp
+        // a group's two best (or the best), a group per warp
         const int size = quotient(a.E, a.n_group);
 #pragma unroll 1
         for (int j = part; live && j < a.n_group; j += kParts) {
@@ -247,7 +247,7 @@ __device__ void choose32(const RouteArgs& a, int token, bool live, int part, int
             const unsigned first = __reduce_max_sync(0xffffffffu, b0);
             const int holder = __ffs(__ballot_sync(0xffffffffu, b0 == first)) - 1;
             const unsigned second = __reduce_max_sync(0xffffffffu, lane == holder ? b1 : b0);
-            const float c0 = from_ordered32(first), c1 = from_ordered32(second);
+            const float c0 = from_ordered32(first), c1 = a.group_max ? 0.0f : from_ordered32(second);
             if (lane == 0) groups[j] = Group{ordered32(c0 + c1), fabsf(c0) < INFINITY && fabsf(c1) < INFINITY ? fabsf(c0) + fabsf(c1) : 0.0f};
         }
         __syncthreads();
@@ -377,7 +377,7 @@ __device__ __noinline__ void choose(const RouteArgs& a, int token, int lane, dou
     __syncwarp();
     if (a.n_group > 1) {
         const int size = a.E / a.n_group;
-        // lane = group: the sum of its two best
+        // lane = group: the sum of its two best, or the best
         long long mine = kNone;
         if (lane < a.n_group) {
             double b0 = -INFINITY, b1 = -INFINITY;
@@ -390,7 +390,7 @@ __device__ __noinline__ void choose(const RouteArgs& a, int token, int lane, dou
                     b1 = c;
                 }
             }
-            mine = ordered(b0 + b1);
+            mine = ordered(a.group_max ? b0 : b0 + b1);
         }
         unsigned kept = 0;
         bool out = lane >= a.n_group;
