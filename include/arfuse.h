@@ -587,8 +587,10 @@ ARFUSE_API ar_status ar_moe_inject_wait_timeout(ar_moe* moe, int product, int64_
  *   ids      device int32 [T, top_k + S]: chosen experts, then the shared ones
  *   weights  device fp32 [T, top_k + S]: weights (1 for the shared experts)
  * The choice is that of 64-bit scores: logits carry about 45 bits, so neither
- * T nor the GPU's summation order moves it.  NaN choices rank last; ids are
- * always distinct experts.  T == 0 returns AR_OK.
+ * T nor the GPU's summation order moves it.  (Products and sums are two fp32
+ * words: logits of 2^128 and more are infinite, and bits of products below 2^-149
+ * are lost.)  NaN choices rank last; ids are always distinct experts.  T == 0
+ * returns AR_OK.
  * Errors: AR_ERR_INVALID_ARG (NULL, ranges above, an output overlapping an
  * input or the other), AR_ERR_ALIGNMENT (x, gate 16 bytes, the others 4),
  * AR_ERR_CAPACITY (T > max_tokens), AR_ERR_CUDA.  The handle's device must be
@@ -646,6 +648,9 @@ ARFUSE_API ar_status ar_moe_experts_w4(ar_moe* moe, const void* x, const int32_t
  *   T      0 .. AR_MAX_MOE_TOKENS (0 returns AR_OK)
  *   N, K   1 .. AR_MAX_MATVEC_ROWS, group .. AR_MAX_MATVEC_COLS
  *   out    device [T, N], bf16 or (out_is_fp32 = 1) fp32
+ * Meant for few tokens: nine and more are taken in groups of up to eight, each of
+ * which unpacks the matrix again, so that from some sixteen tokens on a bf16 copy
+ * of the matrix in a library product is faster.
  * A token with an |x| of 2^101 or more, an infinity or a NaN gets NaN.  Sums are
  * fp32; deterministic, but their order may depend on T.  Should the bounded wait
  * for a copy run out (nothing known makes it), what needed the copy is NaN; with no

@@ -6,11 +6,14 @@
 // is cut into sixteen equal ranges, one per warp.  More than eight tokens make
 // groups of up to eight, each with its share of the SMs; neighbouring CTAs take
 // the same rows for them, once from memory and else from L2.  (13 tokens with
-// 18431 rows of 8192: 41 us; one CTA for one group after the other 49, staging the
+// 18431 rows of 8192: 42 us; one CTA for one group after the other 49, staging the
 // activations twice as often; sixteen columns at a time 60: no registers left.)
 //
-// One token: 36864 x 7168 in groups of 64 takes 25.9 us, 0.80 of the copy rate;
-// 7168 x 2048 takes 4.3 us, launch and two trips to memory.  The 13 tokens' 41 us
+// One token: 36864 x 7168 in groups of 64 takes 26.5 us, 0.78 of the copy rate;
+// 7168 x 2048 takes 4.3 us, launch and two trips to memory.  Of 18431 x 8192 two
+// tokens take 19.6 us (0.64), eight 25.6 (0.49), sixteen 41, 32 91 and 64 178: each
+// group of eight takes the codes out again, and from some sixteen tokens on the
+// same matrix in bf16, read once in 44 us, is the better one.  The 13 tokens' 42 us
 // are 0.30, bound by the reads of the activations from shared memory, 512 bytes
 // per eight columns of weights a lane, twice the weights' own, and by staging them.
 #include "moe_common.cuh"

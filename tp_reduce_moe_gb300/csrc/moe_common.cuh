@@ -14,9 +14,14 @@
 // tensor copies of eight rows by 128 bytes, four times as many to issue.)
 // A kilobyte of weights takes the memory 44 cycles to deliver to an SM; the
 // matrix instructions for it take 4 (bf16) to 16 (4-bit) on each of its four
-// schedulers, and taking the codes out as long again, so that what counts is the
-// instructions: bf16 weights come at the memory's rate, 4-bit ones at 55 to 80 %
-// of it (half the issue slots busy, half the integer pipe).  A tcgen05 tile of
+// schedulers, and taking the codes out as long again.  bf16 weights come at the
+// memory's rate, 4-bit ones at 50 to 80 % of it for up to eight tokens: no pipe is
+// full then (issue slots 33 to 54 %, integer pipe 34 to 53), four warps a scheduler
+// wait for their own dependent instructions, one of them ready on average.  So
+// fewer instructions help, and more independent ones would.  More than eight tokens
+// of one expert or matrix take the weights, and the codes out of them, once for
+// every eight (four in the experts' second product): 30 % for 13 tokens, 7 % for
+// 64.  A tcgen05 tile of
 // 128 rows would need all its operands in shared memory, the 4-bit codes expanded
 // there first, and pay in granularity: at one token an SM owns about 27 rows of
 // the first product.

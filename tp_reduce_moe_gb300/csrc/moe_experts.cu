@@ -4,10 +4,11 @@
 //
 // Two kernels: the first writes the activations a of every (token, expert)
 // slot, the second the sums y; both wait on memory with bf16 weights (64 tokens
-// with 8 of 256 experts of 3 x 256 x 7168: 365 us, 0.99 of the copy rate; one token
-// 18.4 us, 0.70: start, end and the way from one kernel to the other take 6 us).  Both read each chosen expert's weights once,
-// whichever tokens chose it, and deal weight rows evenly over the SMs: the
-// first kernel flattens (chosen expert, row pair), the second gives every CTA
+// with 8 of 256 experts of 3 x 256 x 7168: 367 us, 0.98 of the copy rate; one token
+// 18.6 us, 0.70: start, end and the way from one kernel to the other take 6 us).
+// Both read each chosen expert's weights from memory once, whichever tokens chose
+// it (from L2 again for every item of its tokens: 64 tokens with 2 of 8 experts
+// reach 0.44), and deal weight rows evenly over the SMs: the first kernel flattens (chosen expert, row pair), the second gives every CTA
 // its share of the H output rows for all chosen experts, so that the sum over
 // a token's experts never leaves the CTA: no atomics, one rounding.
 //
@@ -281,6 +282,8 @@ struct GateUp {
     }
 };
 
+// (With 512 threads there are 128 registers for each; groups of 64 and 32 spill 8
+// and 72 bytes.)
 template <int GS>
 __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid_constant__ ExpertsArgs a, const __grid_constant__ Weights weights,
                                                                        const __grid_constant__ ProductPlan plan) {
@@ -305,10 +308,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) moe_gate_up_kernel(const __grid
 //
 // 4-bit weights: the activations are copied to shared memory once, every warp's
 // by itself, if there is room for all.  Loads of them come back behind the
-// copies in flight, two to three microseconds later.  What is left to do then is
-// bound by the instructions: twice the matrix instructions of the first product,
-// since the codes' offset is taken off by them (one token, 8 experts of 7168 x 2048:
-// 16 us, 0.55 of the copy rate).
+// copies in flight, two to three microseconds later.  What is left takes twice the
+// matrix instructions of the first product, since the codes' offset is taken off by
+// them, again for every tile (one token, 8 experts of 7168 x 2048: 16 us, 0.55 of
+// the copy rate, with the issue slots a third busy and the tensor pipe too: chains
+// of instructions that wait for each other).
 struct DownPlan {
     RowShape shape;
     int round, items_at, ring_at, scales_at, slots, step, smem, piece;

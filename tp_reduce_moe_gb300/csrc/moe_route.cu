@@ -9,16 +9,18 @@
 // One CTA per (expert, four tokens) computes four dot products; the last CTA of
 // a token group to arrive chooses.  The choice must not
 // depend on how a sum was split, so the sums carry a second word: bf16
-// products are exact in fp32, and each addition's error is kept (two-sum), which
-// leaves a relative error of about 2^-45 of the sum of magnitudes.  Scores are
+// products are exact in fp32 (between 2^-126 and 2^128), and each addition's error
+// is kept (two-sum), which leaves a relative error of about 2^-45 of the sum of
+// magnitudes.  Scores are
 // formed and compared in 32 bits where the gaps between the chosen are wider than
 // what 32 bits can get wrong, else (one token in some thousands) in 64 bits,
 // whose rate on this GPU is 1/64 of that; the weights of the chosen always are.
 //
 // Bound by latency: the gate is read in 1.5 us, the arrivals take 1.2, the choice
 // 3.9 (a chain of top_k + 1 reductions at its end) and the weights 2.  One token of
-// 256 experts in groups takes 9.3 us, 16 tokens 14.9, 64 tokens (bound by the
-// two-sums, seven operations a product) 20.3.
+// 256 experts in groups takes 9.4 us, 16 tokens of 160 experts 15.1, 64 tokens of 128
+// 20.5: there the two-sums take about 10, seven operations for every product,
+// although only near ties and the chosen experts need them.
 #include "moe_common.cuh"
 
 namespace arf {
