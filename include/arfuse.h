@@ -90,6 +90,9 @@ typedef enum ar_status {
 #define AR_DEVERR_PERM_RANGE 0x1   /* some perm value was outside [0, rows_e); clamped */
 #define AR_DEVERR_TIMEOUT 0x2      /* a pipeline wait gave up after its time limit     */
 #define AR_DEVERR_EXPERT_RANGE 0x4 /* some expert id was neither -1 nor an expert; skipped (ar_moe_device_error) */
+#define AR_DEVERR_PAGE_RANGE 0x8   /* some page of a sequence was outside the cache; its tokens were left out (ar_attn_device_error) */
+#define AR_DEVERR_SLOT_RANGE 0x10  /* some slot was neither -1 nor in the cache; its token was not written (ar_attn_device_error) */
+#define AR_DEVERR_LENGTH_RANGE 0x20 /* some length was negative or beyond the page table; clamped (ar_attn_device_error) */
 
 /* Kernel regimes (ar_workspace_set_regime / ar_workspace_last_regime). */
 #define AR_REGIME_AUTO 0     /* pick by (T, R, K, H) and the SM count                    */
@@ -224,6 +227,33 @@ ARFUSE_API ar_status ar_rmsnorm(ar_workspace* ws, const void* const* partials, i
                                 float weight_bias, float eps, int64_t T, int H,
                                 void* out, void* residual_out, int residual_out_is_fp32,
                                 void* stream);
+
+/*
+ * ar_rmsnorm with an 8-bit output and its scales, as a product of 8-bit matrices
+ * takes it.  (No counterpart on the pages, whose output is bf16: an addition of
+ * this library.)  With y the normalised row before any rounding,
+ *
+ *   s[t,g] = max |y[t,j]| / 448 over the columns j of group g     (1 if all are 0)
+ *   q[t,j] = y[t,j] / s[t,g] rounded to e4m3 (448 is its largest value)
+ *
+ * in one pass, from the fp32 sums.
+ *   group         columns that share a scale: 32, 64, 128, or 0 for the whole row;
+ *                 a row's last group may be shorter.  Others: AR_ERR_UNSUPPORTED
+ *   q             device e4m3 (a byte each) [T, H], 8-byte aligned
+ *   scales        device fp32 [T, ceil(H / group)] ([T, 1] for group 0)
+ *   out           device bf16 [T, H]: y rounded once, as ar_rmsnorm gives it; or NULL
+ *   residual_out  as for ar_rmsnorm, in place over residual too
+ * The other arguments, limits and errors are ar_rmsnorm's; the outputs overlap
+ * neither an input nor each other.  With AR_WS_NORM_BF16_H the norm reads h rounded
+ * to bf16.  A row that holds an infinity or a NaN gets NaN scales wherever y has one
+ * (NaN codes with them).  A scale is at least 2^-126: smaller values of y are subnormal
+ * multiples of it.  Its regime controls have no effect here.
+ */
+ARFUSE_API ar_status ar_rmsnorm_q8(ar_workspace* ws, const void* const* partials, int R,
+                                   const void* residual, const void* gamma, float weight_bias,
+                                   float eps, int64_t T, int H, int group, void* q, float* scales,
+                                   void* out, void* residual_out, int residual_out_is_fp32,
+                                   void* stream);
 
 /*
  * Read and clear the workspace's device error word (AR_DEVERR_* bits) into
@@ -661,6 +691,145 @@ ARFUSE_API ar_status ar_moe_experts_w4(ar_moe* moe, const void* x, const int32_t
  */
 ARFUSE_API ar_status ar_matvec_w4(const void* x, const void* q, const void* s, int group, int64_t T,
                                   int64_t N, int64_t K, void* out, int out_is_fp32, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The attention of a decode layer: rotary positions with the write of the new
+ * keys and values into a paged cache, and the attention of one new token over
+ * that cache.  (No counterpart on the pages: an addition of this library.)
+ * They stand between the q/k/v projection (ar_matvec_w4 gives its rows) and the
+ * output projection, whose partial ar_rmsnorm takes.
+ *
+ * The cache is the caller's: `pages` pages of `page_size` tokens, each with a key
+ * and a value of head_dim values for each key-value head.  Element (page, token,
+ * head, d) of k lies at k + page * k_page + token * k_token + head * k_head + d (in
+ * elements), so that pages of tokens of heads, pages of heads of tokens, and keys
+ * and values in one tensor are all possible.  It holds bf16, or (scales given)
+ * e4m3 bytes that stand for byte * scale[head].
+ */
+#define AR_MAX_ATTN_HEADS 256     /* query heads                              */
+#define AR_MAX_ATTN_SEQS 4096     /* sequences of ar_attn_decode              */
+#define AR_MAX_ATTN_TOKENS 65536  /* tokens of one ar_attn_append             */
+#define AR_MAX_PAGE_SIZE 65536    /* tokens of a page                         */
+#define AR_MAX_ROPE_AXES 4
+
+typedef struct ar_attn ar_attn; /* opaque, library-owned */
+
+typedef struct ar_kv_cache {
+    void* k;                          /* device, 16-byte aligned                               */
+    void* v;
+    int64_t pages;                    /* 1 ..; pages * page_size <= 2^31 - 1                   */
+    int64_t k_page, k_token, k_head;  /* strides in elements: multiples of 16 bytes, at least  */
+    int64_t v_page, v_token, v_head;  /* head_dim, no two elements at one place                */
+    const float* k_scale;             /* device fp32 [kv_heads], 4-byte aligned: an e4m3 cache */
+    const float* v_scale;             /* both NULL: a bf16 cache                               */
+} ar_kv_cache;
+
+/*
+ * Create the handle of a model's attention layers (shared by the layers, as a
+ * workspace is).  Allocates on `device` its scratch: parts of rows split over
+ * several CTAs (32 * SMs * head_dim fp32: 2.5 MB at head_dim 128 on 152 SMs), their
+ * counters, the rotary table and the error word.  Calls on one handle must be
+ * ordered on the GPU (one stream, or event ordering; graphs captured on it must not
+ * run at the same time); concurrent callers need a handle each.  Call it outside
+ * any stream capture.
+ *   heads      query heads, 1 .. AR_MAX_ATTN_HEADS
+ *   kv_heads   key-value heads, a divisor of heads; query head h reads key-value
+ *              head h / (heads / kv_heads)
+ *   head_dim   64, 128 or 256
+ *   page_size  tokens of a page, 1 .. AR_MAX_PAGE_SIZE, any number
+ *   max_seqs   most sequences of an ar_attn_decode call, 1 .. AR_MAX_ATTN_SEQS
+ *   flags      0, or any of AR_WS_DRY_RUN, AR_WS_PDL (as for a workspace)
+ *   out        receives the handle (NULL on error)
+ * Errors: AR_ERR_INVALID_ARG (out NULL, counts below 1, kv_heads no divisor,
+ * unknown flags), AR_ERR_UNSUPPORTED (head_dim, limits above, or a device older
+ * than sm_100), AR_ERR_CUDA.
+ */
+ARFUSE_API ar_status ar_attn_create(int device, int heads, int kv_heads, int head_dim, int page_size,
+                                    int64_t max_seqs, unsigned flags, ar_attn** out);
+
+/* Free the handle.  NULL is accepted.  No call using it may still be running. */
+ARFUSE_API ar_status ar_attn_destroy(ar_attn* attn);
+
+/* Read and clear the handle's error word, as ar_workspace_device_error:
+ * AR_DEVERR_PAGE_RANGE, AR_DEVERR_SLOT_RANGE, AR_DEVERR_LENGTH_RANGE. */
+ARFUSE_API ar_status ar_attn_device_error(ar_attn* attn, int* code);
+
+/*
+ * Set the rotary positions of later ar_attn_append calls (none before the first
+ * call).  Pair i < rot / 2 of a head's first `rot` columns is turned by the angle
+ * freq[i] * (position of the token on axis[i]); the columns behind stay as they are.
+ *   rot          rotated columns, a multiple of 16, 0 .. head_dim (0: none, no axes)
+ *   interleaved  0: pair i is columns i and i + rot / 2; 1: columns 2 i and 2 i + 1
+ *   axes         position axes, 1 .. AR_MAX_ROPE_AXES (time, height, width, ...)
+ *   freq         host fp64 [rot / 2]: radians a position, finite (any scaling of
+ *                long contexts is in them)
+ *   axis         host int32 [rot / 2], 0 .. axes - 1; NULL: axis 0 for all
+ * Angles are formed and reduced in fp64.  Copies the table to the device and waits
+ * for that: call it outside any stream capture, with no ar_attn_append of this
+ * handle running.
+ * Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (rot not a multiple of 16),
+ * AR_ERR_CUDA.  The table before stays in force on an error, but for AR_ERR_CUDA.
+ */
+ARFUSE_API ar_status ar_attn_set_rope(ar_attn* attn, int rot, int interleaved, int axes,
+                                      const double* freq, const int32_t* axis);
+
+/*
+ * Turn the q and k heads of T tokens and write k and v into the cache.
+ *   cache      host pointer, read during the call only
+ *   qkv        device bf16 [T, (heads + 2 kv_heads) * head_dim]: a token's q heads,
+ *              then its k heads, then its v heads, as one projection gives them
+ *   positions  device int32 [axes, T]; NULL if no rotary positions are set
+ *   slots      device int32 [T]: page * page_size + token in the page, or -1 (a
+ *              padded row: its k and v are not written).  Another value is skipped
+ *              too and sets AR_DEVERR_SLOT_RANGE.  Of several tokens with one slot
+ *              the last is the one that stands in the cache after the call.
+ *   T          0 .. AR_MAX_ATTN_TOKENS
+ *   q          device bf16 [T, heads * head_dim]: the turned q heads
+ * k and v in 8 bits: value / scale[head] rounded to e4m3, larger values than 448 to
+ * 448, NaN to NaN.  Turned values are fp32, rounded once.  Nothing else of the cache
+ * is touched.  q, k and v overlap no other argument.
+ * Errors: AR_ERR_INVALID_ARG (NULL, negative T, pages < 1, strides that put two
+ * elements at one place, one of two scales, k and v at one address, q or the cache
+ * overlapping an input), AR_ERR_ALIGNMENT (qkv, q, k, v, the strides 16 bytes, the
+ * others 4), AR_ERR_UNSUPPORTED (pages * page_size), AR_ERR_CAPACITY (T),
+ * AR_ERR_CUDA.  The handle's device must be the current one (else
+ * AR_ERR_INVALID_ARG).
+ */
+ARFUSE_API ar_status ar_attn_append(ar_attn* attn, const ar_kv_cache* cache, const void* qkv,
+                                    const int32_t* positions, const int32_t* slots, int64_t T,
+                                    void* q, void* stream);
+
+/*
+ * Attention of one new token of each of B sequences over their cached tokens
+ * (its own among them, written before):
+ *   s_j = scale * q . k_j for the last `window` of length[b] tokens (all, for
+ *   window 0); out = sum_j softmax(s)_j v_j; lse = log sum_j exp(s_j)
+ *   q           device bf16 [B, heads * head_dim]
+ *   page_table  device int32 [B, table_stride], of which the first `table_width`
+ *               of a row are read: the page of tokens i * page_size and on.  Only
+ *               pages that a sequence's length (and window) reaches are looked at;
+ *               one outside the cache sets AR_DEVERR_PAGE_RANGE and its tokens are
+ *               left out.
+ *   lengths     device int32 [B]; 0: a row of zeros, lse minus infinity.  A negative
+ *               one counts as 0, one beyond table_width * page_size as that; both
+ *               set AR_DEVERR_LENGTH_RANGE.
+ *   B           0 .. the handle's max_seqs
+ *   window      0 (no window) or the number of tokens looked at, the new one among them
+ *   scale       finite, also times log2(e); 1 / sqrt(head_dim) as a rule
+ *   out         device bf16 [B, heads * head_dim]
+ *   lse         device fp32 [B, heads], or NULL
+ * Values of the cache outside the tokens looked at may be anything.  Sums and the
+ * softmax are fp32; deterministic for given lengths and GPU; the order of a sum may
+ * depend on the other sequences of the batch.  One launch; the split of the work
+ * over the SMs follows the lengths on the device, so a captured call serves any.
+ * Errors as for ar_attn_append, and AR_ERR_CAPACITY (B > max_seqs); page_table and
+ * lengths 4-byte aligned; table_stride >= table_width.
+ */
+ARFUSE_API ar_status ar_attn_decode(ar_attn* attn, const ar_kv_cache* cache, const void* q,
+                                    const int32_t* page_table, int64_t table_width,
+                                    int64_t table_stride, const int32_t* lengths, int64_t B,
+                                    int64_t window, float scale, void* out, float* lse, void* stream);
 
 /* Static description of a status code; never NULL.  Every status other than
  * AR_OK / AR_VALIDATED is a clean decline: nothing was launched and the

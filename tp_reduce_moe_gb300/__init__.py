@@ -21,4 +21,7 @@ from .binding import (  # noqa: F401
     ar_workspace_set_split_column_groups, ar_workspace_inject_wait_timeout,
     AR_DEVERR_EXPERT_RANGE, AR_MAX_MATVEC_COLS, AR_MAX_MATVEC_ROWS, AR_MAX_MOE_EXPERTS, AR_MAX_MOE_GROUPS,
     AR_MAX_MOE_TOKENS, AR_MOE_GROUP_MAX, AR_MOE_SIGMOID, AR_MOE_SOFTMAX, Moe, ar_matvec_w4, ar_moe_create, ar_moe_destroy,
-    ar_moe_device_error, ar_moe_inject_wait_timeout, ar_moe_experts, ar_moe_experts_w4, ar_moe_route)
+    ar_moe_device_error, ar_moe_inject_wait_timeout, ar_moe_experts, ar_moe_experts_w4, ar_moe_route,
+    AR_DEVERR_LENGTH_RANGE, AR_DEVERR_PAGE_RANGE, AR_DEVERR_SLOT_RANGE, AR_MAX_ATTN_HEADS, AR_MAX_ATTN_SEQS,
+    AR_MAX_ATTN_TOKENS, AR_MAX_PAGE_SIZE, AR_MAX_ROPE_AXES, Attn, KvCache, ar_attn_append, ar_attn_create, ar_attn_decode,
+    ar_attn_destroy, ar_attn_device_error, ar_attn_set_rope, ar_kv_cache, ar_rmsnorm_q8)

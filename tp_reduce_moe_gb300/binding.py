@@ -33,6 +33,9 @@ AR_WS_PDL = 0x4
 AR_DEVERR_PERM_RANGE = 0x1
 AR_DEVERR_TIMEOUT = 0x2
 AR_DEVERR_EXPERT_RANGE = 0x4
+AR_DEVERR_PAGE_RANGE = 0x8
+AR_DEVERR_SLOT_RANGE = 0x10
+AR_DEVERR_LENGTH_RANGE = 0x20
 AR_REGIME_AUTO = 0
 AR_REGIME_CLUSTER = 1
 AR_REGIME_STREAM = 2
@@ -50,6 +53,11 @@ AR_MAX_MATVEC_ROWS = 1048576
 AR_MOE_SOFTMAX = 0
 AR_MOE_SIGMOID = 1
 AR_MOE_GROUP_MAX = 0x10
+AR_MAX_ATTN_HEADS = 256
+AR_MAX_ATTN_SEQS = 4096
+AR_MAX_ATTN_TOKENS = 65536
+AR_MAX_PAGE_SIZE = 65536
+AR_MAX_ROPE_AXES = 4
 
 _lock = threading.Lock()
 _lib = None
@@ -132,6 +140,20 @@ def load_library(path: str | None = None):
         lib.ar_moe_experts_w4.argtypes = [P, P, P, P, P, P, P, P, I, I64, P, P]
         lib.ar_matvec_w4.restype = I
         lib.ar_matvec_w4.argtypes = [P, P, P, I, I64, I64, I64, P, I, P]
+        lib.ar_rmsnorm_q8.restype = I
+        lib.ar_rmsnorm_q8.argtypes = [P, P, I, P, P, F, F, I64, I, I, P, P, P, P, I, P]
+        lib.ar_attn_create.restype = I
+        lib.ar_attn_create.argtypes = [I, I, I, I, I, I64, U, ctypes.POINTER(P)]
+        lib.ar_attn_destroy.restype = I
+        lib.ar_attn_destroy.argtypes = [P]
+        lib.ar_attn_device_error.restype = I
+        lib.ar_attn_device_error.argtypes = [P, ctypes.POINTER(I)]
+        lib.ar_attn_set_rope.restype = I
+        lib.ar_attn_set_rope.argtypes = [P, I, I, I, P, P]
+        lib.ar_attn_append.restype = I
+        lib.ar_attn_append.argtypes = [P, P, P, P, P, I64, P, P]
+        lib.ar_attn_decode.restype = I
+        lib.ar_attn_decode.argtypes = [P, P, P, P, I64, I64, P, I64, I64, F, P, P, P]
         lib.ar_status_string.restype = ctypes.c_char_p
         lib.ar_status_string.argtypes = [I]
         _lib = lib
@@ -461,6 +483,46 @@ def ar_rmsnorm(ws: Workspace, partials, residual, gamma, weight_bias: float, eps
     return out, residual_out
 
 
+def ar_rmsnorm_q8(ws: Workspace, partials, residual, gamma, weight_bias: float, eps: float, group: int = 128,
+                  q=None, scales=None, residual_out=None, residual_out_fp32: bool = False, out=None, stream=None):
+    """ar_rmsnorm with an 8-bit output: ``q`` float8_e4m3fn [T, H] and ``scales`` fp32
+    [T, ceil(H / group)] (``group`` 32, 64, 128, or 0: one scale a row) stand for the
+    normalised rows q * scale.  ``out`` (bf16 [T, H]), when given, receives them unscaled
+    as well.  ``residual_out`` may be ``residual`` (in place, bf16 only).  Returns (q,
+    scales, residual_out), allocated when not given."""
+    R, H, T = ws.R, ws.H, residual.shape[0]
+    dev = None if ws.dry_run else ws.device
+    if len(partials) != R:
+        raise ValueError(f"partials has {len(partials)} entries, workspace has R={R}")
+    if group not in (0, 32, 64, 128):
+        raise ArfuseError(AR_ERR_UNSUPPORTED, f"group {group} (0, 32, 64 or 128)")
+    for r, p in enumerate(partials):
+        _need_on(dev, p, torch.bfloat16, (T, H), "partials", r)
+    _need_on(dev, residual, torch.bfloat16, (T, H), "residual")
+    _need_on(dev, gamma, torch.bfloat16, (H,), "gamma")
+    res_type = torch.float32 if residual_out_fp32 else torch.bfloat16
+    shape = (T, -(-H // group) if group else 1)
+    if q is None:
+        q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=residual.device)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=residual.device)
+    if residual_out is None:
+        residual_out = torch.empty((T, H), dtype=res_type, device=residual.device)
+    _need_on(dev, q, torch.float8_e4m3fn, (T, H), "q")
+    _need_on(dev, scales, torch.float32, shape, "scales")
+    _need_on(dev, residual_out, res_type, (T, H), "residual_out")
+    if out is not None:
+        _need_on(dev, out, torch.bfloat16, (T, H), "out")
+    p_arr = _ptr_array(partials)
+    st = load_library().ar_rmsnorm_q8(
+        ws.handle if ws.alive else None, ctypes.addressof(p_arr), R, residual.data_ptr(), gamma.data_ptr(), float(weight_bias), float(eps), T, H,
+        int(group), q.data_ptr(), scales.data_ptr(), _ptr(out), residual_out.data_ptr(), 1 if residual_out_fp32 else 0,
+        None if ws.dry_run else _stream_handle(stream, ws.device))
+    if st != AR_OK:
+        _check(st, "ar_rmsnorm_q8", ok=(AR_VALIDATED,) if ws.dry_run else ())
+    return q, scales, residual_out
+
+
 AR_MAX_HC_STREAMS = 8
 
 
@@ -559,12 +621,12 @@ def ar_moe_inject_wait_timeout(moe: Moe, product: int, limit_ns: int) -> None:
     _check(load_library().ar_moe_inject_wait_timeout(moe.handle, int(product), int(limit_ns)), "ar_moe_inject_wait_timeout")
 
 
-def _need_on(device, t, dtype, shape, name):
+def _need_on(device, t, dtype, shape, name, index=None):
     """A contiguous tensor of this type and shape on CUDA device ``device``
     (None: anywhere -- a dry run only looks at addresses)."""
     if t.dtype is dtype and t.shape == shape and t.is_contiguous() and (device is None or t.get_device() == device):
         return
-    _need(t, dtype, shape, name)
+    _need(t, dtype, shape, name, index)
     raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
 
 
@@ -681,3 +743,191 @@ def ar_matvec_w4(x, q, s, group: int, out=None, out_fp32: bool = False, stream=N
                                      1 if out_fp32 else 0, _stream_handle(stream, dev))
     _check(st, "ar_matvec_w4")
     return out
+
+
+# ------------------------------------------------------- attention of a decode layer
+class Attn:
+    """Owner of one ``ar_attn*`` (fixed heads, kv_heads, head_dim, page_size, max_seqs)."""
+
+    def __init__(self, handle: int, heads: int, kv_heads: int, head_dim: int, page_size: int, max_seqs: int,
+                 device: int, dry_run: bool):
+        self.handle = handle
+        self.heads, self.kv_heads, self.head_dim, self.page_size = heads, kv_heads, head_dim, page_size
+        self.max_seqs, self.device, self.dry_run = max_seqs, device, dry_run
+        self.axes = 0
+        self._fin = weakref.finalize(self, _destroy_attn_handle, handle)
+
+    def destroy(self):
+        self.handle = None
+        self._fin()
+
+    @property
+    def alive(self) -> bool:
+        return self._fin.alive
+
+
+def _destroy_attn_handle(handle):
+    if handle:
+        load_library().ar_attn_destroy(ctypes.c_void_p(handle))
+
+
+def ar_attn_create(heads: int, kv_heads: int, head_dim: int, page_size: int, max_seqs: int,
+                   device: int | None = None, flags: int = 0) -> Attn:
+    """Handle of a model's attention layers: ``heads`` query heads that share ``kv_heads``
+    key-value heads of ``head_dim`` (64, 128 or 256) columns, a cache in pages of
+    ``page_size`` tokens, up to ``max_seqs`` sequences a call.  `device` and `flags` as for
+    ar_workspace_create (AR_WS_DRY_RUN, AR_WS_PDL)."""
+    lib = load_library()
+    dry = bool(flags & AR_WS_DRY_RUN)
+    if device is None:
+        device = torch.cuda.current_device() if not dry else 0
+    h = ctypes.c_void_p()
+    _check(lib.ar_attn_create(int(device), int(heads), int(kv_heads), int(head_dim), int(page_size), int(max_seqs),
+                              int(flags), ctypes.byref(h)), "ar_attn_create")
+    return Attn(h.value, int(heads), int(kv_heads), int(head_dim), int(page_size), int(max_seqs), int(device), dry)
+
+
+def ar_attn_destroy(attn: Attn) -> None:
+    """Free the handle (no call on it may still be running)."""
+    attn.destroy()
+
+
+def ar_attn_device_error(attn: Attn) -> int:
+    """Synchronise, read and clear the handle's error word (AR_DEVERR_PAGE_RANGE, _SLOT_RANGE, _LENGTH_RANGE)."""
+    code = ctypes.c_int(0)
+    _check(load_library().ar_attn_device_error(attn.handle, ctypes.byref(code)), "ar_attn_device_error",
+           ok=(AR_OK, AR_ERR_DEVICE_CHECK))
+    return int(code.value)
+
+
+def ar_attn_set_rope(attn: Attn, freq, axis=None, interleaved: bool = False, axes: int | None = None) -> None:
+    """Rotary positions of later ar_attn_append calls: pair i of a head's first
+    ``2 * len(freq)`` columns (a multiple of 16; none for an empty ``freq``) is turned by
+    ``freq[i]`` radians a position on axis ``axis[i]`` (0 when not given).  Pairs are columns
+    i and i + len(freq), or (interleaved) 2 i and 2 i + 1.  ``axes``: rows of the positions
+    tensor (the largest axis named, and one more, when not given).  Waits for the device's
+    copy of the table: not inside a stream capture."""
+    freq = [float(f) for f in freq]
+    n = len(freq)
+    if axis is not None:
+        axis = [int(i) for i in axis]
+        if len(axis) != n:
+            raise ValueError(f"axis has {len(axis)} entries, freq {n}")
+    if axes is None:
+        axes = max(axis, default=0) + 1 if axis is not None else 1
+    f_arr = (ctypes.c_double * max(1, n))(*freq)
+    a_arr = (ctypes.c_int32 * max(1, n))(*axis) if axis is not None else None
+    _check(load_library().ar_attn_set_rope(attn.handle, 2 * n, 1 if interleaved else 0, int(axes), f_arr, a_arr),
+           "ar_attn_set_rope")
+    attn.axes = int(axes) if n else 0
+
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                *[(n, ctypes.c_int64) for n in ("k_page", "k_token", "k_head", "v_page", "v_token", "v_head")],
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class KvCache:
+    """A paged cache: views of the caller's tensors, as ``ar_kv_cache`` describes them to the library."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.shape, self.device = tuple(k.shape), k.get_device()
+        self._struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), k.shape[0], *k.stride()[:3], *v.stride()[:3],
+                                      _ptr(k_scale), _ptr(v_scale))
+        self._ref = ctypes.addressof(self._struct)
+
+
+def ar_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
+    """The paged cache of one layer: ``k`` and ``v`` [pages, page_size, kv_heads, head_dim], bf16, or float8_e4m3fn with
+    fp32 ``k_scale`` and ``v_scale`` [kv_heads] (a value is code * scale of its head).  Any strides (pages of heads of
+    tokens, keys and values in one tensor) whose columns are contiguous and whose rows start at 16 bytes.  Holds
+    references to the tensors; make it once and pass it to every call."""
+    dtype = torch.bfloat16 if k_scale is None else torch.float8_e4m3fn
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale: both or neither")
+    if k.dim() != 4 or k.shape != v.shape:
+        raise ValueError(f"k, v: shapes {tuple(k.shape)} and {tuple(v.shape)}, expected [pages, page_size, kv_heads, head_dim] alike")
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}: the columns must be contiguous")
+        if t.device != k.device:
+            raise ValueError(f"{name}: on {t.device}, expected {k.device}")
+    if k_scale is not None:
+        _need_on(k.get_device(), k_scale, torch.float32, (k.shape[2],), "k_scale")
+        _need_on(k.get_device(), v_scale, torch.float32, (k.shape[2],), "v_scale")
+    return KvCache(k, v, k_scale, v_scale)
+
+
+def _need_cache(attn, cache, dev):
+    pages, size, kv, dim = cache.shape
+    if (size, kv, dim) != (attn.page_size, attn.kv_heads, attn.head_dim):
+        raise ValueError(f"cache: pages of {size} tokens, {kv} heads of {dim}, expected {attn.page_size}, {attn.kv_heads}, "
+                         f"{attn.head_dim}")
+    if dev is not None and cache.device != dev:
+        raise ValueError(f"cache: on {cache.k.device}, expected cuda:{dev}")
+
+
+def ar_attn_append(attn: Attn, cache: KvCache, qkv, positions, slots, q=None, stream=None):
+    """Turn the q and k heads of T tokens and write k and v into the cache.
+
+    qkv: bf16 [T, (heads + 2 kv_heads) * head_dim], a token's q heads, k heads and v heads; positions: int32 [axes, T]
+    (or [T] with one axis; ignored, and may be None, without rotary positions); slots: int32 [T], page * page_size +
+    token in the page, -1: not written; of tokens with one slot the last stands.  Returns q (bf16 [T, heads, head_dim]),
+    allocated when not given."""
+    T, dev = qkv.shape[0], _moe_device(attn)
+    _need_cache(attn, cache, dev)
+    _need_on(dev, qkv, torch.bfloat16, (T, (attn.heads + 2 * attn.kv_heads) * attn.head_dim), "qkv")
+    if attn.axes:
+        if positions is None:
+            raise ValueError("positions: rotary positions are set")
+        _need_on(dev, positions, torch.int32, (T,) if attn.axes == 1 and positions.dim() == 1 else (attn.axes, T), "positions")
+    else:
+        positions = None
+    _need_on(dev, slots, torch.int32, (T,), "slots")
+    shape = (T, attn.heads, attn.head_dim)
+    if q is None:
+        q = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
+    _need_on(dev, q, torch.bfloat16, shape, "q")
+    st = load_library().ar_attn_append(attn.handle, cache._ref, qkv.data_ptr(), _ptr(positions), slots.data_ptr(), T,
+                                       q.data_ptr(), _moe_stream(attn, stream))
+    if st != AR_OK:
+        _check(st, "ar_attn_append", ok=(AR_VALIDATED,) if attn.dry_run else ())
+    return q
+
+
+def ar_attn_decode(attn: Attn, cache: KvCache, q, page_table, lengths, scale: float | None = None, window: int = 0,
+                   out=None, lse=None, stream=None):
+    """Attention of one new token of each of B sequences over the last ``window`` (0: all) of its ``lengths`` cached
+    tokens: softmax(scale * q . k) v, ``scale`` 1 / sqrt(head_dim) when not given.
+
+    q: bf16 [B, heads, head_dim]; page_table: int32 [B, width], the page of a sequence's tokens i * page_size and on
+    (rows may be further apart); lengths: int32 [B], 0: zeros.  Returns out (bf16 [B, heads, head_dim], allocated when not
+    given), or (out, lse) when ``lse`` (fp32 [B, heads]: log of the sum of the scores' exponentials) is given."""
+    B, dev = q.shape[0], _moe_device(attn)
+    _need_cache(attn, cache, dev)
+    shape = (B, attn.heads, attn.head_dim)
+    _need_on(dev, q, torch.bfloat16, shape, "q")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected ({B}, width)")
+    width = page_table.shape[1]
+    apart = page_table.stride(0) if B > 1 else width
+    if page_table.dtype is not torch.int32 or apart < width or (width > 1 and page_table.stride(1) != 1) or (
+            dev is not None and page_table.get_device() != dev):
+        _need_on(dev, page_table, torch.int32, (B, width), "page_table")
+    _need_on(dev, lengths, torch.int32, (B,), "lengths")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    _need_on(dev, out, torch.bfloat16, shape, "out")
+    if lse is not None:
+        _need_on(dev, lse, torch.float32, (B, attn.heads), "lse")
+    st = load_library().ar_attn_decode(
+        attn.handle, cache._ref, q.data_ptr(), page_table.data_ptr() if width else None, width, apart,
+        lengths.data_ptr(), B, int(window), attn.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(), _ptr(lse),
+        _moe_stream(attn, stream))
+    if st != AR_OK:
+        _check(st, "ar_attn_decode", ok=(AR_VALIDATED,) if attn.dry_run else ())
+    return out if lse is None else (out, lse)

@@ -20,7 +20,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libarfuse.so")
 
 SOURCES = ["api.cu", "cluster_rows.cu", "stream_rows.cu", "split_rows.cu", "mhc_post.cu",
-           "moe_api.cu", "moe_route.cu", "moe_experts.cu", "matvec_w4.cu"]
+           "moe_api.cu", "moe_route.cu", "moe_experts.cu", "matvec_w4.cu",
+           "norm_q8.cu", "attn_api.cu", "attn_append.cu", "attn_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]

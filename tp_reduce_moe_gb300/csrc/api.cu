@@ -697,6 +697,66 @@ ar_status ar_rmsnorm(ar_workspace* ws, const void* const* partials, int R, const
                0, H, out, residual_out, residual_out_is_fp32, stream, false);
 }
 
+ar_status ar_rmsnorm_q8(ar_workspace* ws, const void* const* partials, int R, const void* residual,
+                        const void* gamma, float weight_bias, float eps, int64_t T, int H, int group,
+                        void* q, float* scales, void* out, void* residual_out,
+                        int residual_out_is_fp32, void* stream) {
+    if (!ws || !partials) return AR_ERR_INVALID_ARG;
+    if (R < 1 || R > AR_MAX_RANKS || R != ws->R || H != ws->H) return AR_ERR_INVALID_ARG;
+    if (!(eps == ws->eps)) return AR_ERR_INVALID_ARG;
+    if (T < 0) return AR_ERR_INVALID_ARG;
+    if (T > ws->max_tokens) return AR_ERR_CAPACITY;
+    if (residual_out_is_fp32 != 0 && residual_out_is_fp32 != 1) return AR_ERR_INVALID_ARG;
+    if (group != 0 && group != 32 && group != 64 && group != 128) return AR_ERR_UNSUPPORTED;
+    if (T == 0) return AR_OK;
+    if (!residual || !gamma || !q || !scales || !residual_out) return AR_ERR_INVALID_ARG;
+    for (int r = 0; r < R; ++r)
+        if (!partials[r]) return AR_ERR_INVALID_ARG;
+    if (!aligned(residual, 16) || !aligned(gamma, 16) || !aligned(out, 16) || !aligned(residual_out, 16) ||
+        !aligned(q, 8) || !aligned(scales, 4))
+        return AR_ERR_ALIGNMENT;
+    for (int r = 0; r < R; ++r)
+        if (!aligned(partials[r], 16)) return AR_ERR_ALIGNMENT;
+    const int64_t row2 = T * H * 2, groups = group ? (H + group - 1) / group : 1;
+    const bool inplace = residual_out == residual && !residual_out_is_fp32;
+    const Range outs[4] = {range_of(residual_out, residual_out_is_fp32 ? 2 * row2 : row2), range_of(q, T * H),
+                           range_of(scales, T * groups * 4), range_of(out, out ? row2 : 0)};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j])) return AR_ERR_INVALID_ARG;
+        if (overlap(outs[i], range_of(gamma, (int64_t)H * 2))) return AR_ERR_INVALID_ARG;
+        if (!(i == 0 && inplace) && overlap(outs[i], range_of(residual, row2))) return AR_ERR_INVALID_ARG;
+        for (int r = 0; r < R; ++r)
+            if (overlap(outs[i], range_of(partials[r], row2))) return AR_ERR_INVALID_ARG;
+    }
+    if (ws->flags & AR_WS_DRY_RUN) return AR_VALIDATED;
+
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess) return AR_ERR_CUDA;
+    if (cur != ws->device) return AR_ERR_INVALID_ARG;
+    arf::NormQ8Args a;
+    std::memset(&a, 0, sizeof a);
+    for (int r = 0; r < R; ++r) a.P[r] = static_cast<const uint16_t*>(partials[r]);
+    a.residual = static_cast<const uint16_t*>(residual);
+    a.gamma = static_cast<const uint16_t*>(gamma);
+    a.q = static_cast<uint8_t*>(q);
+    a.scales = scales;
+    a.out = static_cast<uint16_t*>(out);
+    a.residual_out = residual_out;
+    a.T = T;
+    a.R = R;
+    a.H = H;
+    a.norm_bf16_h = (ws->flags & AR_WS_NORM_BF16_H) ? 1 : 0;
+    a.weight_bias = weight_bias;
+    a.eps = eps;
+    if (arf::launch_norm_q8(a, group, residual_out_is_fp32 != 0, static_cast<cudaStream_t>(stream),
+                            (ws->flags & AR_WS_PDL) != 0) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return AR_ERR_CUDA;
+    }
+    return AR_OK;
+}
+
 ar_status ar_mhc_post(ar_workspace* ws, const void* const* partials, int R, const void* streams,
                       const float* post, const float* comb, int64_t T, int H, int hc,
                       void* streams_out, void* stream) {

@@ -406,6 +406,22 @@ struct SplitGeom {
                       // reuses the first buffers once they are folded
 };
 
+// Arguments of the norm with an 8-bit output (norm_q8.cu).
+struct NormQ8Args {
+    const uint16_t* P[16];     // R partials, bf16 [T, H]
+    const uint16_t* residual;  // bf16 [T, H]
+    const uint16_t* gamma;     // bf16 [H]
+    uint8_t* q;                // e4m3 [T, H]
+    float* scales;             // [T, groups of a row]
+    uint16_t* out;             // bf16 [T, H], or nullptr
+    void* residual_out;        // bf16 or fp32 [T, H] (may be residual)
+    int64_t T;
+    int R, H;
+    int norm_bf16_h;
+    float weight_bias;
+    float eps;
+};
+
 // Arguments of the all-reduce + mHC write-back (mhc_post.cu).
 struct MhcArgs {
     const uint16_t* P[16];  // R partials, bf16 [T, H]

@@ -35,6 +35,9 @@ bool oneshot_prefer_64(const ClusterPlan& p, int64_t T, int num_sms, int blocks8
 // The all-reduce + mHC write-back (mhc_post.cu).
 cudaError_t launch_mhc_post(const MhcArgs& a, cudaStream_t stream, bool pdl = false);
 
+// The norm with an 8-bit output (norm_q8.cu); group 0: one scale a row.
+cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, cudaStream_t stream, bool pdl);
+
 struct StreamPlan {
     StreamGeom geo;
     int cpt;          // 16-byte chunks per consumer thread

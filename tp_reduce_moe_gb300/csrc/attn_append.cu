@@ -1,0 +1,202 @@
+// attn_append.cu -- rotary positions and the write into the paged cache.
+//
+// Pair i of the first `rot` columns of a q or k head is turned by the angle
+// freq[i] * position[axis[i]]; q goes out, k and v go to their slots of the cache.
+//
+// A piece is sixteen values of a head, of which a thread loads, turns and stores two
+// groups of eight: both halves of eight pairs, so no value is exchanged between threads.
+// A token's cosines and sines are formed once a CTA, in shared memory: the angle in
+// fp64 turns, less its whole turns, so that far positions lose nothing, then sincospi
+// in fp32.
+//
+// Of tokens with one slot the last one wins whatever order the CTAs run in: each CTA
+// looks through the slots behind its own tokens and leaves out what is written again.
+// A bitmap of its own slots (hashed by their low bits) answers for nearly all of them.
+#include "attn_common.cuh"
+
+namespace arf {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 64;  // of a CTA
+constexpr int kTableTokens = 4; // whose angles are in shared memory at a time
+constexpr int kHashBits = 14;
+
+struct Piece {
+    uint4 lo, hi;
+};
+
+__device__ __forceinline__ uint4 ld_once16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Chunks (of eight columns) of piece p of a head: its own two, or both halves of eight pairs.
+__device__ __forceinline__ void chunks_of(int p, int rot, bool split, int* lo, int* hi) {
+    const bool halves = split && p < rot / 16;
+    *lo = halves ? p : 2 * p;
+    *hi = halves ? p + rot / 16 : 2 * p + 1;
+}
+
+__device__ __forceinline__ void store8(const CacheView& c, int head, int64_t token, int chunk, const float f[8]) {
+    uint8_t* row = c.data + token + head * c.head;
+    if (c.scale == nullptr) {
+        *reinterpret_cast<uint4*>(row + chunk * 16) = f32x8_to_bf16x8(f);
+        return;
+    }
+    const float s = c.scale[head];
+    uint2 v;
+    v.x = e4m3x2(f[0] / s, f[1] / s) | e4m3x2(f[2] / s, f[3] / s) << 16;
+    v.y = e4m3x2(f[4] / s, f[5] / s) | e4m3x2(f[6] / s, f[7] / s) << 16;
+    *reinterpret_cast<uint2*>(row + chunk * 8) = v;
+}
+
+__global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_constant__ AppendArgs a, int tokens_per_cta) {
+    __shared__ int s_slot[kMaxTokens];
+    __shared__ int s_dead[kMaxTokens];
+    __shared__ int64_t s_k[kMaxTokens], s_v[kMaxTokens];  // byte offsets of the tokens' places, -1: none
+    __shared__ unsigned s_hash[1 << (kHashBits - 5)];
+    __shared__ float2 s_turn[kTableTokens][kMaxHeadDim / 2];
+    pdl_trigger();
+    pdl_wait();  // no global memory access before this point
+    const int t0 = blockIdx.x * tokens_per_cta, count = min(tokens_per_cta, a.T - t0);
+    const int per_head = a.D / 16, all_heads = a.heads + 2 * a.kv;
+    // this CTA's pieces of a token
+    const int pieces = all_heads * per_head;
+    const int first = (int)((int64_t)pieces * blockIdx.y / gridDim.y);
+    const int own = (int)((int64_t)pieces * (blockIdx.y + 1) / gridDim.y) - first;
+
+    auto load = [&](int i) {
+        const int t = i / own, r = first + (i - t * own), head = r / per_head;
+        int lo, hi;
+        chunks_of(r - head * per_head, head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
+        const uint16_t* row = a.qkv + ((int64_t)(t0 + t) * all_heads + head) * a.D;
+        return Piece{ld_once16(row + lo * 8), ld_once16(row + hi * 8)};
+    };
+    // the first piece is asked for before anything else
+    Piece next;
+    if ((int)threadIdx.x < count * own) next = load(threadIdx.x);
+
+    // places in the cache
+    if (first + own > a.heads * per_head) {
+        for (int i = threadIdx.x; i < 1 << (kHashBits - 5); i += kThreads) s_hash[i] = 0;
+        if ((int)threadIdx.x < count) {
+            int slot = a.slots[t0 + threadIdx.x];
+            if (slot < -1 || slot >= a.slot_count) {
+                atomicOr(a.err, kErrSlotRange);
+                slot = -1;
+            }
+            s_slot[threadIdx.x] = slot;
+            s_dead[threadIdx.x] = slot < 0;
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < count && s_slot[threadIdx.x] >= 0) {
+            const unsigned h = (unsigned)s_slot[threadIdx.x] & ((1u << kHashBits) - 1);
+            atomicOr(&s_hash[h >> 5], 1u << (h & 31));
+        }
+        __syncthreads();
+        for (int t = t0 + 1 + threadIdx.x; t < a.T; t += kThreads) {
+            const int slot = a.slots[t];
+            const unsigned h = (unsigned)slot & ((1u << kHashBits) - 1);
+            if (slot < 0 || !(s_hash[h >> 5] >> (h & 31) & 1)) continue;
+            for (int i = 0; i < count && t0 + i < t; ++i)
+                if (s_slot[i] == slot) s_dead[i] = 1;
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < count) {
+            const int slot = s_slot[threadIdx.x];
+            const int page = slot / a.page_size, token = slot - page * a.page_size;
+            const bool dead = s_dead[threadIdx.x] != 0;
+            s_k[threadIdx.x] = dead ? -1 : page * a.k.page + token * a.k.token;
+            s_v[threadIdx.x] = dead ? -1 : page * a.v.page + token * a.v.token;
+        }
+    }
+
+    const int pairs = a.rot / 2;
+    for (int b = 0; b < count; b += kTableTokens) {
+        const int n = min(kTableTokens, count - b);
+        for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
+            const int t = i / pairs, pair = i - t * pairs;
+            const double turns = a.positions[(int64_t)a.rope->axis[pair] * a.T + t0 + b + t] * a.rope->turns[pair];
+            float s, c;
+            sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+            s_turn[t][pair] = make_float2(c, s);
+        }
+        __syncthreads();
+        // pieces in order: those of the next tokens' batch follow on
+        for (int i = b * own + threadIdx.x; i < (b + n) * own; i += kThreads) {
+            // (a batch's first piece of this thread may be another than the one asked for)
+            const Piece x = b == 0 && i == (int)threadIdx.x ? next : load(i);
+            const int t = i / own, r = first + (i - t * own), head = r / per_head, p = r - head * per_head;
+            const bool turned = head < a.heads + a.kv && p < a.rot / 16;
+            int lo, hi;
+            chunks_of(p, head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
+            float u[8], v[8];
+            bf16x8_to_f32(x.lo, u);
+            bf16x8_to_f32(x.hi, v);
+            if (turned) {
+                const float2* table = s_turn[t - b] + p * 8;
+                if (a.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = table[j], g = table[j + 4];
+                        const float ua = u[2 * j], ub = u[2 * j + 1], va = v[2 * j], vb = v[2 * j + 1];
+                        u[2 * j] = ua * f.x - ub * f.y;
+                        u[2 * j + 1] = ub * f.x + ua * f.y;
+                        v[2 * j] = va * g.x - vb * g.y;
+                        v[2 * j + 1] = vb * g.x + va * g.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 f = table[j];
+                        const float x0 = u[j], x1 = v[j];
+                        u[j] = x0 * f.x - x1 * f.y;
+                        v[j] = x1 * f.x + x0 * f.y;
+                    }
+                }
+            }
+            if (head < a.heads) {
+                uint16_t* row = a.q + ((int64_t)(t0 + t) * a.heads + head) * a.D;
+                st_global16(row + lo * 8, f32x8_to_bf16x8(u));
+                st_global16(row + hi * 8, f32x8_to_bf16x8(v));
+                continue;
+            }
+            const bool key = head < a.heads + a.kv;
+            const int64_t place = key ? s_k[t] : s_v[t];
+            if (place < 0) continue;
+            const int h = key ? head - a.heads : head - a.heads - a.kv;
+            store8(key ? a.k : a.v, h, place, lo, u);
+            store8(key ? a.k : a.v, h, place, hi, v);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_append(const AppendArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
+    const int pieces = (a.heads + 2 * a.kv) * (a.D / 16);
+    // few tokens: a token's pieces over several CTAs; many: several tokens a CTA
+    const int target = 8 * num_sms;
+    int tokens = (a.T + target - 1) / target;
+    if (tokens > kMaxTokens) tokens = kMaxTokens;
+    const int blocks = (a.T + tokens - 1) / tokens;
+    int parts = (pieces + kThreads - 1) / kThreads;
+    if (parts > (target + blocks - 1) / blocks) parts = (target + blocks - 1) / blocks;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)parts);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attn_append_kernel, a, tokens);
+}
+
+}  // namespace arf
