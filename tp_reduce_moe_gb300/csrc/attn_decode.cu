@@ -3,112 +3,713 @@
 //
 //   s_j = scale q . k_j; out = sum_j softmax(s)_j v_j; lse = log sum_j exp(s_j)
 //
-// in one pass with a running maximum m, sum l and weighted sum of values: a token with
-// score s turns them into m' = max(m, s), l 2^(m - m') + 2^(s - m'), o 2^(m - m') +
-// 2^(s - m') v (scores times log2(e)).
+// in one pass with a running maximum m, sum l and weighted sum of values o: tokens with
+// scores s (times log2(e)) turn them into m' = max(m, s), l 2^(m - m') + sum 2^(s - m'),
+// o 2^(m - m') + sum 2^(s - m') v.
 //
-// One CTA per sequence and query head; each warp takes every fourth token, the lanes
-// share its columns, and the warps' results meet in shared memory.
+// Work.  Up to sixteen query heads of a key-value head are the rows of a matrix
+// instruction (m16n8k16) and share what is read.  Such a group of one sequence is an item,
+// its tokens come in units of TOK; the units of all items in a row are cut into one range
+// per SM, by the lengths on the device, so lengths of any mixture keep every SM equally
+// busy and a captured launch serves any.  An item that a range's end cuts is joined from
+// its parts: the last CTA of each sixteen parts to arrive adds them up, the last of those
+// the sums, always in the order of the parts.  No CTA waits for another.
+//
+// Inside a CTA each warp takes every eighth unit of a segment (a range's share of an item)
+// and keeps a softmax of its own; the warps meet once a segment.  A warp streams its units
+// through a ring of its own in shared memory, keys and values in turn, by 16-byte
+// asynchronous copies that run ahead across segments, so that no barrier stands in the
+// stream; the places of a unit's tokens are looked up a unit earlier still.
+//
+// Roundings: scores, maxima, sums and o are fp32.  Weights go to the matrix instruction as
+// two bf16 (their rounding and its remainder: 2^-17, where one bf16 would add 0.7 times the
+// output's own rounding); with 8-bit values as halves (2^-11), whose products are
+// exact, q then scaled by a power of two a row to the halves' range.
 #include "attn_common.cuh"
+
+#include <cuda_fp16.h>
 
 namespace arf {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 16;          // query heads of an item
+constexpr int kRing = 24576;       // bytes of a warp's ring
+constexpr int kMaxGrid = 256;
+constexpr int kFan = 16;           // parts that are joined at a time
+constexpr int kMinUnits = kWarps;  // of a CTA, while there are SMs left
+constexpr int kSlice = 32;         // columns that the warps' results are added up of at a time
+constexpr float kLazy = 8.0f;      // scores (log2) may pass the reference by so much before it moves
+constexpr float kLn2 = 0.6931471805599453f;
 
-template <int PER>
-__device__ __forceinline__ void load_values(const uint8_t* row, bool bytes, int lane, float f[PER]) {
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int d = lane * PER + j;
-        if (bytes) {
-            const uint32_t h = e4m3x2_to_f16x2(row[d]);
-            f[j] = __half2float(__ushort_as_half((unsigned short)h));
-        } else {
-            f[j] = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(row)[d] << 16);
-        }
+// Tokens of a unit: rows of 128 bytes and less come by 32, longer ones by 16.
+constexpr int unit_tokens(int D, bool eight) { return D * (eight ? 1 : 2) <= 128 ? 32 : 16; }
+
+template <int D, bool EIGHT>
+struct Shape {
+    static constexpr int kTok = unit_tokens(D, EIGHT);
+    static constexpr int kRow = D * (EIGHT ? 1 : 2);  // bytes of a key
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kHalf = kTok * kRow;  // bytes of a unit's keys (or values)
+    static constexpr int kHalves = kRing / kHalf;
+    static constexpr int kLead = kHalves - 1;  // halves that are asked for ahead
+    static constexpr int kPad = kSlice + (EIGHT ? 16 : 8);  // floats of a row of the merge buffer, free of bank conflicts
+    static constexpr int kMerge = kWarps * kRows * kPad * 4;
+    static constexpr int kSmem = kWarps * kRing + kMerge;
+    static_assert(kSmem + 2048 <= 232448, "shared memory of a CTA");
+    // where chunk c of row r lies, so that eight rows' chunks c are in eight different groups of banks
+    __device__ static int place(int r, int c) {
+        return r * kRow + ((kChunks >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & (kChunks - 1))) << 4);
     }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    const int bytes = there ? 16 : 0;  // the rest is zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool EIGHT>
+__device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    if (EIGHT)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// Two maxima's share: 2^(m - top), 0 for a part without tokens.
+__device__ __forceinline__ float share_of(float m, float top) { return ex2(m - (top == -INFINITY ? 0.0f : top)); }
+
+// A CTA's share of an item: units [u0, u1) of its n.
+struct Segment {
+    int b, group;    // sequence; group of query heads
+    int start, len;  // tokens looked at
+    int u0, u1, n;
+};
+
+// Walks the segments of a range of units.
+template <int TOK>
+struct Walk {
+    int b, group, u;
+    int start, len, n;
+    int64_t left;  // units of the range that are not handed out
+
+    __device__ void sequence(const DecodeArgs& a) {
+        len = checked_length(a, b, false);
+        start = a.window > 0 && len > a.window ? len - a.window : 0;
+        n = (int)(((int64_t)len - start + TOK - 1) / TOK);
+    }
+    __device__ bool next(const DecodeArgs& a, int groups, Segment* s) {
+        if (left <= 0) return false;
+        if (u == n) {  // the item is done: the next one that has units (there is one, for some are left)
+            u = 0;
+            if (++group == groups) {
+                group = 0;
+                do {
+                    ++b;
+                    sequence(a);
+                } while (n == 0);
+            }
+        }
+        const int take = (int)(left < n - u ? left : n - u);
+        *s = Segment{b, group, start, len, u, u + take, n};
+        u += take;
+        left -= take;
+        return true;
+    }
+};
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += w;
+    }
+    return v;
+}
+
+// What the joins need: a part holds [kRows, D] sums, then kRows maxima and kRows sums of weights.
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) attn_decode_kernel(const __grid_constant__ DecodeArgs a) {
-    constexpr int PER = D / 32;
-    __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-    pdl_trigger();
+constexpr int kPart = kRows * D + 2 * kRows;
+
+template <int D, bool EIGHT>
+__global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_constant__ DecodeArgs a, int groups, int rows_of_group) {
+    using S = Shape<D, EIGHT>;
+    constexpr int TOK = S::kTok, kTiles = TOK / 8, kSteps = D / 16;
+    constexpr float kOffset = EIGHT ? 7.0f : 0.0f;  // halves: weights up to 2^(8 + 7), so that small ones keep their bits
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_fm[kRows], s_fl[kRows];
+    __shared__ int64_t s_scan[kWarps];
+    __shared__ int64_t s_first;  // units of the found sequence before the range's first
+    __shared__ int s_b, s_last;
+    __shared__ unsigned s_mask[kWarps][8];
     pdl_wait();  // no global memory access before this point
-    const int head = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kv = head / (a.heads / a.kv);
-    const bool bytes = a.k.scale != nullptr;
-    const int length = checked_length(a, b, true);
-    const int start = a.window > 0 && length > a.window ? length - a.window : 0;
-    const float ks = bytes ? a.scale * a.k.scale[kv] : a.scale, vs = bytes ? a.v.scale[kv] : 1.0f;
-    const uint16_t* q_row = a.q + ((int64_t)b * a.heads + head) * D;
-    float q[PER], o[PER], m = -INFINITY, l = 0.0f;
-    load_values<PER>(reinterpret_cast<const uint8_t*>(q_row), false, lane, q);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int shared_heads = a.heads / a.kv, per_head = groups / a.kv;
+
+    // ---- the range of this CTA
+    int64_t total, begin, end;
+    int active;
+    {
+        const int each = (a.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(a.B, b0 + each);
+        auto units = [&](int b) {
+            const int len = checked_length(a, b, blockIdx.x == 0);
+            const int n = a.window > 0 && len > a.window ? a.window : len;
+            return ((int64_t)n + TOK - 1) / TOK * groups;
+        };
+        int64_t mine = 0;
+        for (int b = b0; b < b1; ++b) mine += units(b);
+        const int64_t upto = warp_scan(mine, lane);
+        if (lane == 31) s_scan[warp] = upto;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) o[j] = 0.0f;
-    for (int t = start + warp; t < length; t += kWarps) {
-        const int index = t / a.page_size, page = a.table[b * a.table_stride + index];
-        if ((unsigned)page >= (unsigned)a.pages) {
-            atomicOr(a.err, kErrPageRange);
-            continue;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += s_scan[w];
+            total += s_scan[w];
         }
-        const int64_t token = t - index * a.page_size;
-        float f[PER], dot = 0.0f;
-        load_values<PER>(a.k.data + page * a.k.page + token * a.k.token + kv * a.k.head, bytes, lane, f);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) dot = fmaf(q[j], f[j], dot);
-        const float s = warp_sum(dot) * ks, top = fmaxf(m, s), base = top == -INFINITY ? 0.0f : top;
-        const float keep = exp2f(m - base), p = exp2f(s - base);
-        load_values<PER>(a.v.data + page * a.v.page + token * a.v.token + kv * a.v.head, bytes, lane, f);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) o[j] = fmaf(p, f[j], o[j] * keep);
-        l = fmaf(l, keep, p);
-        m = top;
+        const int64_t wanted = (total + kMinUnits - 1) / kMinUnits;
+        active = (int)(wanted < (int64_t)gridDim.x ? wanted : (int64_t)gridDim.x);
+        begin = active > 0 ? total * blockIdx.x / active : 0;
+        end = active > 0 ? total * (blockIdx.x + 1) / active : 0;
+        before += upto - mine;
+        if ((int)blockIdx.x < active && before <= begin && begin < before + mine) {
+            int b = b0;
+            for (int64_t n; before + (n = units(b)) <= begin; ++b) before += n;
+            s_b = b;
+            s_first = begin - before;
+        }
+        // rows without tokens
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+            if (checked_length(a, b, false) == 0) {
+                for (int i = tid; i < a.heads * D / 8; i += kThreads)
+                    st_global16(a.out + (int64_t)b * a.heads * D + i * 8, make_uint4(0, 0, 0, 0));
+                if (a.lse != nullptr)
+                    for (int i = tid; i < a.heads; i += kThreads) a.lse[(int64_t)b * a.heads + i] = -INFINITY;
+            }
+        __syncthreads();
+        if ((int)blockIdx.x >= active) return;
     }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
+
+    Walk<TOK> walk;
+    walk.b = s_b;
+    walk.sequence(a);
+    walk.group = (int)(s_first / walk.n);
+    walk.u = (int)(s_first - (int64_t)walk.group * walk.n);
+    walk.left = end - begin;
+
+    // ---- the stream of this warp's units: looked up, then asked for
+    const uint32_t ring = smem_addr(smem) + warp * kRing;
+    Walk<TOK> ahead = walk;
+    Segment ask;
+    int ask_u = 0;             // unit that is looked up
+    bool asking = ahead.next(a, groups, &ask);
+    int page = -1, in_page = 0;  // of this lane's token of that unit
+    int64_t k_at = -1, v_at = -1;  // places of the unit that is being asked for
+    bool live = false;             // there is such a unit
+    unsigned asked = 0;            // units asked for
+    int fill = 0;                  // slot of the ring that is filled next
+
+    auto look_up = [&]() {
+        page = -1;
+        const int64_t token = ask.start + (int64_t)ask_u * TOK + lane;
+        if (lane < TOK && token < ask.len) {
+            const int index = (int)token / a.page_size;
+            in_page = (int)token - index * a.page_size;
+            page = a.table[ask.b * a.table_stride + index];
+            if ((unsigned)page >= (unsigned)a.pages) {
+                atomicOr(a.err, kErrPageRange);
+                page = -1;
+            }
+        }
+    };
+    auto seek = [&]() {  // from ask_u on, this warp's next unit
+        while (asking && ask_u >= ask.u1) {
+            asking = ahead.next(a, groups, &ask);
+            ask_u = ask.u0 + warp;
+        }
+        if (asking) look_up();
+    };
+    if (asking) ask_u = ask.u0 + warp;
+    seek();
+
+    auto issue = [&](bool keys) {
+        if (keys) {
+            k_at = v_at = -1;
+            live = asking;
+            if (asking) {
+                const int head = ask.group / per_head;
+                if (page >= 0) {
+                    k_at = page * a.k.page + in_page * a.k.token + head * a.k.head;
+                    v_at = page * a.v.page + in_page * a.v.token + head * a.v.head;
+                }
+                const unsigned mask = __ballot_sync(0xffffffffu, page >= 0);
+                if (lane == 0) s_mask[warp][asked & 7] = mask;
+                ++asked;
+                ask_u += kWarps;
+                seek();
+            }
+        }
+        const int64_t at = keys ? k_at : v_at;
+        const uint8_t* base = keys ? a.k.data : a.v.data;
+        const uint32_t slot = ring + fill * S::kHalf;
+        if (__any_sync(0xffffffffu, at >= 0)) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) s_o[warp][lane * PER + j] = o[j];
-    __syncthreads();
-    float top = -INFINITY, total = 0.0f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    for (int w = 0; w < kWarps; ++w) total += s_l[w] * exp2f(s_m[w] - base);
-    for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
-        float sum = 0.0f;
-        for (int w = 0; w < kWarps; ++w) sum += s_o[w][d] * exp2f(s_m[w] - base);
-        const float v = total == 0.0f ? 0.0f : sum / total * vs;
-        a.out[((int64_t)b * a.heads + head) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            for (int i = 0; i < TOK * S::kChunks / 32; ++i) {
+                const int r = (i * 32 + lane) / S::kChunks, c = (i * 32 + lane) % S::kChunks;
+                const int64_t row = __shfl_sync(0xffffffffu, at, r);
+                copy16(slot + S::place(r, c), base + (row < 0 ? 0 : row + c * 16), row >= 0);
+            }
+        } else if (live) {  // no token on a page of the cache: zeros
+            for (int i = 0; i < S::kHalf / 512; ++i)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(slot + (i * 32 + lane) * 16), "r"(0) : "memory");
+        }
+        copy_commit();
+        fill = fill + 1 == S::kHalves ? 0 : fill + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < S::kLead; ++i) issue(i % 2 == 0);
+
+    // ---- segments
+    uint32_t q[kSteps][4];
+    float q_scale[2];  // log2(e) * scale * scale of the keys * power of two of the row, rows g and g + 8
+    auto load_q = [&](const Segment& s) {
+        const int head = s.group / per_head, part = s.group - head * per_head;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = part * rows_of_group + g + 8 * r;
+            const bool there = g + 8 * r < rows_of_group && row < shared_heads;
+            const uint16_t* src = a.q + ((int64_t)s.b * a.heads + head * shared_heads + (there ? row : 0)) * D;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                // columns of a step: 2 t4 (+1) and 2 t4 + 8 (+1); with bytes 4 t4 .. 4 t4 + 3, the order that their keys come in
+                uint2 v;
+                if (EIGHT) {
+                    v = *reinterpret_cast<const uint2*>(src + i * 16 + t4 * 4);
+                } else {
+                    v.x = *reinterpret_cast<const uint32_t*>(src + i * 16 + t4 * 2);
+                    v.y = *reinterpret_cast<const uint32_t*>(src + i * 16 + t4 * 2 + 8);
+                }
+                q[i][r] = there ? v.x : 0;
+                q[i][r + 2] = there ? v.y : 0;
+            }
+            q_scale[r] = a.scale;
+        }
+    };
+    auto prepare_q = [&](const Segment& s) {
+        if (!EIGHT) return;
+        const float ks = a.k.scale[s.group / per_head];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int c = r; c < 4; c += 2)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[i][c] << 16)), fabsf(__uint_as_float(q[i][c] & 0xffff0000u))));
+            top = quad_max(top);
+            // the power of two that brings the row's largest value to [1, 2) (or next to it, at the ends of the range)
+            int e = (int)(__float_as_uint(top) >> 23) - 127;
+            e = e < -126 ? -126 : e > 126 ? 126 : e;
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int c = r; c < 4; c += 2)
+                    q[i][c] = pack_f16x2(__uint_as_float(q[i][c] << 16) * down, __uint_as_float(q[i][c] & 0xffff0000u) * down);
+            q_scale[r] = a.scale * ks * up;
+        }
+    };
+
+    int take = 0;        // slot of the ring that is used next
+    unsigned taken = 0;  // units used
+    int64_t position = begin;
+    Segment seg;
+    bool more = walk.next(a, groups, &seg);
+    load_q(seg);
+    while (more) {
+        prepare_q(seg);
+        float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+
+        for (int u = seg.u0 + warp; u < seg.u1; u += kWarps) {
+            // scores of TOK tokens
+            __syncwarp();  // the slot that is filled now has been read by all lanes
+            issue(S::kLead % 2 == 0);
+            copy_wait<S::kLead>();
+            __syncwarp();
+            float s[kTiles][4];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+            uint32_t slot = ring + take * S::kHalf;
+            take = take + 1 == S::kHalves ? 0 : take + 1;
+            if (EIGHT) {
+                // a matrix is 8 tokens by 16 bytes: one step of the columns
+#pragma unroll
+                for (int i = 0; i < kSteps; i += 2)
+#pragma unroll
+                    for (int h = 0; h < TOK / 16; ++h) {
+                        uint32_t r[4];
+                        ldmatrix4(r, slot + S::place(h * 16 + (lane >> 4) * 8 + (lane & 7), i + ((lane >> 3) & 1)));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma<true>(s[h * 2 + (j >> 1)], q[i + (j & 1)], e4m3x2_to_f16x2((uint16_t)r[j]), e4m3x2_to_f16x2((uint16_t)(r[j] >> 16)));
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                    for (int h = 0; h < TOK / 16; ++h) {
+                        uint32_t r[4];
+                        ldmatrix4(r, slot + S::place(h * 16 + (lane >> 4) * 8 + (lane & 7), i * 2 + ((lane >> 3) & 1)));
+                        mma<false>(s[h * 2], q[i], r[0], r[1]);
+                        mma<false>(s[h * 2 + 1], q[i], r[2], r[3]);
+                    }
+            }
+            // their weights
+            const unsigned mask = s_mask[warp][taken++ & 7] >> (2 * t4);
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = mask >> (i * 8 + (j & 1)) & 1 ? s[i][j] * q_scale[j >> 1] : -INFINITY;
+                    top[j >> 1] = fmaxf(top[j >> 1], s[i][j]);
+                }
+            float keep[2];
+            bool moved = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                top[r] = quad_max(top[r]);
+                keep[r] = 1.0f;
+                if (top[r] > m[r] + kLazy) {  // (the first finite score passes minus infinity)
+                    keep[r] = ex2(m[r] - top[r]);
+                    m[r] = top[r];
+                    l[r] *= keep[r];
+                    moved = true;
+                }
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[i][j] *= keep[j >> 1];
+            }
+            const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0] - kOffset, m[1] == -INFINITY ? 0.0f : m[1] - kOffset};
+            uint32_t p[TOK / 16][4], rest[TOK / 16][4];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float x = ex2(s[i][2 * r] - base[r]), y = ex2(s[i][2 * r + 1] - base[r]);
+                    l[r] += x + y;
+                    const int c = r + 2 * (i & 1);
+                    if (EIGHT) {
+                        p[i / 2][c] = pack_f16x2(x, y);
+                    } else {
+                        const uint32_t w = pack_bf16x2(x, y);
+                        p[i / 2][c] = w;
+                        rest[i / 2][c] = pack_bf16x2(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u));
+                    }
+                }
+            // and values
+            __syncwarp();
+            issue(S::kLead % 2 == 1);
+            copy_wait<S::kLead>();
+            __syncwarp();
+            slot = ring + take * S::kHalf;
+            take = take + 1 == S::kHalves ? 0 : take + 1;
+            if (EIGHT) {
+                // transposed by pairs of bytes: a register holds two columns of two tokens, even columns make one tile, odd
+                // ones another
+#pragma unroll
+                for (int c = 0; c < kSteps; c += 2)
+#pragma unroll
+                    for (int h = 0; h < TOK / 16; ++h) {
+                        uint32_t r[4];
+                        ldmatrix4_trans(r, slot + S::place(h * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c + (lane >> 4)));
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
+                            mma<true>(o[2 * (c + j)], p[h], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)y));
+                            mma<true>(o[2 * (c + j) + 1], p[h], e4m3x2_to_f16x2((uint16_t)(x >> 16)), e4m3x2_to_f16x2((uint16_t)(y >> 16)));
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+                    for (int h = 0; h < TOK / 16; ++h) {
+                        uint32_t r[4];
+                        ldmatrix4_trans(r, slot + S::place(h * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c * 2 + (lane >> 4)));
+                        mma<false>(o[2 * c], p[h], r[0], r[1]);
+                        mma<false>(o[2 * c + 1], p[h], r[2], r[3]);
+                        mma<false>(o[2 * c], rest[h], r[0], r[1]);
+                        mma<false>(o[2 * c + 1], rest[h], r[2], r[3]);
+                    }
+            }
+        }
+
+        // ---- the warps' results, added up in the order of the warps
+        const Segment done = seg;
+        more = walk.next(a, groups, &seg);
+        if (more) load_q(seg);  // arrives while the warps meet
+        else pdl_trigger();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] = quad_sum(l[r]);
+            if (t4 == 0) {
+                s_m[warp][g + 8 * r] = m[r];
+                s_l[warp][g + 8 * r] = l[r];
+            }
+        }
+        __syncthreads();
+        float share[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][g + 8 * r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sum += s_l[w][g + 8 * r] * share_of(s_m[w][g + 8 * r], top);
+            share[r] = share_of(m[r], top);
+            if (warp == 0 && t4 == 0) {
+                s_fm[g + 8 * r] = top;
+                s_fl[g + 8 * r] = sum;
+            }
+        }
+        const int kv_head = done.group / per_head, part_of = done.group - kv_head * per_head;
+        const int rows = min(rows_of_group, shared_heads - part_of * rows_of_group);
+        const int64_t out_row = (int64_t)done.b * a.heads + kv_head * shared_heads + part_of * rows_of_group;
+        const float vs = EIGHT ? a.v.scale[kv_head] : 1.0f;
+        const bool whole = done.u0 == 0 && done.u1 == done.n;
+        // a part's place: one for an item that began in a range before, one for an item that begins in this one
+        const int64_t item = position - done.u0;  // the item's first unit
+        position += done.u1 - done.u0;
+        float* part = a.part + ((int64_t)blockIdx.x * 2 + (done.u0 == 0 ? 1 : 0)) * kPart<D>;
+        float* merge = reinterpret_cast<float*>(smem + kWarps * kRing);
+        const int row = tid / 16, col = tid % 16 * 2;
+        auto finish = [&](int r, int d, float x, float y, float sum) {  // two columns of a row of the output
+            const float f = sum == 0.0f ? 0.0f : vs / sum;
+            *reinterpret_cast<uint32_t*>(a.out + (out_row + r) * D + d) = pack_bf16x2(x * f, y * f);
+        };
+        auto finish_lse = [&](int r, float top, float sum) {
+            if (a.lse != nullptr) a.lse[out_row + r] = sum == 0.0f ? -INFINITY : (top - kOffset + log2f(sum)) * kLn2;
+        };
+#pragma unroll
+        for (int i = 0; i < D / kSlice; ++i) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float* to = merge + (warp * kRows + g + 8 * r) * S::kPad;
+                if (EIGHT) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<float4*>(to + j * 16 + t4 * 4) =
+                            make_float4(o[4 * i + 2 * j][2 * r] * share[r], o[4 * i + 2 * j + 1][2 * r] * share[r],
+                                        o[4 * i + 2 * j][2 * r + 1] * share[r], o[4 * i + 2 * j + 1][2 * r + 1] * share[r]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float2*>(to + j * 8 + t4 * 2) = make_float2(o[4 * i + j][2 * r] * share[r], o[4 * i + j][2 * r + 1] * share[r]);
+                }
+            }
+            __syncthreads();
+            if (row < rows) {
+                float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 v = *reinterpret_cast<const float2*>(merge + (w * kRows + row) * S::kPad + col);
+                    sum.x += v.x;
+                    sum.y += v.y;
+                }
+                if (whole)
+                    finish(row, i * kSlice + col, sum.x, sum.y, s_fl[row]);
+                else
+                    *reinterpret_cast<float2*>(part + row * D + i * kSlice + col) = sum;
+            }
+            __syncthreads();
+        }
+        if (tid < rows) {
+            if (whole) {
+                finish_lse(tid, s_fm[tid], s_fl[tid]);
+            } else {
+                part[kRows * D + tid] = s_fm[tid];
+                part[kRows * D + kRows + tid] = s_fl[tid];
+            }
+        }
+        if (whole) continue;
+
+        // ---- the parts of an item over several CTAs: sixteen at a time, then the sixteens
+        auto owner = [&](int64_t x) { return (int)(((x + 1) * active - 1) / total); };
+        const int first = owner(item), last = owner(item + done.n - 1), parts = last - first + 1;
+        const int fans = (parts + kFan - 1) / kFan;
+        int count = 0, step = 0, leader = 0;
+        for (int level = 0; level < 2; ++level) {
+            if (level == 0) {
+                const int fan = ((int)blockIdx.x - first) / kFan;
+                leader = first + fan * kFan;
+                count = min(kFan, last - leader + 1);
+                step = 1;
+            } else {
+                leader = first;
+                count = fans;
+                step = kFan;
+            }
+            // this level's counter, of the leader's part
+            unsigned* counter = a.count + (leader * 2 + (leader == first ? 1 : 0)) * 2 + level;
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();
+                const unsigned before = atomicAdd(counter, 1);
+                s_last = before == (unsigned)count - 1;
+                if (s_last) {
+                    *counter = 0;
+                    __threadfence();
+                }
+            }
+            __syncthreads();
+            if (!s_last) break;
+            auto part_at = [&](int i) {
+                const int cta = leader + i * step;
+                return a.part + ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * kPart<D>;
+            };
+            const bool end_here = level == 1 || fans == 1;
+            for (int i = tid; i < rows * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), d = i % (D / 4) * 4;
+                float top = -INFINITY, total_l = 0.0f;
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float pm[kFan];
+#pragma unroll
+                for (int j = 0; j < kFan; ++j) {
+                    pm[j] = j < count ? __ldcg(part_at(j) + kRows * D + r) : -INFINITY;
+                    top = fmaxf(top, pm[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < kFan; ++j)
+                    if (j < count) {
+                        const float f = share_of(pm[j], top);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(j) + r * D + d));
+                        total_l += f * __ldcg(part_at(j) + kRows * D + kRows + r);
+                        sum.x += f * v.x;
+                        sum.y += f * v.y;
+                        sum.z += f * v.z;
+                        sum.w += f * v.w;
+                    }
+                if (end_here) {
+                    finish(r, d, sum.x, sum.y, total_l);
+                    finish(r, d + 2, sum.z, sum.w, total_l);
+                    if (d == 0) finish_lse(r, top, total_l);
+                } else {
+                    *reinterpret_cast<float4*>(part_at(0) + r * D + d) = sum;  // (no other thread reads these)
+                    if (d == 0) {
+                        s_fm[r] = top;
+                        s_fl[r] = total_l;
+                    }
+                }
+            }
+            if (end_here) break;
+            __syncthreads();  // all have read the maxima and sums
+            if (tid < rows) {
+                part_at(0)[kRows * D + tid] = s_fm[tid];
+                part_at(0)[kRows * D + kRows + tid] = s_fl[tid];
+            }
+        }
     }
-    if (a.lse != nullptr && threadIdx.x == 0)
-        a.lse[(int64_t)b * a.heads + head] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
 }
 
-}  // namespace
-
-cudaError_t launch_attn_decode(const DecodeArgs& a, int head_dim, int, cudaStream_t stream, bool pdl) {
+template <int D, bool EIGHT>
+cudaError_t launch(const DecodeArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
+    // groups of up to sixteen query heads of a key-value head, of equal size as far as that goes
+    const int shared_heads = a.heads / a.kv, per = (shared_heads + kRows - 1) / kRows;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)a.heads, (unsigned)a.B);
-    cfg.blockDim = dim3(32 * kWarps);
+    cfg.gridDim = dim3((unsigned)(num_sms < kMaxGrid ? num_sms : kMaxGrid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Shape<D, EIGHT>::kSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, EIGHT>, a, per * a.kv, (shared_heads + per - 1) / per);
+}
+
+template <int D, bool EIGHT>
+cudaError_t set_smem() {
+    return cudaFuncSetAttribute(attn_decode_kernel<D, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, EIGHT>::kSmem);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const DecodeArgs& a, int head_dim, int num_sms, cudaStream_t stream, bool pdl) {
+    const bool eight = a.k.scale != nullptr;
     switch (head_dim) {
-        case 64: return cudaLaunchKernelEx(&cfg, attn_decode_kernel<64>, a);
-        case 128: return cudaLaunchKernelEx(&cfg, attn_decode_kernel<128>, a);
-        case 256: return cudaLaunchKernelEx(&cfg, attn_decode_kernel<256>, a);
+        case 64: return eight ? launch<64, true>(a, num_sms, stream, pdl) : launch<64, false>(a, num_sms, stream, pdl);
+        case 128: return eight ? launch<128, true>(a, num_sms, stream, pdl) : launch<128, false>(a, num_sms, stream, pdl);
+        case 256: return eight ? launch<256, true>(a, num_sms, stream, pdl) : launch<256, false>(a, num_sms, stream, pdl);
     }
     return cudaErrorInvalidValue;
 }
 
-cudaError_t attn_decode_set_attributes() { return cudaSuccess; }
-size_t attn_decode_counters(int) { return 64; }
-size_t attn_decode_parts(int, int) { return 64; }
+cudaError_t attn_decode_set_attributes() {
+    for (const cudaError_t e : {set_smem<64, false>(), set_smem<64, true>(), set_smem<128, false>(), set_smem<128, true>(),
+                                set_smem<256, false>(), set_smem<256, true>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
+}
+
+size_t attn_decode_counters(int num_sms) { return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * 4; }
+size_t attn_decode_parts(int num_sms, int head_dim) {
+    return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * 2 * (kRows * head_dim + 2 * kRows);
+}
 
 }  // namespace arf
