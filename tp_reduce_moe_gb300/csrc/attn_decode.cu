@@ -15,11 +15,12 @@
 // its parts: the last CTA of each sixteen parts to arrive adds them up, the last of those
 // the sums, always in the order of the parts.  No CTA waits for another.
 //
-// Inside a CTA each warp takes every eighth unit of a segment (a range's share of an item)
-// and keeps a softmax of its own; the warps meet once a segment.  A warp streams its units
-// through a ring of its own in shared memory, keys and values in turn, by 16-byte
-// asynchronous copies that run ahead across segments, so that no barrier stands in the
-// stream; the places of a unit's tokens are looked up a unit earlier still.
+// A CTA's range is cut into eight for its warps.  A warp streams its units through a ring
+// of its own in shared memory, keys and values in turn, by 16-byte asynchronous copies that
+// run ahead across items, so that no barrier stands in the stream; the places of a unit's
+// tokens are looked up a unit earlier still.  Items that lie within a warp's share are
+// finished from its registers; what is cut is added up once, at the end of the CTA, in the
+// order of the warps.
 //
 // Roundings: scores, maxima, sums and o are fp32.  Weights go to the matrix instruction as
 // two bf16 (their rounding and its remainder: 2^-17, where one bf16 would add 0.7 times the
@@ -39,7 +40,6 @@ constexpr int kRing = 24576;       // bytes of a warp's ring
 constexpr int kMaxGrid = 256;
 constexpr int kFan = 16;           // parts that are joined at a time
 constexpr int kMinUnits = kWarps;  // of a CTA, while there are SMs left
-constexpr int kSlice = 32;         // columns that the warps' results are added up of at a time
 constexpr float kLazy = 8.0f;      // scores (log2) may pass the reference by so much before it moves
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -54,10 +54,9 @@ struct Shape {
     static constexpr int kHalf = kTok * kRow;  // bytes of a unit's keys (or values)
     static constexpr int kHalves = kRing / kHalf;
     static constexpr int kLead = kHalves - 1;  // halves that are asked for ahead
-    static constexpr int kPad = kSlice + (EIGHT ? 16 : 8);  // floats of a row of the merge buffer, free of bank conflicts
-    static constexpr int kMerge = kWarps * kRows * kPad * 4;
-    static constexpr int kSmem = kWarps * kRing + kMerge;
-    static_assert(kSmem + 2048 <= 232448, "shared memory of a CTA");
+    static constexpr int kSmem = kWarps * kRing;
+    static_assert(kSmem + 4096 <= 232448, "shared memory of a CTA");
+    static_assert(kRows * D * 4 <= kRing, "a warp's part of an item, in its ring");
     // where chunk c of row r lies, so that eight rows' chunks c are in eight different groups of banks
     __device__ static int place(int r, int c) {
         return r * kRow + ((kChunks >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & (kChunks - 1))) << 4);
@@ -122,7 +121,7 @@ __device__ __forceinline__ float quad_sum(float v) {
 // Two maxima's share: 2^(m - top), 0 for a part without tokens.
 __device__ __forceinline__ float share_of(float m, float top) { return ex2(m - (top == -INFINITY ? 0.0f : top)); }
 
-// A CTA's share of an item: units [u0, u1) of its n.
+// A warp's share of an item: units [u0, u1) of its n.
 struct Segment {
     int b, group;    // sequence; group of query heads
     int start, len;  // tokens looked at
@@ -170,7 +169,14 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
     return v;
 }
 
-// What the joins need: a part holds [kRows, D] sums, then kRows maxima and kRows sums of weights.
+// A part of an item that the warps or CTAs share.
+struct Part {
+    int64_t item;  // first unit of the item, -1: no part
+    int b, group, n;
+};
+
+// A CTA's part in memory holds [kRows, D] sums, then kRows maxima and kRows sums of weights; behind the parts, two a CTA,
+// lie the sums that its warps leave in mid-stream.
 template <int D>
 constexpr int kPart = kRows * D + 2 * kRows;
 
@@ -180,18 +186,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     constexpr int TOK = S::kTok, kTiles = TOK / 8, kSteps = D / 16;
     constexpr float kOffset = EIGHT ? 7.0f : 0.0f;  // halves: weights up to 2^(8 + 7), so that small ones keep their bits
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_fm[kRows], s_fl[kRows];
+    __shared__ float s_m[2 * kWarps][kRows], s_l[2 * kWarps][kRows], s_fm[kRows], s_fl[kRows];
+    __shared__ Part s_part[2 * kWarps];  // of each warp: what it began with, if it went on; what it ended with
+    __shared__ int s_run[2 * kWarps + 1];
     __shared__ int64_t s_scan[kWarps];
-    __shared__ int64_t s_first;  // units of the found sequence before the range's first
-    __shared__ int s_b, s_last;
+    __shared__ int64_t s_first[kWarps];  // units of the found sequence before the warp's first
+    __shared__ int s_b[kWarps], s_last;
     __shared__ unsigned s_mask[kWarps][8];
     pdl_wait();  // no global memory access before this point
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     const int shared_heads = a.heads / a.kv, per_head = groups / a.kv;
 
-    // ---- the range of this CTA
-    int64_t total, begin, end;
+    // ---- the ranges of this CTA's warps
+    int64_t total, begin, end;  // (the CTA's)
     int active;
     {
         const int each = (a.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(a.B, b0 + each);
@@ -217,11 +225,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         begin = active > 0 ? total * blockIdx.x / active : 0;
         end = active > 0 ? total * (blockIdx.x + 1) / active : 0;
         before += upto - mine;
-        if ((int)blockIdx.x < active && before <= begin && begin < before + mine) {
-            int b = b0;
-            for (int64_t n; before + (n = units(b)) <= begin; ++b) before += n;
-            s_b = b;
-            s_first = begin - before;
+        for (int w = 0; w < kWarps; ++w) {  // whose first unit is here?
+            const int64_t from = active > 0 ? total * (blockIdx.x * kWarps + w) / (active * kWarps) : 0;
+            if ((int)blockIdx.x < active && before <= from && from < before + mine) {
+                int b = b0;
+                int64_t skip = from - before;
+                for (int64_t n; (n = units(b)) <= skip; ++b) skip -= n;
+                s_b[w] = b;
+                s_first[w] = skip;
+            }
         }
         // rows without tokens
         for (int b = blockIdx.x; b < a.B; b += gridDim.x)
@@ -235,12 +247,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         if ((int)blockIdx.x >= active) return;
     }
 
+    const int64_t from = total * (blockIdx.x * kWarps + warp) / (active * kWarps);
+    const int64_t until = total * (blockIdx.x * kWarps + warp + 1) / (active * kWarps);
     Walk<TOK> walk;
-    walk.b = s_b;
-    walk.sequence(a);
-    walk.group = (int)(s_first / walk.n);
-    walk.u = (int)(s_first - (int64_t)walk.group * walk.n);
-    walk.left = end - begin;
+    walk.left = until - from;
+    if (walk.left > 0) {
+        walk.b = s_b[warp];
+        walk.sequence(a);
+        walk.group = (int)(s_first[warp] / walk.n);
+        walk.u = (int)(s_first[warp] - (int64_t)walk.group * walk.n);
+    }
 
     // ---- the stream of this warp's units: looked up, then asked for
     const uint32_t ring = smem_addr(smem) + warp * kRing;
@@ -268,13 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         }
     };
     auto seek = [&]() {  // from ask_u on, this warp's next unit
-        while (asking && ask_u >= ask.u1) {
+        if (asking && ask_u >= ask.u1) {
             asking = ahead.next(a, groups, &ask);
-            ask_u = ask.u0 + warp;
+            ask_u = ask.u0;
         }
         if (asking) look_up();
     };
-    if (asking) ask_u = ask.u0 + warp;
+    if (asking) ask_u = ask.u0;
     seek();
 
     auto issue = [&](bool keys) {
@@ -290,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                 const unsigned mask = __ballot_sync(0xffffffffu, page >= 0);
                 if (lane == 0) s_mask[warp][asked & 7] = mask;
                 ++asked;
-                ask_u += kWarps;
+                ++ask_u;
                 seek();
             }
         }
@@ -313,6 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     };
 #pragma unroll
     for (int i = 0; i < S::kLead; ++i) issue(i % 2 == 0);
+
+    auto mid_stream = [&](int w) { return a.part + (int64_t)gridDim.x * 2 * kPart<D> + ((int64_t)blockIdx.x * kWarps + w) * kRows * D; };
+    auto lse_of = [&](float top, float weight) { return weight == 0.0f ? -INFINITY : (top - kOffset + log2f(weight)) * kLn2; };
 
     // ---- segments
     uint32_t q[kSteps][4];
@@ -367,10 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
 
     int take = 0;        // slot of the ring that is used next
     unsigned taken = 0;  // units used
-    int64_t position = begin;
+    int64_t position = from;
     Segment seg;
     bool more = walk.next(a, groups, &seg);
-    load_q(seg);
+    if (lane < 2) s_part[2 * warp + lane].item = -1;
+    __syncwarp();
+    if (more) load_q(seg);
     while (more) {
         prepare_q(seg);
         float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
@@ -379,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
 
-        for (int u = seg.u0 + warp; u < seg.u1; u += kWarps) {
+        for (int u = seg.u0; u < seg.u1; ++u) {
             // scores of TOK tokens
             __syncwarp();  // the slot that is filled now has been read by all lanes
             issue(S::kLead % 2 == 0);
@@ -499,111 +520,129 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             }
         }
 
-        // ---- the warps' results, added up in the order of the warps
+        // ---- the item, or this warp's part of it
         const Segment done = seg;
         more = walk.next(a, groups, &seg);
-        if (more) load_q(seg);  // arrives while the warps meet
-        else pdl_trigger();
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] = quad_sum(l[r]);
-            if (t4 == 0) {
-                s_m[warp][g + 8 * r] = m[r];
-                s_l[warp][g + 8 * r] = l[r];
-            }
-        }
-        __syncthreads();
-        float share[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][g + 8 * r]);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += s_l[w][g + 8 * r] * share_of(s_m[w][g + 8 * r], top);
-            share[r] = share_of(m[r], top);
-            if (warp == 0 && t4 == 0) {
-                s_fm[g + 8 * r] = top;
-                s_fl[g + 8 * r] = sum;
-            }
-        }
-        const int kv_head = done.group / per_head, part_of = done.group - kv_head * per_head;
-        const int rows = min(rows_of_group, shared_heads - part_of * rows_of_group);
-        const int64_t out_row = (int64_t)done.b * a.heads + kv_head * shared_heads + part_of * rows_of_group;
-        const float vs = EIGHT ? a.v.scale[kv_head] : 1.0f;
-        const bool whole = done.u0 == 0 && done.u1 == done.n;
-        // a part's place: one for an item that began in a range before, one for an item that begins in this one
-        const int64_t item = position - done.u0;  // the item's first unit
+        if (more) load_q(seg);
+        const int64_t item = position - done.u0;
         position += done.u1 - done.u0;
-        float* part = a.part + ((int64_t)blockIdx.x * 2 + (done.u0 == 0 ? 1 : 0)) * kPart<D>;
-        float* merge = reinterpret_cast<float*>(smem + kWarps * kRing);
-        const int row = tid / 16, col = tid % 16 * 2;
-        auto finish = [&](int r, int d, float x, float y, float sum) {  // two columns of a row of the output
-            const float f = sum == 0.0f ? 0.0f : vs / sum;
-            *reinterpret_cast<uint32_t*>(a.out + (out_row + r) * D + d) = pack_bf16x2(x * f, y * f);
-        };
-        auto finish_lse = [&](int r, float top, float sum) {
-            if (a.lse != nullptr) a.lse[out_row + r] = sum == 0.0f ? -INFINITY : (top - kOffset + log2f(sum)) * kLn2;
-        };
+        const bool whole = done.u0 == 0 && done.u1 == done.n;
+        const int kv_head = done.group / per_head, first_row = (done.group - kv_head * per_head) * rows_of_group;
+        const int rows = min(rows_of_group, shared_heads - first_row);
+        const int which = 2 * warp + (more ? 0 : 1);
+        const int64_t out_row = (int64_t)done.b * a.heads + kv_head * shared_heads + first_row;
+        l[0] = quad_sum(l[0]);
+        l[1] = quad_sum(l[1]);
+        __syncwarp();  // all lanes have read the ring
 #pragma unroll
-        for (int i = 0; i < D / kSlice; ++i) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float* to = merge + (warp * kRows + g + 8 * r) * S::kPad;
-                if (EIGHT) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<float4*>(to + j * 16 + t4 * 4) =
-                            make_float4(o[4 * i + 2 * j][2 * r] * share[r], o[4 * i + 2 * j + 1][2 * r] * share[r],
-                                        o[4 * i + 2 * j][2 * r + 1] * share[r], o[4 * i + 2 * j + 1][2 * r + 1] * share[r]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float2*>(to + j * 8 + t4 * 2) = make_float2(o[4 * i + j][2 * r] * share[r], o[4 * i + j][2 * r + 1] * share[r]);
-                }
-            }
-            __syncthreads();
-            if (row < rows) {
-                float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 v = *reinterpret_cast<const float2*>(merge + (w * kRows + row) * S::kPad + col);
-                    sum.x += v.x;
-                    sum.y += v.y;
-                }
-                if (whole)
-                    finish(row, i * kSlice + col, sum.x, sum.y, s_fl[row]);
-                else
-                    *reinterpret_cast<float2*>(part + row * D + i * kSlice + col) = sum;
-            }
-            __syncthreads();
-        }
-        if (tid < rows) {
+        for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r;
+            if (row >= rows) continue;
             if (whole) {
-                finish_lse(tid, s_fm[tid], s_fl[tid]);
-            } else {
-                part[kRows * D + tid] = s_fm[tid];
-                part[kRows * D + kRows + tid] = s_fl[tid];
+                const float f = l[r] == 0.0f ? 0.0f : (EIGHT ? a.v.scale[kv_head] : 1.0f) / l[r];
+                uint16_t* to = a.out + (out_row + row) * D;
+#pragma unroll
+                for (int i = 0; i < D / 8; i += 2) {
+                    if (EIGHT) {
+                        *reinterpret_cast<uint2*>(to + i * 8 + t4 * 4) =
+                            make_uint2(pack_bf16x2(o[i][2 * r] * f, o[i + 1][2 * r] * f), pack_bf16x2(o[i][2 * r + 1] * f, o[i + 1][2 * r + 1] * f));
+                    } else {
+                        *reinterpret_cast<uint32_t*>(to + i * 8 + t4 * 2) = pack_bf16x2(o[i][2 * r] * f, o[i][2 * r + 1] * f);
+                        *reinterpret_cast<uint32_t*>(to + i * 8 + 8 + t4 * 2) = pack_bf16x2(o[i + 1][2 * r] * f, o[i + 1][2 * r + 1] * f);
+                    }
+                }
+                if (a.lse != nullptr && t4 == 0) a.lse[out_row + row] = lse_of(m[r], l[r]);
+                continue;
+            }
+            // (the stream has ended when the last part is written: its ring is free)
+            float* to = (more ? mid_stream(warp) : reinterpret_cast<float*>(smem + warp * kRing)) + row * D;
+#pragma unroll
+            for (int i = 0; i < D / 8; i += 2) {
+                if (EIGHT) {
+                    *reinterpret_cast<float4*>(to + i * 8 + t4 * 4) = make_float4(o[i][2 * r], o[i + 1][2 * r], o[i][2 * r + 1], o[i + 1][2 * r + 1]);
+                } else {
+                    *reinterpret_cast<float2*>(to + i * 8 + t4 * 2) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                    *reinterpret_cast<float2*>(to + i * 8 + 8 + t4 * 2) = make_float2(o[i + 1][2 * r], o[i + 1][2 * r + 1]);
+                }
+            }
+            if (t4 == 0) {
+                s_m[which][row] = m[r];
+                s_l[which][row] = l[r];
             }
         }
-        if (whole) continue;
+        if (!whole && lane == 0) s_part[which] = Part{item, done.b, done.group, done.n};
+    }
+    pdl_trigger();
 
-        // ---- the parts of an item over several CTAs: sixteen at a time, then the sixteens
-        auto owner = [&](int64_t x) { return (int)(((x + 1) * active - 1) / total); };
-        const int first = owner(item), last = owner(item + done.n - 1), parts = last - first + 1;
-        const int fans = (parts + kFan - 1) / kFan;
-        int count = 0, step = 0, leader = 0;
-        for (int level = 0; level < 2; ++level) {
-            if (level == 0) {
-                const int fan = ((int)blockIdx.x - first) / kFan;
-                leader = first + fan * kFan;
-                count = min(kFan, last - leader + 1);
-                step = 1;
-            } else {
-                leader = first;
-                count = fans;
-                step = kFan;
+    // ---- what the warps share: runs of parts of one item
+    __syncthreads();
+    Part mine{-1, 0, 0, 0};
+    if (lane < 2 * kWarps) mine = s_part[lane];
+    const unsigned there = __ballot_sync(0xffffffffu, mine.item >= 0), below = there & ((1u << lane) - 1);
+    const int64_t previous = __shfl_sync(0xffffffffu, mine.item, below ? 31 - __clz(below) : lane);
+    const bool starts = mine.item >= 0 && (below == 0 || previous != mine.item);
+    const unsigned start_mask = __ballot_sync(0xffffffffu, starts);
+    const int runs = __popc(start_mask);
+    if (runs == 0) return;
+    if (warp == 0 && starts) s_run[__popc(start_mask & ((1u << lane) - 1))] = lane;
+    if (tid == 0) s_run[runs] = 2 * kWarps;
+    __syncthreads();
+
+    // a row's output from its sums
+    auto finish = [&](const Part& p, int row, int d, float4 sum, float top, float weight) {
+        const int kv_head = p.group / per_head;
+        const int64_t out_row = (int64_t)p.b * a.heads + kv_head * shared_heads + (p.group - kv_head * per_head) * rows_of_group + row;
+        const float f = weight == 0.0f ? 0.0f : (EIGHT ? a.v.scale[kv_head] : 1.0f) / weight;
+        *reinterpret_cast<uint2*>(a.out + out_row * D + d) = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
+        if (a.lse != nullptr && d == 0) a.lse[out_row] = lse_of(top, weight);
+    };
+    auto rows_of = [&](const Part& p) { return min(rows_of_group, shared_heads - p.group % per_head * rows_of_group); };
+    // a CTA's part of an item: one for an item that began in a range before, one for an item that begins in this one
+    auto part_of = [&](int cta, bool begins) { return a.part + ((int64_t)cta * 2 + (begins ? 1 : 0)) * kPart<D>; };
+
+    for (int i = tid; i < runs * rows_of_group * (D / 4); i += kThreads) {
+        const int run = i / (rows_of_group * (D / 4)), rest = i - run * rows_of_group * (D / 4), row = rest / (D / 4), d = rest % (D / 4) * 4;
+        const int j0 = s_run[run], j1 = s_run[run + 1];
+        const Part p = s_part[j0];
+        if (row >= rows_of(p)) continue;
+        float top = -INFINITY, weight = 0.0f;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int j = j0; j < j1; ++j)
+            if (there >> j & 1) top = fmaxf(top, s_m[j][row]);
+        for (int j = j0; j < j1; ++j)
+            if (there >> j & 1) {
+                const float* from_part = j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * kRing) : mid_stream(j >> 1);
+                const float4 v = *reinterpret_cast<const float4*>(from_part + row * D + d);
+                const float f = share_of(s_m[j][row], top);
+                weight += f * s_l[j][row];
+                sum.x += f * v.x;
+                sum.y += f * v.y;
+                sum.z += f * v.z;
+                sum.w += f * v.w;
             }
+        if (p.item >= begin && p.item + p.n <= end) {
+            finish(p, row, d, sum, top, weight);
+        } else {
+            float* to = part_of(blockIdx.x, p.item >= begin);
+            *reinterpret_cast<float4*>(to + row * D + d) = sum;
+            if (d == 0) {
+                to[kRows * D + row] = top;
+                to[kRows * D + kRows + row] = weight;
+            }
+        }
+    }
+
+    // ---- what CTAs share: sixteen parts at a time, then the sixteens
+    auto owner = [&](int64_t x) { return (int)(((x + 1) * active - 1) / total); };
+    for (int run = 0; run < runs; run += max(1, runs - 1)) {  // the first and the last
+        const Part p = s_part[s_run[run]];
+        if (p.item >= begin && p.item + p.n <= end) continue;
+        const int first = owner(p.item), last = owner(p.item + p.n - 1);
+        const int fans = (last - first + kFan) / kFan, rows = rows_of(p);
+        for (int level = 0; level < 2; ++level) {
+            const int fan = ((int)blockIdx.x - first) / kFan;
+            const int leader = level == 0 ? first + fan * kFan : first, step = level == 0 ? 1 : kFan;
+            const int count = level == 0 ? min(kFan, last - leader + 1) : fans;
             // this level's counter, of the leader's part
             unsigned* counter = a.count + (leader * 2 + (leader == first ? 1 : 0)) * 2 + level;
             __syncthreads();
@@ -618,41 +657,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             }
             __syncthreads();
             if (!s_last) break;
-            auto part_at = [&](int i) {
-                const int cta = leader + i * step;
-                return a.part + ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * kPart<D>;
-            };
+            auto part_at = [&](int i) { return part_of(leader + i * step, leader + i * step == first); };
             const bool end_here = level == 1 || fans == 1;
             for (int i = tid; i < rows * (D / 4); i += kThreads) {
                 const int r = i / (D / 4), d = i % (D / 4) * 4;
-                float top = -INFINITY, total_l = 0.0f;
+                float top = -INFINITY, weight = 0.0f, pm[kFan], pl[kFan];
                 float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float pm[kFan];
 #pragma unroll
                 for (int j = 0; j < kFan; ++j) {
                     pm[j] = j < count ? __ldcg(part_at(j) + kRows * D + r) : -INFINITY;
-                    top = fmaxf(top, pm[j]);
+                    pl[j] = j < count ? __ldcg(part_at(j) + kRows * D + kRows + r) : 0.0f;
                 }
+#pragma unroll
+                for (int j = 0; j < kFan; ++j) top = fmaxf(top, pm[j]);
 #pragma unroll
                 for (int j = 0; j < kFan; ++j)
                     if (j < count) {
                         const float f = share_of(pm[j], top);
                         const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(j) + r * D + d));
-                        total_l += f * __ldcg(part_at(j) + kRows * D + kRows + r);
+                        weight += f * pl[j];
                         sum.x += f * v.x;
                         sum.y += f * v.y;
                         sum.z += f * v.z;
                         sum.w += f * v.w;
                     }
                 if (end_here) {
-                    finish(r, d, sum.x, sum.y, total_l);
-                    finish(r, d + 2, sum.z, sum.w, total_l);
-                    if (d == 0) finish_lse(r, top, total_l);
+                    finish(p, r, d, sum, top, weight);
                 } else {
                     *reinterpret_cast<float4*>(part_at(0) + r * D + d) = sum;  // (no other thread reads these)
                     if (d == 0) {
                         s_fm[r] = top;
-                        s_fl[r] = total_l;
+                        s_fl[r] = weight;
                     }
                 }
             }
@@ -709,7 +744,7 @@ cudaError_t attn_decode_set_attributes() {
 
 size_t attn_decode_counters(int num_sms) { return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * 4; }
 size_t attn_decode_parts(int num_sms, int head_dim) {
-    return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * 2 * (kRows * head_dim + 2 * kRows);
+    return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * (2 * (kRows * head_dim + 2 * kRows) + kWarps * kRows * head_dim);
 }
 
 }  // namespace arf
