@@ -317,6 +317,10 @@ ar_status ar_attn_decode(ar_attn* m, const ar_kv_cache* cache, const void* q, co
     a.heads = m->heads;
     a.kv = m->kv;
     a.page_size = m->page_size;
+    // 2^(s - 1) < page_size <= 2^s: m = ceil(2^(31 + s) / page_size) < 2^32, and m page_size passes 2^(31 + s) by less than
+    // 2^s, too little for the quotient of a number below 2^31 to change
+    while ((1 << a.page_shift) < m->page_size) ++a.page_shift;
+    a.page_mul = (unsigned)((((uint64_t)1 << (31 + a.page_shift)) + m->page_size - 1) / m->page_size);
     a.window = (int)(window < kMostTokens ? window : 0);
     a.scale = scale * kLog2e;
     return launched(arf::launch_attn_decode(a, m->D, m->num_sms, static_cast<cudaStream_t>(stream), (m->flags & AR_WS_PDL) != 0));

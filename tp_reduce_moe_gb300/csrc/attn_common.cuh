@@ -53,6 +53,8 @@ struct DecodeArgs {
     int64_t most;  // longest length that the page table holds
     int pages;
     int B, heads, kv, page_size;
+    unsigned page_mul;  // token / page_size == token * page_mul >> (31 + page_shift) for tokens below 2^31
+    int page_shift;
     int window;    // 0: none
     float scale;   // of the scores, times log2(e)
 };

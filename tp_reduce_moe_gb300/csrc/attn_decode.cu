@@ -39,7 +39,7 @@ constexpr int kRows = 16;          // query heads of an item
 constexpr int kRing = 24576;       // bytes of a warp's ring
 constexpr int kMaxGrid = 256;
 constexpr int kFan = 16;           // parts that are joined at a time
-constexpr int kMinUnits = kWarps;  // of a CTA, while there are SMs left
+constexpr int kMinUnits = 4;       // of a warp, while there are SMs left
 constexpr float kLazy = 8.0f;      // scores (log2) may pass the reference by so much before it moves
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -160,6 +160,11 @@ struct Walk {
     }
 };
 
+// Quotients of numbers that are small as a rule.
+__device__ __forceinline__ int64_t quotient64(int64_t n, int64_t d) {
+    return ((n | d) >> 31) == 0 ? (int64_t)((unsigned)n / (unsigned)d) : n / d;
+}
+
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -187,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     constexpr float kOffset = EIGHT ? 7.0f : 0.0f;  // halves: weights up to 2^(8 + 7), so that small ones keep their bits
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[2 * kWarps][kRows], s_l[2 * kWarps][kRows], s_fm[kRows], s_fl[kRows];
+    __shared__ float s_share[2 * kWarps][kRows], s_top[2 * kWarps][kRows], s_weight[2 * kWarps][kRows];
     __shared__ Part s_part[2 * kWarps];  // of each warp: what it began with, if it went on; what it ended with
     __shared__ int s_run[2 * kWarps + 1];
     __shared__ int64_t s_scan[kWarps];
@@ -198,11 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     const int g = lane >> 2, t4 = lane & 3;
     const int shared_heads = a.heads / a.kv, per_head = groups / a.kv;
 
-    // ---- the ranges of this CTA's warps
-    int64_t total, begin, end;  // (the CTA's)
-    int active;
+    // ---- the ranges of this CTA's warps: equal ones, so that the last may be short or empty
+    int64_t total, each;
     {
-        const int each = (a.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(a.B, b0 + each);
+        const int per_thread = (a.B + kThreads - 1) / kThreads, b0 = tid * per_thread, b1 = min(a.B, b0 + per_thread);
         auto units = [&](int b) {
             const int len = checked_length(a, b, blockIdx.x == 0);
             const int n = a.window > 0 && len > a.window ? a.window : len;
@@ -213,48 +218,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         const int64_t upto = warp_scan(mine, lane);
         if (lane == 31) s_scan[warp] = upto;
         __syncthreads();
-        int64_t before = 0;
+        int64_t before = upto - mine;
         total = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += s_scan[w];
             total += s_scan[w];
         }
-        const int64_t wanted = (total + kMinUnits - 1) / kMinUnits;
-        active = (int)(wanted < (int64_t)gridDim.x ? wanted : (int64_t)gridDim.x);
-        begin = active > 0 ? total * blockIdx.x / active : 0;
-        end = active > 0 ? total * (blockIdx.x + 1) / active : 0;
-        before += upto - mine;
+        each = max((int64_t)kMinUnits, quotient64(total + gridDim.x * kWarps - 1, gridDim.x * kWarps));
         for (int w = 0; w < kWarps; ++w) {  // whose first unit is here?
-            const int64_t from = active > 0 ? total * (blockIdx.x * kWarps + w) / (active * kWarps) : 0;
-            if ((int)blockIdx.x < active && before <= from && from < before + mine) {
+            const int64_t from = each * (blockIdx.x * kWarps + w);
+            if (before <= from && from < before + mine) {
                 int b = b0;
                 int64_t skip = from - before;
-                for (int64_t n; (n = units(b)) <= skip; ++b) skip -= n;
+                if (per_thread > 1)
+                    for (int64_t n; (n = units(b)) <= skip; ++b) skip -= n;
                 s_b[w] = b;
                 s_first[w] = skip;
             }
         }
-        // rows without tokens
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-            if (checked_length(a, b, false) == 0) {
-                for (int i = tid; i < a.heads * D / 8; i += kThreads)
-                    st_global16(a.out + (int64_t)b * a.heads * D + i * 8, make_uint4(0, 0, 0, 0));
-                if (a.lse != nullptr)
-                    for (int i = tid; i < a.heads; i += kThreads) a.lse[(int64_t)b * a.heads + i] = -INFINITY;
-            }
         __syncthreads();
-        if ((int)blockIdx.x >= active) return;
     }
-
-    const int64_t from = total * (blockIdx.x * kWarps + warp) / (active * kWarps);
-    const int64_t until = total * (blockIdx.x * kWarps + warp + 1) / (active * kWarps);
+    const int64_t from = each * (blockIdx.x * kWarps + warp);
+    const int64_t begin = each * (blockIdx.x * kWarps), end = begin + each * kWarps;  // the CTA's
     Walk<TOK> walk;
-    walk.left = until - from;
+    walk.left = min(each, total - from);
     if (walk.left > 0) {
         walk.b = s_b[warp];
         walk.sequence(a);
-        walk.group = (int)(s_first[warp] / walk.n);
+        walk.group = (int)quotient64(s_first[warp], walk.n);
         walk.u = (int)(s_first[warp] - (int64_t)walk.group * walk.n);
     }
 
@@ -262,36 +254,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     const uint32_t ring = smem_addr(smem) + warp * kRing;
     Walk<TOK> ahead = walk;
     Segment ask;
-    int ask_u = 0;             // unit that is looked up
+    int ask_u = 0;             // unit that is asked for next
+    int ask_last = 0;          // last page of its sequence
     bool asking = ahead.next(a, groups, &ask);
-    int page = -1, in_page = 0;  // of this lane's token of that unit
-    int64_t k_at = -1, v_at = -1;  // places of the unit that is being asked for
+    int64_t k_at = -1, v_at = -1;  // places of this lane's token of the unit that is being asked for
     bool live = false;             // there is such a unit
     unsigned asked = 0;            // units asked for
     int fill = 0;                  // slot of the ring that is filled next
-
-    auto look_up = [&]() {
-        page = -1;
-        const int64_t token = ask.start + (int64_t)ask_u * TOK + lane;
-        if (lane < TOK && token < ask.len) {
-            const int index = (int)token / a.page_size;
-            in_page = (int)token - index * a.page_size;
-            page = a.table[ask.b * a.table_stride + index];
-            if ((unsigned)page >= (unsigned)a.pages) {
-                atomicOr(a.err, kErrPageRange);
-                page = -1;
-            }
-        }
+    // the page table's entries from table_at on: this lane's of the first 32 and of the next 32
+    int table_at = 0, entry = 0, entry_next = 0;
+    auto page_of = [&](int64_t token) { return (int)((uint64_t)token * a.page_mul >> (31 + a.page_shift)); };
+    auto table_entry = [&](int index) {  // -1 behind the sequence's last
+        return index <= ask_last ? a.table[ask.b * a.table_stride + index] : -1;
     };
-    auto seek = [&]() {  // from ask_u on, this warp's next unit
-        if (asking && ask_u >= ask.u1) {
-            asking = ahead.next(a, groups, &ask);
-            ask_u = ask.u0;
-        }
-        if (asking) look_up();
+    auto look_up = [&]() {  // a new segment
+        ask_u = ask.u0;
+        ask_last = page_of(ask.len - 1);
+        table_at = page_of(ask.start + (int64_t)ask_u * TOK);
+        entry = table_entry(table_at + lane);
+        entry_next = table_entry(table_at + 32 + lane);
     };
-    if (asking) ask_u = ask.u0;
-    seek();
+    if (asking) look_up();
 
     auto issue = [&](bool keys) {
         if (keys) {
@@ -299,15 +282,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             live = asking;
             if (asking) {
                 const int head = ask.group / per_head;
-                if (page >= 0) {
+                const int64_t first = ask.start + (int64_t)ask_u * TOK, token = first + lane;
+                while (page_of(first) - table_at >= 32) {
+                    table_at += 32;
+                    entry = entry_next;
+                    entry_next = table_entry(table_at + 32 + lane);
+                }
+                const int index = page_of(token), in_page = (int)token - index * a.page_size, at = index - table_at;
+                const int here = __shfl_sync(0xffffffffu, entry, at & 31), next = __shfl_sync(0xffffffffu, entry_next, at & 31);
+                const int page = at < 32 ? here : next;
+                const bool wanted = lane < TOK && token < ask.len, there = wanted && (unsigned)page < (unsigned)a.pages;
+                if (wanted && !there) atomicOr(a.err, kErrPageRange);
+                if (there) {
                     k_at = page * a.k.page + in_page * a.k.token + head * a.k.head;
                     v_at = page * a.v.page + in_page * a.v.token + head * a.v.head;
                 }
-                const unsigned mask = __ballot_sync(0xffffffffu, page >= 0);
+                const unsigned mask = __ballot_sync(0xffffffffu, there);
                 if (lane == 0) s_mask[warp][asked & 7] = mask;
                 ++asked;
-                ++ask_u;
-                seek();
+                if (++ask_u == ask.u1) {
+                    asking = ahead.next(a, groups, &ask);
+                    if (asking) look_up();
+                }
             }
         }
         const int64_t at = keys ? k_at : v_at;
@@ -327,15 +323,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         copy_commit();
         fill = fill + 1 == S::kHalves ? 0 : fill + 1;
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < S::kLead; ++i) issue(i % 2 == 0);
+
+    // rows without tokens: zeros, dealt to the warps
+    for (int64_t b = blockIdx.x + (int64_t)gridDim.x * warp; b < a.B; b += gridDim.x * kWarps)
+        if (checked_length(a, (int)b, false) == 0) {
+            for (int j = lane; j < a.heads * D / 8; j += 32) st_global16(a.out + b * a.heads * D + j * 8, make_uint4(0, 0, 0, 0));
+            if (a.lse != nullptr)
+                for (int j = lane; j < a.heads; j += 32) a.lse[b * a.heads + j] = -INFINITY;
+        }
+    if (begin >= total) return;
 
     auto mid_stream = [&](int w) { return a.part + (int64_t)gridDim.x * 2 * kPart<D> + ((int64_t)blockIdx.x * kWarps + w) * kRows * D; };
     auto lse_of = [&](float top, float weight) { return weight == 0.0f ? -INFINITY : (top - kOffset + log2f(weight)) * kLn2; };
 
     // ---- segments
     uint32_t q[kSteps][4];
-    float q_scale[2];  // log2(e) * scale * scale of the keys * power of two of the row, rows g and g + 8
+    float q_scale[2];  // of the scores, rows g and g + 8: log2(e) * scale * scale of the keys * power of two of the row
     auto load_q = [&](const Segment& s) {
         const int head = s.group / per_head, part = s.group - head * per_head;
 #pragma unroll
@@ -356,31 +361,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                 q[i][r] = there ? v.x : 0;
                 q[i][r + 2] = there ? v.y : 0;
             }
-            q_scale[r] = a.scale;
+            q_scale[r] = EIGHT ? a.scale * a.k.scale[head] : a.scale;
         }
     };
-    auto prepare_q = [&](const Segment& s) {
-        if (!EIGHT) return;
-        const float ks = a.k.scale[s.group / per_head];
+    auto prepare_q = [&]() {
+        if constexpr (EIGHT) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float top = 0.0f;
+            for (int r = 0; r < 2; ++r) {
+                float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
+                for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-                for (int c = r; c < 4; c += 2)
-                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[i][c] << 16)), fabsf(__uint_as_float(q[i][c] & 0xffff0000u))));
-            top = quad_max(top);
-            // the power of two that brings the row's largest value to [1, 2) (or next to it, at the ends of the range)
-            int e = (int)(__float_as_uint(top) >> 23) - 127;
-            e = e < -126 ? -126 : e > 126 ? 126 : e;
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+                    for (int c = r; c < 4; c += 2)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[i][c] << 16)), fabsf(__uint_as_float(q[i][c] & 0xffff0000u))));
+                top = quad_max(top);
+                // the power of two that brings the row's largest value to [1, 2) (or next to it, at the ends of the range)
+                int e = (int)(__float_as_uint(top) >> 23) - 127;
+                e = e < -126 ? -126 : e > 126 ? 126 : e;
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
+                for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-                for (int c = r; c < 4; c += 2)
-                    q[i][c] = pack_f16x2(__uint_as_float(q[i][c] << 16) * down, __uint_as_float(q[i][c] & 0xffff0000u) * down);
-            q_scale[r] = a.scale * ks * up;
+                    for (int c = r; c < 4; c += 2)
+                        q[i][c] = pack_f16x2(__uint_as_float(q[i][c] << 16) * down, __uint_as_float(q[i][c] & 0xffff0000u) * down);
+                q_scale[r] *= up;
+            }
         }
     };
 
@@ -393,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     __syncwarp();
     if (more) load_q(seg);
     while (more) {
-        prepare_q(seg);
+        prepare_q();
         float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
@@ -600,40 +605,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     // a CTA's part of an item: one for an item that began in a range before, one for an item that begins in this one
     auto part_of = [&](int cta, bool begins) { return a.part + ((int64_t)cta * 2 + (begins ? 1 : 0)) * kPart<D>; };
 
-    for (int i = tid; i < runs * rows_of_group * (D / 4); i += kThreads) {
-        const int run = i / (rows_of_group * (D / 4)), rest = i - run * rows_of_group * (D / 4), row = rest / (D / 4), d = rest % (D / 4) * 4;
+    // what each part counts, and the runs' maxima and weights
+    {
+        static_assert(kThreads == 2 * kWarps * kRows, "a thread for each part and row");
+        const int j = tid / kRows, row = tid % kRows;
+        const int first = 31 - __clz(start_mask & ((2u << j) - 1));  // (the run of part j begins here)
+        if (there >> j & 1) {
+            const unsigned behind = start_mask & ~((2u << first) - 1);
+            const unsigned of_run = there & ~((1u << first) - 1) & (behind ? (1u << (__ffs(behind) - 1)) - 1 : ~0u);
+            float top = -INFINITY, weight = 0.0f;
+            for (unsigned i = of_run; i; i &= i - 1) top = fmaxf(top, s_m[__ffs(i) - 1][row]);
+            for (unsigned i = of_run; i; i &= i - 1) weight += share_of(s_m[__ffs(i) - 1][row], top) * s_l[__ffs(i) - 1][row];
+            s_share[j][row] = share_of(s_m[j][row], top);
+            s_top[j][row] = top;
+            s_weight[j][row] = weight;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < runs * kRows * (D / 4); i += kThreads) {
+        const int run = i / (kRows * (D / 4)), row = i / (D / 4) % kRows, d = i % (D / 4) * 4;
         const int j0 = s_run[run], j1 = s_run[run + 1];
         const Part p = s_part[j0];
         if (row >= rows_of(p)) continue;
-        float top = -INFINITY, weight = 0.0f;
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int j = j0; j < j1; ++j)
-            if (there >> j & 1) top = fmaxf(top, s_m[j][row]);
         for (int j = j0; j < j1; ++j)
             if (there >> j & 1) {
                 const float* from_part = j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * kRing) : mid_stream(j >> 1);
                 const float4 v = *reinterpret_cast<const float4*>(from_part + row * D + d);
-                const float f = share_of(s_m[j][row], top);
-                weight += f * s_l[j][row];
+                const float f = s_share[j][row];
                 sum.x += f * v.x;
                 sum.y += f * v.y;
                 sum.z += f * v.z;
                 sum.w += f * v.w;
             }
         if (p.item >= begin && p.item + p.n <= end) {
-            finish(p, row, d, sum, top, weight);
+            finish(p, row, d, sum, s_top[j0][row], s_weight[j0][row]);
         } else {
             float* to = part_of(blockIdx.x, p.item >= begin);
             *reinterpret_cast<float4*>(to + row * D + d) = sum;
             if (d == 0) {
-                to[kRows * D + row] = top;
-                to[kRows * D + kRows + row] = weight;
+                to[kRows * D + row] = s_top[j0][row];
+                to[kRows * D + kRows + row] = s_weight[j0][row];
             }
         }
     }
 
     // ---- what CTAs share: sixteen parts at a time, then the sixteens
-    auto owner = [&](int64_t x) { return (int)(((x + 1) * active - 1) / total); };
+    auto owner = [&](int64_t unit) { return (int)quotient64(unit, each * kWarps); };
     for (int run = 0; run < runs; run += max(1, runs - 1)) {  // the first and the last
         const Part p = s_part[s_run[run]];
         if (p.item >= begin && p.item + p.n <= end) continue;
@@ -661,25 +679,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             const bool end_here = level == 1 || fans == 1;
             for (int i = tid; i < rows * (D / 4); i += kThreads) {
                 const int r = i / (D / 4), d = i % (D / 4) * 4;
+                // everything is asked for before anything is used
                 float top = -INFINITY, weight = 0.0f, pm[kFan], pl[kFan];
-                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float4 v[kFan], sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int j = 0; j < kFan; ++j) {
-                    pm[j] = j < count ? __ldcg(part_at(j) + kRows * D + r) : -INFINITY;
-                    pl[j] = j < count ? __ldcg(part_at(j) + kRows * D + kRows + r) : 0.0f;
+                    const float* from_part = part_at(j < count ? j : 0);
+                    pm[j] = __ldcg(from_part + kRows * D + r);
+                    pl[j] = __ldcg(from_part + kRows * D + kRows + r);
+                    v[j] = __ldcg(reinterpret_cast<const float4*>(from_part + r * D + d));
                 }
 #pragma unroll
-                for (int j = 0; j < kFan; ++j) top = fmaxf(top, pm[j]);
+                for (int j = 0; j < kFan; ++j)
+                    if (j < count) top = fmaxf(top, pm[j]);
 #pragma unroll
                 for (int j = 0; j < kFan; ++j)
                     if (j < count) {
                         const float f = share_of(pm[j], top);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(j) + r * D + d));
                         weight += f * pl[j];
-                        sum.x += f * v.x;
-                        sum.y += f * v.y;
-                        sum.z += f * v.z;
-                        sum.w += f * v.w;
+                        sum.x += f * v[j].x;
+                        sum.y += f * v[j].y;
+                        sum.z += f * v[j].z;
+                        sum.w += f * v[j].w;
                     }
                 if (end_here) {
                     finish(p, r, d, sum, top, weight);
