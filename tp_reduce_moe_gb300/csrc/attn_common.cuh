@@ -48,7 +48,8 @@ struct DecodeArgs {
     float* lse;     // [B, heads] or nullptr
     unsigned* err;
     unsigned* count;  // arrival counters, zero between calls
-    float* part;      // parts of rows split over several CTAs
+    float* part;      // parts of rows split over several warps and CTAs
+    const uint8_t* zeros;  // kMaxHeadDim * 2 bytes of zeros, 16-byte aligned
     int64_t table_stride;
     int64_t most;  // longest length that the page table holds
     int pages;
