@@ -54,6 +54,7 @@ struct DecodeArgs {
     int64_t most;  // longest length that the page table holds
     int pages;
     int B, heads, kv, page_size;
+    int shared, per_head, groups, rows_of_group;  // query heads of a key-value head, their groups, all groups, heads of one
     unsigned page_mul;  // token / page_size == token * page_mul >> (31 + page_shift) for tokens below 2^31
     int page_shift;
     int window;    // 0: none

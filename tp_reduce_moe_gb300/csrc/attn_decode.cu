@@ -17,9 +17,8 @@
 // A warp streams its units through a ring of its own in shared memory, keys and values in
 // turn, by 16-byte asynchronous copies that run ahead across items, so that no barrier stands
 // in the stream.  Items within a warp's range are finished by it; what is cut is added up
-// once, at the end of the CTA, in the order of the warps, and over CTAs by the last of each
-// sixteen to arrive and the last of those, always in the order of the parts.  No CTA waits
-// for another.
+// once, at the end of the CTA, in the order of the warps, and over CTAs by the last of them to
+// arrive, in the order of the CTAs.  No CTA waits for another.
 //
 // Roundings: scores, maxima, sums and o are fp32.  Weights go to the matrix instruction as
 // two bf16 (their rounding and its remainder: 2^-17, where one bf16 would add 0.7 times the
@@ -33,7 +32,7 @@ namespace arf {
 namespace {
 
 constexpr int kMaxGrid = 256;
-constexpr int kFan = 16;          // parts that are joined at a time
+constexpr int kFew = 24;          // parts that are joined at once
 constexpr float kLazy = 8.0f;     // scores (log2) may pass the reference by so much before it moves
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -52,15 +51,17 @@ struct Shape {
     static constexpr int kHalves = kRing / kHalf;
     static constexpr int kLead = kHalves - 1;  // halves that are asked for ahead
     static constexpr int kLeast = kHalf >= 4096 ? 1 : 4096 / kHalf;  // units of a warp, while there are SMs left
+    static constexpr int kCost = kHalf >= 8192 ? 1 : 8192 / kHalf;   // units that an item counts for besides its own
     static constexpr int kAlone = 131072 / kHalf;  // units by which a CTA that keeps an item may pass an equal share
-    static constexpr int kPitch = D + 4;       // floats from a row of sums to the next, free of bank conflicts
-    static constexpr int kSums = kRows * kPitch;
-    static constexpr int kPart = kSums + 2 * kRows;  // a CTA's part in memory: sums, maxima, sums of weights
+    static constexpr int kPitch = D + 4;       // floats from a row of sums to the next in shared memory, free of bank conflicts
+    // In memory nothing is between the rows: sectors that are not written whole would have to be read before they are merged.
+    static constexpr int kSums = kRows * D;
+    static constexpr int kPart = kSums + 2 * kRows;  // a CTA's part: sums, maxima, sums of weights
     static constexpr int kSmem = kWarps * kRing;
     static_assert(kSmem + 16384 <= 232448, "shared memory of a CTA");
-    static_assert(kSums * 4 <= kRing, "a warp's sums, in its ring");
+    static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums, in its ring");
     static_assert(kLead <= 11, "units that are asked for and not used, of the eight masks that are kept");
-    static_assert(kFan * kRows <= kThreads, "a thread for each part and row of a join");
+    static_assert(kPart % 4 == 0 && kSmem >= kPart * 4, "parts come by 16 bytes");
     // where chunk c of row r lies, so that eight rows' chunks c are in eight different groups of banks
     __device__ static int place(int r, int c) {
         return r * kRow + ((kChunks >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & (kChunks - 1))) << 4);
@@ -131,6 +132,7 @@ struct Segment {
     int start, len;  // tokens looked at
     int u0, u1, n;
     int row, rows;   // first row of the output [B * heads], and how many
+    int64_t item;    // where the item's first unit is among all
 };
 
 // What is rare is not inline: it would crowd the loop out of the instruction cache, and code that a call runs through once is
@@ -147,12 +149,14 @@ __device__ __forceinline__ int units_of(int2 t) {
     return (int)(((int64_t)t.y - t.x + TOK - 1) / TOK);
 }
 
-// Walks the segments of a range of units.
-template <int TOK>
+// Walks the segments of a range of units.  An item of n units counts for COST more, before the first, for what it costs to begin
+// and end one; these are walked over.
+template <int TOK, int COST>
 struct Walk {
-    int b, group, u;
+    int b, group, u;  // the next unit, of COST + n
     int start, len, n;
-    int64_t left;  // units of the range that are not handed out
+    int64_t item;     // where the item's first unit (behind what it costs) is among all
+    int64_t left;     // units of the range that are not handed out; 0 once no real one is among them
 
     __device__ __forceinline__ void sequence(const DecodeArgs& a) {
         const int2 t = tokens_of(a, b, false);
@@ -160,11 +164,15 @@ struct Walk {
         len = t.y;
         n = units_of<TOK>(t);
     }
-    // The next segment of a range that has units left.
-    __device__ __noinline__ void next(const DecodeArgs& a, int groups, int rows_of_group, Segment* s) {
-        if (u == n) {  // the item is done: the next one that has units (there is one, for some are left)
+    __device__ __forceinline__ void begin() {
+        if (left <= COST - u) left = 0;
+    }
+    // The next segment of a range that has real units left.
+    __device__ __noinline__ void next(const DecodeArgs& a, Segment* s) {
+        if (u == n + COST) {  // the item is done: the next one that has units (there is one, for some are left)
             u = 0;
-            if (++group == groups) {
+            item += n + COST;
+            if (++group == a.groups) {
                 group = 0;
 #pragma unroll 1
                 do {
@@ -173,12 +181,13 @@ struct Walk {
                 } while (n == 0);
             }
         }
-        const int take = (int)(left < n - u ? left : n - u);
-        const int per_head = groups / a.kv, shared = a.heads / a.kv, head = group / per_head;
-        const int row = (group - head * per_head) * rows_of_group;
-        *s = Segment{b, head, start, len, u, u + take, n, b * a.heads + head * shared + row, min(rows_of_group, shared - row)};
+        const int take = (int)(left < n + COST - u ? left : n + COST - u);
+        const int head = a.per_head == 1 ? group : group / a.per_head, row = (group - head * a.per_head) * a.rows_of_group;
+        *s = Segment{b, head, start, len, max(u - COST, 0), u + take - COST, n,
+                     b * a.heads + head * a.shared + row, min(a.rows_of_group, a.shared - row), item};
         u += take;
         left -= take;
+        if (left <= COST) left = 0;
     }
 };
 
@@ -202,6 +211,12 @@ struct Part {
     int n, kv_head, row, rows;
 };
 
+// An item that CTAs share, `parts` of them from `first` on: every `step`-th has a sum, of which this CTA may add up `count`
+// from `leader` on, each `fan` of them.
+struct Join {
+    int first, parts, fan, step, leader, count;
+};
+
 // Four columns of a row of the output, and with the first of them its lse.
 __device__ __noinline__ void finish_row(const DecodeArgs& a, int row, int d, int D, float4 sum, float weight, float vs, float top) {
     const float f = weight == 0.0f ? 0.0f : __fdividef(vs, weight);
@@ -218,7 +233,7 @@ __device__ __forceinline__ void add(float4& sum, float f, float4 v) {
 
 template <int D, bool EIGHT, int NT>
 __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
-    attn_decode_kernel(const __grid_constant__ DecodeArgs a, int groups, int rows_of_group) {
+    attn_decode_kernel(const __grid_constant__ DecodeArgs a) {
     using S = Shape<D, EIGHT, NT>;
     constexpr int TOK = S::kTok, MT = TOK / 16, kSteps = D / 16, kWarps = S::kWarps, kThreads = S::kThreads, kRows = S::kRows;
     constexpr float kOffset = EIGHT ? 7.0f : 0.0f;  // halves: weights up to 2^(8 + 7), so that small ones keep their bits
@@ -226,11 +241,12 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     __shared__ float s_m[2 * kWarps][kRows], s_l[2 * kWarps][kRows], s_share[2 * kWarps][kRows], s_top[2 * kWarps][kRows],
         s_weight[2 * kWarps][kRows];
     __shared__ Part s_part[2 * kWarps];  // of each warp: what it began with, if it went on; what it ended with
-    __shared__ int s_run[2 * kWarps + 1];
+    __shared__ int s_run[2 * kWarps];
     __shared__ int64_t s_scan[kWarps];
     __shared__ int s_most[kWarps];
     __shared__ int64_t s_first[kWarps];  // units of the found sequence before the warp's first
-    __shared__ int s_b[kWarps], s_last;
+    __shared__ int s_b[kWarps];
+    __shared__ Join s_join[2];
     __shared__ unsigned s_mask[kWarps][8];
     __shared__ const uint8_t* s_row[kWarps][2][32];  // where the keys and values of a unit's tokens are
     pdl_wait();  // no global memory access before this point
@@ -239,45 +255,52 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
 
     // ---- what this CTA's warps take
     int64_t total, each = 0;   // units, and units of a warp where all are dealt out
-    int64_t from, begin, end;  // first unit of this warp; units of this CTA
-    Walk<TOK> walk;
+    int64_t begin, end;        // units of this CTA
+    Walk<TOK, S::kCost> walk;
     {
-        const int per_thread = (a.B + kThreads - 1) / kThreads, b0 = tid * per_thread, b1 = min(a.B, b0 + per_thread);
-        auto units = [&](int b) { return units_of<TOK>(tokens_of(a, b, blockIdx.x == 0)); };  // of one item
+        auto units = [&](int b) {  // of one item, with what it costs
+            const int n = units_of<TOK>(tokens_of(a, b, blockIdx.x == 0));
+            return n > 0 ? n + S::kCost : 0;
+        };
+        // a thread's sequences, and before them the units of the threads before; few sequences: each warp sums by itself
+        const bool few = a.B <= 32;
+        const int per_thread = few ? 1 : (a.B + kThreads - 1) / kThreads;
+        const int b0 = (few ? lane : tid) * per_thread, b1 = min(a.B, b0 + per_thread);
         int64_t mine = 0;
         int most = 0;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int n = units(b);
-            mine += (int64_t)n * groups;
+            mine += (int64_t)n * a.groups;
             most = max(most, n);
         }
-        const int64_t upto = warp_scan(mine, lane);
+        int64_t before = warp_scan(mine, lane);
         most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 31) {
-            s_scan[warp] = upto;
-            s_most[warp] = most;
+        total = __shfl_sync(0xffffffffu, before, 31);
+        before -= mine;
+        if (!few) {
+            if (lane == 0) {
+                s_scan[warp] = total;
+                s_most[warp] = most;
+            }
+            __syncthreads();
+            const int64_t sum = warp_scan(lane < kWarps ? s_scan[lane] : 0, lane);
+            most = __reduce_max_sync(0xffffffffu, lane < kWarps ? s_most[lane] : 0);
+            total = __shfl_sync(0xffffffffu, sum, 31);
+            before += __shfl_sync(0xffffffffu, sum, (warp + 31) & 31) * (warp > 0);
         }
-        __syncthreads();
-        int64_t before = upto - mine;
-        total = 0;
-#pragma unroll 1
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s_scan[w];
-            total += s_scan[w];
-            most = max(most, s_most[w]);
-        }
-        if ((int64_t)a.B * groups <= gridDim.x && (int64_t)(most - S::kAlone) * gridDim.x <= total) {
+        if ((int64_t)a.B * a.groups <= gridDim.x && (int64_t)(most - S::kAlone) * gridDim.x <= total) {
             // One CTA an item: nothing to join over CTAs, and no CTA has much more to do than with equal shares.
-            const int b = blockIdx.x / groups;
+            const int b = blockIdx.x / a.groups;
             walk.b = min(b, a.B - 1);
             walk.sequence(a);
             if (b >= a.B) walk.n = 0;
             const int share = (walk.n + kWarps - 1) / kWarps;
-            walk.group = blockIdx.x - b * groups;
+            walk.group = blockIdx.x - b * a.groups;
             walk.u = min(walk.n, warp * share);
             walk.left = min(share, walk.n - walk.u);
-            from = walk.u;
+            walk.u += S::kCost;
+            walk.item = 0;
             begin = 0;
             end = walk.n;
         } else {
@@ -285,34 +308,44 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             each = max((int64_t)S::kLeast, quotient64(total + gridDim.x * kWarps - 1, gridDim.x * kWarps));
             begin = each * (blockIdx.x * kWarps);
             end = min(total, begin + each * kWarps);
-            from = begin + each * warp;
-#pragma unroll 1
-            for (int w = 0; w < kWarps; ++w) {  // whose first unit is here?
-                const int64_t first = begin + each * w;
-                if (before <= first && first < before + mine) {
-                    int b = b0;
-                    int64_t skip = first - before;
-                    if (per_thread > 1)
-#pragma unroll 1
-                        for (int64_t n; (n = (int64_t)units(b) * groups) <= skip; ++b) skip -= n;
-                    s_b[w] = b;
-                    s_first[w] = skip;
-                }
-            }
-            __syncthreads();
+            const int64_t from = begin + each * warp;
             walk.left = min(each, total - from);
-            if (walk.left > 0) {
+            int64_t skip = 0;
+            if (few) {
+                const unsigned at = __ballot_sync(0xffffffffu, before <= from && from < before + mine);
+                walk.b = at ? __ffs(at) - 1 : 0;
+                skip = from - __shfl_sync(0xffffffffu, before, walk.b);
+            } else {
+#pragma unroll 1
+                for (int w = 0; w < kWarps; ++w) {  // whose first unit is here?
+                    const int64_t first = begin + each * w;
+                    if (before <= first && first < before + mine) {
+                        int b = b0;
+                        int64_t rest = first - before;
+                        if (per_thread > 1)
+#pragma unroll 1
+                            for (int64_t n; (n = (int64_t)units(b) * a.groups) <= rest; ++b) rest -= n;
+                        s_b[w] = b;
+                        s_first[w] = rest;
+                    }
+                }
+                __syncthreads();
                 walk.b = s_b[warp];
+                skip = s_first[warp];
+            }
+            if (walk.left > 0) {
                 walk.sequence(a);
-                walk.group = (int)quotient64(s_first[warp], walk.n);
-                walk.u = (int)(s_first[warp] - (int64_t)walk.group * walk.n);
+                walk.group = (int)quotient64(skip, walk.n + S::kCost);
+                walk.u = (int)(skip - (int64_t)walk.group * (walk.n + S::kCost));
+                walk.item = from - walk.u + S::kCost;
+                walk.begin();
             }
         }
     }
 
     // ---- the stream of this warp's units
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
-    Walk<TOK> ahead = walk;
+    Walk<TOK, S::kCost> ahead = walk;
     Segment ask{};                 // segment whose units are asked for
     int ask_u = 0, ask_last = 0;   // unit that is next, last page of the sequence
     bool asking = true, live = false;  // there are units left; the one that is being asked for is one
@@ -321,7 +354,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     uint32_t fill = 0;             // place in the ring that is filled next
     // the page table's entries from table_at on: this lane's of the first 32 and of the next 32
     int table_at = 0, entry = 0, entry_next = 0;
-    const uint64_t policy = groups == a.kv ? l2_evict_first_policy() : l2_evict_normal_policy();
+    const uint64_t policy = a.per_head == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
     auto page_of = [&](int64_t token) { return (int)((uint64_t)token * a.page_mul >> (31 + a.page_shift)); };
     auto table_entry = [&](int index) {  // -1 behind the sequence's last
         return index <= ask_last ? a.table[ask.b * a.table_stride + index] : -1;
@@ -331,7 +364,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         asking = ahead.left > 0;
         if (!asking) return;
         Segment s;
-        ahead.next(a, groups, rows_of_group, &s);
+        ahead.next(a, &s);
         ask = s;
         ask_u = ask.u0;
         ask_last = page_of(ask.len - 1);
@@ -408,7 +441,6 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     };
 
     // ---- segments
-    int64_t position = from;
     uint32_t take = 0;   // place in the ring that is used next
     unsigned taken = 0;  // units used
     bool more = walk.left > 0;
@@ -424,7 +456,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
 #pragma unroll 1
     while (more) {
         Segment next;
-        walk.next(a, groups, rows_of_group, &next);
+        walk.next(a, &next);
         const Segment seg = next;
         more = walk.left > 0;
         // Query heads 8 i + g.  Columns of a step: 2 t4 (+1) and 2 t4 + 8 (+1); with bytes 4 t4 .. 4 t4 + 3, the order that
@@ -628,13 +660,12 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         }
 
         // ---- the item, or this warp's part of it
-        const int64_t item = position - seg.u0;
-        position += seg.u1 - seg.u0;
         const bool whole = seg.u0 == 0 && seg.u1 == seg.n;
         const int which = 2 * warp + (more && !whole ? 0 : 1);
         __syncwarp();  // all lanes have read the ring
         // (when the last sums are written the stream has ended, and the ring is free)
         float* const to = more ? place_of(warp, whole ? 1 : 0) : reinterpret_cast<float*>(smem + warp * S::kRing);
+        const int pitch = more ? D : S::kPitch;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -647,7 +678,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
                     s_m[which][row] = m[n][h];
                     s_l[which][row] = sum;
                 }
-                float* const line = to + row * S::kPitch + (EIGHT ? 2 * g : g);
+                float* const line = to + row * pitch + (EIGHT ? 2 * g : g);
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i)
                     if (EIGHT) {
@@ -663,12 +694,12 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
 #pragma unroll 1
             for (int i = lane; i < seg.rows * (D / 4); i += 32) {
                 const int row = i / (D / 4), d = i % (D / 4) * 4;
-                finish_row(a, seg.row + row, d, D, *reinterpret_cast<const float4*>(to + row * S::kPitch + d), s_l[which][row], vs,
+                finish_row(a, seg.row + row, d, D, *reinterpret_cast<const float4*>(to + row * pitch + d), s_l[which][row], vs,
                            s_m[which][row] - kOffset);
             }
             __syncwarp();  // before the next sums
         } else if (lane == 0) {
-            s_part[which] = Part{item, seg.n, seg.kv_head, seg.row, seg.rows};
+            s_part[which] = Part{seg.item, seg.n, seg.kv_head, seg.row, seg.rows};
         }
     }
     pdl_trigger();
@@ -683,8 +714,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     const unsigned start_mask = __ballot_sync(0xffffffffu, starts);
     const int runs = __popc(start_mask);
     if (runs == 0) return;
-    if (warp == 0 && starts) s_run[__popc(start_mask & ((1u << lane) - 1))] = lane;
-    if (tid == 0) s_run[runs] = 2 * kWarps;
+    if (warp == 0 && starts) s_run[__popc(below & start_mask)] = lane;
 
     auto finish = [&](const Part& p, int row, int d, float4 sum, float top, float weight) {
         finish_row(a, p.row + row, d, D, sum, weight, EIGHT ? a.v.scale[p.kv_head] : 1.0f, top - kOffset);
@@ -692,128 +722,167 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     // a CTA's part of an item: one for an item that began in a range before, one for an item that begins in this one
     auto part_of = [&](int cta, bool begins) { return a.part + ((int64_t)cta * 2 + (begins ? 1 : 0)) * S::kPart; };
 
-    // what each part counts, and the runs' maxima and weights
-    if (tid < 2 * kWarps * kRows && (there >> (tid / kRows) & 1)) {
-        const int j = tid / kRows, row = tid % kRows;
-        const int first = 31 - __clz(start_mask & ((2u << j) - 1));  // the run of part j begins here
-        const unsigned behind = start_mask & ~((2u << first) - 1);
-        const unsigned of_run = there & ~((1u << first) - 1) & (behind ? (1u << (__ffs(behind) - 1)) - 1 : ~0u);
-        float top = -INFINITY, weight = 0.0f;
+    // what each part counts, and the runs' maxima and weights: a lane a part, a warp a row
+    {
+        const int first = start_mask & ((2u << lane) - 1) ? 31 - __clz(start_mask & ((2u << lane) - 1)) : 0;  // of this lane's run
+        const unsigned behind = start_mask & ~((2u << lane) - 1);
+        const int last = behind ? __ffs(behind) - 2 : 31;
 #pragma unroll 1
-        for (unsigned i = of_run; i; i &= i - 1) top = fmaxf(top, s_m[__ffs(i) - 1][row]);
-#pragma unroll 1
-        for (unsigned i = of_run; i; i &= i - 1) weight += share_of(s_m[__ffs(i) - 1][row], top) * s_l[__ffs(i) - 1][row];
-        s_share[j][row] = share_of(s_m[j][row], top);
-        s_top[j][row] = top;
-        s_weight[j][row] = weight;
+        for (int row = warp; row < kRows; row += kWarps) {
+            const float m = there >> lane & 1 ? s_m[lane][row] : -INFINITY;
+            float top = m;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {  // to the run's end, then back to its beginning
+                const float v = __shfl_down_sync(0xffffffffu, top, x);
+                if (lane + x <= last) top = fmaxf(top, v);
+            }
+            top = __shfl_sync(0xffffffffu, top, first);
+            const float share = share_of(m, top);
+            float weight = there >> lane & 1 ? share * s_l[lane][row] : 0.0f;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const float v = __shfl_down_sync(0xffffffffu, weight, x);
+                if (lane + x <= last) weight += v;
+            }
+            if (lane < 2 * kWarps) {
+                s_share[lane][row] = share;
+                s_top[lane][row] = top;
+                s_weight[lane][row] = weight;  // (of the run, where it begins)
+            }
+        }
     }
     __syncthreads();
 #pragma unroll 1
     for (int i = tid; i < runs * kRows * (D / 4); i += kThreads) {
-        const int run = i / (kRows * (D / 4)), row = i / (D / 4) % kRows, d = i % (D / 4) * 4;
-        const int j0 = s_run[run], j1 = s_run[run + 1];
+        const int row = i / (D / 4) % kRows, d = i % (D / 4) * 4, j0 = s_run[i / (kRows * (D / 4))];
         const Part p = s_part[j0];
-        if (row >= p.rows) continue;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-        for (int j = j0; j < j1; ++j)
-            if (there >> j & 1) {
-                const float* from_part = j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * S::kRing) : place_of(j >> 1, 0);
-                add(sum, s_share[j][row], *reinterpret_cast<const float4*>(from_part + row * S::kPitch + d));
-            }
-        if (p.item >= begin && p.item + p.n <= end) {
-            finish(p, row, d, sum, s_top[j0][row], s_weight[j0][row]);
-        } else {
-            float* to = part_of(blockIdx.x, p.item >= begin);
-            *reinterpret_cast<float4*>(to + row * S::kPitch + d) = sum;
-            if (d == 0) {
-                to[S::kSums + row] = s_top[j0][row];
-                to[S::kSums + kRows + row] = s_weight[j0][row];
-            }
+        const bool inside = p.item >= begin && p.item + p.n <= end;
+        if (!inside && d == 0) {  // (of all rows, for whole sectors)
+            float* to = part_of(blockIdx.x, p.item >= begin) + S::kSums + row;
+            to[0] = s_top[j0][row];
+            to[kRows] = s_weight[j0][row];
         }
+        if (row >= p.rows) continue;
+        const unsigned behind = start_mask & ~((2u << j0) - 1);
+        const unsigned of_run = there & ~((1u << j0) - 1) & (behind ? (1u << (__ffs(behind) - 1)) - 1 : ~0u);
+        // what warps in a row ended with, in their rings, and then perhaps what the next warp began with
+        const unsigned ended = of_run & 0xaaaaaaaau, began = of_run & 0x55555555u;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int w0 = ended ? (__ffs(ended) - 1) >> 1 : 0, w1 = w0 + __popc(ended);
+        const uint8_t* at = smem + w0 * S::kRing + (row * S::kPitch + d) * 4;
+#pragma unroll 4
+        for (int w = w0; w < w1; ++w, at += S::kRing) add(sum, s_share[2 * w + 1][row], *reinterpret_cast<const float4*>(at));
+        if (began) {
+            const int j = __ffs(began) - 1;
+            add(sum, s_share[j][row], *reinterpret_cast<const float4*>(place_of(j >> 1, 0) + row * D + d));
+        }
+        if (inside) finish(p, row, d, sum, s_top[j0][row], s_weight[j0][row]);
+        else *reinterpret_cast<float4*>(part_of(blockIdx.x, p.item >= begin) + row * D + d) = sum;
     }
 
-    // ---- what CTAs share: sixteen parts at a time, then the sixteens
+    // ---- what CTAs share: the last of them to arrive adds up their parts; of many parts the last of each few, and the last
+    // of those.  (One SM reads some 60 GB/s: 76 parts of 4 KB take it 5 us, nine and nine of their sums 1.2.)  A CTA may
+    // share its first item with the CTAs before it, and its last with those behind it.
     auto owner = [&](int64_t unit) { return (int)quotient64(unit, each * kWarps); };
+    if (tid < 2) {
+        const Part p = s_part[s_run[tid == 0 ? 0 : runs - 1]];
+        Join j{0, 0, 0, 0, 0, 0};
+        if ((tid == 0 || runs > 1) && !(p.item >= begin && p.item + p.n <= end)) {
+            j.first = owner(p.item);
+            j.parts = owner(p.item + p.n - 1) - j.first + 1;
+            j.fan = j.parts;
+            if (j.parts > kFew)
+                for (j.fan = 5; j.fan * j.fan < j.parts;) ++j.fan;
+            j.step = 1;
+        }
+        s_join[tid] = j;
+    }
 #pragma unroll 1
-    for (int run = 0; run < runs; run += max(1, runs - 1)) {  // the first and the last
-        const Part p = s_part[s_run[run]];
-        if (p.item >= begin && p.item + p.n <= end) continue;
-        const int first = owner(p.item), last = owner(p.item + p.n - 1);
-        const int fans = (last - first + kFan) / kFan;
-#pragma unroll 1
-        for (int level = 0; level < 2; ++level) {
-            const int fan = ((int)blockIdx.x - first) / kFan;
-            const int leader = level == 0 ? first + fan * kFan : first, step = level == 0 ? 1 : kFan;
-            const int count = level == 0 ? min(kFan, last - leader + 1) : fans;
-            // this level's counter, of the leader's part
-            unsigned* counter = a.count + (leader * 2 + (leader == first ? 1 : 0)) * 2 + level;
-            __syncthreads();
-            if (tid == 0) {
+    for (int level = 0; level < 2; ++level) {
+        __syncthreads();
+        if (tid < 2) {
+            Join& j = s_join[tid];
+            j.count = 0;
+            if (j.step > 0) {
+                const int reach = j.step * j.fan;
+                j.leader = j.first + ((int)blockIdx.x - j.first) / reach * reach;
+                const int count = min(j.fan, (j.first + j.parts - 1 - j.leader) / j.step + 1);
+                // this level's counter, of the leader's part
+                unsigned* counter = a.count + (j.leader * 2 + (j.leader == j.first ? 1 : 0)) * 2 + level;
                 __threadfence();
-                const unsigned before = atomicAdd(counter, 1);
-                s_last = before == (unsigned)count - 1;
-                if (s_last) {
+                if (atomicAdd(counter, 1) == (unsigned)count - 1) {
                     *counter = 0;
-                    __threadfence();
+                    j.count = count;
                 }
-            }
-            __syncthreads();
-            if (!s_last) break;
-            float* const head_part = part_of(leader, leader == first);
-            float* const next_parts = part_of(leader, false);  // of the leader's followers: so much further on
-            const int64_t apart = (int64_t)step * 2 * S::kPart;
-            const bool end_here = level == 1 || fans == 1;
-            const int j = tid / kRows, row = tid % kRows;
-            if (j < kFan) {
-                const float* from_part = j > 0 && j < count ? next_parts + j * apart : head_part;
-                s_m[j][row] = j < count ? __ldcg(from_part + S::kSums + row) : -INFINITY;
-                s_l[j][row] = j < count ? __ldcg(from_part + S::kSums + kRows + row) : 0.0f;
-            }
-            __syncthreads();
-            if (j < kFan) {
-                float top = -INFINITY, weight = 0.0f;
-#pragma unroll 4
-                for (int i = 0; i < kFan; ++i) top = fmaxf(top, s_m[i][row]);
-#pragma unroll 4
-                for (int i = 0; i < kFan; ++i) weight += share_of(s_m[i][row], top) * s_l[i][row];
-                s_share[j][row] = j < count ? share_of(s_m[j][row], top) : 0.0f;
-                if (j == 0) {
-                    s_top[0][row] = top;
-                    s_weight[0][row] = weight;
-                }
-            }
-            __syncthreads();
-#pragma unroll 1
-            for (int i = tid; i < p.rows * (D / 4); i += kThreads) {
-                const int r = i / (D / 4), d = i % (D / 4) * 4;
-                float4 v[kFan], sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                const float* at = next_parts + r * S::kPitch + d;
-                v[0] = __ldcg(reinterpret_cast<const float4*>(head_part + r * S::kPitch + d));
-#pragma unroll
-                for (int k = 1; k < kFan; ++k) {
-                    at += apart;
-                    if (k < count) v[k] = __ldcg(reinterpret_cast<const float4*>(at));
-                }
-#pragma unroll
-                for (int k = 0; k < kFan; ++k)
-                    if (k < count) add(sum, s_share[k][r], v[k]);
-                if (end_here)
-                    finish(p, r, d, sum, s_top[0][r], s_weight[0][r]);
-                else
-                    *reinterpret_cast<float4*>(head_part + r * S::kPitch + d) = sum;  // (no other thread reads these)
-            }
-            if (end_here) break;
-            if (tid < p.rows) {  // (all have read the maxima and sums)
-                head_part[S::kSums + tid] = s_top[0][tid];
-                head_part[S::kSums + kRows + tid] = s_weight[0][tid];
+                __threadfence();
             }
         }
+        __syncthreads();
+        if (s_join[0].count == 0 && s_join[1].count == 0) return;
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const Join join = s_join[which];
+            if (join.count == 0) continue;
+            const Part p = s_part[s_run[which == 0 ? 0 : runs - 1]];
+            const bool end_here = join.step * join.fan >= join.parts;
+            // parts come to shared memory, as many at a time as it holds
+            constexpr int kAtOnce = S::kSmem / (S::kPart * 4), kPieces = S::kPart / 4;
+            float* const head = part_of(join.leader, join.leader == join.first);
+#pragma unroll 1
+            for (int e0 = 0; e0 < p.rows * (D / 4); e0 += kThreads) {
+                const int e = e0 + tid, row = min(e / (D / 4), kRows - 1), d = e % (D / 4) * 4;
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float top = -INFINITY, weight = 0.0f;
+#pragma unroll 1
+                for (int k = 0; k < join.count; k += kAtOnce) {
+                    const int count = min(kAtOnce, join.count - k);
+                    __syncthreads();  // the parts before have been read
+#pragma unroll 4
+                    for (int i = tid; i < count * kPieces; i += kThreads) {
+                        const int j = k + i / kPieces;
+                        copy16(smem_addr(smem) + i * 16, (j == 0 ? head : part_of(join.leader + j * join.step, false)) + i % kPieces * 4, policy);
+                    }
+                    copy_commit();
+                    copy_wait<0>();
+                    __syncthreads();
+                    const float* const parts = reinterpret_cast<const float*>(smem);
+                    float next = top;
+#pragma unroll 8
+                    for (int j = 0; j < count; ++j) next = fmaxf(next, parts[j * S::kPart + S::kSums + row]);
+                    const float keep = share_of(top, next);
+                    top = next;
+                    weight *= keep;
+                    sum = make_float4(sum.x * keep, sum.y * keep, sum.z * keep, sum.w * keep);
+#pragma unroll 4
+                    for (int j = 0; j < count; ++j) {
+                        const float f = share_of(parts[j * S::kPart + S::kSums + row], top);
+                        weight += f * parts[j * S::kPart + S::kSums + kRows + row];
+                        add(sum, f, *reinterpret_cast<const float4*>(parts + j * S::kPart + row * D + d));
+                    }
+                }
+                if (e >= p.rows * (D / 4)) continue;
+                if (end_here) {
+                    finish(p, row, d, sum, top, weight);
+                } else {
+                    *reinterpret_cast<float4*>(head + row * D + d) = sum;
+                    // (the maxima and weights, still read for the columns of a next turn, are left for the end)
+                    if (d == 0) s_top[0][row] = top, s_weight[0][row] = weight;
+                }
+            }
+            __syncthreads();
+            if (!end_here && tid < kRows) {  // (of all rows, for whole sectors)
+                head[S::kSums + tid] = s_top[0][tid];
+                head[S::kSums + kRows + tid] = s_weight[0][tid];
+            }
+            if (tid == 0) s_join[which].step = end_here ? 0 : join.step * join.fan;
+        }
+        // (those that did not arrive last have left this item to others)
+        if (tid < 2 && s_join[tid].count == 0) s_join[tid].step = 0;
     }
 }
 
 template <int D, bool EIGHT, int NT>
-cudaError_t launch(const DecodeArgs& a, int per, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t launch(const DecodeArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
     using S = Shape<D, EIGHT, NT>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -825,16 +894,14 @@ cudaError_t launch(const DecodeArgs& a, int per, int num_sms, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, EIGHT, NT>, a, per * a.kv, (a.heads / a.kv + per - 1) / per);
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, EIGHT, NT>, a);
 }
 
 template <int D>
 cudaError_t launch_dim(const DecodeArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
-    // groups of up to sixteen query heads of a key-value head, of equal size as far as that goes
-    const int shared = a.heads / a.kv, per = (shared + 15) / 16;
-    const bool eight = a.k.scale != nullptr, wide = (shared + per - 1) / per > 8;
-    if (eight) return wide ? launch<D, true, 2>(a, per, num_sms, stream, pdl) : launch<D, true, 1>(a, per, num_sms, stream, pdl);
-    return wide ? launch<D, false, 2>(a, per, num_sms, stream, pdl) : launch<D, false, 1>(a, per, num_sms, stream, pdl);
+    const bool wide = a.rows_of_group > 8;
+    if (a.k.scale != nullptr) return wide ? launch<D, true, 2>(a, num_sms, stream, pdl) : launch<D, true, 1>(a, num_sms, stream, pdl);
+    return wide ? launch<D, false, 2>(a, num_sms, stream, pdl) : launch<D, false, 1>(a, num_sms, stream, pdl);
 }
 
 template <int D, bool EIGHT, int NT>
@@ -851,7 +918,13 @@ cudaError_t set_smem_dim() {
 
 }  // namespace
 
-cudaError_t launch_attn_decode(const DecodeArgs& a, int head_dim, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t launch_attn_decode(const DecodeArgs& args, int head_dim, int num_sms, cudaStream_t stream, bool pdl) {
+    // groups of up to sixteen query heads of a key-value head, of equal size as far as that goes
+    DecodeArgs a = args;
+    a.shared = a.heads / a.kv;
+    a.per_head = (a.shared + 15) / 16;
+    a.groups = a.kv * a.per_head;
+    a.rows_of_group = (a.shared + a.per_head - 1) / a.per_head;
     switch (head_dim) {
         case 64: return launch_dim<64>(a, num_sms, stream, pdl);
         case 128: return launch_dim<128>(a, num_sms, stream, pdl);
@@ -869,8 +942,7 @@ cudaError_t attn_decode_set_attributes() {
 size_t attn_decode_counters(int num_sms) { return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * 4; }
 size_t attn_decode_parts(int num_sms, int head_dim) {
     // two parts a CTA of up to sixteen rows, two places of sums a warp (sixteen of eight rows, or eight of sixteen)
-    const size_t row = (size_t)head_dim + 4;
-    return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * (2 * (16 * row + 32) + 2 * 16 * 8 * row);
+    return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * (2 * (16 * head_dim + 32) + 2 * 16 * 8 * head_dim);
 }
 
 }  // namespace arf
