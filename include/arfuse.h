@@ -247,7 +247,9 @@ ARFUSE_API ar_status ar_rmsnorm(ar_workspace* ws, const void* const* partials, i
  * neither an input nor each other.  With AR_WS_NORM_BF16_H the norm reads h rounded
  * to bf16.  A row that holds an infinity or a NaN gets NaN scales wherever y has one
  * (NaN codes with them).  A scale is at least 2^-126: smaller values of y are subnormal
- * multiples of it.  Its regime controls have no effect here.
+ * multiples of it.  The regime controls have no effect here, nor AR_WS_PDL: the launch
+ * may always begin under the end of the kernel before it (it reads and writes nothing
+ * before that has completed).
  */
 ARFUSE_API ar_status ar_rmsnorm_q8(ar_workspace* ws, const void* const* partials, int R,
                                    const void* residual, const void* gamma, float weight_bias,
@@ -739,7 +741,9 @@ typedef struct ar_kv_cache {
  *   head_dim   64, 128 or 256
  *   page_size  tokens of a page, 1 .. AR_MAX_PAGE_SIZE, any number
  *   max_seqs   most sequences of an ar_attn_decode call, 1 .. AR_MAX_ATTN_SEQS
- *   flags      0, or any of AR_WS_DRY_RUN, AR_WS_PDL (as for a workspace)
+ *   flags      0, or any of AR_WS_DRY_RUN, AR_WS_PDL (taken, and without effect: the
+ *              launches may always begin under the end of the kernel before them on
+ *              the stream; they read and write nothing before it has completed)
  *   out        receives the handle (NULL on error)
  * Errors: AR_ERR_INVALID_ARG (out NULL, counts below 1, kv_heads no divisor,
  * unknown flags), AR_ERR_UNSUPPORTED (head_dim, limits above, or a device older

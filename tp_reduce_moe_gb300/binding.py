@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 import weakref
@@ -374,6 +375,12 @@ def _ptr_array(ts):
     return (ctypes.c_void_p * len(ts))(*[t if isinstance(t, int) else t.data_ptr() for t in ts])
 
 
+@functools.lru_cache(maxsize=None)
+def _pointers(n: int):
+    """The type of an array of n pointers."""
+    return ctypes.c_void_p * n
+
+
 def _stream_handle(stream, device) -> int:
     if stream is None:
         index = device if isinstance(device, int) else getattr(device, "index", None)
@@ -491,33 +498,42 @@ def ar_rmsnorm_q8(ws: Workspace, partials, residual, gamma, weight_bias: float, 
     as well.  ``residual_out`` may be ``residual`` (in place, bf16 only).  Returns (q,
     scales, residual_out), allocated when not given."""
     R, H, T = ws.R, ws.H, residual.shape[0]
-    dev = None if ws.dry_run else ws.device
+    # (a dry run only looks at addresses: any device, one for all)
+    dev, bf16, rows = residual.get_device() if ws.dry_run else ws.device, torch.bfloat16, (T, H)
     if len(partials) != R:
         raise ValueError(f"partials has {len(partials)} entries, workspace has R={R}")
     if group not in (0, 32, 64, 128):
         raise ArfuseError(AR_ERR_UNSUPPORTED, f"group {group} (0, 32, 64 or 128)")
+    # (checked here and not by a function: a call for each tensor costs more than the rest of a small call)
     for r, p in enumerate(partials):
-        _need_on(dev, p, torch.bfloat16, (T, H), "partials", r)
-    _need_on(dev, residual, torch.bfloat16, (T, H), "residual")
-    _need_on(dev, gamma, torch.bfloat16, (H,), "gamma")
-    res_type = torch.float32 if residual_out_fp32 else torch.bfloat16
+        if p.dtype is not bf16 or p.shape != rows or not p.is_contiguous() or p.get_device() != dev:
+            _need_on(dev, p, bf16, rows, "partials", r)
+    if residual.dtype is not bf16 or residual.shape != rows or not residual.is_contiguous() or residual.get_device() != dev:
+        _need_on(dev, residual, bf16, rows, "residual")
+    if gamma.dtype is not bf16 or gamma.shape != (H,) or not gamma.is_contiguous() or gamma.get_device() != dev:
+        _need_on(dev, gamma, bf16, (H,), "gamma")
+    res_type = torch.float32 if residual_out_fp32 else bf16
     shape = (T, -(-H // group) if group else 1)
     if q is None:
-        q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=residual.device)
+        q = torch.empty(rows, dtype=torch.float8_e4m3fn, device=residual.device)
+    elif q.dtype is not torch.float8_e4m3fn or q.shape != rows or not q.is_contiguous() or q.get_device() != dev:
+        _need_on(dev, q, torch.float8_e4m3fn, rows, "q")
     if scales is None:
         scales = torch.empty(shape, dtype=torch.float32, device=residual.device)
+    elif scales.dtype is not torch.float32 or scales.shape != shape or not scales.is_contiguous() or scales.get_device() != dev:
+        _need_on(dev, scales, torch.float32, shape, "scales")
     if residual_out is None:
-        residual_out = torch.empty((T, H), dtype=res_type, device=residual.device)
-    _need_on(dev, q, torch.float8_e4m3fn, (T, H), "q")
-    _need_on(dev, scales, torch.float32, shape, "scales")
-    _need_on(dev, residual_out, res_type, (T, H), "residual_out")
+        residual_out = torch.empty(rows, dtype=res_type, device=residual.device)
+    elif residual_out.dtype is not res_type or residual_out.shape != rows or not residual_out.is_contiguous() or (
+            residual_out.get_device() != dev):
+        _need_on(dev, residual_out, res_type, rows, "residual_out")
     if out is not None:
-        _need_on(dev, out, torch.bfloat16, (T, H), "out")
-    p_arr = _ptr_array(partials)
-    st = load_library().ar_rmsnorm_q8(
-        ws.handle if ws.alive else None, ctypes.addressof(p_arr), R, residual.data_ptr(), gamma.data_ptr(), float(weight_bias), float(eps), T, H,
-        int(group), q.data_ptr(), scales.data_ptr(), _ptr(out), residual_out.data_ptr(), 1 if residual_out_fp32 else 0,
-        None if ws.dry_run else _stream_handle(stream, ws.device))
+        _need_on(dev, out, bf16, rows, "out")
+    p_arr = _pointers(R)(*[p.data_ptr() for p in partials])
+    st = (_lib or load_library()).ar_rmsnorm_q8(
+        ws.handle if ws.alive else None, p_arr, R, residual.data_ptr(), gamma.data_ptr(), weight_bias, eps, T, H, group,
+        q.data_ptr(), scales.data_ptr(), None if out is None else out.data_ptr(), residual_out.data_ptr(),
+        1 if residual_out_fp32 else 0, None if ws.dry_run else _stream_handle(stream, dev))
     if st != AR_OK:
         _check(st, "ar_rmsnorm_q8", ok=(AR_VALIDATED,) if ws.dry_run else ())
     return q, scales, residual_out
@@ -755,6 +771,8 @@ class Attn:
         self.heads, self.kv_heads, self.head_dim, self.page_size = heads, kv_heads, head_dim, page_size
         self.max_seqs, self.device, self.dry_run = max_seqs, device, dry_run
         self.axes = 0
+        self.cache_shape = (page_size, kv_heads, head_dim)
+        self.qkv_cols = (heads + 2 * kv_heads) * head_dim
         self._fin = weakref.finalize(self, _destroy_attn_handle, handle)
 
     def destroy(self):
@@ -867,7 +885,7 @@ def _need_cache(attn, cache, dev):
     if (size, kv, dim) != (attn.page_size, attn.kv_heads, attn.head_dim):
         raise ValueError(f"cache: pages of {size} tokens, {kv} heads of {dim}, expected {attn.page_size}, {attn.kv_heads}, "
                          f"{attn.head_dim}")
-    if dev is not None and cache.device != dev:
+    if cache.device != dev:
         raise ValueError(f"cache: on {cache.k.device}, expected cuda:{dev}")
 
 
@@ -878,22 +896,29 @@ def ar_attn_append(attn: Attn, cache: KvCache, qkv, positions, slots, q=None, st
     (or [T] with one axis; ignored, and may be None, without rotary positions); slots: int32 [T], page * page_size +
     token in the page, -1: not written; of tokens with one slot the last stands.  Returns q (bf16 [T, heads, head_dim]),
     allocated when not given."""
-    T, dev = qkv.shape[0], _moe_device(attn)
-    _need_cache(attn, cache, dev)
-    _need_on(dev, qkv, torch.bfloat16, (T, (attn.heads + 2 * attn.kv_heads) * attn.head_dim), "qkv")
+    T, dev = qkv.shape[0], qkv.get_device() if attn.dry_run else attn.device
+    if cache.shape[1:] != attn.cache_shape or cache.device != dev:
+        _need_cache(attn, cache, dev)
+    if qkv.dtype is not torch.bfloat16 or qkv.shape != (T, attn.qkv_cols) or not qkv.is_contiguous() or qkv.get_device() != dev:
+        _need_on(dev, qkv, torch.bfloat16, (T, attn.qkv_cols), "qkv")
     if attn.axes:
         if positions is None:
             raise ValueError("positions: rotary positions are set")
-        _need_on(dev, positions, torch.int32, (T,) if attn.axes == 1 and positions.dim() == 1 else (attn.axes, T), "positions")
+        if positions.dtype is not torch.int32 or positions.shape != (attn.axes, T) or not positions.is_contiguous() or (
+                positions.get_device() != dev):
+            _need_on(dev, positions, torch.int32, (T,) if attn.axes == 1 and positions.dim() == 1 else (attn.axes, T), "positions")
     else:
         positions = None
-    _need_on(dev, slots, torch.int32, (T,), "slots")
+    if slots.dtype is not torch.int32 or slots.shape != (T,) or not slots.is_contiguous() or slots.get_device() != dev:
+        _need_on(dev, slots, torch.int32, (T,), "slots")
     shape = (T, attn.heads, attn.head_dim)
     if q is None:
         q = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
-    _need_on(dev, q, torch.bfloat16, shape, "q")
-    st = load_library().ar_attn_append(attn.handle, cache._ref, qkv.data_ptr(), _ptr(positions), slots.data_ptr(), T,
-                                       q.data_ptr(), _moe_stream(attn, stream))
+    elif q.dtype is not torch.bfloat16 or q.shape != shape or not q.is_contiguous() or q.get_device() != dev:
+        _need_on(dev, q, torch.bfloat16, shape, "q")
+    st = (_lib or load_library()).ar_attn_append(
+        attn.handle, cache._ref, qkv.data_ptr(), None if positions is None else positions.data_ptr(), slots.data_ptr(), T,
+        q.data_ptr(), None if attn.dry_run else _stream_handle(stream, dev))
     if st != AR_OK:
         _check(st, "ar_attn_append", ok=(AR_VALIDATED,) if attn.dry_run else ())
     return q
@@ -907,27 +932,33 @@ def ar_attn_decode(attn: Attn, cache: KvCache, q, page_table, lengths, scale: fl
     q: bf16 [B, heads, head_dim]; page_table: int32 [B, width], the page of a sequence's tokens i * page_size and on
     (rows may be further apart); lengths: int32 [B], 0: zeros.  Returns out (bf16 [B, heads, head_dim], allocated when not
     given), or (out, lse) when ``lse`` (fp32 [B, heads]: log of the sum of the scores' exponentials) is given."""
-    B, dev = q.shape[0], _moe_device(attn)
-    _need_cache(attn, cache, dev)
+    B, dev = q.shape[0], q.get_device() if attn.dry_run else attn.device
+    if cache.shape[1:] != attn.cache_shape or cache.device != dev:
+        _need_cache(attn, cache, dev)
     shape = (B, attn.heads, attn.head_dim)
-    _need_on(dev, q, torch.bfloat16, shape, "q")
+    if q.dtype is not torch.bfloat16 or q.shape != shape or not q.is_contiguous() or q.get_device() != dev:
+        _need_on(dev, q, torch.bfloat16, shape, "q")
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected ({B}, width)")
-    width = page_table.shape[1]
-    apart = page_table.stride(0) if B > 1 else width
+    width, apart = page_table.shape[1], page_table.stride(0)
+    if B <= 1 or width == 0:
+        apart = width
     if page_table.dtype is not torch.int32 or apart < width or (width > 1 and page_table.stride(1) != 1) or (
-            dev is not None and page_table.get_device() != dev):
+            page_table.get_device() != dev):
         _need_on(dev, page_table, torch.int32, (B, width), "page_table")
-    _need_on(dev, lengths, torch.int32, (B,), "lengths")
+    if lengths.dtype is not torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous() or lengths.get_device() != dev:
+        _need_on(dev, lengths, torch.int32, (B,), "lengths")
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    _need_on(dev, out, torch.bfloat16, shape, "out")
-    if lse is not None:
+    elif out.dtype is not torch.bfloat16 or out.shape != shape or not out.is_contiguous() or out.get_device() != dev:
+        _need_on(dev, out, torch.bfloat16, shape, "out")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, attn.heads) or not lse.is_contiguous() or
+                            lse.get_device() != dev):
         _need_on(dev, lse, torch.float32, (B, attn.heads), "lse")
-    st = load_library().ar_attn_decode(
-        attn.handle, cache._ref, q.data_ptr(), page_table.data_ptr() if width else None, width, apart,
-        lengths.data_ptr(), B, int(window), attn.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(), _ptr(lse),
-        _moe_stream(attn, stream))
+    st = (_lib or load_library()).ar_attn_decode(
+        attn.handle, cache._ref, q.data_ptr(), page_table.data_ptr() if width else None, width, apart, lengths.data_ptr(), B,
+        window, attn.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if attn.dry_run else _stream_handle(stream, dev))
     if st != AR_OK:
         _check(st, "ar_attn_decode", ok=(AR_VALIDATED,) if attn.dry_run else ())
     return out if lse is None else (out, lse)

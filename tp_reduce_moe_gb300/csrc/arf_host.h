@@ -36,7 +36,8 @@ bool oneshot_prefer_64(const ClusterPlan& p, int64_t T, int num_sms, int blocks8
 cudaError_t launch_mhc_post(const MhcArgs& a, cudaStream_t stream, bool pdl = false);
 
 // The norm with an 8-bit output (norm_q8.cu); group 0: one scale a row.
-cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, cudaStream_t stream, bool pdl);
+cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num_sms, cudaStream_t stream);
+cudaError_t norm_q8_set_attributes();
 
 struct StreamPlan {
     StreamGeom geo;

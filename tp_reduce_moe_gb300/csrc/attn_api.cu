@@ -270,7 +270,7 @@ ar_status ar_attn_append(ar_attn* m, const ar_kv_cache* cache, const void* qkv, 
     a.page_size = m->page_size;
     a.rot = m->rot;
     a.interleaved = m->interleaved;
-    return launched(arf::launch_attn_append(a, m->num_sms, static_cast<cudaStream_t>(stream), (m->flags & AR_WS_PDL) != 0));
+    return launched(arf::launch_attn_append(a, m->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 ar_status ar_attn_decode(ar_attn* m, const ar_kv_cache* cache, const void* q, const int32_t* page_table, int64_t table_width,
@@ -327,7 +327,7 @@ ar_status ar_attn_decode(ar_attn* m, const ar_kv_cache* cache, const void* q, co
     a.page_mul = (unsigned)((((uint64_t)1 << (31 + a.page_shift)) + m->page_size - 1) / m->page_size);
     a.window = (int)(window < kMostTokens ? window : 0);
     a.scale = scale * kLog2e;
-    return launched(arf::launch_attn_decode(a, m->D, m->num_sms, static_cast<cudaStream_t>(stream), (m->flags & AR_WS_PDL) != 0));
+    return launched(arf::launch_attn_decode(a, m->D, m->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

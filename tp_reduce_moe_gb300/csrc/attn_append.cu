@@ -21,17 +21,16 @@ constexpr int kThreads = 256;
 constexpr int kMaxTokens = 64;  // of a CTA
 constexpr int kTableTokens = 4; // whose angles are in shared memory at a time
 constexpr int kHashBits = 14;
+constexpr int kAhead = 4;       // pieces that a thread has asked for
 
-struct Piece {
-    uint4 lo, hi;
-};
-
-__device__ __forceinline__ uint4 ld_once16(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// Sixteen bytes of what the kernel before may have written, to a place that only this thread reads.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Chunks (of eight columns) of piece p of a head: its own two, or both halves of eight pairs.
@@ -60,6 +59,7 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
     __shared__ int64_t s_k[kMaxTokens], s_v[kMaxTokens];  // byte offsets of the tokens' places, -1: none
     __shared__ unsigned s_hash[1 << (kHashBits - 5)];
     __shared__ float2 s_turn[kTableTokens][kMaxHeadDim / 2];
+    __shared__ uint4 s_piece[kAhead][2][kThreads];
     pdl_trigger();
     pdl_wait();  // no global memory access before this point
     const int t0 = blockIdx.x * tokens_per_cta, count = min(tokens_per_cta, a.T - t0);
@@ -69,16 +69,23 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
     const int first = (int)((int64_t)pieces * blockIdx.y / gridDim.y);
     const int own = (int)((int64_t)pieces * (blockIdx.y + 1) / gridDim.y) - first;
 
-    auto load = [&](int i) {
-        const int t = i / own, r = first + (i - t * own), head = r / per_head;
-        int lo, hi;
-        chunks_of(r - head * per_head, head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
-        const uint16_t* row = a.qkv + ((int64_t)(t0 + t) * all_heads + head) * a.D;
-        return Piece{ld_once16(row + lo * 8), ld_once16(row + hi * 8)};
+    // a thread's pieces, every kThreads-th of all tokens' one after the other, are asked for ahead of anything else
+    const int total = count * own;
+    int asked = threadIdx.x, slot = 0;
+    auto ask = [&](int into) {
+        if (asked < total) {
+            const int t = asked / own, r = first + (asked - t * own), head = r / per_head;
+            int lo, hi;
+            chunks_of(r - head * per_head, head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
+            const uint16_t* row = a.qkv + ((int64_t)(t0 + t) * all_heads + head) * a.D;
+            copy16(smem_addr(&s_piece[into][0][threadIdx.x]), row + lo * 8);
+            copy16(smem_addr(&s_piece[into][1][threadIdx.x]), row + hi * 8);
+            asked += kThreads;
+        }
+        copy_commit();
     };
-    // the first piece is asked for before anything else
-    Piece next;
-    if ((int)threadIdx.x < count * own) next = load(threadIdx.x);
+#pragma unroll 1
+    for (int i = 0; i < kAhead; ++i) ask(i);
 
     // places in the cache
     if (first + own > a.heads * per_head) {
@@ -116,27 +123,29 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
     }
 
     const int pairs = a.rot / 2;
+    int i = threadIdx.x;
     for (int b = 0; b < count; b += kTableTokens) {
         const int n = min(kTableTokens, count - b);
-        for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
-            const int t = i / pairs, pair = i - t * pairs;
+        for (int j = threadIdx.x; j < n * pairs; j += kThreads) {
+            const int t = j / pairs, pair = j - t * pairs;
             const double turns = a.positions[(int64_t)a.rope->axis[pair] * a.T + t0 + b + t] * a.rope->turns[pair];
             float s, c;
             sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
             s_turn[t][pair] = make_float2(c, s);
         }
         __syncthreads();
-        // pieces in order: those of the next tokens' batch follow on
-        for (int i = b * own + threadIdx.x; i < (b + n) * own; i += kThreads) {
-            // (a batch's first piece of this thread may be another than the one asked for)
-            const Piece x = b == 0 && i == (int)threadIdx.x ? next : load(i);
+        for (; i < (b + n) * own; i += kThreads) {
+            copy_wait<kAhead - 1>();
+            const uint4 x_lo = s_piece[slot][0][threadIdx.x], x_hi = s_piece[slot][1][threadIdx.x];
+            ask(slot);
+            slot = slot + 1 == kAhead ? 0 : slot + 1;
             const int t = i / own, r = first + (i - t * own), head = r / per_head, p = r - head * per_head;
             const bool turned = head < a.heads + a.kv && p < a.rot / 16;
             int lo, hi;
             chunks_of(p, head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
             float u[8], v[8];
-            bf16x8_to_f32(x.lo, u);
-            bf16x8_to_f32(x.hi, v);
+            bf16x8_to_f32(x_lo, u);
+            bf16x8_to_f32(x_hi, v);
             if (turned) {
                 const float2* table = s_turn[t - b] + p * 8;
                 if (a.interleaved) {
@@ -178,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
 
 }  // namespace
 
-cudaError_t launch_attn_append(const AppendArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t launch_attn_append(const AppendArgs& a, int num_sms, cudaStream_t stream) {
     const int pieces = (a.heads + 2 * a.kv) * (a.D / 16);
     // few tokens: a token's pieces over several CTAs; many: several tokens a CTA
     const int target = 8 * num_sms;
@@ -195,7 +204,7 @@ cudaError_t launch_attn_append(const AppendArgs& a, int num_sms, cudaStream_t st
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_append_kernel, a, tokens);
 }
 

@@ -83,8 +83,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return v;
 }
 
-cudaError_t launch_attn_append(const AppendArgs& a, int num_sms, cudaStream_t stream, bool pdl);
-cudaError_t launch_attn_decode(const DecodeArgs& a, int head_dim, int num_sms, cudaStream_t stream, bool pdl);
+// Launches go out with programmatic dependent launch, always: it only moves the launch under the end of the kernel before.
+cudaError_t launch_attn_append(const AppendArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_attn_decode(const DecodeArgs& a, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t attn_decode_set_attributes();
 size_t attn_decode_counters(int num_sms);               // words
 size_t attn_decode_parts(int num_sms, int head_dim);    // floats

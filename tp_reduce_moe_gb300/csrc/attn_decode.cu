@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
 }
 
 template <int D, bool EIGHT, int NT>
-cudaError_t launch(const DecodeArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t launch(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
     using S = Shape<D, EIGHT, NT>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -893,15 +893,15 @@ cudaError_t launch(const DecodeArgs& a, int num_sms, cudaStream_t stream, bool p
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, EIGHT, NT>, a);
 }
 
 template <int D>
-cudaError_t launch_dim(const DecodeArgs& a, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t launch_dim(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
     const bool wide = a.rows_of_group > 8;
-    if (a.k.scale != nullptr) return wide ? launch<D, true, 2>(a, num_sms, stream, pdl) : launch<D, true, 1>(a, num_sms, stream, pdl);
-    return wide ? launch<D, false, 2>(a, num_sms, stream, pdl) : launch<D, false, 1>(a, num_sms, stream, pdl);
+    if (a.k.scale != nullptr) return wide ? launch<D, true, 2>(a, num_sms, stream) : launch<D, true, 1>(a, num_sms, stream);
+    return wide ? launch<D, false, 2>(a, num_sms, stream) : launch<D, false, 1>(a, num_sms, stream);
 }
 
 template <int D, bool EIGHT, int NT>
@@ -918,7 +918,7 @@ cudaError_t set_smem_dim() {
 
 }  // namespace
 
-cudaError_t launch_attn_decode(const DecodeArgs& args, int head_dim, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t launch_attn_decode(const DecodeArgs& args, int head_dim, int num_sms, cudaStream_t stream) {
     // groups of up to sixteen query heads of a key-value head, of equal size as far as that goes
     DecodeArgs a = args;
     a.shared = a.heads / a.kv;
@@ -926,9 +926,9 @@ cudaError_t launch_attn_decode(const DecodeArgs& args, int head_dim, int num_sms
     a.groups = a.kv * a.per_head;
     a.rows_of_group = (a.shared + a.per_head - 1) / a.per_head;
     switch (head_dim) {
-        case 64: return launch_dim<64>(a, num_sms, stream, pdl);
-        case 128: return launch_dim<128>(a, num_sms, stream, pdl);
-        case 256: return launch_dim<256>(a, num_sms, stream, pdl);
+        case 64: return launch_dim<64>(a, num_sms, stream);
+        case 128: return launch_dim<128>(a, num_sms, stream);
+        case 256: return launch_dim<256>(a, num_sms, stream);
     }
     return cudaErrorInvalidValue;
 }

@@ -4,18 +4,25 @@
 //   h = sum_r P_r + residual; y = h * rsqrt(mean(h^2) + eps) * (gamma + weight_bias)
 //   s = max |y| / 448 over a group of columns (or the row), q = e4m3(y / s)
 //
-// One CTA per token row.  A thread holds CPT chunks of eight columns in fp32
-// registers from the loads to the stores, so every byte is read and written
-// once.  Chunks lie along the lanes, so a group of 32, 64 or 128 columns is 4,
-// 8 or 16 neighbouring lanes and its maximum takes that many lanes' shuffles;
-// the row's sum of squares and, for one scale a row, its largest |h * gamma|
-// meet in shared memory behind one barrier.
+// A thread holds CPT chunks of eight columns of a row in fp32 registers from the loads to
+// the stores, so every byte is read and written once.  Chunks lie along the lanes, so a
+// group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes and its maximum takes that
+// many lanes' shuffles; the row's sum of squares and, for one scale a row, its largest
+// |h * gamma| meet in shared memory behind one barrier.
+//
+// Few rows: a CTA a row, partials loaded to registers, four in flight a chunk.  Many: CTAs
+// stay and take every so many rows; the rows of partials come through a ring in shared
+// memory by asynchronous copies, each thread copying what it reads itself, so that loads run
+// ahead over the rows' barriers and nothing waits but for its own copies.
 #include "arf_host.h"
 
 namespace arf {
 namespace {
 
 constexpr int kNormMaxThreads = 1024;
+constexpr int kPlaces = 6;        // of the ring
+constexpr int kNormSmem = 220 * 1024;
+static_assert(kPlaces * 2 * kNormMaxThreads * 16 <= kNormSmem, "shared memory of a CTA");
 constexpr float kE4m3Max = 448.0f;
 
 // A load of data that the kernel before may have written (coherent), read once.
@@ -46,49 +53,27 @@ __device__ __forceinline__ float scale_of(float top) {
     return top == 0.0f ? 1.0f : max_nan(top * (1.0f / kE4m3Max), 0x1p-126f);
 }
 
-// GROUP_LANES: lanes of eight columns that share a scale; 0: the whole row.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void add8(float h[8], uint4 v) {
+    float f[8];
+    bf16x8_to_f32(v, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] += f[j];
+}
+
+// Everything behind the sum: h [CPT chunks of this thread], which is used up.  s_sum and s_top are not written again before
+// all threads have come through a barrier behind this.  GROUP_LANES: lanes of eight columns that share a scale; 0: the row.
 template <int CPT, int GROUP_LANES, bool RES_F32>
-__global__ void __launch_bounds__(kNormMaxThreads) norm_q8_kernel(const __grid_constant__ NormQ8Args a) {
-    __shared__ float s_sum[32], s_top[32];
-    pdl_trigger();
-    pdl_wait();  // no global memory access before this point
-    const int64_t t = blockIdx.x;
+__device__ __forceinline__ void finish_row(const NormQ8Args& a, int64_t t, float h[CPT][8], const uint4 gamma[CPT], float* s_sum, float* s_top) {
     const int chunks = a.H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-
-    uint4 gamma[CPT];
-    float h[CPT][8];
-#pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-        const int chunk = threadIdx.x + c * blockDim.x;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[c][j] = 0.0f;
-        gamma[c] = make_uint4(0, 0, 0, 0);
-        if (chunk < chunks) gamma[c] = *reinterpret_cast<const uint4*>(a.gamma + chunk * 8);
-    }
-    // partials in rank order, then the residual, up to four rows of each chunk in flight
-    for (int r0 = 0; r0 <= a.R; r0 += 4) {
-        uint4 v[CPT][4];
-#pragma unroll
-        for (int c = 0; c < CPT; ++c)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int chunk = threadIdx.x + c * blockDim.x;
-                v[c][u] = make_uint4(0, 0, 0, 0);
-                if (chunk < chunks && r0 + u <= a.R)
-                    v[c][u] = ld_once16((r0 + u < a.R ? a.P[r0 + u] : a.residual) + t * a.H + chunk * 8);
-            }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (r0 + u <= a.R)
-#pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    float f[8];
-                    bf16x8_to_f32(v[c][u], f);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) h[c][j] += f[j];
-                }
-    }
-
     float sum = 0.0f, top = 0.0f;
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
@@ -151,37 +136,163 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_q8_kernel(const __grid_c
     }
 }
 
+template <int CPT, int GROUP_LANES, bool RES_F32>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_q8_kernel(const __grid_constant__ NormQ8Args a) {
+    __shared__ float s_sum[32], s_top[32];
+    pdl_trigger();
+    pdl_wait();  // no global memory access before this point
+    const int64_t t = blockIdx.x;
+    const int chunks = a.H / 8;
+    uint4 gamma[CPT];
+    float h[CPT][8];
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+        const int chunk = threadIdx.x + c * blockDim.x;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[c][j] = 0.0f;
+        gamma[c] = make_uint4(0, 0, 0, 0);
+        if (chunk < chunks) gamma[c] = *reinterpret_cast<const uint4*>(a.gamma + chunk * 8);
+    }
+    // partials in rank order, then the residual, up to four rows of each chunk in flight
+    for (int r0 = 0; r0 <= a.R; r0 += 4) {
+        uint4 v[CPT][4];
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int chunk = threadIdx.x + c * blockDim.x;
+                v[c][u] = make_uint4(0, 0, 0, 0);
+                if (chunk < chunks && r0 + u <= a.R)
+                    v[c][u] = ld_once16((r0 + u < a.R ? a.P[r0 + u] : a.residual) + t * a.H + chunk * 8);
+            }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (r0 + u <= a.R)
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) add8(h[c], v[c][u]);
+    }
+    finish_row<CPT, GROUP_LANES, RES_F32>(a, t, h, gamma, s_sum, s_top);
+}
+
+// Rows t, t + gridDim.x, ...: the ring's places hold CPT chunks of one partial (or the residual) for each thread.
+template <int CPT, int GROUP_LANES, bool RES_F32>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_q8_stream_kernel(const __grid_constant__ NormQ8Args a) {
+    extern __shared__ __align__(16) uint4 s_ring[];  // [kPlaces][CPT][threads]
+    __shared__ float s_sum[2][32], s_top[2][32];
+    pdl_trigger();
+    pdl_wait();  // no global memory access before this point
+    const int chunks = a.H / 8;
+    const uint64_t policy = l2_evict_first_policy();
+    uint4 gamma[CPT];
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+        const int chunk = threadIdx.x + c * blockDim.x;
+        gamma[c] = chunk < chunks ? *reinterpret_cast<const uint4*>(a.gamma + chunk * 8) : make_uint4(0, 0, 0, 0);
+    }
+    int64_t ask_t = blockIdx.x;
+    int ask_r = 0;
+    uint4* const mine = s_ring + threadIdx.x;
+    auto ask = [&](int place) {
+        if (ask_t < a.T) {
+            const uint16_t* row = (ask_r < a.R ? a.P[ask_r] : a.residual) + ask_t * a.H;
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) {
+                const int chunk = threadIdx.x + c * blockDim.x;
+                if (chunk < chunks) copy16(smem_addr(mine + (place * CPT + c) * blockDim.x), row + chunk * 8, policy);
+            }
+            if (++ask_r > a.R) {
+                ask_r = 0;
+                ask_t += gridDim.x;
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int p = 0; p < kPlaces; ++p) ask(p);
+    int place = 0;
+    bool odd = false;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, odd = !odd) {
+        float h[CPT][8];
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[c][j] = 0.0f;
+        for (int r = 0; r <= a.R; ++r) {
+            copy_wait<kPlaces - 1>();
+            uint4 v[CPT];
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) v[c] = mine[(place * CPT + c) * blockDim.x];  // (not there: not used)
+#pragma unroll
+            for (int c = 0; c < CPT; ++c)
+                if (threadIdx.x + c * blockDim.x < chunks) add8(h[c], v[c]);
+            ask(place);  // (a thread reads before it copies over)
+            place = place + 1 == kPlaces ? 0 : place + 1;
+        }
+        // (a thread can be one row ahead of another: two places for the sums)
+        finish_row<CPT, GROUP_LANES, RES_F32>(a, t, h, gamma, s_sum[odd], s_top[odd]);
+    }
+}
+
 using Kernel = void (*)(NormQ8Args);
 
-template <int CPT, bool RES_F32>
+template <int CPT, bool RES_F32, bool STREAM>
 Kernel kernel_of(int group) {
     switch (group) {
-        case 32: return norm_q8_kernel<CPT, 4, RES_F32>;
-        case 64: return norm_q8_kernel<CPT, 8, RES_F32>;
-        case 128: return norm_q8_kernel<CPT, 16, RES_F32>;
+        case 32: return STREAM ? norm_q8_stream_kernel<CPT, 4, RES_F32> : norm_q8_kernel<CPT, 4, RES_F32>;
+        case 64: return STREAM ? norm_q8_stream_kernel<CPT, 8, RES_F32> : norm_q8_kernel<CPT, 8, RES_F32>;
+        case 128: return STREAM ? norm_q8_stream_kernel<CPT, 16, RES_F32> : norm_q8_kernel<CPT, 16, RES_F32>;
     }
-    return norm_q8_kernel<CPT, 0, RES_F32>;
+    return STREAM ? norm_q8_stream_kernel<CPT, 0, RES_F32> : norm_q8_kernel<CPT, 0, RES_F32>;
+}
+
+template <bool STREAM>
+Kernel kernel_for(int cpt, bool res_f32, int group) {
+    return cpt == 1 ? (res_f32 ? kernel_of<1, true, STREAM>(group) : kernel_of<1, false, STREAM>(group))
+                    : (res_f32 ? kernel_of<2, true, STREAM>(group) : kernel_of<2, false, STREAM>(group));
 }
 
 }  // namespace
 
-cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, cudaStream_t stream, bool pdl) {
+cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num_sms, cudaStream_t stream) {
     const int chunks = a.H / 8;
-    const int cpt = chunks > kNormMaxThreads ? 2 : 1;
+    // CTAs that stay, once there are more rows than SMs
+    const bool stay = a.T > num_sms;
+    const int cpt = chunks > (stay ? 256 : kNormMaxThreads) ? 2 : 1;
     const int threads = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
     if (a.T < 1 || a.T > 0x7fffffff || threads > kNormMaxThreads) return cudaErrorInvalidValue;
-    const Kernel k = cpt == 1 ? (res_f32 ? kernel_of<1, true>(group) : kernel_of<1, false>(group))
-                              : (res_f32 ? kernel_of<2, true>(group) : kernel_of<2, false>(group));
+    const Kernel k = stay ? kernel_for<true>(cpt, res_f32, group) : kernel_for<false>(cpt, res_f32, group);
+    int64_t grid = a.T;
+    size_t smem = 0;
+    if (stay) {
+        smem = (size_t)kPlaces * cpt * threads * 16;
+        // as many CTAs as an SM's threads (of up to 64 registers) and shared memory take
+        int per_sm = 1024 / threads;
+        if (per_sm > (int)(kNormSmem / smem)) per_sm = (int)(kNormSmem / smem);
+        if (per_sm < 1) per_sm = 1;
+        if (grid > (int64_t)per_sm * num_sms) grid = (int64_t)per_sm * num_sms;
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)a.T);
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
+    // always: it only moves the launch under the end of the kernel before
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+cudaError_t norm_q8_set_attributes() {
+    for (int cpt = 1; cpt <= 2; ++cpt)
+        for (const bool res_f32 : {false, true})
+            for (const int group : {0, 32, 64, 128}) {
+                const cudaError_t e = cudaFuncSetAttribute(kernel_for<true>(cpt, res_f32, group), cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+                if (e != cudaSuccess) return e;
+            }
+    return cudaSuccess;
 }
 
 }  // namespace arf
