@@ -105,12 +105,20 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
             atomicOr(&s_hash[h >> 5], 1u << (h & 31));
         }
         __syncthreads();
-        for (int t = t0 + 1 + threadIdx.x; t < a.T; t += kThreads) {
-            const int slot = a.slots[t];
-            const unsigned h = (unsigned)slot & ((1u << kHashBits) - 1);
-            if (slot < 0 || !(s_hash[h >> 5] >> (h & 31) & 1)) continue;
-            for (int i = 0; i < count && t0 + i < t; ++i)
-                if (s_slot[i] == slot) s_dead[i] = 1;
+        // eight loads in flight: one after the other they would take longer than the copies
+#pragma unroll 1
+        for (int t = t0 + 1 + threadIdx.x; t < a.T; t += 8 * kThreads) {
+            int later[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) later[k] = t + k * kThreads < a.T ? a.slots[t + k * kThreads] : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const unsigned h = (unsigned)later[k] & ((1u << kHashBits) - 1);
+                if (later[k] < 0 || !(s_hash[h >> 5] >> (h & 31) & 1)) continue;
+#pragma unroll 1
+                for (int i = 0; i < count && t0 + i < t + k * kThreads; ++i)
+                    if (s_slot[i] == later[k]) s_dead[i] = 1;
+            }
         }
         __syncthreads();
         if ((int)threadIdx.x < count) {

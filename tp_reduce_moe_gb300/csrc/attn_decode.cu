@@ -48,8 +48,8 @@ struct Shape {
     static constexpr int kRow = D * (EIGHT ? 1 : 2);                   // bytes of a key
     static constexpr int kChunks = kRow / 16;
     static constexpr int kHalf = kTok * kRow;  // bytes of a unit's keys (or values)
-    static constexpr int kHalves = kRing / kHalf;
-    static constexpr int kLead = kHalves - 1;  // halves that are asked for ahead
+    static constexpr int kAhead = (kRing / kHalf - 1) / 2 < 4 ? (kRing / kHalf - 1) / 2 : 4;  // units that are asked for ahead
+    static constexpr int kHalves = 2 * kAhead + 1;
     static constexpr int kLeast = kHalf >= 4096 ? 1 : 4096 / kHalf;  // units of a warp, while there are SMs left
     static constexpr int kCost = kHalf >= 8192 ? 1 : 8192 / kHalf;   // units that an item counts for besides its own
     static constexpr int kAlone = 131072 / kHalf;  // units by which a CTA that keeps an item may pass an equal share
@@ -60,7 +60,7 @@ struct Shape {
     static constexpr int kSmem = kWarps * kRing;
     static_assert(kSmem + 16384 <= 232448, "shared memory of a CTA");
     static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums, in its ring");
-    static_assert(kLead <= 11, "units that are asked for and not used, of the eight masks that are kept");
+    static_assert(kAhead >= 1 && kAhead + 2 <= 8, "units that are asked for and not used, of the eight masks and segments that are kept");
     static_assert(kPart % 4 == 0 && kSmem >= kPart * 4, "parts come by 16 bytes");
     // where chunk c of row r lies, so that eight rows' chunks c are in eight different groups of banks
     __device__ static int place(int r, int c) {
@@ -128,68 +128,24 @@ __device__ __forceinline__ float share_of(float m, float top) { return ex2(m - (
 
 // A warp's share of an item: units [u0, u1) of its n.
 struct Segment {
-    int b, kv_head;
-    int start, len;  // tokens looked at
-    int u0, u1, n;
-    int row, rows;   // first row of the output [B * heads], and how many
     int64_t item;    // where the item's first unit is among all
+    int u0, u1, n;
+    int kv_head;
+    int row, rows;   // first row of the output [B * heads], and how many
+    bool last;       // of the warp
 };
 
-// What is rare is not inline: it would crowd the loop out of the instruction cache, and code that a call runs through once is
-// fetched slowly.
-
-// First token that is looked at, and the length, of a sequence.
-__device__ __noinline__ int2 tokens_of(const DecodeArgs& a, int b, bool report) {
+// Tokens that are looked at, and where they begin.
+__device__ __forceinline__ int tokens_of(const DecodeArgs& a, int b, bool report, int* start) {
     const int len = checked_length(a, b, report);
-    return make_int2(a.window > 0 && len > a.window ? len - a.window : 0, len);
+    *start = a.window > 0 && len > a.window ? len - a.window : 0;
+    return len;
 }
 
 template <int TOK>
-__device__ __forceinline__ int units_of(int2 t) {
-    return (int)(((int64_t)t.y - t.x + TOK - 1) / TOK);
+__device__ __forceinline__ int units_of(int start, int len) {
+    return (int)(((int64_t)len - start + TOK - 1) / TOK);
 }
-
-// Walks the segments of a range of units.  An item of n units counts for COST more, before the first, for what it costs to begin
-// and end one; these are walked over.
-template <int TOK, int COST>
-struct Walk {
-    int b, group, u;  // the next unit, of COST + n
-    int start, len, n;
-    int64_t item;     // where the item's first unit (behind what it costs) is among all
-    int64_t left;     // units of the range that are not handed out; 0 once no real one is among them
-
-    __device__ __forceinline__ void sequence(const DecodeArgs& a) {
-        const int2 t = tokens_of(a, b, false);
-        start = t.x;
-        len = t.y;
-        n = units_of<TOK>(t);
-    }
-    __device__ __forceinline__ void begin() {
-        if (left <= COST - u) left = 0;
-    }
-    // The next segment of a range that has real units left.
-    __device__ __noinline__ void next(const DecodeArgs& a, Segment* s) {
-        if (u == n + COST) {  // the item is done: the next one that has units (there is one, for some are left)
-            u = 0;
-            item += n + COST;
-            if (++group == a.groups) {
-                group = 0;
-#pragma unroll 1
-                do {
-                    ++b;
-                    sequence(a);
-                } while (n == 0);
-            }
-        }
-        const int take = (int)(left < n + COST - u ? left : n + COST - u);
-        const int head = a.per_head == 1 ? group : group / a.per_head, row = (group - head * a.per_head) * a.rows_of_group;
-        *s = Segment{b, head, start, len, max(u - COST, 0), u + take - COST, n,
-                     b * a.heads + head * a.shared + row, min(a.rows_of_group, a.shared - row), item};
-        u += take;
-        left -= take;
-        if (left <= COST) left = 0;
-    }
-};
 
 // Quotients of numbers that are small as a rule.
 __device__ __noinline__ int64_t quotient64(int64_t n, int64_t d) {
@@ -218,7 +174,7 @@ struct Join {
 };
 
 // Four columns of a row of the output, and with the first of them its lse.
-__device__ __noinline__ void finish_row(const DecodeArgs& a, int row, int d, int D, float4 sum, float weight, float vs, float top) {
+__device__ __forceinline__ void finish_row(const DecodeArgs& a, int row, int d, int D, float4 sum, float weight, float vs, float top) {
     const float f = weight == 0.0f ? 0.0f : __fdividef(vs, weight);
     *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + d) = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
     if (d == 0 && a.lse != nullptr) a.lse[row] = weight == 0.0f ? -INFINITY : (top + lg2(weight)) * kLn2;
@@ -248,6 +204,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     __shared__ int s_b[kWarps];
     __shared__ Join s_join[2];
     __shared__ unsigned s_mask[kWarps][8];
+    __shared__ Segment s_seg[kWarps][8];
     __shared__ const uint8_t* s_row[kWarps][2][32];  // where the keys and values of a unit's tokens are
     pdl_wait();  // no global memory access before this point
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -256,10 +213,19 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     // ---- what this CTA's warps take
     int64_t total, each = 0;   // units, and units of a warp where all are dealt out
     int64_t begin, end;        // units of this CTA
-    Walk<TOK, S::kCost> walk;
+    // The walk over this warp's items.  One counts for kCost units more, before its first, for what it costs to begin and end
+    // it; these are walked over.
+    int w_b = 0, w_group = 0, w_u = 0, w_start = 0, w_len = 0, w_n = 0;  // sequence, group, next unit of kCost + w_n, tokens
+    int64_t w_item = 0;  // where the item's first unit (behind what it costs) is among all
+    int64_t w_left = 0;  // units of the range that are not handed out; 0 once no real one is among them
+    auto sequence = [&]() {
+        w_len = tokens_of(a, w_b, false, &w_start);
+        w_n = units_of<TOK>(w_start, w_len);
+    };
     {
         auto units = [&](int b) {  // of one item, with what it costs
-            const int n = units_of<TOK>(tokens_of(a, b, blockIdx.x == 0));
+            int start;
+            const int len = tokens_of(a, b, blockIdx.x == 0, &start), n = units_of<TOK>(start, len);
             return n > 0 ? n + S::kCost : 0;
         };
         // a thread's sequences, and before them the units of the threads before; few sequences: each warp sums by itself
@@ -291,30 +257,27 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         }
         if ((int64_t)a.B * a.groups <= gridDim.x && (int64_t)(most - S::kAlone) * gridDim.x <= total) {
             // One CTA an item: nothing to join over CTAs, and no CTA has much more to do than with equal shares.
-            const int b = blockIdx.x / a.groups;
-            walk.b = min(b, a.B - 1);
-            walk.sequence(a);
-            if (b >= a.B) walk.n = 0;
-            const int share = (walk.n + kWarps - 1) / kWarps;
-            walk.group = blockIdx.x - b * a.groups;
-            walk.u = min(walk.n, warp * share);
-            walk.left = min(share, walk.n - walk.u);
-            walk.u += S::kCost;
-            walk.item = 0;
+            w_b = blockIdx.x / a.groups;
+            w_group = blockIdx.x - w_b * a.groups;
+            if (w_b < a.B) sequence();
+            const int share = (w_n + kWarps - 1) / kWarps;
+            w_u = min(w_n, warp * share);
+            w_left = min(share, w_n - w_u);
+            w_u += S::kCost;
             begin = 0;
-            end = walk.n;
+            end = w_n;
         } else {
             // Equal ranges of all units; the last ones may be short or empty.
             each = max((int64_t)S::kLeast, quotient64(total + gridDim.x * kWarps - 1, gridDim.x * kWarps));
             begin = each * (blockIdx.x * kWarps);
             end = min(total, begin + each * kWarps);
             const int64_t from = begin + each * warp;
-            walk.left = min(each, total - from);
+            w_left = max((int64_t)0, min(each, total - from));
             int64_t skip = 0;
             if (few) {
                 const unsigned at = __ballot_sync(0xffffffffu, before <= from && from < before + mine);
-                walk.b = at ? __ffs(at) - 1 : 0;
-                skip = from - __shfl_sync(0xffffffffu, before, walk.b);
+                w_b = at ? __ffs(at) - 1 : 0;
+                skip = from - __shfl_sync(0xffffffffu, before, w_b);
             } else {
 #pragma unroll 1
                 for (int w = 0; w < kWarps; ++w) {  // whose first unit is here?
@@ -330,49 +293,66 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
                     }
                 }
                 __syncthreads();
-                walk.b = s_b[warp];
+                w_b = s_b[warp];
                 skip = s_first[warp];
             }
-            if (walk.left > 0) {
-                walk.sequence(a);
-                walk.group = (int)quotient64(skip, walk.n + S::kCost);
-                walk.u = (int)(skip - (int64_t)walk.group * (walk.n + S::kCost));
-                walk.item = from - walk.u + S::kCost;
-                walk.begin();
+            if (w_left > 0) {
+                sequence();
+                w_group = (int)quotient64(skip, w_n + S::kCost);
+                w_u = (int)(skip - (int64_t)w_group * (w_n + S::kCost));
+                w_item = from - w_u + S::kCost;
+                if (w_left <= S::kCost - w_u) w_left = 0;
             }
         }
     }
 
     // ---- the stream of this warp's units
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
-    Walk<TOK, S::kCost> ahead = walk;
-    Segment ask{};                 // segment whose units are asked for
-    int ask_u = 0, ask_last = 0;   // unit that is next, last page of the sequence
-    bool asking = true, live = false;  // there are units left; the one that is being asked for is one
-    const uint8_t *k_head = nullptr, *v_head = nullptr;  // the segment's keys and values
-    unsigned asked = 0;            // units asked for
-    uint32_t fill = 0;             // place in the ring that is filled next
+    bool asking = w_left > 0, live = false;  // there are units left; the one that is being asked for is one
+    int ask_u = 0, ask_u1 = 0, ask_last = 0;  // of the segment that is asked for: next unit, end, last page of the sequence
+    const uint8_t *k_head = nullptr, *v_head = nullptr;  // and its keys and values
+    unsigned asked = 0, found = 0;  // units asked for, segments found
+    uint32_t fill = 0;              // place in the ring that is filled next
     // the page table's entries from table_at on: this lane's of the first 32 and of the next 32
     int table_at = 0, entry = 0, entry_next = 0;
     const uint64_t policy = a.per_head == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
     auto page_of = [&](int64_t token) { return (int)((uint64_t)token * a.page_mul >> (31 + a.page_shift)); };
     auto table_entry = [&](int index) {  // -1 behind the sequence's last
-        return index <= ask_last ? a.table[ask.b * a.table_stride + index] : -1;
+        return index <= ask_last ? a.table[w_b * a.table_stride + index] : -1;
     };
-    auto advance = [&]() {
-        if (!asking || ask_u != ask.u1) return;
-        asking = ahead.left > 0;
+    auto advance = [&]() {  // to the next segment, once this one's units have been asked for
+        if (!asking || ask_u != ask_u1) return;
+        asking = w_left > 0;
         if (!asking) return;
-        Segment s;
-        ahead.next(a, &s);
-        ask = s;
-        ask_u = ask.u0;
-        ask_last = page_of(ask.len - 1);
-        table_at = page_of(ask.start + (int64_t)ask_u * TOK);
+        if (w_u == w_n + S::kCost) {  // the item is done: the next one that has units (there is one, for some are left)
+            w_u = 0;
+            w_item += w_n + S::kCost;
+            if (++w_group == a.groups) {
+                w_group = 0;
+#pragma unroll 1
+                do {
+                    ++w_b;
+                    sequence();
+                } while (w_n == 0);
+            }
+        }
+        const int take = (int)(w_left < w_n + S::kCost - w_u ? w_left : w_n + S::kCost - w_u);
+        const int head = a.per_head == 1 ? w_group : w_group / a.per_head, row = (w_group - head * a.per_head) * a.rows_of_group;
+        ask_u = max(w_u - S::kCost, 0);
+        w_u += take;
+        ask_u1 = w_u - S::kCost;
+        w_left -= take;
+        if (w_left <= S::kCost) w_left = 0;
+        if (lane == 0)
+            s_seg[warp][found & 7] = Segment{w_item, ask_u, ask_u1, w_n, head, w_b * a.heads + head * a.shared + row,
+                                             min(a.rows_of_group, a.shared - row), w_left == 0};
+        ++found;
+        ask_last = page_of(w_len - 1);
+        table_at = page_of(w_start + (int64_t)ask_u * TOK);
         entry = table_entry(table_at + lane);
         entry_next = table_entry(table_at + 32 + lane);
-        k_head = a.k.data + ask.kv_head * a.k.head;
-        v_head = a.v.data + ask.kv_head * a.v.head;
+        k_head = a.k.data + head * a.k.head;
+        v_head = a.v.data + head * a.v.head;
     };
     auto copy_half = [&](int which) {  // keys (0) or values (1) of the unit that was looked up
         if (live) {
@@ -388,7 +368,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     auto ask_keys = [&]() {
         live = asking;
         if (live) {
-            const int64_t first = ask.start + (int64_t)ask_u * TOK, token = first + lane;
+            const int64_t first = w_start + (int64_t)ask_u * TOK, token = first + lane;
             if (page_of(first) - table_at >= 32) {  // (a unit has 32 tokens at most)
                 table_at += 32;
                 entry = entry_next;
@@ -397,7 +377,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             const int index = page_of(token), in_page = (int)token - index * a.page_size, at = index - table_at;
             const int here = __shfl_sync(0xffffffffu, entry, at & 31), next = __shfl_sync(0xffffffffu, entry_next, at & 31);
             const int page = at < 32 ? here : next;
-            const bool wanted = lane < TOK && token < ask.len, there = wanted && (unsigned)page < (unsigned)a.pages;
+            const bool wanted = lane < TOK && token < w_len, there = wanted && (unsigned)page < (unsigned)a.pages;
             if (wanted && !there) atomicOr(a.err, kErrPageRange);
             const unsigned mask = __ballot_sync(0xffffffffu, there);
             __syncwarp();  // all lanes have read the places before
@@ -412,57 +392,51 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         }
         copy_half(0);
     };
-    auto ask_values = [&]() {
-        copy_half(1);
-        advance();
+    auto empty_rows = [&]() {  // rows without tokens: zeros, dealt to the warps
+#pragma unroll 1
+        for (int64_t b = blockIdx.x + (int64_t)gridDim.x * warp; b < a.B; b += gridDim.x * kWarps)
+            if (checked_length(a, (int)b, false) == 0) {
+#pragma unroll 1
+                for (int j = lane; j < a.heads * D / 8; j += 32) st_global16(a.out + b * a.heads * D + j * 8, make_uint4(0, 0, 0, 0));
+                if (a.lse != nullptr)
+#pragma unroll 1
+                    for (int j = lane; j < a.heads; j += 32) a.lse[b * a.heads + j] = -INFINITY;
+            }
     };
-    advance();
-#pragma unroll 1
-    for (int i = 0; i < S::kLead / 2; ++i) {
-        ask_keys();
-        ask_values();
+    if (begin >= end) {
+        empty_rows();
+        return;
     }
-    if (S::kLead % 2 == 1) ask_keys();
-
-    // rows without tokens: zeros, dealt to the warps
-#pragma unroll 1
-    for (int64_t b = blockIdx.x + (int64_t)gridDim.x * warp; b < a.B; b += gridDim.x * kWarps)
-        if (checked_length(a, (int)b, false) == 0) {
-#pragma unroll 1
-            for (int j = lane; j < a.heads * D / 8; j += 32) st_global16(a.out + b * a.heads * D + j * 8, make_uint4(0, 0, 0, 0));
-            if (a.lse != nullptr)
-#pragma unroll 1
-                for (int j = lane; j < a.heads; j += 32) a.lse[b * a.heads + j] = -INFINITY;
-        }
-    if (begin >= end) return;
 
     auto place_of = [&](int w, int which) {  // of a warp's sums: left in mid-stream, or on the way out
         return a.part + (int64_t)gridDim.x * 2 * S::kPart + (((int64_t)blockIdx.x * kWarps + w) * 2 + which) * S::kSums;
     };
 
-    // ---- segments
+    // ---- the units.  A turn asks for one and works on the one that was asked for kAhead turns before; the turn before the
+    // first looks up where the first are.
     uint32_t take = 0;   // place in the ring that is used next
-    unsigned taken = 0;  // units used
-    bool more = walk.left > 0;
+    unsigned taken = 0, begun = 0;  // units used, segments begun
+    bool more = asking;
     if (lane < 2) s_part[2 * warp + lane].item = -1;
-    __syncwarp();
     auto wait_half = [&]() {
-        copy_wait<S::kLead>();
+        copy_wait<2 * S::kAhead>();
         __syncwarp();
         const uint32_t slot = ring + take;
         take = take + S::kHalf == S::kHalves * S::kHalf ? 0 : take + S::kHalf;
         return slot;
     };
-#pragma unroll 1
-    while (more) {
-        Segment next;
-        walk.next(a, &next);
-        const Segment seg = next;
-        more = walk.left > 0;
+    uint32_t q[kSteps][NT][2];
+    float q_scale[NT][2];  // of the scores of heads 8 i + 2 t4 (+1): log2(e), scale, scale of the keys, power of two of the row
+    // o: of heads 8 n + 2 t4 (+1) the columns 16 i + g (+8), with bytes 16 i + 2 g (+1)
+    float o[kSteps][NT][4], m[NT][2], l[NT][2];
+    uint32_t p[MT][NT][2], rest[MT][NT][2];  // weights of a unit
+    int u = 0, u1 = 0;  // of the segment that is worked on: the next unit, the end
+    auto begin_segment = [&]() {
+        const Segment& seg = s_seg[warp][begun & 7];
+        u = seg.u0;
+        u1 = seg.u1;
         // Query heads 8 i + g.  Columns of a step: 2 t4 (+1) and 2 t4 + 8 (+1); with bytes 4 t4 .. 4 t4 + 3, the order that
         // their keys come in.  (Rows that the item does not have are read as its last: what becomes of them is not used.)
-        uint32_t q[kSteps][NT][2];
-        float q_scale[NT][2];  // of the scores of heads 8 i + 2 t4 (+1): log2(e), scale, scale of the keys, power of two of the row
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const uint16_t* src = a.q + (int64_t)(seg.row + min(8 * n + g, seg.rows - 1)) * D;
@@ -503,8 +477,6 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
                 q_scale[n][1] = __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
             }
         }
-        // o: of heads 8 n + 2 t4 (+1) the columns 16 i + g (+8), with bytes 16 i + 2 g (+1)
-        float o[kSteps][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = -INFINITY;
@@ -514,152 +486,148 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[i][n][j] = 0.0f;
         }
-
-#pragma unroll 1
-        for (int u = seg.u0; u < seg.u1; ++u) {
-            // ---- scores of TOK tokens: of heads 8 n + 2 t4 (+1) the tokens 16 i + g (+8)
-            __syncwarp();  // the place that is filled now has been read by all lanes
-            if (S::kLead % 2 == 0) ask_keys();
-            else ask_values();
-            uint32_t slot = wait_half();
-            float s[MT][NT][4];
+    };
+    // this lane's row of a matrix of 16 by 16: eights of rows before or behind eights of columns
+    const int row8 = ((lane >> 3) & 1) * 8 + (lane & 7), odd8 = (lane >> 4) * 8 + (lane & 7);
+    // scores of a unit's tokens, and their weights
+    auto scores = [&]() {
+        // of heads 8 n + 2 t4 (+1) the tokens 16 i + g (+8)
+        const uint32_t slot = wait_half();
+        float s[MT][NT][4];
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][n][j] = 0.0f;
-            const int row8 = ((lane >> 3) & 1) * 8 + (lane & 7), odd8 = (lane >> 4) * 8 + (lane & 7);
-            if (EIGHT) {
-                // a matrix is 8 tokens by 16 bytes: one step of the columns
-#pragma unroll
-                for (int c = 0; c < kSteps; c += 2)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        uint32_t r[4];
-                        ldmatrix4(r, slot + S::place(i * 16 + row8, c + (lane >> 4)));
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)r[2 * j]), a1 = e4m3x2_to_f16x2((uint16_t)r[2 * j + 1]);
-                            const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)(r[2 * j] >> 16)), a3 = e4m3x2_to_f16x2((uint16_t)(r[2 * j + 1] >> 16));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) mma<true>(s[i][n], a0, a1, a2, a3, q[c + j][n][0], q[c + j][n][1]);
-                        }
-                    }
-            } else {
-#pragma unroll
-                for (int c = 0; c < kSteps; ++c)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        uint32_t r[4];
-                        ldmatrix4(r, slot + S::place(i * 16 + row8, c * 2 + (lane >> 4)));
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma<false>(s[i][n], r[0], r[1], r[2], r[3], q[c][n][0], q[c][n][1]);
-                    }
-            }
-            // ---- their weights
-            const unsigned mask = s_mask[warp][taken++ & 7];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][n][j] *= q_scale[n][j & 1];
-            if (mask != 0xffffffffu >> (32 - TOK)) {
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i)
-                    if (!(mask >> (8 * i + g) & 1))
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) s[i >> 1][n][2 * (i & 1)] = s[i >> 1][n][2 * (i & 1) + 1] = -INFINITY;
-            }
-            float keep[NT][2];
-            bool moved = false;
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float top = fmaxf(s[0][n][h], s[0][n][h + 2]);
-                    if (MT == 2) top = fmaxf(top, fmaxf(s[MT - 1][n][h], s[MT - 1][n][h + 2]));
+                for (int j = 0; j < 4; ++j) s[i][n][j] = 0.0f;
+        if (EIGHT) {
+            // a matrix is 8 tokens by 16 bytes: one step of the columns
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    keep[n][h] = 1.0f;
-                    if (top > m[n][h] + kLazy) {  // (the first finite score passes minus infinity)
-                        keep[n][h] = ex2(m[n][h] - top);
-                        m[n][h] = top;
-                        l[n][h] *= keep[n][h];
-                        moved = true;
+            for (int c = 0; c < kSteps; c += 2)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t r[4];
+                    ldmatrix4(r, slot + S::place(i * 16 + row8, c + (lane >> 4)));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)r[2 * j]), a1 = e4m3x2_to_f16x2((uint16_t)r[2 * j + 1]);
+                        const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)(r[2 * j] >> 16)), a3 = e4m3x2_to_f16x2((uint16_t)(r[2 * j + 1] >> 16));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma<true>(s[i][n], a0, a1, a2, a3, q[c + j][n][0], q[c + j][n][1]);
                     }
                 }
-            if (__any_sync(0xffffffffu, moved)) {
+        } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+            for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-                    for (int i = 0; i < kSteps; ++i)
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t r[4];
+                    ldmatrix4(r, slot + S::place(i * 16 + row8, c * 2 + (lane >> 4)));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) o[i][n][j] *= keep[n][j & 1];
-            }
-            uint32_t p[MT][NT][2], rest[MT][NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float base[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) base[h] = m[n][h] == -INFINITY ? 0.0f : m[n][h] - kOffset;
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float x = ex2(s[i][n][2 * r] - base[0]), y = ex2(s[i][n][2 * r + 1] - base[1]);
-                        l[n][0] += x;
-                        l[n][1] += y;
-                        if (EIGHT) {
-                            p[i][n][r] = transposed(pack_f16x2(x, y));
-                        } else {
-                            const uint32_t w = pack_bf16x2(x, y);
-                            p[i][n][r] = transposed(w);
-                            rest[i][n][r] = transposed(pack_bf16x2(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u)));
-                        }
-                    }
-            }
-            // ---- and values
-            __syncwarp();
-            if (S::kLead % 2 == 0) ask_values();
-            else ask_keys();
-            slot = wait_half();
-            if (EIGHT) {
-                // transposed by pairs of bytes: a register holds two columns of two tokens; even columns make rows 0 .. 7 of
-                // an operand, odd ones rows 8 .. 15
-#pragma unroll
-                for (int c = 0; c < kSteps; c += 2)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        uint32_t r[4];
-                        ldmatrix4_trans(r, slot + S::place(i * 16 + row8, c + (lane >> 4)));
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
-                            const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)x), a1 = e4m3x2_to_f16x2((uint16_t)(x >> 16));
-                            const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)y), a3 = e4m3x2_to_f16x2((uint16_t)(y >> 16));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) mma<true>(o[c + j][n], a0, a1, a2, a3, p[i][n][0], p[i][n][1]);
-                        }
-                    }
-            } else {
-#pragma unroll
-                for (int c = 0; c < kSteps; ++c)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        uint32_t r[4];
-                        ldmatrix4_trans(r, slot + S::place(i * 16 + odd8, c * 2 + ((lane >> 3) & 1)));
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma<false>(o[c][n], r[0], r[1], r[2], r[3], p[i][n][0], p[i][n][1]);
-                            mma<false>(o[c][n], r[0], r[1], r[2], r[3], rest[i][n][0], rest[i][n][1]);
-                        }
-                    }
-            }
+                    for (int n = 0; n < NT; ++n) mma<false>(s[i][n], r[0], r[1], r[2], r[3], q[c][n][0], q[c][n][1]);
+                }
         }
-
-        // ---- the item, or this warp's part of it
+        const unsigned mask = s_mask[warp][taken++ & 7];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][n][j] *= q_scale[n][j & 1];
+        if (mask != 0xffffffffu >> (32 - TOK)) {
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i)
+                if (!(mask >> (8 * i + g) & 1))
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[i >> 1][n][2 * (i & 1)] = s[i >> 1][n][2 * (i & 1) + 1] = -INFINITY;
+        }
+        float keep[NT][2];
+        bool moved = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float top = fmaxf(s[0][n][h], s[0][n][h + 2]);
+                if (MT == 2) top = fmaxf(top, fmaxf(s[MT - 1][n][h], s[MT - 1][n][h + 2]));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                keep[n][h] = 1.0f;
+                if (top > m[n][h] + kLazy) {  // (the first finite score passes minus infinity)
+                    keep[n][h] = ex2(m[n][h] - top);
+                    m[n][h] = top;
+                    l[n][h] *= keep[n][h];
+                    moved = true;
+                }
+            }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[i][n][j] *= keep[n][j & 1];
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float base[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) base[h] = m[n][h] == -INFINITY ? 0.0f : m[n][h] - kOffset;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float x = ex2(s[i][n][2 * r] - base[0]), y = ex2(s[i][n][2 * r + 1] - base[1]);
+                    l[n][0] += x;
+                    l[n][1] += y;
+                    if (EIGHT) {
+                        p[i][n][r] = transposed(pack_f16x2(x, y));
+                    } else {
+                        const uint32_t w = pack_bf16x2(x, y);
+                        p[i][n][r] = transposed(w);
+                        rest[i][n][r] = transposed(pack_bf16x2(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u)));
+                    }
+                }
+        }
+    };
+    auto values = [&]() {
+        const uint32_t slot = wait_half();
+        if (EIGHT) {
+            // transposed by pairs of bytes: a register holds two columns of two tokens; even columns make rows 0 .. 7 of
+            // an operand, odd ones rows 8 .. 15
+#pragma unroll
+            for (int c = 0; c < kSteps; c += 2)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t r[4];
+                    ldmatrix4_trans(r, slot + S::place(i * 16 + row8, c + (lane >> 4)));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
+                        const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)x), a1 = e4m3x2_to_f16x2((uint16_t)(x >> 16));
+                        const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)y), a3 = e4m3x2_to_f16x2((uint16_t)(y >> 16));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma<true>(o[c + j][n], a0, a1, a2, a3, p[i][n][0], p[i][n][1]);
+                    }
+                }
+        } else {
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t r[4];
+                    ldmatrix4_trans(r, slot + S::place(i * 16 + odd8, c * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma<false>(o[c][n], r[0], r[1], r[2], r[3], p[i][n][0], p[i][n][1]);
+                        mma<false>(o[c][n], r[0], r[1], r[2], r[3], rest[i][n][0], rest[i][n][1]);
+                    }
+                }
+        }
+    };
+    // the item, or this warp's part of it
+    auto end_segment = [&]() {
+        const Segment& seg = s_seg[warp][begun++ & 7];
+        more = !seg.last;
         const bool whole = seg.u0 == 0 && seg.u1 == seg.n;
         const int which = 2 * warp + (more && !whole ? 0 : 1);
         __syncwarp();  // all lanes have read the ring
@@ -701,8 +669,26 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         } else if (lane == 0) {
             s_part[which] = Part{seg.item, seg.n, seg.kv_head, seg.row, seg.rows};
         }
+    };
+#pragma unroll 1
+    for (int turn = -1; more; ++turn) {
+        __syncwarp();  // the place that is filled now has been read by all lanes
+        if (turn >= 0) ask_keys();
+        const bool work = turn >= S::kAhead;
+        if (work) {
+            if (u == u1) begin_segment();
+            scores();
+        }
+        __syncwarp();
+        if (turn >= 0) copy_half(1);
+        advance();
+        if (work) {
+            values();
+            if (++u == u1) end_segment();
+        }
     }
     pdl_trigger();
+    empty_rows();
 
     // ---- what the warps share: runs of parts of one item
     __syncthreads();
