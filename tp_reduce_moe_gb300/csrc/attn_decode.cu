@@ -52,7 +52,8 @@ struct Shape {
     static constexpr int kHalves = 2 * kAhead + 1;
     static constexpr int kLeast = kHalf >= 4096 ? 1 : 4096 / kHalf;  // units of a warp, while there are SMs left
     static constexpr int kCost = kHalf >= 8192 ? 1 : 8192 / kHalf;   // units that an item counts for besides its own
-    static constexpr int kAlone = 131072 / kHalf;  // units by which a CTA that keeps an item may pass an equal share
+    static constexpr int kMany = (1 << 27) / kHalf;  // units that are too many for all SMs (256 MB)
+    static constexpr int kAlone = 196608 / kHalf;  // units by which a CTA that keeps an item may pass an equal share
     static constexpr int kPitch = D + 4;       // floats from a row of sums to the next in shared memory, free of bank conflicts
     // In memory nothing is between the rows: sectors that are not written whole would have to be read before they are merged.
     static constexpr int kSums = kRows * D;
@@ -255,8 +256,13 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             total = __shfl_sync(0xffffffffu, sum, 31);
             before += __shfl_sync(0xffffffffu, sum, (warp + 31) & 31) * (warp > 0);
         }
-        if ((int64_t)a.B * a.groups <= gridDim.x && (int64_t)(most - S::kAlone) * gridDim.x <= total) {
-            // One CTA an item: nothing to join over CTAs, and no CTA has much more to do than with equal shares.
+        // Three quarters of the SMs draw what the memory gives, with fewer streams in each other's way: 2.4 GB take 360 us from
+        // 114 SMs, 375 from 152; 540 MB take 90 and 92.  134 MB, where each SM's latencies count, take 35 and 33.4, and 8-bit
+        // caches, which each SM has more work with for a byte, take all.
+        const int fewer = max(1, (int)gridDim.x * 3 / 4);
+        if ((int64_t)a.B * a.groups <= gridDim.x && (int64_t)(most - S::kAlone) * fewer <= total) {
+            // One CTA an item: nothing to join over CTAs, and none has much more to do than with equal shares of those.
+            // (128 equal items of 8 bits, 655 MB: 104 us, with equal shares of 152 SMs 114.)
             w_b = blockIdx.x / a.groups;
             w_group = blockIdx.x - w_b * a.groups;
             if (w_b < a.B) sequence();
@@ -268,7 +274,8 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             end = w_n;
         } else {
             // Equal ranges of all units; the last ones may be short or empty.
-            each = max((int64_t)S::kLeast, quotient64(total + gridDim.x * kWarps - 1, gridDim.x * kWarps));
+            const int warps = (!EIGHT && total >= S::kMany ? fewer : (int)gridDim.x) * kWarps;
+            each = max((int64_t)S::kLeast, quotient64(total + warps - 1, warps));
             begin = each * (blockIdx.x * kWarps);
             end = min(total, begin + each * kWarps);
             const int64_t from = begin + each * warp;
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         if (whole) {
             __syncwarp();
             const float vs = EIGHT ? a.v.scale[seg.kv_head] : 1.0f;
-#pragma unroll 1
+#pragma unroll 4
             for (int i = lane; i < seg.rows * (D / 4); i += 32) {
                 const int row = i / (D / 4), d = i % (D / 4) * 4;
                 finish_row(a, seg.row + row, d, D, *reinterpret_cast<const float4*>(to + row * pitch + d), s_l[which][row], vs,
@@ -824,7 +831,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
                     const int count = min(kAtOnce, join.count - k);
                     __syncthreads();  // the parts before have been read
 #pragma unroll 4
-                    for (int i = tid; i < count * kPieces; i += kThreads) {
+                    for (int i = e0 > 0 && join.count <= kAtOnce ? count * kPieces : tid; i < count * kPieces; i += kThreads) {
                         const int j = k + i / kPieces;
                         copy16(smem_addr(smem) + i * 16, (j == 0 ? head : part_of(join.leader + j * join.step, false)) + i % kPieces * 4, policy);
                     }
