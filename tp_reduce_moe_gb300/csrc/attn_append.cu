@@ -58,29 +58,47 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
     __shared__ int s_dead[kMaxTokens];
     __shared__ int64_t s_k[kMaxTokens], s_v[kMaxTokens];  // byte offsets of the tokens' places, -1: none
     __shared__ unsigned s_hash[1 << (kHashBits - 5)];
-    __shared__ float2 s_turn[kTableTokens][kMaxHeadDim / 2];
+    // cosine and sine of a token's pairs 8 p + 2 j and 8 p + 2 j + 1 at [j][p]: neighbouring pieces' in neighbouring banks
+    __shared__ __align__(16) float2 s_turn[kTableTokens][4][kMaxHeadDim / 16][2];
     __shared__ uint4 s_piece[kAhead][2][kThreads];
     pdl_trigger();
     pdl_wait();  // no global memory access before this point
     const int t0 = blockIdx.x * tokens_per_cta, count = min(tokens_per_cta, a.T - t0);
-    const int per_head = a.D / 16, all_heads = a.heads + 2 * a.kv;
+    const int shift = 31 - __clz(a.D / 16), per_head = 1 << shift, all_heads = a.heads + 2 * a.kv;
     // this CTA's pieces of a token
     const int pieces = all_heads * per_head;
     const int first = (int)((int64_t)pieces * blockIdx.y / gridDim.y);
     const int own = (int)((int64_t)pieces * (blockIdx.y + 1) / gridDim.y) - first;
 
-    // a thread's pieces, every kThreads-th of all tokens' one after the other, are asked for ahead of anything else
-    const int total = count * own;
-    int asked = threadIdx.x, slot = 0;
+    // a thread's pieces, every kThreads-th of all tokens' one after the other, are asked for ahead of anything else; one comes
+    // from the one before without a division
+    const int on_t = kThreads / own, on_r = kThreads - on_t * own;
+    struct Place {
+        int t, r;  // token, piece of it
+    };
+    auto follow = [&](Place& x) {
+        x.t += on_t;
+        x.r += on_r;
+        if (x.r >= own) {
+            x.r -= own;
+            ++x.t;
+        }
+    };
+    Place use;
+    use.t = threadIdx.x / own;
+    use.r = threadIdx.x - use.t * own;
+    Place next = use;
+    int slot = 0;
+    const uint16_t* const rows = a.qkv + (int64_t)t0 * all_heads * a.D;
     auto ask = [&](int into) {
-        if (asked < total) {
-            const int t = asked / own, r = first + (asked - t * own), head = r / per_head;
+        if (next.t < count) {
+            const int r = first + next.r, head = r >> shift;
             int lo, hi;
-            chunks_of(r - head * per_head, head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
-            const uint16_t* row = a.qkv + ((int64_t)(t0 + t) * all_heads + head) * a.D;
+            chunks_of(r - (head << shift), head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
+            const uint16_t* row = rows + (next.t * all_heads + head) * a.D;
             copy16(smem_addr(&s_piece[into][0][threadIdx.x]), row + lo * 8);
             copy16(smem_addr(&s_piece[into][1][threadIdx.x]), row + hi * 8);
-            asked += kThreads;
+            follow(next);
         }
         copy_commit();
     };
@@ -131,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
     }
 
     const int pairs = a.rot / 2;
-    int i = threadIdx.x;
+    uint16_t* const out = a.q + (int64_t)t0 * a.heads * a.D;
     for (int b = 0; b < count; b += kTableTokens) {
         const int n = min(kTableTokens, count - b);
         for (int j = threadIdx.x; j < n * pairs; j += kThreads) {
@@ -139,15 +157,15 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
             const double turns = a.positions[(int64_t)a.rope->axis[pair] * a.T + t0 + b + t] * a.rope->turns[pair];
             float s, c;
             sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-            s_turn[t][pair] = make_float2(c, s);
+            s_turn[t][(pair & 7) >> 1][pair >> 3][pair & 1] = make_float2(c, s);
         }
         __syncthreads();
-        for (; i < (b + n) * own; i += kThreads) {
+        for (; use.t < b + n; follow(use)) {
             copy_wait<kAhead - 1>();
             const uint4 x_lo = s_piece[slot][0][threadIdx.x], x_hi = s_piece[slot][1][threadIdx.x];
             ask(slot);
             slot = slot + 1 == kAhead ? 0 : slot + 1;
-            const int t = i / own, r = first + (i - t * own), head = r / per_head, p = r - head * per_head;
+            const int t = use.t, r = first + use.r, head = r >> shift, p = r - (head << shift);
             const bool turned = head < a.heads + a.kv && p < a.rot / 16;
             int lo, hi;
             chunks_of(p, head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
@@ -155,7 +173,10 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
             bf16x8_to_f32(x_lo, u);
             bf16x8_to_f32(x_hi, v);
             if (turned) {
-                const float2* table = s_turn[t - b] + p * 8;
+                float2 table[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<float4*>(table + 2 * j) = *reinterpret_cast<const float4*>(s_turn[t - b][j][p]);
                 if (a.interleaved) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -177,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
                 }
             }
             if (head < a.heads) {
-                uint16_t* row = a.q + ((int64_t)(t0 + t) * a.heads + head) * a.D;
+                uint16_t* row = out + (t * a.heads + head) * a.D;
                 st_global16(row + lo * 8, f32x8_to_bf16x8(u));
                 st_global16(row + hi * 8, f32x8_to_bf16x8(v));
                 continue;
