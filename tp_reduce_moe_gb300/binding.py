@@ -1,15 +1,21 @@
-"""Thin ctypes binding of libarfuse (include/arfuse.h): argument marshalling only.
+"""Thin binding of libarfuse (include/arfuse.h): argument marshalling only.
 
 Every step of the operator runs in the CUDA library; this module turns torch
 tensors into device pointers and sizes, checks that their shapes agree with
 the sizes passed (the C ABI sees only pointers), and raises on any status
 other than AR_OK.  There is no CPU path: if the library is missing, loading it
 raises.
+
+Calls go through ctypes.  The attention's and the 8-bit norm's, which are
+shorter than that takes, go through a native module (csrc/marshal.cpp) that
+makes the same checks; what it does not take is checked again here, for the
+error's sake.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 import weakref
@@ -62,6 +68,8 @@ AR_MAX_ROPE_AXES = 4
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None  # the native module, loaded with the library
+_ANYWHERE = -2  # device of a dry run's tensors, which are only looked at
 
 
 class ArfuseError(RuntimeError):
@@ -157,8 +165,24 @@ def load_library(path: str | None = None):
         lib.ar_attn_decode.argtypes = [P, P, P, P, I64, I64, P, I64, I64, F, P, P, P]
         lib.ar_status_string.restype = ctypes.c_char_p
         lib.ar_status_string.argtypes = [I]
+        _load_marshal(lib)
         _lib = lib
         return lib
+
+
+def _load_marshal(lib):
+    """Load the native module (built beside the library) and give it the library's functions."""
+    global _marshal
+    from .build import marshal_path
+    p = marshal_path()
+    if not os.path.exists(p):
+        raise RuntimeError(f"{os.path.basename(p)} not found in {os.path.dirname(p)}; build it first "
+                           "(python -c 'import __graft_entry__ as g; g.build()')")
+    loader = importlib.machinery.ExtensionFileLoader("_marshal", p)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", p, loader=loader))
+    loader.exec_module(m)
+    m.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (lib.ar_rmsnorm_q8, lib.ar_attn_append, lib.ar_attn_decode)])
+    _marshal = m
 
 
 def ar_status_string(status: int) -> str:
@@ -375,12 +399,6 @@ def _ptr_array(ts):
     return (ctypes.c_void_p * len(ts))(*[t if isinstance(t, int) else t.data_ptr() for t in ts])
 
 
-@functools.lru_cache(maxsize=None)
-def _pointers(n: int):
-    """The type of an array of n pointers."""
-    return ctypes.c_void_p * n
-
-
 def _stream_handle(stream, device) -> int:
     if stream is None:
         index = device if isinstance(device, int) else getattr(device, "index", None)
@@ -497,45 +515,37 @@ def ar_rmsnorm_q8(ws: Workspace, partials, residual, gamma, weight_bias: float, 
     normalised rows q * scale.  ``out`` (bf16 [T, H]), when given, receives them unscaled
     as well.  ``residual_out`` may be ``residual`` (in place, bf16 only).  Returns (q,
     scales, residual_out), allocated when not given."""
+    if _lib is None:
+        load_library()
     R, H, T = ws.R, ws.H, residual.shape[0]
-    # (a dry run only looks at addresses: any device, one for all)
-    dev, bf16, rows = residual.get_device() if ws.dry_run else ws.device, torch.bfloat16, (T, H)
     if len(partials) != R:
         raise ValueError(f"partials has {len(partials)} entries, workspace has R={R}")
     if group not in (0, 32, 64, 128):
         raise ArfuseError(AR_ERR_UNSUPPORTED, f"group {group} (0, 32, 64 or 128)")
-    # (checked here and not by a function: a call for each tensor costs more than the rest of a small call)
-    for r, p in enumerate(partials):
-        if p.dtype is not bf16 or p.shape != rows or not p.is_contiguous() or p.get_device() != dev:
-            _need_on(dev, p, bf16, rows, "partials", r)
-    if residual.dtype is not bf16 or residual.shape != rows or not residual.is_contiguous() or residual.get_device() != dev:
-        _need_on(dev, residual, bf16, rows, "residual")
-    if gamma.dtype is not bf16 or gamma.shape != (H,) or not gamma.is_contiguous() or gamma.get_device() != dev:
-        _need_on(dev, gamma, bf16, (H,), "gamma")
-    res_type = torch.float32 if residual_out_fp32 else bf16
+    res_type = torch.float32 if residual_out_fp32 else torch.bfloat16
     shape = (T, -(-H // group) if group else 1)
     if q is None:
-        q = torch.empty(rows, dtype=torch.float8_e4m3fn, device=residual.device)
-    elif q.dtype is not torch.float8_e4m3fn or q.shape != rows or not q.is_contiguous() or q.get_device() != dev:
-        _need_on(dev, q, torch.float8_e4m3fn, rows, "q")
+        q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=residual.device)
     if scales is None:
         scales = torch.empty(shape, dtype=torch.float32, device=residual.device)
-    elif scales.dtype is not torch.float32 or scales.shape != shape or not scales.is_contiguous() or scales.get_device() != dev:
-        _need_on(dev, scales, torch.float32, shape, "scales")
     if residual_out is None:
-        residual_out = torch.empty(rows, dtype=res_type, device=residual.device)
-    elif residual_out.dtype is not res_type or residual_out.shape != rows or not residual_out.is_contiguous() or (
-            residual_out.get_device() != dev):
-        _need_on(dev, residual_out, res_type, rows, "residual_out")
-    if out is not None:
-        _need_on(dev, out, bf16, rows, "out")
-    p_arr = _pointers(R)(*[p.data_ptr() for p in partials])
-    st = (_lib or load_library()).ar_rmsnorm_q8(
-        ws.handle if ws.alive else None, p_arr, R, residual.data_ptr(), gamma.data_ptr(), weight_bias, eps, T, H, group,
-        q.data_ptr(), scales.data_ptr(), None if out is None else out.data_ptr(), residual_out.data_ptr(),
-        1 if residual_out_fp32 else 0, None if ws.dry_run else _stream_handle(stream, dev))
+        residual_out = torch.empty((T, H), dtype=res_type, device=residual.device)
+    dry = ws.dry_run
+    st = _marshal.rmsnorm_q8(ws.handle if ws.alive else None, R, H, _ANYWHERE if dry else ws.device,
+                             partials if type(partials) is list else list(partials), residual, gamma, weight_bias, eps, group, q,
+                             scales, out, residual_out, residual_out_fp32, None if dry else _stream_handle(stream, ws.device))
+    if st is None:
+        dev = None if dry else ws.device
+        for r, p in enumerate(partials):
+            _need_on(dev, p, torch.bfloat16, (T, H), "partials", r)
+        for t, dtype, size, name in ((residual, torch.bfloat16, (T, H), "residual"), (gamma, torch.bfloat16, (H,), "gamma"),
+                                     (q, torch.float8_e4m3fn, (T, H), "q"), (scales, torch.float32, shape, "scales"),
+                                     (residual_out, res_type, (T, H), "residual_out"), (out, torch.bfloat16, (T, H), "out")):
+            if t is not None:
+                _need_on(dev, t, dtype, size, name)
+        raise TypeError("ar_rmsnorm_q8: plain strided tensors expected")
     if st != AR_OK:
-        _check(st, "ar_rmsnorm_q8", ok=(AR_VALIDATED,) if ws.dry_run else ())
+        _check(st, "ar_rmsnorm_q8", ok=(AR_VALIDATED,) if dry else ())
     return q, scales, residual_out
 
 
@@ -880,13 +890,13 @@ def ar_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
     return KvCache(k, v, k_scale, v_scale)
 
 
-def _need_cache(attn, cache, dev):
+def _need_cache(attn, cache):
     pages, size, kv, dim = cache.shape
-    if (size, kv, dim) != (attn.page_size, attn.kv_heads, attn.head_dim):
+    if (size, kv, dim) != attn.cache_shape:
         raise ValueError(f"cache: pages of {size} tokens, {kv} heads of {dim}, expected {attn.page_size}, {attn.kv_heads}, "
                          f"{attn.head_dim}")
-    if cache.device != dev:
-        raise ValueError(f"cache: on {cache.k.device}, expected cuda:{dev}")
+    if not attn.dry_run and cache.device != attn.device:
+        raise ValueError(f"cache: on {cache.k.device}, expected cuda:{attn.device}")
 
 
 def ar_attn_append(attn: Attn, cache: KvCache, qkv, positions, slots, q=None, stream=None):
@@ -896,31 +906,26 @@ def ar_attn_append(attn: Attn, cache: KvCache, qkv, positions, slots, q=None, st
     (or [T] with one axis; ignored, and may be None, without rotary positions); slots: int32 [T], page * page_size +
     token in the page, -1: not written; of tokens with one slot the last stands.  Returns q (bf16 [T, heads, head_dim]),
     allocated when not given."""
-    T, dev = qkv.shape[0], qkv.get_device() if attn.dry_run else attn.device
-    if cache.shape[1:] != attn.cache_shape or cache.device != dev:
-        _need_cache(attn, cache, dev)
-    if qkv.dtype is not torch.bfloat16 or qkv.shape != (T, attn.qkv_cols) or not qkv.is_contiguous() or qkv.get_device() != dev:
-        _need_on(dev, qkv, torch.bfloat16, (T, attn.qkv_cols), "qkv")
-    if attn.axes:
-        if positions is None:
-            raise ValueError("positions: rotary positions are set")
-        if positions.dtype is not torch.int32 or positions.shape != (attn.axes, T) or not positions.is_contiguous() or (
-                positions.get_device() != dev):
-            _need_on(dev, positions, torch.int32, (T,) if attn.axes == 1 and positions.dim() == 1 else (attn.axes, T), "positions")
-    else:
-        positions = None
-    if slots.dtype is not torch.int32 or slots.shape != (T,) or not slots.is_contiguous() or slots.get_device() != dev:
-        _need_on(dev, slots, torch.int32, (T,), "slots")
+    if cache.shape[1:] != attn.cache_shape or cache.device != attn.device:
+        _need_cache(attn, cache)
+    T, dry = qkv.shape[0], attn.dry_run
     shape = (T, attn.heads, attn.head_dim)
     if q is None:
         q = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
-    elif q.dtype is not torch.bfloat16 or q.shape != shape or not q.is_contiguous() or q.get_device() != dev:
+    st = _marshal.attn_append(attn.handle, cache._ref, _ANYWHERE if dry else attn.device, attn.heads, attn.qkv_cols, attn.head_dim,
+                              attn.axes, qkv, positions, slots, q, None if dry else _stream_handle(stream, attn.device))
+    if st is None:
+        dev = _moe_device(attn)
+        _need_on(dev, qkv, torch.bfloat16, (T, attn.qkv_cols), "qkv")
+        if attn.axes:
+            if positions is None:
+                raise ValueError("positions: rotary positions are set")
+            _need_on(dev, positions, torch.int32, (T,) if attn.axes == 1 and positions.dim() == 1 else (attn.axes, T), "positions")
+        _need_on(dev, slots, torch.int32, (T,), "slots")
         _need_on(dev, q, torch.bfloat16, shape, "q")
-    st = (_lib or load_library()).ar_attn_append(
-        attn.handle, cache._ref, qkv.data_ptr(), None if positions is None else positions.data_ptr(), slots.data_ptr(), T,
-        q.data_ptr(), None if attn.dry_run else _stream_handle(stream, dev))
+        raise TypeError("ar_attn_append: plain strided tensors expected")
     if st != AR_OK:
-        _check(st, "ar_attn_append", ok=(AR_VALIDATED,) if attn.dry_run else ())
+        _check(st, "ar_attn_append", ok=(AR_VALIDATED,) if dry else ())
     return q
 
 
@@ -932,33 +937,29 @@ def ar_attn_decode(attn: Attn, cache: KvCache, q, page_table, lengths, scale: fl
     q: bf16 [B, heads, head_dim]; page_table: int32 [B, width], the page of a sequence's tokens i * page_size and on
     (rows may be further apart); lengths: int32 [B], 0: zeros.  Returns out (bf16 [B, heads, head_dim], allocated when not
     given), or (out, lse) when ``lse`` (fp32 [B, heads]: log of the sum of the scores' exponentials) is given."""
-    B, dev = q.shape[0], q.get_device() if attn.dry_run else attn.device
-    if cache.shape[1:] != attn.cache_shape or cache.device != dev:
-        _need_cache(attn, cache, dev)
-    shape = (B, attn.heads, attn.head_dim)
-    if q.dtype is not torch.bfloat16 or q.shape != shape or not q.is_contiguous() or q.get_device() != dev:
-        _need_on(dev, q, torch.bfloat16, shape, "q")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected ({B}, width)")
-    width, apart = page_table.shape[1], page_table.stride(0)
-    if B <= 1 or width == 0:
-        apart = width
-    if page_table.dtype is not torch.int32 or apart < width or (width > 1 and page_table.stride(1) != 1) or (
-            page_table.get_device() != dev):
-        _need_on(dev, page_table, torch.int32, (B, width), "page_table")
-    if lengths.dtype is not torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous() or lengths.get_device() != dev:
-        _need_on(dev, lengths, torch.int32, (B,), "lengths")
+    if cache.shape[1:] != attn.cache_shape or cache.device != attn.device:
+        _need_cache(attn, cache)
+    dry = attn.dry_run
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    elif out.dtype is not torch.bfloat16 or out.shape != shape or not out.is_contiguous() or out.get_device() != dev:
+        out = torch.empty((q.shape[0], attn.heads, attn.head_dim), dtype=torch.bfloat16, device=q.device)
+    st = _marshal.attn_decode(attn.handle, cache._ref, _ANYWHERE if dry else attn.device, attn.heads, attn.head_dim, q, page_table,
+                              lengths, attn.head_dim ** -0.5 if scale is None else scale, window, out, lse,
+                              None if dry else _stream_handle(stream, attn.device))
+    if st is None:
+        dev, B = _moe_device(attn), q.shape[0]
+        shape = (B, attn.heads, attn.head_dim)
+        _need_on(dev, q, torch.bfloat16, shape, "q")
+        if page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected ({B}, width)")
+        if page_table.dtype != torch.int32:
+            raise TypeError(f"page_table: dtype {page_table.dtype}, expected {torch.int32}")
+        if dev is not None and page_table.get_device() != dev:
+            raise ValueError(f"page_table: on {page_table.device}, expected cuda:{dev}")
+        _need_on(dev, lengths, torch.int32, (B,), "lengths")
         _need_on(dev, out, torch.bfloat16, shape, "out")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, attn.heads) or not lse.is_contiguous() or
-                            lse.get_device() != dev):
-        _need_on(dev, lse, torch.float32, (B, attn.heads), "lse")
-    st = (_lib or load_library()).ar_attn_decode(
-        attn.handle, cache._ref, q.data_ptr(), page_table.data_ptr() if width else None, width, apart, lengths.data_ptr(), B,
-        window, attn.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if attn.dry_run else _stream_handle(stream, dev))
+        if lse is not None:
+            _need_on(dev, lse, torch.float32, (B, attn.heads), "lse")
+        raise ValueError("page_table: the entries of a row must be contiguous, and rows must not overlap")
     if st != AR_OK:
-        _check(st, "ar_attn_decode", ok=(AR_VALIDATED,) if attn.dry_run else ())
+        _check(st, "ar_attn_decode", ok=(AR_VALIDATED,) if dry else ())
     return out if lse is None else (out, lse)

@@ -2,14 +2,19 @@
 
 Each translation unit compiles in parallel; the shared library links the CUDA
 runtime statically so it does not depend on which libcudart the host process
-loaded.  Output: ``tp_reduce_moe_gb300/lib/libarfuse.so`` (git-ignored).
+loaded.  Output: ``tp_reduce_moe_gb300/lib/libarfuse.so`` (git-ignored), and
+beside it ``_marshal.<torch version>.so``, the binding's native module (host
+code, compiled against the installed torch's headers).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -32,6 +37,26 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libarfuse")
+
+
+def torch_paths() -> tuple[str, str]:
+    """torch's folder and version (without importing it)."""
+    root = importlib.util.find_spec("torch").submodule_search_locations[0]
+    with open(os.path.join(root, "version.py")) as f:
+        version = re.search(r"__version__ = '([^']+)'", f.read()).group(1)
+    return root, version
+
+
+def marshal_path() -> str:
+    return os.path.join(LIBDIR, f"_marshal.{torch_paths()[1]}.so")
+
+
+def _marshal_command(target: str) -> list[str]:
+    root, _ = torch_paths()
+    return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            os.path.join(CSRC, "marshal.cpp"), "-o", target, "-L", os.path.join(root, "lib"), "-ltorch_python", "-lc10"]
 
 
 def _stale(target: str, deps) -> bool:
@@ -60,6 +85,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                 stderr=subprocess.STDOUT, text=True)))
+    marshal = marshal_path()
+    marshal_tmp = marshal + f".tmp{os.getpid()}"
+    remade = force or _stale(marshal, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "arfuse.h")])
+    if remade:
+        procs.append(("marshal.cpp", subprocess.Popen(_marshal_command(marshal_tmp), stdout=subprocess.PIPE,
+                                                      stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -68,8 +99,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if p.returncode:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed on {failed}")
-    if force or procs or _stale(LIB, objs):
+        raise RuntimeError(f"the compiler failed on {failed}")
+    if remade:
+        os.replace(marshal_tmp, marshal)
+    if _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
         subprocess.run(cmd, check=True)
