@@ -59,7 +59,7 @@ struct Shape {
     static constexpr int kSums = kRows * D;
     static constexpr int kPart = kSums + 2 * kRows;  // a CTA's part: sums, maxima, sums of weights
     static constexpr int kSmem = kWarps * kRing;
-    static_assert(kSmem + 16384 <= 232448, "shared memory of a CTA");
+    static_assert(kSmem + 26624 <= 232448, "shared memory of a CTA");
     static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums, in its ring");
     static_assert(kAhead >= 1 && kAhead + 2 <= 8, "units that are asked for and not used, of the eight masks and segments that are kept");
     static_assert(kPart % 4 == 0 && kSmem >= kPart * 4, "parts come by 16 bytes");
@@ -201,8 +201,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     __shared__ int s_run[2 * kWarps];
     __shared__ int64_t s_scan[kWarps];
     __shared__ int s_most[kWarps];
-    __shared__ int64_t s_first[kWarps];  // units of the found sequence before the warp's first
-    __shared__ int s_b[kWarps];
+    __shared__ int64_t s_before[kThreads];  // units before a thread's sequences
     __shared__ Join s_join[2];
     __shared__ unsigned s_mask[kWarps][8];
     __shared__ Segment s_seg[kWarps][8];
@@ -286,22 +285,18 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
                 w_b = at ? __ffs(at) - 1 : 0;
                 skip = from - __shfl_sync(0xffffffffu, before, w_b);
             } else {
-#pragma unroll 1
-                for (int w = 0; w < kWarps; ++w) {  // whose first unit is here?
-                    const int64_t first = begin + each * w;
-                    if (before <= first && first < before + mine) {
-                        int b = b0;
-                        int64_t rest = first - before;
-                        if (per_thread > 1)
-#pragma unroll 1
-                            for (int64_t n; (n = (int64_t)units(b) * a.groups) <= rest; ++b) rest -= n;
-                        s_b[w] = b;
-                        s_first[w] = rest;
-                    }
-                }
+                // the last thread whose sequences begin at or before this warp's first unit: of each so many, then among them
+                constexpr int kEach = kThreads / 32;
+                s_before[tid] = before;
                 __syncthreads();
-                w_b = s_b[warp];
-                skip = s_first[warp];
+                const int block = __popc(__ballot_sync(0xffffffffu, s_before[lane * kEach] <= from)) - 1;
+                const unsigned upto = __ballot_sync(0xffffffffu, lane < kEach && s_before[block * kEach + lane % kEach] <= from);
+                const int thread = block * kEach + __popc(upto) - 1;
+                w_b = thread * per_thread;
+                skip = from - s_before[thread];
+                if (per_thread > 1 && w_left > 0)
+#pragma unroll 1
+                    for (int64_t n; (n = (int64_t)units(w_b) * a.groups) <= skip; ++w_b) skip -= n;
             }
             if (w_left > 0) {
                 sequence();
@@ -715,6 +710,23 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     // a CTA's part of an item: one for an item that began in a range before, one for an item that begins in this one
     auto part_of = [&](int cta, bool begins) { return a.part + ((int64_t)cta * 2 + (begins ? 1 : 0)) * S::kPart; };
 
+    // items that this CTA shares with others: perhaps its first with those before it, and its last with those behind it
+    auto owner = [&](int64_t unit) { return (int)quotient64(unit, each * kWarps); };
+    if (tid >= kThreads - 2) {  // (of the last warp, the others have more to do)
+        const int which = tid - (kThreads - 2);
+        const Part p = s_part[which == 0 ? __ffs(start_mask) - 1 : 31 - __clz(start_mask)];
+        Join j{0, 0, 0, 0, 0, 0};
+        if ((which == 0 || runs > 1) && !(p.item >= begin && p.item + p.n <= end)) {
+            j.first = owner(p.item);
+            j.parts = owner(p.item + p.n - 1) - j.first + 1;
+            j.fan = j.parts;
+            if (j.parts > kFew)
+                for (j.fan = 5; j.fan * j.fan < j.parts;) ++j.fan;
+            j.step = 1;
+        }
+        s_join[which] = j;
+    }
+
     // what each part counts, and the runs' maxima and weights: a lane a part, a warp a row
     {
         const int first = start_mask & ((2u << lane) - 1) ? 31 - __clz(start_mask & ((2u << lane) - 1)) : 0;  // of this lane's run
@@ -774,22 +786,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     }
 
     // ---- what CTAs share: the last of them to arrive adds up their parts; of many parts the last of each few, and the last
-    // of those.  (One SM reads some 60 GB/s: 76 parts of 4 KB take it 5 us, nine and nine of their sums 1.2.)  A CTA may
-    // share its first item with the CTAs before it, and its last with those behind it.
-    auto owner = [&](int64_t unit) { return (int)quotient64(unit, each * kWarps); };
-    if (tid < 2) {
-        const Part p = s_part[s_run[tid == 0 ? 0 : runs - 1]];
-        Join j{0, 0, 0, 0, 0, 0};
-        if ((tid == 0 || runs > 1) && !(p.item >= begin && p.item + p.n <= end)) {
-            j.first = owner(p.item);
-            j.parts = owner(p.item + p.n - 1) - j.first + 1;
-            j.fan = j.parts;
-            if (j.parts > kFew)
-                for (j.fan = 5; j.fan * j.fan < j.parts;) ++j.fan;
-            j.step = 1;
-        }
-        s_join[tid] = j;
-    }
+    // of those.  (One SM reads some 60 GB/s: 76 parts of 4 KB take it 5 us, nine and nine of their sums 1.2.)
 #pragma unroll 1
     for (int level = 0; level < 2; ++level) {
         __syncthreads();
