@@ -48,6 +48,12 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return v;
 }
 
+__device__ __forceinline__ float reciprocal(float x) {  // to a last place
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // The scale of values up to `top`: 1 for a group of zeros, and never subnormal, so that its inverse is finite.
 __device__ __forceinline__ float scale_of(float top) {
     return top == 0.0f ? 1.0f : max_nan(top * (1.0f / kE4m3Max), 0x1p-126f);
@@ -69,25 +75,33 @@ __device__ __forceinline__ void add8(float h[8], uint4 v) {
     for (int j = 0; j < 8; ++j) h[j] += f[j];
 }
 
-// Everything behind the sum: h [CPT chunks of this thread], which is used up.  s_sum and s_top are not written again before
-// all threads have come through a barrier behind this.  GROUP_LANES: lanes of eight columns that share a scale; 0: the row.
+// Everything behind the sum: h [CPT chunks of this thread], which is used up; of chunks behind the row it may be anything.
+// s_sum and s_top are not written again before all threads have come through a barrier behind this.  GROUP_LANES: lanes of
+// eight columns that share a scale; 0: the row.
 template <int CPT, int GROUP_LANES, bool RES_F32>
 __device__ __forceinline__ void finish_row(const NormQ8Args& a, int64_t t, float h[CPT][8], const uint4 gamma[CPT], float* s_sum, float* s_top) {
     const int chunks = a.H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool full = chunks == CPT * (int)blockDim.x;  // every thread's chunks are columns
     float sum = 0.0f, top = 0.0f;
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
         const int chunk = threadIdx.x + c * blockDim.x;
-        if (chunk < chunks) store_residual8<RES_F32>(a.residual_out, t * a.H + chunk * 8, h[c]);
+        if (full || chunk < chunks)
+            store_residual8<RES_F32>(a.residual_out, t * a.H + chunk * 8, h[c]);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[c][j] = 0.0f;
         float g[8];
         bf16x8_to_f32(gamma[c], g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float x = norm_input(h[c][j], a.norm_bf16_h);
             sum = fmaf(x, x, sum);
-            h[c][j] = chunk < chunks ? x * (g[j] + a.weight_bias) : 0.0f;
-            if (GROUP_LANES == 0) top = max_nan(top, fabsf(h[c][j]));
+            h[c][j] = x * (g[j] + a.weight_bias);
         }
+        if (GROUP_LANES == 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(h[c][j]));
     }
     sum = warp_sum(sum);
     if (GROUP_LANES == 0)
@@ -100,7 +114,7 @@ __device__ __forceinline__ void finish_row(const NormQ8Args& a, int64_t t, float
     __syncthreads();
     const int warps = blockDim.x >> 5;
     sum = warp_sum(lane < warps ? s_sum[lane] : 0.0f);
-    const float rs = rsqrtf(sum / (float)a.H + a.eps);
+    const float rs = rsqrtf(sum * reciprocal((float)a.H) + a.eps);
     if (GROUP_LANES == 0) {
         top = lane < warps ? s_top[lane] : 0.0f;
 #pragma unroll
@@ -125,7 +139,7 @@ __device__ __forceinline__ void finish_row(const NormQ8Args& a, int64_t t, float
             for (int o = GROUP_LANES / 2; o > 0; o >>= 1) largest = max_nan(largest, __shfl_xor_sync(0xffffffffu, largest, o));
         }
         if (chunk >= chunks) continue;
-        const float s = scale_of(largest), inv = 1.0f / s;
+        const float s = scale_of(largest), inv = reciprocal(s);
         if (a.out != nullptr) st_global16(a.out + t * a.H + chunk * 8, f32x8_to_bf16x8(h[c]));
         uint2 q;
         q.x = e4m3x2(h[c][0] * inv, h[c][1] * inv) | e4m3x2(h[c][2] * inv, h[c][3] * inv) << 16;
@@ -189,20 +203,21 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_q8_stream_kernel(const _
         const int chunk = threadIdx.x + c * blockDim.x;
         gamma[c] = chunk < chunks ? *reinterpret_cast<const uint4*>(a.gamma + chunk * 8) : make_uint4(0, 0, 0, 0);
     }
-    int64_t ask_t = blockIdx.x;
+    int64_t ask_at = (int64_t)blockIdx.x * a.H + threadIdx.x * 8;  // in a partial, of the thread's first chunk
+    const int64_t behind = a.T * a.H, further = (int64_t)gridDim.x * a.H;
     int ask_r = 0;
     uint4* const mine = s_ring + threadIdx.x;
+    const uint32_t mine_at = smem_addr(mine);
+    const bool any = (int)threadIdx.x < chunks, second = (int)(threadIdx.x + blockDim.x) < chunks;
     auto ask = [&](int place) {
-        if (ask_t < a.T) {
-            const uint16_t* row = (ask_r < a.R ? a.P[ask_r] : a.residual) + ask_t * a.H;
-#pragma unroll
-            for (int c = 0; c < CPT; ++c) {
-                const int chunk = threadIdx.x + c * blockDim.x;
-                if (chunk < chunks) copy16(smem_addr(mine + (place * CPT + c) * blockDim.x), row + chunk * 8, policy);
-            }
+        if (ask_at < behind) {
+            const uint16_t* from = (ask_r < a.R ? a.P[ask_r] : a.residual) + ask_at;
+            const uint32_t to = mine_at + place * CPT * blockDim.x * 16;
+            if (any) copy16(to, from, policy);
+            if (CPT == 2 && second) copy16(to + blockDim.x * 16, from + blockDim.x * 8, policy);
             if (++ask_r > a.R) {
                 ask_r = 0;
-                ask_t += gridDim.x;
+                ask_at += further;
             }
         }
         copy_commit();
@@ -221,10 +236,9 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_q8_stream_kernel(const _
             copy_wait<kPlaces - 1>();
             uint4 v[CPT];
 #pragma unroll
-            for (int c = 0; c < CPT; ++c) v[c] = mine[(place * CPT + c) * blockDim.x];  // (not there: not used)
+            for (int c = 0; c < CPT; ++c) v[c] = mine[(place * CPT + c) * blockDim.x];
 #pragma unroll
-            for (int c = 0; c < CPT; ++c)
-                if (threadIdx.x + c * blockDim.x < chunks) add8(h[c], v[c]);
+            for (int c = 0; c < CPT; ++c) add8(h[c], v[c]);  // (of chunks behind the row: anything, not used)
             ask(place);  // (a thread reads before it copies over)
             place = place + 1 == kPlaces ? 0 : place + 1;
         }
