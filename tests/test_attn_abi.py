@@ -319,3 +319,40 @@ def test_norm_q8_python_checks(ws):
     assert e.value.status == arf.AR_ERR_UNSUPPORTED
     with pytest.raises(TypeError, match=r"partials\[1\]"):
         arf.ar_rmsnorm_q8(ws, [parts[0], parts[1].float()], res, gamma, 0.0, EPS)
+
+
+# --------------------------------------------------------------------- tensors without a place in memory, calls without work
+def test_tensors_that_have_no_memory(attn, ws):
+    # their addresses cannot be asked for: an error of Python's, with nothing called
+    mode = pytest.importorskip("torch._subclasses.fake_tensor").FakeTensorMode()
+    T, cols = 3, (HEADS + 2 * KV) * D
+    c = arf.ar_kv_cache(torch.zeros(PAGES, PAGE, KV, D).bfloat16(), torch.zeros(PAGES, PAGE, KV, D).bfloat16())
+    new = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
+    with mode:
+        fake_q, fake_qkv, fake_res = torch.zeros(T, HEADS, D).bfloat16(), torch.zeros(T, cols).bfloat16(), torch.zeros(T, H).bfloat16()
+    table, ints = new(T, 4, dtype=torch.int32), new(T, dtype=torch.int32)
+    out = new(T, HEADS, D)
+    refused = (arf.ArfuseError, TypeError, ValueError, RuntimeError)
+    with pytest.raises(refused):
+        arf.ar_attn_decode(attn, c, fake_q, table, ints, out=out)
+    with pytest.raises(refused):
+        arf.ar_attn_append(attn, c, fake_qkv, None, ints, q=out)
+    with pytest.raises(refused):
+        arf.ar_attn_append(attn, c, new(T, cols).to_sparse(), None, ints, q=out)
+    nested = torch.nested.nested_tensor([new(H), new(H), new(H - 8)])
+    for parts, res in (([new(T, H), new(T, H)], fake_res), ([new(T, H), nested], new(T, H))):
+        with pytest.raises(refused):
+            arf.ar_rmsnorm_q8(ws, parts, res, new(H), 0.0, EPS, q=new(T, H, dtype=torch.float8_e4m3fn),
+                              scales=new(T, 8, dtype=torch.float32), residual_out=new(T, H))
+
+
+def test_calls_without_work(attn, ws):
+    new = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
+    c = arf.ar_kv_cache(new(PAGES, PAGE, KV, D), new(PAGES, PAGE, KV, D))
+    none = new(0, dtype=torch.int32)
+    assert arf.ar_attn_append(attn, c, new(0, (HEADS + 2 * KV) * D), None, none).shape == (0, HEADS, D)
+    assert arf.ar_attn_decode(attn, c, new(0, HEADS, D), new(0, 4, dtype=torch.int32), none).shape == (0, HEADS, D)
+    # no page of any sequence is named: its length can only be 0
+    assert arf.ar_attn_decode(attn, c, new(2, HEADS, D), new(2, 0, dtype=torch.int32), new(2, dtype=torch.int32)).shape == (2, HEADS, D)
+    q, scales, h = arf.ar_rmsnorm_q8(ws, [new(0, H), new(0, H)], new(0, H), new(H), 0.0, EPS)
+    assert q.shape == h.shape == (0, H) and scales.shape == (0, 8)

@@ -141,11 +141,22 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return none();
 }
 
+// Tensors without plain sizes or memory (nested ones, those of traces) throw when they are asked: they are not what a call
+// takes either.
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) noexcept {
+    try {
+        return F(self, a, n);
+    } catch (...) {
+        return none();
+    }
+}
+
 PyMethodDef g_methods[] = {
     {"bind", (PyCFunction)(void*)bind, METH_FASTCALL, nullptr},
-    {"rmsnorm_q8", (PyCFunction)(void*)rmsnorm_q8, METH_FASTCALL, nullptr},
-    {"attn_append", (PyCFunction)(void*)attn_append, METH_FASTCALL, nullptr},
-    {"attn_decode", (PyCFunction)(void*)attn_decode, METH_FASTCALL, nullptr},
+    {"rmsnorm_q8", (PyCFunction)(void*)guarded<rmsnorm_q8>, METH_FASTCALL, nullptr},
+    {"attn_append", (PyCFunction)(void*)guarded<attn_append>, METH_FASTCALL, nullptr},
+    {"attn_decode", (PyCFunction)(void*)guarded<attn_decode>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
