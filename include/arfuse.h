@@ -823,8 +823,9 @@ ARFUSE_API ar_status ar_attn_append(ar_attn* attn, const ar_kv_cache* cache, con
  *   scale       finite, also times log2(e); 1 / sqrt(head_dim) as a rule
  *   out         device bf16 [B, heads * head_dim]
  *   lse         device fp32 [B, heads], or NULL
- * Values of the cache outside the tokens looked at may be anything.  Sums and the
- * softmax are fp32; deterministic for given lengths and GPU; the order of a sum may
+ * Values of the cache outside the tokens looked at may be anything.  A score of
+ * minus infinity counts as no token, a row of nothing else as one without tokens.
+ * Sums and the softmax are fp32; deterministic for given lengths and GPU; the order of a sum may
  * depend on the other sequences of the batch.  One launch; the split of the work
  * over the SMs follows the lengths on the device, so a captured call serves any.
  * Errors as for ar_attn_append, and AR_ERR_CAPACITY (B > max_seqs); page_table and

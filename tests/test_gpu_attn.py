@@ -150,6 +150,83 @@ def test_decode_many_sequences(B):
 
 
 @pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("B", [1, 18, 19, 20, 38])
+def test_decode_equal_lengths(B, eight):
+    # items that have a CTA each, up to all SMs, and more of them than SMs
+    heads, kv, D, page, n = 16, 8, 64, 16, 700
+    g = gen(300 + B)
+    pages = B * -(-n // page) + 1
+    k, v, ks, vs = paged(pages, page, kv, D, eight, "head", g)
+    m = arf.ar_attn_create(heads, kv, D, page, B, device=0)
+    check_decode(m, normal((B, heads, D), g), k, v, ks, vs, tables([n] * B, page, pages, 50, g), [n] * B)
+    m.destroy()
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_decode_much_work(eight):
+    # 400 MB of keys and values to stream (from pages that sequences share): more than all SMs take for two bytes
+    heads, kv, D, page, B = 12, 4, 64, 16, 256
+    g = gen(29)
+    k, v, ks, vs = paged(400, page, kv, D, eight, "token", g)
+    lengths = [(b * 577) % 3200 for b in range(B)]
+    assert sum(lengths) * kv * D * 2 * (1 if eight else 2) > (200 << 20 if eight else 400 << 20)
+    table = torch.randint(0, 400, (B, 200), generator=g, device=DEV, dtype=torch.int32)
+    m = arf.ar_attn_create(heads, kv, D, page, B, device=0)
+    check_decode(m, normal((B, heads, D), g), k, v, ks, vs, table, lengths)
+    assert arf.ar_attn_device_error(m) == 0
+    m.destroy()
+
+
+def test_decode_without_work():
+    heads, kv, D, page = 8, 2, 128, 16
+    g = gen(31)
+    k, v, _, _ = paged(3, page, kv, D, False, "token", g)
+    cache = arf.ar_kv_cache(k, v)
+    m = arf.ar_attn_create(heads, kv, D, page, 4096, device=0)
+    for B, width in ((0, 4), (3, 0), (1, 0), (4096, 0), (33, 2)):
+        lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+        out, ok1 = guarded((B, heads, D), torch.bfloat16)
+        lse, ok2 = guarded((B, heads), torch.float32)
+        out.fill_(5), lse.fill_(5)
+        arf.ar_attn_decode(m, cache, normal((B, heads, D), g), torch.full((B, width), -1, dtype=torch.int32, device=DEV), lens, out=out, lse=lse)
+        torch.cuda.synchronize()
+        assert bool((out == 0).all()) and bool((lse == float("-inf")).all()) and ok1() and ok2()
+    assert arf.ar_attn_device_error(m) == 0
+    m.destroy()
+
+
+def test_decode_scores_of_minus_infinity():
+    # they count as no token; a row of nothing else as one without tokens
+    heads, kv, D, page, n = 4, 2, 64, 16, 100
+    g = gen(32)
+    k, v, _, _ = paged(21, page, kv, D, False, "token", g)
+    q = normal((3, heads, D), g)
+    q[..., 0] = 1.0
+    table = tables([n, n, 1], page, 21, 7, g)
+    gone = torch.zeros(n, dtype=torch.bool, device=DEV)
+    gone[::3] = True
+    gone[:48] = True
+    for t in range(n):
+        for b in range(2):
+            if gone[t] or b == 1:
+                k[int(table[b, t // page]), t % page, :, 0] = float("-inf")
+    m = arf.ar_attn_create(heads, kv, D, page, 3, device=0)
+    lse = torch.empty(3, heads, device=DEV)
+    out, _ = arf.ar_attn_decode(m, arf.ar_kv_cache(k, v), q, table, torch.tensor([n, n, 1], dtype=torch.int32, device=DEV), lse=lse)
+    # the first sequence again, with the tokens that count on pages of one token
+    at = torch.arange(n, device=DEV)[~gone]
+    k1, v1 = (x[table[0, at // page].long(), at % page].unsqueeze(1).contiguous() for x in (k, v))
+    table1 = torch.arange(len(at), dtype=torch.int32, device=DEV).view(1, -1)
+    want, slack, want_lse, lse_slack = _attn.decode_ref(q[:1], k1, v1, table1, [len(at)], 1, 0, D ** -0.5)
+    torch.cuda.synchronize()
+    assert bool(((out[:1].double() - want).abs() <= slack).all())
+    assert bool(((lse[:1].double() - want_lse).abs() <= lse_slack).all())
+    assert bool((out[1] == 0).all()) and bool((lse[1] == float("-inf")).all())
+    assert bool(torch.isfinite(out[2]).all()) and bool(torch.isfinite(lse[2]).all())
+    m.destroy()
+
+
+@pytest.mark.parametrize("eight", [False, True])
 def test_decode_reads_nothing_outside_the_tokens(eight):
     # every place that no sequence holds, and what lies before a window, is NaN
     heads, kv, D, page, lengths, window = 8, 2, 128, 16, [37, 16, 1, 0, 200], 50
@@ -427,6 +504,32 @@ def test_append_the_last_token_of_a_slot_stands(T):
         rows = torch.tensor(list(want.values()), device=DEV)
         assert torch.equal(k.reshape(-1, kv, D)[at], x[rows, heads:heads + kv]) and torch.equal(v.reshape(-1, kv, D)[at], x[rows, heads + kv:])
     assert arf.ar_attn_device_error(m) == 0
+    m.destroy()
+
+
+def test_append_most_tokens():
+    # as many as a call takes, every slot named twice, far apart, and every 9th row padded
+    heads, kv, D, page, T = 2, 1, 64, 16, arf.AR_MAX_ATTN_TOKENS
+    g = gen(51)
+    k, v, _, _ = paged(T // 2 // page, page, kv, D, False, "token", g)
+    qkv = normal((T, (heads + 2 * kv) * D), g)
+    slots = torch.randperm(T // 2, generator=g, device=DEV).int().repeat(2)
+    slots[::9] = -1
+    k0, v0 = k.clone(), v.clone()
+    m = arf.ar_attn_create(heads, kv, D, page, 1, device=0)
+    q = arf.ar_attn_append(m, arf.ar_kv_cache(k, v), qkv, None, slots)
+    torch.cuda.synchronize()
+    x = qkv.view(T, heads + 2 * kv, D)
+    assert torch.equal(q, x[:, :heads])
+    wk, wv = k0.view(-1, D), v0.view(-1, D)
+    for part in (slice(0, T // 2), slice(T // 2, T)):  # (within a half no slot comes twice)
+        s = slots[part].long()
+        wk[s[s >= 0]], wv[s[s >= 0]] = x[part, heads][s >= 0], x[part, heads + kv][s >= 0]
+    assert torch.equal(k.view(-1, D), wk) and torch.equal(v.view(-1, D), wv)
+    assert arf.ar_attn_device_error(m) == 0
+    with pytest.raises(arf.ArfuseError) as e:
+        arf.ar_attn_append(m, arf.ar_kv_cache(k, v), normal((T + 1, qkv.shape[1]), g), None, torch.zeros(T + 1, dtype=torch.int32, device=DEV))
+    assert e.value.status == arf.AR_ERR_CAPACITY
     m.destroy()
 
 
