@@ -62,7 +62,8 @@ struct Shape {
     static_assert(kSmem + 26624 <= 232448, "shared memory of a CTA");
     static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums, in its ring");
     static_assert(kAhead >= 1 && kAhead + 2 <= 8, "units that are asked for and not used, of the eight masks and segments that are kept");
-    static_assert(kPart % 4 == 0 && kSmem >= kPart * 4, "parts come by 16 bytes");
+    static_assert(kPart % 4 == 0 && 2 * kFew * (kPart / 16 + 2 * kRows) * 4 <= kSmem && 16 * 16 >= kMaxGrid && kFew >= 16,
+                  "sixteenths of the columns of all parts that two joins take");
     // where chunk c of row r lies, so that eight rows' chunks c are in eight different groups of banks
     __device__ static int place(int r, int c) {
         return r * kRow + ((kChunks >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & (kChunks - 1))) << 4);
@@ -179,6 +180,13 @@ __device__ __forceinline__ void finish_row(const DecodeArgs& a, int row, int d, 
     const float f = weight == 0.0f ? 0.0f : __fdividef(vs, weight);
     *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + d) = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
     if (d == 0 && a.lse != nullptr) a.lse[row] = weight == 0.0f ? -INFINITY : (top + lg2(weight)) * kLn2;
+}
+
+// One more on a counter, seen by all behind what is written before it, and before what is read after it.
+__device__ __forceinline__ unsigned arrive(unsigned* counter) {
+    unsigned before;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    return before;
 }
 
 __device__ __forceinline__ void add(float4& sum, float f, float4 v) {
@@ -799,75 +807,89 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
                 const int count = min(j.fan, (j.first + j.parts - 1 - j.leader) / j.step + 1);
                 // this level's counter, of the leader's part
                 unsigned* counter = a.count + (j.leader * 2 + (j.leader == j.first ? 1 : 0)) * 2 + level;
-                __threadfence();
-                if (atomicAdd(counter, 1) == (unsigned)count - 1) {
+                if (arrive(counter) == (unsigned)count - 1) {
                     *counter = 0;
                     j.count = count;
                 }
-                __threadfence();
             }
         }
         __syncthreads();
-        if (s_join[0].count == 0 && s_join[1].count == 0) return;
+        const Join left = s_join[0], right = s_join[1];
+        const int n = left.count + right.count;
+        if (n == 0) return;
+        const Part part_left = s_part[s_run[0]], part_right = s_part[s_run[runs - 1]];
+        float* const head_left = part_of(left.leader, left.leader == left.first);
+        float* const head_right = part_of(right.leader, right.leader == right.first);
+        // both items' parts come to shared memory at once, in slices of their columns where they do not fit whole
+        int log_w = D == 64 ? 4 : D == 128 ? 5 : 6;  // of fours of columns
 #pragma unroll 1
-        for (int which = 0; which < 2; ++which) {
-            const Join join = s_join[which];
-            if (join.count == 0) continue;
-            const Part p = s_part[s_run[which == 0 ? 0 : runs - 1]];
-            const bool end_here = join.step * join.fan >= join.parts;
-            // parts come to shared memory, as many at a time as it holds
-            constexpr int kAtOnce = S::kSmem / (S::kPart * 4), kPieces = S::kPart / 4;
-            float* const head = part_of(join.leader, join.leader == join.first);
+        while (n * (kRows * 16 << log_w) + n * kRows * 8 > S::kSmem) --log_w;
+        const int w = 1 << log_w, sums_of_all = n * (kRows * 4 << log_w);  // floats
+        float* const parts = reinterpret_cast<float*>(smem);
+        const float* const tops = parts + sums_of_all;  // of each part, and its weights behind them
 #pragma unroll 1
-            for (int e0 = 0; e0 < p.rows * (D / 4); e0 += kThreads) {
-                const int e = e0 + tid, row = min(e / (D / 4), kRows - 1), d = e % (D / 4) * 4;
-                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float top = -INFINITY, weight = 0.0f;
-#pragma unroll 1
-                for (int k = 0; k < join.count; k += kAtOnce) {
-                    const int count = min(kAtOnce, join.count - k);
-                    __syncthreads();  // the parts before have been read
+        for (int d0 = 0; d0 < D; d0 += 4 * w) {
+            if (d0 > 0) __syncthreads();  // the slice before has been read
+            auto source = [&](int j) {
+                const bool l = j < left.count;
+                const int k = l ? j : j - left.count;
+                if (k == 0) return l ? head_left : head_right;
+                return part_of(l ? left.leader + k * left.step : right.leader + k * right.step, false);
+            };
 #pragma unroll 4
-                    for (int i = e0 > 0 && join.count <= kAtOnce ? count * kPieces : tid; i < count * kPieces; i += kThreads) {
-                        const int j = k + i / kPieces;
-                        copy16(smem_addr(smem) + i * 16, (j == 0 ? head : part_of(join.leader + j * join.step, false)) + i % kPieces * 4, policy);
-                    }
-                    copy_commit();
-                    copy_wait<0>();
-                    __syncthreads();
-                    const float* const parts = reinterpret_cast<const float*>(smem);
-                    float next = top;
-#pragma unroll 8
-                    for (int j = 0; j < count; ++j) next = fmaxf(next, parts[j * S::kPart + S::kSums + row]);
-                    const float keep = share_of(top, next);
-                    top = next;
-                    weight *= keep;
-                    sum = make_float4(sum.x * keep, sum.y * keep, sum.z * keep, sum.w * keep);
-#pragma unroll 4
-                    for (int j = 0; j < count; ++j) {
-                        const float f = share_of(parts[j * S::kPart + S::kSums + row], top);
-                        weight += f * parts[j * S::kPart + S::kSums + kRows + row];
-                        add(sum, f, *reinterpret_cast<const float4*>(parts + j * S::kPart + row * D + d));
-                    }
-                }
-                if (e >= p.rows * (D / 4)) continue;
-                if (end_here) {
-                    finish(p, row, d, sum, top, weight);
-                } else {
-                    *reinterpret_cast<float4*>(head + row * D + d) = sum;
-                    // (the maxima and weights, still read for the columns of a next turn, are left for the end)
-                    if (d == 0) s_top[0][row] = top, s_weight[0][row] = weight;
-                }
+            for (int i = tid; i < n * (kRows << log_w); i += kThreads) {
+                const int j = i / kRows >> log_w, row = i >> log_w & (kRows - 1);
+                if (row < (j < left.count ? part_left : part_right).rows)
+                    copy16(smem_addr(smem) + i * 16, source(j) + row * D + d0 + (i & (w - 1)) * 4, policy);
             }
+            for (int i = tid; i < n * (kRows / 2); i += kThreads)
+                copy16(smem_addr(tops + i * 4), source(i / (kRows / 2)) + S::kSums + i % (kRows / 2) * 4, policy);
+            copy_commit();
+            copy_wait<0>();
             __syncthreads();
-            if (!end_here && tid < kRows) {  // (of all rows, for whole sectors)
-                head[S::kSums + tid] = s_top[0][tid];
-                head[S::kSums + kRows + tid] = s_weight[0][tid];
+            const int of_left = left.count > 0 ? part_left.rows : 0, of_right = right.count > 0 ? part_right.rows : 0;
+#pragma unroll 1
+            for (int e = tid; e < (of_left + of_right) << log_w; e += kThreads) {
+                const bool l = e >> log_w < of_left;
+                const Part& p = l ? part_left : part_right;
+                const Join& join = l ? left : right;
+                const int row = (e >> log_w) - (l ? 0 : of_left), d = (e & (w - 1)) * 4, j0 = l ? 0 : left.count;
+                const float* const top_at = tops + j0 * 2 * kRows + row;
+                const float* const sum_at = parts + (j0 * (kRows * 4) << log_w) + (row * 4 << log_w) + d;
+                float top = -INFINITY, weight = 0.0f;
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                for (int j = 0; j < join.count; ++j) top = fmaxf(top, top_at[j * 2 * kRows]);
+#pragma unroll 4
+                for (int j = 0; j < join.count; ++j) {
+                    const float f = share_of(top_at[j * 2 * kRows], top);
+                    weight += f * top_at[j * 2 * kRows + kRows];
+                    add(sum, f, *reinterpret_cast<const float4*>(sum_at + (j * (kRows * 4) << log_w)));
+                }
+                if (join.step * join.fan >= join.parts) {
+                    finish(p, row, d0 + d, sum, top, weight);
+                } else {
+                    *reinterpret_cast<float4*>((l ? head_left : head_right) + row * D + d0 + d) = sum;
+                    // (the maxima and weights, still read for the next slice, are left for the end)
+                    if (d0 + d == 0) s_top[l ? 0 : 1][row] = top, s_weight[l ? 0 : 1][row] = weight;
+                }
             }
-            if (tid == 0) s_join[which].step = end_here ? 0 : join.step * join.fan;
         }
-        // (those that did not arrive last have left this item to others)
-        if (tid < 2 && s_join[tid].count == 0) s_join[tid].step = 0;
+        __syncthreads();
+        if (tid < 2 * kRows) {  // (of all rows, for whole sectors)
+            const int which = tid / kRows, row = tid % kRows;
+            const Join& join = which == 0 ? left : right;
+            if (join.count > 0 && join.step * join.fan < join.parts) {
+                float* const head = which == 0 ? head_left : head_right;
+                head[S::kSums + row] = s_top[which][row];
+                head[S::kSums + kRows + row] = s_weight[which][row];
+            }
+        }
+        // (those that did not arrive last have left an item to others)
+        if (tid < 2) {
+            Join& j = s_join[tid];
+            j.step = j.count > 0 && j.step * j.fan < j.parts ? j.step * j.fan : 0;
+        }
     }
 }
 
