@@ -32,6 +32,7 @@ namespace arf {
 namespace {
 
 constexpr int kMaxGrid = 256;
+constexpr int kScratchRows = 384;  // rows of sums that a CTA's warps leave in memory: two places a warp, of eight or sixteen
 constexpr int kFew = 24;          // parts that are joined at once
 constexpr float kLazy = 8.0f;     // scores (log2) may pass the reference by so much before it moves
 constexpr float kLn2 = 0.6931471805599453f;
@@ -39,8 +40,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // NT: groups of eight query heads.
 template <int D, bool EIGHT, int NT>
 struct Shape {
-    // sixteen warps of 128 registers hide each other's latencies; more sums need eight of 255
-    static constexpr int kWarps = D <= 128 && NT == 1 ? 16 : 8;
+    // sixteen warps of 128 registers hide each other's latencies; more sums need twelve of 168, or eight of 255
+    static constexpr int kWarps = D == 256 ? 8 : NT == 1 ? 16 : 12;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRows = 8 * NT;
     static constexpr int kRing = 196608 / kWarps;                      // bytes of a warp's ring
@@ -51,7 +52,7 @@ struct Shape {
     static constexpr int kAhead = (kRing / kHalf - 1) / 2 < 4 ? (kRing / kHalf - 1) / 2 : 4;  // units that are asked for ahead
     static constexpr int kHalves = 2 * kAhead + 1;
     static constexpr int kLeast = kHalf >= 4096 ? 1 : 4096 / kHalf;  // units of a warp, while there are SMs left
-    static constexpr int kCost = kHalf >= 8192 ? 1 : 8192 / kHalf;   // units that an item counts for besides its own
+    static constexpr int kCost = 4;  // units that an item counts for besides its own
     static constexpr int kMany = (1 << 27) / kHalf;  // units that are too many for all SMs (256 MB)
     static constexpr int kAlone = 196608 / kHalf;  // units by which a CTA that keeps an item may pass an equal share
     static constexpr int kPitch = D + 4;       // floats from a row of sums to the next in shared memory, free of bank conflicts
@@ -60,6 +61,7 @@ struct Shape {
     static constexpr int kPart = kSums + 2 * kRows;  // a CTA's part: sums, maxima, sums of weights
     static constexpr int kSmem = kWarps * kRing;
     static_assert(kSmem + 26624 <= 232448, "shared memory of a CTA");
+    static_assert(2 * kWarps * kRows <= kScratchRows, "the handle's scratch");
     static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums, in its ring");
     static_assert(kAhead >= 1 && kAhead + 2 <= 8, "units that are asked for and not used, of the eight masks and segments that are kept");
     static_assert(kPart % 4 == 0 && 2 * kFew * (kPart / 16 + 2 * kRows) * 4 <= kSmem && 16 * 16 >= kMaxGrid && kFew >= 16,
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     // ---- what this CTA's warps take
     int64_t total, each = 0;   // units, and units of a warp where all are dealt out
     int64_t begin, end;        // units of this CTA
-    // The walk over this warp's items.  One counts for kCost units more, before its first, for what it costs to begin and end
+    // The walk over this warp's items (clamped where lengths that change during the call could lead it astray).  One counts for kCost units more, before its first, for what it costs to begin and end
     // it; these are walked over.
     int w_b = 0, w_group = 0, w_u = 0, w_start = 0, w_len = 0, w_n = 0;  // sequence, group, next unit of kCost + w_n, tokens
     int64_t w_item = 0;  // where the item's first unit (behind what it costs) is among all
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             end = w_n;
         } else {
             // Equal ranges of all units; the last ones may be short or empty.
-            const int warps = (!EIGHT && total >= S::kMany ? fewer : (int)gridDim.x) * kWarps;
+            const int warps = (!EIGHT && NT == 1 && total >= S::kMany ? fewer : (int)gridDim.x) * kWarps;
             each = max((int64_t)S::kLeast, quotient64(total + warps - 1, warps));
             begin = each * (blockIdx.x * kWarps);
             end = min(total, begin + each * kWarps);
@@ -304,12 +306,13 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
                 skip = from - s_before[thread];
                 if (per_thread > 1 && w_left > 0)
 #pragma unroll 1
-                    for (int64_t n; (n = (int64_t)units(w_b) * a.groups) <= skip; ++w_b) skip -= n;
+                    for (int64_t n; w_b + 1 < a.B && (n = (int64_t)units(w_b) * a.groups) <= skip; ++w_b) skip -= n;
             }
             if (w_left > 0) {
                 sequence();
-                w_group = (int)quotient64(skip, w_n + S::kCost);
-                w_u = (int)(skip - (int64_t)w_group * (w_n + S::kCost));
+                w_n = max(w_n, 1);
+                w_group = (int)min(quotient64(skip, w_n + S::kCost), (int64_t)(a.groups - 1));
+                w_u = (int)min(skip - (int64_t)w_group * (w_n + S::kCost), (int64_t)(w_n + S::kCost - 1));
                 w_item = from - w_u + S::kCost;
                 if (w_left <= S::kCost - w_u) w_left = 0;
             }
@@ -340,10 +343,12 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             if (++w_group == a.groups) {
                 w_group = 0;
 #pragma unroll 1
-                do {
+                while (w_b + 1 < a.B) {
                     ++w_b;
                     sequence();
-                } while (w_n == 0);
+                    if (w_n > 0) break;
+                }
+                w_n = max(w_n, 1);
             }
         }
         const int take = (int)(w_left < w_n + S::kCost - w_u ? w_left : w_n + S::kCost - w_u);
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             s_seg[warp][found & 7] = Segment{w_item, ask_u, ask_u1, w_n, head, w_b * a.heads + head * a.shared + row,
                                              min(a.rows_of_group, a.shared - row), w_left == 0};
         ++found;
-        ask_last = page_of(w_len - 1);
+        ask_last = page_of(max(w_len, 1) - 1);
         table_at = page_of(w_start + (int64_t)ask_u * TOK);
         entry = table_entry(table_at + lane);
         entry_next = table_entry(table_at + 32 + lane);
@@ -719,7 +724,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     auto part_of = [&](int cta, bool begins) { return a.part + ((int64_t)cta * 2 + (begins ? 1 : 0)) * S::kPart; };
 
     // items that this CTA shares with others: perhaps its first with those before it, and its last with those behind it
-    auto owner = [&](int64_t unit) { return (int)quotient64(unit, each * kWarps); };
+    auto owner = [&](int64_t unit) { return (int)min(quotient64(unit, each * kWarps), (int64_t)(gridDim.x - 1)); };
     if (tid >= kThreads - 2) {  // (of the last warp, the others have more to do)
         const int which = tid - (kThreads - 2);
         const Part p = s_part[which == 0 ? __ffs(start_mask) - 1 : 31 - __clz(start_mask)];
@@ -953,8 +958,8 @@ cudaError_t attn_decode_set_attributes() {
 
 size_t attn_decode_counters(int num_sms) { return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * 4; }
 size_t attn_decode_parts(int num_sms, int head_dim) {
-    // two parts a CTA of up to sixteen rows, two places of sums a warp (sixteen of eight rows, or eight of sixteen)
-    return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * (2 * (16 * head_dim + 32) + 2 * 16 * 8 * head_dim);
+    // two parts a CTA of up to sixteen rows, and its warps' sums
+    return (size_t)(num_sms < kMaxGrid ? num_sms : kMaxGrid) * (2 * (16 * head_dim + 32) + kScratchRows * head_dim);
 }
 
 }  // namespace arf
