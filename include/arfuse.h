@@ -825,9 +825,10 @@ ARFUSE_API ar_status ar_attn_append(ar_attn* attn, const ar_kv_cache* cache, con
  *   lse         device fp32 [B, heads], or NULL
  * Values of the cache outside the tokens looked at may be anything.  A score of
  * minus infinity counts as no token, a row of nothing else as one without tokens.
- * Sums and the softmax are fp32; deterministic for given lengths and GPU; the order of a sum may
- * depend on the other sequences of the batch.  One launch; the split of the work
- * over the SMs follows the lengths on the device, so a captured call serves any.
+ * Sums and the softmax are fp32; the same call on the same GPU gives the same bits; the
+ * order of a sum may depend on the other sequences of the batch and on the width of
+ * the page table.  One launch; the split of the work over the SMs follows the lengths
+ * on the device, so a captured call serves any.
  * Errors as for ar_attn_append, and AR_ERR_CAPACITY (B > max_seqs); page_table and
  * lengths 4-byte aligned; table_stride >= table_width.
  */

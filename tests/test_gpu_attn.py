@@ -177,6 +177,21 @@ def test_decode_much_work(eight):
     m.destroy()
 
 
+@pytest.mark.parametrize("heads,kv,D,eight", [(32, 2, 128, False), (24, 2, 64, False), (32, 2, 128, True), (32, 2, 256, False), (40, 1, 64, True)])
+def test_decode_heads_in_groups_of_sixteen(heads, kv, D, eight):
+    # tables so wide that keys and values could be more than 64 MB: groups of up to sixteen heads, otherwise of eight
+    page, lengths = 16, [0, 1, 17, 900, 64, 2500, 33]
+    g = gen(heads * D)
+    pages = sum(-(-n // page) for n in lengths) + 2
+    k, v, ks, vs = paged(pages, page, kv, D, eight, "pair", g)
+    q = normal((len(lengths), heads, D), g, 2.0)
+    m = arf.ar_attn_create(heads, kv, D, page, len(lengths), device=0)
+    for width in (170, 8000):
+        check_decode(m, q, k, v, ks, vs, tables(lengths, page, pages, width, g), lengths)
+    assert arf.ar_attn_device_error(m) == 0
+    m.destroy()
+
+
 def test_decode_without_work():
     heads, kv, D, page = 8, 2, 128, 16
     g = gen(31)

@@ -20,6 +20,12 @@
 // once, at the end of the CTA, in the order of the warps, and over CTAs by the last of them to
 // arrive, in the order of the CTAs.  No CTA waits for another.
 //
+// What bounds it.  Memory, where there is much: 64 sequences of 256 to 8192 tokens (eight
+// key-value heads of 128 columns, 610 MB) take 103 us, 5.9 TB/s.  Else the way there and back,
+// some 13 us: lengths and plan 2, the page's number and the first keys 2 to 3, the spread of
+// the SMs' ends up to 3, a CTA's sums 2.5, joins 3 for each level.  A sequence of 500 tokens
+// takes 10 us, of which the one SM reads for 3; one of 131071 (134 MB) 32.5.
+//
 // Roundings: scores, maxima, sums and o are fp32.  Weights go to the matrix instruction as
 // two bf16 (their rounding and its remainder: 2^-17, where one bf16 would add 0.7 times the
 // output's own rounding); with 8-bit values as halves (2^-11), whose products are exact, q
@@ -40,7 +46,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // NT: groups of eight query heads.
 template <int D, bool EIGHT, int NT>
 struct Shape {
-    // sixteen warps of 128 registers hide each other's latencies; more sums need twelve of 168, or eight of 255
+    // Sixteen warps of 128 registers hide each other's latencies; more sums need twelve of 168, or eight of 255.  (Sixteen heads
+    // of 64 columns, 315 MB: twelve warps 64 us, eight 76, sixteen, whose registers spill, 70.)
     static constexpr int kWarps = D == 256 ? 8 : NT == 1 ? 16 : 12;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRows = 8 * NT;
@@ -51,10 +58,14 @@ struct Shape {
     static constexpr int kHalf = kTok * kRow;  // bytes of a unit's keys (or values)
     static constexpr int kAhead = (kRing / kHalf - 1) / 2 < 4 ? (kRing / kHalf - 1) / 2 : 4;  // units that are asked for ahead
     static constexpr int kHalves = 2 * kAhead + 1;
-    static constexpr int kLeast = kHalf >= 4096 ? 1 : 4096 / kHalf;  // units of a warp, while there are SMs left
-    static constexpr int kCost = 4;  // units that an item counts for besides its own
+    // Units that an item counts for besides its own: to begin and end one takes a warp 2 us.  (700 sequences of up to 89 tokens,
+    // heads of 64 columns: none 37.6 us, two 31.4, four 29.9, six 32.6; five of 1 to 20001 tokens, 256 columns: one 24.5, four
+    // 23.1.)
+    static constexpr int kCost = 4;
     static constexpr int kMany = (1 << 27) / kHalf;  // units that are too many for all SMs (256 MB)
-    static constexpr int kAlone = 196608 / kHalf;  // units by which a CTA that keeps an item may pass an equal share
+    // Units by which a CTA that keeps an item may pass an equal share.  (One sequence, eight heads of 128 columns: 500 tokens
+    // 10.2 us by one CTA, 10.5 cut; 600 10.8 and 11.1; 700 11.7 and 10.7.)
+    static constexpr int kAlone = 172032 / kHalf;
     static constexpr int kPitch = D + 4;       // floats from a row of sums to the next in shared memory, free of bank conflicts
     // In memory nothing is between the rows: sectors that are not written whole would have to be read before they are merged.
     static constexpr int kSums = kRows * D;
@@ -266,8 +277,9 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             before += __shfl_sync(0xffffffffu, sum, (warp + 31) & 31) * (warp > 0);
         }
         // Three quarters of the SMs draw what the memory gives, with fewer streams in each other's way: 2.4 GB take 360 us from
-        // 114 SMs, 375 from 152; 540 MB take 90 and 92.  134 MB, where each SM's latencies count, take 35 and 33.4, and 8-bit
-        // caches, which each SM has more work with for a byte, take all.
+        // 114 SMs, 375 from 152; 540 MB take 90 and 92.  134 MB, where each SM's latencies count, take 35 and 33.4.  Where an SM
+        // has more work with a byte all are needed: 630 MB with sixteen heads a key 112 us from 152 SMs, 141 from 114; 8-bit
+        // caches too.
         const int fewer = max(1, (int)gridDim.x * 3 / 4);
         if ((int64_t)a.B * a.groups <= gridDim.x && (int64_t)(most - S::kAlone) * fewer <= total) {
             // One CTA an item: nothing to join over CTAs, and none has much more to do than with equal shares of those.
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         } else {
             // Equal ranges of all units; the last ones may be short or empty.
             const int warps = (!EIGHT && NT == 1 && total >= S::kMany ? fewer : (int)gridDim.x) * kWarps;
-            each = max((int64_t)S::kLeast, quotient64(total + warps - 1, warps));
+            each = max((int64_t)1, quotient64(total + warps - 1, warps));
             begin = each * (blockIdx.x * kWarps);
             end = min(total, begin + each * kWarps);
             const int64_t from = begin + each * warp;
@@ -936,10 +948,17 @@ cudaError_t set_smem_dim() {
 }  // namespace
 
 cudaError_t launch_attn_decode(const DecodeArgs& args, int head_dim, int num_sms, cudaStream_t stream) {
-    // groups of up to sixteen query heads of a key-value head, of equal size as far as that goes
+    // Groups of up to sixteen query heads of a key-value head, of equal size as far as that goes; of up to eight where their
+    // keys and values, read again from L2 by every group, are 64 MB at most for sixteen heads, as far as the page table and the
+    // window say (the lengths are on the device).  Groups of eight have half the sums to join and twice the warps: sixteen
+    // heads of 128 columns, 8 MB 11.4 us (groups of sixteen: 14.4), 66 MB 23.6 (26.2), 131 MB 40.9 (36.4), 262 MB 85.7 (56.2);
+    // of 256 columns, 33 MB 21.3 (30.4), 66 MB 29.3 (37.5), 131 MB 41.4 (40.9); of 64, 33 MB 12.9 (13.3), 66 MB 17.2 (16.3).
     DecodeArgs a = args;
     a.shared = a.heads / a.kv;
     a.per_head = (a.shared + 15) / 16;
+    const int64_t longest = a.window > 0 && a.window < a.most ? a.window : a.most;
+    const double bytes = (double)a.B * longest * a.kv * a.per_head * head_dim * (a.k.scale != nullptr ? 2 : 4);
+    if (bytes <= (double)(1 << 26)) a.per_head = (a.shared + 7) / 8;
     a.groups = a.kv * a.per_head;
     a.rows_of_group = (a.shared + a.per_head - 1) / a.per_head;
     switch (head_dim) {
