@@ -24,7 +24,6 @@ struct ar_attn {
     uint8_t* d_mem;              // everything below
     unsigned* d_err;
     unsigned* d_count;  // zero between calls
-    uint8_t* d_zeros;   // always
     arf::RopeTable* d_rope;
     float* d_part;
 };
@@ -36,7 +35,6 @@ using arf::overlap;
 using arf::Range;
 using arf::range_of;
 
-constexpr size_t kZeros = arf::kMaxHeadDim * 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kMostTokens = 0x7fffffff;  // of a cache, and of a sequence
 
@@ -146,8 +144,8 @@ ar_status ar_attn_create(int device, int heads, int kv_heads, int head_dim, int 
         if (major < 10)
             st = AR_ERR_UNSUPPORTED;
         else if (arf::attn_decode_set_attributes() == cudaSuccess &&
-                 cudaMalloc(&m->d_mem, 256 + kZeros + count + rope + part) == cudaSuccess &&
-                 cudaMemset(m->d_mem, 0, 256 + kZeros + count + rope) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess)
+                 cudaMalloc(&m->d_mem, 256 + count + rope + part) == cudaSuccess &&
+                 cudaMemset(m->d_mem, 0, 256 + count + rope) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess)
             st = AR_OK;
     }
     if (st != AR_OK) {
@@ -159,10 +157,9 @@ ar_status ar_attn_create(int device, int heads, int kv_heads, int head_dim, int 
     }
     (void)cudaSetDevice(prev);
     m->d_err = reinterpret_cast<unsigned*>(m->d_mem);
-    m->d_zeros = m->d_mem + 256;
-    m->d_count = reinterpret_cast<unsigned*>(m->d_mem + 256 + kZeros);
-    m->d_rope = reinterpret_cast<arf::RopeTable*>(m->d_mem + 256 + kZeros + count);
-    m->d_part = reinterpret_cast<float*>(m->d_mem + 256 + kZeros + count + rope);
+    m->d_count = reinterpret_cast<unsigned*>(m->d_mem + 256);
+    m->d_rope = reinterpret_cast<arf::RopeTable*>(m->d_mem + 256 + count);
+    m->d_part = reinterpret_cast<float*>(m->d_mem + 256 + count + rope);
     *out = m;
     return AR_OK;
 }
@@ -312,7 +309,6 @@ ar_status ar_attn_decode(ar_attn* m, const ar_kv_cache* cache, const void* q, co
     a.err = m->d_err;
     a.count = m->d_count;
     a.part = m->d_part;
-    a.zeros = m->d_zeros;
     a.table_stride = table_stride;
     const int64_t most = table_width * m->page_size;
     a.most = most < kMostTokens ? most : kMostTokens;

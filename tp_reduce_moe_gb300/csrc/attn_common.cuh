@@ -49,7 +49,6 @@ struct DecodeArgs {
     unsigned* err;
     unsigned* count;  // arrival counters, zero between calls
     float* part;      // parts of rows split over several warps and CTAs
-    const uint8_t* zeros;  // kMaxHeadDim * 2 bytes of zeros, 16-byte aligned
     int64_t table_stride;
     int64_t most;  // longest length that the page table holds
     int pages;

@@ -97,6 +97,10 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
+// Or zeros: nothing is read where bytes is 0.
+__device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(policy) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -337,6 +341,8 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     int ask_u = 0, ask_u1 = 0, ask_last = 0;  // of the segment that is asked for: next unit, end, last page of the sequence
     const uint8_t *k_head = nullptr, *v_head = nullptr;  // and its keys and values
     unsigned asked = 0, found = 0;  // units asked for, segments found
+    constexpr unsigned kAll = 0xffffffffu >> (32 - TOK);
+    unsigned present = 0;           // tokens of the unit that was looked up
     uint32_t fill = 0;              // place in the ring that is filled next
     // the page table's entries from table_at on: this lane's of the first 32 and of the next 32
     int table_at = 0, entry = 0, entry_next = 0;
@@ -385,9 +391,18 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         if (live) {
             const uint8_t* const* rows = s_row[warp][which] + lane / S::kChunks;
             const int c = lane % S::kChunks;
+            if (present == kAll) {
 #pragma unroll
-            for (int i = 0; i < TOK * S::kChunks / 32; ++i)
-                copy16(ring + fill + S::place((i * 32 + lane) / S::kChunks, c), rows[i * 32 / S::kChunks] + c * 16, policy);
+                for (int i = 0; i < TOK * S::kChunks / 32; ++i)
+                    copy16(ring + fill + S::place((i * 32 + lane) / S::kChunks, c), rows[i * 32 / S::kChunks] + c * 16, policy);
+            } else {
+                // (zeros that are read would all come from one place: 1184 single tokens take 21 us with them)
+#pragma unroll 1
+                for (int i = 0; i < TOK * S::kChunks; i += 32) {
+                    const int row = (i + lane) / S::kChunks;
+                    copy16_or_zeros(ring + fill + S::place(row, c), rows[i / S::kChunks] + c * 16, present >> row & 1 ? 16 : 0, policy);
+                }
+            }
         }
         copy_commit();
         fill = fill + S::kHalf == S::kHalves * S::kHalf ? 0 : fill + S::kHalf;
@@ -406,12 +421,12 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             const int page = at < 32 ? here : next;
             const bool wanted = lane < TOK && token < w_len, there = wanted && (unsigned)page < (unsigned)a.pages;
             if (wanted && !there) atomicOr(a.err, kErrPageRange);
-            const unsigned mask = __ballot_sync(0xffffffffu, there);
+            present = __ballot_sync(0xffffffffu, there);
             __syncwarp();  // all lanes have read the places before
-            if (lane == 0) s_mask[warp][asked & 7] = mask;
-            if (lane < TOK) {  // what is not there comes as zeros
-                s_row[warp][0][lane] = there ? k_head + (page * a.k.page + in_page * a.k.token) : a.zeros;
-                s_row[warp][1][lane] = there ? v_head + (page * a.v.page + in_page * a.v.token) : a.zeros;
+            if (lane == 0) s_mask[warp][asked & 7] = present;
+            if (lane < TOK) {  // (what is not there is not read)
+                s_row[warp][0][lane] = there ? k_head + (page * a.k.page + in_page * a.k.token) : k_head;
+                s_row[warp][1][lane] = there ? v_head + (page * a.v.page + in_page * a.v.token) : v_head;
             }
             __syncwarp();
             ++asked;
@@ -561,7 +576,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][n][j] *= q_scale[n][j & 1];
-        if (mask != 0xffffffffu >> (32 - TOK)) {
+        if (mask != kAll) {
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i)
                 if (!(mask >> (8 * i + g) & 1))
