@@ -730,7 +730,7 @@ typedef struct ar_kv_cache {
 /*
  * Create the handle of a model's attention layers (shared by the layers, as a
  * workspace is).  Allocates on `device` its scratch: parts of rows split over
- * several warps and CTAs (417 * SMs * head_dim fp32: 32 MB at head_dim 128 on 152 SMs),
+ * several warps and CTAs (225 * SMs * head_dim fp32: 18 MB at head_dim 128 on 152 SMs),
  * their counters, the rotary table and the error word.  Calls on one handle must be
  * ordered on the GPU (one stream, or event ordering; graphs captured on it must not
  * run at the same time); concurrent callers need a handle each.  Call it outside

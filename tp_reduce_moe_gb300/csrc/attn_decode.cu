@@ -16,7 +16,7 @@
 //
 // A warp streams its units through a ring of its own in shared memory, keys and values in
 // turn, by 16-byte asynchronous copies that run ahead across items, so that no barrier stands
-// in the stream.  Items within a warp's range are finished by it; what is cut is added up
+// in the stream.  Items within a warp's range are finished from its registers; what is cut is added up
 // once, at the end of the CTA, in the order of the warps, and over CTAs by the last of them to
 // arrive, in the order of the CTAs.  No CTA waits for another.
 //
@@ -38,7 +38,7 @@ namespace arf {
 namespace {
 
 constexpr int kMaxGrid = 256;
-constexpr int kScratchRows = 384;  // rows of sums that a CTA's warps leave in memory: two places a warp, of eight or sixteen
+constexpr int kScratchRows = 192;  // rows of sums that a CTA's warps leave in memory, eight or sixteen of each
 constexpr int kFew = 24;          // parts that are joined at once
 constexpr float kLazy = 8.0f;     // scores (log2) may pass the reference by so much before it moves
 constexpr float kLn2 = 0.6931471805599453f;
@@ -72,7 +72,7 @@ struct Shape {
     static constexpr int kPart = kSums + 2 * kRows;  // a CTA's part: sums, maxima, sums of weights
     static constexpr int kSmem = kWarps * kRing;
     static_assert(kSmem + 26624 <= 232448, "shared memory of a CTA");
-    static_assert(2 * kWarps * kRows <= kScratchRows, "the handle's scratch");
+    static_assert(kWarps * kRows <= kScratchRows, "the handle's scratch");
     static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums, in its ring");
     static_assert(kAhead >= 1 && kAhead + 2 <= 8, "units that are asked for and not used, of the eight masks and segments that are kept");
     static_assert(kPart % 4 == 0 && 2 * kFew * (kPart / 16 + 2 * kRows) * 4 <= kSmem && 16 * 16 >= kMaxGrid && kFew >= 16,
@@ -192,11 +192,13 @@ struct Join {
     int first, parts, fan, step, leader, count;
 };
 
+__device__ __forceinline__ float lse_of(float top, float weight) { return weight == 0.0f ? -INFINITY : (top + lg2(weight)) * kLn2; }
+
 // Four columns of a row of the output, and with the first of them its lse.
 __device__ __forceinline__ void finish_row(const DecodeArgs& a, int row, int d, int D, float4 sum, float weight, float vs, float top) {
     const float f = weight == 0.0f ? 0.0f : __fdividef(vs, weight);
     *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + d) = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
-    if (d == 0 && a.lse != nullptr) a.lse[row] = weight == 0.0f ? -INFINITY : (top + lg2(weight)) * kLn2;
+    if (d == 0 && a.lse != nullptr) a.lse[row] = lse_of(top, weight);
 }
 
 // One more on a counter, seen by all behind what is written before it, and before what is read after it.
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             end = w_n;
         } else {
             // Equal ranges of all units; the last ones may be short or empty.
-            const int warps = (!EIGHT && NT == 1 && total >= S::kMany ? fewer : (int)gridDim.x) * kWarps;
+            const int warps = (!EIGHT && NT == 1 && a.per_head == 1 && total >= S::kMany ? fewer : (int)gridDim.x) * kWarps;
             each = max((int64_t)1, quotient64(total + warps - 1, warps));
             begin = each * (blockIdx.x * kWarps);
             end = min(total, begin + each * kWarps);
@@ -450,8 +452,8 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         return;
     }
 
-    auto place_of = [&](int w, int which) {  // of a warp's sums: left in mid-stream, or on the way out
-        return a.part + (int64_t)gridDim.x * 2 * S::kPart + (((int64_t)blockIdx.x * kWarps + w) * 2 + which) * S::kSums;
+    auto place_of = [&](int w) {  // of the sums that a warp leaves in mid-stream
+        return a.part + (int64_t)gridDim.x * 2 * S::kPart + ((int64_t)blockIdx.x * kWarps + w) * S::kSums;
     };
 
     // ---- the units.  A turn asks for one and works on the one that was asked for kAhead turns before; the turn before the
@@ -670,46 +672,76 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     auto end_segment = [&]() {
         const Segment& seg = s_seg[warp][begun++ & 7];
         more = !seg.last;
-        const bool whole = seg.u0 == 0 && seg.u1 == seg.n;
-        const int which = 2 * warp + (more && !whole ? 0 : 1);
-        __syncwarp();  // all lanes have read the ring
-        // (when the last sums are written the stream has ended, and the ring is free)
-        float* const to = more ? place_of(warp, whole ? 1 : 0) : reinterpret_cast<float*>(smem + warp * S::kRing);
-        const int pitch = more ? D : S::kPitch;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], x);
+        if (seg.u0 > 0 || seg.u1 < seg.n) {  // a part
+            __syncwarp();  // all lanes have read the ring
+            // (when the last sums are written the stream has ended, and the ring is free)
+            const int which = 2 * warp + (more ? 0 : 1), pitch = more ? D : S::kPitch;
+            float* const to = more ? place_of(warp) : reinterpret_cast<float*>(smem + warp * S::kRing);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 8 * n + 2 * t4 + h;
+                    if (g == 0) {
+                        s_m[which][row] = m[n][h];
+                        s_l[which][row] = l[n][h];
+                    }
+                    float* const line = to + row * pitch + (EIGHT ? 2 * g : g);
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i)
+                        if (EIGHT) {
+                            *reinterpret_cast<float2*>(line + i * 16) = make_float2(o[i][n][h], o[i][n][h + 2]);
+                        } else {
+                            line[i * 16] = o[i][n][h];
+                            line[i * 16 + 8] = o[i][n][h + 2];
+                        }
+                }
+            if (lane == 0) s_part[which] = Part{seg.item, seg.n, seg.kv_head, seg.row, seg.rows};
+            return;
+        }
+        // the whole: straight to the output
+        const float vs = EIGHT ? a.v.scale[seg.kv_head] : 1.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float f[2];
+#pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int row = 8 * n + 2 * t4 + h;
-                float sum = l[n][h];
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                if (g == 0) {
-                    s_m[which][row] = m[n][h];
-                    s_l[which][row] = sum;
-                }
-                float* const line = to + row * pitch + (EIGHT ? 2 * g : g);
+                f[h] = l[n][h] == 0.0f ? 0.0f : __fdividef(vs, l[n][h]);
+                if (g == 0 && a.lse != nullptr && row < seg.rows) a.lse[seg.row + row] = lse_of(m[n][h] - kOffset, l[n][h]);
+            }
+            if (EIGHT) {  // (neighbouring columns)
+                uint16_t* const to = a.out + (int64_t)(seg.row + 8 * n + 2 * t4) * D + 2 * g;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i)
-                    if (EIGHT) {
-                        *reinterpret_cast<float2*>(line + i * 16) = make_float2(o[i][n][h], o[i][n][h + 2]);
-                    } else {
-                        line[i * 16] = o[i][n][h];
-                        line[i * 16 + 8] = o[i][n][h + 2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (8 * n + 2 * t4 + h < seg.rows)
+                            *reinterpret_cast<uint32_t*>(to + h * D + i * 16) = pack_bf16x2(o[i][n][h] * f[h], o[i][n][h + 2] * f[h]);
+            } else {
+                // with the lane next to this one two columns of one head each, with the one behind that four: whole sectors
+                const bool second = g & 1, behind = g & 2;
+                const int row = 8 * n + 2 * t4 + second;
+                uint16_t* const to = a.out + (int64_t)(seg.row + row) * D + (behind ? 8 : 0) + (g & 4);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    uint32_t two[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float x = o[i][n][2 * j] * f[0], y = o[i][n][2 * j + 1] * f[1];
+                        const float next = __shfl_xor_sync(0xffffffffu, second ? x : y, 4);
+                        two[j] = second ? pack_bf16x2(next, y) : pack_bf16x2(x, next);
                     }
+                    const uint32_t next = __shfl_xor_sync(0xffffffffu, behind ? two[0] : two[1], 8);
+                    if (row < seg.rows) *reinterpret_cast<uint2*>(to + i * 16) = behind ? make_uint2(next, two[1]) : make_uint2(two[0], next);
+                }
             }
-        if (whole) {
-            __syncwarp();
-            const float vs = EIGHT ? a.v.scale[seg.kv_head] : 1.0f;
-#pragma unroll 4
-            for (int i = lane; i < seg.rows * (D / 4); i += 32) {
-                const int row = i / (D / 4), d = i % (D / 4) * 4;
-                finish_row(a, seg.row + row, d, D, *reinterpret_cast<const float4*>(to + row * pitch + d), s_l[which][row], vs,
-                           s_m[which][row] - kOffset);
-            }
-            __syncwarp();  // before the next sums
-        } else if (lane == 0) {
-            s_part[which] = Part{seg.item, seg.n, seg.kv_head, seg.row, seg.rows};
         }
     };
 #pragma unroll 1
@@ -819,7 +851,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         for (int w = w0; w < w1; ++w, at += S::kRing) add(sum, s_share[2 * w + 1][row], *reinterpret_cast<const float4*>(at));
         if (began) {
             const int j = __ffs(began) - 1;
-            add(sum, s_share[j][row], *reinterpret_cast<const float4*>(place_of(j >> 1, 0) + row * D + d));
+            add(sum, s_share[j][row], *reinterpret_cast<const float4*>(place_of(j >> 1) + row * D + d));
         }
         if (inside) finish(p, row, d, sum, s_top[j0][row], s_weight[j0][row]);
         else *reinterpret_cast<float4*>(part_of(blockIdx.x, p.item >= begin) + row * D + d) = sum;
