@@ -769,7 +769,7 @@ ARFUSE_API ar_status ar_attn_device_error(ar_attn* attn, int* code);
  *   freq         host fp64 [rot / 2]: radians a position, finite (any scaling of
  *                long contexts is in them)
  *   axis         host int32 [rot / 2], 0 .. axes - 1; NULL: axis 0 for all
- * Angles are formed and reduced in fp64.  Copies the table to the device and waits
+ * Angles are formed in 64-bit fractions of a turn (freq / (2 pi) rounded to fp64).  Copies the table to the device and waits
  * for that: call it outside any stream capture, with no ar_attn_append of this
  * handle running.
  * Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (rot not a multiple of 16),

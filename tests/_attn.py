@@ -23,9 +23,9 @@ def rotated(x, positions, freq, axis, interleaved):
 
 
 def rope_slack(x, freq, interleaved):
-    """What the turned values may be off before they are rounded: the reduced angle, |2 pi frac| <= pi, is good to its last
-    place (2^-24 of it twice: fp64's remainder to fp32, and the doubling is exact), sincospi to 2^-22 with it; two products
-    and a sum add 2^-23: together less than 2^-20 of |a| + |b|."""
+    """What the turned values may be off before they are rounded: the reduced angle, |2 pi frac| <= pi, is cut to 2^-32 of a
+    turn and good to its last place (2^-24 of it), sincospi to 2^-22 with it; two products and a sum add 2^-23: together less
+    than 2^-20 of |a| + |b|."""
     slack, n = torch.zeros_like(x, dtype=torch.float64), len(freq)
     cols = torch.arange(n, device=x.device)
     a, b = (2 * cols, 2 * cols + 1) if interleaved else (cols, cols + n)

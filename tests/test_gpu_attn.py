@@ -522,6 +522,31 @@ def test_append_the_last_token_of_a_slot_stands(T):
     m.destroy()
 
 
+def test_append_angles_at_the_ends_of_their_range():
+    # turns a position rounded to 64 bits, as documented; times the position, less the whole turns, exactly
+    from fractions import Fraction
+    heads, kv, D, page = 1, 1, 64, 16
+    freq = [1.0, -1.0, 3.0, -0.5, 1e-6, -1e-9, 1e4, -12345.678, math.pi, -2 * math.pi, 2 ** 40 * 1.1, 1e300, -1e-300, 0.0, 5e-324, -7.25]
+    where = [0, 1, -1, 2, 7, 100, -100, 2 ** 31 - 1, -2 ** 31, -2 ** 31 + 1, 10 ** 9, -123456789]
+    g = gen(61)
+    k, v, _, _ = paged(2, page, kv, D, False, "token", g)
+    qkv = normal((len(where), (heads + 2 * kv) * D), g)
+    m = arf.ar_attn_create(heads, kv, D, page, 1, device=0)
+    arf.ar_attn_set_rope(m, freq)
+    q = arf.ar_attn_append(m, arf.ar_kv_cache(k, v), qkv, torch.tensor([where], dtype=torch.int32, device=DEV),
+                           torch.arange(len(where), dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    frac = [[Fraction(f / 6.283185307179586476925286766559) * t % 1 for f in freq] for t in where]
+    angle = 2 * math.pi * torch.tensor([[float(x) for x in row] for row in frac], dtype=torch.float64, device=DEV)
+    n, c, s = len(freq), torch.cos(angle), torch.sin(angle)
+    for got, x in ((q[:, 0], qkv[:, :D]), (k.view(-1, D)[:len(where)], qkv[:, D:2 * D])):
+        a, b = x[:, :n].double(), x[:, n:2 * n].double()
+        want = torch.cat([a * c - b * s, b * c + a * s, x[:, 2 * n:].double()], 1)
+        bound = _attn.HALF_BF16 * want.abs() * (1 + 2.0 ** -8) + _attn.rope_slack(x, freq, False) + 2.0 ** -134
+        assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).max())
+    m.destroy()
+
+
 def test_append_most_tokens():
     # as many as a call takes, every slot named twice, far apart, and every 9th row padded
     heads, kv, D, page, T = 2, 1, 64, 16, arf.AR_MAX_ATTN_TOKENS

@@ -208,7 +208,9 @@ ar_status ar_attn_set_rope(ar_attn* m, int rot, int interleaved, int axes, const
     std::memset(&t, 0, sizeof t);
     for (int i = 0; i < rot / 2; ++i) {
         if (!std::isfinite(freq[i]) || (axis && (axis[i] < 0 || axis[i] >= axes))) return AR_ERR_INVALID_ARG;
-        t.turns[i] = freq[i] / 6.283185307179586476925286766559;
+        const double turns = std::fabs(freq[i]) / 6.283185307179586476925286766559;
+        t.turns[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+        if (freq[i] < 0) t.turns[i] = 0 - t.turns[i];
         t.axis[i] = axis ? axis[i] : 0;
     }
     if (!(m->flags & AR_WS_DRY_RUN)) {

@@ -5,9 +5,12 @@
 //
 // A piece is sixteen values of a head, of which a thread loads, turns and stores two
 // groups of eight: both halves of eight pairs, so no value is exchanged between threads.
-// A token's cosines and sines are formed once a CTA, in shared memory: the angle in
-// fp64 turns, less its whole turns, so that far positions lose nothing, then sincospi
-// in fp32.
+// A token's cosines and sines are formed once a CTA, in shared memory: the angle as a
+// fraction of a turn in 64-bit integers, whose overflow takes the whole turns off, so that
+// far positions lose nothing, then sincospi in fp32 of its upper half.
+//
+// What bounds it: memory, for many tokens (8192 of 64 + 2 x 8 heads of 128 columns: 57 us, 5.9 TB/s
+// of what is read and written), and for few the launch, the slots and the positions (2.8 us).
 //
 // Of tokens with one slot the last one wins whatever order the CTAs run in: each CTA
 // looks through the slots behind its own tokens and leaves out what is written again.
@@ -22,6 +25,8 @@ constexpr int kMaxTokens = 64;  // of a CTA
 constexpr int kTableTokens = 4; // whose angles are in shared memory at a time
 constexpr int kHashBits = 14;
 constexpr int kAhead = 4;       // pieces that a thread has asked for
+constexpr int kScan = 8;        // slots that a thread has asked for
+constexpr int kCtas = 5;        // that an SM has room for
 
 // Sixteen bytes of what the kernel before may have written, to a place that only this thread reads.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -53,7 +58,7 @@ __device__ __forceinline__ void store8(const CacheView& c, int head, int64_t tok
     *reinterpret_cast<uint2*>(row + chunk * 8) = v;
 }
 
-__global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_constant__ AppendArgs a, int tokens_per_cta) {
+__global__ void __launch_bounds__(kThreads, kCtas) attn_append_kernel(const __grid_constant__ AppendArgs a, int tokens_per_cta) {
     __shared__ int s_slot[kMaxTokens];
     __shared__ int s_dead[kMaxTokens];
     __shared__ int64_t s_k[kMaxTokens], s_v[kMaxTokens];  // byte offsets of the tokens' places, -1: none
@@ -125,12 +130,12 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
         __syncthreads();
         // eight loads in flight: one after the other they would take longer than the copies
 #pragma unroll 1
-        for (int t = t0 + 1 + threadIdx.x; t < a.T; t += 8 * kThreads) {
-            int later[8];
+        for (int t = t0 + 1 + threadIdx.x; t < a.T; t += kScan * kThreads) {
+            int later[kScan];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) later[k] = t + k * kThreads < a.T ? a.slots[t + k * kThreads] : -1;
+            for (int k = 0; k < kScan; ++k) later[k] = t + k * kThreads < a.T ? a.slots[t + k * kThreads] : -1;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kScan; ++k) {
                 const unsigned h = (unsigned)later[k] & ((1u << kHashBits) - 1);
                 if (later[k] < 0 || !(s_hash[h >> 5] >> (h & 31) & 1)) continue;
 #pragma unroll 1
@@ -154,9 +159,9 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
         const int n = min(kTableTokens, count - b);
         for (int j = threadIdx.x; j < n * pairs; j += kThreads) {
             const int t = j / pairs, pair = j - t * pairs;
-            const double turns = a.positions[(int64_t)a.rope->axis[pair] * a.T + t0 + b + t] * a.rope->turns[pair];
+            const uint64_t turns = (int64_t)a.positions[(int64_t)a.rope->axis[pair] * a.T + t0 + b + t] * a.rope->turns[pair];
             float s, c;
-            sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+            sincospif((float)(int)(turns >> 32) * 0x1p-31f, &s, &c);
             s_turn[t][(pair & 7) >> 1][pair >> 3][pair & 1] = make_float2(c, s);
         }
         __syncthreads();
@@ -218,8 +223,9 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(const __grid_cons
 
 cudaError_t launch_attn_append(const AppendArgs& a, int num_sms, cudaStream_t stream) {
     const int pieces = (a.heads + 2 * a.kv) * (a.D / 16);
-    // few tokens: a token's pieces over several CTAs; many: several tokens a CTA
-    const int target = 8 * num_sms;
+    // Few tokens: a token's pieces over several CTAs; many: several tokens a CTA, so that all CTAs have room at once.  (1024
+    // tokens of 32 + 2 x 8 heads of 128 columns: 7.4 us; with eight CTAs to an SM in two waves, 10.0; 8192 of them 38.1 and 41.3.)
+    const int target = kCtas * num_sms;
     int tokens = (a.T + target - 1) / target;
     if (tokens > kMaxTokens) tokens = kMaxTokens;
     const int blocks = (a.T + tokens - 1) / tokens;

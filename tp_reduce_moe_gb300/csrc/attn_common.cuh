@@ -22,7 +22,7 @@ struct CacheView {
 
 // The rotary table in device memory.
 struct RopeTable {
-    double turns[kMaxHeadDim / 2];  // freq / (2 pi): turns a position
+    uint64_t turns[kMaxHeadDim / 2];  // freq / (2 pi), turns a position, less the whole ones, in units of 2^-64
     int32_t axis[kMaxHeadDim / 2];
 };
 

@@ -16,12 +16,12 @@
 //
 // A warp streams its units through a ring of its own in shared memory, keys and values in
 // turn, by 16-byte asynchronous copies that run ahead across items, so that no barrier stands
-// in the stream.  Items within a warp's range are finished from its registers; what is cut is added up
-// once, at the end of the CTA, in the order of the warps, and over CTAs by the last of them to
-// arrive, in the order of the CTAs.  No CTA waits for another.
+// in the stream.  Items within a warp's range are finished from its registers; what is cut is
+// added up once, at the end of the CTA, in the order of the warps, and over CTAs by the last of
+// them to arrive, in the order of the CTAs.  No CTA waits for another.
 //
 // What bounds it.  Memory, where there is much: 64 sequences of 256 to 8192 tokens (eight
-// key-value heads of 128 columns, 610 MB) take 103 us, 5.9 TB/s.  Else the way there and back,
+// key-value heads of 128 columns, 610 MB) take 100 to 104 us, 6 TB/s.  Else the way there and back,
 // some 13 us: lengths and plan 2, the page's number and the first keys 2 to 3, the spread of
 // the SMs' ends up to 3, a CTA's sums 2.5, joins 3 for each level.  A sequence of 500 tokens
 // takes 10 us, of which the one SM reads for 3; one of 131071 (134 MB) 32.5.
