@@ -600,3 +600,19 @@ def test_append_undefined_and_large_values_in_8_bits():
     # halves between two codes go to the even one
     assert got[0] != got[0] and got[1:] == [448.0, -448.0, 448.0, -448.0, 448.0, 2.0 ** -9, 0.0, 0.0, 0.0, 0.0, 16.0, 20.0]
     m.destroy()
+
+
+def test_append_scales_at_the_ends_of_their_range():
+    # powers of two: every quotient is exact
+    m = arf.ar_attn_create(3, 3, 64, 4, 1, device=0)
+    for scales in ([2.0 ** -133, 2.0 ** -126, 2.0 ** -127], [2.0 ** 127, 2.0 ** 100, 1.0], [-2.0 ** -140, -4.0, 2.0 ** -149]):
+        k, v, _, _ = paged(1, 4, 3, 64, True, "token", gen(34))
+        s = torch.tensor(scales, device=DEV)
+        codes = torch.tensor([1.0, -8.0, 448.0, 0.0, 2.0 ** -6, 2.0 ** -9, -0.4375, 13.0], device=DEV)
+        values = (codes.double() * s.double().unsqueeze(1)).float().bfloat16()  # (small ones may become 0)
+        qkv = torch.zeros(1, 9, 64, dtype=torch.bfloat16, device=DEV)
+        qkv[0, 3:6, :8], qkv[0, 6:, 56:] = values, values
+        arf.ar_attn_append(m, arf.ar_kv_cache(k, v, s, s), qkv.view(1, -1), None, torch.tensor([1], dtype=torch.int32, device=DEV))
+        want = (values.double() / s.double().unsqueeze(1)).clamp(-448, 448).float().to(F8).float()
+        assert torch.equal(k[0, 1, :, :8].float(), want) and torch.equal(v[0, 1, :, 56:].float(), want), scales
+    m.destroy()

@@ -38,11 +38,12 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Chunks (of eight columns) of piece p of a head: its own two, or both halves of eight pairs.
-__device__ __forceinline__ void chunks_of(int p, int rot, bool split, int* lo, int* hi) {
-    const bool halves = split && p < rot / 16;
-    *lo = halves ? p : 2 * p;
-    *hi = halves ? p + rot / 16 : 2 * p + 1;
+// Chunks (of eight columns) of piece p of a head: one of each half of the rotated columns, or of those behind, so that
+// neighbouring threads' are neighbours (and sectors of memory are asked for once).
+__device__ __forceinline__ void chunks_of(int p, int rot, int all, int* lo, int* hi) {
+    const int turned = rot / 16;
+    *lo = p < turned ? p : p + turned;
+    *hi = *lo + (p < turned ? turned : all - turned);
 }
 
 __device__ __forceinline__ void store8(const CacheView& c, int head, int64_t token, int chunk, const float f[8]) {
@@ -63,8 +64,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_append_kernel(const __gr
     __shared__ int s_dead[kMaxTokens];
     __shared__ int64_t s_k[kMaxTokens], s_v[kMaxTokens];  // byte offsets of the tokens' places, -1: none
     __shared__ unsigned s_hash[1 << (kHashBits - 5)];
-    // cosine and sine of a token's pairs 8 p + 2 j and 8 p + 2 j + 1 at [j][p]: neighbouring pieces' in neighbouring banks
-    __shared__ __align__(16) float2 s_turn[kTableTokens][4][kMaxHeadDim / 16][2];
+    // Cosine and sine of a token's pairs, two beside each other, so that neighbouring pieces' are in neighbouring banks:
+    // 8 p + 2 j and the next at 32 j + 2 p; of neighbouring columns 4 c + 2 k and the next, those of chunk c, at 64 k + 2 c.
+    __shared__ __align__(16) float2 s_turn[kTableTokens][kMaxHeadDim / 2];
     __shared__ uint4 s_piece[kAhead][2][kThreads];
     pdl_trigger();
     pdl_wait();  // no global memory access before this point
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_append_kernel(const __gr
         if (next.t < count) {
             const int r = first + next.r, head = r >> shift;
             int lo, hi;
-            chunks_of(r - (head << shift), head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
+            chunks_of(r - (head << shift), head < a.heads + a.kv ? a.rot : 0, per_head, &lo, &hi);
             const uint16_t* row = rows + (next.t * all_heads + head) * a.D;
             copy16(smem_addr(&s_piece[into][0][threadIdx.x]), row + lo * 8);
             copy16(smem_addr(&s_piece[into][1][threadIdx.x]), row + hi * 8);
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_append_kernel(const __gr
             const uint64_t turns = (int64_t)a.positions[(int64_t)a.rope->axis[pair] * a.T + t0 + b + t] * a.rope->turns[pair];
             float s, c;
             sincospif((float)(int)(turns >> 32) * 0x1p-31f, &s, &c);
-            s_turn[t][(pair & 7) >> 1][pair >> 3][pair & 1] = make_float2(c, s);
+            s_turn[t][a.interleaved ? (pair & 2) * 32 + (pair >> 2) * 2 + (pair & 1) : (pair & 6) * 16 + (pair >> 3) * 2 + (pair & 1)] = make_float2(c, s);
         }
         __syncthreads();
         for (; use.t < b + n; follow(use)) {
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_append_kernel(const __gr
             const int t = use.t, r = first + use.r, head = r >> shift, p = r - (head << shift);
             const bool turned = head < a.heads + a.kv && p < a.rot / 16;
             int lo, hi;
-            chunks_of(p, head < a.heads + a.kv ? a.rot : 0, a.interleaved == 0, &lo, &hi);
+            chunks_of(p, head < a.heads + a.kv ? a.rot : 0, per_head, &lo, &hi);
             float u[8], v[8];
             bf16x8_to_f32(x_lo, u);
             bf16x8_to_f32(x_hi, v);
@@ -181,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_append_kernel(const __gr
                 float2 table[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<float4*>(table + 2 * j) = *reinterpret_cast<const float4*>(s_turn[t - b][j][p]);
+                    *reinterpret_cast<float4*>(table + 2 * j) =
+                        *reinterpret_cast<const float4*>(&s_turn[t - b][a.interleaved ? (j & 1) * 64 + (j < 2 ? lo : hi) * 2 : j * 32 + p * 2]);
                 if (a.interleaved) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
