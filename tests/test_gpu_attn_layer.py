@@ -161,3 +161,20 @@ def test_one_call_is_one_kernel_launch():
         assert len(names) == 1 and kernel in names[0], names
     layer.attn.destroy()
     layer.ws.destroy()
+
+
+def test_readme_example():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    blocks = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "ar_attn_append" in b]
+    assert len(blocks) == 1
+    scope = dict(torch=torch, arf=arf)
+    exec(compile(blocks[0], "README.md", "exec"), scope)
+    q, k, v, table, lengths = (scope[n] for n in ("q", "k", "v", "table", "lengths"))
+    for b in range(2):  # the new token's values are where they belong
+        at = int(lengths[b]) - 1
+        x = scope["qkv"][b].view(-1, scope["D"])
+        assert torch.equal(v[int(table[b, at // scope["page"]]), at % scope["page"]], x[scope["heads"] + scope["kv"]:])
+    want, slack, _, _ = _attn.decode_ref(q, k, v, table, lengths.tolist(), scope["page"], 0, scope["D"] ** -0.5)
+    assert bool(((scope["ctx"].double() - want).abs() <= slack).all())
