@@ -709,7 +709,7 @@ ARFUSE_API ar_status ar_matvec_w4(const void* x, const void* q, const void* s, i
  * and values in one tensor are all possible.  It holds bf16, or (scales given)
  * e4m3 bytes that stand for byte * scale[head].
  */
-#define AR_MAX_ATTN_HEADS 256     /* query heads                              */
+#define AR_MAX_ATTN_HEADS 1024    /* query heads                              */
 #define AR_MAX_ATTN_SEQS 4096     /* sequences of ar_attn_decode              */
 #define AR_MAX_ATTN_TOKENS 65536  /* tokens of one ar_attn_append             */
 #define AR_MAX_PAGE_SIZE 65536    /* tokens of a page                         */

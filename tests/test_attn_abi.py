@@ -32,7 +32,7 @@ def addr(i):
 @pytest.mark.parametrize("args,status", [
     ((0, 1, 128, 16, 4, 0), arf.AR_ERR_INVALID_ARG),      # heads
     ((-8, 1, 128, 16, 4, 0), arf.AR_ERR_INVALID_ARG),
-    ((257, 257, 128, 16, 4, 0), arf.AR_ERR_UNSUPPORTED),
+    ((1025, 1025, 128, 16, 4, 0), arf.AR_ERR_UNSUPPORTED),
     ((8, 0, 128, 16, 4, 0), arf.AR_ERR_INVALID_ARG),      # kv_heads
     ((8, 3, 128, 16, 4, 0), arf.AR_ERR_INVALID_ARG),
     ((8, 16, 128, 16, 4, 0), arf.AR_ERR_INVALID_ARG),

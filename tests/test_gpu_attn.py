@@ -113,6 +113,9 @@ DECODES = [  # heads, kv, D, page, eight, layout, window, lengths
     (40, 2, 128, 16, False, "pair", 1, [300, 1, 0, 16, 17]),
     (256, 1, 128, 16, False, "token", 0, [900, 30]),
     (256, 256, 64, 16, False, "token", 0, [40, 7]),
+    (320, 16, 128, 20, False, "head", 0, [400, 1, 90]),
+    (1024, 1024, 64, 16, True, "token", 0, [33]),
+    (1024, 8, 256, 16, False, "token", 20, [70, 19]),
     (24, 8, 128, 1000, False, "token", 0, [999, 1000, 1001, 2500]),
     (80, 1, 256, 3, True, "token", 0, [100, 50, 1]),
     (4, 2, 64, 16, False, "token", 5000, [40000, 10]),
@@ -429,6 +432,8 @@ APPENDS = [  # heads, kv, D, rot, axes, interleaved, page, eight, layout, T, pad
     (3, 3, 128, 0, 0, False, 16, False, "token", 9, 1, 10),
     (3, 1, 128, 0, 0, False, 16, True, "token", 9, 1, 10),
     (256, 256, 64, 32, 1, False, 16, False, "token", 3, 0, 99),
+    (320, 16, 128, 128, 1, False, 16, True, "token", 70, 3, 4000),
+    (1024, 1024, 256, 256, 2, True, 16, False, "token", 9, 1, 99),
     (4, 2, 64, 64, 3, False, 128, False, "token", 5000, 100, 5000),
     (1, 1, 64, 64, 1, False, 16, True, "token", 1300, 0, 5000),
 ]

@@ -60,7 +60,7 @@ AR_MAX_MATVEC_ROWS = 1048576
 AR_MOE_SOFTMAX = 0
 AR_MOE_SIGMOID = 1
 AR_MOE_GROUP_MAX = 0x10
-AR_MAX_ATTN_HEADS = 256
+AR_MAX_ATTN_HEADS = 1024
 AR_MAX_ATTN_SEQS = 4096
 AR_MAX_ATTN_TOKENS = 65536
 AR_MAX_PAGE_SIZE = 65536
