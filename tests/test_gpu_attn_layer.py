@@ -178,3 +178,37 @@ def test_readme_example():
         assert torch.equal(v[int(table[b, at // scope["page"]]), at % scope["page"]], x[scope["heads"] + scope["kv"]:])
     want, slack, _, _ = _attn.decode_ref(q, k, v, table, lengths.tolist(), scope["page"], 0, scope["D"] ** -0.5)
     assert bool(((scope["ctx"].double() - want).abs() <= slack).all())
+
+
+def test_first_calls_are_captured():
+    # a fresh process, nothing launched before: the kernels load during the capture
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, tp_reduce_moe_gb300 as arf
+bf = dict(device="cuda", dtype=torch.bfloat16)
+i32 = lambda x: torch.tensor(x, device="cuda", dtype=torch.int32)
+k, v = torch.zeros(8, 16, 2, 128, **bf), torch.zeros(8, 16, 2, 128, **bf)
+cache = arf.ar_kv_cache(k, v)
+attn, ws = arf.ar_attn_create(8, 2, 128, 16, 4), arf.ar_workspace_create(2, 0, 1024, 4096, 1e-6)
+qkv, slots, table, lengths = torch.ones(2, 12 * 128, **bf), i32([0, 17]), i32([[0], [1]]), i32([1, 2])
+parts = {T: [torch.ones(T, 1024, **bf) for _ in range(3)] for T in (2, 4096)}
+gamma = torch.ones(1024, **bf)
+torch.cuda.synchronize()
+s = torch.cuda.Stream()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=s):
+    q = arf.ar_attn_append(attn, cache, qkv, None, slots)
+    out = arf.ar_attn_decode(attn, cache, q, table, lengths)
+    norms = [arf.ar_rmsnorm_q8(ws, p[:2], p[2], gamma, 0.0, 1e-6) for p in parts.values()]
+g.replay()
+torch.cuda.synchronize()
+assert bool((out == 1).all())  # (of the second two tokens one is zeros and weighs e^-11)
+for y, scale, h in norms:
+    assert bool((h == 3).all()) and bool(((y.float() * scale.repeat_interleave(128, 1) - 1).abs() < 2.0 ** -4).all())
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
