@@ -343,6 +343,9 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     int ask_u = 0, ask_u1 = 0, ask_last = 0;  // of the segment that is asked for: next unit, end, last page of the sequence
     const uint8_t *k_head = nullptr, *v_head = nullptr;  // and its keys and values
     unsigned asked = 0, found = 0;  // units asked for, segments found
+    // Copies are issued without a pause where latencies count (500 tokens 10.3 us with pauses, 9.4 without), and one behind its
+    // place in the table where memory has all it can do (610 MB 103.5 us without pauses, 100.3 with; 1 GB 170.9 and 164.9).
+    const bool quick = EIGHT || NT > 1 || total < S::kMany;
     constexpr unsigned kAll = 0xffffffffu >> (32 - TOK);
     unsigned present = 0;           // tokens of the unit that was looked up
     uint32_t fill = 0;              // place in the ring that is filled next
@@ -393,13 +396,20 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
         if (live) {
             const uint8_t* const* rows = s_row[warp][which] + lane / S::kChunks;
             const int c = lane % S::kChunks;
-            if (present == kAll) {
+            if (present == kAll && quick) {
+                // (places first, some at a time: one that is read behind a copy waits for it to be issued)
+                constexpr int kCopies = TOK * S::kChunks / 32, kBatch = kCopies < 4 ? kCopies : 4;
 #pragma unroll
-                for (int i = 0; i < TOK * S::kChunks / 32; ++i)
-                    copy16(ring + fill + S::place((i * 32 + lane) / S::kChunks, c), rows[i * 32 / S::kChunks] + c * 16, policy);
+                for (int i0 = 0; i0 < kCopies; i0 += kBatch) {
+                    const uint8_t* from[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) from[i] = rows[(i0 + i) * 32 / S::kChunks] + c * 16;
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) copy16(ring + fill + S::place(((i0 + i) * 32 + lane) / S::kChunks, c), from[i], policy);
+                }
             } else {
                 // (zeros that are read would all come from one place: 1184 single tokens take 21 us with them)
-#pragma unroll 1
+#pragma unroll 4
                 for (int i = 0; i < TOK * S::kChunks; i += 32) {
                     const int row = (i + lane) / S::kChunks;
                     copy16_or_zeros(ring + fill + S::place(row, c), rows[i / S::kChunks] + c * 16, present >> row & 1 ? 16 : 0, policy);
