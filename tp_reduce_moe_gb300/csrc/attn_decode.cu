@@ -24,7 +24,7 @@
 // key-value heads of 128 columns, 610 MB) take 100 to 104 us, 6 TB/s.  Else the way there and back,
 // some 13 us: lengths and plan 2, the page's number and the first keys 2 to 3, the spread of
 // the SMs' ends up to 3, a CTA's sums 2.5, joins 3 for each level.  A sequence of 500 tokens
-// takes 10 us, of which the one SM reads for 3; one of 131071 (134 MB) 32.5.
+// takes 9.5 us, of which the one SM reads for 3; one of 131071 (134 MB) 32.5.
 //
 // Roundings: scores, maxima, sums and o are fp32.  Weights go to the matrix instruction as
 // two bf16 (their rounding and its remainder: 2^-17, where one bf16 would add 0.7 times the
@@ -63,9 +63,10 @@ struct Shape {
     // 23.1.)
     static constexpr int kCost = 4;
     static constexpr int kMany = (1 << 27) / kHalf;  // units that are too many for all SMs (256 MB)
-    // Units by which a CTA that keeps an item may pass an equal share.  (One sequence, eight heads of 128 columns: 500 tokens
-    // 10.2 us by one CTA, 10.5 cut; 600 10.8 and 11.1; 700 11.7 and 10.7.)
-    static constexpr int kAlone = 172032 / kHalf;
+    // Units by which a CTA that keeps an item may pass an equal share: 2.6 a warp.  (One sequence, eight heads of 128 columns: 500
+    // tokens 9.6 us by one CTA, 10.4 cut; 600 10.2 and 10.4; 700 10.9 and 10.3.  8-bit ones of 64 columns: 1000 7.8 and 9.0, 2000
+    // 10.4 and 9.3.)
+    static constexpr int kAlone = kWarps * 21 / 8;
     static constexpr int kPitch = D + 4;       // floats from a row of sums to the next in shared memory, free of bank conflicts
     // In memory nothing is between the rows: sectors that are not written whole would have to be read before they are merged.
     static constexpr int kSums = kRows * D;
