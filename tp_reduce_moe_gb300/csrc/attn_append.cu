@@ -9,7 +9,7 @@
 // fraction of a turn in 64-bit integers, whose overflow takes the whole turns off, so that
 // far positions lose nothing, then sincospi in fp32 of its upper half.
 //
-// What bounds it: memory, for many tokens (8192 of 64 + 2 x 8 heads of 128 columns: 57 us, 5.9 TB/s
+// What bounds it: memory, for many tokens (8192 of 64 + 2 x 8 heads of 128 columns: 55.6 us, 6 TB/s
 // of what is read and written), and for few the launch, the slots and the positions (2.8 us).
 //
 // Of tokens with one slot the last one wins whatever order the CTAs run in: each CTA
