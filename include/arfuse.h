@@ -731,7 +731,7 @@ typedef struct ar_kv_cache {
  * Create the handle of a model's attention layers (shared by the layers, as a
  * workspace is).  Allocates on `device` its scratch: parts of rows split over
  * several warps and CTAs (225 * SMs * head_dim fp32: 18 MB at head_dim 128 on 152 SMs),
- * their counters, the rotary table and the error word.  Calls on one handle must be
+ * their counters and the error word.  Calls on one handle must be
  * ordered on the GPU (one stream, or event ordering; graphs captured on it must not
  * run at the same time); concurrent callers need a handle each.  Call it outside
  * any stream capture.
@@ -769,11 +769,13 @@ ARFUSE_API ar_status ar_attn_device_error(ar_attn* attn, int* code);
  *   freq         host fp64 [rot / 2]: radians a position, finite (any scaling of
  *                long contexts is in them)
  *   axis         host int32 [rot / 2], 0 .. axes - 1; NULL: axis 0 for all
- * Angles are formed in 64-bit fractions of a turn (freq / (2 pi) rounded to fp64).  Copies the table to the device and waits
- * for that: call it outside any stream capture, with no ar_attn_append of this
- * handle running.
+ * Angles are formed in 64-bit fractions of a turn (freq / (2 pi) rounded to fp64).
+ * Copies the table to the device and waits for that: call it outside any stream
+ * capture.  Calls made before keep the table that was in force then, whether they
+ * still run or are captured and replayed later: the handle holds every different
+ * table that it has been given (1.5 KB of the device each) until it is destroyed.
  * Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (rot not a multiple of 16),
- * AR_ERR_CUDA.  The table before stays in force on an error, but for AR_ERR_CUDA.
+ * AR_ERR_CUDA.  The table before stays in force on an error.
  */
 ARFUSE_API ar_status ar_attn_set_rope(ar_attn* attn, int rot, int interleaved, int axes,
                                       const double* freq, const int32_t* axis);

@@ -834,7 +834,8 @@ def ar_attn_set_rope(attn: Attn, freq, axis=None, interleaved: bool = False, axe
     ``freq[i]`` radians a position on axis ``axis[i]`` (0 when not given).  Pairs are columns
     i and i + len(freq), or (interleaved) 2 i and 2 i + 1.  ``axes``: rows of the positions
     tensor (the largest axis named, and one more, when not given).  Waits for the device's
-    copy of the table: not inside a stream capture."""
+    copy of the table: not inside a stream capture.  Calls that were made or captured before
+    keep what was set then."""
     freq = [float(f) for f in freq]
     n = len(freq)
     if axis is not None:

@@ -14,6 +14,20 @@ static_assert(arf::kErrPageRange == AR_DEVERR_PAGE_RANGE && arf::kErrSlotRange =
                   arf::kErrLengthRange == AR_DEVERR_LENGTH_RANGE,
               "the kernels' error bits are the header's");
 
+namespace {
+
+// Rotary tables that a handle has had, on the device and (to find one that is set again) here.  One is never written again:
+// calls in flight and captured ones hold its address.
+constexpr int kChunkTables = 64;
+struct RopeChunk {
+    RopeChunk* next;
+    arf::RopeTable* d_tables;
+    int used;
+    arf::RopeTable tables[kChunkTables];
+};
+
+}  // namespace
+
 struct ar_attn {
     int device;
     int heads, kv, D, page_size;
@@ -24,8 +38,9 @@ struct ar_attn {
     uint8_t* d_mem;              // everything below
     unsigned* d_err;
     unsigned* d_count;  // zero between calls
-    arf::RopeTable* d_rope;
     float* d_part;
+    RopeChunk* ropes;                // latest first
+    const arf::RopeTable* d_rope;    // the table in force
 };
 
 namespace {
@@ -50,6 +65,28 @@ ar_status launched(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;
     (void)cudaGetLastError();
     return AR_ERR_CUDA;
+}
+
+// A table's place on the device, nullptr if there is none to be had.  A new one is complete there before this returns.
+const arf::RopeTable* place_of_rope(ar_attn* m, const arf::RopeTable& t) {
+    for (RopeChunk* c = m->ropes; c; c = c->next)
+        for (int i = 0; i < c->used; ++i)
+            if (std::memcmp(&c->tables[i], &t, sizeof t) == 0) return c->d_tables + i;
+    RopeChunk* c = m->ropes;
+    if (!c || c->used == kChunkTables) {
+        c = new (std::nothrow) RopeChunk();
+        if (!c) return nullptr;
+        if (cudaMalloc(&c->d_tables, sizeof c->tables) != cudaSuccess) {
+            delete c;
+            return nullptr;
+        }
+        c->next = m->ropes;
+        m->ropes = c;
+    }
+    if (cudaMemcpy(c->d_tables + c->used, &t, sizeof t, cudaMemcpyHostToDevice) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
+        return nullptr;
+    c->tables[c->used] = t;
+    return c->d_tables + c->used++;
 }
 
 struct Dim {
@@ -134,7 +171,7 @@ ar_status ar_attn_create(int device, int heads, int kv_heads, int head_dim, int 
         return AR_OK;
     }
     int prev = -1, major = 0;
-    size_t count = 0, rope = round_up(sizeof(arf::RopeTable));
+    size_t count = 0;
     ar_status st = AR_ERR_CUDA;
     if (cudaGetDevice(&prev) == cudaSuccess && cudaSetDevice(device) == cudaSuccess &&
         cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) == cudaSuccess &&
@@ -144,8 +181,8 @@ ar_status ar_attn_create(int device, int heads, int kv_heads, int head_dim, int 
         if (major < 10)
             st = AR_ERR_UNSUPPORTED;
         else if (arf::attn_decode_set_attributes() == cudaSuccess &&
-                 cudaMalloc(&m->d_mem, 256 + count + rope + part) == cudaSuccess &&
-                 cudaMemset(m->d_mem, 0, 256 + count + rope) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess)
+                 cudaMalloc(&m->d_mem, 256 + count + part) == cudaSuccess &&
+                 cudaMemset(m->d_mem, 0, 256 + count) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess)
             st = AR_OK;
     }
     if (st != AR_OK) {
@@ -158,8 +195,7 @@ ar_status ar_attn_create(int device, int heads, int kv_heads, int head_dim, int 
     (void)cudaSetDevice(prev);
     m->d_err = reinterpret_cast<unsigned*>(m->d_mem);
     m->d_count = reinterpret_cast<unsigned*>(m->d_mem + 256);
-    m->d_rope = reinterpret_cast<arf::RopeTable*>(m->d_mem + 256 + count);
-    m->d_part = reinterpret_cast<float*>(m->d_mem + 256 + count + rope);
+    m->d_part = reinterpret_cast<float*>(m->d_mem + 256 + count);
     *out = m;
     return AR_OK;
 }
@@ -170,7 +206,14 @@ ar_status ar_attn_destroy(ar_attn* m) {
     if (m->d_mem) {
         int prev = -1;
         (void)cudaGetDevice(&prev);
-        if (cudaSetDevice(m->device) != cudaSuccess || cudaFree(m->d_mem) != cudaSuccess) {
+        bool ok = cudaSetDevice(m->device) == cudaSuccess;
+        ok = ok && cudaFree(m->d_mem) == cudaSuccess;
+        while (RopeChunk* c = m->ropes) {
+            ok = ok && cudaFree(c->d_tables) == cudaSuccess;
+            m->ropes = c->next;
+            delete c;
+        }
+        if (!ok) {
             (void)cudaGetLastError();
             st = AR_ERR_CUDA;
         }
@@ -213,16 +256,14 @@ ar_status ar_attn_set_rope(ar_attn* m, int rot, int interleaved, int axes, const
         if (freq[i] < 0) t.turns[i] = 0 - t.turns[i];
         t.axis[i] = axis ? axis[i] : 0;
     }
-    if (!(m->flags & AR_WS_DRY_RUN)) {
+    if (rot > 0 && !(m->flags & AR_WS_DRY_RUN)) {
         int prev = -1;
         (void)cudaGetDevice(&prev);
-        // (the device is idle on this handle by contract; the copy from pageable memory returns when it is done)
-        const bool ok = cudaSetDevice(m->device) == cudaSuccess &&
-                        cudaMemcpy(m->d_rope, &t, sizeof t, cudaMemcpyHostToDevice) == cudaSuccess &&
-                        cudaDeviceSynchronize() == cudaSuccess;
-        if (!ok) (void)cudaGetLastError();
+        const arf::RopeTable* d = cudaSetDevice(m->device) == cudaSuccess ? place_of_rope(m, t) : nullptr;
+        if (!d) (void)cudaGetLastError();
         if (prev >= 0) (void)cudaSetDevice(prev);
-        if (!ok) return AR_ERR_CUDA;
+        if (!d) return AR_ERR_CUDA;
+        m->d_rope = d;
     }
     m->rot = rot;
     m->interleaved = interleaved;

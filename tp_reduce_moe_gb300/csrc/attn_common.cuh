@@ -20,7 +20,7 @@ struct CacheView {
     const float* scale;         // e4m3: [kv_heads]; bf16: nullptr
 };
 
-// The rotary table in device memory.
+// A rotary table in device memory, written once.
 struct RopeTable {
     uint64_t turns[kMaxHeadDim / 2];  // freq / (2 pi), turns a position, less the whole ones, in units of 2^-64
     int32_t axis[kMaxHeadDim / 2];
