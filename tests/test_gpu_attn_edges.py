@@ -4,7 +4,7 @@ import torch
 
 import tp_reduce_moe_gb300 as arf
 from tests import _attn
-from tests.test_gpu_attn import DEV, gen, normal, paged
+from tests.test_gpu_attn import DEV, check_decode, gen, normal, paged
 
 pytestmark = pytest.mark.gpu
 F8 = torch.float8_e4m3fn
@@ -89,4 +89,47 @@ def test_calls_in_flight_keep_their_rotary_positions():
     for freq, q in zip(ropes, outs):
         want, slack = _attn.rotated(x, pos, freq, None, False), _attn.rope_slack(x, freq, False)
         assert bool(((q.double() - want).abs() <= want.abs() * _attn.HALF_BF16 + slack * (1 + 2.0 ** -7)).all())
+    m.destroy()
+
+
+# ---------------------------------------------------------------- query rows of values far apart, over an 8-bit cache
+@pytest.mark.parametrize("D,heads", [(64, 4), (128, 8), (128, 16), (256, 3)])
+@pytest.mark.parametrize("far", [2.0 ** 10, 2.0 ** 20, 2.0 ** 27])
+def test_decode_small_columns_beside_a_large_one(D, heads, far):
+    # the large column meets keys of zero (or tiny ones): the scores are those of the others
+    page, lengths = 16, [150, 33]
+    g = gen(80 + D)
+    k, v, ks, vs = paged(20, page, 1, D, True, "token", g)
+    bits = k.view(torch.uint8)
+    bits[..., 5] = 0
+    bits[..., 40] = torch.tensor([2.0 ** -9], device=DEV).to(F8).view(torch.uint8)
+    q = normal((2, heads, D), g, 2.0)
+    q[..., 5] = far
+    q[0, 0, 40] = -far
+    table = torch.randperm(20, generator=g, device=DEV).int()[:20].view(2, 10)
+    m = arf.ar_attn_create(heads, 1, D, page, 2, device=0)
+    want, slack, want_lse, lse_slack = _attn.decode_ref(q, k, v, table, lengths, page, 0, D ** -0.5, ks, vs, True)
+    # Queries come to halves whose largest is 2^15 at least, so they are multiples of 2^-24 there: off by 2^-25 at most, 2^-40 of
+    # the largest.  A score is off by that times the sum of its key's magnitudes; weights and their sum by so much each.
+    off = 2.0 ** -40 * far * float(k.float().abs().sum(-1).max() * ks) * D ** -0.5
+    slack += 2 * off * 1.01 * float(v.float().abs().max() * vs)
+    lse_slack += off
+    out, lse = arf.ar_attn_decode(m, arf.ar_kv_cache(k, v, ks, vs), q, table, torch.tensor(lengths, dtype=torch.int32, device=DEV),
+                                  lse=torch.empty(2, heads, device=DEV))
+    assert bool(((out.double() - want).abs() <= slack).all()), f"out: {float(((out.double() - want).abs() / slack).max())} of the bound"
+    assert bool(((lse.double() - want_lse).abs() <= lse_slack).all())
+    m.destroy()
+
+
+@pytest.mark.parametrize("size,scale", [(2.0 ** 126, 2.0 ** -127), (2.0 ** 127, 2.0 ** -126), (2.0 ** -126, 2.0 ** 120), (2.0 ** -133, 2.0 ** 126), (2.0 ** -100, 2.0 ** 97)])
+def test_decode_queries_at_the_ends_of_their_range(size, scale):
+    # (the scale brings the scores back; keys and queries of few bits, so that no product passes the range on its way)
+    heads, D, page, n = 4, 64, 16, 90
+    g = gen(81)
+    k, v, ks, vs = paged(6, page, 1, D, True, "token", g)
+    k.view(torch.uint8).copy_((torch.randint(-2, 3, k.shape, generator=g, device=DEV) / 4).to(F8).view(torch.uint8))
+    q = (torch.randint(0, 2, (1, heads, D), generator=g, device=DEV) * size).bfloat16()
+    table = torch.arange(6, dtype=torch.int32, device=DEV).view(1, 6)
+    m = arf.ar_attn_create(heads, 1, D, page, 1, device=0)
+    check_decode(m, q, k, v, torch.ones_like(ks), vs, table, [n], scale=scale)
     m.destroy()

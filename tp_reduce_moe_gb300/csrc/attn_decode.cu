@@ -29,7 +29,8 @@
 // Roundings: scores, maxima, sums and o are fp32.  Weights go to the matrix instruction as
 // two bf16 (their rounding and its remainder: 2^-17, where one bf16 would add 0.7 times the
 // output's own rounding); with 8-bit values as halves (2^-11), whose products are exact, q
-// then scaled by a power of two a row to the halves' range.
+// then scaled by a power of two a row to the upper end of the halves' range: columns down to
+// 2^-29 of the row's largest keep all their bits, smaller ones are off by 2^-40 of it.
 #include "attn_common.cuh"
 
 #include <cuda_fp16.h>
@@ -519,9 +520,10 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
                         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[i][n][c] << 16)), fabsf(__uint_as_float(q[i][n][c] & 0xffff0000u))));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // the power of two that brings the row's largest value to [1, 2) (or next to it, at the ends of the range)
-                int e = (int)(__float_as_uint(top) >> 23) - 127;
-                e = e < -126 ? -126 : e > 126 ? 126 : e;
+                // the power of two that brings the row's largest value to [2^15, 2^16), less for rows below 2^-111 (65280 at most; a
+                // sum of 256 products with 448 stays below 2^33)
+                int e = (int)(__float_as_uint(top) >> 23) - 127 - 15;
+                e = e < -126 ? -126 : e > 112 ? 112 : e;
                 const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = ks * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i)
