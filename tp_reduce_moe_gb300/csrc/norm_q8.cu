@@ -79,6 +79,29 @@ __device__ __forceinline__ void add8(float h[8], uint4 v) {
     for (int j = 0; j < 8; ++j) h[j] += f[j];
 }
 
+// The largest |y| of a row, of the h that its norm reads, by all threads.
+template <int CPT>
+__device__ __forceinline__ float largest_of_row(const NormQ8Args& a, const float h[CPT][8], const uint4 gamma[CPT], float rs, float* s_top) {
+    float top = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+        float g[8];
+        bf16x8_to_f32(gamma[c], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(h[c][j] * rs * (g[j] + a.weight_bias)));
+    }
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    __syncthreads();  // what was in s_top has been read
+    if (lane == 0) s_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = lane < (int)(blockDim.x >> 5) ? s_top[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
+}
+
 // Everything behind the sum: h [CPT chunks of this thread], which is used up; of chunks behind the row it may be anything.
 // s_sum and s_top are not written again before all threads have come through a barrier behind this.  GROUP_LANES: lanes of
 // eight columns that share a scale; 0: the row.
@@ -95,17 +118,17 @@ __device__ __forceinline__ void finish_row(const NormQ8Args& a, int64_t t, float
         else
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[c][j] = 0.0f;
-        float g[8];
-        bf16x8_to_f32(gamma[c], g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float x = norm_input(h[c][j], a.norm_bf16_h);
-            sum = fmaf(x, x, sum);
-            h[c][j] = x * (g[j] + a.weight_bias);
+            h[c][j] = norm_input(h[c][j], a.norm_bf16_h);
+            sum = fmaf(h[c][j], h[c][j], sum);
         }
-        if (GROUP_LANES == 0)
+        if (GROUP_LANES == 0) {
+            float g[8];
+            bf16x8_to_f32(gamma[c], g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(h[c][j]));
+            for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(h[c][j] * (g[j] + a.weight_bias)));
+        }
     }
     sum = warp_sum(sum);
     if (GROUP_LANES == 0)
@@ -123,16 +146,21 @@ __device__ __forceinline__ void finish_row(const NormQ8Args& a, int64_t t, float
         top = lane < warps ? s_top[lane] : 0.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top *= rs;
+        if (top == INFINITY)  // (all threads) products that pass the range, as y may not: again, of y itself
+            top = largest_of_row<CPT>(a, h, gamma, rs, s_top);
+        else
+            top *= rs;
     }
     const int per_row = GROUP_LANES == 0 ? 1 : (chunks + GROUP_LANES - 1) / GROUP_LANES;
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
         const int chunk = threadIdx.x + c * blockDim.x;
-        float largest = 0.0f;
+        float largest = 0.0f, g[8];
+        bf16x8_to_f32(gamma[c], g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            h[c][j] *= rs;
+            h[c][j] *= rs;  // (first: with the weight it may pass the range)
+            h[c][j] *= g[j] + a.weight_bias;
             largest = max_nan(largest, fabsf(h[c][j]));
         }
         if (GROUP_LANES == 0) {
