@@ -9,7 +9,7 @@ raises.
 Calls go through ctypes.  The attention's and the 8-bit norm's, which are
 shorter than that takes, go through a native module (csrc/marshal.cpp) that
 makes the same checks; what it does not take is checked again here, for the
-error's sake.
+error's sake.  It is loaded at the first of these calls: the others do without it.
 """
 from __future__ import annotations
 
@@ -68,7 +68,7 @@ AR_MAX_ROPE_AXES = 4
 
 _lock = threading.Lock()
 _lib = None
-_marshal = None  # the native module, loaded with the library
+_marshal = None  # the native module, loaded at the first call that goes through it
 _ANYWHERE = -2  # device of a dry run's tensors, which are only looked at
 
 
@@ -165,24 +165,28 @@ def load_library(path: str | None = None):
         lib.ar_attn_decode.argtypes = [P, P, P, P, I64, I64, P, I64, I64, F, P, P, P]
         lib.ar_status_string.restype = ctypes.c_char_p
         lib.ar_status_string.argtypes = [I]
-        _load_marshal(lib)
         _lib = lib
         return lib
 
 
-def _load_marshal(lib):
-    """Load the native module (built beside the library) and give it the library's functions."""
+def _load_marshal():
+    """The native module (built beside the library), which is given the library's functions."""
     global _marshal
+    lib = load_library()
     from .build import marshal_path
-    p = marshal_path()
-    if not os.path.exists(p):
-        raise RuntimeError(f"{os.path.basename(p)} not found in {os.path.dirname(p)}; build it first "
-                           "(python -c 'import __graft_entry__ as g; g.build()')")
-    loader = importlib.machinery.ExtensionFileLoader("_marshal", p)
-    m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", p, loader=loader))
-    loader.exec_module(m)
-    m.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (lib.ar_rmsnorm_q8, lib.ar_attn_append, lib.ar_attn_decode)])
-    _marshal = m
+    with _lock:
+        if _marshal is not None:
+            return _marshal
+        p = marshal_path()
+        if not os.path.exists(p):
+            raise RuntimeError(f"{os.path.basename(p)} not found in {os.path.dirname(p)}: this call goes through the native module of "
+                               "this torch and interpreter; build it first (python -c 'import __graft_entry__ as g; g.build()')")
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", p)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", p, loader=loader))
+        loader.exec_module(m)
+        m.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (lib.ar_rmsnorm_q8, lib.ar_attn_append, lib.ar_attn_decode)])
+        _marshal = m
+        return m
 
 
 def ar_status_string(status: int) -> str:
@@ -515,8 +519,6 @@ def ar_rmsnorm_q8(ws: Workspace, partials, residual, gamma, weight_bias: float, 
     normalised rows q * scale.  ``out`` (bf16 [T, H]), when given, receives them unscaled
     as well.  ``residual_out`` may be ``residual`` (in place, bf16 only).  Returns (q,
     scales, residual_out), allocated when not given."""
-    if _lib is None:
-        load_library()
     R, H, T = ws.R, ws.H, residual.shape[0]
     if len(partials) != R:
         raise ValueError(f"partials has {len(partials)} entries, workspace has R={R}")
@@ -531,9 +533,10 @@ def ar_rmsnorm_q8(ws: Workspace, partials, residual, gamma, weight_bias: float, 
     if residual_out is None:
         residual_out = torch.empty((T, H), dtype=res_type, device=residual.device)
     dry = ws.dry_run
-    st = _marshal.rmsnorm_q8(ws.handle if ws.alive else None, R, H, _ANYWHERE if dry else ws.device,
-                             partials if type(partials) is list else list(partials), residual, gamma, weight_bias, eps, group, q,
-                             scales, out, residual_out, residual_out_fp32, None if dry else _stream_handle(stream, ws.device))
+    native = _marshal or _load_marshal()
+    st = native.rmsnorm_q8(ws.handle if ws.alive else None, R, H, _ANYWHERE if dry else ws.device,
+                           partials if type(partials) is list else list(partials), residual, gamma, weight_bias, eps, group, q,
+                           scales, out, residual_out, residual_out_fp32, None if dry else _stream_handle(stream, ws.device))
     if st is None:
         dev = None if dry else ws.device
         for r, p in enumerate(partials):
@@ -913,8 +916,9 @@ def ar_attn_append(attn: Attn, cache: KvCache, qkv, positions, slots, q=None, st
     shape = (T, attn.heads, attn.head_dim)
     if q is None:
         q = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
-    st = _marshal.attn_append(attn.handle, cache._ref, _ANYWHERE if dry else attn.device, attn.heads, attn.qkv_cols, attn.head_dim,
-                              attn.axes, qkv, positions, slots, q, None if dry else _stream_handle(stream, attn.device))
+    native = _marshal or _load_marshal()
+    st = native.attn_append(attn.handle, cache._ref, _ANYWHERE if dry else attn.device, attn.heads, attn.qkv_cols, attn.head_dim,
+                            attn.axes, qkv, positions, slots, q, None if dry else _stream_handle(stream, attn.device))
     if st is None:
         dev = _moe_device(attn)
         _need_on(dev, qkv, torch.bfloat16, (T, attn.qkv_cols), "qkv")
@@ -943,9 +947,10 @@ def ar_attn_decode(attn: Attn, cache: KvCache, q, page_table, lengths, scale: fl
     dry = attn.dry_run
     if out is None:
         out = torch.empty((q.shape[0], attn.heads, attn.head_dim), dtype=torch.bfloat16, device=q.device)
-    st = _marshal.attn_decode(attn.handle, cache._ref, _ANYWHERE if dry else attn.device, attn.heads, attn.head_dim, q, page_table,
-                              lengths, attn.head_dim ** -0.5 if scale is None else scale, window, out, lse,
-                              None if dry else _stream_handle(stream, attn.device))
+    native = _marshal or _load_marshal()
+    st = native.attn_decode(attn.handle, cache._ref, _ANYWHERE if dry else attn.device, attn.heads, attn.head_dim, q, page_table,
+                            lengths, attn.head_dim ** -0.5 if scale is None else scale, window, out, lse,
+                            None if dry else _stream_handle(stream, attn.device))
     if st is None:
         dev, B = _moe_device(attn), q.shape[0]
         shape = (B, attn.heads, attn.head_dim)

@@ -3,8 +3,9 @@
 Each translation unit compiles in parallel; the shared library links the CUDA
 runtime statically so it does not depend on which libcudart the host process
 loaded.  Output: ``tp_reduce_moe_gb300/lib/libarfuse.so`` (git-ignored), and
-beside it ``_marshal.<torch version>.so``, the binding's native module (host
-code, compiled against the installed torch's headers).
+beside it ``_marshal.<torch version>.<Python's ABI>.so``, the binding's native
+module (host code, compiled against the headers of the installed torch and of the
+interpreter that builds; left out where torch's are missing).
 """
 from __future__ import annotations
 
@@ -39,16 +40,27 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libarfuse")
 
 
-def torch_paths() -> tuple[str, str]:
-    """torch's folder and version (without importing it)."""
-    root = importlib.util.find_spec("torch").submodule_search_locations[0]
+def torch_paths() -> tuple[str, str] | None:
+    """torch's folder and version (without importing it); None where it is not installed."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    root = spec.submodule_search_locations[0]
     with open(os.path.join(root, "version.py")) as f:
         version = re.search(r"__version__ = '([^']+)'", f.read()).group(1)
     return root, version
 
 
 def marshal_path() -> str:
-    return os.path.join(LIBDIR, f"_marshal.{torch_paths()[1]}.so")
+    """Where the native module of this torch and this interpreter lies: neither takes another's."""
+    paths = torch_paths()
+    return os.path.join(LIBDIR, f"_marshal.{paths[1] if paths else 'none'}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+def _can_marshal() -> bool:
+    paths = torch_paths()
+    return (paths is not None and os.path.exists(os.path.join(paths[0], "include", "torch", "csrc", "autograd", "python_variable.h"))
+            and os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")))
 
 
 def _marshal_command(target: str) -> list[str]:
@@ -85,9 +97,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                 stderr=subprocess.STDOUT, text=True)))
+    # the native module beside the library, which does without it
     marshal = marshal_path()
     marshal_tmp = marshal + f".tmp{os.getpid()}"
     remade = force or _stale(marshal, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "arfuse.h")])
+    if remade and not _can_marshal():
+        print("native module of the binding left out: the headers of torch or Python are missing", file=sys.stderr)
+        remade = False
     if remade:
         procs.append(("marshal.cpp", subprocess.Popen(_marshal_command(marshal_tmp), stdout=subprocess.PIPE,
                                                       stderr=subprocess.STDOUT, text=True)))
@@ -98,15 +114,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(out, file=sys.stderr)
         if p.returncode:
             failed.append(src)
-    if failed:
+    if any(src != "marshal.cpp" for src in failed):
         raise RuntimeError(f"the compiler failed on {failed}")
-    if remade:
-        os.replace(marshal_tmp, marshal)
     if _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    if failed:
+        raise RuntimeError(f"the compiler failed on {failed} (the library is built)")
+    if remade:
+        os.replace(marshal_tmp, marshal)
     return LIB
 
 
