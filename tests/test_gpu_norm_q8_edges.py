@@ -47,3 +47,31 @@ def test_an_infinity_of_a_row_is_nan_beside_zeros(T):
     assert torch.equal(torch.isnan(scales[:, 0]), torch.arange(T, device=DEV) == 1)
     assert bool(torch.isnan(q[1].float()).all()) and not bool(torch.isnan(q[0].float()).any())
     ws.destroy()
+
+
+def test_a_workspace_sets_up_what_its_calls_launch():
+    # creating one does nothing for this norm's kernels; the first call that launches one of those that stay does, once
+    from torch.profiler import ProfilerActivity, profile
+
+    def calls(fn):
+        with profile(activities=[ProfilerActivity.CPU, ProfilerActivity.CUDA]) as prof:
+            fn()
+            torch.cuda.synchronize()
+        return [e.name for e in prof.events()]
+
+    g = gen(96)
+    T, H = 400, 1024
+    p, residual, gamma = normal((T, H), g), normal((T, H), g), normal((H,), g)
+    x = torch.ones(1024, device=DEV)
+    if not any("cudaLaunchKernel" in calls(lambda: x.mul_(1.0)) for _ in range(3)):
+        pytest.skip("the profiler records no calls of the runtime on this machine")
+    ws = arf.ar_workspace_create(1, 0, H, T, 1e-6, device=0)
+
+    def norm(rows, group):
+        arf.ar_rmsnorm_q8(ws, [p[:rows]], residual[:rows], gamma, 0.0, 1e-6, group=group)
+
+    for rows, group, told in ((3, 32, 0), (T, 32, 1), (T, 32, 0), (T, 128, 1), (T, 0, 1), (T, 128, 0), (3, 0, 0)):
+        names = calls(lambda: norm(rows, group))
+        assert sum(n.startswith("cudaLaunchKernel") for n in names) == 1
+        assert names.count("cudaFuncSetAttribute") == told, (rows, group)
+    ws.destroy()

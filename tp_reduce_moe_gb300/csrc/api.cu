@@ -43,6 +43,7 @@ struct ar_workspace {
     int last_grid;
     ar_plan_info last_plan;
     unsigned long long stall_wait_ns;  // failure injection (whole-row streaming), 0 = off
+    std::atomic<unsigned> q8_ready{0};  // kernels of the 8-bit norm that a call has set up
     int table_n;  // rules in `table` (0: heuristic only)
     ar_regime_rule table[AR_MAX_REGIME_RULES];
 };
@@ -613,8 +614,7 @@ ar_status ar_workspace_create(int device, int ranks, int top_k, int hidden, int6
         goto fail;
     }
     if (arf::cluster_rows_set_attributes() != cudaSuccess ||
-        arf::split_rows_set_attributes(ws->smem_optin) != cudaSuccess ||
-        arf::norm_q8_set_attributes() != cudaSuccess) {
+        arf::split_rows_set_attributes(ws->smem_optin) != cudaSuccess) {
         st = AR_ERR_CUDA;
         goto fail;
     }
@@ -750,7 +750,8 @@ ar_status ar_rmsnorm_q8(ar_workspace* ws, const void* const* partials, int R, co
     a.norm_bf16_h = (ws->flags & AR_WS_NORM_BF16_H) ? 1 : 0;
     a.weight_bias = weight_bias;
     a.eps = eps;
-    if (arf::launch_norm_q8(a, group, residual_out_is_fp32 != 0, ws->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    if (arf::launch_norm_q8(a, group, residual_out_is_fp32 != 0, ws->num_sms, &ws->q8_ready, static_cast<cudaStream_t>(stream)) !=
+        cudaSuccess) {
         (void)cudaGetLastError();
         return AR_ERR_CUDA;
     }

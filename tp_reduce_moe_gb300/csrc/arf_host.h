@@ -3,6 +3,8 @@
 // parameters are in arf_common.cuh).
 #pragma once
 
+#include <atomic>
+
 #include "arf_common.cuh"
 
 namespace arf {
@@ -35,9 +37,9 @@ bool oneshot_prefer_64(const ClusterPlan& p, int64_t T, int num_sms, int blocks8
 // The all-reduce + mHC write-back (mhc_post.cu).
 cudaError_t launch_mhc_post(const MhcArgs& a, cudaStream_t stream, bool pdl = false);
 
-// The norm with an 8-bit output (norm_q8.cu); group 0: one scale a row.
-cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num_sms, cudaStream_t stream);
-cudaError_t norm_q8_set_attributes();
+// The norm with an 8-bit output (norm_q8.cu); group 0: one scale a row.  ready: which kernels the device has been told of,
+// zero at first; a call tells it of the one that it launches, so that workspaces which never launch any load none.
+cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num_sms, std::atomic<unsigned>* ready, cudaStream_t stream);
 
 struct StreamPlan {
     StreamGeom geo;

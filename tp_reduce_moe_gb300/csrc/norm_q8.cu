@@ -299,7 +299,7 @@ Kernel kernel_for(int cpt, bool res_f32, int group) {
 
 }  // namespace
 
-cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num_sms, cudaStream_t stream) {
+cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num_sms, std::atomic<unsigned>* ready, cudaStream_t stream) {
     const int chunks = a.H / 8;
     // CTAs that stay, once there are more rows than SMs.  (Two partials of 7168 columns: 300 rows 4.6 us, a CTA a row 4.8; 608
     // 9.8 and 11.1; 4096 44 and 67.  Eight of 6144: 200 rows 5.9 and 7.2, 4096 85 and 118.)
@@ -311,6 +311,12 @@ cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num
     int64_t grid = a.T;
     size_t smem = 0;
     if (stay) {
+        const unsigned bit = 1u << ((cpt - 1) * 8 + res_f32 * 4 + (group == 0 ? 0 : group == 32 ? 1 : group == 64 ? 2 : 3));
+        if (!(ready->load(std::memory_order_acquire) & bit)) {  // (two threads may both do this: it sets the same value)
+            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+            if (e != cudaSuccess) return e;
+            ready->fetch_or(bit, std::memory_order_release);
+        }
         smem = (size_t)kPlaces * cpt * threads * 16;
         // as many CTAs as an SM's threads (of up to 64 registers) and shared memory take
         int per_sm = 1024 / threads;
@@ -330,16 +336,6 @@ cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, a);
-}
-
-cudaError_t norm_q8_set_attributes() {
-    for (int cpt = 1; cpt <= 2; ++cpt)
-        for (const bool res_f32 : {false, true})
-            for (const int group : {0, 32, 64, 128}) {
-                const cudaError_t e = cudaFuncSetAttribute(kernel_for<true>(cpt, res_f32, group), cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
-                if (e != cudaSuccess) return e;
-            }
-    return cudaSuccess;
 }
 
 }  // namespace arf
