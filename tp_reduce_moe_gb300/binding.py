@@ -965,7 +965,11 @@ def ar_attn_decode(attn: Attn, cache: KvCache, q, page_table, lengths, scale: fl
         _need_on(dev, out, torch.bfloat16, shape, "out")
         if lse is not None:
             _need_on(dev, lse, torch.float32, (B, attn.heads), "lse")
-        raise ValueError("page_table: the entries of a row must be contiguous, and rows must not overlap")
+        width = page_table.shape[1]
+        if page_table.layout is torch.strided and ((width > 1 and page_table.stride(1) != 1) or
+                                                   (B > 1 and page_table.stride(0) < width)):
+            raise ValueError("page_table: the entries of a row must be contiguous, and rows must not overlap")
+        raise TypeError("ar_attn_decode: plain strided tensors expected")
     if st != AR_OK:
         _check(st, "ar_attn_decode", ok=(AR_VALIDATED,) if dry else ())
     return out if lse is None else (out, lse)
