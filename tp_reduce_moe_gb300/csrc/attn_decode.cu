@@ -284,9 +284,10 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             total = __shfl_sync(0xffffffffu, sum, 31);
             before += __shfl_sync(0xffffffffu, sum, (warp + 31) & 31) * (warp > 0);
         }
-        // Three quarters of the SMs draw what the memory gives, with fewer streams in each other's way: 2.4 GB take 360 us from
-        // 114 SMs, 375 from 152; 540 MB take 90 and 92.  134 MB, where each SM's latencies count, take 35 and 33.4.  Where an SM
-        // has more work with a byte all are needed: 630 MB with sixteen heads a key 112 us from 152 SMs, 141 from 114; 8-bit
+        // Three quarters of the SMs draw what the memory gives, with fewer streams in each other's way.  128 columns: 610 MB 102 us
+        // from 114 SMs, 108 from 152; 1.05 GB 168 and 180; 1.2 GB 191 and 202.  256: 525 MB 94 and 96, 1.3 GB 215 and 220.  134 MB,
+        // where each SM's latencies count, take 35 and 33.4.  Where an SM has more work with a byte all are needed: 64 columns 540 MB
+        // 109 us from 114 SMs, 103 from 152, 890 MB 173 and 164, 1.07 GB 210 and 196; sixteen heads a key 630 MB 141 and 112; 8-bit
         // caches too.
         const int fewer = max(1, (int)gridDim.x * 3 / 4);
         if ((int64_t)a.B * a.groups <= gridDim.x && (int64_t)(most - S::kAlone) * fewer <= total) {
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             end = w_n;
         } else {
             // Equal ranges of all units; the last ones may be short or empty.
-            const int warps = (!EIGHT && NT == 1 && a.per_head == 1 && total >= S::kMany ? fewer : (int)gridDim.x) * kWarps;
+            const int warps = (D > 64 && !EIGHT && NT == 1 && a.per_head == 1 && total >= S::kMany ? fewer : (int)gridDim.x) * kWarps;
             each = max((int64_t)1, quotient64(total + warps - 1, warps));
             begin = each * (blockIdx.x * kWarps);
             end = min(total, begin + each * kWarps);
