@@ -827,6 +827,12 @@ ARFUSE_API ar_status ar_attn_append(ar_attn* attn, const ar_kv_cache* cache, con
  *   lse         device fp32 [B, heads], or NULL
  * Values of the cache outside the tokens looked at may be anything.  A score of
  * minus infinity counts as no token, a row of nothing else as one without tokens.
+ * An infinity among the values looked at leaves its column of the rows that it counts
+ * in infinite or NaN, and nothing else.  Weighted values are added up before they are
+ * divided by the weights' sum, up to 2^8 times what the softmax gives: those of 2^120 /
+ * tokens and above may overflow.  Over an e4m3 cache, columns of q below 2^-29 of their
+ * row's largest and weights below 2^-21 of the largest lose bits (off by 2^-40 and 2^-32
+ * of it at most).
  * Sums and the softmax are fp32; the same call on the same GPU gives the same bits; the
  * order of a sum may depend on the other sequences of the batch and on the width of
  * the page table.  One launch; the split of the work over the SMs follows the lengths

@@ -133,3 +133,33 @@ def test_decode_queries_at_the_ends_of_their_range(size, scale):
     m = arf.ar_attn_create(heads, 1, D, page, 1, device=0)
     check_decode(m, q, k, v, torch.ones_like(ks), vs, table, [n], scale=scale)
     m.destroy()
+
+
+# ---------------------------------------------------------------- infinities among the values
+@pytest.mark.parametrize("heads,D,n", [(8, 128, 150), (12, 64, 3000), (4, 256, 700)])
+def test_decode_infinite_values_stay_in_their_column(heads, D, n):
+    kv, page, lengths = 2, 16, [n, 90]
+    g = gen(85 + D)
+    pages = -(-n // page) + 7
+    k, v, _, _ = paged(pages, page, kv, D, False, "token", g)
+    order = torch.randperm(pages, generator=g, device=DEV).int()
+    table = torch.full((2, pages), -1, dtype=torch.int32, device=DEV)
+    table[0, :-(-n // page)], table[1, :6] = order[:-(-n // page)], order[-6:]
+    m = arf.ar_attn_create(heads, kv, D, page, 2, device=0)
+    cache, lens = arf.ar_kv_cache(k, v), torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    for size in (0.0, 1.0):  # equal weights, whose second parts are zero; others
+        q = normal((2, heads, D), g, size)
+        lse, lse0 = torch.empty(2, heads, device=DEV), torch.empty(2, heads, device=DEV)
+        kept = v.clone()
+        before, _ = arf.ar_attn_decode(m, cache, q, table, lens, lse=lse0)
+        v[int(table[0, 3]), 7, 0, 9] = float("inf")
+        v[int(table[0, 0]), 0, 1, 33] = -float("inf")
+        v[int(table[1, 5]), 9, 1, 0] = float("inf")   # the last token of its sequence
+        v[int(table[1, 5]), 10, 0, 5] = float("inf")  # behind it
+        out, _ = arf.ar_attn_decode(m, cache, q, table, lens, lse=lse)
+        hit, G = torch.zeros_like(out, dtype=torch.bool), heads // kv
+        hit[0, :G, 9], hit[0, G:, 33], hit[1, G:, 0] = True, True, True
+        assert torch.equal(~torch.isfinite(out), hit)
+        assert torch.equal(out[~hit], before[~hit]) and torch.equal(lse, lse0)
+        v.copy_(kept)
+    m.destroy()
