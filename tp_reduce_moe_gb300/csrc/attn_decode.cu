@@ -48,7 +48,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <int D, bool EIGHT, int NT>
 struct Shape {
     // Sixteen warps of 128 registers hide each other's latencies; more sums need twelve of 168, or eight of 255.  (Sixteen heads
-    // of 64 columns, 315 MB: twelve warps 64 us, eight 76, sixteen, whose registers spill, 70.)
+    // of 64 columns, 315 MB: twelve warps 64 us, eight 76, sixteen, whose registers spill, 70.)  Two groups of more columns spill
+    // even so: of 128 columns 32 bytes a thread (228 over 8 bits), of 256 156 (148).
     static constexpr int kWarps = D == 256 ? 8 : NT == 1 ? 16 : 12;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRows = 8 * NT;
@@ -242,8 +243,8 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
     // ---- what this CTA's warps take
     int64_t total, each = 0;   // units, and units of a warp where all are dealt out
     int64_t begin, end;        // units of this CTA
-    // The walk over this warp's items (clamped where lengths that change during the call could lead it astray).  One counts for kCost units more, before its first, for what it costs to begin and end
-    // it; these are walked over.
+    // The walk over this warp's items (clamped where lengths that change during the call could lead it astray).  One counts for
+    // kCost units more, before its first, for what it costs to begin and end it; these are walked over.
     int w_b = 0, w_group = 0, w_u = 0, w_start = 0, w_len = 0, w_n = 0;  // sequence, group, next unit of kCost + w_n, tokens
     int64_t w_item = 0;  // where the item's first unit (behind what it costs) is among all
     int64_t w_left = 0;  // units of the range that are not handed out; 0 once no real one is among them
@@ -257,7 +258,8 @@ __global__ void __launch_bounds__(Shape<D, EIGHT, NT>::kThreads, 1)
             const int len = tokens_of(a, b, blockIdx.x == 0, &start), n = units_of<TOK>(start, len);
             return n > 0 ? n + S::kCost : 0;
         };
-        // a thread's sequences, and before them the units of the threads before; few sequences: each warp sums by itself
+        // a thread's sequences, and before them the units of the threads before; few sequences: each warp sums by itself (4096
+        // single tokens, whose lengths a thread reads one after the other: 14.8 us; 256 columns, half the threads, 31.6)
         const bool few = a.B <= 32;
         const int per_thread = few ? 1 : (a.B + kThreads - 1) / kThreads;
         const int b0 = (few ? lane : tid) * per_thread, b1 = min(a.B, b0 + per_thread);
@@ -1014,6 +1016,10 @@ cudaError_t launch_attn_decode(const DecodeArgs& args, int head_dim, int num_sms
     // window say (the lengths are on the device).  Groups of eight have half the sums to join and twice the warps: sixteen
     // heads of 128 columns, 8 MB 11.4 us (groups of sixteen: 14.4), 66 MB 23.6 (26.2), 131 MB 40.9 (36.4), 262 MB 85.7 (56.2);
     // of 256 columns, 33 MB 21.3 (30.4), 66 MB 29.3 (37.5), 131 MB 41.4 (40.9); of 64, 33 MB 12.9 (13.3), 66 MB 17.2 (16.3).
+    // Short sequences under a wide table get groups of sixteen: 8 of 500 tokens, table of 8192 pages, 13.3 us (exact table: 9.4), of
+    // 256 columns 18.1 (12.0), in 8 bits 11.2 (8.0); 8 of 2000 15.0 (11.6).
+    // More than sixteen heads: the groups of a key-value head lie one behind the other, and caches beyond L2 are read from memory once
+    // a group (13 of 6000 tokens, 20 heads on each of 8: 640 MB of reads for 320, 110 us).
     DecodeArgs a = args;
     a.shared = a.heads / a.kv;
     a.per_head = (a.shared + 15) / 16;

@@ -12,7 +12,8 @@
 //
 // What bounds it: memory, for many rows (8192 of 8192 columns, two partials: 101 us, 6.1 TB/s of
 // what is read and written, 0.90 of a copy's rate; 73 % of the issue slots are in use), and
-// for few the launch and two trips to memory (one row 2.5 us).
+// for few the launch and two trips to memory (one row 2.4 us).  The kernel of a CTA a row spills 32 bytes a thread where a thread has
+// two chunks (rows of more than 8192 columns).
 //
 // Few rows: a CTA a row, partials loaded to registers, four in flight a chunk.  Many: CTAs
 // stay and take every so many rows; the rows of partials come through a ring in shared
@@ -301,8 +302,10 @@ Kernel kernel_for(int cpt, bool res_f32, int group) {
 
 cudaError_t launch_norm_q8(const NormQ8Args& a, int group, bool res_f32, int num_sms, std::atomic<unsigned>* ready, cudaStream_t stream) {
     const int chunks = a.H / 8;
-    // CTAs that stay, once there are more rows than SMs.  (Two partials of 7168 columns: 300 rows 4.6 us, a CTA a row 4.8; 608
-    // 9.8 and 11.1; 4096 44 and 67.  Eight of 6144: 200 rows 5.9 and 7.2, 4096 85 and 118.)
+    // CTAs that stay, once there are more rows than SMs.  (Two partials of 7168 columns, 896 threads a row: 152 rows 2.5 us, a CTA a
+    // row; 153 4.1, a CTA a row 4.2; 200 4.2 and 4.3; 304 4.4 and 4.7; 400 7.9 and 7.1; 608 9.8 and 11.2; 4096 44 and 67.  Eight of
+    // 6144: 153 rows 5.5 and 6.0, 200 5.9 and 7.2, 304 7.7 and 9.5, 4096 85 and 118.  Rows of 4096 columns, of which two CTAs fit an SM,
+    // would rather have one each up to some 500 of them: 153 3.5 and 2.5, 256 4.4 and 2.6, 400 4.6 and 4.1, 608 4.8 and 4.9.)
     const bool stay = a.T > num_sms;
     const int cpt = chunks > (stay ? 256 : kNormMaxThreads) ? 2 : 1;
     const int threads = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
